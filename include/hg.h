@@ -63,7 +63,8 @@ extern "C" {
 #define HG_EHIP (-3)   /* a HIP runtime call failed (see hg_last_error_detail)  */
 #define HG_ETIMEOUT (-4) /* a bounded poll gave up (reported by hg_poll_status)  */
 #define HG_ESTATE (-5) /* split-variant call out of order                       */
-#define HG_ESIZE (-6)  /* beyond the static scratch buffer (hg_gather_static)   */
+#define HG_ESIZE (-6)  /* beyond the static scratch buffer (hg_gather_static), or
+                          a workspace that is too small                         */
 
 typedef struct hg_ctx hg_ctx;
 
@@ -319,6 +320,117 @@ int hg_gather_static(int tp, int shard, const void *const *shards, int m, void *
  * grid sizing of the pages' kernel is not shown (API page, HeadGather.__init__
  * source names only its per-row-count grid table). */
 int hg_fused_grid_limit(hg_ctx *h, int m);
+
+/* ---------------------------------------------------------------------------
+ * Training and scoring at the vocabulary matrix. These entry points need no
+ * context. The matrix is the lm_head weight of hg_lmhead: `tp` blocks of
+ * [shard][hidden], block r holding entries r*shard .. of the vocabulary, row
+ * major, each 16-byte aligned. They follow no page; their definitions are
+ * given here.
+ *
+ * Element types (`dtype`): inputs, 16-bit gradients and outputs share one.
+ */
+#define HG_BF16 0
+#define HG_FP16 1
+#define HG_FP32 2 /* embedding only */
+
+/*
+ * The softmax cross entropy of the lm_head product, without keeping the
+ * logits. For a row i that counts, over the real vocabulary v < vocab:
+ *     z_iv   = scale * x_i . W_v
+ *     lse_i  = log sum_v exp z_iv
+ *     loss_i = lse_i - z_it + z_weight * lse_i^2,      t = labels[i]
+ * A row whose label is `ignore` is left out: loss = lse = 0, its x is not
+ * read into any product, its dx is 0. A row whose label is neither `ignore`
+ * nor in 0 .. vocab-1 gets loss = lse = NaN and is left out of the gradients.
+ */
+typedef struct hg_xent_shape {
+  int tp, shard, hidden; /* the matrix; shard % 32 == 0, hidden % 8 == 0       */
+  int m;                 /* rows of x                                          */
+  int vocab;             /* real vocabulary, 1 .. tp*shard                     */
+  int dtype;             /* HG_BF16 or HG_FP16: x, W, dx (and dw unless wide)  */
+  int label_bytes;       /* 4 or 8: labels are int32 or int64                  */
+  long long ignore;      /* label of a row that is left out                    */
+  float scale;           /* factor of the logits                               */
+  float z_weight;        /* weight of the squared log-sum-exp                  */
+} hg_xent_shape;
+
+/* What a workspace is for. */
+#define HG_XENT_SCORE 0
+#define HG_XENT_GRAD 1
+#define HG_XENT_STEP 2
+
+/*
+ * Bytes of device workspace for a call of the given kind: at most `limit`
+ * (0: no limit), or the least that the call can do with if that is more.
+ * GRAD and STEP keep 16-bit values of m rows x one piece of the vocabulary;
+ * a workspace that holds fewer columns than the vocabulary makes several
+ * pieces of it (and STEP then computes the logits twice). HG_EINVAL on a bad
+ * shape or kind, or bytes == NULL.
+ */
+int hg_xent_workspace(const hg_xent_shape *s, int kind, size_t limit, size_t *bytes);
+
+/*
+ * The loss alone (scoring): loss[m] and lse[m], fp32.
+ * x: device [m][hidden]; w: host array of tp device pointers; labels: device
+ * [m]; ws: device workspace of ws_bytes, 256-byte aligned, as large as
+ * hg_xent_workspace asks (else HG_ESIZE), in use until the call's work on
+ * `stream` is done. m == 0 does nothing. HG_EINVAL on a bad shape, a NULL or
+ * misaligned pointer, or an output overlapping an input, another output or the
+ * workspace. Deterministic: the same call gives the same bits.
+ */
+int hg_xent(const hg_xent_shape *s, const void *x, const void *const *w, const void *labels,
+            float *loss, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The gradient for a known lse[m] (of hg_xent) and upstream gradient grad[m],
+ * fp32:
+ *     d_iv = scale * grad_i * ((1 + 2 z_weight lse_i) exp(z_iv - lse_i) - [v = t_i])
+ *     dx_i = sum_v d_iv W_v            [m][hidden], in dtype
+ *     dw_v = sum_i d_iv x_i            [tp*shard][hidden], in dtype, or fp32 if
+ *                                      dw_wide; rows from vocab on get zeros
+ * accumulate: dw += instead of dw = (rows from vocab on keep their values).
+ * d is rounded to dtype, as the matrix cores take it; sums are fp32, each
+ * result rounded once. m == 0 zeroes dw unless accumulating.
+ */
+int hg_xent_grad(const hg_xent_shape *s, const void *x, const void *const *w, const void *labels,
+                 const float *lse, const float *grad, void *dx, void *dw, int dw_wide,
+                 int accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Loss and gradient in one call, for an upstream gradient that is known before
+ * the loss (a mean's 1/n, a row's weight). With a workspace for the whole
+ * vocabulary the logits are computed once.
+ */
+int hg_xent_step(const hg_xent_shape *s, const void *x, const void *const *w, const void *labels,
+                 const float *grad, float *loss, float *lse, void *dx, void *dw, int dw_wide,
+                 int accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Embedding lookup with scaling: out[j] = scale * W[tokens[j]], rounded once,
+ * [n][hidden] in dtype (HG_BF16, HG_FP16, HG_FP32); a token outside
+ * 0 .. tp*shard-1 gives a row of zeros. tokens: device, int32 or int64
+ * (token_bytes 4 or 8). tp in 1..HG_MAX_TP, shard >= 1, hidden a multiple of 8.
+ * Rows are 16-byte aligned; out must not overlap the matrix or the tokens.
+ * n == 0 does nothing.
+ */
+int hg_embed(int tp, int shard, int hidden, int dtype, const void *const *w, const void *tokens,
+             int token_bytes, int n, float scale, void *out, void *stream);
+
+/* Bytes of device workspace for hg_embed_grad. */
+int hg_embed_workspace(int tp, int shard, int hidden, int n, size_t *bytes);
+
+/*
+ * The lookup's gradient: dw_v = scale * sum over j with tokens[j] = v of dy_j,
+ * for every row v of the matrix (zeros where no token names it), or
+ * dw_v += ... with accumulate (other rows untouched). dy: [n][hidden] in
+ * dtype; dw: [tp*shard][hidden] in dtype, or fp32 if dw_wide. Sums are fp32, in
+ * the order of j inside runs of the sorted tokens, so the same call gives the
+ * same bits; each row is rounded once. ws as above.
+ */
+int hg_embed_grad(int tp, int shard, int hidden, int dtype, const void *tokens, int token_bytes,
+                  int n, const void *dy, float scale, void *dw, int dw_wide, int accumulate,
+                  void *ws, size_t ws_bytes, void *stream);
 
 /* Static description of a status code. Not on the pages (the pages report
  * a failed build with a logged warning: API page, _install_gather source). */

@@ -25,12 +25,26 @@ HG_ESTATE = -5
 HG_ESIZE = -6
 HG_STATIC_PARITY_BYTES = 8 << 20
 HG_MAX_TP = 64
+HG_BF16, HG_FP16, HG_FP32 = 0, 1, 2
+HG_XENT_SCORE, HG_XENT_GRAD, HG_XENT_STEP = 0, 1, 2
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _ull = ctypes.c_ulonglong
 _size = ctypes.c_size_t
 _ctxp = ctypes.c_void_p
+
+
+
+class XentShape(ctypes.Structure):
+    """``hg_xent_shape``."""
+
+    _fields_ = [(n, ctypes.c_int) for n in ("tp", "shard", "hidden", "m", "vocab", "dtype", "label_bytes")] + [
+        ("ignore", ctypes.c_longlong), ("scale", ctypes.c_float), ("z_weight", ctypes.c_float)]
+
+
+_shapep = ctypes.POINTER(XentShape)
+_f = ctypes.c_float
 
 # name -> (restype, argtypes); the C declarations are in include/hg.h
 SIGNATURES = {
@@ -54,6 +68,14 @@ SIGNATURES = {
     "hg_poll_status": (_i, [_ctxp, _vp]),
     "hg_fused_grid_limit": (_i, [_ctxp, _i]),
     "hg_gather_static": (_i, [_i, _i, ctypes.POINTER(_vp), _i, _vp, _vp]),
+    "hg_xent_workspace": (_i, [_shapep, _i, _size, ctypes.POINTER(_size)]),
+    "hg_xent": (_i, [_shapep, _vp, ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _size, _vp]),
+    "hg_xent_grad": (_i, [_shapep, _vp, ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _size, _vp]),
+    "hg_xent_step": (_i, [_shapep, _vp, ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _size,
+                          _vp]),
+    "hg_embed": (_i, [_i, _i, _i, _i, ctypes.POINTER(_vp), _vp, _i, _i, _f, _vp, _vp]),
+    "hg_embed_workspace": (_i, [_i, _i, _i, _i, ctypes.POINTER(_size)]),
+    "hg_embed_grad": (_i, [_i, _i, _i, _i, _vp, _i, _i, _vp, _f, _vp, _i, _i, _vp, _size, _vp]),
     "hg_strerror": (ctypes.c_char_p, [_i]),
     "hg_last_error_detail": (ctypes.c_char_p, []),
 }

@@ -1,0 +1,552 @@
+// The embedding lookup with scaling, and its gradient by sorted tokens.
+//
+//   out_j = scale * W[t_j]                 (0 where t_j lies outside W)
+//   dW_v  = scale * sum over j with t_j = v of dy_j
+//
+// Both move rows and hardly compute: HBM bounds them, latency the small ones.
+//
+// The gradient sorts the (token, position) pairs by token, stably, so that
+// every sum runs over its positions in increasing order and repeated calls
+// give the same bits. The sort is a radix sort, least significant digit first,
+// of 9 bits a pass (two passes up to 2^18 entries, the smallest number that
+// covers a large vocabulary): one workgroup in LDS while its 4096-key tile
+// holds all tokens, one launch each for counts, offsets and scatter beyond.
+// The sorted run is then cut into blocks of equally many positions, whatever
+// their tokens: a frequent token's sum is spread over many workgroups. A sum
+// inside one block is written at once; one that crosses a block's edge leaves
+// fp32 partial rows, joined in order by a second launch. The rows no token
+// names are filled with zeros by the same launch that sums.
+
+#include <type_traits>
+
+#include "hg_tile.h"
+#include "hg_vocab.h"
+
+namespace hg {
+
+namespace {
+
+struct TypeF32 {};
+
+// 16 bytes of a row as fp32 values, and back (rounded to nearest even).
+template <class T>
+struct Vec {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void get(u32x4 v, float *f) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      f[2 * t] = from16<T>(v[t] & 0xFFFFu);
+      f[2 * t + 1] = from16<T>(v[t] >> 16);
+    }
+  }
+  static __device__ __forceinline__ u32x4 put(const float *f) {
+    u32x4 v;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = bits16<T>(f[2 * t]) | bits16<T>(f[2 * t + 1]) << 16;
+    return v;
+  }
+};
+template <>
+struct Vec<TypeF32> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void get(u32x4 v, float *f) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint32_t b = v[t];  // (a bit cast of a vector's element takes the first one)
+      f[t] = __builtin_bit_cast(float, b);
+    }
+  }
+  static __device__ __forceinline__ u32x4 put(const float *f) {
+    u32x4 v;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = __builtin_bit_cast(uint32_t, f[t]);
+    return v;
+  }
+};
+
+__device__ __forceinline__ long long token_at(const void *tokens, int bytes, long long i) {
+  return bytes == 8 ? static_cast<const long long *>(tokens)[i]
+                    : static_cast<const int *>(tokens)[i];
+}
+
+// One 16-byte vector per lane; a workgroup takes 256 vectors of a row.
+template <class T, int NT>
+__global__ __launch_bounds__(256) void k_embed(ShardTableN<NT> w, int shard, int rows,
+                                               const void *tokens, int token_bytes, int n, int hv,
+                                               float scale, u32x4 *out) {
+  const int k = static_cast<int>(blockIdx.x * 256 + threadIdx.x);
+  for (int j = static_cast<int>(blockIdx.y); j < n; j += static_cast<int>(gridDim.y)) {
+    const long long t = token_at(tokens, token_bytes, j);
+    if (k >= hv) continue;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (t >= 0 && t < rows) {
+      const int rank = NT == 1 ? 0 : static_cast<int>(t) / shard;
+      v = w.p[rank][(t - static_cast<long long>(rank) * shard) * hv + k];
+      float f[Vec<T>::N];
+      Vec<T>::get(v, f);
+#pragma unroll
+      for (int e = 0; e < Vec<T>::N; ++e) f[e] *= scale;
+      v = Vec<T>::put(f);
+    }
+    out[static_cast<long long>(j) * hv + k] = v;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The sort. A key is the token, or `rows` where the token lies outside.
+
+constexpr int kSortTile = 4096;  // keys per workgroup
+constexpr int kDigits = 512;
+constexpr int kSortWaves = 16;
+
+__device__ __forceinline__ int key_at(const void *tokens, int bytes, long long i, int rows) {
+  const long long t = token_at(tokens, bytes, i);
+  return t >= 0 && t < rows ? static_cast<int>(t) : rows;
+}
+
+// Lanes of the wave (of those in `live`) with this lane's digit.
+__device__ __forceinline__ unsigned long long same_digit(int digit, unsigned long long live) {
+  unsigned long long m = live;
+#pragma unroll
+  for (int b = 0; b < 9; ++b) {
+    const unsigned long long votes = __ballot((digit >> b) & 1);
+    m &= ((digit >> b) & 1) ? votes : ~votes;
+  }
+  return m;
+}
+
+// Exclusive scan of 8 values per thread over the 1024 threads of a workgroup.
+__device__ __forceinline__ void scan8(int (&v)[8], int *wave_sum) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+  int sum = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum += v[e];
+  int up = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(up, d);
+    if (lane >= d) up += o;
+  }
+  if (lane == 63) wave_sum[wave] = up;
+  __syncthreads();
+  int run = up - sum;
+  for (int k = 0; k < wave; ++k) run += wave_sum[k];
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int c = v[e];
+    v[e] = run;
+    run += c;
+  }
+}
+
+// The per-wave digit counts [kDigits][kSortWaves] of a workgroup's keys; wave
+// w holds keys w*per .. of the tile, in order.
+template <class K>
+__device__ __forceinline__ void count_digits(int *count, int n, int per, int shift, K key) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+  for (int k = tid; k < kDigits * kSortWaves; k += 1024) count[k] = 0;
+  __syncthreads();
+  const int end = (wave + 1) * per < n ? (wave + 1) * per : n;
+  for (int k = wave * per + lane; k < end; k += 64)
+    atomicAdd(&count[((key(k) >> shift) & (kDigits - 1)) * kSortWaves + wave], 1);
+  __syncthreads();
+}
+
+// Each wave hands its keys, in order, the places its counters hold.
+template <class K, class P>
+__device__ __forceinline__ void place_keys(volatile int *place, int n, int per, int shift, K key, P put) {
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+  const int end = (wave + 1) * per < n ? (wave + 1) * per : n;
+  for (int k0 = wave * per; k0 < end; k0 += 64) {
+    const int k = k0 + lane;
+    const bool live = k < end;
+    const int v = live ? key(k) : 0;
+    const int digit = (v >> shift) & (kDigits - 1);
+    const unsigned long long lanes = same_digit(digit, __ballot(live));
+    const int at = live ? place[digit * kSortWaves + wave] : 0;
+    const int rank = __popcll(lanes & ((1ull << lane) - 1));
+    // the counter is the wave's own; its last lane of the digit moves it on
+    if (live && (lanes >> lane) == 1ull) place[digit * kSortWaves + wave] = at + rank + 1;
+    if (live) put(k, v, at + rank);
+  }
+}
+
+// All keys in one workgroup's LDS.
+__global__ __launch_bounds__(1024) void k_sort_tile(const void *tokens, int token_bytes, int n,
+                                                    int rows, int passes, int *keys, int *pos) {
+  __shared__ int count[kDigits * kSortWaves];
+  __shared__ int sk[2][kSortTile], sp[2][kSortTile];
+  __shared__ int wave_sum[16];
+  const int tid = static_cast<int>(threadIdx.x);
+  const int per = ((n + 1023) / 1024) * 64;
+  for (int k = tid; k < n; k += 1024) {
+    sk[0][k] = key_at(tokens, token_bytes, k, rows);
+    sp[0][k] = k;
+  }
+  __syncthreads();
+  for (int p = 0; p < passes; ++p) {
+    const int *ik = sk[p & 1], *ip = sp[p & 1];
+    int *ok = sk[(p & 1) ^ 1], *op = sp[(p & 1) ^ 1];
+    auto key = [&](int k) { return ik[k]; };
+    count_digits(count, n, per, 9 * p, key);
+    int v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = count[8 * tid + e];
+    scan8(v, wave_sum);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) count[8 * tid + e] = v[e];
+    __syncthreads();
+    place_keys(count, n, per, 9 * p, key, [&](int k, int kv, int at) {
+      ok[at] = kv;
+      op[at] = ip[k];
+    });
+    __syncthreads();
+  }
+  for (int k = tid; k < n; k += 1024) {
+    keys[k] = sk[passes & 1][k];
+    pos[k] = sp[passes & 1][k];
+  }
+}
+
+// Counts of one pass: hist[digit][tile].
+__global__ __launch_bounds__(1024) void k_sort_count(const void *tokens, int token_bytes,
+                                                     const int *keys, long long n, int rows,
+                                                     int shift, int *hist, int tiles) {
+  __shared__ int count[kDigits];
+  const int tid = static_cast<int>(threadIdx.x);
+  const long long base = static_cast<long long>(blockIdx.x) * kSortTile;
+  if (tid < kDigits) count[tid] = 0;
+  __syncthreads();
+  for (int k = tid; k < kSortTile && base + k < n; k += 1024) {
+    const int v = keys ? keys[base + k] : key_at(tokens, token_bytes, base + k, rows);
+    atomicAdd(&count[(v >> shift) & (kDigits - 1)], 1);
+  }
+  __syncthreads();
+  if (tid < kDigits) hist[tid * tiles + blockIdx.x] = count[tid];
+}
+
+// Exclusive scan of the counts, in place; one workgroup, 8192 at a time.
+__global__ __launch_bounds__(1024) void k_sort_scan(int *hist, int n) {
+  __shared__ int wave_sum[16], total;
+  const int tid = static_cast<int>(threadIdx.x);
+  int carry = 0;
+  for (int k0 = 0; k0 < n; k0 += 8192) {
+    int v[8], last = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int k = k0 + 8 * tid + e;
+      v[e] = k < n ? hist[k] : 0;
+      last = v[e];
+    }
+    scan8(v, wave_sum);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int k = k0 + 8 * tid + e;
+      if (k < n) hist[k] = carry + v[e];
+    }
+    if (tid == 1023) total = v[7] + last;
+    __syncthreads();
+    carry += total;
+    __syncthreads();
+  }
+}
+
+// Scatter of one pass.
+__global__ __launch_bounds__(1024) void k_sort_place(const void *tokens, int token_bytes,
+                                                     const int *keys, const int *pos, long long n,
+                                                     int rows, int shift, const int *hist,
+                                                     int tiles, int *okeys, int *opos) {
+  __shared__ int count[kDigits * kSortWaves];
+  __shared__ int sk[kSortTile];
+  const int tid = static_cast<int>(threadIdx.x);
+  const long long base = static_cast<long long>(blockIdx.x) * kSortTile;
+  const int here = n - base < kSortTile ? static_cast<int>(n - base) : kSortTile;
+  for (int k = tid; k < here; k += 1024)
+    sk[k] = keys ? keys[base + k] : key_at(tokens, token_bytes, base + k, rows);
+  __syncthreads();
+  auto key = [&](int k) { return sk[k]; };
+  const int per = kSortTile / kSortWaves;
+  count_digits(count, here, per, shift, key);
+  if (tid < kDigits) {
+    int run = hist[tid * tiles + blockIdx.x];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = count[tid * kSortWaves + w];
+      count[tid * kSortWaves + w] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+  place_keys(count, here, per, shift, key, [&](int k, int kv, int at) {
+    okeys[at] = kv;
+    opos[at] = pos ? pos[base + k] : static_cast<int>(base + k);
+  });
+}
+
+// ---------------------------------------------------------------------------
+// The sums.
+
+struct SumArgs {
+  const int *keys, *pos;
+  const u32x4 *dy;
+  void *dw;
+  float *part;      // [blocks][2][hidden]
+  long long n;
+  int rows, hidden, per;  // per: positions per block
+  int blocks, slabs;      // slabs of 256 vectors in a row
+  float scale;
+  int accumulate;
+};
+
+template <class T, class D>
+__device__ __forceinline__ void write_row(const SumArgs &a, int v, int col, const float *sum) {
+  constexpr int N = Vec<T>::N;
+  float f[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) f[e] = sum[e] * a.scale;
+  const long long at = static_cast<long long>(v) * a.hidden + col;
+  if constexpr (std::is_same_v<T, D>) {
+    u32x4 *o = reinterpret_cast<u32x4 *>(static_cast<char *>(a.dw) + at * (16 / N));
+    if (a.accumulate) {
+      float old[N];
+      Vec<T>::get(*o, old);
+#pragma unroll
+      for (int e = 0; e < N; ++e) f[e] += old[e];
+    }
+    *o = Vec<T>::put(f);
+  } else {  // 16-bit dy, fp32 gradient
+    f32x4 *o = reinterpret_cast<f32x4 *>(static_cast<float *>(a.dw) + at);
+#pragma unroll
+    for (int h = 0; h < N / 4; ++h) {
+      f32x4 x = {f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]};
+      o[h] = a.accumulate ? o[h] + x : x;
+    }
+  }
+}
+
+// Workgroups 0 .. blocks*slabs-1 sum; the rest fill 64 rows each (`fill`).
+template <class T, class D>
+__global__ __launch_bounds__(256) void k_sum(SumArgs a) {
+  constexpr int N = Vec<T>::N;
+  const int tid = static_cast<int>(threadIdx.x);
+  const int bid = static_cast<int>(blockIdx.x);
+  const int hv = a.hidden / N;
+  if (bid < a.blocks * a.slabs) {
+    const int blk = bid / a.slabs, k = (bid - blk * a.slabs) * 256 + tid;
+    const long long j0 = static_cast<long long>(blk) * a.per;
+    const int here = a.n - j0 < a.per ? static_cast<int>(a.n - j0) : a.per;
+    const int *keys = a.keys + j0, *pos = a.pos + j0;
+    const int before = blk > 0 ? keys[-1] : -1;
+    const int after = j0 + here < a.n ? keys[here] : -1;
+    if (k >= hv) return;
+    float sum[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum[e] = 0.f;
+    float *part = a.part + static_cast<long long>(blk) * 2 * a.hidden + k * N;
+    constexpr int kAhead = 8;  // rows in flight
+    for (int j = 0; j < here; j += kAhead) {
+      u32x4 v[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (j + u < here && keys[j + u] < a.rows)
+          v[u] = __builtin_nontemporal_load(a.dy + static_cast<long long>(pos[j + u]) * hv + k);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (j + u >= here) break;
+        const int key = keys[j + u];
+        if (key >= a.rows) return;  // tokens outside sort last
+        float f[N];
+        Vec<T>::get(v[u], f);
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum[e] += f[e];
+        const int next = j + u + 1 < here ? keys[j + u + 1] : -2;
+        if (key == next) continue;
+        // the sum of `key` ends here, or goes on in the next block
+        const bool on = next == -2 && key == after;
+        if (key == before || on) {
+          float *o = part + (key == before ? 0 : a.hidden);
+#pragma unroll
+          for (int e = 0; e < N; ++e) o[e] = sum[e];
+        } else {
+          write_row<T, D>(a, key, k * N, sum);
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum[e] = 0.f;
+      }
+    }
+    return;
+  }
+  // Zeros for the rows no token names: lane l looks for row v0 + l.
+  const int v0 = (bid - a.blocks * a.slabs) * 64;
+  const int v = v0 + (tid & 63);
+  long long lo = 0, hi = a.n;
+  while (lo < hi) {
+    const long long mid = (lo + hi) >> 1;
+    if (a.keys[mid] < v) lo = mid + 1;
+    else hi = mid;
+  }
+  const bool absent = v < a.rows && (lo == a.n || a.keys[lo] != v);
+  unsigned long long rows = __ballot(absent);
+  const int vecs = hv * (std::is_same_v<T, D> ? 1 : 2);
+  u32x4 *dw = static_cast<u32x4 *>(a.dw);
+  while (rows) {
+    const int r = __ffsll(rows) - 1;
+    rows &= rows - 1;
+    u32x4 *o = dw + static_cast<long long>(v0 + r) * vecs;
+    for (int k = tid; k < vecs; k += 256) o[k] = u32x4{0u, 0u, 0u, 0u};
+  }
+}
+
+// Sums that cross block edges: the block in which such a sum begins adds the
+// partial rows of the blocks it runs through, in order.
+template <class T, class D>
+__global__ __launch_bounds__(256) void k_sum_join(SumArgs a) {
+  constexpr int N = Vec<T>::N;
+  const int hv = a.hidden / N;
+  const int blk = static_cast<int>(blockIdx.x) / a.slabs;
+  const int k = (static_cast<int>(blockIdx.x) - blk * a.slabs) * 256 + static_cast<int>(threadIdx.x);
+  const long long j1 = static_cast<long long>(blk + 1) * a.per;
+  if (j1 >= a.n) return;
+  const int key = a.keys[j1 - 1];
+  if (key >= a.rows || a.keys[j1] != key) return;  // nothing crosses this edge
+  // a sum that began before this block is joined there
+  if (blk > 0 && a.keys[j1 - a.per - 1] == key) return;
+  if (k >= hv) return;
+  float sum[N];
+  const float *p = a.part + (static_cast<long long>(blk) * 2 + 1) * a.hidden + k * N;
+#pragma unroll
+  for (int e = 0; e < N; ++e) sum[e] = p[e];
+  for (int b = blk + 1; b < a.blocks && a.keys[static_cast<long long>(b) * a.per] == key; ++b) {
+    p = a.part + static_cast<long long>(b) * 2 * a.hidden + k * N;
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum[e] += p[e];
+  }
+  write_row<T, D>(a, key, k * N, sum);
+}
+
+__global__ __launch_bounds__(256) void k_zero(u32x4 *p, long long vecs) {
+  for (long long k = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; k < vecs;
+       k += static_cast<long long>(gridDim.x) * 256)
+    p[k] = u32x4{0u, 0u, 0u, 0u};
+}
+
+template <class F>
+void by_dtype(int dtype, F f) {
+  if (dtype == HG_BF16) f(TypeBf16{});
+  else if (dtype == HG_FP16) f(TypeF16{});
+  else f(TypeF32{});
+}
+
+}  // namespace
+
+hipError_t launch_embed(const VocabMatrix &w, int rows, int dtype, const void *tokens,
+                        int token_bytes, int n, float scale, void *out, hipStream_t s) {
+  by_dtype(dtype, [&](auto type) {
+    using T = decltype(type);
+    const int hv = w.hidden / Vec<T>::N;
+    const dim3 grid((hv + 255) / 256, n < 32768 ? n : 32768);
+    if (w.tp == 1) {
+      ShardTableN<1> t;
+      t.p[0] = w.t.p[0];
+      hipLaunchKernelGGL((k_embed<T, 1>), grid, dim3(256), 0, s, t, w.shard, rows, tokens,
+                         token_bytes, n, hv, scale, static_cast<u32x4 *>(out));
+    } else {
+      hipLaunchKernelGGL((k_embed<T, HG_MAX_TP>), grid, dim3(256), 0, s, w.t, w.shard, rows, tokens,
+                         token_bytes, n, hv, scale, static_cast<u32x4 *>(out));
+    }
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_zero(void *p, size_t bytes, hipStream_t s) {
+  const long long vecs = static_cast<long long>(bytes / 16);
+  if (vecs == 0) return hipSuccess;
+  const long long want = (vecs + 255) / 256;
+  hipLaunchKernelGGL(k_zero, dim3(static_cast<unsigned>(want < 8192 ? want : 8192)), dim3(256), 0,
+                     s, static_cast<u32x4 *>(p), vecs);
+  return hipGetLastError();
+}
+
+EmbedPlan embed_plan(int rows, int hidden, long long n) {
+  EmbedPlan p;
+  int bits = 1;
+  while ((1ll << bits) <= rows) ++bits;  // the largest key is `rows`
+  p.passes = (bits + 8) / 9;
+  p.tiles = static_cast<int>((n + kSortTile - 1) / kSortTile);
+  // Positions per block: at least 8 (the rows in flight), and no more blocks
+  // than about eight workgroups per CU need.
+  long long per = n / 2048;
+  p.per = static_cast<int>(per < 8 ? 8 : per > 256 ? 256 : per);
+  p.blocks = static_cast<int>((n + p.per - 1) / p.per);
+  const size_t ints = static_cast<size_t>(n) * sizeof(int);
+  auto up = [](size_t b) { return (b + 255) & ~static_cast<size_t>(255); };
+  size_t at = 0;
+  for (int k = 0; k < 4; ++k) {
+    p.off[k] = at;  // keys, positions, and the other side of each pass
+    at += up(ints);
+  }
+  p.off[4] = at;  // counts
+  at += up(static_cast<size_t>(p.tiles) * kDigits * sizeof(int));
+  p.off[5] = at;  // partial rows
+  at += up(static_cast<size_t>(p.blocks) * 2 * hidden * sizeof(float));
+  p.bytes = at;
+  return p;
+}
+
+hipError_t launch_embed_grad(const EmbedPlan &p, void *ws, int rows, int hidden, int dtype,
+                             const void *tokens, int token_bytes, long long n, const void *dy,
+                             float scale, void *dw, bool wide, bool accumulate, hipStream_t s) {
+  char *base = static_cast<char *>(ws);
+  int *buf[4], *hist = reinterpret_cast<int *>(base + p.off[4]);
+  for (int k = 0; k < 4; ++k) buf[k] = reinterpret_cast<int *>(base + p.off[k]);
+  int side = 0;
+  if (n > 0 && n <= kSortTile) {
+    hipLaunchKernelGGL(k_sort_tile, dim3(1), dim3(1024), 0, s, tokens, token_bytes,
+                       static_cast<int>(n), rows, p.passes, buf[0], buf[1]);
+  } else if (n > 0) {
+    for (int k = 0; k < p.passes; ++k) {
+      const int *ik = k ? buf[2 * side] : nullptr, *ip = k ? buf[2 * side + 1] : nullptr;
+      if (k) side ^= 1;
+      hipLaunchKernelGGL(k_sort_count, dim3(p.tiles), dim3(1024), 0, s, tokens, token_bytes, ik, n,
+                         rows, 9 * k, hist, p.tiles);
+      hipLaunchKernelGGL(k_sort_scan, dim3(1), dim3(1024), 0, s, hist, p.tiles * kDigits);
+      hipLaunchKernelGGL(k_sort_place, dim3(p.tiles), dim3(1024), 0, s, tokens, token_bytes, ik, ip,
+                         n, rows, 9 * k, hist, p.tiles, buf[2 * side], buf[2 * side + 1]);
+    }
+  }
+  by_dtype(dtype, [&](auto type) {
+    using T = decltype(type);
+    SumArgs a;
+    a.keys = buf[2 * side];
+    a.pos = buf[2 * side + 1];
+    a.dy = static_cast<const u32x4 *>(dy);
+    a.dw = dw;
+    a.part = reinterpret_cast<float *>(base + p.off[5]);
+    a.n = n;
+    a.rows = rows;
+    a.hidden = hidden;
+    a.per = p.per;
+    a.blocks = p.blocks;
+    a.slabs = (hidden / Vec<T>::N + 255) / 256;
+    a.scale = scale;
+    a.accumulate = accumulate ? 1 : 0;
+    const int sums = a.blocks * a.slabs, fills = accumulate ? 0 : (rows + 63) / 64;
+    auto go = [&](auto dtag) {
+      using D = decltype(dtag);
+      if (sums + fills > 0)
+        hipLaunchKernelGGL((k_sum<T, D>), dim3(sums + fills), dim3(256), 0, s, a);
+      if (a.blocks > 1)
+        hipLaunchKernelGGL((k_sum_join<T, D>), dim3((a.blocks - 1) * a.slabs), dim3(256), 0, s, a);
+    };
+    if constexpr (!std::is_same_v<T, TypeF32>) {
+      if (wide) {
+        go(TypeF32{});
+        return;
+      }
+    }
+    go(type);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace hg

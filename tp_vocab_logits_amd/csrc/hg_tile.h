@@ -1,0 +1,398 @@
+// The 256 x 256 matrix-product tile of the vocabulary operators, on gfx950
+// matrix cores: 16-bit operands, fp32 accumulation in registers.
+//
+// C[m][n] = sum_k A[m][k] B[n][k] for one 256 x 256 tile. Either operand may
+// lie in memory with k contiguous in a row ("row" operands: [m][k]) or with k
+// as the row index ("column" operands: [k][m]); the column form is turned
+// while it is read from LDS (ds_read_b64_tr_b16), so no operand is ever
+// transposed in memory.
+//
+// LDS: two stages of 64 k; a stage is eight 64 x 64 sub-tiles of 8 KB (four
+// of A, four of B), 128 bytes per LDS row (a row is an m for a row operand, a
+// k for a column operand). Sub-tiles arrive by buffer loads straight into LDS,
+// 1 KB (8 LDS rows) per instruction; the lanes' global addresses carry the
+// swizzle of the eight 16-byte chunks of a row that keeps the fragment reads
+// off one another's banks:
+//   row operand:    chunk ^ ((row >> 1) & 7); a fragment read takes 16
+//                   consecutive rows at one chunk
+//   column operand: chunk ^ 2*f(k), f(k) = bit 1 of k | bit 3 of k << 1; a
+//                   transposed read takes 8 k rows (k0..k0+3 and k0+8..k0+11)
+//                   at one pair of chunks
+//
+// Waves: 8, as 2 (m) x 4 (n); a wave owns 128 x 64 of C as 8 x 4 blocks of
+// v_mfma_f32_16x16x32. The operands are given to the MFMA in the order (B, A),
+// so a lane holds four consecutive n of one m: the epilogues store 8 or 16
+// bytes at a time and reduce over n mostly inside the lane.
+//
+// Schedule: the two waves of a SIMD (w and w + 4) alternate between reading
+// fragments and multiplying. A step of 64 k has two phases per wave -- the
+// upper and the lower 64 rows of A, each against the wave's 64 columns of B --
+// and each phase is a memory part (fragment reads, loads of later steps into
+// sub-tiles whose last reader is done) and a part of 32 MFMAs, with a barrier
+// after each. Waves 4-7 run one barrier behind, so that one wave of every SIMD
+// multiplies while the other one reads.
+//   memory part 1 of step k reads A's upper half and B, and loads A's lower
+//   half of step k+1; part 2 reads A's lower half, and loads B and A's upper
+//   half of step k+2. Each ends with vmcnt(8): everything but the newest eight
+//   loads of the wave has landed, which is what the next part reads.
+// Loads past the last step, past K or past an operand's rows lie beyond their
+// buffer resource, which fills LDS with zeros without touching memory: the
+// counts stay the same to the end and no operand needs padding.
+#pragma once
+
+#include "hg_internal.h"
+
+namespace hg {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+// The two 16-bit types: their product and their rounding (to nearest even).
+struct TypeBf16 {
+  using elt = __bf16;
+  static __device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static constexpr bool kHalf = false;
+};
+struct TypeF16 {
+  using elt = _Float16;
+  static __device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static constexpr bool kHalf = true;
+};
+
+template <class T>
+__device__ __forceinline__ uint32_t bits16(float f) {
+  return __builtin_bit_cast(unsigned short, static_cast<typename T::elt>(f));
+}
+template <class T>
+__device__ __forceinline__ float from16(uint32_t b) {
+  return static_cast<float>(__builtin_bit_cast(typename T::elt, static_cast<unsigned short>(b)));
+}
+
+constexpr int kTile = 256;           // C tile edge
+constexpr int kStep = 64;            // k per step
+constexpr int kSubBytes = 64 * 128;  // one 64 x 64 sub-tile
+constexpr int kStageBytes = 8 * kSubBytes;
+constexpr int kTileLds = 2 * kStageBytes;
+constexpr unsigned kBeyond = 0x80000000u;  // an offset past every buffer resource used here
+constexpr int kRawWord3 = 0x00020000;      // buffer resource word 3: raw 32-bit data
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void *base, long long bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0,
+                                           bytes > 0 ? static_cast<int>(bytes) : 0, kRawWord3);
+}
+
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, unsigned char *lds,
+                                         unsigned offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      r, (__attribute__((address_space(3))) void *)lds, 16, offset, 0, 0, 0);
+}
+
+// Lane constants of the loads: LDS row l >> 3 of the instruction's eight, slot
+// l & 7; the chunk that belongs there, by the parity of the instruction.
+struct LoadLane {
+  int row;
+  int chunk[2];
+};
+template <bool COLUMN>
+__device__ __forceinline__ LoadLane load_lane(int lane) {
+  LoadLane p;
+  p.row = lane >> 3;
+#pragma unroll
+  for (int odd = 0; odd < 2; ++odd)
+    p.chunk[odd] = COLUMN ? (lane & 7) ^ ((((lane >> 4) & 1) | (odd << 1)) << 1)
+                          : (lane & 7) ^ ((odd << 2) | (lane >> 4));
+  return p;
+}
+
+// Operand sources. load(lds, sub, q, step): instruction q (LDS rows 8q..8q+7)
+// of sub-tile `sub` at step `step`.
+
+// Row operand in one matrix: row m of the tile at base + m*stride bytes, k
+// from the base on; `rows` rows below the matrix's end, K a multiple of 8.
+struct RowSource {
+  static constexpr bool kColumn = false;
+  __amdgpu_buffer_rsrc_t r;
+  unsigned off[2];
+  int chunk[2];
+  int k8, stride;
+  __device__ __forceinline__ void init(const void *base, int rows, int stride_bytes, int k_,
+                                       long long bytes, int lane) {
+    const LoadLane p = load_lane<false>(lane);
+    r = resource(base, rows > 0 ? bytes : 0);
+    stride = stride_bytes;
+    k8 = k_ >> 3;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      chunk[o] = p.chunk[o];
+      off[o] = static_cast<unsigned>(p.row * stride_bytes + p.chunk[o] * 16);
+    }
+  }
+  __device__ __forceinline__ void load(unsigned char *lds, int sub, int q, int step) const {
+    const int o = q & 1;
+    const unsigned v = off[o] + static_cast<unsigned>((64 * sub + 8 * q) * stride + step * 128);
+    load_lds(r, lds + q * 1024, step * 8 + chunk[o] < k8 ? v : kBeyond);
+  }
+};
+
+// Row operand in rank blocks (NT table entries): tile row m is matrix row
+// n0 + m. Blocks are a multiple of 32 rows, so eight rows share a block. A
+// wave always loads the same four instructions of the same sub-tile, so it
+// keeps one resource for each.
+template <int NT>
+struct RankRowSource {
+  static constexpr bool kColumn = false;
+  __amdgpu_buffer_rsrc_t r[4];
+  unsigned off[2];
+  int chunk[2];
+  int k8;
+  __device__ __forceinline__ void init(const ShardTableN<NT> &w, int shard, int limit, int hidden,
+                                       int n0, int sub, int q0, int lane) {
+    const LoadLane p = load_lane<false>(lane);
+    k8 = hidden >> 3;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      chunk[o] = p.chunk[o];
+      off[o] = static_cast<unsigned>(p.row * hidden * 2 + p.chunk[o] * 16);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int n = n0 + 64 * sub + 8 * (q0 + t);
+      const int left = limit - n;
+      const int rank = NT == 1 || left <= 0 ? 0 : n / shard;
+      const int at = left <= 0 ? 0 : n - rank * shard;
+      const unsigned char *base = reinterpret_cast<const unsigned char *>(w.p[rank]) +
+                                  static_cast<long long>(at) * hidden * 2;
+      r[t] = resource(base, left <= 0 ? 0 : (left < 8 ? left : 8) * hidden * 2);
+    }
+  }
+  __device__ __forceinline__ void load(unsigned char *lds, int, int q, int step) const {
+    const int o = q & 1;
+    load_lds(r[q & 3], lds + q * 1024,
+             step * 8 + chunk[o] < k8 ? off[o] + static_cast<unsigned>(step * 128) : kBeyond);
+  }
+};
+
+// Column operand in one matrix: k row k at base + k*stride bytes, the tile's
+// columns from `col` on; K rows.
+struct ColumnSource {
+  static constexpr bool kColumn = true;
+  const unsigned char *base;
+  unsigned off[2];
+  int rows, stride, col;
+  __device__ __forceinline__ void init(const void *base_, int col_, int rows_, int stride_bytes,
+                                       int lane) {
+    const LoadLane p = load_lane<true>(lane);
+    base = static_cast<const unsigned char *>(base_) + static_cast<long long>(col_) * 2;
+    col = col_;
+    rows = rows_;
+    stride = stride_bytes;
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+      off[o] = static_cast<unsigned>(p.row * stride_bytes + p.chunk[o] * 16);
+  }
+  __device__ __forceinline__ void load(unsigned char *lds, int sub, int q, int step) const {
+    const int k = step * 64 + 8 * q;
+    const int left = rows - k;
+    // the last row ends `col` columns early, counted from this base
+    const int n = left <= 0 ? 0 : left > 8 ? 8 * stride : left * stride - 2 * col;
+    const __amdgpu_buffer_rsrc_t r =
+        resource(base + static_cast<long long>(left <= 0 ? 0 : k) * stride, n);
+    load_lds(r, lds + q * 1024, off[q & 1] + static_cast<unsigned>(sub * 128));
+  }
+};
+
+// Column operand in rank blocks: k row k is matrix row v0 + k (v0 a multiple
+// of 8); rows from `limit` on read as zero.
+template <int NT>
+struct RankColumnSource {
+  static constexpr bool kColumn = true;
+  const ShardTableN<NT> *w;
+  unsigned off[2];
+  int shard, limit, v0, stride, col;
+  __device__ __forceinline__ void init(const ShardTableN<NT> &w_, int shard_, int limit_, int v0_,
+                                       int col_, int hidden, int lane) {
+    const LoadLane p = load_lane<true>(lane);
+    w = &w_;
+    shard = shard_;
+    limit = limit_;
+    v0 = v0_;
+    col = col_;
+    stride = hidden * 2;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) off[o] = static_cast<unsigned>(p.row * stride + p.chunk[o] * 16);
+  }
+  __device__ __forceinline__ void load(unsigned char *lds, int sub, int q, int step) const {
+    const int v = v0 + step * 64 + 8 * q;
+    const int left = limit - v;
+    const int rank = NT == 1 || left <= 0 ? 0 : v / shard;
+    const int at = left <= 0 ? 0 : v - rank * shard;
+    // the resource stays inside the block: 8 rows, less the columns before
+    // this tile's at its end (reads past a row's end belong to columns that no
+    // one stores)
+    const int n = left <= 0 ? 0 : (left < 8 ? left : 8) * stride - 2 * col;
+    const unsigned char *base = reinterpret_cast<const unsigned char *>(w->p[rank]) +
+                                static_cast<long long>(at) * stride + 2 * col;
+    load_lds(resource(base, n), lds + q * 1024, off[q & 1] + static_cast<unsigned>(sub * 128));
+  }
+};
+
+// Fragment of a 16-row block: eight consecutive k (of the step's slice ks) of
+// one row per lane.
+template <bool COLUMN>
+struct FragLane {
+  int off[COLUMN ? 4 : 2];
+  __device__ __forceinline__ void init(int lane) {
+    const int i = lane & 15, g = lane >> 4;
+    if constexpr (COLUMN) {
+      const int f = (i >> 3) | ((g & 1) << 1);
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        off[b] = (g * 8 + (i >> 2)) * 128 + ((b ^ f) << 5) + (i & 3) * 8;
+    } else {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) off[ks] = i * 128 + (((ks * 4 + g) ^ (i >> 1)) << 4);
+    }
+  }
+  __device__ __forceinline__ s16x8 read(const unsigned char *sub, int block, int ks) const {
+    if constexpr (COLUMN) {
+      typedef __attribute__((address_space(3))) s16x4 *lds4;
+      const unsigned char *p = sub + off[block] + ks * 32 * 128;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(p + 4 * 128));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      return *reinterpret_cast<const s16x8 *>(sub + off[ks] + block * 16 * 128);
+    }
+  }
+};
+
+// s_waitcnt vmcnt(N) lgkmcnt(0) (N < 64).
+template <int N>
+__device__ __forceinline__ void wait_vm_lds() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x70);
+}
+
+__device__ __forceinline__ void tile_barrier() {
+  __asm__ __volatile__("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  __asm__ __volatile__("" ::: "memory");
+}
+
+// acc[i][j]: rows 128*(wave >> 2) + 16*i + (lane & 15), columns
+// 64*(wave & 3) + 16*j + 4*(lane >> 4) + t of the tile. On return every load
+// has landed and every wave is past its last LDS read.
+template <class T, class SA, class SB>
+__device__ __forceinline__ void tile_product(const SA &a, const SB &b, int steps,
+                                             unsigned char *lds, f32x4 (&acc)[8][4]) {
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int wr = wave >> 2, wc = wave & 3;
+  FragLane<SA::kColumn> fa;
+  FragLane<SB::kColumn> fb;
+  fa.init(lane);
+  fb.init(lane);
+
+  // A: each half (64 rows) of the wave's 128 is a sub-tile, loaded by the
+  // four waves that read it; B: sub-tile wc, half of it per wave.
+  auto load_a = [&](int half, int step) __attribute__((always_inline)) {
+    const int sub = 2 * wr + half;
+    unsigned char *st = lds + (step & 1) * kStageBytes + sub * kSubBytes;
+    a.load(st, sub, 2 * wc, step);
+    a.load(st, sub, 2 * wc + 1, step);
+  };
+  auto load_b = [&](int step) __attribute__((always_inline)) {
+    unsigned char *st = lds + (step & 1) * kStageBytes + (4 + wc) * kSubBytes;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) b.load(st, wc, 4 * wr + t, step);
+  };
+
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  load_b(0);
+  load_a(0, 0);
+  load_a(1, 0);
+  load_b(1);
+  load_a(0, 1);
+  wait_vm_lds<8>();
+  tile_barrier();
+  if (wr == 1) tile_barrier();
+
+  s16x8 ra[4][2], rb[4][2];
+  auto multiply = [&](int half) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[4 * half + i][j] = T::mma(rb[j][ks], ra[i][ks], acc[4 * half + i][j]);
+    __builtin_amdgcn_s_setprio(0);
+  };
+  for (int kb = 0; kb < steps; ++kb) {
+    const unsigned char *st = lds + (kb & 1) * kStageBytes;
+    const unsigned char *sa = st + 2 * wr * kSubBytes;
+    const unsigned char *sb = st + (4 + wc) * kSubBytes;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) rb[j][ks] = fb.read(sb, j, ks);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ra[i][ks] = fa.read(sa, i, ks);
+    }
+    load_a(1, kb + 1);
+    wait_vm_lds<8>();
+    tile_barrier();
+    multiply(0);
+    tile_barrier();
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ra[i][ks] = fa.read(sa + kSubBytes, i, ks);
+    load_b(kb + 2);
+    load_a(0, kb + 2);
+    wait_vm_lds<8>();
+    tile_barrier();
+    multiply(1);
+    tile_barrier();
+  }
+  if (wr == 0) tile_barrier();
+  wait_vm_lds<0>();
+  tile_barrier();
+}
+
+// Tile `id` of tm x tn: groups of 8 tile rows, columns inside a group, rows
+// fastest, so that the workgroups in flight on an XCD share operands in its
+// L2. Workgroups are dealt to the 8 XCDs in turn; each XCD gets a contiguous
+// run of ids.
+__device__ __forceinline__ void tile_at(int bid, int total, int tm, int tn, int *z, int *mt,
+                                        int *nt) {
+  const int xcd = bid & 7, local = bid >> 3;
+  const int per = total >> 3, more = total & 7;
+  int id = xcd * per + (xcd < more ? xcd : more) + local;
+  const int plane = tm * tn;
+  *z = id / plane;
+  id -= *z * plane;
+  const int group = id / (8 * tn);
+  const int first = group * 8;
+  const int gm = tm - first < 8 ? tm - first : 8;
+  const int in = id - group * 8 * tn;
+  *mt = first + in % gm;
+  *nt = in / gm;
+}
+
+}  // namespace hg

@@ -1,0 +1,89 @@
+// Internal declarations of the vocabulary matrix's training operators: the
+// softmax cross entropy of the lm_head product (hg_xent.hip) and the
+// embedding lookup with its gradient (hg_embed.hip). The C ABI is in
+// include/hg.h; argument checks and workspace layout in hg_vocab_api.cpp.
+#pragma once
+
+#include "hg_internal.h"
+
+namespace hg {
+
+// Rank blocks of the vocabulary matrix. Blocks that follow one another in
+// memory are one block of tp*shard rows (NT = 1); others keep the table.
+struct VocabMatrix {
+  ShardTable t;
+  int tp;       // table entries in use: 1 when the blocks are contiguous
+  int shard;    // rows per entry
+  int hidden;
+};
+
+// Per-row work arrays of the cross entropy, in the caller's workspace. Rows
+// that count are packed: packed row p is row idx[p] of the call.
+struct XentRows {
+  int *head;      // [0] packed rows, [1] bits of the largest gradient factor (fp32)
+  int *idx;       // [m] packed -> row
+  int *inv;       // [m] row -> packed, or -1
+  int *lab;       // [m] packed labels
+  float *zt;      // [m] packed: the label's logit
+  float *lse2;    // [m] packed: log-sum-exp in base 2
+  float *ca;      // [m] packed: factor of the probability in d
+  float *cb;      // [m] packed: factor of the label's one in d
+};
+
+struct XentPlan {
+  int m, hidden, vocab, rows;  // rows = tp*shard
+  bool half;                   // fp16 inputs (bf16 otherwise)
+  float scale, z_weight;
+  long long ignore;
+  int label_bytes;
+  int piece;       // vocabulary columns per piece, a multiple of 256
+  int split_dx;    // splits of the vocabulary in dX = d W
+  int split_dw;    // splits of the rows in dW = d^T X
+  int dw_rows;     // matrix rows of one split's partial sums
+  XentRows r;
+  void *xc;        // [m][hidden] packed rows of X
+  void *d;         // [m][piece] d (or unnormalised probabilities) of one piece
+  float *part;     // [2][tiles][m] per 256-column tile: maximum (base 2), sum
+  float *dxp;      // [split_dx][m][hidden]
+  float *dwp;      // [split_dw][dw_rows][hidden] when split_dw > 1
+};
+
+hipError_t launch_xent_pack(const XentPlan &p, const void *x, const void *labels, float *loss,
+                            float *lse, hipStream_t s);
+// Logits of columns v0 .. v0+cols-1: mode 0 keeps the row statistics alone, 1
+// also the unnormalised probabilities, 2 writes d (the row factors are known).
+hipError_t launch_xent_logits(const XentPlan &p, const VocabMatrix &w, int mode, int v0, int cols,
+                              hipStream_t s);
+// Row statistics -> loss, lse and the rows' factors (grad null: none).
+hipError_t launch_xent_join(const XentPlan &p, const float *grad, float *loss, float *lse,
+                            hipStream_t s);
+// The rows' factors for a known lse.
+hipError_t launch_xent_factors(const XentPlan &p, const float *lse, const float *grad,
+                               hipStream_t s);
+// Unnormalised probabilities -> d, in place.
+hipError_t launch_xent_normalise(const XentPlan &p, hipStream_t s);
+hipError_t launch_xent_dx(const XentPlan &p, const VocabMatrix &w, int v0, int cols, bool first,
+                          hipStream_t s);
+hipError_t launch_xent_dx_join(const XentPlan &p, void *dx, hipStream_t s);
+hipError_t launch_xent_dw(const XentPlan &p, int v0, int cols, void *dw, bool wide, bool accumulate,
+                          hipStream_t s);
+
+// `bytes` zero bytes at a 16-byte aligned address (bytes a multiple of 16).
+hipError_t launch_zero(void *p, size_t bytes, hipStream_t s);
+
+// out[j] = scale * W[tokens[j]], zero for tokens outside 0 .. rows-1.
+hipError_t launch_embed(const VocabMatrix &w, int rows, int dtype, const void *tokens,
+                        int token_bytes, int n, float scale, void *out, hipStream_t s);
+
+// Sort passes and workspace of an embedding gradient over n tokens.
+struct EmbedPlan {
+  int passes, tiles;
+  int per, blocks;  // sorted positions per block of the sums
+  size_t off[6], bytes;
+};
+EmbedPlan embed_plan(int rows, int hidden, long long n);
+hipError_t launch_embed_grad(const EmbedPlan &p, void *ws, int rows, int hidden, int dtype,
+                             const void *tokens, int token_bytes, long long n, const void *dy,
+                             float scale, void *dw, bool wide, bool accumulate, hipStream_t s);
+
+}  // namespace hg

@@ -1,0 +1,609 @@
+// Softmax cross entropy of the lm_head product, on gfx950 matrix cores,
+// without keeping the logits.
+//
+// For the rows i that count (label t_i, not the ignored value), logits over
+// the real vocabulary v < vocab of the rank blocks W_r (rank r at r*shard):
+//   z_iv = scale * x_i . W_v
+//   lse_i = log sum_v exp z_iv
+//   loss_i = lse_i - z_it + z_weight * lse_i^2
+//   d_iv = scale * g_i * ((1 + 2 z_weight lse_i) exp(z_iv - lse_i) - [v = t_i])
+//   dx_i = sum_v d_iv W_v,   dW_v = sum_i d_iv x_i
+//
+// The rows that count are packed first (k_pack, k_pack_rows): rows left out
+// cost nothing in the products, and what their x holds (NaN, infinities) is
+// never multiplied. All products then run over the packed rows, whose number
+// stays on the device.
+//
+// Logits: 256 x 256 tiles (hg_tile.h). The epilogue reduces each row of its
+// tile to a maximum and a sum of exponentials (one pass, in base 2, fp32);
+// k_join merges a row's tiles. For the gradient either
+//  - the epilogue also stores the unnormalised probabilities exp(z - tile
+//    maximum), and k_normalise turns them into d once lse is known: the logits
+//    are computed once (hg_xent_step), or
+//  - lse is known, and the epilogue writes d itself (hg_xent_grad, and steps
+//    whose workspace holds fewer columns than the vocabulary).
+// d is 16 bits wide, as the matrix cores take it. fp16 has 5 exponent bits:
+// there the probabilities are scaled by 2^15 and d by a power of two that
+// brings its largest row factor to 2^13..2^14, so that probabilities down to
+// about 2^-27 of the largest keep all their bits; both scales are exact and
+// are taken back in fp32. Each of the two roundings is off by at most half a
+// step of the type and falls on single terms of sums over many.
+
+#include <type_traits>
+
+#include "hg_tile.h"
+#include "hg_vocab.h"
+
+namespace hg {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kHalfProb = 32768.f;  // scale of fp16 probabilities
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The power of two by which d is scaled (and its inverse): 1 for bf16.
+template <class T>
+__device__ __forceinline__ float d_scale(const XentRows &r, bool inverse) {
+  if constexpr (!T::kHalf) return 1.f;
+  // 2^(13 - exponent of the largest factor): products end in 2^13..2^14
+  const int e = static_cast<int>((static_cast<unsigned>(r.head[1]) >> 23) & 255u);
+  int up = e == 0 ? 0 : 13 - (e - 127);
+  up = up > 126 ? 126 : up < -126 ? -126 : up;
+  return __builtin_bit_cast(float, static_cast<unsigned>(127 + (inverse ? -up : up)) << 23);
+}
+
+__device__ __forceinline__ long long label_at(const void *labels, int bytes, int i) {
+  return bytes == 8 ? static_cast<const long long *>(labels)[i]
+                    : static_cast<const int *>(labels)[i];
+}
+
+// Packs the rows that count, in order: one workgroup walks the labels 1024 at
+// a time (a running total in LDS). A row left out gets loss = lse = 0, a label
+// outside the vocabulary loss = lse = NaN and no part in the gradients.
+__global__ __launch_bounds__(1024) void k_pack(XentRows r, const void *labels, int label_bytes,
+                                               int m, int vocab, long long ignore, float *loss,
+                                               float *lse) {
+  __shared__ int wave_sum[16];
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+  int base = 0;
+  for (int i0 = 0; i0 < m; i0 += 1024) {
+    const int i = i0 + tid;
+    const long long t = i < m ? label_at(labels, label_bytes, i) : ignore;
+    const bool out = t == ignore;
+    const bool kept = i < m && !out && t >= 0 && t < vocab;
+    const unsigned long long votes = __ballot(kept);
+    if (lane == 0) wave_sum[wave] = __popcll(votes);
+    __syncthreads();
+    int before = base, total = 0;
+    for (int k = 0; k < 16; ++k) {
+      if (k < wave) before += wave_sum[k];
+      total += wave_sum[k];
+    }
+    const int p = before + __popcll(votes & ((1ull << lane) - 1));
+    if (kept) {
+      r.idx[p] = i;
+      r.lab[p] = static_cast<int>(t);
+    }
+    if (i < m) {
+      r.inv[i] = kept ? p : -1;
+      if (!kept && loss) {
+        const float v = out ? 0.f : __builtin_nanf("");
+        loss[i] = v;
+        lse[i] = v;
+      }
+    }
+    base += total;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    r.head[0] = base;
+    r.head[1] = 0;
+  }
+}
+
+// The packed rows' x, 16 bytes per lane.
+__global__ __launch_bounds__(256) void k_pack_rows(XentRows r, const u32x4 *x, u32x4 *xc, int m,
+                                                   int hv) {
+  const int kept = r.head[0];
+  for (int p = static_cast<int>(blockIdx.x); p < kept; p += static_cast<int>(gridDim.x)) {
+    const u32x4 *src = x + static_cast<long long>(r.idx[p]) * hv;
+    u32x4 *dst = xc + static_cast<long long>(p) * hv;
+    for (int k = static_cast<int>(threadIdx.x); k < hv; k += 256) dst[k] = src[k];
+  }
+}
+
+enum LogitsMode { kStats = 0, kProb = 1, kGrad = 2 };
+
+template <class T, int NT, int MODE>
+__global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc, ShardTableN<NT> w,
+                                                   int shard, int v0, int vend, int tm, int tn) {
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[kTileLds];
+  int z, mt, nt;
+  tile_at(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), tm, tn, &z, &mt, &nt);
+  const int kept = pl.r.head[0];
+  const int m0 = mt * kTile, n0 = v0 + nt * kTile;
+  if (m0 >= kept) return;
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int wr = wave >> 2, wc = wave & 3, l16 = lane & 15, g = lane >> 4;
+
+  RowSource a;
+  const int rows = kept - m0 < kTile ? kept - m0 : kTile;
+  a.init(xc + static_cast<long long>(m0) * (pl.hidden >> 3), rows, pl.hidden * 2, pl.hidden,
+         static_cast<long long>(rows) * pl.hidden * 2, lane);
+  RankRowSource<NT> b;
+  b.init(w, shard, vend, pl.hidden, n0, wc, 4 * wr, lane);
+  f32x4 acc[8][4];
+  tile_product<T>(a, b, (pl.hidden + kStep - 1) / kStep, lds, acc);
+
+  const float s2 = pl.scale * kLog2e;
+  const int nl = n0 + 64 * wc + 4 * g;  // the lane's column of block 0
+  unsigned short *dout = static_cast<unsigned short *>(pl.d);
+  if constexpr (MODE == kGrad) {
+    const float up = d_scale<T>(pl.r, false);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = m0 + 128 * wr + 16 * i + l16;
+      if (row >= kept) continue;
+      const float lse2 = pl.r.lse2[row], ca = pl.r.ca[row] * up, cb = pl.r.cb[row] * up;
+      const int lab = pl.r.lab[row];
+      unsigned short *o = dout + static_cast<long long>(row) * pl.piece + (nl - v0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t q[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int n = nl + 16 * j + t;
+          float v = exp2_(acc[i][j][t] * s2 - lse2) * ca;
+          v = n == lab ? v - cb : v;
+          q[t] = n < vend ? bits16<T>(v) : 0u;
+        }
+        *reinterpret_cast<uint2 *>(o + 16 * j) = uint2{q[0] | q[1] << 16, q[2] | q[3] << 16};
+      }
+    }
+    return;
+  } else {
+    // A row's 256 columns lie in 4 waves x 4 lane groups x 16 registers: the
+    // maximum, then the sum of exponentials, each reduced in registers, over
+    // the lane groups, and over the waves through LDS.
+    float *red = reinterpret_cast<float *>(lds);  // [4][256] maxima, then [4][256] sums
+    float top[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float mx = -__builtin_inff();
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int n = nl + 16 * j + t;
+          acc[i][j][t] = n < vend ? acc[i][j][t] * s2 : -__builtin_inff();
+          mx = fmaxf(mx, acc[i][j][t]);
+        }
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      if (g == 0) red[wc * kTile + 128 * wr + 16 * i + l16] = mx;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = 128 * wr + 16 * i + l16;
+      const float mx = fmaxf(fmaxf(red[at], red[kTile + at]),
+                             fmaxf(red[2 * kTile + at], red[3 * kTile + at]));
+      top[i] = mx == -__builtin_inff() ? 0.f : mx;  // a row of -inf: every exponential is 0
+    }
+    float *sums = red + 4 * kTile;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = m0 + 128 * wr + 16 * i + l16;
+      const int lab = row < kept ? pl.r.lab[row] - nl : -1;
+      float sum = 0.f, zt = 0.f;
+      bool mine = false;
+      unsigned short *o = dout + static_cast<long long>(row) * pl.piece + (nl - v0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t q[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float e = exp2_(acc[i][j][t] - top[i]);
+          sum += e;
+          if (lab == 16 * j + t) {
+            zt = acc[i][j][t];
+            mine = true;
+          }
+          if (MODE == kProb) q[t] = bits16<T>(T::kHalf ? e * kHalfProb : e);
+        }
+        if (MODE == kProb && row < kept)
+          *reinterpret_cast<uint2 *>(o + 16 * j) = uint2{q[0] | q[1] << 16, q[2] | q[3] << 16};
+      }
+      if (mine) pl.r.zt[row] = zt;
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (g == 0) sums[wc * kTile + 128 * wr + 16 * i + l16] = sum;
+      top[i] = sum;
+    }
+    __syncthreads();
+    const int at = static_cast<int>(threadIdx.x);
+    if (at < kTile && m0 + at < kept) {
+      const float mx = fmaxf(fmaxf(red[at], red[kTile + at]),
+                             fmaxf(red[2 * kTile + at], red[3 * kTile + at]));
+      const float sum = (sums[at] + sums[kTile + at]) + (sums[2 * kTile + at] + sums[3 * kTile + at]);
+      const int tiles = (pl.vocab + kTile - 1) / kTile;
+      float *part = pl.part + static_cast<long long>(n0 / kTile) * pl.m + m0 + at;
+      part[0] = mx;
+      part[static_cast<long long>(tiles) * pl.m] = sum;
+    }
+  }
+}
+
+// One wave of 16 rows x 16 tile lanes... merges a row's tiles: 16 rows per
+// workgroup of 256, 16 threads a row.
+__global__ __launch_bounds__(256) void k_join(XentPlan pl, const float *grad, float *loss,
+                                              float *lse) {
+  __shared__ float smax[16][17], ssum[16][17];
+  const int kept = pl.r.head[0];
+  const int tiles = (pl.vocab + kTile - 1) / kTile;
+  const int c = static_cast<int>(threadIdx.x) & 15, k = static_cast<int>(threadIdx.x) >> 4;
+  const int row = static_cast<int>(blockIdx.x) * 16 + c;
+  float mx = -__builtin_inff(), sum = 0.f;
+  if (row < kept) {
+    const float *pm = pl.part + row;
+    const float *ps = pm + static_cast<long long>(tiles) * pl.m;
+    for (int t = k; t < tiles; t += 16) {
+      const float a = pm[static_cast<long long>(t) * pl.m], b = ps[static_cast<long long>(t) * pl.m];
+      const float hi = fmaxf(mx, a);
+      const float ref = hi == -__builtin_inff() ? 0.f : hi;
+      sum = sum * exp2_(mx - ref) + b * exp2_(a - ref);
+      mx = hi;
+    }
+  }
+  smax[k][c] = mx;
+  ssum[k][c] = sum;
+  __syncthreads();
+  if (k != 0 || row >= kept) return;
+  for (int t = 1; t < 16; ++t) mx = fmaxf(mx, smax[t][c]);
+  const float ref = mx == -__builtin_inff() ? 0.f : mx;
+  sum = 0.f;
+  for (int t = 0; t < 16; ++t) sum += ssum[t][c] * exp2_(smax[t][c] - ref);
+  const float l2 = ref + __log2f(sum);
+  const float l = l2 * kLn2;
+  const int i = pl.r.idx[row];
+  // the difference in base 2 first: lse and the label's logit may be close
+  loss[i] = (l2 - pl.r.zt[row]) * kLn2 + pl.z_weight * l * l;
+  lse[i] = l;
+  if (!grad) return;
+  const float u = pl.scale * grad[i];
+  const float ca = u * (1.f + 2.f * pl.z_weight * l);
+  pl.r.lse2[row] = l2;
+  pl.r.ca[row] = ca;
+  pl.r.cb[row] = u;
+  const float f = fmaxf(fabsf(u), fabsf(ca));
+  if (f < __builtin_inff()) atomicMax(pl.r.head + 1, __builtin_bit_cast(int, f));
+}
+
+__global__ __launch_bounds__(256) void k_factors(XentPlan pl, const float *lse, const float *grad) {
+  const int row = static_cast<int>(blockIdx.x) * 256 + static_cast<int>(threadIdx.x);
+  if (row >= pl.r.head[0]) return;
+  const int i = pl.r.idx[row];
+  const float l = lse[i], u = pl.scale * grad[i];
+  const float ca = u * (1.f + 2.f * pl.z_weight * l);
+  pl.r.lse2[row] = l * kLog2e;
+  pl.r.ca[row] = ca;
+  pl.r.cb[row] = u;
+  const float f = fmaxf(fabsf(u), fabsf(ca));
+  if (f < __builtin_inff()) atomicMax(pl.r.head + 1, __builtin_bit_cast(int, f));
+}
+
+// Unnormalised probabilities -> d in place: 16 bytes (8 columns) per lane and
+// step. HBM-bound: reads and writes d once.
+template <class T>
+__global__ __launch_bounds__(256) void k_normalise(XentPlan pl) {
+  const int kept = pl.r.head[0];
+  const int vecs = pl.piece >> 3;
+  const float up = d_scale<T>(pl.r, false);
+  for (int row = static_cast<int>(blockIdx.y); row < kept; row += static_cast<int>(gridDim.y)) {
+    const float lse2 = pl.r.lse2[row], ca = pl.r.ca[row] * up, cb = pl.r.cb[row] * up;
+    const int lab = pl.r.lab[row];
+    u32x4 *d = static_cast<u32x4 *>(pl.d) + static_cast<long long>(row) * vecs;
+    for (int k = static_cast<int>(blockIdx.x * 256 + threadIdx.x); k < vecs;
+         k += static_cast<int>(gridDim.x) * 256) {
+      const float mx = pl.part[static_cast<long long>(k >> 5) * pl.m + row];
+      const float ref = mx == -__builtin_inff() ? 0.f : mx;
+      const float c = exp2_(ref - lse2) * (T::kHalf ? ca * (1.f / kHalfProb) : ca);
+      u32x4 v = d[k];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        float lo = from16<T>(v[t] & 0xFFFFu) * c, hi = from16<T>(v[t] >> 16) * c;
+        if (lab == 8 * k + 2 * t) lo -= cb;
+        if (lab == 8 * k + 2 * t + 1) hi -= cb;
+        v[t] = bits16<T>(lo) | bits16<T>(hi) << 16;
+      }
+      d[k] = v;
+    }
+  }
+}
+
+// dX = d W over the piece's columns, split over the vocabulary; fp32 partial
+// sums, joined in a fixed order by k_dx_join.
+template <class T, int NT>
+__global__ __launch_bounds__(512, 2) void k_dx(XentPlan pl, ShardTableN<NT> w, int shard, int v0,
+                                               int vend, int per, int first, int tm, int tn) {
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[kTileLds];
+  int z, mt, nt;
+  tile_at(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), tm, tn, &z, &mt, &nt);
+  const int kept = pl.r.head[0];
+  const int m0 = mt * kTile, n0 = nt * kTile;
+  if (m0 >= kept) return;
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int k0 = z * per * kStep;            // the split's first column of the piece
+  int k1 = k0 + per * kStep;
+  if (k1 > vend - v0) k1 = vend - v0;
+  const int steps = k1 > k0 ? (k1 - k0 + kStep - 1) / kStep : 0;
+  RowSource a;
+  const int rows = kept - m0 < kTile ? kept - m0 : kTile;
+  const int stride = pl.piece * 2;
+  // d's columns past the vocabulary are zero up to a multiple of 256
+  a.init(static_cast<const unsigned char *>(pl.d) + static_cast<long long>(m0) * stride + 2 * k0,
+         rows, stride, steps * kStep, static_cast<long long>(rows) * stride - 2 * k0, lane);
+  RankColumnSource<NT> b;
+  b.init(w, shard, v0 + (k1 > k0 ? k1 : k0), v0 + k0, n0, pl.hidden, lane);
+  f32x4 acc[8][4];
+  tile_product<T>(a, b, steps, lds, acc);
+  const int wr = wave >> 2, wc = wave & 3, l16 = lane & 15, g = lane >> 4;
+  float *out = pl.dxp + static_cast<long long>(z) * pl.m * pl.hidden;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = m0 + 128 * wr + 16 * i + l16;
+    if (row >= kept) continue;
+    float *o = out + static_cast<long long>(row) * pl.hidden;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + 64 * wc + 16 * j + 4 * g;
+      if (n >= pl.hidden) continue;
+      f32x4 *at = reinterpret_cast<f32x4 *>(o + n);
+      *at = first ? acc[i][j] : *at + acc[i][j];
+    }
+  }
+}
+
+// Partial sums -> dx rows (zero where the row is left out): four columns per
+// lane.
+template <class T>
+__global__ __launch_bounds__(256) void k_dx_join(XentPlan pl, uint2 *dx) {
+  const float down = d_scale<T>(pl.r, true);
+  const int hq = pl.hidden >> 2;
+  const long long plane = static_cast<long long>(pl.m) * hq;
+  for (int row = static_cast<int>(blockIdx.y); row < pl.m; row += static_cast<int>(gridDim.y)) {
+    const int p = pl.r.inv[row];
+    for (int k = static_cast<int>(blockIdx.x * 256 + threadIdx.x); k < hq;
+         k += static_cast<int>(gridDim.x) * 256) {
+      uint2 o = {0u, 0u};
+      if (p >= 0) {
+        const f32x4 *src = reinterpret_cast<const f32x4 *>(pl.dxp) + static_cast<long long>(p) * hq + k;
+        f32x4 v = src[0];
+        for (int z = 1; z < pl.split_dx; ++z) v += src[z * plane];
+        v *= down;
+        o = uint2{bits16<T>(v[0]) | bits16<T>(v[1]) << 16, bits16<T>(v[2]) | bits16<T>(v[3]) << 16};
+      }
+      dx[static_cast<long long>(row) * hq + k] = o;
+    }
+  }
+}
+
+// Four consecutive columns of dW.
+template <class T, bool WIDE>
+__device__ __forceinline__ void dw_store(void *dw, long long at, f32x4 v, int accumulate) {
+  if constexpr (WIDE) {
+    f32x4 *o = reinterpret_cast<f32x4 *>(static_cast<float *>(dw) + at);
+    *o = accumulate ? *o + v : v;
+  } else {
+    uint2 *o = reinterpret_cast<uint2 *>(static_cast<unsigned short *>(dw) + at);
+    if (accumulate) {
+      const uint2 old = *o;
+      v += f32x4{from16<T>(old.x & 0xFFFFu), from16<T>(old.x >> 16), from16<T>(old.y & 0xFFFFu),
+                 from16<T>(old.y >> 16)};
+    }
+    *o = uint2{bits16<T>(v[0]) | bits16<T>(v[1]) << 16, bits16<T>(v[2]) | bits16<T>(v[3]) << 16};
+  }
+}
+
+// dW rows v0 .. of the piece = d^T X over the packed rows. SPLIT: fp32 partial
+// sums of a run of rows, joined by k_dw_join.
+template <class T, bool WIDE, bool SPLIT>
+__global__ __launch_bounds__(512, 2) void k_dw(XentPlan pl, const void *xc, int v0, int vend,
+                                               void *dw, int accumulate, int tm, int tn) {
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[kTileLds];
+  int z, mt, nt;
+  tile_at(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), tm, tn, &z, &mt, &nt);
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int m0 = v0 + mt * kTile, n0 = nt * kTile;  // m0: matrix row
+  const int kept = pl.r.head[0];
+  int k0 = 0, k1 = kept;
+  if constexpr (SPLIT) {
+    const int per = ((kept + kStep - 1) / kStep + pl.split_dw - 1) / pl.split_dw * kStep;
+    k0 = z * per < kept ? z * per : kept;
+    k1 = k0 + per < kept ? k0 + per : kept;
+  }
+  // a tile of rows past the vocabulary has no columns in d: nothing to read
+  const int kdim = m0 < vend ? k1 - k0 : 0;
+  ColumnSource a, b;
+  const int stride = pl.piece * 2;
+  a.init(static_cast<const unsigned char *>(pl.d) + static_cast<long long>(k0) * stride, m0 - v0,
+         kdim, stride, lane);
+  b.init(static_cast<const unsigned char *>(xc) + static_cast<long long>(k0) * pl.hidden * 2, n0,
+         kdim, pl.hidden * 2, lane);
+  f32x4 acc[8][4];
+  tile_product<T>(a, b, (kdim + kStep - 1) / kStep, lds, acc);
+  const int wr = wave >> 2, wc = wave & 3, l16 = lane & 15, g = lane >> 4;
+  const float down = SPLIT ? 1.f : d_scale<T>(pl.r, true);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = m0 + 128 * wr + 16 * i + l16;
+    if (row >= pl.rows) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + 64 * wc + 16 * j + 4 * g;
+      if (n >= pl.hidden) continue;
+      // rows past the vocabulary get no gradient, whatever x holds
+      const f32x4 v = row < vend ? acc[i][j] * down : f32x4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (SPLIT)
+        *reinterpret_cast<f32x4 *>(pl.dwp +
+                                   (static_cast<long long>(z) * pl.dw_rows + (row - v0)) * pl.hidden +
+                                   n) = v;
+      else
+        dw_store<T, WIDE>(dw, static_cast<long long>(row) * pl.hidden + n, v, accumulate);
+    }
+  }
+}
+
+template <class T, bool WIDE>
+__global__ __launch_bounds__(256) void k_dw_join(XentPlan pl, int v0, int rows, void *dw,
+                                                 int accumulate) {
+  const float down = d_scale<T>(pl.r, true);
+  const int hq = pl.hidden >> 2;
+  const long long n = static_cast<long long>(rows) * hq;
+  const long long plane = static_cast<long long>(pl.dw_rows) * hq;
+  for (long long k = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; k < n;
+       k += static_cast<long long>(gridDim.x) * 256) {
+    const f32x4 *src = reinterpret_cast<const f32x4 *>(pl.dwp) + k;
+    f32x4 v = src[0];
+    for (int z = 1; z < pl.split_dw; ++z) v += src[z * plane];
+    dw_store<T, WIDE>(dw, static_cast<long long>(v0) * pl.hidden + 4 * k, v * down, accumulate);
+  }
+}
+
+template <int NT>
+ShardTableN<NT> small_table(const ShardTable &t) {
+  ShardTableN<NT> o;
+  for (int r = 0; r < NT; ++r) o.p[r] = t.p[r];
+  return o;
+}
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+template <class F>
+void by_type(bool half, F f) {
+  if (half) f(TypeF16{});
+  else f(TypeBf16{});
+}
+template <class F>
+void by_table(int tp, F f) {
+  if (tp == 1) f(std::integral_constant<int, 1>{});
+  else f(std::integral_constant<int, HG_MAX_TP>{});
+}
+
+}  // namespace
+
+hipError_t launch_xent_pack(const XentPlan &p, const void *x, const void *labels, float *loss,
+                            float *lse, hipStream_t s) {
+  hipLaunchKernelGGL(k_pack, dim3(1), dim3(1024), 0, s, p.r, labels, p.label_bytes, p.m, p.vocab,
+                     p.ignore, loss, lse);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_pack_rows, dim3(p.m < 2048 ? p.m : 2048), dim3(256), 0, s, p.r,
+                     static_cast<const u32x4 *>(x), static_cast<u32x4 *>(p.xc), p.m, p.hidden >> 3);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_logits(const XentPlan &p, const VocabMatrix &w, int mode, int v0, int cols,
+                              hipStream_t s) {
+  const int tm = ceil_div(p.m, kTile), tn = ceil_div(cols, kTile);
+  const int vend = v0 + cols;
+  by_type(p.half, [&](auto type) {
+    by_table(w.tp, [&](auto nt) {
+      using T = decltype(type);
+      constexpr int NT = decltype(nt)::value;
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(tm * tn), dim3(512), 0, s, p,
+                           static_cast<const u32x4 *>(p.xc), small_table<NT>(w.t), w.shard, v0,
+                           vend, tm, tn);
+      };
+      if (mode == kStats) go(k_logits<T, NT, kStats>);
+      else if (mode == kProb) go(k_logits<T, NT, kProb>);
+      else go(k_logits<T, NT, kGrad>);
+    });
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_join(const XentPlan &p, const float *grad, float *loss, float *lse,
+                            hipStream_t s) {
+  hipLaunchKernelGGL(k_join, dim3(ceil_div(p.m, 16)), dim3(256), 0, s, p, grad, loss, lse);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_factors(const XentPlan &p, const float *lse, const float *grad,
+                               hipStream_t s) {
+  hipLaunchKernelGGL(k_factors, dim3(ceil_div(p.m, 256)), dim3(256), 0, s, p, lse, grad);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_normalise(const XentPlan &p, hipStream_t s) {
+  const dim3 grid(ceil_div(p.piece >> 3, 1024), p.m < 16384 ? p.m : 16384);
+  by_type(p.half, [&](auto type) {
+    hipLaunchKernelGGL(k_normalise<decltype(type)>, grid, dim3(256), 0, s, p);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_dx(const XentPlan &p, const VocabMatrix &w, int v0, int cols, bool first,
+                          hipStream_t s) {
+  const int tm = ceil_div(p.m, kTile), tn = ceil_div(p.hidden, kTile);
+  const int per = ceil_div(ceil_div(cols, kStep), p.split_dx);
+  by_type(p.half, [&](auto type) {
+    by_table(w.tp, [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      hipLaunchKernelGGL((k_dx<decltype(type), NT>), dim3(tm * tn * p.split_dx), dim3(512), 0, s, p,
+                         small_table<NT>(w.t), w.shard, v0, v0 + cols, per, first ? 1 : 0, tm, tn);
+    });
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_dx_join(const XentPlan &p, void *dx, hipStream_t s) {
+  const dim3 grid(ceil_div(p.hidden >> 2, 1024), p.m < 16384 ? p.m : 16384);
+  by_type(p.half, [&](auto type) {
+    hipLaunchKernelGGL(k_dx_join<decltype(type)>, grid, dim3(256), 0, s, p,
+                       static_cast<uint2 *>(dx));
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_dw(const XentPlan &p, int v0, int cols, void *dw, bool wide, bool accumulate,
+                          hipStream_t s) {
+  // the last piece also covers the matrix's rows past the vocabulary
+  const int vend = v0 + cols;
+  const int rows = vend == p.vocab ? p.rows - v0 : cols;
+  const int tm = ceil_div(rows, kTile), tn = ceil_div(p.hidden, kTile);
+  const bool split = p.split_dw > 1;
+  const int acc = accumulate ? 1 : 0;
+  by_type(p.half, [&](auto type) {
+    using T = decltype(type);
+    const dim3 grid(tm * tn * p.split_dw), block(512);
+    if (split)
+      hipLaunchKernelGGL((k_dw<T, false, true>), grid, block, 0, s, p, p.xc, v0, vend, dw, acc, tm,
+                         tn);
+    else if (wide)
+      hipLaunchKernelGGL((k_dw<T, true, false>), grid, block, 0, s, p, p.xc, v0, vend, dw, acc, tm,
+                         tn);
+    else
+      hipLaunchKernelGGL((k_dw<T, false, false>), grid, block, 0, s, p, p.xc, v0, vend, dw, acc, tm,
+                         tn);
+    if (split) {
+      const long long quads = static_cast<long long>(rows) * (p.hidden >> 2);
+      const long long want = (quads + 255) / 256;
+      const dim3 g2(static_cast<unsigned>(want < 4096 ? want : 4096));
+      if (wide)
+        hipLaunchKernelGGL((k_dw_join<T, true>), g2, dim3(256), 0, s, p, v0, rows, dw, acc);
+      else
+        hipLaunchKernelGGL((k_dw_join<T, false>), g2, dim3(256), 0, s, p, v0, rows, dw, acc);
+    }
+  });
+  return hipGetLastError();
+}
+
+}  // namespace hg

@@ -1,0 +1,317 @@
+"""Training and scoring at the vocabulary matrix: the softmax cross entropy of
+the vocab-parallel lm_head product without keeping the logits, the embedding
+lookup with scaling, and the gradients of both, through libhg.so.
+
+The matrix is the head weight of :func:`~tp_vocab_logits_amd.head_gather.lmhead`:
+``tp`` blocks of ``[shard, hidden]``, block r holding the vocabulary's entries
+``r * shard`` and on, given as one ``[tp * shard, hidden]`` (or ``[tp, shard,
+hidden]``) tensor or as a sequence of ``tp`` blocks. Gradients come as one
+``[tp * shard, hidden]`` tensor; a tied matrix passes the head's gradient to
+:func:`embed_grad` as ``dw`` with ``accumulate=True``.
+
+:func:`head_loss` and :func:`embedding` are the differentiable forms for
+autograd; the others are the plain calls. Work is enqueued on the current
+stream of the inputs' device; workspaces come from torch's allocator on that
+stream. All of it can be captured into a graph.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import torch
+
+from . import _lib
+from ._lib import check, lib, pointer_array
+
+__all__ = ["head_xent", "head_xent_grad", "head_xent_step", "head_loss", "embed", "embed_grad", "embedding"]
+
+_DTYPES = {torch.bfloat16: _lib.HG_BF16, torch.float16: _lib.HG_FP16, torch.float32: _lib.HG_FP32}
+
+# Workspace a gradient call may take by default: enough for 4096 rows over a
+# vocabulary of 163840 in one piece (1.3 GB of 16-bit values, 0.6 GB of partial
+# sums), 1.4 % of the card's 288 GB. Larger calls work through the vocabulary
+# in pieces.
+WORKSPACE_LIMIT = 4 << 30
+
+
+def _pointer(t: torch.Tensor | None) -> ctypes.c_void_p | None:
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _matrix(w, tp: int, shard: int, dtypes) -> tuple[list[int], int, torch.dtype, torch.device]:
+    """Block pointers, hidden size, type and device of the vocabulary matrix."""
+    tp, shard = int(tp), int(shard)
+    if tp < 1 or shard < 1:
+        raise ValueError(f"tp and shard must be positive, got {tp} and {shard}")
+    if isinstance(w, torch.Tensor):
+        if w.dim() not in (2, 3) or not w.is_contiguous() or w.numel() != tp * shard * w.shape[-1]:
+            raise ValueError(f"the matrix must be a contiguous [{tp * shard}, H] tensor, got {tuple(w.shape)}")
+        if w.dim() == 3 and tuple(w.shape[:2]) != (tp, shard):
+            raise ValueError(f"the matrix must be [{tp}, {shard}, H], got {tuple(w.shape)}")
+        blocks, hidden = [w], int(w.shape[-1])
+        step = shard * hidden * w.element_size()
+        ptrs = [w.data_ptr() + r * step for r in range(tp)]
+    else:
+        blocks = list(w)
+        if len(blocks) != tp:
+            raise ValueError(f"expected {tp} blocks of the matrix, got {len(blocks)}")
+        hidden = int(blocks[0].shape[-1])
+        for t in blocks:
+            if t.dim() != 2 or tuple(t.shape) != (shard, hidden) or not t.is_contiguous():
+                raise ValueError(f"every block must be a contiguous [{shard}, {hidden}] tensor, got {tuple(t.shape)}")
+            if t.dtype != blocks[0].dtype or t.device != blocks[0].device:
+                raise ValueError("the blocks must share dtype and device")
+        ptrs = [t.data_ptr() for t in blocks]
+    if blocks[0].dtype not in dtypes:
+        raise ValueError(f"the matrix must be one of {[str(d) for d in dtypes]}, got {blocks[0].dtype}")
+    return ptrs, hidden, blocks[0].dtype, blocks[0].device
+
+
+def _given(t, name: str, shape, dtypes, device) -> torch.Tensor:
+    """An argument tensor of the given shape, type and device, contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {' or '.join(str(d) for d in dtypes)} {list(shape)} tensor, "
+                         f"got {t.dtype} {list(t.shape)}{'' if t.is_contiguous() else ', not contiguous'}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the matrix on {device}")
+    return t
+
+
+_INTS = (torch.int64, torch.int32)
+_HALVES = (torch.bfloat16, torch.float16)
+
+
+def _on_gpu(device: torch.device) -> None:
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {device}")
+
+
+def _workspace(nbytes: int, device) -> torch.Tensor:
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+@functools.lru_cache(maxsize=256)
+def _xent_bytes(shape: bytes, kind: int, limit: int) -> int:
+    """hg_xent_workspace, once per shape: a training loop asks for the same one every step."""
+    n = ctypes.c_size_t()
+    s = _lib.XentShape.from_buffer_copy(shape)
+    check(lib().hg_xent_workspace(ctypes.byref(s), kind, limit, ctypes.byref(n)), "hg_xent_workspace")
+    return n.value
+
+
+class _Head:
+    """The arguments that every cross entropy call shares, checked."""
+
+    def __init__(self, x, w, labels, tp, shard, vocab, ignore, scale, z_weight):
+        self.ptrs, hidden, self.dtype, self.device = _matrix(w, tp, shard, _HALVES)
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x must be a [M, H] tensor")
+        m = int(x.shape[0])
+        self.x = _given(x, "x", (m, hidden), (self.dtype,), self.device)
+        self.labels = _given(labels, "labels", (m,), _INTS, self.device)
+        _on_gpu(self.device)
+        self.m, self.hidden, self.rows = m, hidden, int(tp) * int(shard)
+        vocab = self.rows if vocab is None else int(vocab)
+        if not 1 <= vocab <= self.rows:
+            raise ValueError(f"vocab must lie in 1..{self.rows}, got {vocab}")
+        self.shape = _lib.XentShape(int(tp), int(shard), hidden, m, vocab, _DTYPES[self.dtype],
+                                    self.labels.element_size(), int(ignore), float(scale), float(z_weight))
+
+    def rows_of(self, t, name):
+        return _given(t, name, (self.m,), (torch.float32,), self.device)
+
+    def workspace(self, kind: int, limit: int) -> torch.Tensor:
+        return _workspace(_xent_bytes(bytes(self.shape), kind, int(limit)), self.device)
+
+    def losses(self) -> tuple[torch.Tensor, torch.Tensor]:
+        both = torch.empty((2, self.m), dtype=torch.float32, device=self.device)
+        return both[0], both[1]
+
+    def grads(self, dx, dw, accumulate):
+        if dx is None:
+            dx = torch.empty((self.m, self.hidden), dtype=self.dtype, device=self.device)
+        else:
+            _given(dx, "dx", (self.m, self.hidden), (self.dtype,), self.device)
+        return dx, _gradient_buffer(dw, self.rows, self.hidden, self.dtype, self.device, accumulate)
+
+    def call(self, name, *args):
+        with torch.cuda.device(self.device):
+            stream = ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+            check(getattr(lib(), name)(ctypes.byref(self.shape), _pointer(self.x), pointer_array(self.ptrs),
+                                       _pointer(self.labels), *args, stream), name)
+
+
+def _gradient_buffer(dw, rows, hidden, dtype, device, accumulate) -> torch.Tensor:
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dw to add to")
+        return torch.empty((rows, hidden), dtype=dtype, device=device)
+    return _given(dw, "dw", (rows, hidden), tuple({dtype, torch.float32}), device)
+
+
+def head_xent(x: torch.Tensor, w, labels: torch.Tensor, tp: int, shard: int, vocab: int | None = None,
+              ignore: int = -100, scale: float = 1.0,
+              z_weight: float = 0.0) -> tuple[torch.Tensor, torch.Tensor]:
+    """The softmax cross entropy of ``scale * x @ w.T`` per row, and its
+    log-sum-exp: ``(loss [M], lse [M])`` in fp32, without keeping the logits.
+
+    ``x`` is ``[M, H]`` BF16 or FP16, ``labels`` ``[M]`` int64 or int32, the
+    softmax runs over the first ``vocab`` entries (default: all). ``loss = lse -
+    z_label + z_weight * lse**2``; the negated loss at ``z_weight = 0`` is the
+    label's log-probability. Rows with the label ``ignore`` get 0 in both; a
+    label outside the vocabulary gives NaN."""
+    h = _Head(x, w, labels, tp, shard, vocab, ignore, scale, z_weight)
+    loss, lse = h.losses()
+    ws = h.workspace(_lib.HG_XENT_SCORE, 0)
+    h.call("hg_xent", _pointer(loss), _pointer(lse), _pointer(ws), ws.numel())
+    return loss, lse
+
+
+def head_xent_grad(x: torch.Tensor, w, labels: torch.Tensor, lse: torch.Tensor, grad: torch.Tensor, tp: int,
+                   shard: int, vocab: int | None = None, ignore: int = -100, scale: float = 1.0,
+                   z_weight: float = 0.0, dx: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                   accumulate: bool = False,
+                   workspace_limit: int = WORKSPACE_LIMIT) -> tuple[torch.Tensor, torch.Tensor]:
+    """The gradients ``(dx [M, H], dw [tp*shard, H])`` of ``sum(grad * loss)``
+    for the ``lse`` that :func:`head_xent` returned and an upstream ``grad [M]``
+    (both fp32). Given, ``dx`` and ``dw`` are written; ``dw`` may be fp32, and
+    with ``accumulate`` is added to. The call keeps at most ``workspace_limit``
+    bytes of workspace where the vocabulary can be cut into pieces for it."""
+    h = _Head(x, w, labels, tp, shard, vocab, ignore, scale, z_weight)
+    lse, grad = h.rows_of(lse, "lse"), h.rows_of(grad, "grad")
+    dx, dw = h.grads(dx, dw, accumulate)
+    ws = h.workspace(_lib.HG_XENT_GRAD, workspace_limit)
+    h.call("hg_xent_grad", _pointer(lse), _pointer(grad), _pointer(dx), _pointer(dw),
+           int(dw.dtype != h.dtype), int(accumulate), _pointer(ws), ws.numel())
+    return dx, dw
+
+
+def head_xent_step(x: torch.Tensor, w, labels: torch.Tensor, grad: torch.Tensor, tp: int, shard: int,
+                   vocab: int | None = None, ignore: int = -100, scale: float = 1.0, z_weight: float = 0.0,
+                   dx: torch.Tensor | None = None, dw: torch.Tensor | None = None, accumulate: bool = False,
+                   workspace_limit: int = WORKSPACE_LIMIT):
+    """Loss and gradients in one call, ``(loss, lse, dx, dw)``, for an upstream
+    ``grad [M]`` (fp32) that is known before the loss: the mean's ``1/n``, a
+    row's weight. Cheaper than :func:`head_xent` and :func:`head_xent_grad`
+    together by one of four products, as the logits are computed once when the
+    workspace holds the whole vocabulary."""
+    h = _Head(x, w, labels, tp, shard, vocab, ignore, scale, z_weight)
+    grad = h.rows_of(grad, "grad")
+    loss, lse = h.losses()
+    dx, dw = h.grads(dx, dw, accumulate)
+    ws = h.workspace(_lib.HG_XENT_STEP, workspace_limit)
+    h.call("hg_xent_step", _pointer(grad), _pointer(loss), _pointer(lse), _pointer(dx), _pointer(dw),
+           int(dw.dtype != h.dtype), int(accumulate), _pointer(ws), ws.numel())
+    return loss, lse, dx, dw
+
+
+class _HeadLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, labels, tp, shard, how):
+        loss, lse = head_xent(x, w, labels, tp, shard, **how)
+        ctx.save_for_backward(x, w, labels, lse)
+        ctx.args = (tp, shard, how)
+        return loss
+
+    @staticmethod
+    def backward(ctx, grad):
+        x, w, labels, lse = ctx.saved_tensors
+        tp, shard, how = ctx.args
+        # the upstream gradient of a sum or mean is one value expanded
+        dx, dw = head_xent_grad(x, w, labels, lse, grad.float().contiguous(), tp, shard, **how)
+        return dx, dw.view(w.shape), None, None, None, None
+
+
+def head_loss(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, tp: int, shard: int,
+              vocab: int | None = None, ignore: int = -100, scale: float = 1.0,
+              z_weight: float = 0.0) -> torch.Tensor:
+    """:func:`head_xent`'s loss ``[M]``, differentiable in ``x`` and ``w`` (one
+    tensor). Only ``lse`` is kept for the backward pass, which computes the
+    logits again."""
+    if not isinstance(w, torch.Tensor):
+        raise ValueError("head_loss takes the matrix as one tensor")
+    how = {"vocab": vocab, "ignore": ignore, "scale": scale, "z_weight": z_weight}
+    return _HeadLoss.apply(x, w, labels, tp, shard, how)
+
+
+def _tokens(tokens, device) -> torch.Tensor:
+    if not isinstance(tokens, torch.Tensor) or tokens.dtype not in _INTS or not tokens.is_contiguous():
+        raise ValueError("tokens must be a contiguous int64 or int32 tensor")
+    if tokens.device != device:
+        raise ValueError(f"tokens are on {tokens.device}, not on {device}")
+    return tokens
+
+
+def embed(tokens: torch.Tensor, w, tp: int, shard: int, scale: float = 1.0,
+          out: torch.Tensor | None = None) -> torch.Tensor:
+    """Embedding lookup with scaling: ``scale * w[tokens]`` of shape
+    ``[*tokens.shape, H]``, rounded once to the matrix's type (BF16, FP16 or
+    FP32). A token outside the matrix gives a row of zeros."""
+    ptrs, hidden, dtype, device = _matrix(w, tp, shard, tuple(_DTYPES))
+    tokens = _tokens(tokens, device)
+    _on_gpu(device)
+    shape = (*tokens.shape, hidden)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+    else:
+        _given(out, "out", shape, (dtype,), device)
+    with torch.cuda.device(device):
+        check(lib().hg_embed(int(tp), int(shard), hidden, _DTYPES[dtype], pointer_array(ptrs), _pointer(tokens),
+                             tokens.element_size(), tokens.numel(), float(scale), _pointer(out),
+                             ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)), "hg_embed")
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _embed_bytes(tp: int, shard: int, hidden: int, n: int) -> int:
+    size = ctypes.c_size_t()
+    check(lib().hg_embed_workspace(tp, shard, hidden, n, ctypes.byref(size)), "hg_embed_workspace")
+    return size.value
+
+
+def embed_grad(tokens: torch.Tensor, dy: torch.Tensor, tp: int, shard: int, scale: float = 1.0,
+               dw: torch.Tensor | None = None, accumulate: bool = False) -> torch.Tensor:
+    """The gradient of :func:`embed` in the matrix, ``[tp*shard, H]``: ``dw[v] =
+    scale * sum(dy[tokens == v])``, zero where no token names the row. ``dy`` is
+    ``[*tokens.shape, H]``. A given ``dw`` (``dy``'s type or fp32) is written,
+    or added to with ``accumulate``; sums are fp32 in the order of the tokens."""
+    if not isinstance(dy, torch.Tensor) or dy.dtype not in _DTYPES or dy.dim() < 1:
+        raise ValueError(f"dy must be one of {[str(d) for d in _DTYPES]}")
+    device, hidden = dy.device, int(dy.shape[-1])
+    tokens = _tokens(tokens, device)
+    _given(dy, "dy", (*tokens.shape, hidden), (dy.dtype,), device)
+    _on_gpu(device)
+    tp, shard = int(tp), int(shard)
+    dw = _gradient_buffer(dw, tp * shard, hidden, dy.dtype, device, accumulate)
+    ws = _workspace(_embed_bytes(tp, shard, hidden, tokens.numel()), device)
+    with torch.cuda.device(device):
+        check(lib().hg_embed_grad(tp, shard, hidden, _DTYPES[dy.dtype], _pointer(tokens), tokens.element_size(),
+                                  tokens.numel(), _pointer(dy), float(scale), _pointer(dw),
+                                  int(dw.dtype != dy.dtype), int(accumulate), _pointer(ws), ws.numel(),
+                                  ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)), "hg_embed_grad")
+    return dw
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, w, tp, shard, scale):
+        ctx.save_for_backward(tokens)
+        ctx.args = (tp, shard, scale, w.shape)
+        return embed(tokens, w, tp, shard, scale)
+
+    @staticmethod
+    def backward(ctx, dy):
+        tokens, = ctx.saved_tensors
+        tp, shard, scale, shape = ctx.args
+        return None, embed_grad(tokens, dy.contiguous(), tp, shard, scale).view(shape), None, None, None
+
+
+def embedding(tokens: torch.Tensor, w: torch.Tensor, tp: int, shard: int, scale: float = 1.0) -> torch.Tensor:
+    """:func:`embed`, differentiable in ``w`` (one tensor)."""
+    if not isinstance(w, torch.Tensor):
+        raise ValueError("embedding takes the matrix as one tensor")
+    return _Embedding.apply(tokens, w, tp, shard, scale)

@@ -116,30 +116,35 @@ __device__ __forceinline__ LoadLane load_lane(int lane) {
 // Operand sources. load(lds, sub, q, step): instruction q (LDS rows 8q..8q+7)
 // of sub-tile `sub` at step `step`.
 
-// Row operand in one matrix: row m of the tile at base + m*stride bytes, k
-// from the base on; `rows` rows below the matrix's end, K a multiple of 8.
-struct RowSource {
+// Row operand in panels of 256 k: row m of the tile at base + m*512 bytes,
+// the k of panel i at base + i*panel; k counts from column `k0` (a multiple of
+// 64), K a multiple of 8.
+struct PanelRowSource {
   static constexpr bool kColumn = false;
-  __amdgpu_buffer_rsrc_t r;
+  const unsigned char *base;
+  long long panel;
   unsigned off[2];
   int chunk[2];
-  int k8, stride;
-  __device__ __forceinline__ void init(const void *base, int rows, int stride_bytes, int k_,
-                                       long long bytes, int lane) {
+  int k8, s0, bytes;
+  __device__ __forceinline__ void init(const void *base_, int rows, long long panel_bytes, int k0,
+                                       int k_, int lane) {
     const LoadLane p = load_lane<false>(lane);
-    r = resource(base, rows > 0 ? bytes : 0);
-    stride = stride_bytes;
+    base = static_cast<const unsigned char *>(base_);
+    panel = panel_bytes;
+    bytes = rows * 512;
+    s0 = k0 >> 6;
     k8 = k_ >> 3;
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
       chunk[o] = p.chunk[o];
-      off[o] = static_cast<unsigned>(p.row * stride_bytes + p.chunk[o] * 16);
+      off[o] = static_cast<unsigned>(p.row * 512 + p.chunk[o] * 16);
     }
   }
   __device__ __forceinline__ void load(unsigned char *lds, int sub, int q, int step) const {
-    const int o = q & 1;
-    const unsigned v = off[o] + static_cast<unsigned>((64 * sub + 8 * q) * stride + step * 128);
-    load_lds(r, lds + q * 1024, step * 8 + chunk[o] < k8 ? v : kBeyond);
+    const int o = q & 1, s = s0 + step;
+    const unsigned v = off[o] + static_cast<unsigned>((64 * sub + 8 * q) * 512 + (s & 3) * 128);
+    load_lds(resource(base + (s >> 2) * panel, bytes), lds + q * 1024,
+             step * 8 + chunk[o] < k8 ? v : kBeyond);
   }
 };
 
@@ -181,32 +186,25 @@ struct RankRowSource {
   }
 };
 
-// Column operand in one matrix: k row k at base + k*stride bytes, the tile's
-// columns from `col` on; K rows.
-struct ColumnSource {
+// Column operand in one panel: k row k at base + k*512 bytes; K rows.
+struct PanelColumnSource {
   static constexpr bool kColumn = true;
   const unsigned char *base;
   unsigned off[2];
-  int rows, stride, col;
-  __device__ __forceinline__ void init(const void *base_, int col_, int rows_, int stride_bytes,
-                                       int lane) {
+  int rows;
+  __device__ __forceinline__ void init(const void *base_, int rows_, int lane) {
     const LoadLane p = load_lane<true>(lane);
-    base = static_cast<const unsigned char *>(base_) + static_cast<long long>(col_) * 2;
-    col = col_;
+    base = static_cast<const unsigned char *>(base_);
     rows = rows_;
-    stride = stride_bytes;
 #pragma unroll
-    for (int o = 0; o < 2; ++o)
-      off[o] = static_cast<unsigned>(p.row * stride_bytes + p.chunk[o] * 16);
+    for (int o = 0; o < 2; ++o) off[o] = static_cast<unsigned>(p.row * 512 + p.chunk[o] * 16);
   }
   __device__ __forceinline__ void load(unsigned char *lds, int sub, int q, int step) const {
-    const int k = step * 64 + 8 * q;
-    const int left = rows - k;
-    // the last row ends `col` columns early, counted from this base
-    const int n = left <= 0 ? 0 : left > 8 ? 8 * stride : left * stride - 2 * col;
-    const __amdgpu_buffer_rsrc_t r =
-        resource(base + static_cast<long long>(left <= 0 ? 0 : k) * stride, n);
-    load_lds(r, lds + q * 1024, off[q & 1] + static_cast<unsigned>(sub * 128));
+    const int left = rows - step * 64;
+    const __amdgpu_buffer_rsrc_t r = resource(
+        base + (left <= 0 ? 0ll : static_cast<long long>(step) * (64 * 512)),
+        left > 64 ? 64 * 512 : left * 512);
+    load_lds(r, lds + q * 1024, off[q & 1] + static_cast<unsigned>(8 * q * 512 + sub * 128));
   }
 };
 

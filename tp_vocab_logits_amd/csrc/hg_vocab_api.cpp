@@ -112,7 +112,7 @@ size_t lay_out(const hg_xent_shape &s, int kind, int piece, char *ws, XentPlan *
   p->r.lse2 = reinterpret_cast<float *>(take(4 * m));
   p->r.ca = reinterpret_cast<float *>(take(4 * m));
   p->r.cb = reinterpret_cast<float *>(take(4 * m));
-  p->xc = take(2 * m * h);
+  p->xc = take(2 * m * hg::kPanel * ceil_div(s.hidden, hg::kPanel));
   const size_t tiles = static_cast<size_t>(ceil_div(s.vocab, kTile));
   if (kind != HG_XENT_GRAD) p->part = reinterpret_cast<float *>(take(8 * tiles * m));
   if (kind != HG_XENT_SCORE) {

@@ -22,12 +22,14 @@
 //    are computed once (hg_xent_step), or
 //  - lse is known, and the epilogue writes d itself (hg_xent_grad, and steps
 //    whose workspace holds fewer columns than the vocabulary).
-// d is 16 bits wide, as the matrix cores take it. fp16 has 5 exponent bits:
-// there the probabilities are scaled by 2^15 and d by a power of two that
-// brings its largest row factor to 2^13..2^14, so that probabilities down to
-// about 2^-27 of the largest keep all their bits; both scales are exact and
-// are taken back in fp32. Each of the two roundings is off by at most half a
-// step of the type and falls on single terms of sums over many.
+// d is 16 bits wide, as the matrix cores take it: one rounding to the type on
+// each term of sums over many. fp16 has 5 exponent bits: there d is scaled by a
+// power of two that brings its largest row factor to 2^13..2^14, so that terms
+// down to about 2^-27 of the largest keep all their bits; the scale is exact
+// and is taken back in fp32.
+// The unnormalised probabilities, all in 0..1, wait in 16 bits without a sign
+// (see Prob): 10 bits of mantissa for bf16 and 11 for fp16, so that this first
+// rounding is off by at most a quarter (bf16: an eighth) of what d's own is.
 
 #include <type_traits>
 
@@ -40,7 +42,22 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kHalfProb = 32768.f;  // scale of fp16 probabilities
+
+// An unnormalised probability p in 0..1 in 16 bits: the top of its fp32 bits,
+// exponents 2^-(2^E - 1) .. 2^0 with M mantissa bits, E + M = 16, rounded to
+// nearest; what is smaller (2^-63 for bf16, 2^-31 for fp16) becomes 0.
+template <class T>
+struct Prob {
+  static constexpr int M = T::kHalf ? 11 : 10, E = 16 - M, S = 23 - M;
+  static constexpr int kLow = (127 - ((1 << E) - 1)) << M;
+  static __device__ __forceinline__ uint32_t put(float p) {
+    const int b = (__builtin_bit_cast(int, p) + (1 << (S - 1))) >> S;
+    return static_cast<uint32_t>(b > kLow ? b - kLow : 0);
+  }
+  static __device__ __forceinline__ float get(uint32_t c) {
+    return c ? __builtin_bit_cast(float, static_cast<int>(c + kLow) << S) : 0.f;
+  }
+};
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -110,8 +127,9 @@ __global__ __launch_bounds__(256) void k_pack_rows(XentRows r, const u32x4 *x, u
   const int kept = r.head[0];
   for (int p = static_cast<int>(blockIdx.x); p < kept; p += static_cast<int>(gridDim.x)) {
     const u32x4 *src = x + static_cast<long long>(r.idx[p]) * hv;
-    u32x4 *dst = xc + static_cast<long long>(p) * hv;
-    for (int k = static_cast<int>(threadIdx.x); k < hv; k += 256) dst[k] = src[k];
+    u32x4 *dst = xc + static_cast<long long>(p) * 32;
+    for (int k = static_cast<int>(threadIdx.x); k < hv; k += 256)
+      dst[static_cast<long long>(k >> 5) * m * 32 + (k & 31)] = src[k];
   }
 }
 
@@ -130,10 +148,9 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int wr = wave >> 2, wc = wave & 3, l16 = lane & 15, g = lane >> 4;
 
-  RowSource a;
+  PanelRowSource a;
   const int rows = kept - m0 < kTile ? kept - m0 : kTile;
-  a.init(xc + static_cast<long long>(m0) * (pl.hidden >> 3), rows, pl.hidden * 2, pl.hidden,
-         static_cast<long long>(rows) * pl.hidden * 2, lane);
+  a.init(xc + static_cast<long long>(m0) * 32, rows, pl.m * 512ll, 0, pl.hidden, lane);
   RankRowSource<NT> b;
   b.init(w, shard, vend, pl.hidden, n0, wc, 4 * wr, lane);
   f32x4 acc[8][4];
@@ -141,7 +158,9 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
 
   const float s2 = pl.scale * kLog2e;
   const int nl = n0 + 64 * wc + 4 * g;  // the lane's column of block 0
-  unsigned short *dout = static_cast<unsigned short *>(pl.d);
+  // d's panel of this tile, from the wave's columns on
+  unsigned short *dout = static_cast<unsigned short *>(pl.d) +
+                         static_cast<long long>((n0 - v0) / kPanel) * pl.m * kPanel + (nl - n0);
   if constexpr (MODE == kGrad) {
     const float up = d_scale<T>(pl.r, false);
 #pragma unroll
@@ -150,7 +169,7 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
       if (row >= kept) continue;
       const float lse2 = pl.r.lse2[row], ca = pl.r.ca[row] * up, cb = pl.r.cb[row] * up;
       const int lab = pl.r.lab[row];
-      unsigned short *o = dout + static_cast<long long>(row) * pl.piece + (nl - v0);
+      unsigned short *o = dout + static_cast<long long>(row) * kPanel;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t q[4];
@@ -201,7 +220,7 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
       const int lab = row < kept ? pl.r.lab[row] - nl : -1;
       float sum = 0.f, zt = 0.f;
       bool mine = false;
-      unsigned short *o = dout + static_cast<long long>(row) * pl.piece + (nl - v0);
+      unsigned short *o = dout + static_cast<long long>(row) * kPanel;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t q[4];
@@ -213,7 +232,7 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
             zt = acc[i][j][t];
             mine = true;
           }
-          if (MODE == kProb) q[t] = bits16<T>(T::kHalf ? e * kHalfProb : e);
+          if (MODE == kProb) q[t] = Prob<T>::put(e);
         }
         if (MODE == kProb && row < kept)
           *reinterpret_cast<uint2 *>(o + 16 * j) = uint2{q[0] | q[1] << 16, q[2] | q[3] << 16};
@@ -297,31 +316,31 @@ __global__ __launch_bounds__(256) void k_factors(XentPlan pl, const float *lse, 
 }
 
 // Unnormalised probabilities -> d in place: 16 bytes (8 columns) per lane and
-// step. HBM-bound: reads and writes d once.
+// step, 8 rows of a panel per workgroup and step. HBM-bound: reads and writes d
+// once.
 template <class T>
 __global__ __launch_bounds__(256) void k_normalise(XentPlan pl) {
   const int kept = pl.r.head[0];
-  const int vecs = pl.piece >> 3;
+  const int tile = static_cast<int>(blockIdx.x);
   const float up = d_scale<T>(pl.r, false);
-  for (int row = static_cast<int>(blockIdx.y); row < kept; row += static_cast<int>(gridDim.y)) {
-    const float lse2 = pl.r.lse2[row], ca = pl.r.ca[row] * up, cb = pl.r.cb[row] * up;
-    const int lab = pl.r.lab[row];
-    u32x4 *d = static_cast<u32x4 *>(pl.d) + static_cast<long long>(row) * vecs;
-    for (int k = static_cast<int>(blockIdx.x * 256 + threadIdx.x); k < vecs;
-         k += static_cast<int>(gridDim.x) * 256) {
-      const float mx = pl.part[static_cast<long long>(k >> 5) * pl.m + row];
-      const float ref = mx == -__builtin_inff() ? 0.f : mx;
-      const float c = exp2_(ref - lse2) * (T::kHalf ? ca * (1.f / kHalfProb) : ca);
-      u32x4 v = d[k];
+  const float *part = pl.part + static_cast<long long>(tile) * pl.m;
+  u32x4 *d = static_cast<u32x4 *>(pl.d) + static_cast<long long>(tile) * pl.m * 32;
+  const int k = static_cast<int>(threadIdx.x) & 31;
+  for (int row = static_cast<int>(blockIdx.y * 8 + threadIdx.x / 32); row < kept;
+       row += static_cast<int>(gridDim.y) * 8) {
+    const float mx = part[row];
+    const float ref = mx == -__builtin_inff() ? 0.f : mx;
+    const float c = exp2_(ref - pl.r.lse2[row]) * (pl.r.ca[row] * up), cb = pl.r.cb[row] * up;
+    const int at = pl.r.lab[row] - tile * kPanel - 8 * k;
+    u32x4 v = d[static_cast<long long>(row) * 32 + k];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        float lo = from16<T>(v[t] & 0xFFFFu) * c, hi = from16<T>(v[t] >> 16) * c;
-        if (lab == 8 * k + 2 * t) lo -= cb;
-        if (lab == 8 * k + 2 * t + 1) hi -= cb;
-        v[t] = bits16<T>(lo) | bits16<T>(hi) << 16;
-      }
-      d[k] = v;
+    for (int t = 0; t < 4; ++t) {
+      float lo = Prob<T>::get(v[t] & 0xFFFFu) * c, hi = Prob<T>::get(v[t] >> 16) * c;
+      if (at == 2 * t) lo -= cb;
+      if (at == 2 * t + 1) hi -= cb;
+      v[t] = bits16<T>(lo) | bits16<T>(hi) << 16;
     }
+    d[static_cast<long long>(row) * 32 + k] = v;
   }
 }
 
@@ -342,12 +361,11 @@ __global__ __launch_bounds__(512, 2) void k_dx(XentPlan pl, ShardTableN<NT> w, i
   int k1 = k0 + per * kStep;
   if (k1 > vend - v0) k1 = vend - v0;
   const int steps = k1 > k0 ? (k1 - k0 + kStep - 1) / kStep : 0;
-  RowSource a;
+  PanelRowSource a;
   const int rows = kept - m0 < kTile ? kept - m0 : kTile;
-  const int stride = pl.piece * 2;
   // d's columns past the vocabulary are zero up to a multiple of 256
-  a.init(static_cast<const unsigned char *>(pl.d) + static_cast<long long>(m0) * stride + 2 * k0,
-         rows, stride, steps * kStep, static_cast<long long>(rows) * stride - 2 * k0, lane);
+  a.init(static_cast<const unsigned char *>(pl.d) + m0 * 512ll, rows, pl.m * 512ll, k0,
+         steps * kStep, lane);
   RankColumnSource<NT> b;
   b.init(w, shard, v0 + (k1 > k0 ? k1 : k0), v0 + k0, n0, pl.hidden, lane);
   f32x4 acc[8][4];
@@ -430,12 +448,12 @@ __global__ __launch_bounds__(512, 2) void k_dw(XentPlan pl, const void *xc, int 
   }
   // a tile of rows past the vocabulary has no columns in d: nothing to read
   const int kdim = m0 < vend ? k1 - k0 : 0;
-  ColumnSource a, b;
-  const int stride = pl.piece * 2;
-  a.init(static_cast<const unsigned char *>(pl.d) + static_cast<long long>(k0) * stride, m0 - v0,
-         kdim, stride, lane);
-  b.init(static_cast<const unsigned char *>(xc) + static_cast<long long>(k0) * pl.hidden * 2, n0,
-         kdim, pl.hidden * 2, lane);
+  PanelColumnSource a, b;
+  a.init(static_cast<const unsigned char *>(pl.d) +
+             (static_cast<long long>(mt) * pl.m + k0) * 512,
+         kdim, lane);
+  b.init(static_cast<const unsigned char *>(xc) + (static_cast<long long>(nt) * pl.m + k0) * 512,
+         kdim, lane);
   f32x4 acc[8][4];
   tile_product<T>(a, b, (kdim + kStep - 1) / kStep, lds, acc);
   const int wr = wave >> 2, wc = wave & 3, l16 = lane & 15, g = lane >> 4;
@@ -543,7 +561,8 @@ hipError_t launch_xent_factors(const XentPlan &p, const float *lse, const float 
 }
 
 hipError_t launch_xent_normalise(const XentPlan &p, hipStream_t s) {
-  const dim3 grid(ceil_div(p.piece >> 3, 1024), p.m < 16384 ? p.m : 16384);
+  const int per = ceil_div(p.m, 8 * 16);  // 16 steps of 8 rows per workgroup
+  const dim3 grid(p.piece / kPanel, per < 65535 ? per : 65535);
   by_type(p.half, [&](auto type) {
     hipLaunchKernelGGL(k_normalise<decltype(type)>, grid, dim3(256), 0, s, p);
   });

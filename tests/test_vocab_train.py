@@ -684,3 +684,21 @@ def test_argument_rules_on_device():
         vt.embed(t, w, 1, 95)
     with pytest.raises(ValueError):
         vt.embed_grad(t, x.double(), 1, 96)
+
+
+@gpu
+@pytest.mark.parametrize("m", [1, 15, 16, 17, 31, 32, 33, 64, 65, 100, 127, 128, 129])
+@pytest.mark.parametrize("tp,shard,hidden,vocab", [(1, 32, 8, 5), (8, 2592, 136, 20700)])
+def test_few_rows(tp, shard, hidden, vocab, m):
+    """Up to 128 rows the matrix is streamed, by row counts rounded up to 16,
+    32, 64 and 128; the vocabulary's runs end inside tiles and units."""
+    note(f"few rows {tp=} {shard=} {hidden=} {vocab=} {m=}")
+    p = Problem(tp, shard, hidden, m, vocab, "bf16", 0.1, scale=1.5, z_weight=0.01)
+    x, w, t, _ = p.on_gpu()
+    x = torch.cat([x, torch.full_like(x, float("nan"))])[:m]  # rows past m hold anything
+    w[vocab:] = float("nan")
+    loss, lse = vt.head_xent(x, w, t, tp, shard, **p.how)
+    p.check_loss(loss, lse)
+    p.blocks = True
+    again = vt.head_xent(x, p.on_gpu()[1], t, tp, shard, **p.how)
+    assert torch.equal(again[0], loss) and torch.equal(again[1], lse)

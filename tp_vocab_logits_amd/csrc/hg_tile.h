@@ -85,15 +85,37 @@ constexpr int kTileLds = 2 * kStageBytes;
 constexpr unsigned kBeyond = 0x80000000u;  // an offset past every buffer resource used here
 constexpr int kRawWord3 = 0x00020000;      // buffer resource word 3: raw 32-bit data
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void *base, long long bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0,
-                                           bytes > 0 ? static_cast<int>(bytes) : 0, kRawWord3);
+typedef uint32_t rsrc_t __attribute__((ext_vector_type(4)));
+
+// Raw buffer resource of `bytes` bytes (none if negative) at a wave-uniform base.
+__device__ __forceinline__ rsrc_t resource(const void *base, long long bytes) {
+  const unsigned long long p = reinterpret_cast<unsigned long long>(base);
+  return rsrc_t{static_cast<uint32_t>(p), static_cast<uint32_t>(p >> 32) & 0xFFFFu,
+                static_cast<uint32_t>(bytes > 0 ? bytes : 0), kRawWord3};
 }
 
-__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, unsigned char *lds,
-                                         unsigned offset) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(
-      r, (__attribute__((address_space(3))) void *)lds, 16, offset, 0, 0, 0);
+// One load of 16 bytes per lane straight into LDS, at lds + 16*lane. Written
+// as an instruction because the compiler, which knows that the builtin form
+// writes LDS, waits for every load in flight before a transposed LDS read
+// (vmcnt(0); dW at 4096 rows, V = 163840, H = 7168: NOASM ms). The load has
+// no output register; its order against the LDS reads is kept by the waits and
+// barriers of tile_product and by the memory clobber.
+// STREAM: data that is read once (non-temporal).
+template <bool STREAM = false>
+__device__ __forceinline__ void load_lds(rsrc_t r, unsigned char *lds, unsigned offset) {
+  const uint32_t at = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char *)lds));
+  if constexpr (STREAM)
+    __asm__ __volatile__(
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+        :
+        : "s"(at), "v"(offset), "s"(r)
+        : "memory");
+  else
+    __asm__ __volatile__("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                         :
+                         : "s"(at), "v"(offset), "s"(r)
+                         : "memory");
 }
 
 // Lane constants of the loads: LDS row l >> 3 of the instruction's eight, slot
@@ -152,10 +174,10 @@ struct PanelRowSource {
 // n0 + m. Blocks are a multiple of 32 rows, so eight rows share a block. A
 // wave always loads the same four instructions of the same sub-tile, so it
 // keeps one resource for each.
-template <int NT>
+template <int NT, bool STREAM = false>
 struct RankRowSource {
   static constexpr bool kColumn = false;
-  __amdgpu_buffer_rsrc_t r[4];
+  rsrc_t r[4];
   unsigned off[2];
   int chunk[2];
   int k8;
@@ -181,7 +203,7 @@ struct RankRowSource {
   }
   __device__ __forceinline__ void load(unsigned char *lds, int, int q, int step) const {
     const int o = q & 1;
-    load_lds(r[q & 3], lds + q * 1024,
+    load_lds<STREAM>(r[q & 3], lds + q * 1024,
              step * 8 + chunk[o] < k8 ? off[o] + static_cast<unsigned>(step * 128) : kBeyond);
   }
 };
@@ -201,7 +223,7 @@ struct PanelColumnSource {
   }
   __device__ __forceinline__ void load(unsigned char *lds, int sub, int q, int step) const {
     const int left = rows - step * 64;
-    const __amdgpu_buffer_rsrc_t r = resource(
+    const rsrc_t r = resource(
         base + (left <= 0 ? 0ll : static_cast<long long>(step) * (64 * 512)),
         left > 64 ? 64 * 512 : left * 512);
     load_lds(r, lds + q * 1024, off[q & 1] + static_cast<unsigned>(8 * q * 512 + sub * 128));
@@ -229,17 +251,27 @@ struct RankColumnSource {
     for (int o = 0; o < 2; ++o) off[o] = static_cast<unsigned>(p.row * stride + p.chunk[o] * 16);
   }
   __device__ __forceinline__ void load(unsigned char *lds, int sub, int q, int step) const {
-    const int v = v0 + step * 64 + 8 * q;
-    const int left = limit - v;
-    const int rank = NT == 1 || left <= 0 ? 0 : v / shard;
-    const int at = left <= 0 ? 0 : v - rank * shard;
-    // the resource stays inside the block: 8 rows, less the columns before
-    // this tile's at its end (reads past a row's end belong to columns that no
-    // one stores)
-    const int n = left <= 0 ? 0 : (left < 8 ? left : 8) * stride - 2 * col;
-    const unsigned char *base = reinterpret_cast<const unsigned char *>(w->p[rank]) +
-                                static_cast<long long>(at) * stride + 2 * col;
-    load_lds(resource(base, n), lds + q * 1024, off[q & 1] + static_cast<unsigned>(sub * 128));
+    // The resource ends with the block's (or the limit's) last row: counted
+    // from this tile's columns it is 2*col short of whole rows. Reads past a
+    // row's end belong to columns that no one stores.
+    const unsigned v_off = off[q & 1] + static_cast<unsigned>(sub * 128);
+    if constexpr (NT == 1) {  // one block: the step's 64 rows share a resource
+      const int v = v0 + step * 64, left = limit - v;
+      const int n = left > 64 ? 64 * stride : left * stride - 2 * col;
+      const unsigned char *base = reinterpret_cast<const unsigned char *>(w->p[0]) +
+                                  static_cast<long long>(left > 0 ? v : 0) * stride + 2 * col;
+      load_lds(resource(base, left > 0 ? n : 0), lds + q * 1024,
+               v_off + static_cast<unsigned>(8 * q * stride));
+    } else {
+      const int v = v0 + step * 64 + 8 * q;
+      const int left = limit - v;
+      const int rank = left <= 0 ? 0 : v / shard;
+      const int at = left <= 0 ? 0 : v - rank * shard;
+      const int n = left <= 0 ? 0 : (left < 8 ? left : 8) * stride - 2 * col;
+      const unsigned char *base = reinterpret_cast<const unsigned char *>(w->p[rank]) +
+                                  static_cast<long long>(at) * stride + 2 * col;
+      load_lds(resource(base, n), lds + q * 1024, v_off);
+    }
   }
 };
 

@@ -51,7 +51,8 @@ struct XentPlan {
   XentRows r;
   void *xc;        // packed rows of X, [hidden / 256 up][m][256]
   void *d;         // d (or unnormalised probabilities) of one piece, [piece / 256][m][256]
-  float *part;     // [2][tiles][m] per 256-column tile: maximum (base 2), sum
+  float *part;     // [2][tiles][m] per 256-column tile: maximum (base 2), sum; few rows:
+                   // [m][kScoreGroups][2]
   float *dxp;      // [split_dx][m][hidden]
   float *dwp;      // [split_dw][dw_rows][hidden] when split_dw > 1
 };
@@ -62,6 +63,11 @@ hipError_t launch_xent_pack(const XentPlan &p, const void *x, const void *labels
 // also the unnormalised probabilities, 2 writes d (the row factors are known).
 hipError_t launch_xent_logits(const XentPlan &p, const VocabMatrix &w, int mode, int v0, int cols,
                               hipStream_t s);
+// Few rows (m <= kScoreRows): loss and lse straight from x, with no packing.
+constexpr int kScoreRows = 128;
+constexpr int kScoreGroups = 256;  // workgroups, each with a run of the vocabulary
+hipError_t launch_xent_score(const XentPlan &p, const VocabMatrix &w, const void *x,
+                             const void *labels, float *loss, float *lse, hipStream_t s);
 // Row statistics -> loss, lse and the rows' factors (grad null: none).
 hipError_t launch_xent_join(const XentPlan &p, const float *grad, float *loss, float *lse,
                             hipStream_t s);

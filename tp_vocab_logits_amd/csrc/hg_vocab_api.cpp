@@ -112,8 +112,12 @@ size_t lay_out(const hg_xent_shape &s, int kind, int piece, char *ws, XentPlan *
   p->r.lse2 = reinterpret_cast<float *>(take(4 * m));
   p->r.ca = reinterpret_cast<float *>(take(4 * m));
   p->r.cb = reinterpret_cast<float *>(take(4 * m));
-  p->xc = take(2 * m * hg::kPanel * ceil_div(s.hidden, hg::kPanel));
   const size_t tiles = static_cast<size_t>(ceil_div(s.vocab, kTile));
+  if (kind == HG_XENT_SCORE && s.m <= hg::kScoreRows) {
+    p->part = reinterpret_cast<float *>(take(8 * m * hg::kScoreGroups));
+    return at;
+  }
+  p->xc = take(2 * m * hg::kPanel * ceil_div(s.hidden, hg::kPanel));
   if (kind != HG_XENT_GRAD) p->part = reinterpret_cast<float *>(take(8 * tiles * m));
   if (kind != HG_XENT_SCORE) {
     const int tm = ceil_div(s.m, kTile), tn = ceil_div(s.hidden, kTile);
@@ -265,6 +269,10 @@ HG_API int hg_xent(const hg_xent_shape *s, const void *x, const void *const *w, 
                        nullptr, 0, 0, ws, ws_bytes, &v, &p);
   if (rc != HG_OK || s->m == 0) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
+  if (s->m <= hg::kScoreRows) {
+    HIP_TRY(hg::launch_xent_score(p, v, x, labels, loss, lse, st));
+    return HG_OK;
+  }
   HIP_TRY(hg::launch_xent_pack(p, x, labels, loss, lse, st));
   HIP_TRY(hg::launch_xent_logits(p, v, 0, 0, p.vocab, st));
   HIP_TRY(hg::launch_xent_join(p, nullptr, loss, lse, st));

@@ -257,8 +257,197 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
   }
 }
 
-// One wave of 16 rows x 16 tile lanes... merges a row's tiles: 16 rows per
-// workgroup of 256, 16 threads a row.
+// ---------------------------------------------------------------------------
+// Few rows (decode, speculative tokens): the matrix is read once and bounds the
+// call, so every CU streams its own run of the vocabulary, without a break from
+// its first row to its last: workgroup b takes the 16-row units b*units/G ..,
+// in tiles of 256 rows x 64 k, the loads running on across tile ends.
+//
+// A stage is 256 rows of W (32 KB) and 16*MB rows of x, read back from L2 by
+// every workgroup (rows from m on lie beyond the resource and cost nothing).
+// Wave v loads and multiplies rows 32v .. 32v+31 of the tile, so a barrier per
+// step is needed for x alone. v_mfma_f32_16x16x32 with W as its rows: a lane
+// holds, of one row of x, 8 columns per tile, and keeps a running maximum and
+// sum over all of its columns; lanes, waves and workgroups are joined at the
+// end. Four stages up to 64 rows, three beyond: 80 KB or more in flight per CU.
+template <class T, int NT, int MB>
+__global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, const void *labels,
+                                                  ShardTableN<NT> w, int shard) {
+  constexpr int XI = MB > 4 ? MB / 4 : 1;       // x loads per wave and step
+  constexpr int kXBytes = XI * 8 * 1024;        // 64 or 128 rows of 128 bytes
+  constexpr int kStageB = 4 * kSubBytes + kXBytes;
+  constexpr int ST = MB > 4 ? 3 : 4;
+  constexpr int kLoads = 4 + XI;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[ST * kStageB];
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const long long units = (pl.vocab + 15) >> 4;
+  const int r0 = static_cast<int>(units * blockIdx.x / gridDim.x) * 16;
+  int r1 = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x) * 16;
+  if (r1 > pl.vocab) r1 = pl.vocab;
+  const int ks = (pl.hidden + kStep - 1) / kStep;
+  const int steps = r1 > r0 ? (r1 - r0 + kTile - 1) / kTile * ks : 0;
+
+  const LoadLane ll = load_lane<false>(lane);
+  const rsrc_t xr = resource(x, static_cast<long long>(pl.m) * pl.hidden * 2);
+  const int k8 = pl.hidden >> 3;
+  const int sub = wave >> 1, q0 = 4 * (wave & 1);
+  RankRowSource<NT, true> b;
+  int lt = 0, lk = 0;  // tile and step of k of the next loads
+  b.init(w, shard, r1, pl.hidden, r0, sub, q0, lane);
+  auto load = [&](int s) __attribute__((always_inline)) {
+    unsigned char *st = lds + (s % ST) * kStageB;
+    // steps past the last one load nothing and keep the counts
+    const int kk = s < steps ? lk : ks;
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+      const int q = 8 * i + wave;
+      const int o = q & 1;
+      const unsigned v = static_cast<unsigned>((8 * q + ll.row) * pl.hidden * 2 + kk * 128 +
+                                               ll.chunk[o] * 16);
+      load_lds(xr, st + 4 * kSubBytes + q * 1024, kk * 8 + ll.chunk[o] < k8 ? v : kBeyond);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) b.load(st + sub * kSubBytes, sub, q0 + t, kk);
+    if (++lk == ks && s + 1 < steps) {
+      lk = 0;
+      ++lt;
+      b.init(w, shard, r1, pl.hidden, r0 + lt * kTile, sub, q0, lane);
+    }
+  };
+
+  FragLane<false> f;
+  f.init(lane);
+  f32x4 acc[2][MB];
+  float top[MB], sum[MB];
+  int lab[MB];
+#pragma unroll
+  for (int j = 0; j < MB; ++j) {
+    acc[0][j] = acc[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    top[j] = -__builtin_inff();
+    sum[j] = 0.f;
+    const int row = 16 * j + l16;
+    const long long t = row < pl.m ? label_at(labels, pl.label_bytes, row) : -1;
+    lab[j] = t >= 0 && t < pl.vocab ? static_cast<int>(t) : -1;
+  }
+  const float s2 = pl.scale * kLog2e;
+  __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");  // the labels: only the loads below count
+
+#pragma unroll
+  for (int s = 0; s < ST - 1; ++s) load(s);
+  int ck = 0, n0 = r0 + 32 * wave + 4 * g;
+  for (int s = 0; s < steps; ++s) {
+    wait_vm_lds<kLoads * (ST - 2)>();
+    tile_barrier();
+    load(s + ST - 1);
+    const unsigned char *st = lds + (s % ST) * kStageB;
+    const unsigned char *sw = st + sub * kSubBytes + (wave & 1) * 32 * 128;
+    const unsigned char *sx = st + 4 * kSubBytes;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const s16x8 w0 = f.read(sw, 0, kk), w1 = f.read(sw, 1, kk);
+#pragma unroll
+      for (int j = 0; j < MB; ++j) {
+        const s16x8 xv = f.read(sx, j, kk);
+        acc[0][j] = T::mma(w0, xv, acc[0][j]);
+        acc[1][j] = T::mma(w1, xv, acc[1][j]);
+      }
+    }
+    if (++ck == ks) {  // the tile's columns are done
+      ck = 0;
+#pragma unroll
+      for (int j = 0; j < MB; ++j) {
+        float mx = top[j];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int n = n0 + 16 * h + t;
+            const float v = n < r1 ? acc[h][j][t] * s2 : -__builtin_inff();
+            if (n == lab[j] && n < r1) pl.r.zt[16 * j + l16] = v;  // past r1: another's
+            acc[h][j][t] = v;
+            mx = fmaxf(mx, v);
+          }
+        const float ref = mx == -__builtin_inff() ? 0.f : mx;
+        float e = sum[j] * exp2_(top[j] - ref);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) e += exp2_(acc[h][j][t] - ref);
+        sum[j] = e;
+        top[j] = mx;
+        acc[0][j] = acc[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      n0 += kTile;
+    }
+  }
+  wait_vm_lds<0>();
+  tile_barrier();
+  float *red = reinterpret_cast<float *>(lds);  // [8][16*MB][2]
+#pragma unroll
+  for (int j = 0; j < MB; ++j) {
+    float mx = top[j];
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    float e = sum[j] * exp2_(top[j] - (mx == -__builtin_inff() ? 0.f : mx));
+    e += __shfl_xor(e, 16);
+    e += __shfl_xor(e, 32);
+    if (g == 0) {
+      red[(wave * 16 * MB + 16 * j + l16) * 2] = mx;
+      red[(wave * 16 * MB + 16 * j + l16) * 2 + 1] = e;
+    }
+  }
+  __syncthreads();
+  const int row = static_cast<int>(threadIdx.x);
+  if (row < 16 * MB && row < pl.m) {
+    float mx = -__builtin_inff(), e = 0.f;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) mx = fmaxf(mx, red[(v * 16 * MB + row) * 2]);
+    const float ref = mx == -__builtin_inff() ? 0.f : mx;
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+      e += red[(v * 16 * MB + row) * 2 + 1] * exp2_(red[(v * 16 * MB + row) * 2] - ref);
+    float2 *part = reinterpret_cast<float2 *>(pl.part);
+    part[static_cast<long long>(row) * kScoreGroups + blockIdx.x] = float2{mx, e};
+  }
+}
+
+// One wave per row joins the workgroups' statistics.
+__global__ __launch_bounds__(64) void k_score_join(XentPlan pl, const void *labels, int groups,
+                                                   float *loss, float *lse) {
+  const int row = static_cast<int>(blockIdx.x), lane = static_cast<int>(threadIdx.x);
+  const float2 *part = reinterpret_cast<const float2 *>(pl.part) +
+                       static_cast<long long>(row) * kScoreGroups;
+  const long long t = label_at(labels, pl.label_bytes, row);
+  const float zt = pl.r.zt[row];
+  float2 p[kScoreGroups / 64];
+  float mx = -__builtin_inff(), sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kScoreGroups / 64; ++k) {
+    p[k] = lane + 64 * k < groups ? part[lane + 64 * k] : float2{-__builtin_inff(), 0.f};
+    mx = fmaxf(mx, p[k].x);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+  const float ref = mx == -__builtin_inff() ? 0.f : mx;
+#pragma unroll
+  for (int k = 0; k < kScoreGroups / 64; ++k) sum += p[k].y * exp2_(p[k].x - ref);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+  if (lane != 0) return;
+  float a = 0.f, b = 0.f;
+  if (t != pl.ignore) {
+    const float l2 = ref + __log2f(sum);
+    const bool real = t >= 0 && t < pl.vocab;
+    b = real ? l2 * kLn2 : __builtin_nanf("");
+    a = real ? (l2 - zt) * kLn2 + pl.z_weight * b * b : b;
+  }
+  loss[row] = a;
+  lse[row] = b;
+}
+
+// Merges a row's tiles: 16 rows per workgroup, 16 threads a row.
 __global__ __launch_bounds__(256) void k_join(XentPlan pl, const float *grad, float *loss,
                                               float *lse) {
   __shared__ float smax[16][17], ssum[16][17];
@@ -545,6 +734,30 @@ hipError_t launch_xent_logits(const XentPlan &p, const VocabMatrix &w, int mode,
       else go(k_logits<T, NT, kGrad>);
     });
   });
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_score(const XentPlan &p, const VocabMatrix &w, const void *x,
+                             const void *labels, float *loss, float *lse, hipStream_t s) {
+  const int units = ceil_div(p.vocab, 16);
+  const int groups = units < kScoreGroups ? units : kScoreGroups;
+  by_type(p.half, [&](auto type) {
+    by_table(w.tp, [&](auto nt) {
+      using T = decltype(type);
+      constexpr int NT = decltype(nt)::value;
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(groups), dim3(512), 0, s, p, static_cast<const u32x4 *>(x),
+                           labels, small_table<NT>(w.t), w.shard);
+      };
+      if (p.m <= 16) go(k_score<T, NT, 1>);
+      else if (p.m <= 32) go(k_score<T, NT, 2>);
+      else if (p.m <= 64) go(k_score<T, NT, 4>);
+      else go(k_score<T, NT, 8>);
+    });
+  });
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_score_join, dim3(p.m), dim3(64), 0, s, p, labels, groups, loss, lse);
   return hipGetLastError();
 }
 

@@ -23,7 +23,7 @@ import functools
 import torch
 
 from . import _lib
-from ._lib import check, lib, pointer_array
+from ._lib import check, lib
 
 __all__ = ["head_xent", "head_xent_grad", "head_xent_step", "head_loss", "embed", "embed_grad", "embedding"]
 
@@ -36,8 +36,20 @@ _DTYPES = {torch.bfloat16: _lib.HG_BF16, torch.float16: _lib.HG_FP16, torch.floa
 WORKSPACE_LIMIT = 4 << 30
 
 
-def _pointer(t: torch.Tensor | None) -> ctypes.c_void_p | None:
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+@functools.lru_cache(maxsize=None)
+def _table(tp: int):
+    """The C type of a table of tp block pointers."""
+    return ctypes.c_void_p * tp
+
+
+def _call(name: str, device: torch.device, *args) -> None:
+    """One library call on the device's current stream, appended to `args`."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        check(getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index)), name)
+        return
+    with torch.cuda.device(device):
+        check(getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index)), name)
 
 
 def _matrix(w, tp: int, shard: int, dtypes) -> tuple[list[int], int, torch.dtype, torch.device]:
@@ -139,10 +151,8 @@ class _Head:
         return dx, _gradient_buffer(dw, self.rows, self.hidden, self.dtype, self.device, accumulate)
 
     def call(self, name, *args):
-        with torch.cuda.device(self.device):
-            stream = ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
-            check(getattr(lib(), name)(ctypes.byref(self.shape), _pointer(self.x), pointer_array(self.ptrs),
-                                       _pointer(self.labels), *args, stream), name)
+        _call(name, self.device, self.shape, self.x.data_ptr(), _table(len(self.ptrs))(*self.ptrs),
+              self.labels.data_ptr(), *args)
 
 
 def _gradient_buffer(dw, rows, hidden, dtype, device, accumulate) -> torch.Tensor:
@@ -167,7 +177,7 @@ def head_xent(x: torch.Tensor, w, labels: torch.Tensor, tp: int, shard: int, voc
     h = _Head(x, w, labels, tp, shard, vocab, ignore, scale, z_weight)
     loss, lse = h.losses()
     ws = h.workspace(_lib.HG_XENT_SCORE, 0)
-    h.call("hg_xent", _pointer(loss), _pointer(lse), _pointer(ws), ws.numel())
+    h.call("hg_xent", loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
     return loss, lse
 
 
@@ -185,8 +195,8 @@ def head_xent_grad(x: torch.Tensor, w, labels: torch.Tensor, lse: torch.Tensor, 
     lse, grad = h.rows_of(lse, "lse"), h.rows_of(grad, "grad")
     dx, dw = h.grads(dx, dw, accumulate)
     ws = h.workspace(_lib.HG_XENT_GRAD, workspace_limit)
-    h.call("hg_xent_grad", _pointer(lse), _pointer(grad), _pointer(dx), _pointer(dw),
-           int(dw.dtype != h.dtype), int(accumulate), _pointer(ws), ws.numel())
+    h.call("hg_xent_grad", lse.data_ptr(), grad.data_ptr(), dx.data_ptr(), dw.data_ptr(),
+           int(dw.dtype != h.dtype), int(accumulate), ws.data_ptr(), ws.numel())
     return dx, dw
 
 
@@ -204,8 +214,8 @@ def head_xent_step(x: torch.Tensor, w, labels: torch.Tensor, grad: torch.Tensor,
     loss, lse = h.losses()
     dx, dw = h.grads(dx, dw, accumulate)
     ws = h.workspace(_lib.HG_XENT_STEP, workspace_limit)
-    h.call("hg_xent_step", _pointer(grad), _pointer(loss), _pointer(lse), _pointer(dx), _pointer(dw),
-           int(dw.dtype != h.dtype), int(accumulate), _pointer(ws), ws.numel())
+    h.call("hg_xent_step", grad.data_ptr(), loss.data_ptr(), lse.data_ptr(), dx.data_ptr(), dw.data_ptr(),
+           int(dw.dtype != h.dtype), int(accumulate), ws.data_ptr(), ws.numel())
     return loss, lse, dx, dw
 
 
@@ -259,10 +269,8 @@ def embed(tokens: torch.Tensor, w, tp: int, shard: int, scale: float = 1.0,
         out = torch.empty(shape, dtype=dtype, device=device)
     else:
         _given(out, "out", shape, (dtype,), device)
-    with torch.cuda.device(device):
-        check(lib().hg_embed(int(tp), int(shard), hidden, _DTYPES[dtype], pointer_array(ptrs), _pointer(tokens),
-                             tokens.element_size(), tokens.numel(), float(scale), _pointer(out),
-                             ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)), "hg_embed")
+    _call("hg_embed", device, tp, shard, hidden, _DTYPES[dtype], _table(tp)(*ptrs), tokens.data_ptr(),
+          tokens.element_size(), tokens.numel(), scale, out.data_ptr())
     return out
 
 
@@ -288,11 +296,9 @@ def embed_grad(tokens: torch.Tensor, dy: torch.Tensor, tp: int, shard: int, scal
     tp, shard = int(tp), int(shard)
     dw = _gradient_buffer(dw, tp * shard, hidden, dy.dtype, device, accumulate)
     ws = _workspace(_embed_bytes(tp, shard, hidden, tokens.numel()), device)
-    with torch.cuda.device(device):
-        check(lib().hg_embed_grad(tp, shard, hidden, _DTYPES[dy.dtype], _pointer(tokens), tokens.element_size(),
-                                  tokens.numel(), _pointer(dy), float(scale), _pointer(dw),
-                                  int(dw.dtype != dy.dtype), int(accumulate), _pointer(ws), ws.numel(),
-                                  ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)), "hg_embed_grad")
+    _call("hg_embed_grad", device, tp, shard, hidden, _DTYPES[dy.dtype], tokens.data_ptr(), tokens.element_size(),
+          tokens.numel(), dy.data_ptr(), scale, dw.data_ptr(), int(dw.dtype != dy.dtype), int(accumulate),
+          ws.data_ptr(), ws.numel())
     return dw
 
 

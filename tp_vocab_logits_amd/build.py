@@ -8,6 +8,7 @@ Always recompiles; each result replaces the previous file atomically.
 
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
@@ -37,16 +38,40 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found: cannot build libhg.so")
 
 
-def compile_command(output: str) -> list[str]:
+def compile_command(source: str, output: str) -> list[str]:
+    """One source of libhg.so to an object file."""
     return [
-        hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+        hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-c",
         "-fvisibility=hidden", "-Wall", "-Wno-unused-function",
         # keep the compiler from forming packed-FP32 instructions
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-        "-I", INCLUDE, "-I", CSRC, "-x", "hip",
-        *[os.path.join(CSRC, s) for s in SOURCES],
-        "-o", output,
+        "-I", INCLUDE, "-I", CSRC, "-x", "hip", os.path.join(CSRC, source), "-o", output,
     ]
+
+
+def _run(cmd: list[str], verbose: bool) -> subprocess.CompletedProcess:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.run(cmd, capture_output=True, text=True)
+
+
+def compile_library(output: str, verbose: bool = False) -> None:
+    """Compile the sources side by side and link them into `output`."""
+    with tempfile.TemporaryDirectory(prefix="hg_build.") as tmp:
+        objects = [os.path.join(tmp, s + ".o") for s in SOURCES]
+        with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as pool:
+            results = list(pool.map(lambda so: _run(compile_command(*so), verbose), zip(SOURCES, objects)))
+        if all(r.returncode == 0 for r in results):
+            results.append(_run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objects, "-o", output],
+                                verbose))
+    for res in results:
+        if res.returncode != 0:
+            raise RuntimeError("libhg.so build failed:\n" + (res.stderr or res.stdout))
+        # hipcc's host pass does not know the packed-fp32 feature and says so
+        noise = [ln for ln in (res.stderr or "").splitlines()
+                 if ln.strip() and "packed-fp32-ops" not in ln and "not a recognized feature" not in ln]
+        if verbose and noise:
+            print("\n".join(noise), file=sys.stderr)
 
 
 def build_fastcall(verbose: bool = False) -> str:
@@ -124,17 +149,7 @@ def build(verbose: bool = False) -> str:
     fd, tmp = tempfile.mkstemp(prefix="libhg.", suffix=".so.tmp", dir=PKG)
     os.close(fd)
     try:
-        cmd = compile_command(tmp)
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        # hipcc's host pass does not know the packed-fp32 feature and says so
-        noise = [ln for ln in (res.stderr or "").splitlines()
-                 if ln.strip() and "packed-fp32-ops" not in ln and "not a recognized feature" not in ln]
-        if res.returncode != 0:
-            raise RuntimeError("libhg.so build failed:\n" + (res.stderr or res.stdout))
-        if verbose and noise:
-            print("\n".join(noise), file=sys.stderr)
+        compile_library(tmp, verbose)
         os.replace(tmp, LIB)
     finally:
         if os.path.exists(tmp):

@@ -77,7 +77,7 @@ __device__ __forceinline__ float from16(uint32_t b) {
   return static_cast<float>(__builtin_bit_cast(typename T::elt, static_cast<unsigned short>(b)));
 }
 
-constexpr int kTile = 256;           // C tile edge
+constexpr int kTile = 256;           // C tile edge (the small tile's is half of it)
 constexpr int kStep = 64;            // k per step
 constexpr int kSubBytes = 64 * 128;  // one 64 x 64 sub-tile
 constexpr int kStageBytes = 8 * kSubBytes;
@@ -172,12 +172,12 @@ struct PanelRowSource {
 
 // Row operand in rank blocks (NT table entries): tile row m is matrix row
 // n0 + m. Blocks are a multiple of 32 rows, so eight rows share a block. A
-// wave always loads the same four instructions of the same sub-tile, so it
-// keeps one resource for each.
-template <int NT, bool STREAM = false>
+// wave always loads the same L instructions of the same sub-tile, so it keeps
+// one resource for each.
+template <int NT, int L, bool STREAM = false>
 struct RankRowSource {
   static constexpr bool kColumn = false;
-  rsrc_t r[4];
+  rsrc_t r[L];
   unsigned off[2];
   int chunk[2];
   int k8;
@@ -191,7 +191,7 @@ struct RankRowSource {
       off[o] = static_cast<unsigned>(p.row * hidden * 2 + p.chunk[o] * 16);
     }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < L; ++t) {
       const int n = n0 + 64 * sub + 8 * (q0 + t);
       const int left = limit - n;
       const int rank = NT == 1 || left <= 0 ? 0 : n / shard;
@@ -203,29 +203,30 @@ struct RankRowSource {
   }
   __device__ __forceinline__ void load(unsigned char *lds, int, int q, int step) const {
     const int o = q & 1;
-    load_lds<STREAM>(r[q & 3], lds + q * 1024,
+    load_lds<STREAM>(r[q & (L - 1)], lds + q * 1024,
              step * 8 + chunk[o] < k8 ? off[o] + static_cast<unsigned>(step * 128) : kBeyond);
   }
 };
 
-// Column operand in one panel: k row k at base + k*512 bytes; K rows.
+// Column operand in one panel, from its column `col` on: k row k at base +
+// k*512 bytes; K rows.
 struct PanelColumnSource {
   static constexpr bool kColumn = true;
   const unsigned char *base;
   unsigned off[2];
-  int rows;
-  __device__ __forceinline__ void init(const void *base_, int rows_, int lane) {
+  int rows, col;
+  __device__ __forceinline__ void init(const void *base_, int col_, int rows_, int lane) {
     const LoadLane p = load_lane<true>(lane);
-    base = static_cast<const unsigned char *>(base_);
+    base = static_cast<const unsigned char *>(base_) + 2 * col_;
+    col = col_;
     rows = rows_;
 #pragma unroll
     for (int o = 0; o < 2; ++o) off[o] = static_cast<unsigned>(p.row * 512 + p.chunk[o] * 16);
   }
   __device__ __forceinline__ void load(unsigned char *lds, int sub, int q, int step) const {
     const int left = rows - step * 64;
-    const rsrc_t r = resource(
-        base + (left <= 0 ? 0ll : static_cast<long long>(step) * (64 * 512)),
-        left > 64 ? 64 * 512 : left * 512);
+    const rsrc_t r = resource(base + (left <= 0 ? 0ll : static_cast<long long>(step) * (64 * 512)),
+                              left > 64 ? 64 * 512 : left * 512 - 2 * col);
     load_lds(r, lds + q * 1024, off[q & 1] + static_cast<unsigned>(8 * q * 512 + sub * 128));
   }
 };
@@ -319,91 +320,157 @@ __device__ __forceinline__ void tile_barrier() {
   __asm__ __volatile__("" ::: "memory");
 }
 
-// acc[i][j]: rows 128*(wave >> 2) + 16*i + (lane & 15), columns
-// 64*(wave & 3) + 16*j + 4*(lane >> 4) + t of the tile. On return every load
-// has landed and every wave is past its last LDS read.
-template <class T, class SA, class SB>
-__device__ __forceinline__ void tile_product(const SA &a, const SB &b, int steps,
-                                             unsigned char *lds, f32x4 (&acc)[8][4]) {
-  const int lane = static_cast<int>(threadIdx.x) & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-  const int wr = wave >> 2, wc = wave & 3;
-  FragLane<SA::kColumn> fa;
-  FragLane<SB::kColumn> fb;
-  fa.init(lane);
-  fb.init(lane);
+// The two tiles. acc[i][j][t] is row kRows*(wave >> 2) + 16*i + (lane & 15) and
+// column kCols*(wave & 3) + 16*j + 4*(lane >> 4) + t. On return of product()
+// every load has landed and every wave is past its last LDS read.
+struct BigTile {
+  static constexpr int kEdge = 256, MI = 8, NJ = 4, kRows = 128, kCols = 64;
+  static constexpr int kBLoads = 4;  // B's load instructions per wave and step,
+  static __device__ __forceinline__ int b_sub(int wave) { return wave & 3; }  // their sub-tile
+  static __device__ __forceinline__ int b_first(int wave) { return 4 * (wave >> 2); }  // and first
 
-  // A: each half (64 rows) of the wave's 128 is a sub-tile, loaded by the
-  // four waves that read it; B: sub-tile wc, half of it per wave.
-  auto load_a = [&](int half, int step) __attribute__((always_inline)) {
-    const int sub = 2 * wr + half;
-    unsigned char *st = lds + (step & 1) * kStageBytes + sub * kSubBytes;
-    a.load(st, sub, 2 * wc, step);
-    a.load(st, sub, 2 * wc + 1, step);
-  };
-  auto load_b = [&](int step) __attribute__((always_inline)) {
-    unsigned char *st = lds + (step & 1) * kStageBytes + (4 + wc) * kSubBytes;
+  template <class T, class SA, class SB>
+  static __device__ __forceinline__ void product(const SA &a, const SB &b, int steps,
+                                               unsigned char *lds, f32x4 (&acc)[8][4]) {
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int wr = wave >> 2, wc = wave & 3;
+    FragLane<SA::kColumn> fa;
+    FragLane<SB::kColumn> fb;
+    fa.init(lane);
+    fb.init(lane);
+
+    // A: each half (64 rows) of the wave's 128 is a sub-tile, loaded by the
+    // four waves that read it; B: sub-tile wc, half of it per wave.
+    auto load_a = [&](int half, int step) __attribute__((always_inline)) {
+      const int sub = 2 * wr + half;
+      unsigned char *st = lds + (step & 1) * kStageBytes + sub * kSubBytes;
+      a.load(st, sub, 2 * wc, step);
+      a.load(st, sub, 2 * wc + 1, step);
+    };
+    auto load_b = [&](int step) __attribute__((always_inline)) {
+      unsigned char *st = lds + (step & 1) * kStageBytes + (4 + wc) * kSubBytes;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) b.load(st, wc, 4 * wr + t, step);
-  };
+      for (int t = 0; t < 4; ++t) b.load(st, wc, 4 * wr + t, step);
+    };
 
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  load_b(0);
-  load_a(0, 0);
-  load_a(1, 0);
-  load_b(1);
-  load_a(0, 1);
-  wait_vm_lds<8>();
-  tile_barrier();
-  if (wr == 1) tile_barrier();
+    load_b(0);
+    load_a(0, 0);
+    load_a(1, 0);
+    load_b(1);
+    load_a(0, 1);
+    wait_vm_lds<8>();
+    tile_barrier();
+    if (wr == 1) tile_barrier();
 
-  s16x8 ra[4][2], rb[4][2];
-  auto multiply = [&](int half) __attribute__((always_inline)) {
-    __builtin_amdgcn_s_setprio(1);
+    s16x8 ra[4][2], rb[4][2];
+    auto multiply = [&](int half) __attribute__((always_inline)) {
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+      for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[4 * half + i][j] = T::mma(rb[j][ks], ra[i][ks], acc[4 * half + i][j]);
-    __builtin_amdgcn_s_setprio(0);
-  };
-  for (int kb = 0; kb < steps; ++kb) {
-    const unsigned char *st = lds + (kb & 1) * kStageBytes;
-    const unsigned char *sa = st + 2 * wr * kSubBytes;
-    const unsigned char *sb = st + (4 + wc) * kSubBytes;
+          for (int j = 0; j < 4; ++j)
+            acc[4 * half + i][j] = T::mma(rb[j][ks], ra[i][ks], acc[4 * half + i][j]);
+      __builtin_amdgcn_s_setprio(0);
+    };
+    for (int kb = 0; kb < steps; ++kb) {
+      const unsigned char *st = lds + (kb & 1) * kStageBytes;
+      const unsigned char *sa = st + 2 * wr * kSubBytes;
+      const unsigned char *sb = st + (4 + wc) * kSubBytes;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
+      for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) rb[j][ks] = fb.read(sb, j, ks);
+        for (int j = 0; j < 4; ++j) rb[j][ks] = fb.read(sb, j, ks);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ra[i][ks] = fa.read(sa, i, ks);
+        for (int i = 0; i < 4; ++i) ra[i][ks] = fa.read(sa, i, ks);
+      }
+      load_a(1, kb + 1);
+      wait_vm_lds<8>();
+      tile_barrier();
+      multiply(0);
+      tile_barrier();
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ra[i][ks] = fa.read(sa + kSubBytes, i, ks);
+      load_b(kb + 2);
+      load_a(0, kb + 2);
+      wait_vm_lds<8>();
+      tile_barrier();
+      multiply(1);
+      tile_barrier();
     }
-    load_a(1, kb + 1);
-    wait_vm_lds<8>();
-    tile_barrier();
-    multiply(0);
-    tile_barrier();
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ra[i][ks] = fa.read(sa + kSubBytes, i, ks);
-    load_b(kb + 2);
-    load_a(0, kb + 2);
-    wait_vm_lds<8>();
-    tile_barrier();
-    multiply(1);
+    if (wr == 0) tile_barrier();
+    wait_vm_lds<0>();
     tile_barrier();
   }
-  if (wr == 0) tile_barrier();
-  wait_vm_lds<0>();
-  tile_barrier();
-}
+};
+
+// 128 x 128 for problems whose 256 x 256 tiles would leave CUs idle: a quarter
+// of the work per tile, a ring of four 32 KB stages loaded three steps ahead
+// and one barrier per step. (At 256-column tiles, 33 rows over V = 4096, H = 264
+// spread over 16 workgroups; measured SMALLTILE.)
+struct SmallTile {
+  static constexpr int kEdge = 128, MI = 4, NJ = 2, kRows = 64, kCols = 32;
+  static constexpr int kBLoads = 2;
+  static __device__ __forceinline__ int b_sub(int wave) { return wave >> 2; }
+  static __device__ __forceinline__ int b_first(int wave) { return 2 * (wave & 3); }
+
+  template <class T, class SA, class SB>
+  static __device__ __forceinline__ void product(const SA &a, const SB &b, int steps,
+                                                 unsigned char *lds, f32x4 (&acc)[4][2]) {
+    constexpr int kBytes = 4 * kSubBytes;
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int wr = wave >> 2, wc = wave & 3;
+    FragLane<SA::kColumn> fa;
+    FragLane<SB::kColumn> fb;
+    fa.init(lane);
+    fb.init(lane);
+    auto load = [&](int step) __attribute__((always_inline)) {
+      unsigned char *st = lds + (step & 3) * kBytes + wr * kSubBytes;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) a.load(st, wr, 2 * wc + t, step);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) b.load(st + 2 * kSubBytes, wr, 2 * wc + t, step);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 3; ++s) load(s);
+    for (int s = 0; s < steps; ++s) {
+      wait_vm_lds<8>();
+      tile_barrier();
+      load(s + 3);
+      const unsigned char *sa = lds + (s & 3) * kBytes + wr * kSubBytes;
+      const unsigned char *sb = lds + (s & 3) * kBytes + (2 + (wc >> 1)) * kSubBytes;
+      s16x8 ra[4], rb[2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        // block 2*(wc & 1) + j: the selection stays in the lane offsets
+#pragma unroll
+        for (int j = 0; j < 2; ++j) rb[j] = (wc & 1) ? fb.read(sb, 2 + j, ks) : fb.read(sb, j, ks);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ra[i] = fa.read(sa, i, ks);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = T::mma(rb[j], ra[i], acc[i][j]);
+      }
+    }
+    wait_vm_lds<0>();
+    tile_barrier();
+  }
+};
 
 // Tile `id` of tm x tn: groups of 8 tile rows, columns inside a group, rows
 // fastest, so that the workgroups in flight on an XCD share operands in its

@@ -45,13 +45,15 @@ struct XentPlan {
   long long ignore;
   int label_bytes;
   int piece;       // vocabulary columns per piece, a multiple of 256
+  bool small_logits, small_grads;  // products on 128 x 128 tiles (256 x 256 otherwise)
+  int ref;         // columns that share a probability reference: the logits' tile edge
   int split_dx;    // splits of the vocabulary in dX = d W
   int split_dw;    // splits of the rows in dW = d^T X
   int dw_rows;     // matrix rows of one split's partial sums
   XentRows r;
   void *xc;        // packed rows of X, [hidden / 256 up][m][256]
   void *d;         // d (or unnormalised probabilities) of one piece, [piece / 256][m][256]
-  float *part;     // [2][tiles][m] per 256-column tile: maximum (base 2), sum; few rows:
+  float *part;     // [2][tiles][m] per tile of `ref` columns: maximum (base 2), sum; few rows:
                    // [m][kScoreGroups][2]
   float *dxp;      // [split_dx][m][hidden]
   float *dwp;      // [split_dw][dw_rows][hidden] when split_dw > 1
@@ -76,11 +78,10 @@ hipError_t launch_xent_factors(const XentPlan &p, const float *lse, const float 
                                hipStream_t s);
 // Unnormalised probabilities -> d, in place.
 hipError_t launch_xent_normalise(const XentPlan &p, hipStream_t s);
-hipError_t launch_xent_dx(const XentPlan &p, const VocabMatrix &w, int v0, int cols, bool first,
-                          hipStream_t s);
+// dX's partial sums and dW's rows of the piece, in one launch.
+hipError_t launch_xent_grads(const XentPlan &p, const VocabMatrix &w, int v0, int cols, bool first,
+                             void *dw, bool wide, bool accumulate, hipStream_t s);
 hipError_t launch_xent_dx_join(const XentPlan &p, void *dx, hipStream_t s);
-hipError_t launch_xent_dw(const XentPlan &p, int v0, int cols, void *dw, bool wide, bool accumulate,
-                          hipStream_t s);
 
 // `bytes` zero bytes at a 16-byte aligned address (bytes a multiple of 16).
 hipError_t launch_zero(void *p, size_t bytes, hipStream_t s);

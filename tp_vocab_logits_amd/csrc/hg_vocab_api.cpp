@@ -112,7 +112,12 @@ size_t lay_out(const hg_xent_shape &s, int kind, int piece, char *ws, XentPlan *
   p->r.lse2 = reinterpret_cast<float *>(take(4 * m));
   p->r.ca = reinterpret_cast<float *>(take(4 * m));
   p->r.cb = reinterpret_cast<float *>(take(4 * m));
-  const size_t tiles = static_cast<size_t>(ceil_div(s.vocab, kTile));
+  // The small tile while the big one gives fewer tiles than CUs.
+  const long long tm = ceil_div(s.m, kTile), tn = ceil_div(s.hidden, kTile);
+  p->small_logits = tm * ceil_div(kind == HG_XENT_GRAD ? piece : s.vocab, kTile) < kCus;
+  p->small_grads = ceil_div(piece, kTile) * tn < kCus;
+  p->ref = p->small_logits ? kTile / 2 : kTile;
+  const size_t tiles = static_cast<size_t>(ceil_div(s.vocab, p->ref));
   if (kind == HG_XENT_SCORE && s.m <= hg::kScoreRows) {
     p->part = reinterpret_cast<float *>(take(8 * m * hg::kScoreGroups));
     return at;
@@ -120,11 +125,10 @@ size_t lay_out(const hg_xent_shape &s, int kind, int piece, char *ws, XentPlan *
   p->xc = take(2 * m * hg::kPanel * ceil_div(s.hidden, hg::kPanel));
   if (kind != HG_XENT_GRAD) p->part = reinterpret_cast<float *>(take(8 * tiles * m));
   if (kind != HG_XENT_SCORE) {
-    const int tm = ceil_div(s.m, kTile), tn = ceil_div(s.hidden, kTile);
-    p->split_dx = pick_split(static_cast<long long>(tm) * tn, ceil_div(piece, kStep),
-                             4.0 * m * h, false);
-    p->split_dw = pick_split(static_cast<long long>(piece / kTile) * tn, ceil_div(s.m, kStep),
-                             4.0 * piece * h, true);
+    const int edge = p->small_grads ? kTile / 2 : kTile;
+    const long long hn = ceil_div(s.hidden, edge);
+    p->split_dx = pick_split(ceil_div(s.m, edge) * hn, ceil_div(piece, kStep), 4.0 * m * h, false);
+    p->split_dw = pick_split(piece / edge * hn, ceil_div(s.m, kStep), 4.0 * piece * h, true);
     p->d = take(2 * m * piece);
     p->dxp = reinterpret_cast<float *>(take(4 * m * h * p->split_dx));
     if (p->split_dw > 1) {
@@ -232,8 +236,7 @@ int products(const XentPlan &p, const VocabMatrix &v, bool ready, void *dx, void
   for (int v0 = 0; v0 < p.vocab; v0 += p.piece) {
     const int cols = p.vocab - v0 < p.piece ? p.vocab - v0 : p.piece;
     if (!ready) HIP_TRY(hg::launch_xent_logits(p, v, 2, v0, cols, s));
-    HIP_TRY(hg::launch_xent_dx(p, v, v0, cols, v0 == 0, s));
-    HIP_TRY(hg::launch_xent_dw(p, v0, cols, dw, wide != 0, accumulate != 0, s));
+    HIP_TRY(hg::launch_xent_grads(p, v, v0, cols, v0 == 0, dw, wide != 0, accumulate != 0, s));
   }
   HIP_TRY(hg::launch_xent_dx_join(p, dx, s));
   return HG_OK;

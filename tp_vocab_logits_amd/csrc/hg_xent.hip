@@ -77,9 +77,64 @@ __device__ __forceinline__ long long label_at(const void *labels, int bytes, int
                     : static_cast<const int *>(labels)[i];
 }
 
-// Packs the rows that count, in order: one workgroup walks the labels 1024 at
-// a time (a running total in LDS). A row left out gets loss = lse = 0, a label
-// outside the vocabulary loss = lse = NaN and no part in the gradients.
+// What a row left out gets: loss = lse = 0, or NaN in both for a label outside
+// the vocabulary.
+__device__ __forceinline__ void leave_out(long long t, long long ignore, int i, float *loss,
+                                          float *lse) {
+  if (!loss) return;
+  const float v = t == ignore ? 0.f : __builtin_nanf("");
+  loss[i] = v;
+  lse[i] = v;
+}
+
+// The packed rows' x, 16 bytes per lane.
+__device__ __forceinline__ void pack_row(const u32x4 *x, u32x4 *xc, int i, int p, int m, int hv) {
+  const u32x4 *src = x + static_cast<long long>(i) * hv;
+  u32x4 *dst = xc + static_cast<long long>(p) * 32;
+  for (int k = static_cast<int>(threadIdx.x); k < hv; k += 256)
+    dst[static_cast<long long>(k >> 5) * m * 32 + (k & 31)] = src[k];
+}
+
+// Packs the rows that count, in order, in one launch: a workgroup per row
+// counts the rows before it that count. Up to kPackRows rows, where the labels
+// (32 KB) stay in the caches; one launch less than the two below.
+constexpr int kPackRows = 4096;
+__global__ __launch_bounds__(256) void k_pack_few(XentRows r, const void *labels, int label_bytes,
+                                                  int m, int vocab, long long ignore,
+                                                  const u32x4 *x, u32x4 *xc, int hv, float *loss,
+                                                  float *lse) {
+  __shared__ int wave_sum[4];
+  const int tid = static_cast<int>(threadIdx.x), i = static_cast<int>(blockIdx.x);
+  const long long t = label_at(labels, label_bytes, i);
+  const bool kept = t != ignore && t >= 0 && t < vocab;
+  int before = 0;
+  for (int k = tid; k < i; k += 256) {
+    const long long o = label_at(labels, label_bytes, k);
+    before += o != ignore && o >= 0 && o < vocab;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) before += __shfl_xor(before, d);
+  if ((tid & 63) == 0) wave_sum[tid >> 6] = before;
+  __syncthreads();
+  const int p = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
+  if (tid == 0) {
+    if (kept) {
+      r.idx[p] = i;
+      r.lab[p] = static_cast<int>(t);
+    } else {
+      leave_out(t, ignore, i, loss, lse);
+    }
+    r.inv[i] = kept ? p : -1;
+    if (i == m - 1) {
+      r.head[0] = p + kept;
+      r.head[1] = 0;
+    }
+  }
+  if (kept) pack_row(x, xc, i, p, m, hv);
+}
+
+// The same for more rows: one workgroup walks the labels 1024 at a time (a
+// running total in LDS), a second launch copies.
 __global__ __launch_bounds__(1024) void k_pack(XentRows r, const void *labels, int label_bytes,
                                                int m, int vocab, long long ignore, float *loss,
                                                float *lse) {
@@ -89,8 +144,7 @@ __global__ __launch_bounds__(1024) void k_pack(XentRows r, const void *labels, i
   for (int i0 = 0; i0 < m; i0 += 1024) {
     const int i = i0 + tid;
     const long long t = i < m ? label_at(labels, label_bytes, i) : ignore;
-    const bool out = t == ignore;
-    const bool kept = i < m && !out && t >= 0 && t < vocab;
+    const bool kept = i < m && t != ignore && t >= 0 && t < vocab;
     const unsigned long long votes = __ballot(kept);
     if (lane == 0) wave_sum[wave] = __popcll(votes);
     __syncthreads();
@@ -106,11 +160,7 @@ __global__ __launch_bounds__(1024) void k_pack(XentRows r, const void *labels, i
     }
     if (i < m) {
       r.inv[i] = kept ? p : -1;
-      if (!kept && loss) {
-        const float v = out ? 0.f : __builtin_nanf("");
-        loss[i] = v;
-        lse[i] = v;
-      }
+      if (!kept) leave_out(t, ignore, i, loss, lse);
     }
     base += total;
     __syncthreads();
@@ -121,57 +171,54 @@ __global__ __launch_bounds__(1024) void k_pack(XentRows r, const void *labels, i
   }
 }
 
-// The packed rows' x, 16 bytes per lane.
 __global__ __launch_bounds__(256) void k_pack_rows(XentRows r, const u32x4 *x, u32x4 *xc, int m,
                                                    int hv) {
   const int kept = r.head[0];
-  for (int p = static_cast<int>(blockIdx.x); p < kept; p += static_cast<int>(gridDim.x)) {
-    const u32x4 *src = x + static_cast<long long>(r.idx[p]) * hv;
-    u32x4 *dst = xc + static_cast<long long>(p) * 32;
-    for (int k = static_cast<int>(threadIdx.x); k < hv; k += 256)
-      dst[static_cast<long long>(k >> 5) * m * 32 + (k & 31)] = src[k];
-  }
+  for (int p = static_cast<int>(blockIdx.x); p < kept; p += static_cast<int>(gridDim.x))
+    pack_row(x, xc, r.idx[p], p, m, hv);
 }
 
 enum LogitsMode { kStats = 0, kProb = 1, kGrad = 2 };
 
-template <class T, int NT, int MODE>
+template <class T, class Tile, int NT, int MODE>
 __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc, ShardTableN<NT> w,
                                                    int shard, int v0, int vend, int tm, int tn) {
   __shared__ __attribute__((aligned(1024))) unsigned char lds[kTileLds];
   int z, mt, nt;
   tile_at(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), tm, tn, &z, &mt, &nt);
   const int kept = pl.r.head[0];
-  const int m0 = mt * kTile, n0 = v0 + nt * kTile;
+  constexpr int kEdge = Tile::kEdge, MI = Tile::MI, NJ = Tile::NJ;
+  const int m0 = mt * kEdge, n0 = v0 + nt * kEdge;
   if (m0 >= kept) return;
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int wr = wave >> 2, wc = wave & 3, l16 = lane & 15, g = lane >> 4;
 
   PanelRowSource a;
-  const int rows = kept - m0 < kTile ? kept - m0 : kTile;
+  const int rows = kept - m0 < kEdge ? kept - m0 : kEdge;
   a.init(xc + static_cast<long long>(m0) * 32, rows, pl.m * 512ll, 0, pl.hidden, lane);
-  RankRowSource<NT> b;
-  b.init(w, shard, vend, pl.hidden, n0, wc, 4 * wr, lane);
-  f32x4 acc[8][4];
-  tile_product<T>(a, b, (pl.hidden + kStep - 1) / kStep, lds, acc);
+  RankRowSource<NT, Tile::kBLoads> b;
+  b.init(w, shard, vend, pl.hidden, n0, Tile::b_sub(wave), Tile::b_first(wave), lane);
+  f32x4 acc[MI][NJ];
+  Tile::template product<T>(a, b, (pl.hidden + kStep - 1) / kStep, lds, acc);
 
   const float s2 = pl.scale * kLog2e;
-  const int nl = n0 + 64 * wc + 4 * g;  // the lane's column of block 0
+  const int nl = n0 + Tile::kCols * wc + 4 * g;  // the lane's column of block 0
   // d's panel of this tile, from the wave's columns on
   unsigned short *dout = static_cast<unsigned short *>(pl.d) +
-                         static_cast<long long>((n0 - v0) / kPanel) * pl.m * kPanel + (nl - n0);
+                         static_cast<long long>((n0 - v0) / kPanel) * pl.m * kPanel +
+                         (n0 - v0) % kPanel + (nl - n0);
   if constexpr (MODE == kGrad) {
     const float up = d_scale<T>(pl.r, false);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = m0 + 128 * wr + 16 * i + l16;
+    for (int i = 0; i < MI; ++i) {
+      const int row = m0 + Tile::kRows * wr + 16 * i + l16;
       if (row >= kept) continue;
       const float lse2 = pl.r.lse2[row], ca = pl.r.ca[row] * up, cb = pl.r.cb[row] * up;
       const int lab = pl.r.lab[row];
       unsigned short *o = dout + static_cast<long long>(row) * kPanel;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         uint32_t q[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -185,16 +232,16 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
     }
     return;
   } else {
-    // A row's 256 columns lie in 4 waves x 4 lane groups x 16 registers: the
+    // A row's columns of the tile lie in 4 waves x 4 lane groups x 4*NJ registers: the
     // maximum, then the sum of exponentials, each reduced in registers, over
     // the lane groups, and over the waves through LDS.
-    float *red = reinterpret_cast<float *>(lds);  // [4][256] maxima, then [4][256] sums
-    float top[8];
+    float *red = reinterpret_cast<float *>(lds);  // [4][kEdge] maxima, then [4][kEdge] sums
+    float top[MI];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < MI; ++i) {
       float mx = -__builtin_inff();
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int n = nl + 16 * j + t;
@@ -203,26 +250,26 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
         }
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
-      if (g == 0) red[wc * kTile + 128 * wr + 16 * i + l16] = mx;
+      if (g == 0) red[wc * kEdge + Tile::kRows * wr + 16 * i + l16] = mx;
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = 128 * wr + 16 * i + l16;
-      const float mx = fmaxf(fmaxf(red[at], red[kTile + at]),
-                             fmaxf(red[2 * kTile + at], red[3 * kTile + at]));
+    for (int i = 0; i < MI; ++i) {
+      const int at = Tile::kRows * wr + 16 * i + l16;
+      const float mx = fmaxf(fmaxf(red[at], red[kEdge + at]),
+                             fmaxf(red[2 * kEdge + at], red[3 * kEdge + at]));
       top[i] = mx == -__builtin_inff() ? 0.f : mx;  // a row of -inf: every exponential is 0
     }
-    float *sums = red + 4 * kTile;
+    float *sums = red + 4 * kEdge;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = m0 + 128 * wr + 16 * i + l16;
+    for (int i = 0; i < MI; ++i) {
+      const int row = m0 + Tile::kRows * wr + 16 * i + l16;
       const int lab = row < kept ? pl.r.lab[row] - nl : -1;
       float sum = 0.f, zt = 0.f;
       bool mine = false;
       unsigned short *o = dout + static_cast<long long>(row) * kPanel;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         uint32_t q[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -240,17 +287,17 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
       if (mine) pl.r.zt[row] = zt;
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
-      if (g == 0) sums[wc * kTile + 128 * wr + 16 * i + l16] = sum;
+      if (g == 0) sums[wc * kEdge + Tile::kRows * wr + 16 * i + l16] = sum;
       top[i] = sum;
     }
     __syncthreads();
     const int at = static_cast<int>(threadIdx.x);
-    if (at < kTile && m0 + at < kept) {
-      const float mx = fmaxf(fmaxf(red[at], red[kTile + at]),
-                             fmaxf(red[2 * kTile + at], red[3 * kTile + at]));
-      const float sum = (sums[at] + sums[kTile + at]) + (sums[2 * kTile + at] + sums[3 * kTile + at]);
-      const int tiles = (pl.vocab + kTile - 1) / kTile;
-      float *part = pl.part + static_cast<long long>(n0 / kTile) * pl.m + m0 + at;
+    if (at < kEdge && m0 + at < kept) {
+      const float mx = fmaxf(fmaxf(red[at], red[kEdge + at]),
+                             fmaxf(red[2 * kEdge + at], red[3 * kEdge + at]));
+      const float sum = (sums[at] + sums[kEdge + at]) + (sums[2 * kEdge + at] + sums[3 * kEdge + at]);
+      const int tiles = (pl.vocab + kEdge - 1) / kEdge;
+      float *part = pl.part + static_cast<long long>(n0 / kEdge) * pl.m + m0 + at;
       part[0] = mx;
       part[static_cast<long long>(tiles) * pl.m] = sum;
     }
@@ -293,7 +340,7 @@ __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, c
   const rsrc_t xr = resource(x, static_cast<long long>(pl.m) * pl.hidden * 2);
   const int k8 = pl.hidden >> 3;
   const int sub = wave >> 1, q0 = 4 * (wave & 1);
-  RankRowSource<NT, true> b;
+  RankRowSource<NT, 4, true> b;
   int lt = 0, lk = 0;  // tile and step of k of the next loads
   b.init(w, shard, r1, pl.hidden, r0, sub, q0, lane);
   auto load = [&](int s) __attribute__((always_inline)) {
@@ -452,7 +499,7 @@ __global__ __launch_bounds__(256) void k_join(XentPlan pl, const float *grad, fl
                                               float *lse) {
   __shared__ float smax[16][17], ssum[16][17];
   const int kept = pl.r.head[0];
-  const int tiles = (pl.vocab + kTile - 1) / kTile;
+  const int tiles = (pl.vocab + pl.ref - 1) / pl.ref;
   const int c = static_cast<int>(threadIdx.x) & 15, k = static_cast<int>(threadIdx.x) >> 4;
   const int row = static_cast<int>(blockIdx.x) * 16 + c;
   float mx = -__builtin_inff(), sum = 0.f;
@@ -510,17 +557,19 @@ __global__ __launch_bounds__(256) void k_factors(XentPlan pl, const float *lse, 
 template <class T>
 __global__ __launch_bounds__(256) void k_normalise(XentPlan pl) {
   const int kept = pl.r.head[0];
-  const int tile = static_cast<int>(blockIdx.x);
+  const int panel = static_cast<int>(blockIdx.x);
   const float up = d_scale<T>(pl.r, false);
-  const float *part = pl.part + static_cast<long long>(tile) * pl.m;
-  u32x4 *d = static_cast<u32x4 *>(pl.d) + static_cast<long long>(tile) * pl.m * 32;
   const int k = static_cast<int>(threadIdx.x) & 31;
+  const int tile = (panel * kPanel + 8 * k) / pl.ref;
+  if (tile >= (pl.vocab + pl.ref - 1) / pl.ref) return;  // columns no tile wrote or reads
+  const float *part = pl.part + static_cast<long long>(tile) * pl.m;
+  u32x4 *d = static_cast<u32x4 *>(pl.d) + static_cast<long long>(panel) * pl.m * 32;
   for (int row = static_cast<int>(blockIdx.y * 8 + threadIdx.x / 32); row < kept;
        row += static_cast<int>(gridDim.y) * 8) {
     const float mx = part[row];
     const float ref = mx == -__builtin_inff() ? 0.f : mx;
     const float c = exp2_(ref - pl.r.lse2[row]) * (pl.r.ca[row] * up), cb = pl.r.cb[row] * up;
-    const int at = pl.r.lab[row] - tile * kPanel - 8 * k;
+    const int at = pl.r.lab[row] - panel * kPanel - 8 * k;
     u32x4 v = d[static_cast<long long>(row) * 32 + k];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -533,45 +582,120 @@ __global__ __launch_bounds__(256) void k_normalise(XentPlan pl) {
   }
 }
 
-// dX = d W over the piece's columns, split over the vocabulary; fp32 partial
-// sums, joined in a fixed order by k_dx_join.
-template <class T, int NT>
-__global__ __launch_bounds__(512, 2) void k_dx(XentPlan pl, ShardTableN<NT> w, int shard, int v0,
-                                               int vend, int per, int first, int tm, int tn) {
+// Four consecutive columns of dW, in fp32 or 16 bits.
+template <class T>
+__device__ __forceinline__ void dw_store(void *dw, long long at, f32x4 v, int wide,
+                                         int accumulate) {
+  if (wide) {
+    f32x4 *o = reinterpret_cast<f32x4 *>(static_cast<float *>(dw) + at);
+    *o = accumulate ? *o + v : v;
+  } else {
+    uint2 *o = reinterpret_cast<uint2 *>(static_cast<unsigned short *>(dw) + at);
+    if (accumulate) {
+      const uint2 old = *o;
+      v += f32x4{from16<T>(old.x & 0xFFFFu), from16<T>(old.x >> 16), from16<T>(old.y & 0xFFFFu),
+                 from16<T>(old.y >> 16)};
+    }
+    *o = uint2{bits16<T>(v[0]) | bits16<T>(v[1]) << 16, bits16<T>(v[2]) | bits16<T>(v[3]) << 16};
+  }
+}
+
+// The two products of the gradient, in one launch: the first workgroups take
+// dX's tiles (few and long, so they start first), the others dW's, which fill
+// the CUs that dX leaves over.
+struct GradArgs {
+  int v0, vend;       // the piece's columns
+  int xgroups, xm, per, first;  // dX: workgroups, tile rows, steps per split
+  int wm, tn;         // dW: tile rows; both: tile columns
+  void *dw;
+  int wide, accumulate;
+};
+
+template <class T, class Tile, int NT>
+__global__ __launch_bounds__(512, 2) void k_grads(XentPlan pl, ShardTableN<NT> w, int shard,
+                                                  GradArgs ga) {
   __shared__ __attribute__((aligned(1024))) unsigned char lds[kTileLds];
-  int z, mt, nt;
-  tile_at(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), tm, tn, &z, &mt, &nt);
-  const int kept = pl.r.head[0];
-  const int m0 = mt * kTile, n0 = nt * kTile;
-  if (m0 >= kept) return;
+  constexpr int kEdge = Tile::kEdge, MI = Tile::MI, NJ = Tile::NJ;
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-  const int k0 = z * per * kStep;            // the split's first column of the piece
-  int k1 = k0 + per * kStep;
-  if (k1 > vend - v0) k1 = vend - v0;
-  const int steps = k1 > k0 ? (k1 - k0 + kStep - 1) / kStep : 0;
-  PanelRowSource a;
-  const int rows = kept - m0 < kTile ? kept - m0 : kTile;
-  // d's columns past the vocabulary are zero up to a multiple of 256
-  a.init(static_cast<const unsigned char *>(pl.d) + m0 * 512ll, rows, pl.m * 512ll, k0,
-         steps * kStep, lane);
-  RankColumnSource<NT> b;
-  b.init(w, shard, v0 + (k1 > k0 ? k1 : k0), v0 + k0, n0, pl.hidden, lane);
-  f32x4 acc[8][4];
-  tile_product<T>(a, b, steps, lds, acc);
   const int wr = wave >> 2, wc = wave & 3, l16 = lane & 15, g = lane >> 4;
-  float *out = pl.dxp + static_cast<long long>(z) * pl.m * pl.hidden;
+  const int kept = pl.r.head[0];
+  const int v0 = ga.v0, vend = ga.vend;
+  int z, mt, nt;
+  f32x4 acc[MI][NJ];
+  if (static_cast<int>(blockIdx.x) < ga.xgroups) {
+    // dX = d W over a run of the piece's columns; fp32 partial sums, joined in a
+    // fixed order by k_dx_join
+    tile_at(static_cast<int>(blockIdx.x), ga.xgroups, ga.xm, ga.tn, &z, &mt, &nt);
+    const int m0 = mt * kEdge, n0 = nt * kEdge;
+    if (m0 >= kept) return;
+    const int k0 = z * ga.per * kStep;
+    int k1 = k0 + ga.per * kStep;
+    if (k1 > vend - v0) k1 = vend - v0;
+    const int steps = k1 > k0 ? (k1 - k0 + kStep - 1) / kStep : 0;
+    PanelRowSource a;
+    const int rows = kept - m0 < kEdge ? kept - m0 : kEdge;
+    // d's columns past the vocabulary are zero up to a whole tile
+    a.init(static_cast<const unsigned char *>(pl.d) + m0 * 512ll, rows, pl.m * 512ll, k0,
+           steps * kStep, lane);
+    RankColumnSource<NT> b;
+    b.init(w, shard, v0 + (k1 > k0 ? k1 : k0), v0 + k0, n0, pl.hidden, lane);
+    Tile::template product<T>(a, b, steps, lds, acc);
+    float *out = pl.dxp + static_cast<long long>(z) * pl.m * pl.hidden;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = m0 + 128 * wr + 16 * i + l16;
-    if (row >= kept) continue;
-    float *o = out + static_cast<long long>(row) * pl.hidden;
+    for (int i = 0; i < MI; ++i) {
+      const int row = m0 + Tile::kRows * wr + 16 * i + l16;
+      if (row >= kept) continue;
+      float *o = out + static_cast<long long>(row) * pl.hidden;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + 64 * wc + 16 * j + 4 * g;
+      for (int j = 0; j < NJ; ++j) {
+        const int n = n0 + Tile::kCols * wc + 16 * j + 4 * g;
+        if (n >= pl.hidden) continue;
+        f32x4 *at = reinterpret_cast<f32x4 *>(o + n);
+        *at = ga.first ? acc[i][j] : *at + acc[i][j];
+      }
+    }
+    return;
+  }
+  // dW rows of the piece = d^T X over the packed rows, or over a run of them
+  // (fp32 partial sums, joined by k_dw_join)
+  tile_at(static_cast<int>(blockIdx.x) - ga.xgroups, static_cast<int>(gridDim.x) - ga.xgroups,
+          ga.wm, ga.tn, &z, &mt, &nt);
+  const int c0 = mt * kEdge, n0 = nt * kEdge;  // column of the piece
+  int k0 = 0, k1 = kept;
+  const bool split = pl.split_dw > 1;
+  if (split) {
+    const int per = ((kept + kStep - 1) / kStep + pl.split_dw - 1) / pl.split_dw * kStep;
+    k0 = z * per < kept ? z * per : kept;
+    k1 = k0 + per < kept ? k0 + per : kept;
+  }
+  // a tile of rows past the vocabulary has no columns in d: nothing to read
+  const int kdim = v0 + c0 < vend ? k1 - k0 : 0;
+  PanelColumnSource a, b;
+  a.init(static_cast<const unsigned char *>(pl.d) +
+             (static_cast<long long>(kdim ? c0 / kPanel : 0) * pl.m + k0) * 512,
+         c0 % kPanel, kdim, lane);
+  b.init(static_cast<const unsigned char *>(pl.xc) +
+             (static_cast<long long>(n0 / kPanel) * pl.m + k0) * 512,
+         n0 % kPanel, kdim, lane);
+  Tile::template product<T>(a, b, (kdim + kStep - 1) / kStep, lds, acc);
+  const float down = split ? 1.f : d_scale<T>(pl.r, true);
+  void *out = split ? static_cast<void *>(pl.dwp +
+                                          static_cast<long long>(z) * pl.dw_rows * pl.hidden)
+                    : ga.dw;
+  const int wide = split ? 1 : ga.wide, accumulate = split ? 0 : ga.accumulate;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int row = v0 + c0 + Tile::kRows * wr + 16 * i + l16;
+    if (row >= pl.rows) continue;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int n = n0 + Tile::kCols * wc + 16 * j + 4 * g;
       if (n >= pl.hidden) continue;
-      f32x4 *at = reinterpret_cast<f32x4 *>(o + n);
-      *at = first ? acc[i][j] : *at + acc[i][j];
+      // rows past the vocabulary get no gradient, whatever x holds
+      const f32x4 v = row < vend ? acc[i][j] * down : f32x4{0.f, 0.f, 0.f, 0.f};
+      dw_store<T>(out, static_cast<long long>(split ? row - v0 : row) * pl.hidden + n, v, wide,
+                  accumulate);
     }
   }
 }
@@ -600,75 +724,8 @@ __global__ __launch_bounds__(256) void k_dx_join(XentPlan pl, uint2 *dx) {
   }
 }
 
-// Four consecutive columns of dW.
-template <class T, bool WIDE>
-__device__ __forceinline__ void dw_store(void *dw, long long at, f32x4 v, int accumulate) {
-  if constexpr (WIDE) {
-    f32x4 *o = reinterpret_cast<f32x4 *>(static_cast<float *>(dw) + at);
-    *o = accumulate ? *o + v : v;
-  } else {
-    uint2 *o = reinterpret_cast<uint2 *>(static_cast<unsigned short *>(dw) + at);
-    if (accumulate) {
-      const uint2 old = *o;
-      v += f32x4{from16<T>(old.x & 0xFFFFu), from16<T>(old.x >> 16), from16<T>(old.y & 0xFFFFu),
-                 from16<T>(old.y >> 16)};
-    }
-    *o = uint2{bits16<T>(v[0]) | bits16<T>(v[1]) << 16, bits16<T>(v[2]) | bits16<T>(v[3]) << 16};
-  }
-}
-
-// dW rows v0 .. of the piece = d^T X over the packed rows. SPLIT: fp32 partial
-// sums of a run of rows, joined by k_dw_join.
-template <class T, bool WIDE, bool SPLIT>
-__global__ __launch_bounds__(512, 2) void k_dw(XentPlan pl, const void *xc, int v0, int vend,
-                                               void *dw, int accumulate, int tm, int tn) {
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[kTileLds];
-  int z, mt, nt;
-  tile_at(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), tm, tn, &z, &mt, &nt);
-  const int lane = static_cast<int>(threadIdx.x) & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-  const int m0 = v0 + mt * kTile, n0 = nt * kTile;  // m0: matrix row
-  const int kept = pl.r.head[0];
-  int k0 = 0, k1 = kept;
-  if constexpr (SPLIT) {
-    const int per = ((kept + kStep - 1) / kStep + pl.split_dw - 1) / pl.split_dw * kStep;
-    k0 = z * per < kept ? z * per : kept;
-    k1 = k0 + per < kept ? k0 + per : kept;
-  }
-  // a tile of rows past the vocabulary has no columns in d: nothing to read
-  const int kdim = m0 < vend ? k1 - k0 : 0;
-  PanelColumnSource a, b;
-  a.init(static_cast<const unsigned char *>(pl.d) +
-             (static_cast<long long>(mt) * pl.m + k0) * 512,
-         kdim, lane);
-  b.init(static_cast<const unsigned char *>(xc) + (static_cast<long long>(nt) * pl.m + k0) * 512,
-         kdim, lane);
-  f32x4 acc[8][4];
-  tile_product<T>(a, b, (kdim + kStep - 1) / kStep, lds, acc);
-  const int wr = wave >> 2, wc = wave & 3, l16 = lane & 15, g = lane >> 4;
-  const float down = SPLIT ? 1.f : d_scale<T>(pl.r, true);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = m0 + 128 * wr + 16 * i + l16;
-    if (row >= pl.rows) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + 64 * wc + 16 * j + 4 * g;
-      if (n >= pl.hidden) continue;
-      // rows past the vocabulary get no gradient, whatever x holds
-      const f32x4 v = row < vend ? acc[i][j] * down : f32x4{0.f, 0.f, 0.f, 0.f};
-      if constexpr (SPLIT)
-        *reinterpret_cast<f32x4 *>(pl.dwp +
-                                   (static_cast<long long>(z) * pl.dw_rows + (row - v0)) * pl.hidden +
-                                   n) = v;
-      else
-        dw_store<T, WIDE>(dw, static_cast<long long>(row) * pl.hidden + n, v, accumulate);
-    }
-  }
-}
-
-template <class T, bool WIDE>
-__global__ __launch_bounds__(256) void k_dw_join(XentPlan pl, int v0, int rows, void *dw,
+template <class T>
+__global__ __launch_bounds__(256) void k_dw_join(XentPlan pl, int v0, int rows, void *dw, int wide,
                                                  int accumulate) {
   const float down = d_scale<T>(pl.r, true);
   const int hq = pl.hidden >> 2;
@@ -679,7 +736,7 @@ __global__ __launch_bounds__(256) void k_dw_join(XentPlan pl, int v0, int rows, 
     const f32x4 *src = reinterpret_cast<const f32x4 *>(pl.dwp) + k;
     f32x4 v = src[0];
     for (int z = 1; z < pl.split_dw; ++z) v += src[z * plane];
-    dw_store<T, WIDE>(dw, static_cast<long long>(v0) * pl.hidden + 4 * k, v * down, accumulate);
+    dw_store<T>(dw, static_cast<long long>(v0) * pl.hidden + 4 * k, v * down, wide, accumulate);
   }
 }
 
@@ -698,6 +755,11 @@ void by_type(bool half, F f) {
   else f(TypeBf16{});
 }
 template <class F>
+void by_tile(bool small, F f) {
+  if (small) f(SmallTile{});
+  else f(BigTile{});
+}
+template <class F>
 void by_table(int tp, F f) {
   if (tp == 1) f(std::integral_constant<int, 1>{});
   else f(std::integral_constant<int, HG_MAX_TP>{});
@@ -707,6 +769,12 @@ void by_table(int tp, F f) {
 
 hipError_t launch_xent_pack(const XentPlan &p, const void *x, const void *labels, float *loss,
                             float *lse, hipStream_t s) {
+  if (p.m <= kPackRows) {
+    hipLaunchKernelGGL(k_pack_few, dim3(p.m), dim3(256), 0, s, p.r, labels, p.label_bytes, p.m,
+                       p.vocab, p.ignore, static_cast<const u32x4 *>(x),
+                       static_cast<u32x4 *>(p.xc), p.hidden >> 3, loss, lse);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(k_pack, dim3(1), dim3(1024), 0, s, p.r, labels, p.label_bytes, p.m, p.vocab,
                      p.ignore, loss, lse);
   hipError_t e = hipGetLastError();
@@ -718,20 +786,24 @@ hipError_t launch_xent_pack(const XentPlan &p, const void *x, const void *labels
 
 hipError_t launch_xent_logits(const XentPlan &p, const VocabMatrix &w, int mode, int v0, int cols,
                               hipStream_t s) {
-  const int tm = ceil_div(p.m, kTile), tn = ceil_div(cols, kTile);
+  const int edge = p.small_logits ? SmallTile::kEdge : BigTile::kEdge;
+  const int tm = ceil_div(p.m, edge), tn = ceil_div(cols, edge);
   const int vend = v0 + cols;
   by_type(p.half, [&](auto type) {
     by_table(w.tp, [&](auto nt) {
-      using T = decltype(type);
-      constexpr int NT = decltype(nt)::value;
-      auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(tm * tn), dim3(512), 0, s, p,
-                           static_cast<const u32x4 *>(p.xc), small_table<NT>(w.t), w.shard, v0,
-                           vend, tm, tn);
-      };
-      if (mode == kStats) go(k_logits<T, NT, kStats>);
-      else if (mode == kProb) go(k_logits<T, NT, kProb>);
-      else go(k_logits<T, NT, kGrad>);
+      by_tile(p.small_logits, [&](auto tile) {
+        using T = decltype(type);
+        using Tile = decltype(tile);
+        constexpr int NT = decltype(nt)::value;
+        auto go = [&](auto kernel) {
+          hipLaunchKernelGGL(kernel, dim3(tm * tn), dim3(512), 0, s, p,
+                             static_cast<const u32x4 *>(p.xc), small_table<NT>(w.t), w.shard, v0,
+                             vend, tm, tn);
+        };
+        if (mode == kStats) go(k_logits<T, Tile, NT, kStats>);
+        else if (mode == kProb) go(k_logits<T, Tile, NT, kProb>);
+        else go(k_logits<T, Tile, NT, kGrad>);
+      });
     });
   });
   return hipGetLastError();
@@ -782,20 +854,6 @@ hipError_t launch_xent_normalise(const XentPlan &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_xent_dx(const XentPlan &p, const VocabMatrix &w, int v0, int cols, bool first,
-                          hipStream_t s) {
-  const int tm = ceil_div(p.m, kTile), tn = ceil_div(p.hidden, kTile);
-  const int per = ceil_div(ceil_div(cols, kStep), p.split_dx);
-  by_type(p.half, [&](auto type) {
-    by_table(w.tp, [&](auto nt) {
-      constexpr int NT = decltype(nt)::value;
-      hipLaunchKernelGGL((k_dx<decltype(type), NT>), dim3(tm * tn * p.split_dx), dim3(512), 0, s, p,
-                         small_table<NT>(w.t), w.shard, v0, v0 + cols, per, first ? 1 : 0, tm, tn);
-    });
-  });
-  return hipGetLastError();
-}
-
 hipError_t launch_xent_dx_join(const XentPlan &p, void *dx, hipStream_t s) {
   const dim3 grid(ceil_div(p.hidden >> 2, 1024), p.m < 16384 ? p.m : 16384);
   by_type(p.half, [&](auto type) {
@@ -805,34 +863,40 @@ hipError_t launch_xent_dx_join(const XentPlan &p, void *dx, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_xent_dw(const XentPlan &p, int v0, int cols, void *dw, bool wide, bool accumulate,
-                          hipStream_t s) {
+hipError_t launch_xent_grads(const XentPlan &p, const VocabMatrix &w, int v0, int cols, bool first,
+                             void *dw, bool wide, bool accumulate, hipStream_t s) {
   // the last piece also covers the matrix's rows past the vocabulary
   const int vend = v0 + cols;
   const int rows = vend == p.vocab ? p.rows - v0 : cols;
-  const int tm = ceil_div(rows, kTile), tn = ceil_div(p.hidden, kTile);
-  const bool split = p.split_dw > 1;
-  const int acc = accumulate ? 1 : 0;
+  const int edge = p.small_grads ? SmallTile::kEdge : BigTile::kEdge;
+  GradArgs a;
+  a.v0 = v0;
+  a.vend = vend;
+  a.tn = ceil_div(p.hidden, edge);
+  a.xm = ceil_div(p.m, edge);
+  a.xgroups = a.xm * a.tn * p.split_dx;
+  a.per = ceil_div(ceil_div(cols, kStep), p.split_dx);
+  a.first = first ? 1 : 0;
+  a.wm = ceil_div(rows, edge);
+  a.dw = dw;
+  a.wide = wide ? 1 : 0;
+  a.accumulate = accumulate ? 1 : 0;
+  const dim3 grid(a.xgroups + a.wm * a.tn * p.split_dw);
   by_type(p.half, [&](auto type) {
     using T = decltype(type);
-    const dim3 grid(tm * tn * p.split_dw), block(512);
-    if (split)
-      hipLaunchKernelGGL((k_dw<T, false, true>), grid, block, 0, s, p, p.xc, v0, vend, dw, acc, tm,
-                         tn);
-    else if (wide)
-      hipLaunchKernelGGL((k_dw<T, true, false>), grid, block, 0, s, p, p.xc, v0, vend, dw, acc, tm,
-                         tn);
-    else
-      hipLaunchKernelGGL((k_dw<T, false, false>), grid, block, 0, s, p, p.xc, v0, vend, dw, acc, tm,
-                         tn);
-    if (split) {
+    by_table(w.tp, [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      by_tile(p.small_grads, [&](auto tile) {
+        hipLaunchKernelGGL((k_grads<T, decltype(tile), NT>), grid, dim3(512), 0, s, p,
+                           small_table<NT>(w.t), w.shard, a);
+      });
+    });
+    if (p.split_dw > 1) {
       const long long quads = static_cast<long long>(rows) * (p.hidden >> 2);
       const long long want = (quads + 255) / 256;
       const dim3 g2(static_cast<unsigned>(want < 4096 ? want : 4096));
-      if (wide)
-        hipLaunchKernelGGL((k_dw_join<T, true>), g2, dim3(256), 0, s, p, v0, rows, dw, acc);
-      else
-        hipLaunchKernelGGL((k_dw_join<T, false>), g2, dim3(256), 0, s, p, v0, rows, dw, acc);
+      hipLaunchKernelGGL((k_dw_join<T>), g2, dim3(256), 0, s, p, v0, rows, dw, a.wide,
+                         a.accumulate);
     }
   });
   return hipGetLastError();

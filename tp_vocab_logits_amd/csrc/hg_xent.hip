@@ -51,8 +51,8 @@ struct Prob {
   static constexpr int M = T::kHalf ? 11 : 10, E = 16 - M, S = 23 - M;
   static constexpr int kLow = (127 - ((1 << E) - 1)) << M;
   static __device__ __forceinline__ uint32_t put(float p) {
-    const int b = (__builtin_bit_cast(int, p) + (1 << (S - 1))) >> S;
-    return static_cast<uint32_t>(b > kLow ? b - kLow : 0);
+    const uint32_t b = (__builtin_bit_cast(uint32_t, p) + (1u << (S - 1))) >> S;
+    return __builtin_elementwise_sub_sat(b, static_cast<uint32_t>(kLow));
   }
   static __device__ __forceinline__ float get(uint32_t c) {
     return c ? __builtin_bit_cast(float, static_cast<int>(c + kLow) << S) : 0.f;
@@ -217,18 +217,29 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
       const float lse2 = pl.r.lse2[row], ca = pl.r.ca[row] * up, cb = pl.r.cb[row] * up;
       const int lab = pl.r.lab[row];
       unsigned short *o = dout + static_cast<long long>(row) * kPanel;
+      // few of a tile's rows have their label in it, and few tiles columns past
+      // the vocabulary
+      auto emit = [&](auto special) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        uint32_t q[4];
+        for (int j = 0; j < NJ; ++j) {
+          uint32_t q[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int n = nl + 16 * j + t;
-          float v = exp2_(acc[i][j][t] * s2 - lse2) * ca;
-          v = n == lab ? v - cb : v;
-          q[t] = n < vend ? bits16<T>(v) : 0u;
+          for (int t = 0; t < 4; ++t) {
+            float v = exp2_(fmaf(acc[i][j][t], s2, -lse2)) * ca;
+            if constexpr (decltype(special)::value) {
+              const int n = nl + 16 * j + t;
+              v = n == lab ? v - cb : v;
+              v = n < vend ? v : 0.f;
+            }
+            q[t] = bits16<T>(v);
+          }
+          *reinterpret_cast<uint2 *>(o + 16 * j) = uint2{q[0] | q[1] << 16, q[2] | q[3] << 16};
         }
-        *reinterpret_cast<uint2 *>(o + 16 * j) = uint2{q[0] | q[1] << 16, q[2] | q[3] << 16};
-      }
+      };
+      if (n0 + kEdge > vend || __any(lab >= nl && lab < nl + 16 * NJ))
+        emit(std::integral_constant<bool, true>{});
+      else
+        emit(std::integral_constant<bool, false>{});
     }
     return;
   } else {
@@ -237,21 +248,37 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
     // the lane groups, and over the waves through LDS.
     float *red = reinterpret_cast<float *>(lds);  // [4][kEdge] maxima, then [4][kEdge] sums
     float top[MI];
+    // Columns past the vocabulary, in its last tile alone, become -inf logits.
+    const float masked = s2 < 0.f ? __builtin_inff() : -__builtin_inff();
+    const bool last = n0 + kEdge > vend;
+    if (last) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      float mx = -__builtin_inff();
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int n = nl + 16 * j + t;
-          acc[i][j][t] = n < vend ? acc[i][j][t] * s2 : -__builtin_inff();
-          mx = fmaxf(mx, acc[i][j][t]);
-        }
-      mx = fmaxf(mx, __shfl_xor(mx, 16));
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
-      if (g == 0) red[wc * kEdge + Tile::kRows * wr + 16 * i + l16] = mx;
+          for (int t = 0; t < 4; ++t)
+            if (nl + 16 * j + t >= vend) acc[i][j][t] = masked;
     }
+    // The largest logit is the largest product, or the smallest if the scale
+    // is negative.
+    auto row_top = [&](auto pick) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        float mx = acc[i][0][0];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) mx = pick(mx, acc[i][j][t]);
+        mx = pick(mx, __shfl_xor(mx, 16));
+        mx = pick(mx, __shfl_xor(mx, 32));
+        if (g == 0) red[wc * kEdge + Tile::kRows * wr + 16 * i + l16] = mx * s2;
+      }
+    };
+    if (s2 < 0.f)
+      row_top([](float a, float b) __attribute__((always_inline)) { return fminf(a, b); });
+    else
+      row_top([](float a, float b) __attribute__((always_inline)) { return fmaxf(a, b); });
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -265,30 +292,32 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
     for (int i = 0; i < MI; ++i) {
       const int row = m0 + Tile::kRows * wr + 16 * i + l16;
       const int lab = row < kept ? pl.r.lab[row] - nl : -1;
-      float sum = 0.f, zt = 0.f;
-      bool mine = false;
+      // few of a tile's rows have their label in it
+      if (__any(lab >= 0 && lab < 16 * NJ)) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            if (lab == 16 * j + t) pl.r.zt[row] = acc[i][j][t] * s2;
+      }
+      float sum = 0.f;
       unsigned short *o = dout + static_cast<long long>(row) * kPanel;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         uint32_t q[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const float e = exp2_(acc[i][j][t] - top[i]);
+          float e = exp2_(fmaf(acc[i][j][t], s2, -top[i]));
+          if (last && nl + 16 * j + t >= vend) e = 0.f;  // (at scale 0 too)
           sum += e;
-          if (lab == 16 * j + t) {
-            zt = acc[i][j][t];
-            mine = true;
-          }
           if (MODE == kProb) q[t] = Prob<T>::put(e);
         }
         if (MODE == kProb && row < kept)
           *reinterpret_cast<uint2 *>(o + 16 * j) = uint2{q[0] | q[1] << 16, q[2] | q[3] << 16};
       }
-      if (mine) pl.r.zt[row] = zt;
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
       if (g == 0) sums[wc * kEdge + Tile::kRows * wr + 16 * i + l16] = sum;
-      top[i] = sum;
     }
     __syncthreads();
     const int at = static_cast<int>(threadIdx.x);

@@ -612,7 +612,7 @@ def check_embed_grad(tokens, dy, tp, shard, scale, dtype, wide=False, old=None):
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("tp,shard,hidden,n", [(1, 1, 8, 1), (2, 33, 16, 7), (1, 513, 72, 64), (3, 5, 2056, 400),
                                                (8, 96, 264, 4096), (8, 96, 264, 4097), (64, 300, 40, 9000),
-                                               (5, 70000, 8, 5000)])
+                                               (5, 70000, 8, 5000), (64, 5000, 264, 9001)])
 def test_embed_grad(tp, shard, hidden, n, dtype):
     note(f"embed_grad {tp=} {shard=} {hidden=} {n=} {dtype}")
     rows = tp * shard

@@ -138,17 +138,18 @@ _FAST = None
 
 def fast():
     """The ``_hgcall`` extension, bound to the loaded library: ``gather``,
-    ``push``, ``collect`` and ``stock`` taking plain integers (handle, sizes,
-    host-array address, rows, device address, stream) in the C argument order
-    and returning the status code -- the same calls as through ctypes, with
-    less per-call conversion."""
+    ``push``, ``collect``, ``stock``, ``embed`` and ``embed_grad`` taking plain
+    integers (handle, sizes, host-array address, rows, device address, stream)
+    in the C argument order and returning the status code -- the same calls as
+    through ctypes, with less per-call conversion."""
     global _FAST
     if _FAST is None:
         from . import _hgcall
 
         handle = lib()
         _hgcall.bind(*[ctypes.cast(getattr(handle, n), ctypes.c_void_p).value
-                       for n in ("hg_gather", "hg_push", "hg_collect", "hg_stock_gather")])
+                       for n in ("hg_gather", "hg_push", "hg_collect", "hg_stock_gather", "hg_embed",
+                                  "hg_embed_grad")])
         _FAST = _hgcall
     return _FAST
 

@@ -1,14 +1,16 @@
 /*
  * _hgcall: fast-call Python wrappers of the per-call entry points of
- * libhg.so (hg_gather, hg_push, hg_collect, hg_stock_gather), for loops where
- * the ctypes conversion of the arguments (about 0.5 us a call) is a sizeable
- * part of a 3 us M=1 gather.
+ * libhg.so (hg_gather, hg_push, hg_collect, hg_stock_gather, hg_embed,
+ * hg_embed_grad), for loops where the ctypes conversion of the arguments
+ * (about 0.5 us a call, 2 us with a dozen of them) is a sizeable part of a
+ * call of a few microseconds.
  * Argument marshalling only: every argument is an integer (a handle, a
- * host-array address, a row count, a device address, a stream), passed on
- * unchanged; the return value is the library's status code.
+ * host-array address, a row count, a device address, a stream), a float or a
+ * tuple of device addresses, passed on unchanged; the return value is the
+ * library's status code.
  *
  * The module does not link against libhg.so: bind() receives the addresses of
- * the four entry points from the already loaded library (see _lib.fast()).
+ * the six entry points from the already loaded library (see _lib.fast()).
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -19,10 +21,21 @@ typedef int (*collect_fn)(void *h, int m, void *out, void *stream);
 typedef int (*stock_fn)(int tp, int shard, const void *const *shards, int m, void *out,
                         int vocab, void *stream);
 
+typedef int (*embed_fn)(int tp, int shard, int hidden, int dtype, const void *const *w,
+                        const void *tokens, int token_bytes, int n, float scale, void *out,
+                        void *stream);
+typedef int (*embed_grad_fn)(int tp, int shard, int hidden, int dtype, const void *tokens,
+                             int token_bytes, int n, const void *dy, float scale, void *dw,
+                             int dw_wide, int accumulate, void *ws, size_t ws_bytes, void *stream);
+
 static gather_fn g_gather;
 static push_fn g_push;
 static collect_fn g_collect;
 static stock_fn g_stock;
+static embed_fn g_embed;
+static embed_grad_fn g_embed_grad;
+
+#define MAX_BLOCKS 64 /* HG_MAX_TP */
 
 static int as_ptr(PyObject *o, void **p) {
   *p = PyLong_AsVoidPtr(o);
@@ -52,25 +65,34 @@ static int check_bound(void *fn, Py_ssize_t nargs, Py_ssize_t want) {
   return 1;
 }
 
-/* bind(gather_addr, push_addr, collect_addr, stock_addr) */
+static int as_float(PyObject *o, float *v) {
+  const double x = PyFloat_AsDouble(o);
+  if (x == -1.0 && PyErr_Occurred()) return 0;
+  *v = (float)x;
+  return 1;
+}
+
+/* bind(gather, push, collect, stock, embed, embed_grad): their addresses */
 static PyObject *py_bind(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
-  void *a, *b, *c, *d;
+  void *fn[6];
   (void)self;
-  if (nargs != 4) {
-    PyErr_SetString(PyExc_TypeError, "bind expects four function addresses");
+  if (nargs != 6) {
+    PyErr_SetString(PyExc_TypeError, "bind expects six function addresses");
     return NULL;
   }
-  if (!as_ptr(args[0], &a) || !as_ptr(args[1], &b) || !as_ptr(args[2], &c) ||
-      !as_ptr(args[3], &d))
-    return NULL;
-  if (!a || !b || !c || !d) {
-    PyErr_SetString(PyExc_ValueError, "bind: null function address");
-    return NULL;
+  for (int k = 0; k < 6; ++k) {
+    if (!as_ptr(args[k], &fn[k])) return NULL;
+    if (!fn[k]) {
+      PyErr_SetString(PyExc_ValueError, "bind: null function address");
+      return NULL;
+    }
   }
-  g_gather = (gather_fn)a;
-  g_push = (push_fn)b;
-  g_collect = (collect_fn)c;
-  g_stock = (stock_fn)d;
+  g_gather = (gather_fn)fn[0];
+  g_push = (push_fn)fn[1];
+  g_collect = (collect_fn)fn[2];
+  g_stock = (stock_fn)fn[3];
+  g_embed = (embed_fn)fn[4];
+  g_embed_grad = (embed_grad_fn)fn[5];
   Py_RETURN_NONE;
 }
 
@@ -123,9 +145,58 @@ static PyObject *py_stock(PyObject *self, PyObject *const *args, Py_ssize_t narg
   return PyLong_FromLong(g_stock(tp, shard, (const void *const *)shards, m, out, vocab, stream));
 }
 
+/* embed(tp, shard, hidden, dtype, blocks, tokens, token_bytes, n, scale, out, stream) -> status;
+ * blocks: a tuple of tp device addresses */
+static PyObject *py_embed(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  const void *w[MAX_BLOCKS];
+  void *tokens, *out, *stream;
+  int tp, shard, hidden, dtype, bytes, n;
+  float scale;
+  (void)self;
+  if (!check_bound((void *)g_embed, nargs, 11)) return NULL;
+  if (!as_int(args[0], &tp) || !as_int(args[1], &shard) || !as_int(args[2], &hidden) ||
+      !as_int(args[3], &dtype) || !as_ptr(args[5], &tokens) || !as_int(args[6], &bytes) ||
+      !as_int(args[7], &n) || !as_float(args[8], &scale) || !as_ptr(args[9], &out) ||
+      !as_ptr(args[10], &stream))
+    return NULL;
+  if (!PyTuple_Check(args[4]) || tp < 0 || tp > MAX_BLOCKS || PyTuple_GET_SIZE(args[4]) != tp) {
+    PyErr_SetString(PyExc_TypeError, "blocks must be a tuple of tp addresses");
+    return NULL;
+  }
+  for (int r = 0; r < tp; ++r) {
+    void *p;
+    if (!as_ptr(PyTuple_GET_ITEM(args[4], r), &p)) return NULL;
+    w[r] = p;
+  }
+  return PyLong_FromLong(
+      g_embed(tp, shard, hidden, dtype, w, tokens, bytes, n, scale, out, stream));
+}
+
+/* embed_grad(tp, shard, hidden, dtype, tokens, token_bytes, n, dy, scale, dw, dw_wide, accumulate,
+ * ws, ws_bytes, stream) -> status */
+static PyObject *py_embed_grad(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  void *tokens, *dy, *dw, *ws, *stream;
+  int tp, shard, hidden, dtype, bytes, n, wide, accumulate;
+  float scale;
+  size_t ws_bytes;
+  (void)self;
+  if (!check_bound((void *)g_embed_grad, nargs, 15)) return NULL;
+  if (!as_int(args[0], &tp) || !as_int(args[1], &shard) || !as_int(args[2], &hidden) ||
+      !as_int(args[3], &dtype) || !as_ptr(args[4], &tokens) || !as_int(args[5], &bytes) ||
+      !as_int(args[6], &n) || !as_ptr(args[7], &dy) || !as_float(args[8], &scale) ||
+      !as_ptr(args[9], &dw) || !as_int(args[10], &wide) || !as_int(args[11], &accumulate) ||
+      !as_ptr(args[12], &ws))
+    return NULL;
+  ws_bytes = PyLong_AsSize_t(args[13]);
+  if (ws_bytes == (size_t)-1 && PyErr_Occurred()) return NULL;
+  if (!as_ptr(args[14], &stream)) return NULL;
+  return PyLong_FromLong(g_embed_grad(tp, shard, hidden, dtype, tokens, bytes, n, dy, scale, dw,
+                                      wide, accumulate, ws, ws_bytes, stream));
+}
+
 static PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)(void))py_bind, METH_FASTCALL,
-     "bind(gather, push, collect, stock)"},
+     "bind(gather, push, collect, stock, embed, embed_grad)"},
     {"gather", (PyCFunction)(void (*)(void))py_gather, METH_FASTCALL,
      "gather(handle, shards_addr, m, out_addr, stream) -> status"},
     {"push", (PyCFunction)(void (*)(void))py_push, METH_FASTCALL,
@@ -134,6 +205,11 @@ static PyMethodDef methods[] = {
      "collect(handle, m, out_addr, stream) -> status"},
     {"stock", (PyCFunction)(void (*)(void))py_stock, METH_FASTCALL,
      "stock(tp, shard, shards_addr, m, out_addr, vocab, stream) -> status"},
+    {"embed", (PyCFunction)(void (*)(void))py_embed, METH_FASTCALL,
+     "embed(tp, shard, hidden, dtype, blocks, tokens, token_bytes, n, scale, out, stream) -> status"},
+    {"embed_grad", (PyCFunction)(void (*)(void))py_embed_grad, METH_FASTCALL,
+     "embed_grad(tp, shard, hidden, dtype, tokens, token_bytes, n, dy, scale, dw, dw_wide, "
+     "accumulate, ws, ws_bytes, stream) -> status"},
     {NULL, NULL, 0, NULL},
 };
 

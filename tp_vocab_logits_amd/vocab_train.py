@@ -42,18 +42,21 @@ def _table(tp: int):
     return ctypes.c_void_p * tp
 
 
-def _call(name: str, device: torch.device, *args) -> None:
-    """One library call on the device's current stream, appended to `args`."""
+def _call(fn, name: str, device: torch.device, *args) -> None:
+    """One library call on the device's current stream, appended to ``args``."""
     index = device.index
     if torch.cuda.current_device() == index:
-        check(getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index)), name)
-        return
-    with torch.cuda.device(device):
-        check(getattr(lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index)), name)
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if code:
+        check(code, name)
 
 
-def _matrix(w, tp: int, shard: int, dtypes) -> tuple[list[int], int, torch.dtype, torch.device]:
-    """Block pointers, hidden size, type and device of the vocabulary matrix."""
+def _matrix(w, tp: int, shard: int, dtypes) -> tuple[tuple[int, ...], int, torch.dtype, torch.device]:
+    """Block pointers (one for a tensor), hidden size, type and device of the
+    vocabulary matrix."""
     tp, shard = int(tp), int(shard)
     if tp < 1 or shard < 1:
         raise ValueError(f"tp and shard must be positive, got {tp} and {shard}")
@@ -62,9 +65,8 @@ def _matrix(w, tp: int, shard: int, dtypes) -> tuple[list[int], int, torch.dtype
             raise ValueError(f"the matrix must be a contiguous [{tp * shard}, H] tensor, got {tuple(w.shape)}")
         if w.dim() == 3 and tuple(w.shape[:2]) != (tp, shard):
             raise ValueError(f"the matrix must be [{tp}, {shard}, H], got {tuple(w.shape)}")
-        blocks, hidden = [w], int(w.shape[-1])
-        step = shard * hidden * w.element_size()
-        ptrs = [w.data_ptr() + r * step for r in range(tp)]
+        blocks, hidden = (w,), int(w.shape[-1])
+        ptrs = (w.data_ptr(),)
     else:
         blocks = list(w)
         if len(blocks) != tp:
@@ -75,7 +77,7 @@ def _matrix(w, tp: int, shard: int, dtypes) -> tuple[list[int], int, torch.dtype
                 raise ValueError(f"every block must be a contiguous [{shard}, {hidden}] tensor, got {tuple(t.shape)}")
             if t.dtype != blocks[0].dtype or t.device != blocks[0].device:
                 raise ValueError("the blocks must share dtype and device")
-        ptrs = [t.data_ptr() for t in blocks]
+        ptrs = tuple(t.data_ptr() for t in blocks)
     if blocks[0].dtype not in dtypes:
         raise ValueError(f"the matrix must be one of {[str(d) for d in dtypes]}, got {blocks[0].dtype}")
     return ptrs, hidden, blocks[0].dtype, blocks[0].device
@@ -127,6 +129,9 @@ class _Head:
         self.labels = _given(labels, "labels", (m,), _INTS, self.device)
         _on_gpu(self.device)
         self.m, self.hidden, self.rows = m, hidden, int(tp) * int(shard)
+        if len(self.ptrs) < tp:
+            step = int(shard) * hidden * 2
+            self.ptrs = tuple(self.ptrs[0] + r * step for r in range(int(tp)))
         vocab = self.rows if vocab is None else int(vocab)
         if not 1 <= vocab <= self.rows:
             raise ValueError(f"vocab must lie in 1..{self.rows}, got {vocab}")
@@ -151,7 +156,7 @@ class _Head:
         return dx, _gradient_buffer(dw, self.rows, self.hidden, self.dtype, self.device, accumulate)
 
     def call(self, name, *args):
-        _call(name, self.device, self.shape, self.x.data_ptr(), _table(len(self.ptrs))(*self.ptrs),
+        _call(getattr(lib(), name), name, self.device, self.shape, self.x.data_ptr(), _table(len(self.ptrs))(*self.ptrs),
               self.labels.data_ptr(), *args)
 
 
@@ -269,8 +274,9 @@ def embed(tokens: torch.Tensor, w, tp: int, shard: int, scale: float = 1.0,
         out = torch.empty(shape, dtype=dtype, device=device)
     else:
         _given(out, "out", shape, (dtype,), device)
-    _call("hg_embed", device, tp, shard, hidden, _DTYPES[dtype], _table(tp)(*ptrs), tokens.data_ptr(),
-          tokens.element_size(), tokens.numel(), scale, out.data_ptr())
+    rows = int(tp) * int(shard)  # (blocks that make one tensor are one block)
+    _call(_lib.fast().embed, "hg_embed", device, len(ptrs), rows // len(ptrs), hidden, _DTYPES[dtype], ptrs,
+          tokens.data_ptr(), tokens.element_size(), tokens.numel(), scale, out.data_ptr())
     return out
 
 
@@ -296,7 +302,7 @@ def embed_grad(tokens: torch.Tensor, dy: torch.Tensor, tp: int, shard: int, scal
     tp, shard = int(tp), int(shard)
     dw = _gradient_buffer(dw, tp * shard, hidden, dy.dtype, device, accumulate)
     ws = _workspace(_embed_bytes(tp, shard, hidden, tokens.numel()), device)
-    _call("hg_embed_grad", device, tp, shard, hidden, _DTYPES[dy.dtype], tokens.data_ptr(), tokens.element_size(),
+    _call(_lib.fast().embed_grad, "hg_embed_grad", device, tp, shard, hidden, _DTYPES[dy.dtype], tokens.data_ptr(), tokens.element_size(),
           tokens.numel(), dy.data_ptr(), scale, dw.data_ptr(), int(dw.dtype != dy.dtype), int(accumulate),
           ws.data_ptr(), ws.numel())
     return dw

@@ -472,16 +472,21 @@ struct SmallTile {
   }
 };
 
-// Tile `id` of tm x tn: groups of 8 tile rows, columns inside a group, rows
-// fastest, so that the workgroups in flight on an XCD share operands in its
-// L2. Workgroups are dealt to the 8 XCDs in turn; each XCD gets a contiguous
-// run of ids.
-__device__ __forceinline__ void tile_at(int bid, int total, int tm, int tn, int *z, int *mt,
-                                        int *nt) {
-  const int xcd = bid & 7, local = bid >> 3;
-  const int per = total >> 3, more = total & 7;
-  int id = xcd * per + (xcd < more ? xcd : more) + local;
-  const int plane = tm * tn;
+// The tile of workgroup `bid` of `groups`, out of tm x tn x tz: false if there
+// is none left for it. Workgroups are dealt to the 8 XCDs in turn; each XCD
+// takes a contiguous run of ids, which go through groups of 8 tile rows, columns
+// inside a group, rows fastest, so that the workgroups in flight on an XCD share
+// operands in its L2. `tm` may be the number of tile rows that the device found
+// (rows that count), with workgroups launched for more: the ones left over are
+// the last of each XCD. (Cut by the launched number, 1228 of 2047 rows at
+// V = 32000, H = 2048 took 204 us for their logits instead of WALK.)
+__device__ __forceinline__ bool tile_at(int bid, int groups, int tm, int tn, int tz, int *z,
+                                        int *mt, int *nt) {
+  const int plane = tm * tn, total = plane * tz;
+  const int n = groups < 8 ? groups : 8;
+  const int xcd = bid % n, per = total / n, more = total % n;
+  if (bid / n >= per + (xcd < more ? 1 : 0)) return false;
+  int id = xcd * per + (xcd < more ? xcd : more) + bid / n;
   *z = id / plane;
   id -= *z * plane;
   const int group = id / (8 * tn);
@@ -490,6 +495,7 @@ __device__ __forceinline__ void tile_at(int bid, int total, int tm, int tn, int 
   const int in = id - group * 8 * tn;
   *mt = first + in % gm;
   *nt = in / gm;
+  return true;
 }
 
 }  // namespace hg

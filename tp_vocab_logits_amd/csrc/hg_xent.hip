@@ -182,14 +182,15 @@ enum LogitsMode { kStats = 0, kProb = 1, kGrad = 2 };
 
 template <class T, class Tile, int NT, int MODE>
 __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc, ShardTableN<NT> w,
-                                                   int shard, int v0, int vend, int tm, int tn) {
+                                                   int shard, int v0, int vend, int tn) {
   __shared__ __attribute__((aligned(1024))) unsigned char lds[kTileLds];
-  int z, mt, nt;
-  tile_at(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), tm, tn, &z, &mt, &nt);
-  const int kept = pl.r.head[0];
   constexpr int kEdge = Tile::kEdge, MI = Tile::MI, NJ = Tile::NJ;
+  const int kept = pl.r.head[0];
+  int z, mt, nt;
+  if (!tile_at(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x),
+               (kept + kEdge - 1) / kEdge, tn, 1, &z, &mt, &nt))
+    return;
   const int m0 = mt * kEdge, n0 = v0 + nt * kEdge;
-  if (m0 >= kept) return;
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int wr = wave >> 2, wc = wave & 3, l16 = lane & 15, g = lane >> 4;
@@ -535,11 +536,20 @@ __global__ __launch_bounds__(256) void k_join(XentPlan pl, const float *grad, fl
   if (row < kept) {
     const float *pm = pl.part + row;
     const float *ps = pm + static_cast<long long>(tiles) * pl.m;
-    for (int t = k; t < tiles; t += 16) {
-      const float a = pm[static_cast<long long>(t) * pl.m], b = ps[static_cast<long long>(t) * pl.m];
-      const float hi = fmaxf(mx, a);
+    for (int t0 = k; t0 < tiles; t0 += 16 * 8) {  // eight tiles in flight
+      float a[8], b[8], hi = mx;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int t = t0 + 16 * u;
+        a[u] = t < tiles ? pm[static_cast<long long>(t) * pl.m] : -__builtin_inff();
+        b[u] = t < tiles ? ps[static_cast<long long>(t) * pl.m] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) hi = fmaxf(hi, a[u]);
       const float ref = hi == -__builtin_inff() ? 0.f : hi;
-      sum = sum * exp2_(mx - ref) + b * exp2_(a - ref);
+      sum *= exp2_(mx - ref);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) sum += b[u] * exp2_(a[u] - ref);
       mx = hi;
     }
   }
@@ -634,7 +644,7 @@ __device__ __forceinline__ void dw_store(void *dw, long long at, f32x4 v, int wi
 // the CUs that dX leaves over.
 struct GradArgs {
   int v0, vend;       // the piece's columns
-  int xgroups, xm, per, first;  // dX: workgroups, tile rows, steps per split
+  int xgroups, per, first;  // dX: workgroups, steps per split, whether sums start at 0
   int wm, tn;         // dW: tile rows; both: tile columns
   void *dw;
   int wide, accumulate;
@@ -655,9 +665,10 @@ __global__ __launch_bounds__(512, 2) void k_grads(XentPlan pl, ShardTableN<NT> w
   if (static_cast<int>(blockIdx.x) < ga.xgroups) {
     // dX = d W over a run of the piece's columns; fp32 partial sums, joined in a
     // fixed order by k_dx_join
-    tile_at(static_cast<int>(blockIdx.x), ga.xgroups, ga.xm, ga.tn, &z, &mt, &nt);
+    if (!tile_at(static_cast<int>(blockIdx.x), ga.xgroups, (kept + kEdge - 1) / kEdge, ga.tn,
+                 pl.split_dx, &z, &mt, &nt))
+      return;
     const int m0 = mt * kEdge, n0 = nt * kEdge;
-    if (m0 >= kept) return;
     const int k0 = z * ga.per * kStep;
     int k1 = k0 + ga.per * kStep;
     if (k1 > vend - v0) k1 = vend - v0;
@@ -688,8 +699,9 @@ __global__ __launch_bounds__(512, 2) void k_grads(XentPlan pl, ShardTableN<NT> w
   }
   // dW rows of the piece = d^T X over the packed rows, or over a run of them
   // (fp32 partial sums, joined by k_dw_join)
-  tile_at(static_cast<int>(blockIdx.x) - ga.xgroups, static_cast<int>(gridDim.x) - ga.xgroups,
-          ga.wm, ga.tn, &z, &mt, &nt);
+  if (!tile_at(static_cast<int>(blockIdx.x) - ga.xgroups,
+               static_cast<int>(gridDim.x) - ga.xgroups, ga.wm, ga.tn, pl.split_dw, &z, &mt, &nt))
+    return;
   const int c0 = mt * kEdge, n0 = nt * kEdge;  // column of the piece
   int k0 = 0, k1 = kept;
   const bool split = pl.split_dw > 1;
@@ -827,7 +839,7 @@ hipError_t launch_xent_logits(const XentPlan &p, const VocabMatrix &w, int mode,
         auto go = [&](auto kernel) {
           hipLaunchKernelGGL(kernel, dim3(tm * tn), dim3(512), 0, s, p,
                              static_cast<const u32x4 *>(p.xc), small_table<NT>(w.t), w.shard, v0,
-                             vend, tm, tn);
+                             vend, tn);
         };
         if (mode == kStats) go(k_logits<T, Tile, NT, kStats>);
         else if (mode == kProb) go(k_logits<T, Tile, NT, kProb>);
@@ -902,8 +914,7 @@ hipError_t launch_xent_grads(const XentPlan &p, const VocabMatrix &w, int v0, in
   a.v0 = v0;
   a.vend = vend;
   a.tn = ceil_div(p.hidden, edge);
-  a.xm = ceil_div(p.m, edge);
-  a.xgroups = a.xm * a.tn * p.split_dx;
+  a.xgroups = ceil_div(p.m, edge) * a.tn * p.split_dx;
   a.per = ceil_div(ceil_div(cols, kStep), p.split_dx);
   a.first = first ? 1 : 0;
   a.wm = ceil_div(rows, edge);

@@ -78,6 +78,15 @@ hipError_t launch_xent_factors(const XentPlan &p, const float *lse, const float 
                                hipStream_t s);
 // Unnormalised probabilities -> d, in place.
 hipError_t launch_xent_normalise(const XentPlan &p, hipStream_t s);
+// Both of the above in one launch, every workgroup merging its rows' tiles by
+// itself: while a row's tiles fit two per lane of its 32 lanes and the rows'
+// largest factor, which fp16's d needs, can be found on the way (m labels per
+// workgroup; it must not depend on lse).
+inline bool xent_joins_in_place(const XentPlan &p) {
+  return (p.vocab + p.ref - 1) / p.ref <= 64 && p.m <= 1024 && (!p.half || p.z_weight == 0.f);
+}
+hipError_t launch_xent_join_normalise(const XentPlan &p, const float *grad, float *loss, float *lse,
+                                      hipStream_t s);
 // dX's partial sums and dW's rows of the piece, in one launch.
 hipError_t launch_xent_grads(const XentPlan &p, const VocabMatrix &w, int v0, int cols, bool first,
                              void *dw, bool wide, bool accumulate, hipStream_t s);

@@ -61,12 +61,13 @@ struct Prob {
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// The power of two by which d is scaled (and its inverse): 1 for bf16.
+// The power of two by which d is scaled (and its inverse) for the bits of the
+// largest row factor: 1 for bf16.
 template <class T>
-__device__ __forceinline__ float d_scale(const XentRows &r, bool inverse) {
+__device__ __forceinline__ float d_scale_of(int largest, bool inverse) {
   if constexpr (!T::kHalf) return 1.f;
   // 2^(13 - exponent of the largest factor): products end in 2^13..2^14
-  const int e = static_cast<int>((static_cast<unsigned>(r.head[1]) >> 23) & 255u);
+  const int e = static_cast<int>((static_cast<unsigned>(largest) >> 23) & 255u);
   int up = e == 0 ? 0 : 13 - (e - 127);
   up = up > 126 ? 126 : up < -126 ? -126 : up;
   return __builtin_bit_cast(float, static_cast<unsigned>(127 + (inverse ? -up : up)) << 23);
@@ -85,6 +86,11 @@ __device__ __forceinline__ void leave_out(long long t, long long ignore, int i, 
   const float v = t == ignore ? 0.f : __builtin_nanf("");
   loss[i] = v;
   lse[i] = v;
+}
+
+template <class T>
+__device__ __forceinline__ float d_scale(const XentRows &r, bool inverse) {
+  return d_scale_of<T>(T::kHalf ? r.head[1] : 0, inverse);
 }
 
 // The packed rows' x, 16 bytes per lane.
@@ -590,9 +596,22 @@ __global__ __launch_bounds__(256) void k_factors(XentPlan pl, const float *lse, 
   if (f < __builtin_inff()) atomicMax(pl.r.head + 1, __builtin_bit_cast(int, f));
 }
 
-// Unnormalised probabilities -> d in place: 16 bytes (8 columns) per lane and
-// step, 8 rows of a panel per workgroup and step. HBM-bound: reads and writes d
-// once.
+// 16 bytes (8 columns) of unnormalised probabilities -> d: times c, less cb at
+// column `at` of them.
+template <class T>
+__device__ __forceinline__ u32x4 normalised(u32x4 v, float c, float cb, int at) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    float lo = Prob<T>::get(v[t] & 0xFFFFu) * c, hi = Prob<T>::get(v[t] >> 16) * c;
+    if (at == 2 * t) lo -= cb;
+    if (at == 2 * t + 1) hi -= cb;
+    v[t] = bits16<T>(lo) | bits16<T>(hi) << 16;
+  }
+  return v;
+}
+
+// Unnormalised probabilities -> d in place: 16 bytes per lane and step, 8 rows
+// of a panel per workgroup and step. HBM-bound: reads and writes d once.
 template <class T>
 __global__ __launch_bounds__(256) void k_normalise(XentPlan pl) {
   const int kept = pl.r.head[0];
@@ -608,16 +627,71 @@ __global__ __launch_bounds__(256) void k_normalise(XentPlan pl) {
     const float mx = part[row];
     const float ref = mx == -__builtin_inff() ? 0.f : mx;
     const float c = exp2_(ref - pl.r.lse2[row]) * (pl.r.ca[row] * up), cb = pl.r.cb[row] * up;
-    const int at = pl.r.lab[row] - panel * kPanel - 8 * k;
-    u32x4 v = d[static_cast<long long>(row) * 32 + k];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      float lo = Prob<T>::get(v[t] & 0xFFFFu) * c, hi = Prob<T>::get(v[t] >> 16) * c;
-      if (at == 2 * t) lo -= cb;
-      if (at == 2 * t + 1) hi -= cb;
-      v[t] = bits16<T>(lo) | bits16<T>(hi) << 16;
+    u32x4 *o = d + static_cast<long long>(row) * 32 + k;
+    *o = normalised<T>(*o, c, cb, pl.r.lab[row] - panel * kPanel - 8 * k);
+  }
+}
+
+// k_join and k_normalise in one (see xent_joins_in_place): the 32 lanes of a
+// row merge its tiles, two at most each. One launch less where launches are
+// what a call takes (33 rows at V = 4096, H = 264: FUSEDJOIN).
+template <class T>
+__global__ __launch_bounds__(256) void k_join_normalise(XentPlan pl, const float *grad, float *loss,
+                                                        float *lse) {
+  __shared__ int wave_top[4];
+  const int kept = pl.r.head[0];
+  const int panel = static_cast<int>(blockIdx.x), tid = static_cast<int>(threadIdx.x);
+  const int tiles = (pl.vocab + pl.ref - 1) / pl.ref;
+  int largest = 0;
+  if constexpr (T::kHalf) {
+    for (int row = tid; row < kept; row += 256) {
+      const float f = fabsf(pl.scale * grad[pl.r.idx[row]]);
+      const int bits = f < __builtin_inff() ? __builtin_bit_cast(int, f) : 0;
+      largest = largest > bits ? largest : bits;
     }
-    d[static_cast<long long>(row) * 32 + k] = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_xor(largest, d);
+      largest = largest > o ? largest : o;
+    }
+    if ((tid & 63) == 0) wave_top[tid >> 6] = largest;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) largest = largest > wave_top[k] ? largest : wave_top[k];
+    if (panel == 0 && blockIdx.y == 0 && tid == 0) pl.r.head[1] = largest;
+  }
+  const float up = d_scale_of<T>(largest, false);
+  const int k = tid & 31, mine = (panel * kPanel + 8 * k) / pl.ref;
+  u32x4 *d = static_cast<u32x4 *>(pl.d) + static_cast<long long>(panel) * pl.m * 32;
+  for (int row = static_cast<int>(blockIdx.y * 8 + tid / 32); row < kept;
+       row += static_cast<int>(gridDim.y) * 8) {
+    const float *pm = pl.part + row;
+    const float *ps = pm + static_cast<long long>(tiles) * pl.m;
+    const float a0 = k < tiles ? pm[static_cast<long long>(k) * pl.m] : -__builtin_inff();
+    const float b0 = k < tiles ? ps[static_cast<long long>(k) * pl.m] : 0.f;
+    const bool two = k + 32 < tiles;
+    const float a1 = two ? pm[static_cast<long long>(k + 32) * pl.m] : -__builtin_inff();
+    const float b1 = two ? ps[static_cast<long long>(k + 32) * pl.m] : 0.f;
+    float mx = fmaxf(a0, a1);
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor(mx, s));
+    const float all = mx == -__builtin_inff() ? 0.f : mx;
+    float sum = b0 * exp2_(a0 - all) + b1 * exp2_(a1 - all);
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) sum += __shfl_xor(sum, s);
+    const float l2 = all + __log2f(sum), l = l2 * kLn2;
+    const int i = pl.r.idx[row];
+    const float u = pl.scale * grad[i];
+    if (panel == 0 && k == 0) {
+      loss[i] = (l2 - pl.r.zt[row]) * kLn2 + pl.z_weight * l * l;
+      lse[i] = l;
+    }
+    if (mine >= tiles) continue;
+    const float top = pm[static_cast<long long>(mine) * pl.m];
+    const float ref = top == -__builtin_inff() ? 0.f : top;
+    const float c = exp2_(ref - l2) * (u * (1.f + 2.f * pl.z_weight * l) * up);
+    u32x4 *o = d + static_cast<long long>(row) * 32 + k;
+    *o = normalised<T>(*o, c, u * up, pl.r.lab[row] - panel * kPanel - 8 * k);
   }
 }
 
@@ -900,6 +974,15 @@ hipError_t launch_xent_dx_join(const XentPlan &p, void *dx, hipStream_t s) {
   by_type(p.half, [&](auto type) {
     hipLaunchKernelGGL(k_dx_join<decltype(type)>, grid, dim3(256), 0, s, p,
                        static_cast<uint2 *>(dx));
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_join_normalise(const XentPlan &p, const float *grad, float *loss, float *lse,
+                                      hipStream_t s) {
+  const dim3 grid(p.piece / kPanel, ceil_div(p.m, 8));
+  by_type(p.half, [&](auto type) {
+    hipLaunchKernelGGL(k_join_normalise<decltype(type)>, grid, dim3(256), 0, s, p, grad, loss, lse);
   });
   return hipGetLastError();
 }

@@ -417,7 +417,8 @@ int hg_xent_step(const hg_xent_shape *s, const void *x, const void *const *w, co
 int hg_embed(int tp, int shard, int hidden, int dtype, const void *const *w, const void *tokens,
              int token_bytes, int n, float scale, void *out, void *stream);
 
-/* Bytes of device workspace for hg_embed_grad. */
+/* Bytes of device workspace for hg_embed_grad: 0 for few tokens (the call then
+ * takes ws == NULL). */
 int hg_embed_workspace(int tp, int shard, int hidden, int n, size_t *bytes);
 
 /*

@@ -181,13 +181,15 @@ def test_embed_refusals():
     assert look(w=None) == _lib.HG_EINVAL and look(out=None) == _lib.HG_EINVAL
     assert look(out=ctypes.c_void_p(1 << 24)) == _lib.HG_EINVAL
     assert look(k=0) == _lib.HG_OK  # nothing to do
-    assert grad(dw=None) == _lib.HG_EINVAL and grad(dy=None) == _lib.HG_EINVAL and grad(ws=None) == _lib.HG_EINVAL
+    assert grad(dw=None) == _lib.HG_EINVAL and grad(dy=None) == _lib.HG_EINVAL
+    assert grad(k=300, ws=None) == _lib.HG_EINVAL and grad(k=300, ws=ctypes.c_void_p((5 << 24) + 64)) == _lib.HG_EINVAL
     assert grad(dw=ctypes.c_void_p(1 << 24)) == _lib.HG_EINVAL and grad(wide=2) == _lib.HG_EINVAL
-    assert grad(nbytes=64) == _lib.HG_ESIZE
+    assert grad(k=300, nbytes=64) == _lib.HG_ESIZE
     assert grad(k=0, acc=1) == _lib.HG_OK
     assert lib.hg_embed_workspace(2, 64, 16, 4, None) == _lib.HG_EINVAL
     assert lib.hg_embed_workspace(2, 64, 16, -1, ctypes.byref(n)) == _lib.HG_EINVAL
     assert lib.hg_embed_workspace(2, 64, 16, 0, ctypes.byref(n)) == _lib.HG_OK and n.value == 0
+    assert lib.hg_embed_workspace(2, 64, 16, 300, ctypes.byref(n)) == _lib.HG_OK and n.value > 0
 
 
 def test_python_refusals():
@@ -610,7 +612,8 @@ def check_embed_grad(tokens, dy, tp, shard, scale, dtype, wide=False, old=None):
 
 @gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("tp,shard,hidden,n", [(1, 1, 8, 1), (2, 33, 16, 7), (1, 513, 72, 64), (3, 5, 2056, 400),
+@pytest.mark.parametrize("tp,shard,hidden,n", [(1, 1, 8, 1), (2, 33, 16, 7), (1, 513, 72, 64), (3, 5, 2056, 400), (2, 40, 2056, 256),
+                                               (2, 40, 72, 257),
                                                (8, 96, 264, 4096), (8, 96, 264, 4097), (64, 300, 40, 9000),
                                                (5, 70000, 8, 5000), (64, 5000, 264, 9001)])
 def test_embed_grad(tp, shard, hidden, n, dtype):
@@ -631,7 +634,7 @@ def test_embed_grad(tp, shard, hidden, n, dtype):
 
 
 @gpu
-@pytest.mark.parametrize("n", [1, 63, 64, 65, 1000, 4096, 20000])
+@pytest.mark.parametrize("n", [1, 63, 64, 65, 256, 257, 1000, 4096, 20000])
 def test_embed_grad_of_one_token(n):
     """Every position the same token: one sum through every block."""
     note(f"one token {n=}")

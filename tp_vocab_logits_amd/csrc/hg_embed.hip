@@ -486,6 +486,82 @@ __global__ __launch_bounds__(256) void k_sum_join(SumArgs a) {
   write_row<T, D>(a, key, k * N, sum);
 }
 
+// Few tokens: everything in one launch, with no sort. The first workgroups take
+// a position and 256 vectors of its row each; the one whose position is its
+// token's first adds up the rows of all of them, in order. The others write
+// zeros, 64 rows each, but for the rows that a token names.
+constexpr int kFewTokens = 256;  // one per thread
+template <class T, class D>
+__global__ __launch_bounds__(256) void k_sum_few(SumArgs a, const void *tokens, int token_bytes) {
+  constexpr int N = Vec<T>::N;
+  const int tid = static_cast<int>(threadIdx.x), bid = static_cast<int>(blockIdx.x);
+  const int n = static_cast<int>(a.n), hv = a.hidden / N;
+  __shared__ unsigned long long named[4];
+  const int mine = tid < n ? key_at(tokens, token_bytes, tid, a.rows) : a.rows;
+  if (bid < n * a.slabs) {
+    const int j = bid / a.slabs, k = (bid - j * a.slabs) * 256 + tid;
+    const int key = key_at(tokens, token_bytes, j, a.rows);
+    if (key >= a.rows) return;
+    const unsigned long long votes = __ballot(mine == key);
+    if ((tid & 63) == 0) named[tid >> 6] = votes;
+    __syncthreads();
+    unsigned long long m[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m[w] = named[w];
+    for (int w = 0; w < (j >> 6); ++w)
+      if (m[w]) return;
+    if (m[j >> 6] & ((1ull << (j & 63)) - 1)) return;  // an earlier position has the token
+    if (k >= hv) return;
+    float sum[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      while (m[w]) {
+        u32x4 v[8];
+        int got = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (m[w]) {
+            const int p = 64 * w + __ffsll(m[w]) - 1;
+            m[w] &= m[w] - 1;
+            v[u] = a.dy[static_cast<long long>(p) * hv + k];
+            got = u + 1;
+          }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (u < got) {
+            float f[N];
+            Vec<T>::get(v[u], f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum[e] += f[e];
+          }
+      }
+    }
+    write_row<T, D>(a, key, k * N, sum);
+    return;
+  }
+  const int v0 = (bid - n * a.slabs) * 64;
+  if (tid == 0) named[0] = 0;
+  __syncthreads();
+  if (mine >= v0 && mine < v0 + 64 && mine < a.rows) atomicOr(&named[0], 1ull << (mine - v0));
+  __syncthreads();
+  const unsigned long long skip = named[0];
+  const int vecs = hv * (std::is_same_v<T, D> ? 1 : 2);
+  u32x4 *dw = static_cast<u32x4 *>(a.dw) + static_cast<long long>(v0) * vecs;
+  const int last = a.rows - v0 < 64 ? a.rows - v0 : 64;
+  if (!skip) {  // one run of memory
+    const long long all = static_cast<long long>(last) * vecs;
+    for (long long k = tid; k < all; k += 256) dw[k] = u32x4{0u, 0u, 0u, 0u};
+    return;
+  }
+  for (int r = 0; r < last; ++r) {
+    if ((skip >> r) & 1) continue;
+    for (int k = tid; k < vecs; k += 256)
+      dw[static_cast<long long>(r) * vecs + k] = u32x4{0u, 0u, 0u, 0u};
+  }
+}
+
 __global__ __launch_bounds__(256) void k_zero(u32x4 *p, long long vecs) {
   for (long long k = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; k < vecs;
        k += static_cast<long long>(gridDim.x) * 256)
@@ -538,7 +614,8 @@ hipError_t launch_zero(void *p, size_t bytes, hipStream_t s) {
 }
 
 EmbedPlan embed_plan(int rows, int hidden, long long n) {
-  EmbedPlan p;
+  EmbedPlan p = {};
+  if (n <= kFewTokens) return p;  // no workspace
   int bits = 1;
   while ((1ll << bits) <= rows) ++bits;  // the largest key is `rows`
   p.passes = (bits + 8) / 9;
@@ -566,15 +643,45 @@ EmbedPlan embed_plan(int rows, int hidden, long long n) {
 hipError_t launch_embed_grad(const EmbedPlan &p, void *ws, int rows, int hidden, int dtype,
                              const void *tokens, int token_bytes, long long n, const void *dy,
                              float scale, void *dw, bool wide, bool accumulate, hipStream_t s) {
+  const long long zeros = accumulate ? 0
+                                     : static_cast<long long>(rows) * hidden *
+                                           (wide || dtype == HG_FP32 ? 4 : 2) / 16;
+  if (n == 0) return launch_zero(dw, static_cast<size_t>(zeros) * 16, s);
+  SumArgs a = {};
+  a.dy = static_cast<const u32x4 *>(dy);
+  a.dw = dw;
+  a.n = n;
+  a.rows = rows;
+  a.hidden = hidden;
+  a.scale = scale;
+  a.accumulate = accumulate ? 1 : 0;
+  auto with_types = [&](auto go) {
+    by_dtype(dtype, [&](auto type) {
+      using T = decltype(type);
+      a.slabs = (hidden / Vec<T>::N + 255) / 256;
+      if constexpr (!std::is_same_v<T, TypeF32>) {
+        if (wide) {
+          go(type, TypeF32{});
+          return;
+        }
+      }
+      go(type, type);
+    });
+  };
+  if (n <= kFewTokens) {
+    const int fills = accumulate ? 0 : (rows + 63) / 64;
+    with_types([&](auto t, auto d) {
+      hipLaunchKernelGGL((k_sum_few<decltype(t), decltype(d)>),
+                         dim3(static_cast<unsigned>(n) * a.slabs + fills), dim3(256), 0, s, a,
+                         tokens, token_bytes);
+    });
+    return hipGetLastError();
+  }
   char *base = static_cast<char *>(ws);
   int *buf[4], *hist = reinterpret_cast<int *>(base + p.off[4]);
   for (int k = 0; k < 4; ++k) buf[k] = reinterpret_cast<int *>(base + p.off[k]);
   int side = 0;
   // the zeros, cut into one part per launch of the sort
-  const long long zeros = accumulate ? 0
-                                     : static_cast<long long>(rows) * hidden *
-                                           (wide || dtype == HG_FP32 ? 4 : 2) / 16;
-  if (n == 0) return launch_zero(dw, static_cast<size_t>(zeros) * 16, s);
   const int launches = n <= kSortTile ? 1 : 3 * p.passes;
   const long long share = (zeros + launches - 1) / launches;
   int part = 0;
@@ -604,35 +711,17 @@ hipError_t launch_embed_grad(const EmbedPlan &p, void *ws, int rows, int hidden,
                          rows, 9 * k, hist, p.tiles, buf[2 * side], buf[2 * side + 1], f3);
     }
   }
-  by_dtype(dtype, [&](auto type) {
-    using T = decltype(type);
-    SumArgs a;
-    a.keys = buf[2 * side];
-    a.pos = buf[2 * side + 1];
-    a.dy = static_cast<const u32x4 *>(dy);
-    a.dw = dw;
-    a.part = reinterpret_cast<float *>(base + p.off[5]);
-    a.n = n;
-    a.rows = rows;
-    a.hidden = hidden;
-    a.per = p.per;
-    a.blocks = p.blocks;
-    a.slabs = (hidden / Vec<T>::N + 255) / 256;
-    a.scale = scale;
-    a.accumulate = accumulate ? 1 : 0;
-    auto go = [&](auto dtag) {
-      using D = decltype(dtag);
-      hipLaunchKernelGGL((k_sum<T, D>), dim3(a.blocks * a.slabs), dim3(256), 0, s, a);
-      if (a.blocks > 1)
-        hipLaunchKernelGGL((k_sum_join<T, D>), dim3((a.blocks - 1) * a.slabs), dim3(256), 0, s, a);
-    };
-    if constexpr (!std::is_same_v<T, TypeF32>) {
-      if (wide) {
-        go(TypeF32{});
-        return;
-      }
-    }
-    go(type);
+  a.keys = buf[2 * side];
+  a.pos = buf[2 * side + 1];
+  a.part = reinterpret_cast<float *>(base + p.off[5]);
+  a.per = p.per;
+  a.blocks = p.blocks;
+  with_types([&](auto t, auto d) {
+    using T = decltype(t);
+    using D = decltype(d);
+    hipLaunchKernelGGL((k_sum<T, D>), dim3(a.blocks * a.slabs), dim3(256), 0, s, a);
+    if (a.blocks > 1)
+      hipLaunchKernelGGL((k_sum_join<T, D>), dim3((a.blocks - 1) * a.slabs), dim3(256), 0, s, a);
   });
   return hipGetLastError();
 }

@@ -372,19 +372,19 @@ HG_API int hg_embed_grad(int tp, int shard, int hidden, int dtype, const void *t
   if (!dw || !aligned(dw, 16)) return HG_EINVAL;
   const size_t esize = dtype == HG_FP32 ? 4 : 2;
   const size_t rows = static_cast<size_t>(tp) * shard;
+  const hg::EmbedPlan p = hg::embed_plan(static_cast<int>(rows), hidden, n);
   Ranges r;
   r.add(dw, rows * hidden * (dw_wide ? 4 : esize), true);
   if (n) {
-    if (!tokens || !aligned(tokens, token_bytes) || !dy || !aligned(dy, 16) || !ws ||
-        !aligned(ws, 256))
+    if (!tokens || !aligned(tokens, token_bytes) || !dy || !aligned(dy, 16) ||
+        (p.bytes && (!ws || !aligned(ws, 256))))
       return HG_EINVAL;
     r.add(tokens, static_cast<size_t>(n) * token_bytes, false);
     r.add(dy, static_cast<size_t>(n) * hidden * esize, false);
-    r.add(ws, ws_bytes, true);
+    if (p.bytes) r.add(ws, ws_bytes, true);
   }
   if (r.clash()) return HG_EINVAL;
-  const hg::EmbedPlan p = hg::embed_plan(static_cast<int>(rows), hidden, n);
-  if (n && p.bytes > ws_bytes) {
+  if (p.bytes > ws_bytes) {
     hg::record_error("the workspace is smaller than hg_embed_workspace asks");
     return HG_ESIZE;
   }

@@ -301,10 +301,12 @@ def embed_grad(tokens: torch.Tensor, dy: torch.Tensor, tp: int, shard: int, scal
     _on_gpu(device)
     tp, shard = int(tp), int(shard)
     dw = _gradient_buffer(dw, tp * shard, hidden, dy.dtype, device, accumulate)
-    ws = _workspace(_embed_bytes(tp, shard, hidden, tokens.numel()), device)
-    _call(_lib.fast().embed_grad, "hg_embed_grad", device, tp, shard, hidden, _DTYPES[dy.dtype], tokens.data_ptr(), tokens.element_size(),
-          tokens.numel(), dy.data_ptr(), scale, dw.data_ptr(), int(dw.dtype != dy.dtype), int(accumulate),
-          ws.data_ptr(), ws.numel())
+    n = tokens.numel()
+    nbytes = _embed_bytes(tp, shard, hidden, n)
+    ws = _workspace(nbytes, device) if nbytes else None
+    _call(_lib.fast().embed_grad, "hg_embed_grad", device, tp, shard, hidden, _DTYPES[dy.dtype], tokens.data_ptr(),
+          tokens.element_size(), n, dy.data_ptr(), scale, dw.data_ptr(), int(dw.dtype != dy.dtype), int(accumulate),
+          ws.data_ptr() if nbytes else 0, nbytes)
     return dw
 
 

@@ -100,7 +100,7 @@ def scale_mag(x, w, kept, vocab, scale):
 def grad_bounds(x, w, labels, lse, grad, vocab, ignore, scale, z_weight, dtype, lse_off):
     """(dx bound, dw bound): d is off by its probability's error (the logit's
     and lse's, as factors of the exponential), by the rounding to `dtype`, by the
-    probability's own earlier one (a quarter of that at most), and by the
+    probability's own earlier one (an eighth of that, for FP16 a half), and by the
     smallest steps of the 16-bit values (probabilities 2^-32 below a tile's
     largest, d 2^-38 below the largest factor; BF16 2^-64 and none); the sums are fp32
     in any order; results are rounded once."""
@@ -113,7 +113,8 @@ def grad_bounds(x, w, labels, lse, grad, vocab, ignore, scale, z_weight, dtype, 
     part = np.abs(d + np.where(hit > 0, hit * np.sign(scale * grad[kept])[:, None], 0.0))  # |ca| p
     e = logit_bound(x, w, kept, vocab, scale) + lse_off + 16.0 * U32 * (1 + np.abs(lse[kept]))
     e = e + 4.0 * U32 * scale_mag(x, w, kept, vocab, scale)
-    off = part * (1.01 * np.expm1(e)[:, None] + 1.26 * u + 8 * U32) + hit * (1.01 * u + 8 * U32)
+    first = 0.5 if dtype == "fp16" else 0.125
+    off = part * (1.01 * np.expm1(e)[:, None] + 1.01 * (1 + first) * u + 8 * U32) + hit * (1.01 * u + 8 * U32)
     tiny = 2.0 ** -31 if dtype == "fp16" else 2.0 ** -62
     largest = (f * np.maximum(1.0, np.abs(1 + 2 * z_weight * lse[kept]))).max(initial=0.0)
     off = off + tiny * largest

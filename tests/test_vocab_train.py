@@ -705,3 +705,20 @@ def test_few_rows(tp, shard, hidden, vocab, m):
     p.blocks = True
     again = vt.head_xent(x, p.on_gpu()[1], t, tp, shard, **p.how)
     assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+
+
+@gpu
+def test_the_example_learns():
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "tied_vocab_training.py")
+    spec = importlib.util.spec_from_file_location("tied_vocab_training", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    note("example")
+    losses = example.train(40, tell=note)
+    assert np.isfinite(losses).all()
+    assert abs(losses[0] - np.log(1000)) < 1.0 and losses[-1] < 0.8 * losses[0]
+    assert losses == example.train(40, tell=note)  # the same bits every time

@@ -15,8 +15,11 @@
 // their tokens: a frequent token's sum is spread over many workgroups. A sum
 // inside one block is written at once; one that crosses a block's edge leaves
 // fp32 partial rows, joined in order by a second launch. The whole gradient is
-// first filled with zeros, beside the sort and in its launches: rows that get a
-// sum are written twice, which costs less than finding out which they are.
+// first filled with zeros, beside the sort and in its launches; rows that get a
+// sum are written twice. (65536 tokens of 2048 columns into 163840 rows: 240 us,
+// 140 of them fill and sort, 80 sums, 18 joins; filled after the sort by the
+// launch that sums, 350.)
+// Up to 256 tokens, one launch does it all without a sort (k_sum_few).
 
 #include <type_traits>
 

@@ -35,6 +35,16 @@
 //   half of step k+1; part 2 reads A's lower half, and loads B and A's upper
 //   half of step k+2. Each ends with vmcnt(8): everything but the newest eight
 //   loads of the wave has landed, which is what the next part reads.
+// Measured (4096 rows, V = 163840, H = 7168): logits 6.45 ms, 1.49 PFLOP/s, the
+// matrix cores busy 79 % of the cycles at 1.74 GHz, the clock that the power
+// limit leaves; the gradient's products (a column operand on one or both sides)
+// 14.55 ms, 1.32 PFLOP/s, busy 68 % at 1.79 GHz. The memory parts bound it:
+// five wait states more per load cost 3 to 5 %. Not kept, measured the same or
+// slower: a third stage of B (160 KB of LDS), B's reads spread over both parts,
+// the loads spread over both parts (logits 5 % slower) or all in the second (6 %
+// slower) or among the MFMAs (15 % slower), X turned in memory for dW, workgroups
+// that stay and load ahead of their epilogue (3 % slower here, 2 % faster at
+// H = 1024), no s_setprio (logits 1 % faster, gradients 1 % slower).
 // Loads past the last step, past K or past an operand's rows lie beyond their
 // buffer resource, which fills LDS with zeros without touching memory: the
 // counts stay the same to the end and no operand needs padding.
@@ -96,10 +106,15 @@ __device__ __forceinline__ rsrc_t resource(const void *base, long long bytes) {
 
 // One load of 16 bytes per lane straight into LDS, at lds + 16*lane. Written
 // as an instruction because the compiler, which knows that the builtin form
-// writes LDS, waits for every load in flight before a transposed LDS read
-// (vmcnt(0); dW at 4096 rows, V = 163840, H = 7168: NOASM ms). The load has
-// no output register; its order against the LDS reads is kept by the waits and
-// barriers of tile_product and by the memory clobber.
+// writes LDS, waits for every load in flight (vmcnt(0)) before a transposed LDS
+// read: the gradient's two products of 4096 rows at V = 163840, H = 7168 take
+// 14.55 ms so and 14.78 with the builtin, of 8192 rows at V = 32768, H = 1024
+// 781 us and 818. The load has no output register; its order against the LDS
+// reads is kept by the waits and barriers of the products and by the memory
+// clobber. What the compiler does not see it does not guard: the resource must
+// come from scalar instructions (a vector instruction that writes a scalar
+// register needs five wait states before this reads it), which
+// tests/test_vocab_asm.py checks in the compiled kernels.
 // STREAM: data that is read once (non-temporal).
 template <bool STREAM = false>
 __device__ __forceinline__ void load_lds(rsrc_t r, unsigned char *lds, unsigned offset) {
@@ -415,8 +430,8 @@ struct BigTile {
 
 // 128 x 128 for problems whose 256 x 256 tiles would leave CUs idle: a quarter
 // of the work per tile, a ring of four 32 KB stages loaded three steps ahead
-// and one barrier per step. (At 256-column tiles, 33 rows over V = 4096, H = 264
-// spread over 16 workgroups; measured SMALLTILE.)
+// and one barrier per step. 33 rows over V = 4096, H = 264 take 8.7 us for their
+// logits on 32 small tiles and 16 us on 16 big ones.
 struct SmallTile {
   static constexpr int kEdge = 128, MI = 4, NJ = 2, kRows = 64, kCols = 32;
   static constexpr int kBLoads = 2;
@@ -479,7 +494,7 @@ struct SmallTile {
 // operands in its L2. `tm` may be the number of tile rows that the device found
 // (rows that count), with workgroups launched for more: the ones left over are
 // the last of each XCD. (Cut by the launched number, 1228 of 2047 rows at
-// V = 32000, H = 2048 took 204 us for their logits instead of WALK.)
+// V = 32000, H = 2048 took 212 us for their logits instead of 172.)
 __device__ __forceinline__ bool tile_at(int bid, int groups, int tm, int tn, int tz, int *z,
                                         int *mt, int *nt) {
   const int plane = tm * tn, total = plane * tz;

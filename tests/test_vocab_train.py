@@ -92,7 +92,8 @@ def shape(**over):
 
 BAD_SHAPES = [dict(tp=0), dict(tp=65), dict(shard=0), dict(shard=48), dict(hidden=0), dict(hidden=12), dict(m=-1),
               dict(vocab=0), dict(vocab=129), dict(dtype=2), dict(dtype=-1), dict(label_bytes=2),
-              dict(hidden=(1 << 20) + 8), dict(m=(1 << 24) + 1)]
+              dict(hidden=(1 << 20) + 8), dict(m=(1 << 24) + 1), dict(m=1 << 24, shard=1 << 20, tp=2),
+              dict(hidden=1 << 20, shard=1 << 22, tp=2), dict(hidden=1 << 20, m=1 << 22)]
 
 
 @pytest.mark.parametrize("over", BAD_SHAPES)
@@ -129,7 +130,7 @@ def test_xent_workspace_rules():
         least = need(large, kind, 1)  # the least it can do with
         assert least < whole and need(large, kind, least) <= least
     # d of 2^20 rows: pieces stay within the limit without unbounded search
-    assert need(shape(tp=64, shard=32768, hidden=64, m=1 << 20, vocab=1 << 21), 1, 64 << 30) <= 64 << 30
+    assert need(shape(tp=64, shard=4096, hidden=64, m=1 << 20, vocab=1 << 18), 1, 64 << 30) <= 64 << 30
 
 
 def test_xent_refuses_pointers():

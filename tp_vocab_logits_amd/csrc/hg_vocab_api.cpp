@@ -22,7 +22,7 @@ using hg::XentPlan;
 
 constexpr int kCus = 256;  // compute units of the one device these kernels are built for
 constexpr int kTile = 256, kStep = 64;
-constexpr int kMaxPiece = 1 << 21;  // columns of d: 256 rows of it stay below 2^31 bytes
+constexpr long long kMaxTiles = 1 << 22;  // of 512 lanes: a launch has fewer than 2^32 lanes
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -58,6 +58,9 @@ bool shape_ok(const hg_xent_shape *s) {
     return false;
   const long long rows = static_cast<long long>(s->tp) * s->shard;
   if (rows >= (1ll << 30) || s->vocab < 1 || s->vocab > rows) return false;
+  const long long tm = ceil_div(s->m, kTile), tv = ceil_div(rows, kTile),
+                  th = ceil_div(s->hidden, kTile);
+  if (tm * tv > kMaxTiles || tm * th > kMaxTiles / 4 || tv * th > kMaxTiles / 4) return false;
   if (s->dtype != HG_BF16 && s->dtype != HG_FP16) return false;
   return s->label_bytes == 4 || s->label_bytes == 8;
 }
@@ -70,7 +73,10 @@ bool shape_ok(const hg_xent_shape *s) {
 int pick_split(long long tiles, int steps, double bytes, bool direct) {
   int best = 1;
   double least = 0;
-  const int most = steps / 8 < 1 ? 1 : steps / 8 > 64 ? 64 : steps / 8;
+  long long most = kMaxTiles / 2 / tiles;
+  if (most > steps / 8) most = steps / 8;
+  if (most > 64) most = 64;
+  if (most < 1) most = 1;
   for (int s = 1; s <= most; ++s) {
     const double rounds = static_cast<double>((tiles * s + kCus - 1) / kCus);
     const double cost = rounds * (ceil_div(steps, s) + 6) +
@@ -148,8 +154,7 @@ size_t lay_out(const hg_xent_shape &s, int kind, int piece, char *ws, XentPlan *
 // The plan for a workspace of `limit` bytes (0: any size): the fewest pieces
 // of the vocabulary that fit, all about equally wide.
 size_t plan(const hg_xent_shape &s, int kind, size_t limit, char *ws, XentPlan *p) {
-  const int all = ceil_div(s.vocab, kTile) * kTile;
-  int pieces = ceil_div(all, kMaxPiece);
+  int pieces = 1;
   size_t bytes = 0;
   for (;;) {
     const int piece = ceil_div(ceil_div(s.vocab, pieces), kTile) * kTile;
@@ -328,7 +333,7 @@ namespace {
 
 bool embed_shape_ok(int tp, int shard, int hidden, int n) {
   return tp >= 1 && tp <= HG_MAX_TP && shard >= 1 && hidden >= 8 && hidden % 8 == 0 &&
-         hidden <= (1 << 20) && n >= 0 && static_cast<long long>(tp) * shard < (1ll << 30);
+         hidden <= (1 << 20) && n >= 0 && static_cast<long long>(tp) * shard < (1ll << 29);
 }
 bool embed_type_ok(int dtype) { return dtype == HG_BF16 || dtype == HG_FP16 || dtype == HG_FP32; }
 

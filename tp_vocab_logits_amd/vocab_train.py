@@ -233,6 +233,7 @@ class _HeadLoss(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         x, w, labels, lse = ctx.saved_tensors
         tp, shard, how = ctx.args
@@ -318,6 +319,7 @@ class _Embedding(torch.autograd.Function):
         return embed(tokens, w, tp, shard, scale)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         tokens, = ctx.saved_tensors
         tp, shard, scale, shape = ctx.args

@@ -723,3 +723,28 @@ def test_the_example_learns():
     assert np.isfinite(losses).all()
     assert abs(losses[0] - np.log(1000)) < 1.0 and losses[-1] < 0.8 * losses[0]
     assert losses == example.train(40, tell=note)  # the same bits every time
+
+
+@gpu
+@pytest.mark.parametrize("m", [8, 200])
+def test_losses_of_certain_rows_keep_their_digits(m):
+    """Labels far above the other logits: losses down to 1e-6, from logits
+    around 20. The logits here are exact (a product of few powers of two), so
+    the loss may be off by the exponentials and sums alone: a handful of fp32
+    roundings of numbers about 1 and of the loss itself."""
+    note(f"certain rows {m=}")
+    vocab, hidden = 640, 64
+    x = torch.zeros(m, hidden)
+    x[:, 0] = 1.0
+    x[:, 1] = torch.arange(m) % 8 * 0.25
+    w = torch.zeros(vocab, hidden)
+    w[:, 0] = torch.randint(0, 9, (vocab,), generator=torch.Generator().manual_seed(1)) * 0.25
+    w[7, 0], w[7, 1] = 19.0, 1.0
+    labels = torch.full((m,), 7)
+    loss, lse = vt.head_xent(x.bfloat16().to(DEV), w.bfloat16().to(DEV), labels.to(DEV), 2, 320)
+    want, exact = ov.head_xent(x.numpy().astype(float), w.numpy().astype(float), labels.numpy(), vocab)
+    assert (np.abs(f64(loss) - want) <= 64 * ov.U32 * want + 4 * ov.U32).all()
+    assert (np.abs(f64(lse) - exact) <= 16 * ov.U32 * exact).all()
+    g = torch.full((m,), 1.0 / m)
+    step = vt.head_xent_step(x.bfloat16().to(DEV), w.bfloat16().to(DEV), labels.to(DEV), g.to(DEV), 2, 320)
+    assert (np.abs(f64(step[0]) - want) <= 64 * ov.U32 * want + 4 * ov.U32).all()

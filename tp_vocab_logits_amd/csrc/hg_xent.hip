@@ -73,6 +73,23 @@ __device__ __forceinline__ float d_scale_of(int largest, bool inverse) {
   return __builtin_bit_cast(float, static_cast<unsigned>(127 + (inverse ? -up : up)) << 23);
 }
 
+// A row's results from its largest logit (base 2), the sum of exponentials
+// relative to it, and how far its label's logit lies below it. For a confident
+// row that gap and the sum's logarithm are small, while lse and the logit are
+// large and nearly equal: they never meet in a difference. The sum holds the
+// largest logit's 1, so the logarithm is that of 1 + (sum - 1).
+struct RowLoss {
+  float lse2, lse, loss;
+};
+__device__ __forceinline__ RowLoss row_loss(float top, float sum, float gap, float z_weight) {
+  const float log_sum = log1pf(sum - 1.f);
+  RowLoss o;
+  o.lse2 = top + log_sum * kLog2e;
+  o.lse = top * kLn2 + log_sum;
+  o.loss = gap * kLn2 + log_sum + z_weight * o.lse * o.lse;
+  return o;
+}
+
 __device__ __forceinline__ long long label_at(const void *labels, int bytes, int i) {
   return bytes == 8 ? static_cast<const long long *>(labels)[i]
                     : static_cast<const int *>(labels)[i];
@@ -305,7 +322,7 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
           for (int t = 0; t < 4; ++t)
-            if (lab == 16 * j + t) pl.r.zt[row] = acc[i][j][t] * s2;
+            if (lab == 16 * j + t) pl.r.zt[row] = fmaf(acc[i][j][t], s2, -top[i]);
       }
       float sum = 0.f;
       unsigned short *o = dout + static_cast<long long>(row) * kPanel;
@@ -523,10 +540,10 @@ __global__ __launch_bounds__(64) void k_score_join(XentPlan pl, const void *labe
   if (lane != 0) return;
   float a = 0.f, b = 0.f;
   if (t != pl.ignore) {
-    const float l2 = ref + __log2f(sum);
+    const RowLoss o = row_loss(ref, sum, ref - zt, pl.z_weight);
     const bool real = t >= 0 && t < pl.vocab;
-    b = real ? l2 * kLn2 : __builtin_nanf("");
-    a = real ? (l2 - zt) * kLn2 + pl.z_weight * b * b : b;
+    b = real ? o.lse : __builtin_nanf("");
+    a = real ? o.loss : b;
   }
   loss[row] = a;
   lse[row] = b;
@@ -570,11 +587,11 @@ __global__ __launch_bounds__(256) void k_join(XentPlan pl, const float *grad, fl
   const float ref = mx == -__builtin_inff() ? 0.f : mx;
   sum = 0.f;
   for (int t = 0; t < 16; ++t) sum += ssum[t][c] * exp2_(smax[t][c] - ref);
-  const float l2 = ref + __log2f(sum);
-  const float l = l2 * kLn2;
+  const float own = pl.part[static_cast<long long>(pl.r.lab[row] / pl.ref) * pl.m + row];
+  const RowLoss o = row_loss(ref, sum, (ref - own) - pl.r.zt[row], pl.z_weight);
+  const float l2 = o.lse2, l = o.lse;
   const int i = pl.r.idx[row];
-  // the difference in base 2 first: lse and the label's logit may be close
-  loss[i] = (l2 - pl.r.zt[row]) * kLn2 + pl.z_weight * l * l;
+  loss[i] = o.loss;
   lse[i] = l;
   if (!grad) return;
   const float u = pl.scale * grad[i];
@@ -684,11 +701,13 @@ __global__ __launch_bounds__(256) void k_join_normalise(XentPlan pl, const float
     float sum = b0 * exp2_(a0 - all) + b1 * exp2_(a1 - all);
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) sum += __shfl_xor(sum, s);
-    const float l2 = all + __log2f(sum), l = l2 * kLn2;
+    const float own = pm[static_cast<long long>(pl.r.lab[row] / pl.ref) * pl.m];
+    const RowLoss r = row_loss(all, sum, (all - own) - pl.r.zt[row], pl.z_weight);
+    const float l2 = r.lse2, l = r.lse;
     const int i = pl.r.idx[row];
     const float u = pl.scale * grad[i];
     if (panel == 0 && k == 0) {
-      loss[i] = (l2 - pl.r.zt[row]) * kLn2 + pl.z_weight * l * l;
+      loss[i] = r.loss;
       lse[i] = l;
     }
     if (mine >= tiles) continue;

@@ -692,7 +692,8 @@ def test_argument_rules_on_device():
 
 @gpu
 @pytest.mark.parametrize("m", [1, 15, 16, 17, 31, 32, 33, 64, 65, 100, 127, 128, 129])
-@pytest.mark.parametrize("tp,shard,hidden,vocab", [(1, 32, 8, 5), (8, 2592, 136, 20700)])
+@pytest.mark.parametrize("tp,shard,hidden,vocab", [(1, 32, 8, 5), (8, 2592, 136, 20700), (1, 12320, 328, 12301),
+                                                   (2, 20512, 72, 41001)])
 def test_few_rows(tp, shard, hidden, vocab, m):
     """Up to 128 rows the matrix is streamed, by row counts rounded up to 16,
     32, 64 and 128; the vocabulary's runs end inside tiles and units."""

@@ -69,7 +69,7 @@ hipError_t launch_xent_logits(const XentPlan &p, const VocabMatrix &w, int mode,
                               hipStream_t s);
 // Few rows (m <= kScoreRows): loss and lse straight from x, with no packing.
 constexpr int kScoreRows = 128;
-constexpr int kScoreGroups = 256;  // workgroups, each with a run of the vocabulary
+constexpr int kScoreGroups = 512;  // workgroups at most, each with a run of the vocabulary
 hipError_t launch_xent_score(const XentPlan &p, const VocabMatrix &w, const void *x,
                              const void *labels, float *loss, float *lse, hipStream_t s);
 // Row statistics -> loss, lse and the rows' factors (grad null: none).

@@ -40,6 +40,7 @@ namespace hg {
 
 namespace {
 
+constexpr int kCus = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -369,16 +370,24 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
 // step is needed for x alone. v_mfma_f32_16x16x32 with W as its rows: a lane
 // holds, of one row of x, 8 columns per tile, and keeps a running maximum and
 // sum over all of its columns; lanes, waves and workgroups are joined at the
-// end. Four stages up to 64 rows, three beyond: 80 KB or more in flight per CU.
+// end. As many stages as LDS holds, up to four: 64 KB or more in flight per CU.
 // HBM-bound: one row at V = 163840, H = 7168 takes 342 us, 6.87 TB/s of weights
 // (64 rows: 360 us; on 256 x 256 tiles, 2.5 rounds of the CUs, 445 and 460).
-template <class T, int NT, int MB>
+//
+// KC: a run of at most 128 or 64 rows leaves sub-tiles of the 256 empty, and
+// with them bytes in flight. Its stage holds KC = 2 or 4 times as much k instead:
+// sub-tile s is the rows 64*(s % RB) of chunk s / RB of the step's 64*KC k, and
+// the waves of the chunks add up their parts of the one tile at the end. (One
+// row at V = 20480, H = 7168, a rank's share at TP = 8: 64 us with KC = 1, 49
+// with KC = 2.)
+template <class T, int NT, int MB, int KC>
 __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, const void *labels,
                                                   ShardTableN<NT> w, int shard) {
-  constexpr int XI = MB > 4 ? MB / 4 : 1;       // x loads per wave and step
-  constexpr int kXBytes = XI * 8 * 1024;        // 64 or 128 rows of 128 bytes
-  constexpr int kStageB = 4 * kSubBytes + kXBytes;
-  constexpr int ST = MB > 4 ? 3 : 4;
+  constexpr int RB = 4 / KC;                                 // 64-row blocks of a tile
+  constexpr int XR = 16 * MB > 64 / KC ? 16 * MB : 64 / KC;  // rows of x in a chunk's stage
+  constexpr int XI = KC * XR / 64;                           // x loads per wave and step
+  constexpr int kStageB = 4 * kSubBytes + KC * XR * 128;
+  constexpr int ST = 4 * kStageB <= 160 * 1024 ? 4 : 3 * kStageB <= 160 * 1024 ? 3 : 2;
   constexpr int kLoads = 4 + XI;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[ST * kStageB];
   const int lane = static_cast<int>(threadIdx.x) & 63;
@@ -388,34 +397,35 @@ __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, c
   const int r0 = static_cast<int>(units * blockIdx.x / gridDim.x) * 16;
   int r1 = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x) * 16;
   if (r1 > pl.vocab) r1 = pl.vocab;
-  const int ks = (pl.hidden + kStep - 1) / kStep;
-  const int steps = r1 > r0 ? (r1 - r0 + kTile - 1) / kTile * ks : 0;
+  const int ks = (pl.hidden + kStep * KC - 1) / (kStep * KC);
+  const int steps = r1 > r0 ? (r1 - r0 + 64 * RB - 1) / (64 * RB) * ks : 0;
 
   const LoadLane ll = load_lane<false>(lane);
   const rsrc_t xr = resource(x, static_cast<long long>(pl.m) * pl.hidden * 2);
   const int k8 = pl.hidden >> 3;
   const int sub = wave >> 1, q0 = 4 * (wave & 1);
+  const int block = sub % RB, chunk = sub / RB;  // of the wave's sub-tile
   RankRowSource<NT, 4, true> b;
   int lt = 0, lk = 0;  // tile and step of k of the next loads
-  b.init(w, shard, r1, pl.hidden, r0, sub, q0, lane);
+  b.init(w, shard, r1, pl.hidden, r0, block, q0, lane);
   auto load = [&](int s) __attribute__((always_inline)) {
     unsigned char *st = lds + (s % ST) * kStageB;
     // steps past the last one load nothing and keep the counts
     const int kk = s < steps ? lk : ks;
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
-      const int q = 8 * i + wave;
-      const int o = q & 1;
-      const unsigned v = static_cast<unsigned>((8 * q + ll.row) * pl.hidden * 2 + kk * 128 +
+      const int all = 8 * i + wave, q = all % (XR / 8), o = q & 1;
+      const int k64 = kk * KC + all / (XR / 8);
+      const unsigned v = static_cast<unsigned>((8 * q + ll.row) * pl.hidden * 2 + k64 * 128 +
                                                ll.chunk[o] * 16);
-      load_lds(xr, st + 4 * kSubBytes + q * 1024, kk * 8 + ll.chunk[o] < k8 ? v : kBeyond);
+      load_lds(xr, st + 4 * kSubBytes + all * 1024, k64 * 8 + ll.chunk[o] < k8 ? v : kBeyond);
     }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) b.load(st + sub * kSubBytes, sub, q0 + t, kk);
+    for (int t = 0; t < 4; ++t) b.load(st + sub * kSubBytes, block, q0 + t, kk * KC + chunk);
     if (++lk == ks && s + 1 < steps) {
       lk = 0;
       ++lt;
-      b.init(w, shard, r1, pl.hidden, r0 + lt * kTile, sub, q0, lane);
+      b.init(w, shard, r1, pl.hidden, r0 + lt * 64 * RB, block, q0, lane);
     }
   };
 
@@ -436,16 +446,44 @@ __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, c
   const float s2 = pl.scale * kLog2e;
   __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");  // the labels: only the loads below count
 
+  int n0 = r0 + 64 * block + 32 * (wave & 1) + 4 * g;
+  // The tile's columns are done: into the running statistics.
+  auto tile_done = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < MB; ++j) {
+      float mx = top[j];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int n = n0 + 16 * h + t;
+          const float v = n < r1 ? acc[h][j][t] * s2 : -__builtin_inff();
+          if (n == lab[j] && n < r1) pl.r.zt[16 * j + l16] = v;  // past r1: another's
+          acc[h][j][t] = v;
+          mx = fmaxf(mx, v);
+        }
+      const float ref = mx == -__builtin_inff() ? 0.f : mx;
+      float e = sum[j] * exp2_(top[j] - ref);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) e += exp2_(acc[h][j][t] - ref);
+      sum[j] = e;
+      top[j] = mx;
+      acc[0][j] = acc[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  };
+
 #pragma unroll
   for (int s = 0; s < ST - 1; ++s) load(s);
-  int ck = 0, n0 = r0 + 32 * wave + 4 * g;
+  int ck = 0;
   for (int s = 0; s < steps; ++s) {
     wait_vm_lds<kLoads * (ST - 2)>();
     tile_barrier();
     load(s + ST - 1);
     const unsigned char *st = lds + (s % ST) * kStageB;
     const unsigned char *sw = st + sub * kSubBytes + (wave & 1) * 32 * 128;
-    const unsigned char *sx = st + 4 * kSubBytes;
+    const unsigned char *sx = st + 4 * kSubBytes + chunk * XR * 128;
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       const s16x8 w0 = f.read(sw, 0, kk), w1 = f.read(sw, 1, kk);
@@ -456,36 +494,35 @@ __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, c
         acc[1][j] = T::mma(w1, xv, acc[1][j]);
       }
     }
-    if (++ck == ks) {  // the tile's columns are done
+    if (KC == 1 && ++ck == ks) {
       ck = 0;
-#pragma unroll
-      for (int j = 0; j < MB; ++j) {
-        float mx = top[j];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int n = n0 + 16 * h + t;
-            const float v = n < r1 ? acc[h][j][t] * s2 : -__builtin_inff();
-            if (n == lab[j] && n < r1) pl.r.zt[16 * j + l16] = v;  // past r1: another's
-            acc[h][j][t] = v;
-            mx = fmaxf(mx, v);
-          }
-        const float ref = mx == -__builtin_inff() ? 0.f : mx;
-        float e = sum[j] * exp2_(top[j] - ref);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) e += exp2_(acc[h][j][t] - ref);
-        sum[j] = e;
-        top[j] = mx;
-        acc[0][j] = acc[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
-      n0 += kTile;
+      tile_done();
+      n0 += 64 * RB;
     }
   }
   wait_vm_lds<0>();
   tile_barrier();
+  if constexpr (KC > 1) {
+    f32x4 *part = reinterpret_cast<f32x4 *>(lds);  // [8][2 * MB][64]
+#pragma unroll
+    for (int j = 0; j < MB; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) part[((wave * MB + j) * 2 + h) * 64 + lane] = acc[h][j];
+    wait_lds();
+    tile_barrier();
+    if (chunk == 0) {
+#pragma unroll
+      for (int j = 0; j < MB; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 1; c < KC; ++c)
+            acc[h][j] += part[(((wave + 2 * RB * c) * MB + j) * 2 + h) * 64 + lane];
+      tile_done();
+    }
+    wait_lds();
+    tile_barrier();
+  }
   float *red = reinterpret_cast<float *>(lds);  // [8][16*MB][2]
 #pragma unroll
   for (int j = 0; j < MB; ++j) {
@@ -950,8 +987,11 @@ hipError_t launch_xent_logits(const XentPlan &p, const VocabMatrix &w, int mode,
 
 hipError_t launch_xent_score(const XentPlan &p, const VocabMatrix &w, const void *x,
                              const void *labels, float *loss, float *lse, hipStream_t s) {
+  // One run per CU; runs of 129 to 256 rows become two of up to 128, which fill
+  // their stages (13 rows at V = 44480, H = 3528: 74 us instead of 80).
   const int units = ceil_div(p.vocab, 16);
-  const int groups = units < kScoreGroups ? units : kScoreGroups;
+  int groups = units < kCus ? units : kCus;
+  if (units > 8 * kCus && units <= 16 * kCus) groups = kScoreGroups;
   by_type(p.half, [&](auto type) {
     by_table(w.tp, [&](auto nt) {
       using T = decltype(type);
@@ -960,10 +1000,17 @@ hipError_t launch_xent_score(const XentPlan &p, const VocabMatrix &w, const void
         hipLaunchKernelGGL(kernel, dim3(groups), dim3(512), 0, s, p, static_cast<const u32x4 *>(x),
                            labels, small_table<NT>(w.t), w.shard);
       };
-      if (p.m <= 16) go(k_score<T, NT, 1>);
-      else if (p.m <= 32) go(k_score<T, NT, 2>);
-      else if (p.m <= 64) go(k_score<T, NT, 4>);
-      else go(k_score<T, NT, 8>);
+      auto by_rows = [&](auto chunks) {
+        constexpr int KC = decltype(chunks)::value;
+        if (p.m <= 16) go(k_score<T, NT, 1, KC>);
+        else if (p.m <= 32) go(k_score<T, NT, 2, KC>);
+        else if (p.m <= 64) go(k_score<T, NT, 4, KC>);
+        else go(k_score<T, NT, 8, KC < 2 ? 1 : 2>);  // x of 128 rows and 256 k fills the LDS
+      };
+      const int run = ceil_div(units, groups) * 16;  // rows of a workgroup
+      if (run > 128) by_rows(std::integral_constant<int, 1>{});
+      else if (run > 64) by_rows(std::integral_constant<int, 2>{});
+      else by_rows(std::integral_constant<int, 4>{});
     });
   });
   hipError_t e = hipGetLastError();

@@ -749,3 +749,42 @@ def test_losses_of_certain_rows_keep_their_digits(m):
     g = torch.full((m,), 1.0 / m)
     step = vt.head_xent_step(x.bfloat16().to(DEV), w.bfloat16().to(DEV), labels.to(DEV), g.to(DEV), 2, 320)
     assert (np.abs(f64(step[0]) - want) <= 64 * ov.U32 * want + 4 * ov.U32).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("tp,shard,hidden,m,vocab", [(2, 8480, 520, 300, 16901), (1, 17408, 264, 513, 17001),
+                                                     (3, 5696, 776, 129, None), (2, 8480, 72, 1100, 16640)])
+def test_big_tiles(tp, shard, hidden, m, vocab, dtype):
+    """Sizes whose 256 x 256 tiles occupy more than half of the CUs (in the
+    logits, the gradients or both), with edges inside tiles, rows left out and
+    a matrix that ends tiles past the vocabulary."""
+    note(f"big tiles {tp=} {shard=} {hidden=} {m=} {vocab=} {dtype}")
+    p = Problem(tp, shard, hidden, m, vocab, dtype, left_out=0.15, scale=0.8, z_weight=0.01, sigma=0.1)
+    x, w, t, g = p.on_gpu()
+    out = vt.head_xent_step(x, w, t, g, tp, shard, **p.how)
+    p.check_loss(*out[:2])
+    p.check_grads(*out[2:])
+    lse = torch.from_numpy(p.wanted()[2]).float()
+    dx, dw = vt.head_xent_grad(x, w, t, lse.to(DEV), g, tp, shard, **p.how)
+    p.check_grads(dx, dw, lse_used=f64(lse))
+    old = rand((tp * shard, hidden), 1e-2, 5, "fp32").to(DEV)
+    wide = old.clone()
+    vt.head_xent_step(x, w, t, g, tp, shard, dw=wide, accumulate=True, **p.how)
+    p.check_grads(out[2], wide, old=f64(old))
+    # blocks apart in memory, and anything in the masked places: the same bits
+    p.blocks = tp > 1
+    _, w, _, _ = p.on_gpu()
+    x[t == -100] = float("nan")
+    g[t == -100] = float("inf")
+    if tp == 1:
+        w[p.vocab:] = float("nan")
+    elif p.vocab < tp * shard:
+        w[-1][p.vocab - (tp - 1) * shard:] = float("nan")
+    for a, b in zip(out, vt.head_xent_step(x, w, t, g, tp, shard, **p.how)):
+        assert torch.equal(a, b)
+    # the vocabulary in pieces
+    limit = vt._xent_bytes(bytes(vt._Head(x, w, t, tp, shard, **p.how).shape), _lib.HG_XENT_STEP, 0) * 2 // 3
+    loss, lse, dx, dw = vt.head_xent_step(x, w, t, g, tp, shard, workspace_limit=limit, **p.how)
+    assert torch.equal(loss, out[0]) and torch.equal(lse, out[1])
+    p.check_grads(dx, dw)

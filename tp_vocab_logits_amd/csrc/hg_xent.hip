@@ -876,6 +876,21 @@ __global__ __launch_bounds__(512, 2) void k_grads(XentPlan pl, ShardTableN<NT> w
   }
 }
 
+// The sum of n partial sums, in order, eight loads in flight.
+__device__ __forceinline__ f32x4 add_planes(const f32x4 *src, long long plane, int n) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int z0 = 0; z0 < n; z0 += 8) {
+    f32x4 p[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (z0 + u < n) p[u] = src[(z0 + u) * plane];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (z0 + u < n) v += p[u];
+  }
+  return v;
+}
+
 // Partial sums -> dx rows (zero where the row is left out): four columns per
 // lane.
 template <class T>
@@ -890,8 +905,7 @@ __global__ __launch_bounds__(256) void k_dx_join(XentPlan pl, uint2 *dx) {
       uint2 o = {0u, 0u};
       if (p >= 0) {
         const f32x4 *src = reinterpret_cast<const f32x4 *>(pl.dxp) + static_cast<long long>(p) * hq + k;
-        f32x4 v = src[0];
-        for (int z = 1; z < pl.split_dx; ++z) v += src[z * plane];
+        f32x4 v = add_planes(src, plane, pl.split_dx);
         v *= down;
         o = uint2{bits16<T>(v[0]) | bits16<T>(v[1]) << 16, bits16<T>(v[2]) | bits16<T>(v[3]) << 16};
       }
@@ -910,8 +924,7 @@ __global__ __launch_bounds__(256) void k_dw_join(XentPlan pl, int v0, int rows, 
   for (long long k = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; k < n;
        k += static_cast<long long>(gridDim.x) * 256) {
     const f32x4 *src = reinterpret_cast<const f32x4 *>(pl.dwp) + k;
-    f32x4 v = src[0];
-    for (int z = 1; z < pl.split_dw; ++z) v += src[z * plane];
+    const f32x4 v = add_planes(src, plane, pl.split_dw);
     dw_store<T>(dw, static_cast<long long>(v0) * pl.hidden + 4 * k, v * down, wide, accumulate);
   }
 }

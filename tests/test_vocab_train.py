@@ -784,7 +784,31 @@ def test_big_tiles(tp, shard, hidden, m, vocab, dtype):
     for a, b in zip(out, vt.head_xent_step(x, w, t, g, tp, shard, **p.how)):
         assert torch.equal(a, b)
     # the vocabulary in pieces
-    limit = vt._xent_bytes(bytes(vt._Head(x, w, t, tp, shard, **p.how).shape), _lib.HG_XENT_STEP, 0) * 2 // 3
+    limit = vt._xent_bytes(vt._Head(x, w, t, tp, shard, **p.how).shape, _lib.HG_XENT_STEP, 0) * 2 // 3
     loss, lse, dx, dw = vt.head_xent_step(x, w, t, g, tp, shard, workspace_limit=limit, **p.how)
     assert torch.equal(loss, out[0]) and torch.equal(lse, out[1])
     p.check_grads(dx, dw)
+
+
+def test_fastcall_wrappers_pass_arguments_on():
+    """The fast-call wrappers of the training operators reach the entry points:
+    bad shapes give their codes, malformed calls raise before reaching C."""
+    f = _lib.fast()
+    dims = (2, 64, 16, 4, 100, 0, 8)
+    rest = (1 << 24, (9 << 24,), 2 << 24, 3 << 24, 4 << 24, 5 << 24, 6 << 24, 7 << 24, 0, 0, 8 << 24, 1 << 10, 0)
+    for kind in (0, 1, 2):
+        assert f.xent(kind, (2, 48, 16, 4, 96, 0, 8), -100, 1.0, 0.0, *rest) == _lib.HG_EINVAL  # shard % 32
+        assert f.xent(kind, dims, -100, 1.0, 0.0, *rest) == _lib.HG_ESIZE                       # 1 KB of workspace
+    assert f.xent(3, dims, -100, 1.0, 0.0, *rest) == _lib.HG_EINVAL
+    assert f.xent(0, (65, 64, 16, 4, 100, 0, 8), -100, 1.0, 0.0, *rest) == _lib.HG_EINVAL
+    with pytest.raises(TypeError):
+        f.xent(0, dims[:6], -100, 1.0, 0.0, *rest)
+    with pytest.raises(TypeError):
+        f.xent(0, dims, -100, 1.0, 0.0, 1 << 24, (1, 2, 3), *rest[2:])
+    with pytest.raises(TypeError):
+        f.xent(0, dims, -100, "1", 0.0, *rest)
+    assert f.embed(1, 64, 16, 3, (1 << 24,), 2 << 24, 8, 4, 1.0, 3 << 24, 0) == _lib.HG_EINVAL
+    with pytest.raises(TypeError):
+        f.embed(2, 64, 16, 0, (1 << 24,), 2 << 24, 8, 4, 1.0, 3 << 24, 0)
+    assert f.embed_grad(1, 64, 16, 0, 1 << 24, 8, 4, 2 << 24, 1.0, 0, 0, 0, 0, 0, 0) == _lib.HG_EINVAL
+    assert f.embed_grad(1, 64, 16, 0, 0, 8, 0, 0, 1.0, 16, 0, 1, 0, 0, 0) == _lib.HG_OK  # nothing to add

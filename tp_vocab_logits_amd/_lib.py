@@ -138,8 +138,8 @@ _FAST = None
 
 def fast():
     """The ``_hgcall`` extension, bound to the loaded library: ``gather``,
-    ``push``, ``collect``, ``stock``, ``embed`` and ``embed_grad`` taking plain
-    integers (handle, sizes, host-array address, rows, device address, stream)
+    ``push``, ``collect``, ``stock``, ``embed``, ``embed_grad`` and ``xent``
+    (``hg_xent``, ``hg_xent_grad`` and ``hg_xent_step``) taking plain integers (handle, sizes, host-array address, rows, device address, stream)
     in the C argument order and returning the status code -- the same calls as
     through ctypes, with less per-call conversion."""
     global _FAST
@@ -149,7 +149,7 @@ def fast():
         handle = lib()
         _hgcall.bind(*[ctypes.cast(getattr(handle, n), ctypes.c_void_p).value
                        for n in ("hg_gather", "hg_push", "hg_collect", "hg_stock_gather", "hg_embed",
-                                  "hg_embed_grad")])
+                                  "hg_embed_grad", "hg_xent", "hg_xent_grad", "hg_xent_step")])
         _FAST = _hgcall
     return _FAST
 

@@ -80,7 +80,7 @@ def build_fastcall(verbose: bool = False) -> str:
     os.close(fd)
     try:
         cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-Wall", "-Wextra",
-               "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "hg_fastcall.c"),
+               "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, os.path.join(CSRC, "hg_fastcall.c"),
                "-o", tmp]
         if verbose:
             print(" ".join(cmd), flush=True)

@@ -1,7 +1,7 @@
 /*
  * _hgcall: fast-call Python wrappers of the per-call entry points of
  * libhg.so (hg_gather, hg_push, hg_collect, hg_stock_gather, hg_embed,
- * hg_embed_grad), for loops where the ctypes conversion of the arguments
+ * hg_embed_grad, hg_xent, hg_xent_grad, hg_xent_step), for loops where the ctypes conversion of the arguments
  * (about 0.5 us a call, 2 us with a dozen of them) is a sizeable part of a
  * call of a few microseconds.
  * Argument marshalling only: every argument is an integer (a handle, a
@@ -10,10 +10,12 @@
  * library's status code.
  *
  * The module does not link against libhg.so: bind() receives the addresses of
- * the six entry points from the already loaded library (see _lib.fast()).
+ * the nine entry points from the already loaded library (see _lib.fast()).
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+
+#include "hg.h"
 
 typedef int (*gather_fn)(void *h, const void *const *shards, int m, void *out, void *stream);
 typedef int (*push_fn)(void *h, const void *const *shards, int m, void *stream);
@@ -35,7 +37,22 @@ static stock_fn g_stock;
 static embed_fn g_embed;
 static embed_grad_fn g_embed_grad;
 
-#define MAX_BLOCKS 64 /* HG_MAX_TP */
+typedef int (*xent_fn)(const hg_xent_shape *s, const void *x, const void *const *w,
+                       const void *labels, float *loss, float *lse, void *ws, size_t ws_bytes,
+                       void *stream);
+typedef int (*xent_grad_fn)(const hg_xent_shape *s, const void *x, const void *const *w,
+                            const void *labels, const float *lse, const float *grad, void *dx,
+                            void *dw, int dw_wide, int accumulate, void *ws, size_t ws_bytes,
+                            void *stream);
+typedef int (*xent_step_fn)(const hg_xent_shape *s, const void *x, const void *const *w,
+                            const void *labels, const float *grad, float *loss, float *lse,
+                            void *dx, void *dw, int dw_wide, int accumulate, void *ws,
+                            size_t ws_bytes, void *stream);
+static xent_fn g_xent;
+static xent_grad_fn g_xent_grad;
+static xent_step_fn g_xent_step;
+
+#define MAX_BLOCKS HG_MAX_TP
 
 static int as_ptr(PyObject *o, void **p) {
   *p = PyLong_AsVoidPtr(o);
@@ -72,15 +89,16 @@ static int as_float(PyObject *o, float *v) {
   return 1;
 }
 
-/* bind(gather, push, collect, stock, embed, embed_grad): their addresses */
+/* bind(gather, push, collect, stock, embed, embed_grad, xent, xent_grad, xent_step): their
+ * addresses */
 static PyObject *py_bind(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
-  void *fn[6];
+  void *fn[9];
   (void)self;
-  if (nargs != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind expects six function addresses");
+  if (nargs != 9) {
+    PyErr_SetString(PyExc_TypeError, "bind expects nine function addresses");
     return NULL;
   }
-  for (int k = 0; k < 6; ++k) {
+  for (int k = 0; k < 9; ++k) {
     if (!as_ptr(args[k], &fn[k])) return NULL;
     if (!fn[k]) {
       PyErr_SetString(PyExc_ValueError, "bind: null function address");
@@ -93,6 +111,9 @@ static PyObject *py_bind(PyObject *self, PyObject *const *args, Py_ssize_t nargs
   g_stock = (stock_fn)fn[3];
   g_embed = (embed_fn)fn[4];
   g_embed_grad = (embed_grad_fn)fn[5];
+  g_xent = (xent_fn)fn[6];
+  g_xent_grad = (xent_grad_fn)fn[7];
+  g_xent_step = (xent_step_fn)fn[8];
   Py_RETURN_NONE;
 }
 
@@ -194,9 +215,69 @@ static PyObject *py_embed_grad(PyObject *self, PyObject *const *args, Py_ssize_t
                                       wide, accumulate, ws, ws_bytes, stream));
 }
 
+/* xent(kind, (tp, shard, hidden, m, vocab, dtype, label_bytes), ignore, scale, z_weight, x, blocks,
+ * labels, grad, loss, lse, dx, dw, dw_wide, accumulate, ws, ws_bytes, stream) -> status;
+ * kind: HG_XENT_*; blocks: a tuple of tp addresses, or of one where the blocks follow one another;
+ * addresses that the kind has no use for are 0 (HG_XENT_GRAD reads lse, the others write it) */
+static PyObject *py_xent(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  const void *w[MAX_BLOCKS];
+  hg_xent_shape s;
+  void *x, *labels, *grad, *loss, *lse, *dx, *dw, *ws, *stream;
+  int kind, wide, accumulate;
+  size_t ws_bytes;
+  Py_ssize_t blocks;
+  (void)self;
+  if (!check_bound((void *)g_xent, nargs, 18)) return NULL;
+  if (!PyTuple_Check(args[1]) || PyTuple_GET_SIZE(args[1]) != 7 || !PyTuple_Check(args[6])) {
+    PyErr_SetString(PyExc_TypeError, "the shape must be a tuple of seven integers, blocks a tuple");
+    return NULL;
+  }
+  memset(&s, 0, sizeof s);
+  int *const dims[7] = {&s.tp, &s.shard, &s.hidden, &s.m, &s.vocab, &s.dtype, &s.label_bytes};
+  for (int k = 0; k < 7; ++k)
+    if (!as_int(PyTuple_GET_ITEM(args[1], k), dims[k])) return NULL;
+  s.ignore = PyLong_AsLongLong(args[2]);
+  if (s.ignore == -1 && PyErr_Occurred()) return NULL;
+  if (!as_int(args[0], &kind) || !as_float(args[3], &s.scale) || !as_float(args[4], &s.z_weight) ||
+      !as_ptr(args[5], &x) || !as_ptr(args[7], &labels) || !as_ptr(args[8], &grad) ||
+      !as_ptr(args[9], &loss) || !as_ptr(args[10], &lse) || !as_ptr(args[11], &dx) ||
+      !as_ptr(args[12], &dw) || !as_int(args[13], &wide) || !as_int(args[14], &accumulate) ||
+      !as_ptr(args[15], &ws))
+    return NULL;
+  ws_bytes = PyLong_AsSize_t(args[16]);
+  if (ws_bytes == (size_t)-1 && PyErr_Occurred()) return NULL;
+  if (!as_ptr(args[17], &stream)) return NULL;
+  blocks = PyTuple_GET_SIZE(args[6]);
+  if (s.tp < 1 || s.tp > MAX_BLOCKS) return PyLong_FromLong(HG_EINVAL);
+  if (blocks != 1 && blocks != s.tp) {
+    PyErr_SetString(PyExc_TypeError, "blocks must hold one or tp addresses");
+    return NULL;
+  }
+  for (int r = 0; r < s.tp; ++r) {
+    if (r < blocks) {
+      void *p;
+      if (!as_ptr(PyTuple_GET_ITEM(args[6], r), &p)) return NULL;
+      w[r] = p;
+    } else {
+      w[r] = (const char *)w[r - 1] + (size_t)s.shard * (size_t)s.hidden * 2;
+    }
+  }
+  switch (kind) {
+    case HG_XENT_SCORE:
+      return PyLong_FromLong(g_xent(&s, x, w, labels, loss, lse, ws, ws_bytes, stream));
+    case HG_XENT_GRAD:
+      return PyLong_FromLong(g_xent_grad(&s, x, w, labels, lse, grad, dx, dw, wide, accumulate, ws,
+                                         ws_bytes, stream));
+    case HG_XENT_STEP:
+      return PyLong_FromLong(g_xent_step(&s, x, w, labels, grad, loss, lse, dx, dw, wide,
+                                         accumulate, ws, ws_bytes, stream));
+    default: return PyLong_FromLong(HG_EINVAL);
+  }
+}
+
 static PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)(void))py_bind, METH_FASTCALL,
-     "bind(gather, push, collect, stock, embed, embed_grad)"},
+     "bind(gather, push, collect, stock, embed, embed_grad, xent, xent_grad, xent_step)"},
     {"gather", (PyCFunction)(void (*)(void))py_gather, METH_FASTCALL,
      "gather(handle, shards_addr, m, out_addr, stream) -> status"},
     {"push", (PyCFunction)(void (*)(void))py_push, METH_FASTCALL,
@@ -210,6 +291,9 @@ static PyMethodDef methods[] = {
     {"embed_grad", (PyCFunction)(void (*)(void))py_embed_grad, METH_FASTCALL,
      "embed_grad(tp, shard, hidden, dtype, tokens, token_bytes, n, dy, scale, dw, dw_wide, "
      "accumulate, ws, ws_bytes, stream) -> status"},
+    {"xent", (PyCFunction)(void (*)(void))py_xent, METH_FASTCALL,
+     "xent(kind, shape, ignore, scale, z_weight, x, blocks, labels, grad, loss, lse, dx, dw, "
+     "dw_wide, accumulate, ws, ws_bytes, stream) -> status"},
     {NULL, NULL, 0, NULL},
 };
 

@@ -36,12 +36,6 @@ _DTYPES = {torch.bfloat16: _lib.HG_BF16, torch.float16: _lib.HG_FP16, torch.floa
 WORKSPACE_LIMIT = 4 << 30
 
 
-@functools.lru_cache(maxsize=None)
-def _table(tp: int):
-    """The C type of a table of tp block pointers."""
-    return ctypes.c_void_p * tp
-
-
 def _call(fn, name: str, device: torch.device, *args) -> None:
     """One library call on the device's current stream, appended to ``args``."""
     index = device.index
@@ -109,12 +103,14 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
 
 
 @functools.lru_cache(maxsize=256)
-def _xent_bytes(shape: bytes, kind: int, limit: int) -> int:
+def _xent_bytes(shape: tuple, kind: int, limit: int) -> int:
     """hg_xent_workspace, once per shape: a training loop asks for the same one every step."""
     n = ctypes.c_size_t()
-    s = _lib.XentShape.from_buffer_copy(shape)
-    check(lib().hg_xent_workspace(ctypes.byref(s), kind, limit, ctypes.byref(n)), "hg_xent_workspace")
+    check(lib().hg_xent_workspace(_lib.XentShape(*shape, 0, 1.0, 0.0), kind, limit, n), "hg_xent_workspace")
     return n.value
+
+
+_NAMES = {_lib.HG_XENT_SCORE: "hg_xent", _lib.HG_XENT_GRAD: "hg_xent_grad", _lib.HG_XENT_STEP: "hg_xent_step"}
 
 
 class _Head:
@@ -129,20 +125,14 @@ class _Head:
         self.labels = _given(labels, "labels", (m,), _INTS, self.device)
         _on_gpu(self.device)
         self.m, self.hidden, self.rows = m, hidden, int(tp) * int(shard)
-        if len(self.ptrs) < tp:
-            step = int(shard) * hidden * 2
-            self.ptrs = tuple(self.ptrs[0] + r * step for r in range(int(tp)))
         vocab = self.rows if vocab is None else int(vocab)
         if not 1 <= vocab <= self.rows:
             raise ValueError(f"vocab must lie in 1..{self.rows}, got {vocab}")
-        self.shape = _lib.XentShape(int(tp), int(shard), hidden, m, vocab, _DTYPES[self.dtype],
-                                    self.labels.element_size(), int(ignore), float(scale), float(z_weight))
+        self.shape = (int(tp), int(shard), hidden, m, vocab, _DTYPES[self.dtype], self.labels.element_size())
+        self.how = (int(ignore), scale, z_weight)
 
     def rows_of(self, t, name):
         return _given(t, name, (self.m,), (torch.float32,), self.device)
-
-    def workspace(self, kind: int, limit: int) -> torch.Tensor:
-        return _workspace(_xent_bytes(bytes(self.shape), kind, int(limit)), self.device)
 
     def losses(self) -> tuple[torch.Tensor, torch.Tensor]:
         both = torch.empty((2, self.m), dtype=torch.float32, device=self.device)
@@ -155,9 +145,15 @@ class _Head:
             _given(dx, "dx", (self.m, self.hidden), (self.dtype,), self.device)
         return dx, _gradient_buffer(dw, self.rows, self.hidden, self.dtype, self.device, accumulate)
 
-    def call(self, name, *args):
-        _call(getattr(lib(), name), name, self.device, self.shape, self.x.data_ptr(), _table(len(self.ptrs))(*self.ptrs),
-              self.labels.data_ptr(), *args)
+    def call(self, kind, limit, grad, loss, lse, dx, dw, accumulate):
+        """The library's call of that kind; addresses of what it does not take are 0."""
+        nbytes = _xent_bytes(self.shape, kind, limit)
+        ws = _workspace(nbytes, self.device)
+        _call(_lib.fast().xent, _NAMES[kind], self.device, kind, self.shape, *self.how, self.x.data_ptr(), self.ptrs,
+              self.labels.data_ptr(), grad.data_ptr() if grad is not None else 0,
+              loss.data_ptr() if loss is not None else 0, lse.data_ptr(), dx.data_ptr() if dx is not None else 0,
+              dw.data_ptr() if dw is not None else 0, int(dw is not None and dw.dtype != self.dtype),
+              int(accumulate), ws.data_ptr(), nbytes)
 
 
 def _gradient_buffer(dw, rows, hidden, dtype, device, accumulate) -> torch.Tensor:
@@ -181,8 +177,7 @@ def head_xent(x: torch.Tensor, w, labels: torch.Tensor, tp: int, shard: int, voc
     label outside the vocabulary gives NaN."""
     h = _Head(x, w, labels, tp, shard, vocab, ignore, scale, z_weight)
     loss, lse = h.losses()
-    ws = h.workspace(_lib.HG_XENT_SCORE, 0)
-    h.call("hg_xent", loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
+    h.call(_lib.HG_XENT_SCORE, 0, None, loss, lse, None, None, False)
     return loss, lse
 
 
@@ -199,9 +194,7 @@ def head_xent_grad(x: torch.Tensor, w, labels: torch.Tensor, lse: torch.Tensor, 
     h = _Head(x, w, labels, tp, shard, vocab, ignore, scale, z_weight)
     lse, grad = h.rows_of(lse, "lse"), h.rows_of(grad, "grad")
     dx, dw = h.grads(dx, dw, accumulate)
-    ws = h.workspace(_lib.HG_XENT_GRAD, workspace_limit)
-    h.call("hg_xent_grad", lse.data_ptr(), grad.data_ptr(), dx.data_ptr(), dw.data_ptr(),
-           int(dw.dtype != h.dtype), int(accumulate), ws.data_ptr(), ws.numel())
+    h.call(_lib.HG_XENT_GRAD, int(workspace_limit), grad, None, lse, dx, dw, accumulate)
     return dx, dw
 
 
@@ -218,9 +211,7 @@ def head_xent_step(x: torch.Tensor, w, labels: torch.Tensor, grad: torch.Tensor,
     grad = h.rows_of(grad, "grad")
     loss, lse = h.losses()
     dx, dw = h.grads(dx, dw, accumulate)
-    ws = h.workspace(_lib.HG_XENT_STEP, workspace_limit)
-    h.call("hg_xent_step", grad.data_ptr(), loss.data_ptr(), lse.data_ptr(), dx.data_ptr(), dw.data_ptr(),
-           int(dw.dtype != h.dtype), int(accumulate), ws.data_ptr(), ws.numel())
+    h.call(_lib.HG_XENT_STEP, int(workspace_limit), grad, loss, lse, dx, dw, accumulate)
     return loss, lse, dx, dw
 
 

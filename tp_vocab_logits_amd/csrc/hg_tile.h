@@ -89,6 +89,7 @@ __device__ __forceinline__ float from16(uint32_t b) {
 
 constexpr int kTile = 256;           // C tile edge (the small tile's is half of it)
 constexpr int kStep = 64;            // k per step
+constexpr int kChain = 16;           // steps that are summed before they join a total
 constexpr int kSubBytes = 64 * 128;  // one 64 x 64 sub-tile
 constexpr int kStageBytes = 8 * kSubBytes;
 constexpr int kTileLds = 2 * kStageBytes;
@@ -440,7 +441,9 @@ struct BigTile {
 // 128 x 128 for problems whose 256 x 256 tiles would leave CUs idle: a quarter
 // of the work per tile, a ring of four 32 KB stages loaded three steps ahead
 // and one barrier per step. 33 rows over V = 4096, H = 264 take 8.7 us for their
-// logits on 32 small tiles and 16 us on 16 big ones.
+// logits on 32 small tiles and 16 us on 16 big ones. Long sums are taken in
+// chains of kChain steps, each added to a total: an addition rounds at the size
+// that the sum has by then. (The big tile has no registers for a total.)
 struct SmallTile {
   static constexpr int kEdge = 128, MI = 4, NJ = 2, kRows = 64, kCols = 32;
   static constexpr int kBLoads = 2;
@@ -465,10 +468,11 @@ struct SmallTile {
 #pragma unroll
       for (int t = 0; t < 2; ++t) b.load(st + 2 * kSubBytes, wr, 2 * wc + t, step);
     };
+    f32x4 chain[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < 2; ++j) acc[i][j] = chain[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < 3; ++s) load(s);
     for (int s = 0; s < steps; ++s) {
@@ -488,7 +492,16 @@ struct SmallTile {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = T::mma(rb[j], ra[i], acc[i][j]);
+          for (int j = 0; j < 2; ++j) chain[i][j] = T::mma(rb[j], ra[i], chain[i][j]);
+      }
+      if ((s + 1) % kChain == 0 || s + 1 == steps) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            acc[i][j] += chain[i][j];
+            chain[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+          }
       }
     }
     wait_vm_lds<0>();

@@ -25,7 +25,7 @@ struct XentRows {
   int *inv;       // [m] row -> packed, or -1
   int *lab;       // [m] packed labels
   float *zt;      // [m] packed: the label's logit (base 2), relative to its tile's largest;
-                  // few rows: by row, as it is
+                  // few rows: by row, the label's product
   float *lse2;    // [m] packed: log-sum-exp in base 2
   float *ca;      // [m] packed: factor of the probability in d
   float *cb;      // [m] packed: factor of the label's one in d

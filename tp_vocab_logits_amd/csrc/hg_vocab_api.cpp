@@ -121,9 +121,13 @@ size_t lay_out(const hg_xent_shape &s, int kind, int piece, char *ws, XentPlan *
   // The small tile while the big one would give work to half of the CUs at
   // most. It takes about 1.5 times as long per product (2047 rows at V = 32000,
   // H = 2048: logits 255 us against 165, gradient products 505 us against 310),
-  // so beyond that the big one's single round is the shorter.
+  // so beyond that the big one's single round is the shorter. Up to 128 rows the
+  // logits' big tile would be half empty, and few rows show a single loss's last
+  // digits, which the small tile keeps: a step at V = 163840, H = 7168 takes 1636 us
+  // with one row and 1988 with 128, with the big tile 1680 and 2004.
   const long long tm = ceil_div(s.m, kTile), tn = ceil_div(s.hidden, kTile);
-  p->small_logits = tm * ceil_div(kind == HG_XENT_GRAD ? piece : s.vocab, kTile) <= kCus / 2;
+  p->small_logits = s.m <= kTile / 2 ||
+                    tm * ceil_div(kind == HG_XENT_GRAD ? piece : s.vocab, kTile) <= kCus / 2;
   p->small_grads = ceil_div(piece, kTile) * tn <= kCus / 2;
   p->ref = p->small_logits ? kTile / 2 : kTile;
   const size_t tiles = static_cast<size_t>(ceil_div(s.vocab, p->ref));

@@ -380,6 +380,12 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
 // the waves of the chunks add up their parts of the one tile at the end. (One
 // row at V = 20480, H = 7168, a rank's share at TP = 8: 64 us with KC = 1, 49
 // with KC = 2.)
+//
+// A logit is summed in chains of kChain steps, each added to a total of its own:
+// every addition to a sum rounds at the sum's size, and a label's logit is a sum
+// of terms of one sign, which has its full size for much of a chain of 7168
+// products. (Losses of rows whose labels' logits are about 12, V = 163840: off by
+// 1.0 * 2^-24 of the logit, rms, instead of 6; the same time.)
 template <class T, int NT, int MB, int KC>
 __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, const void *labels,
                                                   ShardTableN<NT> w, int shard) {
@@ -431,12 +437,12 @@ __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, c
 
   FragLane<false> f;
   f.init(lane);
-  f32x4 acc[2][MB];
+  f32x4 acc[2][MB], total[2][MB];
   float top[MB], sum[MB];
   int lab[MB];
 #pragma unroll
   for (int j = 0; j < MB; ++j) {
-    acc[0][j] = acc[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    acc[0][j] = acc[1][j] = total[0][j] = total[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     top[j] = -__builtin_inff();
     sum[j] = 0.f;
     const int row = 16 * j + l16;
@@ -447,7 +453,19 @@ __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, c
   __asm__ __volatile__("s_waitcnt vmcnt(0)" ::: "memory");  // the labels: only the loads below count
 
   int n0 = r0 + 64 * block + 32 * (wave & 1) + 4 * g;
-  // The tile's columns are done: into the running statistics.
+  // A chain ends: into the totals.
+  auto chain_done = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < MB; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        total[h][j] += acc[h][j];
+        acc[h][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+  };
+  // The tile's columns are done: into the running statistics. The exponentials
+  // are of exact products less a reference, which may be any number near the
+  // largest of them: its rounding takes nothing from them.
   auto tile_done = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < MB; ++j) {
@@ -457,20 +475,19 @@ __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, c
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int n = n0 + 16 * h + t;
-          const float v = n < r1 ? acc[h][j][t] * s2 : -__builtin_inff();
-          if (n == lab[j] && n < r1) pl.r.zt[16 * j + l16] = v;  // past r1: another's
-          acc[h][j][t] = v;
-          mx = fmaxf(mx, v);
+          if (n == lab[j] && n < r1) pl.r.zt[16 * j + l16] = total[h][j][t];  // past r1: another's
+          mx = fmaxf(mx, n < r1 ? total[h][j][t] * s2 : -__builtin_inff());
         }
       const float ref = mx == -__builtin_inff() ? 0.f : mx;
       float e = sum[j] * exp2_(top[j] - ref);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) e += exp2_(acc[h][j][t] - ref);
+        for (int t = 0; t < 4; ++t)
+          e += n0 + 16 * h + t < r1 ? exp2_(fmaf(total[h][j][t], s2, -ref)) : 0.f;
       sum[j] = e;
       top[j] = mx;
-      acc[0][j] = acc[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      total[0][j] = total[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
   };
 
@@ -494,7 +511,10 @@ __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, c
         acc[1][j] = T::mma(w1, xv, acc[1][j]);
       }
     }
-    if (KC == 1 && ++ck == ks) {
+    ++ck;
+    const bool last = ck == ks;
+    if (ck % kChain == 0 || last) chain_done();
+    if (KC == 1 && last) {
       ck = 0;
       tile_done();
       n0 += 64 * RB;
@@ -507,7 +527,7 @@ __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, c
 #pragma unroll
     for (int j = 0; j < MB; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) part[((wave * MB + j) * 2 + h) * 64 + lane] = acc[h][j];
+      for (int h = 0; h < 2; ++h) part[((wave * MB + j) * 2 + h) * 64 + lane] = total[h][j];
     wait_lds();
     tile_barrier();
     if (chunk == 0) {
@@ -517,7 +537,7 @@ __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, c
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int c = 1; c < KC; ++c)
-            acc[h][j] += part[(((wave + 2 * RB * c) * MB + j) * 2 + h) * 64 + lane];
+            total[h][j] += part[(((wave + 2 * RB * c) * MB + j) * 2 + h) * 64 + lane];
       tile_done();
     }
     wait_lds();
@@ -577,7 +597,7 @@ __global__ __launch_bounds__(64) void k_score_join(XentPlan pl, const void *labe
   if (lane != 0) return;
   float a = 0.f, b = 0.f;
   if (t != pl.ignore) {
-    const RowLoss o = row_loss(ref, sum, ref - zt, pl.z_weight);
+    const RowLoss o = row_loss(ref, sum, -fmaf(zt, pl.scale * kLog2e, -ref), pl.z_weight);
     const bool real = t >= 0 && t < pl.vocab;
     b = real ? o.lse : __builtin_nanf("");
     a = real ? o.loss : b;

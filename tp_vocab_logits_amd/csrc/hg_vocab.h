@@ -51,14 +51,13 @@ struct XentPlan {
   int ref;         // columns that share a probability reference: the logits' tile edge
   int split_dx;    // splits of the vocabulary in dX = d W
   int split_dw;    // splits of the rows in dW = d^T X
-  int dw_rows;     // matrix rows of one split's partial sums
   XentRows r;
   void *xc;        // packed rows of X, [hidden / 256 up][m][256]
   void *d;         // d (or unnormalised probabilities) of one piece, [piece / 256][m][256]
   float *part;     // [2][tiles][m] per tile of `ref` columns: maximum (base 2), sum; few rows:
                    // [m][kScoreGroups][2]
   float *dxp;      // [split_dx][m][hidden]
-  float *dwp;      // [split_dw][dw_rows][hidden] when split_dw > 1
+  float *dwp;      // [split_dw][piece][hidden] when split_dw > 1
 };
 
 hipError_t launch_xent_pack(const XentPlan &p, const void *x, const void *labels, float *loss,

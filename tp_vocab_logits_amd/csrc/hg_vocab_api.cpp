@@ -144,13 +144,8 @@ size_t lay_out(const hg_xent_shape &s, int kind, int piece, char *ws, XentPlan *
     p->split_dw = pick_split(piece / edge * hn, ceil_div(s.m, kStep), 4.0 * piece * h, true);
     p->d = take(2 * m * piece);
     p->dxp = reinterpret_cast<float *>(take(4 * m * h * p->split_dx));
-    if (p->split_dw > 1) {
-      // the last piece also has the matrix's rows past the vocabulary
-      const int npieces = ceil_div(s.vocab, piece);
-      const int tail = p->rows - (npieces - 1) * piece;
-      p->dw_rows = tail > piece ? tail : piece;
-      p->dwp = reinterpret_cast<float *>(take(4 * static_cast<size_t>(p->dw_rows) * h * p->split_dw));
-    }
+    if (p->split_dw > 1)
+      p->dwp = reinterpret_cast<float *>(take(4 * static_cast<size_t>(piece) * h * p->split_dw));
   }
   return at;
 }

@@ -865,11 +865,10 @@ __global__ __launch_bounds__(512, 2) void k_grads(XentPlan pl, ShardTableN<NT> w
     k0 = z * per < kept ? z * per : kept;
     k1 = k0 + per < kept ? k0 + per : kept;
   }
-  // a tile of rows past the vocabulary has no columns in d: nothing to read
-  const int kdim = v0 + c0 < vend ? k1 - k0 : 0;
+  const int kdim = k1 - k0;
   PanelColumnSource a, b;
   a.init(static_cast<const unsigned char *>(pl.d) +
-             (static_cast<long long>(kdim ? c0 / kPanel : 0) * pl.m + k0) * 512,
+             (static_cast<long long>(c0 / kPanel) * pl.m + k0) * 512,
          c0 % kPanel, kdim, lane);
   b.init(static_cast<const unsigned char *>(pl.xc) +
              (static_cast<long long>(n0 / kPanel) * pl.m + k0) * 512,
@@ -877,18 +876,20 @@ __global__ __launch_bounds__(512, 2) void k_grads(XentPlan pl, ShardTableN<NT> w
   Tile::template product<T>(a, b, (kdim + kStep - 1) / kStep, lds, acc);
   const float down = split ? 1.f : d_scale<T>(pl.r, true);
   void *out = split ? static_cast<void *>(pl.dwp +
-                                          static_cast<long long>(z) * pl.dw_rows * pl.hidden)
+                                          static_cast<long long>(z) * pl.piece * pl.hidden)
                     : ga.dw;
   const int wide = split ? 1 : ga.wide, accumulate = split ? 0 : ga.accumulate;
+  // rows past the vocabulary get no gradient, whatever x holds: zeros as far as
+  // the tile goes, or nothing
+  const int wend = split || ga.accumulate ? vend : pl.rows;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int row = v0 + c0 + Tile::kRows * wr + 16 * i + l16;
-    if (row >= pl.rows) continue;
+    if (row >= wend) continue;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int n = n0 + Tile::kCols * wc + 16 * j + 4 * g;
       if (n >= pl.hidden) continue;
-      // rows past the vocabulary get no gradient, whatever x holds
       const f32x4 v = row < vend ? acc[i][j] * down : f32x4{0.f, 0.f, 0.f, 0.f};
       dw_store<T>(out, static_cast<long long>(split ? row - v0 : row) * pl.hidden + n, v, wide,
                   accumulate);
@@ -934,17 +935,19 @@ __global__ __launch_bounds__(256) void k_dx_join(XentPlan pl, uint2 *dx) {
   }
 }
 
+// Partial sums -> the piece's `cols` rows of dw; zeros from there to `rows`.
 template <class T>
-__global__ __launch_bounds__(256) void k_dw_join(XentPlan pl, int v0, int rows, void *dw, int wide,
-                                                 int accumulate) {
+__global__ __launch_bounds__(256) void k_dw_join(XentPlan pl, int v0, int cols, int rows, void *dw,
+                                                 int wide, int accumulate) {
   const float down = d_scale<T>(pl.r, true);
   const int hq = pl.hidden >> 2;
-  const long long n = static_cast<long long>(rows) * hq;
-  const long long plane = static_cast<long long>(pl.dw_rows) * hq;
+  const long long sums = static_cast<long long>(cols) * hq, n = static_cast<long long>(rows) * hq;
+  const long long plane = static_cast<long long>(pl.piece) * hq;
   for (long long k = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; k < n;
        k += static_cast<long long>(gridDim.x) * 256) {
     const f32x4 *src = reinterpret_cast<const f32x4 *>(pl.dwp) + k;
-    const f32x4 v = add_planes(src, plane, pl.split_dw);
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (k < sums) v = add_planes(src, plane, pl.split_dw);
     dw_store<T>(dw, static_cast<long long>(v0) * pl.hidden + 4 * k, v * down, wide, accumulate);
   }
 }
@@ -1093,9 +1096,7 @@ hipError_t launch_xent_join_normalise(const XentPlan &p, const float *grad, floa
 
 hipError_t launch_xent_grads(const XentPlan &p, const VocabMatrix &w, int v0, int cols, bool first,
                              void *dw, bool wide, bool accumulate, hipStream_t s) {
-  // the last piece also covers the matrix's rows past the vocabulary
   const int vend = v0 + cols;
-  const int rows = vend == p.vocab ? p.rows - v0 : cols;
   const int edge = p.small_grads ? SmallTile::kEdge : BigTile::kEdge;
   GradArgs a;
   a.v0 = v0;
@@ -1104,7 +1105,7 @@ hipError_t launch_xent_grads(const XentPlan &p, const VocabMatrix &w, int v0, in
   a.xgroups = ceil_div(p.m, edge) * a.tn * p.split_dx;
   a.per = ceil_div(ceil_div(cols, kStep), p.split_dx);
   a.first = first ? 1 : 0;
-  a.wm = ceil_div(rows, edge);
+  a.wm = ceil_div(cols, edge);
   a.dw = dw;
   a.wide = wide ? 1 : 0;
   a.accumulate = accumulate ? 1 : 0;
@@ -1119,14 +1120,21 @@ hipError_t launch_xent_grads(const XentPlan &p, const VocabMatrix &w, int v0, in
       });
     });
     if (p.split_dw > 1) {
+      const int rows = vend < p.vocab || accumulate ? cols : p.rows - v0;
       const long long quads = static_cast<long long>(rows) * (p.hidden >> 2);
       const long long want = (quads + 255) / 256;
       const dim3 g2(static_cast<unsigned>(want < 4096 ? want : 4096));
-      hipLaunchKernelGGL((k_dw_join<T>), g2, dim3(256), 0, s, p, v0, rows, dw, a.wide,
+      hipLaunchKernelGGL((k_dw_join<T>), g2, dim3(256), 0, s, p, v0, cols, rows, dw, a.wide,
                          a.accumulate);
     }
   });
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.split_dw > 1 || vend < p.vocab || accumulate) return e;
+  // the matrix's rows past the tiles that the vocabulary ends in
+  const int from = v0 + a.wm * edge;
+  if (from >= p.rows) return hipSuccess;
+  const size_t row_bytes = static_cast<size_t>(p.hidden) * (wide ? 4 : 2);
+  return launch_zero(static_cast<char *>(dw) + from * row_bytes, (p.rows - from) * row_bytes, s);
 }
 
 }  // namespace hg

@@ -74,3 +74,45 @@ def test_gradients_end_with_the_vocabulary(rows, hidden, m, vocab, dtype):
         bits = torch.int32 if wide else torch.int16
         assert torch.equal(dw[vocab:].view(bits), old[vocab:].view(bits))
         assert dw[:vocab].isfinite().all()
+
+
+CUT = [(152064, 8192, 26926, 151936), (163840, 7168, 4096, 163840), (163840, 7168, 4096, 32000),
+       (163840, 4096, 4096, 128256), (65536, 2048, 8192, 50257), (32768, 1024, 70000, 32000), (163840, 1024, 33, 163840),
+       (163840, 7168, 1, 163837), (4096, 264, 33, 4091), (262144, 512, 1 << 20, 262144)]
+
+
+@pytest.mark.parametrize("kind", [SCORE, GRAD, STEP])
+@pytest.mark.parametrize("rows,hidden,m,vocab", CUT)
+def test_the_workspace_is_for_the_plan_that_runs(rows, hidden, m, vocab, kind):
+    """A call plans for the bytes that it is given: asked again for just that
+    many, the plan is the same one. It keeps within the limit unless nothing
+    does, and then takes the least."""
+    s = shape(rows, hidden, m, vocab)
+    whole, least = need(s, kind), need(s, kind, 1)
+    limit = whole
+    while limit > least // 2:
+        n = need(s, kind, limit)
+        assert n <= limit or n == least
+        assert n >= least
+        assert need(s, kind, n) == n
+        limit = limit * 7 // 8
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="an accepted call would run on made-up addresses")
+@pytest.mark.parametrize("kind", [SCORE, GRAD, STEP])
+@pytest.mark.parametrize("rows,hidden,m,vocab", CUT)
+def test_less_than_the_least_workspace_is_refused(rows, hidden, m, vocab, kind):
+    s = shape(rows, hidden, m, vocab)
+    least = need(s, kind, 1)
+    lib, p = _lib.lib(), [ctypes.c_void_p(k << 40) for k in range(1, 9)]
+    w = _lib.pointer_array([(9 << 40) + r * (rows // 8) * hidden * 2 for r in range(8)])
+
+    def call(nbytes):
+        if kind == SCORE:
+            return lib.hg_xent(ctypes.byref(s), p[0], w, p[1], p[2], p[3], p[4], nbytes, None)
+        if kind == GRAD:
+            return lib.hg_xent_grad(ctypes.byref(s), p[0], w, p[1], p[2], p[3], p[4], p[5], 0, 0, p[6], nbytes, None)
+        return lib.hg_xent_step(ctypes.byref(s), p[0], w, p[1], p[2], p[3], p[4], p[5], p[6], 0, 0, p[7], nbytes, None)
+
+    assert call(least - 1) == _lib.HG_ESIZE
+    assert call(least) != _lib.HG_ESIZE

@@ -90,8 +90,8 @@ int pick_split(long long tiles, int steps, double bytes, bool direct) {
 }
 
 // Lays the workspace out from `ws` for one kind of call and a piece of the
-// vocabulary; returns its size.
-size_t lay_out(const hg_xent_shape &s, int kind, int piece, char *ws, XentPlan *p) {
+// vocabulary, with the products split or not; returns its size.
+size_t lay_out(const hg_xent_shape &s, int kind, int piece, bool splits, char *ws, XentPlan *p) {
   memset(p, 0, sizeof *p);
   p->m = s.m;
   p->hidden = s.hidden;
@@ -140,8 +140,11 @@ size_t lay_out(const hg_xent_shape &s, int kind, int piece, char *ws, XentPlan *
   if (kind != HG_XENT_SCORE) {
     const int edge = p->small_grads ? kTile / 2 : kTile;
     const long long hn = ceil_div(s.hidden, edge);
-    p->split_dx = pick_split(ceil_div(s.m, edge) * hn, ceil_div(piece, kStep), 4.0 * m * h, false);
-    p->split_dw = pick_split(piece / edge * hn, ceil_div(s.m, kStep), 4.0 * piece * h, true);
+    p->split_dx = p->split_dw = 1;
+    if (splits) {
+      p->split_dx = pick_split(ceil_div(s.m, edge) * hn, ceil_div(piece, kStep), 4.0 * m * h, false);
+      p->split_dw = pick_split(piece / edge * hn, ceil_div(s.m, kStep), 4.0 * piece * h, true);
+    }
     p->d = take(2 * m * piece);
     p->dxp = reinterpret_cast<float *>(take(4 * m * h * p->split_dx));
     if (p->split_dw > 1)
@@ -150,30 +153,26 @@ size_t lay_out(const hg_xent_shape &s, int kind, int piece, char *ws, XentPlan *
   return at;
 }
 
-// The plan for a workspace of `limit` bytes (0: any size): the fewest pieces
-// of the vocabulary that fit, all about equally wide.
+// The plan for a workspace of `limit` bytes (0: any size), and its bytes: the
+// fewest pieces of the vocabulary that fit, all about equally wide; if none do,
+// the fewest that fit with no product split; if none do, the narrowest of those,
+// which no plan takes less than. Every width is tried, widest first, so the plan
+// for the bytes of a plan is that plan: what did not fit the limit does not fit
+// them either.
 size_t plan(const hg_xent_shape &s, int kind, size_t limit, char *ws, XentPlan *p) {
-  int pieces = 1;
-  size_t bytes = 0;
-  for (;;) {
-    const int piece = ceil_div(ceil_div(s.vocab, pieces), kTile) * kTile;
-    bytes = lay_out(s, kind, piece, ws, p);
-    if (kind == HG_XENT_SCORE || limit == 0 || bytes <= limit || piece == kTile) return bytes;
-    // at least one piece more, and straight to the number that d alone asks for
-    const size_t d = up256(2 * static_cast<size_t>(s.m) * piece);
-    const size_t rest = bytes - d;
-    int next = pieces + 1;
-    if (limit > rest) {
-      const size_t room = (limit - rest) / (2 * static_cast<size_t>(s.m ? s.m : 1));
-      if (room >= static_cast<size_t>(kTile)) {
-        const int want = ceil_div(s.vocab, static_cast<long long>(room / kTile * kTile));
-        if (want > next) next = want;
+  for (const bool splits : {true, false}) {
+    for (int pieces = 1;;) {
+      const int piece = ceil_div(ceil_div(s.vocab, pieces), kTile) * kTile;
+      const size_t bytes = lay_out(s, kind, piece, splits, ws, p);
+      if (kind == HG_XENT_SCORE || limit == 0 || bytes <= limit) return bytes;
+      if (piece == kTile) {
+        if (!splits) return bytes;
+        break;
       }
-    } else {
-      next = 2 * pieces;
+      pieces = ceil_div(s.vocab, piece - kTile);  // the fewest that are narrower
     }
-    pieces = next;
   }
+  return 0;
 }
 
 int matrix(int tp, int shard, int hidden, const void *const *w, size_t row_bytes, VocabMatrix *v) {
@@ -262,12 +261,8 @@ HG_API int hg_xent_workspace(const hg_xent_shape *s, int kind, size_t limit, siz
   if (!bytes || !shape_ok(s) || kind < HG_XENT_SCORE || kind > HG_XENT_STEP) return HG_EINVAL;
   *bytes = 0;
   if (s->m == 0) return HG_OK;
-  // Never less than the narrowest pieces need: whatever plan a call makes of
-  // this many bytes, it ends in one that fits.
   XentPlan p;
-  const size_t want = plan(*s, kind, limit, nullptr, &p);
-  const size_t least = lay_out(*s, kind, kTile, nullptr, &p);
-  *bytes = kind == HG_XENT_SCORE || want > least ? want : least;
+  *bytes = plan(*s, kind, limit, nullptr, &p);
   return HG_OK;
 }
 

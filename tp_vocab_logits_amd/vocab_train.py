@@ -218,7 +218,10 @@ def head_xent_step(x: torch.Tensor, w, labels: torch.Tensor, grad: torch.Tensor,
 class _HeadLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, labels, tp, shard, how):
-        loss, lse = head_xent(x, w, labels, tp, shard, **how)
+        h = _Head(x, w, labels, tp, shard, **how)
+        # two tensors: autograd lets no one change a view that is made in here
+        loss, lse = (torch.empty(h.m, dtype=torch.float32, device=h.device) for _ in range(2))
+        h.call(_lib.HG_XENT_SCORE, 0, None, loss, lse, None, None, False)
         ctx.save_for_backward(x, w, labels, lse)
         ctx.args = (tp, shard, how)
         return loss

@@ -361,6 +361,9 @@ typedef struct hg_xent_shape {
 #define HG_XENT_SCORE 0
 #define HG_XENT_GRAD 1
 #define HG_XENT_STEP 2
+/* With HG_XENT_GRAD, or-ed in: a call that is given no dx, or no dw. */
+#define HG_XENT_NO_DX 16
+#define HG_XENT_NO_DW 32
 
 /*
  * Bytes of device workspace for a call of the given kind: at most `limit`
@@ -392,6 +395,8 @@ int hg_xent(const hg_xent_shape *s, const void *x, const void *const *w, const v
  *     dw_v = sum_i d_iv x_i            [tp*shard][hidden], in dtype, or fp32 if
  *                                      dw_wide; rows from vocab on get zeros
  * accumulate: dw += instead of dw = (rows from vocab on keep their values).
+ * dx or dw may be NULL (a frozen matrix, a frozen body), not both: that gradient
+ * is not computed, and the workspace is that of HG_XENT_NO_DX or HG_XENT_NO_DW.
  * d is rounded to dtype, as the matrix cores take it; sums are fp32, each
  * result rounded once. m == 0 zeroes dw unless accumulating.
  */

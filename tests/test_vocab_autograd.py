@@ -32,3 +32,44 @@ def test_the_loss_can_be_changed_in_place():
     loss.sum().backward()
     lse = vt.head_xent(x.detach(), w.detach(), t, *ARGS, **p.how)[1]
     p.check_grads(x.grad, w.grad, lse_used=f64(lse))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("tp,shard,hidden,m", [(2, 96, 64, 50), (2, 8480, 520, 300), (1, 256, 1024, 2500)])
+def test_a_frozen_side_gets_no_gradient(tp, shard, hidden, m, dtype):
+    """Small and big tiles, and sums that are split: the other side's gradient
+    is the same bits."""
+    print(f"[gpu] frozen {tp=} {shard=} {hidden=} {m=} {dtype}", flush=True)
+    p = Problem(tp, shard, hidden, m, tp * shard - 7, dtype, left_out=0.1, scale=0.7, z_weight=0.01)
+    got = {}
+    for frozen in ((), ("x",), ("w",)):
+        x, w, t, g = leaves(p, frozen)
+        (vt.head_loss(x, w, t, tp, shard, **p.how) * g).sum().backward()
+        got[frozen] = x.grad, w.grad
+    assert got["x",][0] is None and torch.equal(got["x",][1], got[()][1])
+    assert got["w",][1] is None and torch.equal(got["w",][0], got[()][0])
+
+
+@gpu
+@pytest.mark.parametrize("frozen", [(), ("x",), ("w",)])
+def test_no_rows(frozen):
+    print(f"[gpu] no rows {frozen}", flush=True)
+    x, w, t, _ = leaves(Problem(*ARGS, 64, 0, 150), frozen)
+    vt.head_loss(x, w, t, *ARGS, vocab=150).sum().backward()
+    assert x.grad is None if "x" in frozen else x.grad.shape == (0, 64)
+    assert w.grad is None if "w" in frozen else not w.grad.any()
+
+
+@gpu
+def test_a_frozen_matrix_costs_no_gradient_of_it():
+    """The backward pass of a frozen head allocates nothing of the matrix's size."""
+    print("[gpu] frozen memory", flush=True)
+    p = Problem(2, 8192, 1024, 64)
+    x, w, t, _ = leaves(p, ("w",))
+    loss = vt.head_loss(x, w, t, 2, 8192, **p.how).sum()
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    loss.backward()
+    assert torch.cuda.max_memory_allocated() - before < w.numel() * w.element_size()

@@ -116,3 +116,29 @@ def test_less_than_the_least_workspace_is_refused(rows, hidden, m, vocab, kind):
 
     assert call(least - 1) == _lib.HG_ESIZE
     assert call(least) != _lib.HG_ESIZE
+
+
+@pytest.mark.parametrize("rows,hidden,m,vocab", CUT + PADDED)
+def test_a_gradient_that_is_not_wanted_takes_no_workspace(rows, hidden, m, vocab):
+    s = shape(rows, hidden, m, vocab)
+    for limit in (0, GIB):
+        both = need(s, GRAD, limit)
+        for flag in (_lib.HG_XENT_NO_DX, _lib.HG_XENT_NO_DW):
+            n = need(s, GRAD | flag, limit)
+            assert need(s, GRAD | flag, n) == n and (limit or n <= both)
+    n = ctypes.c_size_t()
+    for kind in (GRAD | _lib.HG_XENT_NO_DX | _lib.HG_XENT_NO_DW, STEP | _lib.HG_XENT_NO_DX, SCORE | _lib.HG_XENT_NO_DW,
+                 GRAD | 64):
+        assert _lib.lib().hg_xent_workspace(ctypes.byref(s), kind, 0, ctypes.byref(n)) == _lib.HG_EINVAL
+
+
+def test_one_gradient_at_least_is_wanted():
+    lib, p, w = _lib.lib(), [ctypes.c_void_p(k << 24) for k in range(1, 9)], _lib.pointer_array([9 << 24])
+    s = _lib.XentShape(1, 64, 16, 4, 60, 0, 8, -100, 1.0, 0.0)
+
+    def grad(dx, dw, nbytes=1024):
+        return lib.hg_xent_grad(ctypes.byref(s), p[0], w, p[1], p[2], p[3], dx, dw, 0, 0, p[6], nbytes, None)
+
+    assert grad(None, None) == _lib.HG_EINVAL
+    assert grad(p[4], None) == grad(None, p[5]) == _lib.HG_ESIZE  # taken, but for the workspace
+    assert grad(ctypes.c_void_p((5 << 24) + 8), None) == _lib.HG_EINVAL

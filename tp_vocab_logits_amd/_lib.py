@@ -27,6 +27,7 @@ HG_STATIC_PARITY_BYTES = 8 << 20
 HG_MAX_TP = 64
 HG_BF16, HG_FP16, HG_FP32 = 0, 1, 2
 HG_XENT_SCORE, HG_XENT_GRAD, HG_XENT_STEP = 0, 1, 2
+HG_XENT_NO_DX, HG_XENT_NO_DW = 16, 32
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int

@@ -88,7 +88,8 @@ inline bool xent_joins_in_place(const XentPlan &p) {
 }
 hipError_t launch_xent_join_normalise(const XentPlan &p, const float *grad, float *loss, float *lse,
                                       hipStream_t s);
-// dX's partial sums and dW's rows of the piece, in one launch.
+// dX's partial sums and dW's rows of the piece, in one launch (without the one
+// whose output is not there: p.dxp or dw null).
 hipError_t launch_xent_grads(const XentPlan &p, const VocabMatrix &w, int v0, int cols, bool first,
                              void *dw, bool wide, bool accumulate, hipStream_t s);
 hipError_t launch_xent_dx_join(const XentPlan &p, void *dx, hipStream_t s);

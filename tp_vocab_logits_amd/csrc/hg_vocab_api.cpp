@@ -90,8 +90,11 @@ int pick_split(long long tiles, int steps, double bytes, bool direct) {
 }
 
 // Lays the workspace out from `ws` for one kind of call and a piece of the
-// vocabulary, with the products split or not; returns its size.
+// vocabulary, with the products split or not; returns its size. kind: HG_XENT_*,
+// with the flags of what is not wanted.
 size_t lay_out(const hg_xent_shape &s, int kind, int piece, bool splits, char *ws, XentPlan *p) {
+  const bool want_dx = !(kind & HG_XENT_NO_DX), want_dw = !(kind & HG_XENT_NO_DW);
+  kind &= ~(HG_XENT_NO_DX | HG_XENT_NO_DW);
   memset(p, 0, sizeof *p);
   p->m = s.m;
   p->hidden = s.hidden;
@@ -146,8 +149,8 @@ size_t lay_out(const hg_xent_shape &s, int kind, int piece, bool splits, char *w
       p->split_dw = pick_split(piece / edge * hn, ceil_div(s.m, kStep), 4.0 * piece * h, true);
     }
     p->d = take(2 * m * piece);
-    p->dxp = reinterpret_cast<float *>(take(4 * m * h * p->split_dx));
-    if (p->split_dw > 1)
+    if (want_dx) p->dxp = reinterpret_cast<float *>(take(4 * m * h * p->split_dx));
+    if (want_dw && p->split_dw > 1)
       p->dwp = reinterpret_cast<float *>(take(4 * static_cast<size_t>(piece) * h * p->split_dw));
   }
   return at;
@@ -202,7 +205,8 @@ int begin(const hg_xent_shape *s, int kind, const void *x, const void *const *w,
   const size_t m = static_cast<size_t>(s->m), h = static_cast<size_t>(s->hidden);
   const size_t rows = static_cast<size_t>(s->tp) * s->shard;
   const bool grads = kind != HG_XENT_SCORE;
-  if (grads && (!dw || !aligned(dw, 16))) return HG_EINVAL;
+  if (grads && !dw && (kind != HG_XENT_GRAD || (m && !dx))) return HG_EINVAL;
+  if (!aligned(dw, 16)) return HG_EINVAL;
   Ranges r;
   if (m) {
     const int rc = matrix(s->tp, s->shard, s->hidden, w, 2 * h, v);
@@ -210,7 +214,8 @@ int begin(const hg_xent_shape *s, int kind, const void *x, const void *const *w,
     if (!x || !aligned(x, 16) || !labels || !aligned(labels, s->label_bytes)) return HG_EINVAL;
     if (kind != HG_XENT_GRAD && (!loss || !lse || !aligned(loss, 4) || !aligned(lse, 4)))
       return HG_EINVAL;
-    if (grads && (!grad || !aligned(grad, 4) || !dx || !aligned(dx, 16))) return HG_EINVAL;
+    if (grads && (!grad || !aligned(grad, 4) || (!dx && kind != HG_XENT_GRAD) || !aligned(dx, 16)))
+      return HG_EINVAL;
     if (kind == HG_XENT_GRAD && (!lse_in || !aligned(lse_in, 4))) return HG_EINVAL;
     if (!ws || !aligned(ws, 256)) return HG_EINVAL;
     for (int k = 0; k < v->tp; ++k)
@@ -223,11 +228,12 @@ int begin(const hg_xent_shape *s, int kind, const void *x, const void *const *w,
       r.add(loss, 4 * m, true);
       r.add(lse, 4 * m, true);
     }
-    if (grads) r.add(dx, 2 * m * h, true);
+    if (dx) r.add(dx, 2 * m * h, true);
     r.add(ws, ws_bytes, true);
   }
-  if (grads) r.add(dw, rows * h * (wide ? 4 : 2), true);
+  if (dw) r.add(dw, rows * h * (wide ? 4 : 2), true);
   if (r.clash()) return HG_EINVAL;
+  if (kind == HG_XENT_GRAD) kind |= (dx ? 0 : HG_XENT_NO_DX) | (dw ? 0 : HG_XENT_NO_DW);
   if (m && plan(*s, kind, ws_bytes, static_cast<char *>(ws), p) > ws_bytes) {
     hg::record_error("the workspace is smaller than hg_xent_workspace asks");
     return HG_ESIZE;
@@ -244,12 +250,12 @@ int products(const XentPlan &p, const VocabMatrix &v, bool ready, void *dx, void
     if (!ready) HIP_TRY(hg::launch_xent_logits(p, v, 2, v0, cols, s));
     HIP_TRY(hg::launch_xent_grads(p, v, v0, cols, v0 == 0, dw, wide != 0, accumulate != 0, s));
   }
-  HIP_TRY(hg::launch_xent_dx_join(p, dx, s));
+  if (dx) HIP_TRY(hg::launch_xent_dx_join(p, dx, s));
   return HG_OK;
 }
 
 int no_rows(const hg_xent_shape *s, void *dw, int wide, int accumulate, hipStream_t st) {
-  if (accumulate) return HG_OK;
+  if (accumulate || !dw) return HG_OK;
   const size_t n = static_cast<size_t>(s->tp) * s->shard * s->hidden * (wide ? 4 : 2);
   HIP_TRY(hg::launch_zero(dw, n, st));
   return HG_OK;
@@ -258,7 +264,9 @@ int no_rows(const hg_xent_shape *s, void *dw, int wide, int accumulate, hipStrea
 }  // namespace
 
 HG_API int hg_xent_workspace(const hg_xent_shape *s, int kind, size_t limit, size_t *bytes) {
-  if (!bytes || !shape_ok(s) || kind < HG_XENT_SCORE || kind > HG_XENT_STEP) return HG_EINVAL;
+  const bool one_of_two = kind == (HG_XENT_GRAD | HG_XENT_NO_DX) || kind == (HG_XENT_GRAD | HG_XENT_NO_DW);
+  if (!bytes || !shape_ok(s) || ((kind < HG_XENT_SCORE || kind > HG_XENT_STEP) && !one_of_two))
+    return HG_EINVAL;
   *bytes = 0;
   if (s->m == 0) return HG_OK;
   XentPlan p;

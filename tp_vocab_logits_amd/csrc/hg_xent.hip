@@ -1102,10 +1102,10 @@ hipError_t launch_xent_grads(const XentPlan &p, const VocabMatrix &w, int v0, in
   a.v0 = v0;
   a.vend = vend;
   a.tn = ceil_div(p.hidden, edge);
-  a.xgroups = ceil_div(p.m, edge) * a.tn * p.split_dx;
+  a.xgroups = p.dxp ? ceil_div(p.m, edge) * a.tn * p.split_dx : 0;
   a.per = ceil_div(ceil_div(cols, kStep), p.split_dx);
   a.first = first ? 1 : 0;
-  a.wm = ceil_div(cols, edge);
+  a.wm = dw ? ceil_div(cols, edge) : 0;
   a.dw = dw;
   a.wide = wide ? 1 : 0;
   a.accumulate = accumulate ? 1 : 0;
@@ -1119,7 +1119,7 @@ hipError_t launch_xent_grads(const XentPlan &p, const VocabMatrix &w, int v0, in
                            small_table<NT>(w.t), w.shard, a);
       });
     });
-    if (p.split_dw > 1) {
+    if (dw && p.split_dw > 1) {
       const int rows = vend < p.vocab || accumulate ? cols : p.rows - v0;
       const long long quads = static_cast<long long>(rows) * (p.hidden >> 2);
       const long long want = (quads + 255) / 256;
@@ -1129,7 +1129,7 @@ hipError_t launch_xent_grads(const XentPlan &p, const VocabMatrix &w, int v0, in
     }
   });
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.split_dw > 1 || vend < p.vocab || accumulate) return e;
+  if (e != hipSuccess || !dw || p.split_dw > 1 || vend < p.vocab || accumulate) return e;
   // the matrix's rows past the tiles that the vocabulary ends in
   const int from = v0 + a.wm * edge;
   if (from >= p.rows) return hipSuccess;

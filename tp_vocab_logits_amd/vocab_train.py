@@ -147,7 +147,10 @@ class _Head:
 
     def call(self, kind, limit, grad, loss, lse, dx, dw, accumulate):
         """The library's call of that kind; addresses of what it does not take are 0."""
-        nbytes = _xent_bytes(self.shape, kind, limit)
+        less = 0
+        if kind == _lib.HG_XENT_GRAD:
+            less = _lib.HG_XENT_NO_DX * (dx is None) | _lib.HG_XENT_NO_DW * (dw is None)
+        nbytes = _xent_bytes(self.shape, kind | less, limit)
         ws = _workspace(nbytes, self.device)
         _call(_lib.fast().xent, _NAMES[kind], self.device, kind, self.shape, *self.how, self.x.data_ptr(), self.ptrs,
               self.labels.data_ptr(), grad.data_ptr() if grad is not None else 0,
@@ -231,9 +234,13 @@ class _HeadLoss(torch.autograd.Function):
     def backward(ctx, grad):
         x, w, labels, lse = ctx.saved_tensors
         tp, shard, how = ctx.args
-        # the upstream gradient of a sum or mean is one value expanded
-        dx, dw = head_xent_grad(x, w, labels, lse, grad.float().contiguous(), tp, shard, **how)
-        return dx, dw.view(w.shape), None, None, None, None
+        h = _Head(x, w, labels, tp, shard, **how)
+        grad = h.rows_of(grad.float().contiguous(), "grad")  # of a sum or mean: one value expanded
+        need_x, need_w = ctx.needs_input_grad[:2]
+        dx = torch.empty_like(x) if need_x else None
+        dw = torch.empty_like(w) if need_w else None
+        h.call(_lib.HG_XENT_GRAD, WORKSPACE_LIMIT, grad, None, lse, dx, dw, False)
+        return dx, dw, None, None, None, None
 
 
 def head_loss(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, tp: int, shard: int,
@@ -241,7 +248,7 @@ def head_loss(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, tp: int, s
               z_weight: float = 0.0) -> torch.Tensor:
     """:func:`head_xent`'s loss ``[M]``, differentiable in ``x`` and ``w`` (one
     tensor). Only ``lse`` is kept for the backward pass, which computes the
-    logits again."""
+    logits again, and the gradients of those that require one."""
     if not isinstance(w, torch.Tensor):
         raise ValueError("head_loss takes the matrix as one tensor")
     how = {"vocab": vocab, "ignore": ignore, "scale": scale, "z_weight": z_weight}

@@ -73,3 +73,23 @@ def test_a_frozen_matrix_costs_no_gradient_of_it():
     before = torch.cuda.memory_allocated()
     loss.backward()
     assert torch.cuda.max_memory_allocated() - before < w.numel() * w.element_size()
+
+
+@gpu
+def test_the_backward_pass_keeps_within_its_workspace_limit():
+    print("[gpu] workspace limit", flush=True)
+    p = Problem(2, 16384, 64, 2000, left_out=0.1)
+    got, took = [], []
+    for limit in (vt.WORKSPACE_LIMIT, 16 << 20):
+        x, w, t, g = leaves(p)
+        loss = (vt.head_loss(x, w, t, 2, 16384, workspace_limit=limit, **p.how) * g).sum()
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        loss.backward()
+        took.append(torch.cuda.max_memory_allocated() - before)
+        got.append((x.grad, w.grad))
+    assert took[0] > 2 * 2000 * 32768 and took[1] < 32 << 20
+    lse = f64(vt.head_xent(x.detach(), w.detach(), t, 2, 16384, **p.how)[1])
+    for dx, dw in got:
+        p.check_grads(dx, dw, lse_used=lse)

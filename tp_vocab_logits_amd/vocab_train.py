@@ -220,39 +220,40 @@ def head_xent_step(x: torch.Tensor, w, labels: torch.Tensor, grad: torch.Tensor,
 
 class _HeadLoss(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, labels, tp, shard, how):
+    def forward(ctx, x, w, labels, tp, shard, how, workspace_limit):
         h = _Head(x, w, labels, tp, shard, **how)
         # two tensors: autograd lets no one change a view that is made in here
         loss, lse = (torch.empty(h.m, dtype=torch.float32, device=h.device) for _ in range(2))
         h.call(_lib.HG_XENT_SCORE, 0, None, loss, lse, None, None, False)
         ctx.save_for_backward(x, w, labels, lse)
-        ctx.args = (tp, shard, how)
+        ctx.args = (tp, shard, how, workspace_limit)
         return loss
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         x, w, labels, lse = ctx.saved_tensors
-        tp, shard, how = ctx.args
+        tp, shard, how, workspace_limit = ctx.args
         h = _Head(x, w, labels, tp, shard, **how)
         grad = h.rows_of(grad.float().contiguous(), "grad")  # of a sum or mean: one value expanded
         need_x, need_w = ctx.needs_input_grad[:2]
         dx = torch.empty_like(x) if need_x else None
         dw = torch.empty_like(w) if need_w else None
-        h.call(_lib.HG_XENT_GRAD, WORKSPACE_LIMIT, grad, None, lse, dx, dw, False)
-        return dx, dw, None, None, None, None
+        h.call(_lib.HG_XENT_GRAD, int(workspace_limit), grad, None, lse, dx, dw, False)
+        return dx, dw, None, None, None, None, None
 
 
 def head_loss(x: torch.Tensor, w: torch.Tensor, labels: torch.Tensor, tp: int, shard: int,
-              vocab: int | None = None, ignore: int = -100, scale: float = 1.0,
-              z_weight: float = 0.0) -> torch.Tensor:
+              vocab: int | None = None, ignore: int = -100, scale: float = 1.0, z_weight: float = 0.0,
+              workspace_limit: int = WORKSPACE_LIMIT) -> torch.Tensor:
     """:func:`head_xent`'s loss ``[M]``, differentiable in ``x`` and ``w`` (one
     tensor). Only ``lse`` is kept for the backward pass, which computes the
-    logits again, and the gradients of those that require one."""
+    logits again, and the gradients of those that require one, within
+    ``workspace_limit`` as :func:`head_xent_grad` does."""
     if not isinstance(w, torch.Tensor):
         raise ValueError("head_loss takes the matrix as one tensor")
     how = {"vocab": vocab, "ignore": ignore, "scale": scale, "z_weight": z_weight}
-    return _HeadLoss.apply(x, w, labels, tp, shard, how)
+    return _HeadLoss.apply(x, w, labels, tp, shard, how, workspace_limit)
 
 
 def _tokens(tokens, device) -> torch.Tensor:

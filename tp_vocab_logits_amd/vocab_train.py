@@ -10,7 +10,8 @@ hidden]``) tensor or as a sequence of ``tp`` blocks. Gradients come as one
 :func:`embed_grad` as ``dw`` with ``accumulate=True``.
 
 :func:`head_loss` and :func:`embedding` are the differentiable forms for
-autograd; the others are the plain calls. Work is enqueued on the current
+autograd; the others are the plain calls, whose results carry no history even
+if their inputs require gradients. Work is enqueued on the current
 stream of the inputs' device; workspaces come from torch's allocator on that
 stream. All of it can be captured into a graph.
 """
@@ -177,7 +178,8 @@ def head_xent(x: torch.Tensor, w, labels: torch.Tensor, tp: int, shard: int, voc
     softmax runs over the first ``vocab`` entries (default: all). ``loss = lse -
     z_label + z_weight * lse**2``; the negated loss at ``z_weight = 0`` is the
     label's log-probability. Rows with the label ``ignore`` get 0 in both; a
-    label outside the vocabulary gives NaN."""
+    label outside the vocabulary gives NaN. Autograd does not see this call:
+    :func:`head_loss` is the differentiable form."""
     h = _Head(x, w, labels, tp, shard, vocab, ignore, scale, z_weight)
     loss, lse = h.losses()
     h.call(_lib.HG_XENT_SCORE, 0, None, loss, lse, None, None, False)
@@ -268,7 +270,8 @@ def embed(tokens: torch.Tensor, w, tp: int, shard: int, scale: float = 1.0,
           out: torch.Tensor | None = None) -> torch.Tensor:
     """Embedding lookup with scaling: ``scale * w[tokens]`` of shape
     ``[*tokens.shape, H]``, rounded once to the matrix's type (BF16, FP16 or
-    FP32). A token outside the matrix gives a row of zeros."""
+    FP32). A token outside the matrix gives a row of zeros. Autograd does not
+    see this call: :func:`embedding` is the differentiable form."""
     ptrs, hidden, dtype, device = _matrix(w, tp, shard, tuple(_DTYPES))
     tokens = _tokens(tokens, device)
     _on_gpu(device)

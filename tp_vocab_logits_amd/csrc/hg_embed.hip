@@ -23,6 +23,7 @@
 
 #include <type_traits>
 
+#include "hg_fill.h"
 #include "hg_tile.h"
 #include "hg_vocab.h"
 
@@ -192,23 +193,23 @@ __device__ __forceinline__ void place_keys(volatile int *place, int n, int per, 
 // the sort is a chain of latencies on few CUs, the fill needs HBM alone. One
 // store per thread: the chip then writes one front through memory (671 MB: 110
 // us; 8 stores per thread, a front per workgroup, 119, 16 stores 125).
-constexpr int kFillVecs = 1024;
-__device__ __forceinline__ void fill_part(u32x4 *p, long long vecs, int k) {
-  const long long i = static_cast<long long>(k) * kFillVecs + threadIdx.x;
-  if (i < vecs) p[i] = u32x4{0u, 0u, 0u, 0u};
-}
-
 struct Fill {
   u32x4 *p;
   long long vecs;
+  int groups;
 };
+__device__ __forceinline__ void fill_part(const Fill &f, int k) {
+  for (long long i = static_cast<long long>(k) * kFillVecs + threadIdx.x; i < f.vecs;
+       i += static_cast<long long>(f.groups) * kFillVecs)
+    f.p[i] = u32x4{0u, 0u, 0u, 0u};
+}
 
 // All keys in one workgroup's LDS.
 __global__ __launch_bounds__(1024) void k_sort_tile(const void *tokens, int token_bytes, int n,
                                                     int rows, int passes, int *keys, int *pos,
                                                     Fill fill) {
   if (blockIdx.x > 0) {
-    fill_part(fill.p, fill.vecs, static_cast<int>(blockIdx.x) - 1);
+    fill_part(fill, static_cast<int>(blockIdx.x) - 1);
     return;
   }
   __shared__ int count[kDigits * kSortWaves];
@@ -250,7 +251,7 @@ __global__ __launch_bounds__(1024) void k_sort_count(const void *tokens, int tok
                                                      const int *keys, long long n, int rows,
                                                      int shift, int *hist, int tiles, Fill fill) {
   if (static_cast<int>(blockIdx.x) >= tiles) {
-    fill_part(fill.p, fill.vecs, static_cast<int>(blockIdx.x) - tiles);
+    fill_part(fill, static_cast<int>(blockIdx.x) - tiles);
     return;
   }
   __shared__ int count[kDigits];
@@ -269,7 +270,7 @@ __global__ __launch_bounds__(1024) void k_sort_count(const void *tokens, int tok
 // Exclusive scan of the counts, in place; one workgroup, 8192 at a time.
 __global__ __launch_bounds__(1024) void k_sort_scan(int *hist, int n, Fill fill) {
   if (blockIdx.x > 0) {
-    fill_part(fill.p, fill.vecs, static_cast<int>(blockIdx.x) - 1);
+    fill_part(fill, static_cast<int>(blockIdx.x) - 1);
     return;
   }
   __shared__ int wave_sum[16], total;
@@ -302,7 +303,7 @@ __global__ __launch_bounds__(1024) void k_sort_place(const void *tokens, int tok
                                                      int rows, int shift, const int *hist,
                                                      int tiles, int *okeys, int *opos, Fill fill) {
   if (static_cast<int>(blockIdx.x) >= tiles) {
-    fill_part(fill.p, fill.vecs, static_cast<int>(blockIdx.x) - tiles);
+    fill_part(fill, static_cast<int>(blockIdx.x) - tiles);
     return;
   }
   __shared__ int count[kDigits * kSortWaves];
@@ -699,7 +700,8 @@ hipError_t launch_embed_grad(const EmbedPlan &p, void *ws, int rows, int hidden,
     const long long at = share * part++;
     f.p = static_cast<u32x4 *>(dw) + at;
     f.vecs = zeros - at < share ? zeros - at : share;
-    *groups += f.vecs > 0 ? static_cast<int>((f.vecs + kFillVecs - 1) / kFillVecs) : 0;
+    f.groups = fill_groups(f.vecs);
+    *groups += f.groups;
     return f;
   };
   if (n <= kSortTile) {

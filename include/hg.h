@@ -397,7 +397,8 @@ int hg_xent(const hg_xent_shape *s, const void *x, const void *const *w, const v
  * accumulate: dw += instead of dw = (rows from vocab on keep their values).
  * dx or dw may be NULL (a frozen matrix, a frozen body), not both: that gradient
  * is not computed, and the workspace is that of HG_XENT_NO_DX or HG_XENT_NO_DW.
- * d is rounded to dtype, as the matrix cores take it; sums are fp32, each
+ * d is rounded to dtype, as the matrix cores take it; what that leaves out of a
+ * label's d, the large one of its row, is added in fp32. Sums are fp32, each
  * result rounded once. m == 0 zeroes dw unless accumulating.
  */
 int hg_xent_grad(const hg_xent_shape *s, const void *x, const void *const *w, const void *labels,

@@ -1,5 +1,6 @@
-"""How many digits the cross entropy keeps of logits that are long sums of one
-sign, by the rms of its losses' errors over rows that lean to their labels."""
+"""How many digits the cross entropy keeps: of logits that are long sums of one
+sign, by the rms of its losses' errors over rows that lean to their labels; of
+gradients, against the rounding of the result alone."""
 
 from __future__ import annotations
 
@@ -81,3 +82,62 @@ def test_many_rows_are_off_by_one_chain(dtype):
     x, w, labels, want, size = leaning(66048, 7168, 300, dtype, 2)
     loss = vt.head_xent(x, w, labels, 8, 8256)[0]
     assert rms_error(loss, want) <= ONE_CHAIN * U32 * size
+
+
+HALF_STEP = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+
+
+def gradients(x, w, labels, grad, vocab):
+    """In 64 bits."""
+    kept = labels >= 0
+    xd, wd = torch.where(kept[:, None], x.double(), 0.0), w[:vocab].double()
+    d = torch.softmax(xd @ wd.t(), dim=1)
+    d[torch.nonzero(kept).squeeze(1), labels[kept]] -= 1.0
+    d *= torch.where(kept, grad.double(), 0.0)[:, None]
+    dw = torch.zeros(w.shape, dtype=torch.float64, device=DEV)
+    dw[:vocab] = d.t() @ xd
+    return d @ wd, dw
+
+
+def off(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+# m, rows of the matrix, hidden, vocabulary, limit of the workspace: small tiles,
+# big ones, sums split over the vocabulary and over the rows, the vocabulary in
+# pieces, more labels than one turn lists and more in a tile than one step takes
+GRADIENTS = [(1, 2048, 64, 2048, 0), (33, 2048, 264, 2001, 0), (300, 17408, 520, 17001, 0),
+             (3000, 2048, 1032, 2047, 0), (6000, 1024, 136, 1000, 0), (700, 8192, 264, 8190, 6 << 20)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("often", [0.0, 0.5])
+@pytest.mark.parametrize("m,rows,hidden,vocab,limit", GRADIENTS)
+def test_a_gradient_is_rounded_once(m, rows, hidden, vocab, limit, often, dtype):
+    """The label's d is rounded to 16 bits for the products and would be off by
+    up to half a step, which is as much as the result's own rounding, on the
+    one large term of a row of dX and of dW. What the rounding leaves out is
+    added, so the other terms' roundings are left. Probabilities here are about
+    1/vocab each: their errors, half a step of each at random signs, sum up to
+    vocab^-1/2 <= 1/30 of what the label's would be (with the label's term 1, a
+    row of dX has vocab others of 1/vocab; a row of dW has m, on vocab rows). The
+    rounding of the result may thus be exceeded by a thousandth, and 10 % is
+    allowed; in fp32, a tenth of half a step."""
+    print(f"[gpu] gradients {m=} {rows=} {hidden=} {vocab=} {often=} {dtype}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(m + vocab)
+    x = torch.randn(m, hidden, generator=g, device=DEV).to(DT[dtype])
+    w = (torch.randn(rows, hidden, generator=g, device=DEV) * 0.4 / hidden ** 0.5).to(DT[dtype])
+    labels = torch.randint(0, vocab, (m,), generator=g, device=DEV)
+    labels[torch.rand(m, generator=g, device=DEV) < often] = vocab - 3
+    grad = 0.5 + torch.rand(m, generator=g, device=DEV)
+    if m > 1:
+        labels[torch.rand(m, generator=g, device=DEV) < 0.1] = -100
+    want_x, want_w = gradients(x, w, labels, grad, vocab)
+    _, lse, dx, dw = vt.head_xent_step(x, w, labels, grad, 2, rows // 2, vocab=vocab, workspace_limit=limit)
+    later = vt.head_xent_grad(x, w, labels, lse, grad, 2, rows // 2, vocab=vocab, workspace_limit=limit)
+    wide = vt.head_xent_step(x, w, labels, grad, 2, rows // 2, vocab=vocab, workspace_limit=limit,
+                             dw=torch.empty(rows, hidden, device=DEV))[3]
+    for got, want in ((dx, want_x), (dw, want_w), (later[0], want_x), (later[1], want_w)):
+        assert off(got, want) <= 1.1 * off(want.to(DT[dtype]), want)
+    assert off(wide, want_w) <= 0.1 * HALF_STEP[dtype]

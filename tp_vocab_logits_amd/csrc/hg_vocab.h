@@ -29,6 +29,7 @@ struct XentRows {
   float *lse2;    // [m] packed: log-sum-exp in base 2
   float *ca;      // [m] packed: factor of the probability in d
   float *cb;      // [m] packed: factor of the label's one in d
+  float *res;     // [m] packed: what the rounding of the label's d left out
 };
 
 // The 16-bit work arrays (packed x, d) lie in panels of 256 columns: element
@@ -92,7 +93,7 @@ hipError_t launch_xent_join_normalise(const XentPlan &p, const float *grad, floa
 // whose output is not there: p.dxp or dw null).
 hipError_t launch_xent_grads(const XentPlan &p, const VocabMatrix &w, int v0, int cols, bool first,
                              void *dw, bool wide, bool accumulate, hipStream_t s);
-hipError_t launch_xent_dx_join(const XentPlan &p, void *dx, hipStream_t s);
+hipError_t launch_xent_dx_join(const XentPlan &p, const VocabMatrix &w, void *dx, hipStream_t s);
 
 // `bytes` zero bytes at a 16-byte aligned address (bytes a multiple of 16).
 hipError_t launch_zero(void *p, size_t bytes, hipStream_t s);

@@ -121,6 +121,7 @@ size_t lay_out(const hg_xent_shape &s, int kind, int piece, bool splits, char *w
   p->r.lse2 = reinterpret_cast<float *>(take(4 * m));
   p->r.ca = reinterpret_cast<float *>(take(4 * m));
   p->r.cb = reinterpret_cast<float *>(take(4 * m));
+  p->r.res = reinterpret_cast<float *>(take(4 * m));
   // The small tile while the big one would give work to half of the CUs at
   // most. It takes about 1.5 times as long per product (2047 rows at V = 32000,
   // H = 2048: logits 255 us against 165, gradient products 505 us against 310),
@@ -250,7 +251,7 @@ int products(const XentPlan &p, const VocabMatrix &v, bool ready, void *dx, void
     if (!ready) HIP_TRY(hg::launch_xent_logits(p, v, 2, v0, cols, s));
     HIP_TRY(hg::launch_xent_grads(p, v, v0, cols, v0 == 0, dw, wide != 0, accumulate != 0, s));
   }
-  if (dx) HIP_TRY(hg::launch_xent_dx_join(p, dx, s));
+  if (dx) HIP_TRY(hg::launch_xent_dx_join(p, v, dx, s));
   return HG_OK;
 }
 

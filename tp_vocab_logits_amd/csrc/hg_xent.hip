@@ -23,7 +23,11 @@
 //  - lse is known, and the epilogue writes d itself (hg_xent_grad, and steps
 //    whose workspace holds fewer columns than the vocabulary).
 // d is 16 bits wide, as the matrix cores take it: one rounding to the type on
-// each term of sums over many. fp16 has 5 exponent bits: there d is scaled by a
+// each term of sums over many. A label's d is no term among many: it is the
+// largest of its row by far, and often the one large term of its row of dW, and
+// its rounding would show in the results as one more rounding of their own. What
+// it leaves out (XentRows::res) joins both products in fp32, as a multiple of
+// the label's row of W and of x. fp16 has 5 exponent bits: there d is scaled by a
 // power of two that brings its largest row factor to 2^13..2^14, so that terms
 // down to about 2^-27 of the largest keep all their bits; the scale is exact
 // and is taken back in fp32.
@@ -94,6 +98,13 @@ __device__ __forceinline__ RowLoss row_loss(float top, float sum, float gap, flo
 __device__ __forceinline__ long long label_at(const void *labels, int bytes, int i) {
   return bytes == 8 ? static_cast<const long long *>(labels)[i]
                     : static_cast<const int *>(labels)[i];
+}
+
+// What the rounding of a label's d leaves out; nothing where d is not finite.
+template <class T>
+__device__ __forceinline__ float residue(float d) {
+  const float r = d - from16<T>(bits16<T>(d));
+  return fabsf(r) < __builtin_inff() ? r : 0.f;
 }
 
 // What a row left out gets: loss = lse = 0, or NaN in both for a label outside
@@ -253,7 +264,10 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
             float v = exp2_(fmaf(acc[i][j][t], s2, -lse2)) * ca;
             if constexpr (decltype(special)::value) {
               const int n = nl + 16 * j + t;
-              v = n == lab ? v - cb : v;
+              if (n == lab) {
+                v -= cb;
+                pl.r.res[row] = residue<T>(v);
+              }
               v = n < vend ? v : 0.f;
             }
             q[t] = bits16<T>(v);
@@ -673,15 +687,22 @@ __global__ __launch_bounds__(256) void k_factors(XentPlan pl, const float *lse, 
   if (f < __builtin_inff()) atomicMax(pl.r.head + 1, __builtin_bit_cast(int, f));
 }
 
-// 16 bytes (8 columns) of unnormalised probabilities -> d: times c, less cb at
-// column `at` of them.
+// 16 bytes (8 columns) of a row's unnormalised probabilities -> d: times c, less
+// cb at column `at` of them. The label's probability comes from its logit, not
+// from the 16 bits that waited.
 template <class T>
-__device__ __forceinline__ u32x4 normalised(u32x4 v, float c, float cb, int at) {
+__device__ __forceinline__ u32x4 normalised(const XentRows &r, int row, u32x4 v, float c, float cb,
+                                            int at) {
+  float label = 0.f;
+  if (at >= 0 && at < 8) {
+    label = exp2_(r.zt[row]) * c - cb;
+    r.res[row] = residue<T>(label);
+  }
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     float lo = Prob<T>::get(v[t] & 0xFFFFu) * c, hi = Prob<T>::get(v[t] >> 16) * c;
-    if (at == 2 * t) lo -= cb;
-    if (at == 2 * t + 1) hi -= cb;
+    if (at == 2 * t) lo = label;
+    if (at == 2 * t + 1) hi = label;
     v[t] = bits16<T>(lo) | bits16<T>(hi) << 16;
   }
   return v;
@@ -706,7 +727,7 @@ __global__ __launch_bounds__(256) void k_normalise(XentPlan pl) {
     const float ref = mx == -__builtin_inff() ? 0.f : mx;
     const float c = exp2_(ref - pl.r.lse2[row]) * (pl.r.ca[row] * up), cb = pl.r.cb[row] * up;
     u32x4 *o = d + static_cast<long long>(row) * 32 + k;
-    *o = normalised<T>(*o, c, cb, pl.r.lab[row] - panel * kPanel - 8 * k);
+    *o = normalised<T>(pl.r, row, *o, c, cb, pl.r.lab[row] - panel * kPanel - 8 * k);
   }
 }
 
@@ -772,7 +793,7 @@ __global__ __launch_bounds__(256) void k_join_normalise(XentPlan pl, const float
     const float ref = top == -__builtin_inff() ? 0.f : top;
     const float c = exp2_(ref - l2) * (u * (1.f + 2.f * pl.z_weight * l) * up);
     u32x4 *o = d + static_cast<long long>(row) * 32 + k;
-    *o = normalised<T>(*o, c, u * up, pl.r.lab[row] - panel * kPanel - 8 * k);
+    *o = normalised<T>(pl.r, row, *o, c, u * up, pl.r.lab[row] - panel * kPanel - 8 * k);
   }
 }
 
@@ -803,6 +824,120 @@ struct GradArgs {
   int wm, tn;         // dW: tile rows; both: tile columns
   void *dw;
   int wide, accumulate;
+};
+
+// The residues of the labels' d in a dW tile of vocabulary rows v0 .. and columns
+// n0 .., over the packed rows k0 .. k1-1. The rows with a label in the tile are
+// listed in order, eight labels per thread (whose order is the rows') and turn.
+// 64 of them at a time are the k of one more step of the product: their x is
+// gathered into LDS as a column operand, and the other operand, with one residue
+// for each k, is made in registers. The first labels are loaded before the
+// product, which covers their latency. A step of 1228 rows at V = 32000, H = 2048
+// takes 513 us with the residues and 505 without, of 8192 rows at V = 32768,
+// H = 1024 1610 and 1586, of 4096 at V = 163840, H = 7168 the same within the
+// noise; one by one from registers, four in flight, the middle one took 1817.
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+template <class T, class Tile>
+struct Residues {
+  static constexpr int kTurn = 8 * 512;
+  // LDS: x of 64 rows, then the list, the 64 entries and the waves' counts
+  static constexpr int kList = 8 * kSubBytes, kEntries = kList + 4 * kTurn, kCounts = kEntries + 256;
+  static_assert(kCounts + 32 <= kTileLds);
+  // The thread's labels of the turn from `base` (a multiple of 64, as k0 is) on.
+  static __device__ __forceinline__ i32x8 load(const XentPlan &pl, int base, int k1) {
+    const int p = base + 8 * static_cast<int>(threadIdx.x);
+    return p < k1 ? *reinterpret_cast<const i32x8 *>(pl.r.lab + p) : i32x8(-1);
+  }
+  // After the product, when LDS is free; `at`: the first turn's labels.
+  static __device__ __forceinline__ void add(const XentPlan &pl, i32x8 at, int v0, int n0, int k0,
+                                             int k1, unsigned char *lds,
+                                             f32x4 (&acc)[Tile::MI][Tile::NJ]) {
+    const int tid = static_cast<int>(threadIdx.x);
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = wave >> 2, wc = wave & 3, l16 = lane & 15, g = lane >> 4;
+    unsigned *list = reinterpret_cast<unsigned *>(lds + kList);  // tile row << 24 | packed row
+    unsigned *entry = reinterpret_cast<unsigned *>(lds + kEntries);  // tile row | residue << 16
+    int *count = reinterpret_cast<int *>(lds + kCounts);
+    const unsigned char *x = static_cast<const unsigned char *>(pl.xc) +
+                             static_cast<long long>(n0 / kPanel) * pl.m * (2 * kPanel) +
+                             n0 % kPanel * 2;
+    FragLane<true> fb;
+    fb.init(lane);
+    for (int base = k0; base < k1; base += kTurn) {
+      if (base > k0) at = load(pl, base, k1);
+      at -= v0;
+      unsigned in = 0;  // which of the eight are rows of the tile
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        in |= (at[u] >= 0 && at[u] < Tile::kEdge && base + 8 * tid + u < k1 ? 1u : 0u) << u;
+      const int mine = __popc(in);
+      int upto = mine;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(upto, d);
+        if (lane >= d) upto += o;
+      }
+      if (lane == 63) count[wave] = upto;
+      __syncthreads();
+      int to = upto - mine, all = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        if (w < wave) to += count[w];
+        all += count[w];
+      }
+      if (in) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if ((in >> u) & 1)
+            list[to++] = static_cast<unsigned>(at[u]) << 24 | static_cast<unsigned>(base + 8 * tid + u);
+      }
+      __syncthreads();
+      for (int q0 = 0; q0 < all; q0 += 64) {
+        constexpr int kChunks = Tile::kEdge / 8;  // of 16 bytes in a row of x
+#pragma unroll
+        for (int u = 0; u < 64 * kChunks / 512; ++u) {
+          const int q = (u * 512 + tid) / kChunks, c = tid % kChunks;
+          u32x4 v = {0u, 0u, 0u, 0u};
+          if (q0 + q < all)
+            v = *reinterpret_cast<const u32x4 *>(
+                x + static_cast<long long>(list[q0 + q] & 0xFFFFFFu) * (2 * kPanel) + 16 * c);
+          const int f = ((q >> 1) & 1) | ((q >> 3) & 1) << 1;
+          *reinterpret_cast<u32x4 *>(lds + (c >> 3) * kSubBytes + q * 128 + (((c & 7) ^ (2 * f)) << 4)) = v;
+        }
+        if (tid < 64) {
+          const unsigned e = q0 + tid < all ? list[q0 + tid] : 0u;
+          entry[tid] = q0 + tid < all ? e >> 24 | bits16<T>(pl.r.res[e & 0xFFFFFFu]) << 16 : 0xFFFFu;
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int ks = 0; ks < (all - q0 > 32 ? 2 : 1); ++ks) {
+          s16x8 rb[Tile::NJ];
+          unsigned e[8];
+#pragma unroll
+          for (int j = 0; j < Tile::NJ; ++j) {
+            if constexpr (Tile::NJ == 4)
+              rb[j] = fb.read(lds + wc * kSubBytes, j, ks);
+            else
+              rb[j] = (wc & 1) ? fb.read(lds + (wc >> 1) * kSubBytes, 2 + j, ks)
+                               : fb.read(lds + (wc >> 1) * kSubBytes, j, ks);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) e[k] = entry[32 * ks + 8 * g + k];
+#pragma unroll
+          for (int i = 0; i < Tile::MI; ++i) {
+            const unsigned row = Tile::kRows * wr + 16 * i + l16;
+            s16x8 ra;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              ra[k] = static_cast<short>((e[k] & 0xFFFFu) == row ? e[k] >> 16 : 0u);
+#pragma unroll
+            for (int j = 0; j < Tile::NJ; ++j) acc[i][j] = T::mma(rb[j], ra, acc[i][j]);
+          }
+        }
+        __syncthreads();
+      }
+    }
+  }
 };
 
 template <class T, class Tile, int NT>
@@ -873,7 +1008,10 @@ __global__ __launch_bounds__(512, 2) void k_grads(XentPlan pl, ShardTableN<NT> w
   b.init(static_cast<const unsigned char *>(pl.xc) +
              (static_cast<long long>(n0 / kPanel) * pl.m + k0) * 512,
          n0 % kPanel, kdim, lane);
+  using Res = Residues<T, Tile>;
+  const i32x8 labels = Res::load(pl, k0, k1);
   Tile::template product<T>(a, b, (kdim + kStep - 1) / kStep, lds, acc);
+  Res::add(pl, labels, v0 + c0, n0, k0, k1, lds, acc);
   const float down = split ? 1.f : d_scale<T>(pl.r, true);
   void *out = split ? static_cast<void *>(pl.dwp +
                                           static_cast<long long>(z) * pl.piece * pl.hidden)
@@ -912,21 +1050,30 @@ __device__ __forceinline__ f32x4 add_planes(const f32x4 *src, long long plane, i
   return v;
 }
 
-// Partial sums -> dx rows (zero where the row is left out): four columns per
-// lane.
-template <class T>
-__global__ __launch_bounds__(256) void k_dx_join(XentPlan pl, uint2 *dx) {
+// Partial sums and the label's residue -> dx rows (zero where the row is left
+// out): four columns per lane.
+template <class T, int NT>
+__global__ __launch_bounds__(256) void k_dx_join(XentPlan pl, ShardTableN<NT> w, int shard,
+                                                 uint2 *dx) {
   const float down = d_scale<T>(pl.r, true);
   const int hq = pl.hidden >> 2;
   const long long plane = static_cast<long long>(pl.m) * hq;
   for (int row = static_cast<int>(blockIdx.y); row < pl.m; row += static_cast<int>(gridDim.y)) {
     const int p = pl.r.inv[row];
+    const float res = p >= 0 ? pl.r.res[p] : 0.f;
+    const int lab = p >= 0 ? pl.r.lab[p] : 0, rank = NT == 1 ? 0 : lab / shard;
+    const uint2 *wl = reinterpret_cast<const uint2 *>(w.p[rank]) +
+                      static_cast<long long>(lab - rank * shard) * hq;
     for (int k = static_cast<int>(blockIdx.x * 256 + threadIdx.x); k < hq;
          k += static_cast<int>(gridDim.x) * 256) {
       uint2 o = {0u, 0u};
       if (p >= 0) {
         const f32x4 *src = reinterpret_cast<const f32x4 *>(pl.dxp) + static_cast<long long>(p) * hq + k;
+        const uint2 wv = wl[k];
         f32x4 v = add_planes(src, plane, pl.split_dx);
+        if (res != 0.f)
+          v += f32x4{from16<T>(wv.x & 0xFFFFu), from16<T>(wv.x >> 16), from16<T>(wv.y & 0xFFFFu),
+                     from16<T>(wv.y >> 16)} * res;
         v *= down;
         o = uint2{bits16<T>(v[0]) | bits16<T>(v[1]) << 16, bits16<T>(v[2]) | bits16<T>(v[3]) << 16};
       }
@@ -1076,11 +1223,14 @@ hipError_t launch_xent_normalise(const XentPlan &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_xent_dx_join(const XentPlan &p, void *dx, hipStream_t s) {
+hipError_t launch_xent_dx_join(const XentPlan &p, const VocabMatrix &w, void *dx, hipStream_t s) {
   const dim3 grid(ceil_div(p.hidden >> 2, 1024), p.m < 16384 ? p.m : 16384);
   by_type(p.half, [&](auto type) {
-    hipLaunchKernelGGL(k_dx_join<decltype(type)>, grid, dim3(256), 0, s, p,
-                       static_cast<uint2 *>(dx));
+    by_table(w.tp, [&](auto nt) {
+      constexpr int NT = decltype(nt)::value;
+      hipLaunchKernelGGL((k_dx_join<decltype(type), NT>), grid, dim3(256), 0, s, p,
+                         small_table<NT>(w.t), w.shard, static_cast<uint2 *>(dx));
+    });
   });
   return hipGetLastError();
 }

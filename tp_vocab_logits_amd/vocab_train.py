@@ -106,6 +106,8 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
 @functools.lru_cache(maxsize=256)
 def _xent_bytes(shape: tuple, kind: int, limit: int) -> int:
     """hg_xent_workspace, once per shape: a training loop asks for the same one every step."""
+    if limit < 0:  # (a size_t would make it no limit at all)
+        raise ValueError(f"workspace_limit must not be negative, got {limit}")
     n = ctypes.c_size_t()
     check(lib().hg_xent_workspace(_lib.XentShape(*shape, 0, 1.0, 0.0), kind, limit, n), "hg_xent_workspace")
     return n.value
@@ -195,7 +197,8 @@ def head_xent_grad(x: torch.Tensor, w, labels: torch.Tensor, lse: torch.Tensor, 
     for the ``lse`` that :func:`head_xent` returned and an upstream ``grad [M]``
     (both fp32). Given, ``dx`` and ``dw`` are written; ``dw`` may be fp32, and
     with ``accumulate`` is added to. The call keeps at most ``workspace_limit``
-    bytes of workspace where the vocabulary can be cut into pieces for it."""
+    bytes of workspace (0: as many as it likes) where the vocabulary can be cut
+    into pieces for it."""
     h = _Head(x, w, labels, tp, shard, vocab, ignore, scale, z_weight)
     lse, grad = h.rows_of(lse, "lse"), h.rows_of(grad, "grad")
     dx, dw = h.grads(dx, dw, accumulate)

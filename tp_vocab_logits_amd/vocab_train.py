@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+from collections.abc import Iterable
 
 import torch
 
@@ -63,11 +64,15 @@ def _matrix(w, tp: int, shard: int, dtypes) -> tuple[tuple[int, ...], int, torch
         blocks, hidden = (w,), int(w.shape[-1])
         ptrs = (w.data_ptr(),)
     else:
+        if not isinstance(w, Iterable):
+            raise ValueError(f"the matrix must be a tensor or {tp} blocks, got {type(w).__name__}")
         blocks = list(w)
         if len(blocks) != tp:
             raise ValueError(f"expected {tp} blocks of the matrix, got {len(blocks)}")
-        hidden = int(blocks[0].shape[-1])
+        hidden = int(blocks[0].shape[-1]) if isinstance(blocks[0], torch.Tensor) and blocks[0].dim() else 0
         for t in blocks:
+            if not isinstance(t, torch.Tensor):
+                raise ValueError(f"every block must be a tensor, got {type(t).__name__}")
             if t.dim() != 2 or tuple(t.shape) != (shard, hidden) or not t.is_contiguous():
                 raise ValueError(f"every block must be a contiguous [{shard}, {hidden}] tensor, got {tuple(t.shape)}")
             if t.dtype != blocks[0].dtype or t.device != blocks[0].device:

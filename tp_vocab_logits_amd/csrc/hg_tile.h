@@ -247,9 +247,12 @@ struct PanelColumnSource {
     for (int o = 0; o < 2; ++o) off[o] = static_cast<unsigned>(p.row * 512 + p.chunk[o] * 16);
   }
   __device__ __forceinline__ void load(unsigned char *lds, int sub, int q, int step) const {
+    // Past the last row the resource is empty, wherever it points. (Without the
+    // test of that and with one minimum for the length: 14.83 ms for the gradient's
+    // products of 4096 rows at V = 163840, H = 7168, with them 15.06.)
     const int left = rows - step * 64;
-    const rsrc_t r = resource(base + (left <= 0 ? 0ll : static_cast<long long>(step) * (64 * 512)),
-                              left > 64 ? 64 * 512 : left * 512 - 2 * col);
+    const rsrc_t r = resource(base + static_cast<long long>(step) * (64 * 512),
+                              (left < 64 ? left : 64) * 512 - 2 * col);
     load_lds(r, lds + q * 1024, off[q & 1] + static_cast<unsigned>(8 * q * 512 + sub * 128));
   }
 };

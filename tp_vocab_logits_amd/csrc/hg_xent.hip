@@ -832,10 +832,11 @@ struct GradArgs {
 // 64 of them at a time are the k of one more step of the product: their x is
 // gathered into LDS as a column operand, and the other operand, with one residue
 // for each k, is made in registers. The first labels are loaded before the
-// product, which covers their latency. A step of 1228 rows at V = 32000, H = 2048
-// takes 513 us with the residues and 505 without, of 8192 rows at V = 32768,
-// H = 1024 1610 and 1586, of 4096 at V = 163840, H = 7168 the same within the
-// noise; one by one from registers, four in flight, the middle one took 1817.
+// product, which covers their latency. (Both products of the gradient of 4096 rows
+// at V = 163840, H = 7168 take 15.21 ms with the residues and 15.06 without, of 8192
+// rows at V = 32768, H = 1024 792 us and 763, of 777 rows at V = 32768, H = 4096 411
+// and 391. One row at a time, from registers, 225 us more at 8192 rows, 680 of which
+// share a label; gathered behind the product's first loads, the same.)
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 template <class T, class Tile>
 struct Residues {
@@ -934,7 +935,7 @@ struct Residues {
             for (int j = 0; j < Tile::NJ; ++j) acc[i][j] = T::mma(rb[j], ra, acc[i][j]);
           }
         }
-        __syncthreads();
+        if (q0 + 64 < all || base + kTurn < k1) __syncthreads();  // LDS is written again
       }
     }
   }

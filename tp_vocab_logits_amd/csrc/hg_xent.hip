@@ -828,114 +828,131 @@ struct GradArgs {
 
 // The residues of the labels' d in a dW tile of vocabulary rows v0 .. and columns
 // n0 .., over the packed rows k0 .. k1-1. The rows with a label in the tile are
-// listed in order, eight labels per thread (whose order is the rows') and turn.
-// 64 of them at a time are the k of one more step of the product: their x is
-// gathered into LDS as a column operand, and the other operand, with one residue
-// for each k, is made in registers. The first labels are loaded before the
-// product, which covers their latency. (Both products of the gradient of 4096 rows
-// at V = 163840, H = 7168 take 15.21 ms with the residues and 15.06 without, of 8192
-// rows at V = 32768, H = 1024 792 us and 763, of 777 rows at V = 32768, H = 4096 411
-// and 391. One row at a time, from registers, 225 us more at 8192 rows, 680 of which
-// share a label; gathered behind the product's first loads, the same.)
+// listed, each wave's in a part of the list of its own, and 64 of them at a time
+// are the k of one more step of the product: their x is gathered into LDS as a
+// column operand, beside an operand of zeros with one residue for each k. The first
+// labels are loaded before the product, which covers their latency.
+// (Both products of the gradient of 4096 rows at V = 163840, H = 7168 take 14.86 ms
+// with the residues and 14.68 without, of 8192 rows at V = 32768, H = 1024 779 us and
+// 759, of 777 rows at V = 32768, H = 4096 406 and 386. One row at a time, from
+// registers, 225 us more at 8192 rows, 780 of which share a label; the residues'
+// operand compared together in registers 8 us more there; gathered behind the
+// product's first loads, the same.)
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 template <class T, class Tile>
 struct Residues {
-  static constexpr int kTurn = 8 * 512;
-  // LDS: x of 64 rows, then the list, the 64 entries and the waves' counts
-  static constexpr int kList = 8 * kSubBytes, kEntries = kList + 4 * kTurn, kCounts = kEntries + 256;
+  static constexpr int kTurn = 8 * 512;                    // labels listed at a time
+  static constexpr int kSubs = Tile::kEdge / 64;           // sub-tiles of an operand
+  static constexpr int kX = 0, kA = kSubs * kSubBytes, kList = 2 * kA, kCounts = kList + 4 * kTurn;
   static_assert(kCounts + 32 <= kTileLds);
-  // The thread's labels of the turn from `base` (a multiple of 64, as k0 is) on.
+
+  // The thread's labels of the turn from `base` on.
   static __device__ __forceinline__ i32x8 load(const XentPlan &pl, int base, int k1) {
-    const int p = base + 8 * static_cast<int>(threadIdx.x);
-    return p < k1 ? *reinterpret_cast<const i32x8 *>(pl.r.lab + p) : i32x8(-1);
+    i32x8 at;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int p = base + 512 * u + static_cast<int>(threadIdx.x);
+      at[u] = p < k1 ? pl.r.lab[p] : -1;
+    }
+    return at;
   }
   // After the product, when LDS is free; `at`: the first turn's labels.
   static __device__ __forceinline__ void add(const XentPlan &pl, i32x8 at, int v0, int n0, int k0,
                                              int k1, unsigned char *lds,
                                              f32x4 (&acc)[Tile::MI][Tile::NJ]) {
-    const int tid = static_cast<int>(threadIdx.x);
-    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wr = wave >> 2, wc = wave & 3, l16 = lane & 15, g = lane >> 4;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = wave >> 2, wc = wave & 3;
     unsigned *list = reinterpret_cast<unsigned *>(lds + kList);  // tile row << 24 | packed row
-    unsigned *entry = reinterpret_cast<unsigned *>(lds + kEntries);  // tile row | residue << 16
     int *count = reinterpret_cast<int *>(lds + kCounts);
     const unsigned char *x = static_cast<const unsigned char *>(pl.xc) +
                              static_cast<long long>(n0 / kPanel) * pl.m * (2 * kPanel) +
                              n0 % kPanel * 2;
-    FragLane<true> fb;
-    fb.init(lane);
+    auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int u = 0; u < kSubs; ++u)
+        *reinterpret_cast<u32x4 *>(lds + kA + (u * 512 + tid) * 16) = u32x4{0u, 0u, 0u, 0u};
+    };
+    FragLane<true> f;
+    f.init(lane);
     for (int base = k0; base < k1; base += kTurn) {
-      if (base > k0) at = load(pl, base, k1);
-      at -= v0;
-      unsigned in = 0;  // which of the eight are rows of the tile
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        in |= (at[u] >= 0 && at[u] < Tile::kEdge && base + 8 * tid + u < k1 ? 1u : 0u) << u;
-      const int mine = __popc(in);
-      int upto = mine;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(upto, d);
-        if (lane >= d) upto += o;
+      if (base > k0) {
+        at = load(pl, base, k1);
+        __syncthreads();
       }
-      if (lane == 63) count[wave] = upto;
+      int run = 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int row = at[u] - v0;  // (no label: -1, below every tile)
+        const bool in = at[u] >= v0 && row < Tile::kEdge;
+        const unsigned long long lanes = __ballot(in);
+        if (in)
+          list[wave * 512 + run + __popcll(lanes & ((1ull << lane) - 1))] =
+              static_cast<unsigned>(row) << 24 | static_cast<unsigned>(base + 512 * u + tid);
+        run += __popcll(lanes);
+      }
+      if (lane == 0) count[wave] = run;
+      clear();
       __syncthreads();
-      int to = upto - mine, all = 0;
+      int first[9];  // of each wave's rows among all
+      first[0] = 0;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        if (w < wave) to += count[w];
-        all += count[w];
-      }
-      if (in) {
+      for (int w = 0; w < 8; ++w)
+        first[w + 1] = first[w] + __builtin_amdgcn_readfirstlane(count[w]);
+      const int all = first[8];
+      auto listed = [&](int q) __attribute__((always_inline)) {
+        int at_q = q;
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if ((in >> u) & 1)
-            list[to++] = static_cast<unsigned>(at[u]) << 24 | static_cast<unsigned>(base + 8 * tid + u);
-      }
-      __syncthreads();
+        for (int w = 1; w < 8; ++w) at_q = q >= first[w] ? q - first[w] + 512 * w : at_q;
+        return list[at_q];
+      };
       for (int q0 = 0; q0 < all; q0 += 64) {
+        if (q0) {
+          __syncthreads();
+          clear();
+          __syncthreads();
+        }
+        const int here = all - q0 < 64 ? all - q0 : 64, steps = here > 32 ? 2 : 1;
+        if (tid < here) {
+          const unsigned e = listed(q0 + tid), row = e >> 24;
+          const int fk = ((tid >> 1) & 1) | ((tid >> 3) & 1) << 1;
+          *reinterpret_cast<unsigned short *>(lds + kA + (row >> 6) * kSubBytes + tid * 128 +
+                                              ((((row >> 3) & 7) ^ (2 * fk)) << 4) + (row & 7) * 2) =
+              static_cast<unsigned short>(bits16<T>(pl.r.res[e & 0xFFFFFFu]));
+        }
         constexpr int kChunks = Tile::kEdge / 8;  // of 16 bytes in a row of x
 #pragma unroll
-        for (int u = 0; u < 64 * kChunks / 512; ++u) {
+        for (int u = 0; u < kSubs; ++u) {
           const int q = (u * 512 + tid) / kChunks, c = tid % kChunks;
+          if (u >= kSubs / 2 && steps == 1) break;
           u32x4 v = {0u, 0u, 0u, 0u};
-          if (q0 + q < all)
+          if (q < here)
             v = *reinterpret_cast<const u32x4 *>(
-                x + static_cast<long long>(list[q0 + q] & 0xFFFFFFu) * (2 * kPanel) + 16 * c);
-          const int f = ((q >> 1) & 1) | ((q >> 3) & 1) << 1;
-          *reinterpret_cast<u32x4 *>(lds + (c >> 3) * kSubBytes + q * 128 + (((c & 7) ^ (2 * f)) << 4)) = v;
-        }
-        if (tid < 64) {
-          const unsigned e = q0 + tid < all ? list[q0 + tid] : 0u;
-          entry[tid] = q0 + tid < all ? e >> 24 | bits16<T>(pl.r.res[e & 0xFFFFFFu]) << 16 : 0xFFFFu;
+                x + static_cast<long long>(listed(q0 + q) & 0xFFFFFFu) * (2 * kPanel) + 16 * c);
+          const int fk = ((q >> 1) & 1) | ((q >> 3) & 1) << 1;
+          *reinterpret_cast<u32x4 *>(lds + kX + (c >> 3) * kSubBytes + q * 128 +
+                                     (((c & 7) ^ (2 * fk)) << 4)) = v;
         }
         __syncthreads();
 #pragma unroll 1
-        for (int ks = 0; ks < (all - q0 > 32 ? 2 : 1); ++ks) {
-          s16x8 rb[Tile::NJ];
-          unsigned e[8];
+        for (int ks = 0; ks < steps; ++ks) {
+          s16x8 ra[Tile::MI], rb[Tile::NJ];
 #pragma unroll
           for (int j = 0; j < Tile::NJ; ++j) {
             if constexpr (Tile::NJ == 4)
-              rb[j] = fb.read(lds + wc * kSubBytes, j, ks);
+              rb[j] = f.read(lds + kX + wc * kSubBytes, j, ks);
             else
-              rb[j] = (wc & 1) ? fb.read(lds + (wc >> 1) * kSubBytes, 2 + j, ks)
-                               : fb.read(lds + (wc >> 1) * kSubBytes, j, ks);
+              rb[j] = (wc & 1) ? f.read(lds + kX + (wc >> 1) * kSubBytes, 2 + j, ks)
+                               : f.read(lds + kX + (wc >> 1) * kSubBytes, j, ks);
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) e[k] = entry[32 * ks + 8 * g + k];
+          for (int i = 0; i < Tile::MI; ++i)
+            ra[i] = f.read(lds + kA + (wr * (Tile::MI / 4) + i / 4) * kSubBytes, i % 4, ks);
 #pragma unroll
-          for (int i = 0; i < Tile::MI; ++i) {
-            const unsigned row = Tile::kRows * wr + 16 * i + l16;
-            s16x8 ra;
+          for (int i = 0; i < Tile::MI; ++i)
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              ra[k] = static_cast<short>((e[k] & 0xFFFFu) == row ? e[k] >> 16 : 0u);
-#pragma unroll
-            for (int j = 0; j < Tile::NJ; ++j) acc[i][j] = T::mma(rb[j], ra, acc[i][j]);
-          }
+            for (int j = 0; j < Tile::NJ; ++j) acc[i][j] = T::mma(rb[j], ra[i], acc[i][j]);
         }
-        if (q0 + 64 < all || base + kTurn < k1) __syncthreads();  // LDS is written again
       }
     }
   }

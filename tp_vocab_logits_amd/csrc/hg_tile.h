@@ -35,11 +35,12 @@
 //   half of step k+1; part 2 reads A's lower half, and loads B and A's upper
 //   half of step k+2. Each ends with vmcnt(8): everything but the newest eight
 //   loads of the wave has landed, which is what the next part reads.
-// Measured (4096 rows, V = 163840, H = 7168): logits 6.45 to 6.65 ms, 1.45 to
-// 1.49 PFLOP/s, the matrix cores busy 81 % of the cycles at 1.7 GHz, the clock
-// that the power limit leaves; the gradient's products (a column operand on one
-// or both sides) 14.5 to 14.95 ms, 1.29 to 1.33 PFLOP/s, busy 69 % at 1.78 GHz. The memory parts bound it:
-// five wait states more per load cost 3 to 5 %. Not kept, measured the same or
+// Measured (4096 rows, V = 163840, H = 7168): logits 6.45 to 6.8 ms, 1.41 to
+// 1.49 PFLOP/s, the matrix cores busy 83 % of the cycles at 1.63 to 1.7 GHz, the
+// clock that the power limit leaves; the gradient's products (a column operand on
+// one or both sides, the labels' residues included) 14.7 to 15.6 ms, 1.23 to 1.31
+// PFLOP/s, busy 68 % at 1.73 GHz. The memory parts bound it: five wait states more
+// per load cost 3 to 5 %. Not kept, measured the same or
 // slower: a third stage of B (160 KB of LDS), B's reads spread over both parts,
 // the loads spread over both parts (logits 5 % slower) or all in the second (6 %
 // slower) or among the MFMAs (15 % slower), X turned in memory for dW, workgroups

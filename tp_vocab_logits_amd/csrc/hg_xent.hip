@@ -385,8 +385,8 @@ __global__ __launch_bounds__(512, 2) void k_logits(XentPlan pl, const u32x4 *xc,
 // holds, of one row of x, 8 columns per tile, and keeps a running maximum and
 // sum over all of its columns; lanes, waves and workgroups are joined at the
 // end. As many stages as LDS holds, up to four: 64 KB or more in flight per CU.
-// HBM-bound: one row at V = 163840, H = 7168 takes 342 us, 6.87 TB/s of weights
-// (64 rows: 360 us; on 256 x 256 tiles, 2.5 rounds of the CUs, 445 and 460).
+// HBM-bound: one row at V = 163840, H = 7168 takes 343 us, 6.85 TB/s of weights
+// (64 rows: 370 us; on 256 x 256 tiles, 2.5 rounds of the CUs, 445 and 460).
 //
 // KC: a run of at most 128 or 64 rows leaves sub-tiles of the 256 empty, and
 // with them bytes in flight. Its stage holds KC = 2 or 4 times as much k instead:

@@ -93,3 +93,34 @@ def test_the_backward_pass_keeps_within_its_workspace_limit():
     lse = f64(vt.head_xent(x.detach(), w.detach(), t, 2, 16384, **p.how)[1])
     for dx, dw in got:
         p.check_grads(dx, dw, lse_used=lse)
+
+
+@gpu
+def test_both_passes_replay_in_a_graph():
+    """Captured with no other autograd graph of the same leaves alive; every
+    replay against the eager result of the same inputs."""
+    print("[gpu] autograd in a graph", flush=True)
+    p = Problem(2, 320, 136, 70, 601, left_out=0.1, z_weight=0.01)
+    x, w, t, g = leaves(p)
+    tokens = torch.randint(0, 640, (70,), generator=torch.Generator().manual_seed(1)).to(DEV)
+
+    def both(x, w):
+        loss = vt.head_loss(x + vt.embedding(tokens, w, 2, 320, 3.0), w, t, 2, 320, **p.how)
+        return (loss.detach(), *torch.autograd.grad((loss * g).sum(), (x, w)))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both(x, w)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(x, w)
+    for k in range(4):
+        with torch.no_grad():
+            x.copy_(torch.randn(x.shape, generator=torch.Generator().manual_seed(k)))
+        want = both(x.detach().clone().requires_grad_(), w.detach().clone().requires_grad_())
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), k

@@ -134,3 +134,36 @@ def test_gradients_of_two_backward_passes_add_up():
     even = torch.full_like(g, 1 / 50)
     second = vt.head_xent_grad(x.detach(), w.detach(), t, lse, even, 2, 96, **p.how)
     assert torch.equal(x.grad, first[0] + second[0]) and torch.equal(w.grad, first[1] + second[1])
+
+
+@gpu
+def test_work_arrays_past_32_bits():
+    """d of 20001 rows by 131000 entries is 5.2 GB in one piece: offsets in
+    bytes and in elements pass 32 bits."""
+    print("[gpu] large d", flush=True)
+    m, rows, vocab, hidden = 20001, 131072, 131000, 64
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(m, hidden, generator=g, device=DEV).bfloat16()
+    w = (torch.randn(rows, hidden, generator=g, device=DEV) * 0.1).bfloat16()
+    labels = torch.randint(0, vocab, (m,), generator=g, device=DEV)
+    grad = 0.5 + torch.rand(m, generator=g, device=DEV)
+    loss, lse, dx, dw = vt.head_xent_step(x, w, labels, grad, 8, rows // 8, vocab=vocab, workspace_limit=0,
+                                          dw=torch.empty(rows, hidden, device=DEV))
+    wd, want_w, at = w[:vocab].double(), torch.zeros(rows, hidden, dtype=torch.float64, device=DEV), 0
+    for rx, rt, rg, rl, rd in zip(*(v.split(2500) for v in (x, labels, grad, loss, dx))):
+        logp = torch.log_softmax(rx.double() @ wd.t(), dim=1)
+        here = torch.arange(len(rt), device=DEV)
+        # fp32 sums of 64 products and of 131000 exponentials, joined by tiles
+        assert ((rl.double() + logp[here, rt]).abs() <= 1e-5).all()
+        d = logp.exp_()
+        d[here, rt] -= 1.0
+        d *= rg[:, None].double()
+        want = d @ wd
+        # one rounding of the result; the probabilities' own are 1/362 of the label's
+        assert float((rd.double() - want).norm() / want.norm()) <= 1.1 * float(
+            (want.bfloat16().double() - want).norm() / want.norm())
+        want_w[:vocab] += d.t() @ rx.double()
+    assert float((dw.double() - want_w).norm() / want_w.norm()) <= 0.1 * 2.0 ** -8
+    assert not dw[vocab:].any()
+    del logp, d, want_w, dw
+    torch.cuda.empty_cache()

@@ -24,8 +24,8 @@ LIB = os.path.join(PKG, "libhg.so")
 SOURCES = ["hg_api.cpp", "hg_kernels.hip", "hg_lmhead.hip", "hg_static.hip", "hg_vocab_api.cpp",
            "hg_xent.hip", "hg_embed.hip"]
 ARCH = "gfx950"
-# The gradient products' loops run up to 4 % slower (dX of 4096 rows at V = 163840, H = 7168: 7.60 ms instead of 7.34)
-# where the code before them happens to end in the first half of a 64-byte line.
+# The gradient products' loops run up to 4 % slower where their code starts 16 to 28 bytes into a 64-byte line (dX of
+# 4096 rows at V = 163840, H = 7168: 7.60 ms, aligned 7.34).
 SOURCE_FLAGS = {"hg_xent.hip": ["-falign-loops=64"]}
 FASTCALL = os.path.join(PKG, "_hgcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 REF_LIB = os.path.join(PKG, "libhgref.so")  # the benchmark's reference streaming kernel

@@ -477,9 +477,9 @@ __global__ __launch_bounds__(512, 2) void k_score(XentPlan pl, const u32x4 *x, c
         acc[h][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
   };
-  // The tile's columns are done: into the running statistics. The exponentials
-  // are of exact products less a reference, which may be any number near the
-  // largest of them: its rounding takes nothing from them.
+  // The tile's columns are done: into the running statistics. An exponential is
+  // of a logit less a reference, rounded once; the reference may be any number
+  // near the largest logit, so its own rounding takes nothing from it.
   auto tile_done = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < MB; ++j) {

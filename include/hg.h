@@ -442,6 +442,84 @@ int hg_embed_grad(int tp, int shard, int hidden, int dtype, const void *tokens, 
                   int n, const void *dy, float scale, void *dw, int dw_wide, int accumulate,
                   void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Beam search on the logits. These entry points need no context and follow no
+ * page; their definitions are given here. A request has `beams` rows: row
+ * q*beams + k is beam k of request q, in the logits, the scores and the states.
+ */
+#define HG_MAX_BEAMS 64
+#define HG_MAX_KEEP 64
+
+/*
+ * The continuations to keep: of all (beam k, token v < vocab) of a request, the
+ * `keep` largest
+ *     c_kv = score_k + scale * z_kv - log sum_v exp(scale * z_kv)
+ * in descending order, equal ones by k * vocab + v. No candidate is
+ *   - a token whose logit is minus infinity or NaN (NaN counts as minus
+ *     infinity in the sum as well);
+ *   - any token of a beam whose score is not finite (its logits are not read).
+ * A finished beam stands for itself: one candidate, its score unchanged, token
+ * `pad`; its logits are not read. Logits of plus infinity share the
+ * probability of their row, its others are no candidates. Places that no
+ * candidate fills hold score minus infinity, parent -1, token -1.
+ */
+typedef struct hg_beam_shape {
+  int requests, beams, keep; /* requests >= 0; beams and keep in 1..64          */
+  int tp, shard;             /* blocks of the logits: block r is [requests *
+                                beams][shard], the vocabulary's r*shard and on;
+                                gathered rows are one block. tp at most
+                                HG_MAX_TP                                       */
+  int vocab;                 /* 1 .. tp*shard, at most 2^20                     */
+  int dtype;                 /* HG_BF16, HG_FP16 or HG_FP32                     */
+  int pad;                   /* 0 .. vocab-1                                    */
+  float scale;               /* factor of the logits, positive and finite       */
+} hg_beam_shape;
+
+/* Bytes of device workspace for hg_beam_select. */
+int hg_beam_workspace(const hg_beam_shape *s, size_t *bytes);
+
+/*
+ * logits: host array of tp device pointers, aligned to the element (rows may
+ * start anywhere); scores: device [requests][beams] fp32; finished: device
+ * [requests][beams] bytes (non-zero: finished), or NULL; out, parents, tokens:
+ * device [requests][keep], fp32, int64 (the beam k), int64. ws: device
+ * workspace, 256-byte aligned, as large as hg_beam_workspace asks (else
+ * HG_ESIZE), in use until the call's work on `stream` is done. The rows' sums
+ * and the order of candidates are in 64 bits (exponentials to 1e-10), scores
+ * are rounded once. requests == 0 does nothing. HG_EINVAL on a bad shape, a
+ * NULL or misaligned pointer, or an output overlapping an input, another output
+ * or the workspace. The same call gives the same bits.
+ */
+int hg_beam_select(const hg_beam_shape *s, const void *const *logits, const float *scores,
+                   const void *finished, float *out, long long *parents, long long *tokens,
+                   void *ws, size_t ws_bytes, void *stream);
+
+/* One state of the beams: requests*beams rows of `outer` runs; a run is `steps`
+ * positions of step_bytes, without gaps. Strides in bytes, any sign of order
+ * (rows may lie inside runs' blocks or the other way round), at least one run
+ * apart; run i of row r is at ptr + r*row_stride + i*outer_stride. */
+typedef struct hg_beam_state {
+  void *ptr;
+  long long row_stride, outer_stride;
+  long long step_bytes;
+  int outer, steps;
+} hg_beam_state;
+
+/*
+ * Every state's beams take the place of others, in place: for each request q
+ * and beam k with p = parents[q][k] in 0..beams-1, row q*beams + k becomes what
+ * row q*beams + p was. A parent outside 0..beams-1 leaves its row as it is.
+ * lengths (or NULL): only positions < lengths[q] of request q move, the others
+ * keep their bytes; lengths below 0 count as 0, above `steps` as `steps`.
+ * parents, lengths: device int32 or int64 (parent_bytes, length_bytes 4 or 8).
+ * states: host array of `count` entries. HG_EINVAL on a bad size, a NULL or
+ * misaligned pointer, or states that overlap each other, themselves, or
+ * parents or lengths.
+ */
+int hg_beam_reorder(int requests, int beams, int count, const hg_beam_state *states,
+                    const void *parents, int parent_bytes, const void *lengths, int length_bytes,
+                    void *stream);
+
 /* Static description of a status code. Not on the pages (the pages report
  * a failed build with a logged warning: API page, _install_gather source). */
 const char *hg_strerror(int code);

@@ -28,6 +28,7 @@ HG_MAX_TP = 64
 HG_BF16, HG_FP16, HG_FP32 = 0, 1, 2
 HG_XENT_SCORE, HG_XENT_GRAD, HG_XENT_STEP = 0, 1, 2
 HG_XENT_NO_DX, HG_XENT_NO_DW = 16, 32
+HG_MAX_BEAMS, HG_MAX_KEEP = 64, 64
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -44,7 +45,22 @@ class XentShape(ctypes.Structure):
         ("ignore", ctypes.c_longlong), ("scale", ctypes.c_float), ("z_weight", ctypes.c_float)]
 
 
+class BeamShape(ctypes.Structure):
+    """``hg_beam_shape``."""
+
+    _fields_ = [(n, ctypes.c_int) for n in ("requests", "beams", "keep", "tp", "shard", "vocab", "dtype", "pad")] + [
+        ("scale", ctypes.c_float)]
+
+
+class BeamState(ctypes.Structure):
+    """``hg_beam_state``."""
+
+    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_longlong), ("outer_stride", ctypes.c_longlong),
+                ("step_bytes", ctypes.c_longlong), ("outer", ctypes.c_int), ("steps", ctypes.c_int)]
+
+
 _shapep = ctypes.POINTER(XentShape)
+_beamp = ctypes.POINTER(BeamShape)
 _f = ctypes.c_float
 
 # name -> (restype, argtypes); the C declarations are in include/hg.h
@@ -77,6 +93,9 @@ SIGNATURES = {
     "hg_embed": (_i, [_i, _i, _i, _i, ctypes.POINTER(_vp), _vp, _i, _i, _f, _vp, _vp]),
     "hg_embed_workspace": (_i, [_i, _i, _i, _i, ctypes.POINTER(_size)]),
     "hg_embed_grad": (_i, [_i, _i, _i, _i, _vp, _i, _i, _vp, _f, _vp, _i, _i, _vp, _size, _vp]),
+    "hg_beam_workspace": (_i, [_beamp, ctypes.POINTER(_size)]),
+    "hg_beam_select": (_i, [_beamp, ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _vp, _vp, _size, _vp]),
+    "hg_beam_reorder": (_i, [_i, _i, _i, ctypes.POINTER(BeamState), _vp, _i, _vp, _i, _vp]),
     "hg_strerror": (ctypes.c_char_p, [_i]),
     "hg_last_error_detail": (ctypes.c_char_p, []),
 }
@@ -139,8 +158,9 @@ _FAST = None
 
 def fast():
     """The ``_hgcall`` extension, bound to the loaded library: ``gather``,
-    ``push``, ``collect``, ``stock``, ``embed``, ``embed_grad`` and ``xent``
-    (``hg_xent``, ``hg_xent_grad`` and ``hg_xent_step``) taking plain integers (handle, sizes, host-array address, rows, device address, stream)
+    ``push``, ``collect``, ``stock``, ``embed``, ``embed_grad``, ``xent``
+    (``hg_xent``, ``hg_xent_grad`` and ``hg_xent_step``), ``beam_select`` and
+    ``beam_reorder`` taking plain integers (handle, sizes, host-array address, rows, device address, stream)
     in the C argument order and returning the status code -- the same calls as
     through ctypes, with less per-call conversion."""
     global _FAST
@@ -150,7 +170,8 @@ def fast():
         handle = lib()
         _hgcall.bind(*[ctypes.cast(getattr(handle, n), ctypes.c_void_p).value
                        for n in ("hg_gather", "hg_push", "hg_collect", "hg_stock_gather", "hg_embed",
-                                  "hg_embed_grad", "hg_xent", "hg_xent_grad", "hg_xent_step")])
+                                  "hg_embed_grad", "hg_xent", "hg_xent_grad", "hg_xent_step", "hg_beam_select",
+                                  "hg_beam_reorder")])
         _FAST = _hgcall
     return _FAST
 

@@ -1,7 +1,8 @@
 /*
  * _hgcall: fast-call Python wrappers of the per-call entry points of
  * libhg.so (hg_gather, hg_push, hg_collect, hg_stock_gather, hg_embed,
- * hg_embed_grad, hg_xent, hg_xent_grad, hg_xent_step), for loops where the ctypes conversion of the arguments
+ * hg_embed_grad, hg_xent, hg_xent_grad, hg_xent_step, hg_beam_select,
+ * hg_beam_reorder), for loops where the ctypes conversion of the arguments
  * (about 0.5 us a call, 2 us with a dozen of them) is a sizeable part of a
  * call of a few microseconds.
  * Argument marshalling only: every argument is an integer (a handle, a
@@ -10,7 +11,7 @@
  * library's status code.
  *
  * The module does not link against libhg.so: bind() receives the addresses of
- * the nine entry points from the already loaded library (see _lib.fast()).
+ * these entry points from the already loaded library (see _lib.fast()).
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -52,7 +53,18 @@ static xent_fn g_xent;
 static xent_grad_fn g_xent_grad;
 static xent_step_fn g_xent_step;
 
+typedef int (*beam_select_fn)(const hg_beam_shape *s, const void *const *logits,
+                              const float *scores, const void *finished, float *out,
+                              long long *parents, long long *tokens, void *ws, size_t ws_bytes,
+                              void *stream);
+typedef int (*beam_reorder_fn)(int requests, int beams, int count, const hg_beam_state *states,
+                               const void *parents, int parent_bytes, const void *lengths,
+                               int length_bytes, void *stream);
+static beam_select_fn g_beam_select;
+static beam_reorder_fn g_beam_reorder;
+
 #define MAX_BLOCKS HG_MAX_TP
+#define ENTRIES 11
 
 static int as_ptr(PyObject *o, void **p) {
   *p = PyLong_AsVoidPtr(o);
@@ -89,16 +101,16 @@ static int as_float(PyObject *o, float *v) {
   return 1;
 }
 
-/* bind(gather, push, collect, stock, embed, embed_grad, xent, xent_grad, xent_step): their
- * addresses */
+/* bind(gather, push, collect, stock, embed, embed_grad, xent, xent_grad, xent_step, beam_select,
+ * beam_reorder): their addresses */
 static PyObject *py_bind(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
-  void *fn[9];
+  void *fn[ENTRIES];
   (void)self;
-  if (nargs != 9) {
-    PyErr_SetString(PyExc_TypeError, "bind expects nine function addresses");
+  if (nargs != ENTRIES) {
+    PyErr_SetString(PyExc_TypeError, "bind expects the address of every entry point");
     return NULL;
   }
-  for (int k = 0; k < 9; ++k) {
+  for (int k = 0; k < ENTRIES; ++k) {
     if (!as_ptr(args[k], &fn[k])) return NULL;
     if (!fn[k]) {
       PyErr_SetString(PyExc_ValueError, "bind: null function address");
@@ -114,6 +126,8 @@ static PyObject *py_bind(PyObject *self, PyObject *const *args, Py_ssize_t nargs
   g_xent = (xent_fn)fn[6];
   g_xent_grad = (xent_grad_fn)fn[7];
   g_xent_step = (xent_step_fn)fn[8];
+  g_beam_select = (beam_select_fn)fn[9];
+  g_beam_reorder = (beam_reorder_fn)fn[10];
   Py_RETURN_NONE;
 }
 
@@ -275,9 +289,98 @@ static PyObject *py_xent(PyObject *self, PyObject *const *args, Py_ssize_t nargs
   }
 }
 
+/* A tuple of addresses: 1 and `most` at most, into w. */
+static int as_blocks(PyObject *o, const void **w, int most) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) < 1 || PyTuple_GET_SIZE(o) > most) {
+    PyErr_SetString(PyExc_TypeError, "blocks must be a tuple of addresses, at most HG_MAX_TP");
+    return 0;
+  }
+  for (Py_ssize_t r = 0; r < PyTuple_GET_SIZE(o); ++r) {
+    void *p;
+    if (!as_ptr(PyTuple_GET_ITEM(o, r), &p)) return 0;
+    w[r] = p;
+  }
+  return 1;
+}
+
+/* beam_select((requests, beams, keep, shard, vocab, dtype, pad), scale, blocks, scores, finished,
+ * out, parents, tokens, ws, ws_bytes, stream) -> status; blocks: a tuple of tp device addresses */
+static PyObject *py_beam_select(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  const void *w[MAX_BLOCKS];
+  hg_beam_shape s;
+  void *scores, *finished, *out, *parents, *tokens, *ws, *stream;
+  size_t ws_bytes;
+  (void)self;
+  if (!check_bound((void *)g_beam_select, nargs, 11)) return NULL;
+  if (!PyTuple_Check(args[0]) || PyTuple_GET_SIZE(args[0]) != 7) {
+    PyErr_SetString(PyExc_TypeError, "the shape must be a tuple of seven integers");
+    return NULL;
+  }
+  int *const dims[7] = {&s.requests, &s.beams, &s.keep, &s.shard, &s.vocab, &s.dtype, &s.pad};
+  for (int k = 0; k < 7; ++k)
+    if (!as_int(PyTuple_GET_ITEM(args[0], k), dims[k])) return NULL;
+  if (!as_float(args[1], &s.scale) || !as_blocks(args[2], w, MAX_BLOCKS) ||
+      !as_ptr(args[3], &scores) || !as_ptr(args[4], &finished) || !as_ptr(args[5], &out) ||
+      !as_ptr(args[6], &parents) || !as_ptr(args[7], &tokens) || !as_ptr(args[8], &ws))
+    return NULL;
+  s.tp = (int)PyTuple_GET_SIZE(args[2]);
+  ws_bytes = PyLong_AsSize_t(args[9]);
+  if (ws_bytes == (size_t)-1 && PyErr_Occurred()) return NULL;
+  if (!as_ptr(args[10], &stream)) return NULL;
+  return PyLong_FromLong(g_beam_select(&s, w, scores, finished, out, parents, tokens, ws, ws_bytes,
+                                       stream));
+}
+
+/* beam_reorder(requests, beams, states, parents, parent_bytes, lengths, length_bytes, stream) ->
+ * status; states: a tuple of (address, (row_stride, outer_stride, step_bytes, outer, steps)) */
+static PyObject *py_beam_reorder(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  void *parents, *lengths, *stream;
+  int requests, beams, parent_bytes, length_bytes, code;
+  hg_beam_state *states;
+  Py_ssize_t count;
+  (void)self;
+  if (!check_bound((void *)g_beam_reorder, nargs, 8)) return NULL;
+  if (!as_int(args[0], &requests) || !as_int(args[1], &beams) || !as_ptr(args[3], &parents) ||
+      !as_int(args[4], &parent_bytes) || !as_ptr(args[5], &lengths) ||
+      !as_int(args[6], &length_bytes) || !as_ptr(args[7], &stream))
+    return NULL;
+  if (!PyTuple_Check(args[2]) || PyTuple_GET_SIZE(args[2]) > INT_MAX) {
+    PyErr_SetString(PyExc_TypeError, "states must be a tuple");
+    return NULL;
+  }
+  count = PyTuple_GET_SIZE(args[2]);
+  states = PyMem_Calloc(count ? (size_t)count : 1, sizeof *states);
+  if (!states) return PyErr_NoMemory();
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    PyObject *one = PyTuple_GET_ITEM(args[2], i), *g;
+    if (!PyTuple_Check(one) || PyTuple_GET_SIZE(one) != 2 ||
+        !PyTuple_Check(g = PyTuple_GET_ITEM(one, 1)) || PyTuple_GET_SIZE(g) != 5) {
+      PyErr_SetString(PyExc_TypeError, "a state must be (address, five integers)");
+      goto bad;
+    }
+    if (!as_ptr(PyTuple_GET_ITEM(one, 0), &states[i].ptr)) goto bad;
+    long long *const wide[3] = {&states[i].row_stride, &states[i].outer_stride, &states[i].step_bytes};
+    for (int k = 0; k < 3; ++k) {
+      *wide[k] = PyLong_AsLongLong(PyTuple_GET_ITEM(g, k));
+      if (*wide[k] == -1 && PyErr_Occurred()) goto bad;
+    }
+    if (!as_int(PyTuple_GET_ITEM(g, 3), &states[i].outer) ||
+        !as_int(PyTuple_GET_ITEM(g, 4), &states[i].steps))
+      goto bad;
+  }
+  code = g_beam_reorder(requests, beams, (int)count, states, parents, parent_bytes, lengths,
+                        length_bytes, stream);
+  PyMem_Free(states);
+  return PyLong_FromLong(code);
+bad:
+  PyMem_Free(states);
+  return NULL;
+}
+
 static PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)(void))py_bind, METH_FASTCALL,
-     "bind(gather, push, collect, stock, embed, embed_grad, xent, xent_grad, xent_step)"},
+     "bind(gather, push, collect, stock, embed, embed_grad, xent, xent_grad, xent_step, "
+     "beam_select, beam_reorder)"},
     {"gather", (PyCFunction)(void (*)(void))py_gather, METH_FASTCALL,
      "gather(handle, shards_addr, m, out_addr, stream) -> status"},
     {"push", (PyCFunction)(void (*)(void))py_push, METH_FASTCALL,
@@ -294,6 +397,12 @@ static PyMethodDef methods[] = {
     {"xent", (PyCFunction)(void (*)(void))py_xent, METH_FASTCALL,
      "xent(kind, shape, ignore, scale, z_weight, x, blocks, labels, grad, loss, lse, dx, dw, "
      "dw_wide, accumulate, ws, ws_bytes, stream) -> status"},
+    {"beam_select", (PyCFunction)(void (*)(void))py_beam_select, METH_FASTCALL,
+     "beam_select(shape, scale, blocks, scores, finished, out, parents, tokens, ws, ws_bytes, "
+     "stream) -> status"},
+    {"beam_reorder", (PyCFunction)(void (*)(void))py_beam_reorder, METH_FASTCALL,
+     "beam_reorder(requests, beams, states, parents, parent_bytes, lengths, length_bytes, "
+     "stream) -> status"},
     {NULL, NULL, 0, NULL},
 };
 

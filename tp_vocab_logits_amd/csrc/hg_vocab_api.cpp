@@ -5,12 +5,15 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "hg_ranges.h"
 #include "hg_vocab.h"
 
 #define HG_API extern "C" __attribute__((visibility("default")))
 
 namespace {
 
+using hg::aligned;
+using hg::Ranges;
 using hg::VocabMatrix;
 using hg::XentPlan;
 
@@ -23,30 +26,6 @@ using hg::XentPlan;
 constexpr int kCus = 256;  // compute units of the one device these kernels are built for
 constexpr int kTile = 256, kStep = 64;
 constexpr long long kMaxTiles = 1 << 22;  // of 512 lanes: a launch has fewer than 2^32 lanes
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Address ranges of a call; an output may overlap nothing else.
-struct Ranges {
-  struct One {
-    uintptr_t at;
-    size_t bytes;
-    bool written;
-  };
-  One r[HG_MAX_TP + 12];
-  int n = 0;
-  void add(const void *p, size_t bytes, bool written) {
-    if (bytes) r[n++] = {reinterpret_cast<uintptr_t>(p), bytes, written};
-  }
-  bool clash() const {
-    for (int i = 0; i < n; ++i)
-      for (int j = 0; j < i; ++j)
-        if ((r[i].written || r[j].written) && r[i].at < r[j].at + r[j].bytes &&
-            r[j].at < r[i].at + r[i].bytes)
-          return true;
-    return false;
-  }
-};
 
 int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }

@@ -443,6 +443,70 @@ int hg_embed_grad(int tp, int shard, int hidden, int dtype, const void *tokens, 
                   void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * Low-rank adapters beside the shared head: every row has one of `adapters`
+ * pairs (A_i [rank][hidden], B_i [tp*shard][rank]), or none. These entry points
+ * need no context and follow no page; their definitions are given here.
+ */
+#define HG_MAX_RANK 256
+
+typedef struct hg_adapt_shape {
+  int tp, shard, hidden; /* the head; shard and hidden multiples of 8, hidden at
+                            most 2^20, tp*shard below 2^29, tp at most HG_MAX_TP */
+  int m;                 /* rows, at most 2^24; m x tp*shard at most 2^40        */
+  int adapters;          /* pairs, 1 .. 2^15; x tp*shard/64 and x hidden/64 below
+                            2^23 for gradients                                  */
+  int rank;              /* a multiple of 8, 8 .. HG_MAX_RANK                    */
+  int dtype;             /* HG_BF16 or HG_FP16: x, y, A, B, 16-bit gradients     */
+  int index_bytes;       /* 4 or 8: the index is int32 or int64                  */
+} hg_adapt_shape;
+
+/* What a workspace is for. */
+#define HG_ADAPT_ADD 0
+#define HG_ADAPT_GRAD 1
+
+/* Bytes of device workspace for a call of the given kind. */
+int hg_adapt_workspace(const hg_adapt_shape *s, int kind, size_t *bytes);
+
+/*
+ * What the rows' adapters add to a product beside them: for row j with
+ * i = index[j] in 0 .. adapters-1
+ *     out_j = y_j + scale_i * B_i (A_i x_j)
+ * and out_j = y_j, bit for bit, for any other index (its x is not used).
+ * y, out: device [tp][m][shard], as hg_lmhead leaves its shards in one buffer;
+ * out may be y (rows without an adapter are then not written), and overlaps
+ * nothing else. x: device [m][hidden]; a: device [adapters][rank][hidden]; b:
+ * device [adapters][tp*shard][rank]; scale: device [adapters] fp32, or NULL for
+ * ones; index: device [m]. Sums are fp32, the low-rank values are held to 2^-16
+ * of themselves (bf16) or 2^-21 of the row's largest (fp16), each result is
+ * rounded once.
+ * All pointers but scale and index 16-byte aligned. ws: device workspace,
+ * 256-byte aligned, as large as hg_adapt_workspace asks (else HG_ESIZE), in use
+ * until the call's work on `stream` is done. m == 0 does nothing. HG_EINVAL on
+ * a bad shape, a NULL or misaligned pointer, or an overlap. The same call gives
+ * the same bits.
+ */
+int hg_adapt(const hg_adapt_shape *s, const void *y, const void *x, const void *a, const void *b,
+             const float *scale, const void *index, void *out, void *ws, size_t ws_bytes,
+             void *stream);
+
+/*
+ * The gradients for an upstream dy ([tp][m][shard]; y's own gradient is dy):
+ *     g_j  = scale_i * B_i^T dy_j
+ *     dx_j = A_i^T g_j                             [m][hidden] in dtype; 0 without
+ *                                                  an adapter
+ *     da_i = sum over j of i, g_j x_j^T            [adapters][rank][hidden]
+ *     db_i = sum over j of i, scale_i dy_j u_j^T   [adapters][tp*shard][rank], with
+ *                                                  u_j = A_i x_j
+ * da, db: in dtype, or fp32 if wide; zeros for an adapter that no row has. Each
+ * of dx, da and db may be NULL and is then not computed, not all three. Sums are
+ * fp32, over the rows in their order; g and u are held as in hg_adapt (fp16: to
+ * 2^-21 of the call's largest). m == 0 zeroes da and db. The rest is as above.
+ */
+int hg_adapt_grad(const hg_adapt_shape *s, const void *dy, const void *x, const void *a,
+                  const void *b, const float *scale, const void *index, void *dx, void *da,
+                  void *db, int wide, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Beam search on the logits. These entry points need no context and follow no
  * page; their definitions are given here. A request has `beams` rows: row
  * q*beams + k is beam k of request q, in the logits, the scores and the states.

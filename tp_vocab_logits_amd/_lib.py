@@ -29,6 +29,8 @@ HG_BF16, HG_FP16, HG_FP32 = 0, 1, 2
 HG_XENT_SCORE, HG_XENT_GRAD, HG_XENT_STEP = 0, 1, 2
 HG_XENT_NO_DX, HG_XENT_NO_DW = 16, 32
 HG_MAX_BEAMS, HG_MAX_KEEP = 64, 64
+HG_MAX_RANK = 256
+HG_ADAPT_ADD, HG_ADAPT_GRAD = 0, 1
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -59,7 +61,14 @@ class BeamState(ctypes.Structure):
                 ("step_bytes", ctypes.c_longlong), ("outer", ctypes.c_int), ("steps", ctypes.c_int)]
 
 
+class AdaptShape(ctypes.Structure):
+    """``hg_adapt_shape``."""
+
+    _fields_ = [(n, ctypes.c_int) for n in ("tp", "shard", "hidden", "m", "adapters", "rank", "dtype", "index_bytes")]
+
+
 _shapep = ctypes.POINTER(XentShape)
+_adaptp = ctypes.POINTER(AdaptShape)
 _beamp = ctypes.POINTER(BeamShape)
 _f = ctypes.c_float
 
@@ -93,6 +102,9 @@ SIGNATURES = {
     "hg_embed": (_i, [_i, _i, _i, _i, ctypes.POINTER(_vp), _vp, _i, _i, _f, _vp, _vp]),
     "hg_embed_workspace": (_i, [_i, _i, _i, _i, ctypes.POINTER(_size)]),
     "hg_embed_grad": (_i, [_i, _i, _i, _i, _vp, _i, _i, _vp, _f, _vp, _i, _i, _vp, _size, _vp]),
+    "hg_adapt_workspace": (_i, [_adaptp, _i, ctypes.POINTER(_size)]),
+    "hg_adapt": (_i, [_adaptp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _size, _vp]),
+    "hg_adapt_grad": (_i, [_adaptp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _size, _vp]),
     "hg_beam_workspace": (_i, [_beamp, ctypes.POINTER(_size)]),
     "hg_beam_select": (_i, [_beamp, ctypes.POINTER(_vp), _vp, _vp, _vp, _vp, _vp, _vp, _size, _vp]),
     "hg_beam_reorder": (_i, [_i, _i, _i, ctypes.POINTER(BeamState), _vp, _i, _vp, _i, _vp]),
@@ -159,8 +171,8 @@ _FAST = None
 def fast():
     """The ``_hgcall`` extension, bound to the loaded library: ``gather``,
     ``push``, ``collect``, ``stock``, ``embed``, ``embed_grad``, ``xent``
-    (``hg_xent``, ``hg_xent_grad`` and ``hg_xent_step``), ``beam_select`` and
-    ``beam_reorder`` taking plain integers (handle, sizes, host-array address, rows, device address, stream)
+    (``hg_xent``, ``hg_xent_grad`` and ``hg_xent_step``), ``beam_select``,
+    ``beam_reorder``, ``adapt`` and ``adapt_grad`` taking plain integers (handle, sizes, host-array address, rows, device address, stream)
     in the C argument order and returning the status code -- the same calls as
     through ctypes, with less per-call conversion."""
     global _FAST
@@ -171,7 +183,7 @@ def fast():
         _hgcall.bind(*[ctypes.cast(getattr(handle, n), ctypes.c_void_p).value
                        for n in ("hg_gather", "hg_push", "hg_collect", "hg_stock_gather", "hg_embed",
                                   "hg_embed_grad", "hg_xent", "hg_xent_grad", "hg_xent_step", "hg_beam_select",
-                                  "hg_beam_reorder")])
+                                  "hg_beam_reorder", "hg_adapt", "hg_adapt_grad")])
         _FAST = _hgcall
     return _FAST
 

@@ -22,7 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libhg.so")
 SOURCES = ["hg_api.cpp", "hg_kernels.hip", "hg_lmhead.hip", "hg_static.hip", "hg_vocab_api.cpp",
-           "hg_xent.hip", "hg_embed.hip", "hg_beam_api.cpp", "hg_beam.hip"]
+           "hg_xent.hip", "hg_embed.hip", "hg_beam_api.cpp", "hg_beam.hip",
+           "hg_adapt_api.cpp", "hg_adapt.hip"]
 ARCH = "gfx950"
 # The gradient products' loops run up to 4 % slower where their code starts 16 to 28 bytes into a 64-byte line (dX of
 # 4096 rows at V = 163840, H = 7168: 7.60 ms, aligned 7.34).

@@ -1,0 +1,71 @@
+// Internal declarations of the low-rank adapters (hg_adapt.hip). The C ABI is in
+// include/hg.h; argument checks and workspace layout in hg_adapt_api.cpp.
+#pragma once
+
+#include "hg_vocab.h"
+
+namespace hg {
+
+// Up to this many rows hg_adapt goes through them as they are, without a sort.
+constexpr int kFewRows = 64;
+constexpr int kRankChunk = 64;  // ranks that a workgroup holds at once
+
+// A matrix of 16-bit elements in blocks: column c of row j is at
+// ((c / shard) * m + j) * shard + c % shard. One block is a plain matrix.
+struct Blocked {
+  const void *p;
+  int blocks, shard;
+};
+
+// The rows' adapters: sorted by adapter (keys ascending, rows without one last),
+// or as the caller gave them (keys NULL).
+struct AdaptRows {
+  const int *keys, *pos;
+  const void *index;
+  int index_bytes;
+};
+
+struct AdaptPlan {
+  int m, adapters, rank, hidden, tp, shard;
+  bool half, sorted;
+  SortPlan sort;
+  int split_u, split_g;  // parts of the sums over hidden and over the vocabulary
+  int padded;            // rows, up to a multiple of 32
+  void *sort_ws;
+  float *pu, *pg;        // [split][m][rank] partial sums of u and g
+  float *u, *g;          // [m][rank] scaled sums, by sorted position
+  int *head;             // [0], [1]: bits of the largest |u| and |g|
+  int *seg;              // [adapters + 1] sorted positions where they begin
+  unsigned short *ut, *gt;  // [2][ranks][padded] upper and lower halves of u and g
+  unsigned short *at;    // [adapters][hidden][rank]: A turned
+};
+
+// pu or pg: the products of `of` with A (turned = false: w is [adapters][rank][columns])
+// or B (true: w is [adapters][columns][rank]), in `splits` parts.
+hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocked &of, const void *w,
+                            bool turned, int splits, float *part, hipStream_t s);
+// out = y + (sum of the parts) W^T per row; y NULL: zeros.
+hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *part, int splits,
+                           const float *scale, const void *w, const Blocked &y, void *out,
+                           hipStream_t s);
+// The sorted rows' segments; clears head.
+hipError_t launch_adapt_segments(const AdaptPlan &p, const AdaptRows &r, hipStream_t s);
+// u and g from their parts, scaled; their largest.
+hipError_t launch_adapt_join(const AdaptPlan &p, const AdaptRows &r, const float *scale, hipStream_t s);
+// Their halves, by rank.
+hipError_t launch_adapt_halves(const AdaptPlan &p, hipStream_t s);
+// sum over an adapter's rows of low^T x wide: [adapters][rank][columns], or
+// [adapters][columns][rank] if turned.
+hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Blocked &of,
+                              const unsigned short *low, const int *largest, bool turned, bool wide,
+                              void *out, hipStream_t s);
+hipError_t launch_adapt_turn(const AdaptPlan &p, const void *a, hipStream_t s);
+
+// Whether hg_adapt's second product takes big pieces (64 rows x 1024 columns per
+// workgroup) or small ones (16 x 256).
+inline bool adapt_big(int m, int rank) { return m > kFewRows && rank <= kRankChunk; }
+
+// Parts that a sum over `columns` columns of `m` rows is cut into.
+int adapt_splits(int m, int blocks, int shard, int rank, bool few);
+
+}  // namespace hg

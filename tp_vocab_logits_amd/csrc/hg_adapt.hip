@@ -1,0 +1,819 @@
+// Low-rank adapters of many requests beside the shared head, and their gradients.
+//
+//   u_j = A_i x_j,  out_j = y_j + s_i B_i u_j            i = index[j]
+//   g_j = s_i B_i^T dy_j,  dx_j = A_i^T g_j,  dA_i = sum_j g_j x_j^T,
+//   dB_i = sum_j s_i dy_j u_j^T
+//
+// Everything with a side of the vocabulary's length is bound by HBM: y read and
+// written, dy, B, dB. The products run on the matrix cores all the same
+// (v_mfma_f32_16x16x32, tiles of 16 rows), so that nothing else comes near.
+//
+// Rows. A tile is 16 rows next to each other, sorted by adapter (a few rows go as
+// they are). A tile with rows of several adapters runs through each of them and
+// every row takes its own one's result: no tile lists, y passes once whatever the
+// mixture, and no value of one adapter (an infinity in its B) reaches the rows of
+// another.
+//
+// Precision. u and g are fp32 sums that enter a second product of 16-bit operands.
+// They enter as the sum of two 16-bit numbers, so that what is lost is 2^-16 of
+// them; rounded to bf16 alone they would add as much error to a row as its own
+// final rounding. For fp16 they are first scaled by a power of two.
+#include <type_traits>
+
+#include "hg_adapt.h"
+#include "hg_tile.h"
+
+namespace hg {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ int key_of_row(const AdaptRows &r, int p, int adapters) {
+  if (r.keys) return r.keys[p];
+  const long long i = r.index_bytes == 8 ? static_cast<const long long *>(r.index)[p]
+                                         : static_cast<const int *>(r.index)[p];
+  return i >= 0 && i < adapters ? static_cast<int>(i) : adapters;
+}
+__device__ __forceinline__ int row_of(const AdaptRows &r, int p) { return r.keys ? r.pos[p] : p; }
+
+__device__ __forceinline__ s16x8 load8(const unsigned short *p) {
+  return *reinterpret_cast<const s16x8 *>(p);
+}
+__device__ __forceinline__ s16x8 zero8() { return s16x8{0, 0, 0, 0, 0, 0, 0, 0}; }
+
+// A power of two that brings `largest` to 1 .. 2 (1 for bf16, whose exponent
+// needs none), and its inverse. Nothing to scale: 1.
+template <class T>
+__device__ __forceinline__ float to_unit(float largest) {
+  if constexpr (!T::kHalf) return 1.f;
+  const uint32_t e = __builtin_bit_cast(uint32_t, largest) >> 23 & 255;
+  return e == 0 || e > 250 ? 1.f : __builtin_bit_cast(float, (254 - e) << 23);
+}
+template <class T>
+__device__ __forceinline__ float from_unit(float largest) {
+  if constexpr (!T::kHalf) return 1.f;
+  const uint32_t e = __builtin_bit_cast(uint32_t, largest) >> 23 & 255;
+  return e == 0 || e > 250 ? 1.f : __builtin_bit_cast(float, e << 23);
+}
+
+// f as upper + lower.
+template <class T>
+__device__ __forceinline__ void halves(float f, uint32_t &hi, uint32_t &lo) {
+  hi = bits16<T>(f);
+  const float rest = f - from16<T>(hi);
+  lo = rest == rest ? bits16<T>(rest) : 0u;  // (an infinity leaves none)
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: u of one row, or a part of it, per workgroup. A lane holds 8 elements
+// of x and meets them with those of each rank's row of A.
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void k_adapt_row(AdaptRows rows, const unsigned short *x,
+                                                        const unsigned short *a, int adapters, int m,
+                                                        int rank, int hidden, int splits, float *part) {
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int j = static_cast<int>(blockIdx.x) / splits, split = static_cast<int>(blockIdx.x) - j * splits;
+  const int i = key_of_row(rows, j, adapters);
+  if (i >= adapters) return;
+  const unsigned short *const xr = x + static_cast<size_t>(row_of(rows, j)) * hidden;
+  const unsigned short *const ai = a + static_cast<size_t>(i) * rank * hidden;
+  float *const out = part + (static_cast<size_t>(split) * m + j) * rank;
+  const int steps = (hidden + 511) / 512, from = steps * split / splits, to = steps * (split + 1) / splits;
+  constexpr int kRows = 4;  // ranks at once per wave
+  for (int r0 = wave * kRows; r0 < rank; r0 += 4 * kRows) {  // (rank is a multiple of 8)
+    float sum[kRows] = {0.f, 0.f, 0.f, 0.f};
+    for (int step = from; step < to; ++step) {
+      const int k = step * 512 + lane * 8;
+      if (k >= hidden) continue;
+      const s16x8 xv = load8(xr + k);
+      s16x8 av[kRows];
+#pragma unroll
+      for (int t = 0; t < kRows; ++t) av[t] = load8(ai + static_cast<size_t>(r0 + t) * hidden + k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float f = from16<T>(static_cast<unsigned short>(xv[e]));
+#pragma unroll
+        for (int t = 0; t < kRows; ++t)
+          sum[t] = __builtin_fmaf(f, from16<T>(static_cast<unsigned short>(av[t][e])), sum[t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kRows; ++t) {
+#pragma unroll
+      for (int d = 32; d; d >>= 1) sum[t] += __shfl_xor(sum[t], d);
+      if (lane == t) out[r0 + t] = sum[t];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Low-rank products of many rows: part[split][p][rank] = sum over the split's
+// columns of of[p][c] w_i[rank][c]. A workgroup has TT tiles of rows, a part of
+// the columns and up to 64 ranks (RB blocks of 16); its waves take every fourth
+// chunk of 64 columns. w's columns are next to each other in memory (A), or, if
+// TURNED, its ranks are (B): those chunks go through LDS and are turned while
+// they are read from it.
+
+struct LowArgs {
+  AdaptRows rows;
+  const unsigned short *of, *w;
+  int m, adapters, rank;
+  int blocks, shard, per_block, chunks;  // chunks of 64 columns per block, in all
+  int splits;
+  float *part;
+};
+
+template <class T, bool TURNED, int RB, int TT>
+__global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
+  constexpr int kRow = RB * 32 + 16;                // bytes of an LDS row of 16*RB ranks
+  constexpr int kStage = TURNED ? 64 * kRow : 0;    // per wave
+  constexpr int kSum = TT * 16 * RB * 16 * 4;       // a wave's sums
+  constexpr int kLds = 4 * kStage > 2 * kSum ? 4 * kStage : 2 * kSum;
+  __shared__ __align__(16) unsigned char lds[kLds];
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int ml = lane & 15, g = lane >> 4;
+  const int groups = (a.m + TT * 16 - 1) / (TT * 16);
+  const int split = static_cast<int>(blockIdx.x) / groups, group = static_cast<int>(blockIdx.x) - split * groups;
+  const int rc = static_cast<int>(blockIdx.y) * kRankChunk;
+  const int ranks = a.rank - rc < RB * 16 ? a.rank - rc : RB * 16;  // a multiple of 8
+  const int from = static_cast<int>(static_cast<long long>(a.chunks) * split / a.splits);
+  const int to = static_cast<int>(static_cast<long long>(a.chunks) * (split + 1) / a.splits);
+  const int p0 = group * TT * 16;
+  const int pend = a.m < p0 + TT * 16 ? a.m : p0 + TT * 16;
+  const size_t columns = static_cast<size_t>(a.blocks) * a.shard;
+
+  int key[TT];
+  const unsigned short *src[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int p = p0 + t * 16 + ml;
+    key[t] = p < a.m ? a.rows.keys[p] : a.adapters;
+    src[t] = a.of + static_cast<size_t>(p < a.m ? a.rows.pos[p] : 0) * a.shard;
+  }
+  int cur = __builtin_amdgcn_readfirstlane(key[0]);
+  while (cur < a.adapters) {
+    bool active[TT];
+    int done = 0;
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      active[t] = __ballot(key[t] == cur) != 0;
+      done += __popcll(__ballot(key[t] <= cur) & 0xFFFF);
+    }
+    f32x4 acc[TT][RB];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int b = 0; b < RB; ++b) acc[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const unsigned short *const wi = a.w + static_cast<size_t>(cur) * a.rank * columns;
+
+    for (int chunk = from + wave; chunk < to; chunk += 4) {
+      const int block = chunk / a.per_block, c0 = (chunk - block * a.per_block) * 64;
+      const int left = a.shard - c0;  // columns of the block from here on
+      const size_t at = static_cast<size_t>(block) * a.m * a.shard + c0;
+      const size_t col = static_cast<size_t>(block) * a.shard + c0;
+      s16x8 xf[TT][2], wf[RB][2];
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const int c = ks * 32 + 8 * g;
+          xf[t][ks] = active[t] && c < left ? load8(src[t] + at + c) : zero8();
+        }
+      if constexpr (TURNED) {
+        unsigned char *const st = lds + wave * kStage;
+        // 64 rows (columns of the product) of 16*RB ranks: 16-byte pieces
+        constexpr int kPieces = RB * 2;
+        s16x8 piece[kPieces];
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+          const int id = q * 64 + lane, v = id / kPieces, e = (id % kPieces) * 8;
+          piece[q] = v < left && e < ranks ? load8(wi + (col + v) * a.rank + rc + e) : zero8();
+        }
+        wait_lds();  // the last chunk's reads
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+          const int id = q * 64 + lane, v = id / kPieces, e = (id % kPieces) * 8;
+          *reinterpret_cast<s16x8 *>(st + v * kRow + e * 2) = piece[q];
+        }
+        wait_lds();
+        __builtin_amdgcn_wave_barrier();
+        typedef __attribute__((address_space(3))) s16x4 *lds4;
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            unsigned char *const q = st + (ks * 32 + g * 8 + (ml >> 2)) * kRow + b * 32 + (ml & 3) * 8;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q + 4 * kRow));
+            wf[b][ks] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          }
+      } else {
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            const int c = ks * 32 + 8 * g;
+            wf[b][ks] = c < left && b * 16 + ml < ranks
+                            ? load8(wi + static_cast<size_t>(rc + b * 16 + ml) * columns + col + c)
+                            : zero8();
+          }
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int b = 0; b < RB; ++b)
+            if (active[t]) acc[t][b] = T::mma(wf[b][ks], xf[t][ks], acc[t][b]);
+    }
+
+    // the four waves' sums, in a fixed order: (0 + 2) + (1 + 3)
+    auto slot = [&](int w, int t, int b) __attribute__((always_inline)) {
+      return reinterpret_cast<f32x4 *>(lds + w * kSum) + (t * RB + b) * 64 + lane;
+    };
+    __syncthreads();
+    if (wave >= 2)
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) *slot(wave - 2, t, b) = acc[t][b];
+    __syncthreads();
+    if (wave < 2)
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) acc[t][b] += *slot(wave, t, b);
+    __syncthreads();
+    if (wave == 1)
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) *slot(0, t, b) = acc[t][b];
+    __syncthreads();
+    if (wave == 0)
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          const f32x4 sum = acc[t][b] + *slot(0, t, b);
+          const int r = b * 16 + 4 * g;
+          if (key[t] == cur && r < ranks)
+            *reinterpret_cast<f32x4 *>(a.part + (static_cast<size_t>(split) * a.m + p0 + t * 16 + ml) * a.rank +
+                                       rc + r) = sum;
+        }
+    __syncthreads();
+    const int next = p0 + done;
+    cur = next < pend ? a.rows.keys[next] : a.adapters;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// out = y + low W^T: W is [adapters][columns][rank]. A workgroup has TT tiles of
+// rows and kCol blocks of 64 columns for each of its four waves. A lane of a tile
+// holds one row's 8 + 8 columns: the rows of W are dealt to the matrix cores' rows
+// so that these are next to each other (stores of 64 bytes per row).
+
+struct UpArgs {
+  AdaptRows rows;
+  const float *part;
+  const float *scale;
+  const unsigned short *w, *y;
+  unsigned short *out;
+  int m, adapters, rank, splits;
+  int blocks, shard, per_block, chunks;  // chunks of 64 columns per block, in all
+  int groups, strips;
+};
+
+// KS: steps of 32 ranks held at once: 0 for up to 16 ranks (upper and lower halves
+// share one step), 2 otherwise (more than 64 ranks: in turns).
+template <class T, int KS, int TT, int COL>
+__global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
+  constexpr int kRanks = KS == 0 ? 16 : TT > 1 ? kRankChunk : HG_MAX_RANK;
+  constexpr int kRow = 2 * kRanks + 8;  // 16-bit elements of an LDS row: upper, lower halves
+  constexpr int kPer = kThreads / (TT * 16);  // threads per row of the prologue
+  constexpr int kPieces = (kRanks / 8 + kPer - 1) / kPer;
+  constexpr int KF = KS ? KS : 1;
+  __shared__ __align__(16) unsigned short low[TT * 16 * kRow];
+  __shared__ float back[TT * 16];
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ml = lane & 15, g = lane >> 4;
+  // Row groups of one strip of columns go to one XCD (workgroups are dealt to the
+  // eight in turn): they share W's strip in its L2.
+  const int id = static_cast<int>(blockIdx.x);
+  const int eight = id / (8 * a.groups), in = id - eight * 8 * a.groups;
+  const int strip = eight * 8 + in % 8, group = in / 8;
+  if (strip >= a.strips) return;
+  const int p0 = group * TT * 16;
+
+  {
+    const int r = tid / kPer, sub = tid % kPer, p = p0 + r;
+    const int key = p < a.m ? key_of_row(a.rows, p, a.adapters) : a.adapters;
+    float v[kPieces][8];
+    float largest = 0.f;
+    const float s = key < a.adapters && a.scale ? a.scale[key] : 1.f;
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+      const int e = (q * kPer + sub) * 8;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) v[q][t] = 0.f;
+      if (key < a.adapters && e < a.rank) {
+        for (int k = 0; k < a.splits; ++k) {
+          const f32x4 *const from =
+              reinterpret_cast<const f32x4 *>(a.part + (static_cast<size_t>(k) * a.m + p) * a.rank + e);
+          const f32x4 lo = from[0], hi = from[1];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            v[q][t] += lo[t];
+            v[q][4 + t] += hi[t];
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        v[q][t] *= s;
+        largest = fmaxf(largest, fabsf(v[q][t]));
+      }
+    }
+    if constexpr (T::kHalf) {
+#pragma unroll
+      for (int d = 1; d < kPer; d <<= 1) largest = fmaxf(largest, __shfl_xor(largest, d));
+    }
+    const float unit = to_unit<T>(largest);
+    if (sub == 0) back[r] = from_unit<T>(largest);
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+      const int e = (q * kPer + sub) * 8;
+      if (e < kRanks) {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          uint32_t h0, l0, h1, l1;
+          halves<T>(v[q][2 * t] * unit, h0, l0);
+          halves<T>(v[q][2 * t + 1] * unit, h1, l1);
+          hi[t] = h0 | h1 << 16;
+          lo[t] = l0 | l1 << 16;
+        }
+        *reinterpret_cast<u32x4 *>(low + r * kRow + e) = hi;
+        *reinterpret_cast<u32x4 *>(low + r * kRow + kRanks + e) = lo;
+      }
+    }
+  }
+  int key[TT];
+  size_t row[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int p = p0 + t * 16 + ml;
+    key[t] = p < a.m ? key_of_row(a.rows, p, a.adapters) : -1;  // -1: no row
+    row[t] = static_cast<size_t>(p < a.m ? row_of(a.rows, p) : 0) * a.shard;
+  }
+  __syncthreads();
+
+  const int turns = KS == 0 ? 1 : (a.rank + kRankChunk - 1) / kRankChunk;
+  const bool in_place = a.y == a.out;
+#pragma unroll 1
+  for (int c = 0; c < COL; ++c) {
+    const int chunk = (strip * COL + c) * 4 + wave;
+    if (chunk >= a.chunks) break;
+    const int block = chunk / a.per_block, c0 = (chunk - block * a.per_block) * 64;
+    const int left = a.shard - c0;
+    const size_t at = static_cast<size_t>(block) * a.m * a.shard + c0;
+    const unsigned short *const wcol = a.w + (static_cast<size_t>(block) * a.shard + c0) * a.rank;
+    const size_t each = static_cast<size_t>(a.blocks) * a.shard * a.rank;
+    s16x8 yv[TT][2];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        yv[t][h] = a.y && key[t] >= 0 && h * 32 + 8 * g < left ? load8(a.y + at + row[t] + h * 32 + 8 * g)
+                                                               : zero8();
+    int have = -1;
+    s16x8 wf[4][KF];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      f32x4 res[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) res[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+      unsigned todo = static_cast<unsigned>(__ballot(key[t] >= 0 && key[t] < a.adapters)) & 0xFFFF;
+      while (todo) {
+        const int cur = __builtin_amdgcn_readlane(key[t], __builtin_ctz(todo));
+        todo &= ~static_cast<unsigned>(__ballot(key[t] == cur));
+        f32x4 acc[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int turn = 0; turn < turns; ++turn) {
+          const int rc = turn * kRankChunk;
+          if (have != cur || turns > 1) {
+            const unsigned short *const wi = wcol + static_cast<size_t>(cur) * each;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int col = 32 * (v >> 1) + 8 * (ml >> 2) + 4 * (v & 1) + (ml & 3);
+#pragma unroll
+              for (int ks = 0; ks < KF; ++ks) {
+                const int r = KS == 0 ? 8 * (g & 1) : rc + ks * 32 + 8 * g;
+                wf[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
+              }
+            }
+            have = cur;
+          }
+          const unsigned short *const mine = low + (t * 16 + ml) * kRow + rc;
+#pragma unroll
+          for (int ks = 0; ks < KF; ++ks) {
+            if constexpr (KS == 0) {
+              const s16x8 both = load8(mine + 8 * g);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[v] = T::mma(wf[v][0], both, acc[v]);
+            } else {
+              const s16x8 hi = load8(mine + ks * 32 + 8 * g), lo = load8(mine + kRanks + ks * 32 + 8 * g);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[v] = T::mma(wf[v][ks], hi, acc[v]);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[v] = T::mma(wf[v][ks], lo, acc[v]);
+            }
+          }
+        }
+        const bool take = key[t] == cur;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) res[v][e] = take ? acc[v][e] : res[v][e];
+      }
+      const bool has = key[t] < a.adapters;
+      if (key[t] < 0 || (in_place && !has)) continue;
+      const float inv = back[t * 16 + ml];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h * 32 + 8 * g >= left) continue;
+        u32x4 o = __builtin_bit_cast(u32x4, yv[t][h]);
+        if (has) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f0 = __builtin_fmaf(res[2 * h + (e >> 1)][(2 * e) & 3], inv,
+                                            from16<T>(static_cast<unsigned short>(yv[t][h][2 * e])));
+            const float f1 = __builtin_fmaf(res[2 * h + (e >> 1)][(2 * e + 1) & 3], inv,
+                                            from16<T>(static_cast<unsigned short>(yv[t][h][2 * e + 1])));
+            o[e] = bits16<T>(f0) | bits16<T>(f1) << 16;
+          }
+        }
+        *reinterpret_cast<u32x4 *>(a.out + at + row[t] + h * 32 + 8 * g) = o;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The gradients' small pieces.
+
+// seg[i]: the first sorted position of adapter i or a later one.
+__global__ __launch_bounds__(kThreads) void k_adapt_segments(const int *keys, int m, int adapters,
+                                                             int *seg, int *head) {
+  const int j = static_cast<int>(blockIdx.x * kThreads + threadIdx.x);
+  if (j == 0) head[0] = head[1] = 0;
+  if (j > m) return;
+  const int before = j > 0 ? keys[j - 1] : -1, here = j < m ? keys[j] : adapters;
+  for (int i = before + 1; i <= here && i <= adapters; ++i) seg[i] = j;
+}
+
+// The parts' sums, scaled, and their largest: blockIdx.y 0: u, 1: g.
+struct JoinSide {
+  const float *part;
+  float *sum;
+  int splits;
+};
+__global__ __launch_bounds__(kThreads) void k_adapt_join(JoinSide u, JoinSide g, const int *keys,
+                                                         const float *scale, int m, int adapters,
+                                                         int rank, int *head) {
+  const JoinSide side = blockIdx.y ? g : u;
+  const size_t n = static_cast<size_t>(m) * rank;
+  float largest = 0.f;
+  if (side.splits)
+    for (size_t k = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) * 4; k < n;
+         k += static_cast<size_t>(gridDim.x) * kThreads * 4) {
+      const int key = keys[k / rank];  // (four ranks are of one row)
+      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+      if (key < adapters) {
+        for (int s = 0; s < side.splits; ++s) sum += *reinterpret_cast<const f32x4 *>(side.part + s * n + k);
+        const float f = scale ? scale[key] : 1.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sum[e] *= f;
+          const float size = fabsf(sum[e]);
+          if (size > largest && size < __builtin_inff()) largest = size;
+        }
+      }
+      *reinterpret_cast<f32x4 *>(side.sum + k) = sum;
+    }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) largest = fmaxf(largest, __shfl_xor(largest, d));
+  // (the largest of all does not depend on the order)
+  if ((threadIdx.x & 63) == 0 && largest > 0.f)
+    atomicMax(head + blockIdx.y, static_cast<int>(__builtin_bit_cast(uint32_t, largest)));
+}
+
+// low [m][rank] -> [2][rank][padded], upper and lower halves, zeros past m.
+// blockIdx.y 0: u, 1: g. A workgroup turns 64 rows of 32 ranks.
+struct HalvesSide {
+  const float *low;
+  unsigned short *out;
+};
+template <class T>
+__global__ __launch_bounds__(kThreads) void k_adapt_halves(HalvesSide u, HalvesSide g, const int *head,
+                                                           int m, int rank, int padded) {
+  const HalvesSide side = blockIdx.y ? g : u;
+  if (!side.out) return;
+  __shared__ float t[64][33];
+  const float unit = to_unit<T>(__builtin_bit_cast(float, head[blockIdx.y]));
+  const int p0 = static_cast<int>(blockIdx.x) * 64, r0 = static_cast<int>(blockIdx.z) * 32;
+  for (int k = static_cast<int>(threadIdx.x); k < 64 * 32; k += kThreads) {
+    const int p = p0 + k / 32, r = r0 + k % 32;
+    t[k / 32][k % 32] = p < m && r < rank ? side.low[static_cast<size_t>(p) * rank + r] * unit : 0.f;
+  }
+  __syncthreads();
+  for (int k = static_cast<int>(threadIdx.x); k < 64 * 32; k += kThreads) {
+    const int p = p0 + k % 64, r = r0 + k / 64;
+    if (p >= padded || r >= rank) continue;
+    uint32_t hi, lo;
+    halves<T>(t[k % 64][k / 64], hi, lo);
+    side.out[static_cast<size_t>(r) * padded + p] = static_cast<unsigned short>(hi);
+    side.out[static_cast<size_t>(rank + r) * padded + p] = static_cast<unsigned short>(lo);
+  }
+}
+
+// A [rank][hidden] -> [hidden][rank] of each adapter that has rows, 64 x 64.
+__global__ __launch_bounds__(kThreads) void k_adapt_turn(const unsigned short *a, unsigned short *at,
+                                                         int rank, int hidden, const int *seg) {
+  const int i = static_cast<int>(blockIdx.z);
+  if (seg[i] == seg[i + 1]) return;
+  __shared__ unsigned short t[64][66];
+  const size_t base = static_cast<size_t>(i) * rank * hidden;
+  const int h0 = static_cast<int>(blockIdx.x) * 64, r0 = static_cast<int>(blockIdx.y) * 64;
+  for (int k = static_cast<int>(threadIdx.x); k < 64 * 64; k += kThreads) {
+    const int r = r0 + k / 64, h = h0 + k % 64;
+    if (r < rank && h < hidden) t[k / 64][k % 64] = a[base + static_cast<size_t>(r) * hidden + h];
+  }
+  __syncthreads();
+  for (int k = static_cast<int>(threadIdx.x); k < 64 * 64; k += kThreads) {
+    const int h = h0 + k / 64, r = r0 + k % 64;
+    if (r < rank && h < hidden) at[base + static_cast<size_t>(h) * rank + r] = t[k % 64][k / 64];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sums over an adapter's rows: out_i[rank][column] = sum_p low[p][rank] of[p][column]
+// (dA, of = x), or turned, [column][rank] (dB, of = dy). A workgroup has one
+// adapter, 64 columns and up to 64 ranks; its waves take every fourth step of 32
+// rows, which go through LDS and are turned while they are read from it.
+
+struct OuterArgs {
+  const int *pos, *seg, *largest;
+  const unsigned short *of, *low;
+  void *out;
+  int m, rank, padded, blocks, shard, per_block;
+};
+
+template <class T, bool TURNED, int RB, bool WIDE>
+__global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
+  constexpr int kRow = 128 + 16;        // bytes of an LDS row of 64 columns
+  constexpr int kStage = 32 * kRow;     // per wave
+  constexpr int kSum = RB * 4 * 64 * 16;  // a wave's sums
+  constexpr int kLds = 4 * kStage > 4 * kSum ? 4 * kStage : 4 * kSum;
+  __shared__ __align__(16) unsigned char lds[kLds];
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int ml = lane & 15, g = lane >> 4;
+  const int i = static_cast<int>(blockIdx.y);
+  const int rc = static_cast<int>(blockIdx.z) * kRankChunk;
+  const int ranks = a.rank - rc < RB * 16 ? a.rank - rc : RB * 16;
+  const int block = static_cast<int>(blockIdx.x) / a.per_block;
+  const int c0 = (static_cast<int>(blockIdx.x) - block * a.per_block) * 64;
+  const int left = a.shard - c0;
+  const int from = a.seg[i], to = a.seg[i + 1];
+  const unsigned short *const of = a.of + static_cast<size_t>(block) * a.m * a.shard + c0;
+  unsigned char *const st = lds + wave * kStage;
+  f32x4 acc[RB][4];
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[b][v] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  for (int p0 = from + wave * 32; p0 < to; p0 += 128) {
+    s16x8 piece[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int p = p0 + q * 8 + (lane >> 3), c = (lane & 7) * 8;
+      piece[q] = p < to && c < left ? load8(of + static_cast<size_t>(a.pos[p]) * a.shard + c) : zero8();
+    }
+    s16x8 lf[RB][2];
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = b * 16 + ml, p = p0 + 8 * g;
+        s16x8 v = zero8();
+        if (r < ranks && p < to) {
+          // positions begin anywhere: two bytes' alignment
+          typedef short any8 __attribute__((ext_vector_type(8), aligned(2)));
+          v = *reinterpret_cast<const any8 *>(a.low + static_cast<size_t>(h * a.rank + rc + r) * a.padded + p);
+          if (p + 8 > to)  // the rows of the next adapter
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (p + e >= to) v[e] = 0;
+        }
+        lf[b][h] = v;
+      }
+    wait_lds();
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<s16x8 *>(st + (q * 8 + (lane >> 3)) * kRow + (lane & 7) * 16) = piece[q];
+    wait_lds();
+    __builtin_amdgcn_wave_barrier();
+    typedef __attribute__((address_space(3))) s16x4 *lds4;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      unsigned char *const q = st + (g * 8 + (ml >> 2)) * kRow + v * 32 + (ml & 3) * 8;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q + 4 * kRow));
+      const s16x8 of8 = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          acc[b][v] = TURNED ? T::mma(lf[b][h], of8, acc[b][v]) : T::mma(of8, lf[b][h], acc[b][v]);
+    }
+  }
+  // every wave adds up a quarter of the blocks, in the waves' order
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) reinterpret_cast<f32x4 *>(lds + wave * kSum)[(b * 4 + v) * 64 + lane] = acc[b][v];
+  __syncthreads();
+  const float inv = from_unit<T>(__builtin_bit_cast(float, *a.largest));
+  const size_t columns = static_cast<size_t>(a.blocks) * a.shard;
+  const size_t col0 = static_cast<size_t>(block) * a.shard + c0;
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int v = wave;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) sum += reinterpret_cast<const f32x4 *>(lds + w * kSum)[(b * 4 + v) * 64 + lane];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] *= inv;
+    size_t at;
+    if constexpr (TURNED) {  // column v*16 + ml, ranks b*16 + 4g ..
+      if (v * 16 + ml >= left || b * 16 + 4 * g >= ranks) continue;
+      at = (static_cast<size_t>(i) * columns + col0 + v * 16 + ml) * a.rank + rc + b * 16 + 4 * g;
+    } else {  // rank b*16 + ml, columns v*16 + 4g ..
+      if (b * 16 + ml >= ranks || v * 16 + 4 * g >= left) continue;
+      at = (static_cast<size_t>(i) * a.rank + rc + b * 16 + ml) * columns + col0 + v * 16 + 4 * g;
+    }
+    if constexpr (WIDE) {
+      *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = sum;
+    } else {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      *reinterpret_cast<u32x2 *>(static_cast<unsigned short *>(a.out) + at) =
+          u32x2{bits16<T>(sum[0]) | bits16<T>(sum[1]) << 16, bits16<T>(sum[2]) | bits16<T>(sum[3]) << 16};
+    }
+  }
+}
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+template <class F>
+void by_type(bool half, F f) {
+  half ? f(TypeF16{}) : f(TypeBf16{});
+}
+
+int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
+
+}  // namespace
+
+int adapt_splits(int m, int blocks, int shard, int rank, bool few) {
+  if (few) {  // k_adapt_row: steps of 512 columns, about 256 workgroups
+    const int steps = ceil_div(shard, 512), want = 256 / m;
+    return want < 1 ? 1 : want < steps ? want : steps;
+  }
+  // k_adapt_low: about 1024 workgroups, at least four chunks of 64 columns each
+  const long long groups = ceil_div(m, 64) * static_cast<long long>(ceil_div(rank, kRankChunk));
+  const int chunks = blocks * ceil_div(shard, 64);
+  long long s = 1024 / groups;
+  if (s > chunks / 4) s = chunks / 4;
+  if (s > 64) s = 64;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocked &of, const void *w,
+                            bool turned, int splits, float *part, hipStream_t s) {
+  const auto *x = static_cast<const unsigned short *>(of.p), *wp = static_cast<const unsigned short *>(w);
+  if (!p.sorted) {
+    by_type(p.half, [&](auto type) {
+      hipLaunchKernelGGL((k_adapt_row<decltype(type)>), dim3(p.m * splits), dim3(kThreads), 0, s, r, x, wp,
+                         p.adapters, p.m, p.rank, of.shard, splits, part);
+    });
+    return hipGetLastError();
+  }
+  const int per = ceil_div(of.shard, 64);
+  const LowArgs a{r, x, wp, p.m, p.adapters, p.rank, of.blocks, of.shard, per, per * of.blocks, splits, part};
+  by_type(p.half, [&](auto type) {
+    using T = decltype(type);
+    auto go = [&](auto turn, auto rb, auto tt) {
+      constexpr int RB = decltype(rb)::value, TT = decltype(tt)::value;
+      const dim3 grid(static_cast<unsigned>(ceil_div(p.m, TT * 16)) * splits, ceil_div(p.rank, kRankChunk));
+      hipLaunchKernelGGL((k_adapt_low<T, decltype(turn)::value != 0, RB, TT>), grid, dim3(kThreads), 0, s, a);
+    };
+    if (turned)
+      p.rank <= 16 ? go(Int<1>{}, Int<1>{}, Int<4>{}) : go(Int<1>{}, Int<4>{}, Int<4>{});
+    else
+      p.rank <= 16 ? go(Int<0>{}, Int<1>{}, Int<4>{}) : go(Int<0>{}, Int<4>{}, Int<4>{});
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *part, int splits,
+                           const float *scale, const void *w, const Blocked &y, void *out,
+                           hipStream_t s) {
+  const int per = ceil_div(y.shard, 64);
+  UpArgs a{r, part, scale, static_cast<const unsigned short *>(w), static_cast<const unsigned short *>(y.p),
+           static_cast<unsigned short *>(out), p.m, p.adapters, p.rank, splits, y.blocks, y.shard, per,
+           per * y.blocks, 0, 0};
+  by_type(p.half, [&](auto type) {
+    using T = decltype(type);
+    auto go = [&](auto ks, auto tt, auto col) {
+      constexpr int KS = decltype(ks)::value, TT = decltype(tt)::value, COL = decltype(col)::value;
+      a.groups = ceil_div(p.m, TT * 16);
+      a.strips = ceil_div(a.chunks, 4 * COL);
+      hipLaunchKernelGGL((k_adapt_up<T, KS, TT, COL>), dim3(static_cast<unsigned>(ceil_div(a.strips, 8)) * 8 * a.groups),
+                         dim3(kThreads), 0, s, a);
+    };
+    auto sized = [&](auto ks) {
+      if (adapt_big(p.m, p.rank))
+        go(ks, Int<4>{}, Int<4>{});
+      else
+        go(ks, Int<1>{}, Int<1>{});
+    };
+    p.rank <= 16 ? sized(Int<0>{}) : sized(Int<2>{});
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_adapt_segments(const AdaptPlan &p, const AdaptRows &r, hipStream_t s) {
+  hipLaunchKernelGGL(k_adapt_segments, dim3(ceil_div(p.m + 1, kThreads)), dim3(kThreads), 0, s, r.keys, p.m,
+                     p.adapters, p.seg, p.head);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapt_join(const AdaptPlan &p, const AdaptRows &r, const float *scale, hipStream_t s) {
+  const int want = ceil_div(static_cast<long long>(p.m) * p.rank, 4 * kThreads);
+  hipLaunchKernelGGL(k_adapt_join, dim3(want < 1024 ? want : 1024, 2), dim3(kThreads), 0, s,
+                     JoinSide{p.pu, p.u, p.u ? p.split_u : 0}, JoinSide{p.pg, p.g, p.g ? p.split_g : 0}, r.keys,
+                     scale, p.m, p.adapters, p.rank, p.head);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapt_halves(const AdaptPlan &p, hipStream_t s) {
+  by_type(p.half, [&](auto type) {
+    hipLaunchKernelGGL((k_adapt_halves<decltype(type)>), dim3(ceil_div(p.padded, 64), 2, ceil_div(p.rank, 32)),
+                       dim3(kThreads), 0, s, HalvesSide{p.u, p.ut}, HalvesSide{p.g, p.gt}, p.head, p.m, p.rank,
+                       p.padded);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Blocked &of,
+                              const unsigned short *low, const int *largest, bool turned, bool wide,
+                              void *out, hipStream_t s) {
+  const int per = ceil_div(of.shard, 64);
+  const OuterArgs a{r.pos, p.seg, largest, static_cast<const unsigned short *>(of.p), low, out, p.m, p.rank,
+                    p.padded, of.blocks, of.shard, per};
+  const dim3 grid(per * of.blocks, p.adapters, ceil_div(p.rank, kRankChunk));
+  by_type(p.half, [&](auto type) {
+    using T = decltype(type);
+    auto go = [&](auto turn, auto rb, auto fp32) {
+      hipLaunchKernelGGL((k_adapt_outer<T, decltype(turn)::value != 0, decltype(rb)::value, decltype(fp32)::value != 0>),
+                         grid, dim3(kThreads), 0, s, a);
+    };
+    auto ranks = [&](auto turn, auto fp32) {
+      p.rank <= 16 ? go(turn, Int<1>{}, fp32) : go(turn, Int<4>{}, fp32);
+    };
+    if (turned)
+      wide ? ranks(Int<1>{}, Int<1>{}) : ranks(Int<1>{}, Int<0>{});
+    else
+      wide ? ranks(Int<0>{}, Int<1>{}) : ranks(Int<0>{}, Int<0>{});
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_adapt_turn(const AdaptPlan &p, const void *a, hipStream_t s) {
+  hipLaunchKernelGGL(k_adapt_turn, dim3(ceil_div(p.hidden, 64), ceil_div(p.rank, 64), p.adapters), dim3(kThreads),
+                     0, s, static_cast<const unsigned short *>(a), p.at, p.rank, p.hidden, p.seg);
+  return hipGetLastError();
+}
+
+}  // namespace hg

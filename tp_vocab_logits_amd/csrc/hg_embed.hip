@@ -109,6 +109,8 @@ __global__ __launch_bounds__(256) void k_embed(ShardTableN<NT> w, int shard, int
   }
 }
 
+size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+
 // ---------------------------------------------------------------------------
 // The sort. A key is the token, or `rows` where the token lies outside.
 
@@ -617,30 +619,75 @@ hipError_t launch_zero(void *p, size_t bytes, hipStream_t s) {
   return hipGetLastError();
 }
 
-EmbedPlan embed_plan(int rows, int hidden, long long n) {
-  EmbedPlan p = {};
-  if (n <= kFewTokens) return p;  // no workspace
+SortPlan sort_plan(int rows, long long n) {
+  SortPlan p = {};
   int bits = 1;
   while ((1ll << bits) <= rows) ++bits;  // the largest key is `rows`
   p.passes = (bits + 8) / 9;
   p.tiles = static_cast<int>((n + kSortTile - 1) / kSortTile);
+  size_t at = 0;
+  for (int k = 0; k < 4; ++k) {
+    p.off[k] = at;  // keys, positions, and the other side of each pass
+    at += up256(static_cast<size_t>(n) * sizeof(int));
+  }
+  p.off[4] = at;  // counts
+  at += up256(static_cast<size_t>(p.tiles) * kDigits * sizeof(int));
+  p.bytes = at;
+  return p;
+}
+
+namespace {
+
+int sort_launches(const SortPlan &p) { return p.tiles <= 1 ? 1 : 3 * p.passes; }
+
+// fill(&groups) gives each launch its share of zeros to write beside the sort, and
+// adds the workgroups that it takes.
+template <class F>
+Sorted launch_sort(const SortPlan &p, char *base, int rows, const void *tokens, int token_bytes,
+                   long long n, hipStream_t s, F fill) {
+  int *buf[4], *hist = reinterpret_cast<int *>(base + p.off[4]);
+  for (int k = 0; k < 4; ++k) buf[k] = reinterpret_cast<int *>(base + p.off[k]);
+  int side = 0;
+  if (p.tiles <= 1) {
+    int groups = 1;
+    const Fill f = fill(&groups);
+    hipLaunchKernelGGL(k_sort_tile, dim3(groups), dim3(1024), 0, s, tokens, token_bytes,
+                       static_cast<int>(n), rows, p.passes, buf[0], buf[1], f);
+  } else {
+    for (int k = 0; k < p.passes; ++k) {
+      const int *ik = k ? buf[2 * side] : nullptr, *ip = k ? buf[2 * side + 1] : nullptr;
+      if (k) side ^= 1;
+      int g1 = p.tiles, g2 = 1, g3 = p.tiles;
+      const Fill f1 = fill(&g1), f2 = fill(&g2), f3 = fill(&g3);
+      hipLaunchKernelGGL(k_sort_count, dim3(g1), dim3(1024), 0, s, tokens, token_bytes, ik, n, rows,
+                         9 * k, hist, p.tiles, f1);
+      hipLaunchKernelGGL(k_sort_scan, dim3(g2), dim3(1024), 0, s, hist, p.tiles * kDigits, f2);
+      hipLaunchKernelGGL(k_sort_place, dim3(g3), dim3(1024), 0, s, tokens, token_bytes, ik, ip, n,
+                         rows, 9 * k, hist, p.tiles, buf[2 * side], buf[2 * side + 1], f3);
+    }
+  }
+  return Sorted{buf[2 * side], buf[2 * side + 1]};
+}
+
+}  // namespace
+
+hipError_t launch_sort(const SortPlan &p, void *ws, int rows, const void *index, int index_bytes,
+                       long long n, Sorted *sorted, hipStream_t s) {
+  *sorted = launch_sort(p, static_cast<char *>(ws), rows, index, index_bytes, n, s,
+                        [](int *) { return Fill{nullptr, 0, 1}; });
+  return hipGetLastError();
+}
+
+EmbedPlan embed_plan(int rows, int hidden, long long n) {
+  EmbedPlan p = {};
+  if (n <= kFewTokens) return p;  // no workspace
   // Positions per block: at least 8 (the rows in flight), and no more blocks
   // than about eight workgroups per CU need.
   long long per = n / 2048;
   p.per = static_cast<int>(per < 8 ? 8 : per > 256 ? 256 : per);
   p.blocks = static_cast<int>((n + p.per - 1) / p.per);
-  const size_t ints = static_cast<size_t>(n) * sizeof(int);
-  auto up = [](size_t b) { return (b + 255) & ~static_cast<size_t>(255); };
-  size_t at = 0;
-  for (int k = 0; k < 4; ++k) {
-    p.off[k] = at;  // keys, positions, and the other side of each pass
-    at += up(ints);
-  }
-  p.off[4] = at;  // counts
-  at += up(static_cast<size_t>(p.tiles) * kDigits * sizeof(int));
-  p.off[5] = at;  // partial rows
-  at += up(static_cast<size_t>(p.blocks) * 2 * hidden * sizeof(float));
-  p.bytes = at;
+  p.part = sort_plan(rows, n).bytes;
+  p.bytes = p.part + up256(static_cast<size_t>(p.blocks) * 2 * hidden * sizeof(float));
   return p;
 }
 
@@ -688,14 +735,12 @@ hipError_t launch_embed_grad(const EmbedPlan &p, void *ws, int rows, int hidden,
     return hipGetLastError();
   }
   char *base = static_cast<char *>(ws);
-  int *buf[4], *hist = reinterpret_cast<int *>(base + p.off[4]);
-  for (int k = 0; k < 4; ++k) buf[k] = reinterpret_cast<int *>(base + p.off[k]);
-  int side = 0;
-  // the zeros, cut into one part per launch of the sort
-  const int launches = n <= kSortTile ? 1 : 3 * p.passes;
+  const SortPlan sort = sort_plan(rows, n);
+  const int launches = sort_launches(sort);
   const long long share = (zeros + launches - 1) / launches;
   int part = 0;
-  auto fill = [&](int *groups) {
+  // the zeros, cut into one part per launch of the sort
+  const Sorted sorted = launch_sort(sort, base, rows, tokens, token_bytes, n, s, [&](int *groups) {
     Fill f;
     const long long at = share * part++;
     f.p = static_cast<u32x4 *>(dw) + at;
@@ -703,28 +748,10 @@ hipError_t launch_embed_grad(const EmbedPlan &p, void *ws, int rows, int hidden,
     f.groups = fill_groups(f.vecs);
     *groups += f.groups;
     return f;
-  };
-  if (n <= kSortTile) {
-    int groups = 1;
-    const Fill f = fill(&groups);
-    hipLaunchKernelGGL(k_sort_tile, dim3(groups), dim3(1024), 0, s, tokens, token_bytes,
-                       static_cast<int>(n), rows, p.passes, buf[0], buf[1], f);
-  } else {
-    for (int k = 0; k < p.passes; ++k) {
-      const int *ik = k ? buf[2 * side] : nullptr, *ip = k ? buf[2 * side + 1] : nullptr;
-      if (k) side ^= 1;
-      int g1 = p.tiles, g2 = 1, g3 = p.tiles;
-      const Fill f1 = fill(&g1), f2 = fill(&g2), f3 = fill(&g3);
-      hipLaunchKernelGGL(k_sort_count, dim3(g1), dim3(1024), 0, s, tokens, token_bytes, ik, n, rows,
-                         9 * k, hist, p.tiles, f1);
-      hipLaunchKernelGGL(k_sort_scan, dim3(g2), dim3(1024), 0, s, hist, p.tiles * kDigits, f2);
-      hipLaunchKernelGGL(k_sort_place, dim3(g3), dim3(1024), 0, s, tokens, token_bytes, ik, ip, n,
-                         rows, 9 * k, hist, p.tiles, buf[2 * side], buf[2 * side + 1], f3);
-    }
-  }
-  a.keys = buf[2 * side];
-  a.pos = buf[2 * side + 1];
-  a.part = reinterpret_cast<float *>(base + p.off[5]);
+  });
+  a.keys = sorted.keys;
+  a.pos = sorted.pos;
+  a.part = reinterpret_cast<float *>(base + p.part);
   a.per = p.per;
   a.blocks = p.blocks;
   with_types([&](auto t, auto d) {

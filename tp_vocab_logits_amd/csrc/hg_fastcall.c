@@ -2,7 +2,7 @@
  * _hgcall: fast-call Python wrappers of the per-call entry points of
  * libhg.so (hg_gather, hg_push, hg_collect, hg_stock_gather, hg_embed,
  * hg_embed_grad, hg_xent, hg_xent_grad, hg_xent_step, hg_beam_select,
- * hg_beam_reorder), for loops where the ctypes conversion of the arguments
+ * hg_beam_reorder, hg_adapt, hg_adapt_grad), for loops where the ctypes conversion of the arguments
  * (about 0.5 us a call, 2 us with a dozen of them) is a sizeable part of a
  * call of a few microseconds.
  * Argument marshalling only: every argument is an integer (a handle, a
@@ -63,8 +63,17 @@ typedef int (*beam_reorder_fn)(int requests, int beams, int count, const hg_beam
 static beam_select_fn g_beam_select;
 static beam_reorder_fn g_beam_reorder;
 
+typedef int (*adapt_fn)(const hg_adapt_shape *s, const void *y, const void *x, const void *a,
+                        const void *b, const float *scale, const void *index, void *out, void *ws,
+                        size_t ws_bytes, void *stream);
+typedef int (*adapt_grad_fn)(const hg_adapt_shape *s, const void *dy, const void *x, const void *a,
+                             const void *b, const float *scale, const void *index, void *dx,
+                             void *da, void *db, int wide, void *ws, size_t ws_bytes, void *stream);
+static adapt_fn g_adapt;
+static adapt_grad_fn g_adapt_grad;
+
 #define MAX_BLOCKS HG_MAX_TP
-#define ENTRIES 11
+#define ENTRIES 13
 
 static int as_ptr(PyObject *o, void **p) {
   *p = PyLong_AsVoidPtr(o);
@@ -102,7 +111,7 @@ static int as_float(PyObject *o, float *v) {
 }
 
 /* bind(gather, push, collect, stock, embed, embed_grad, xent, xent_grad, xent_step, beam_select,
- * beam_reorder): their addresses */
+ * beam_reorder, adapt, adapt_grad): their addresses */
 static PyObject *py_bind(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
   void *fn[ENTRIES];
   (void)self;
@@ -128,6 +137,8 @@ static PyObject *py_bind(PyObject *self, PyObject *const *args, Py_ssize_t nargs
   g_xent_step = (xent_step_fn)fn[8];
   g_beam_select = (beam_select_fn)fn[9];
   g_beam_reorder = (beam_reorder_fn)fn[10];
+  g_adapt = (adapt_fn)fn[11];
+  g_adapt_grad = (adapt_grad_fn)fn[12];
   Py_RETURN_NONE;
 }
 
@@ -377,10 +388,56 @@ bad:
   return NULL;
 }
 
+/* (tp, shard, hidden, m, adapters, rank, dtype, index_bytes) and `count` addresses after it. */
+static int as_adapt(PyObject *const *args, hg_adapt_shape *s, void **p, int count) {
+  if (!PyTuple_Check(args[0]) || PyTuple_GET_SIZE(args[0]) != 8) {
+    PyErr_SetString(PyExc_TypeError, "the shape must be a tuple of eight integers");
+    return 0;
+  }
+  int *const dims[8] = {&s->tp,       &s->shard, &s->hidden, &s->m,
+                        &s->adapters, &s->rank,  &s->dtype,  &s->index_bytes};
+  for (int k = 0; k < 8; ++k)
+    if (!as_int(PyTuple_GET_ITEM(args[0], k), dims[k])) return 0;
+  for (int k = 0; k < count; ++k)
+    if (!as_ptr(args[1 + k], &p[k])) return 0;
+  return 1;
+}
+
+/* adapt(shape, y, x, a, b, scale, index, out, ws, ws_bytes, stream) -> status */
+static PyObject *py_adapt(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  hg_adapt_shape s;
+  void *p[8], *stream;
+  size_t ws_bytes;
+  (void)self;
+  if (!check_bound((void *)g_adapt, nargs, 11)) return NULL;
+  if (!as_adapt(args, &s, p, 8)) return NULL;
+  ws_bytes = PyLong_AsSize_t(args[9]);
+  if (ws_bytes == (size_t)-1 && PyErr_Occurred()) return NULL;
+  if (!as_ptr(args[10], &stream)) return NULL;
+  return PyLong_FromLong(
+      g_adapt(&s, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], ws_bytes, stream));
+}
+
+/* adapt_grad(shape, dy, x, a, b, scale, index, dx, da, db, wide, ws, ws_bytes, stream) -> status */
+static PyObject *py_adapt_grad(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  hg_adapt_shape s;
+  void *p[9], *ws, *stream;
+  size_t ws_bytes;
+  int wide;
+  (void)self;
+  if (!check_bound((void *)g_adapt_grad, nargs, 14)) return NULL;
+  if (!as_adapt(args, &s, p, 9) || !as_int(args[10], &wide) || !as_ptr(args[11], &ws)) return NULL;
+  ws_bytes = PyLong_AsSize_t(args[12]);
+  if (ws_bytes == (size_t)-1 && PyErr_Occurred()) return NULL;
+  if (!as_ptr(args[13], &stream)) return NULL;
+  return PyLong_FromLong(g_adapt_grad(&s, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8],
+                                      wide, ws, ws_bytes, stream));
+}
+
 static PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)(void))py_bind, METH_FASTCALL,
      "bind(gather, push, collect, stock, embed, embed_grad, xent, xent_grad, xent_step, "
-     "beam_select, beam_reorder)"},
+     "beam_select, beam_reorder, adapt, adapt_grad)"},
     {"gather", (PyCFunction)(void (*)(void))py_gather, METH_FASTCALL,
      "gather(handle, shards_addr, m, out_addr, stream) -> status"},
     {"push", (PyCFunction)(void (*)(void))py_push, METH_FASTCALL,
@@ -403,6 +460,10 @@ static PyMethodDef methods[] = {
     {"beam_reorder", (PyCFunction)(void (*)(void))py_beam_reorder, METH_FASTCALL,
      "beam_reorder(requests, beams, states, parents, parent_bytes, lengths, length_bytes, "
      "stream) -> status"},
+    {"adapt", (PyCFunction)(void (*)(void))py_adapt, METH_FASTCALL,
+     "adapt(shape, y, x, a, b, scale, index, out, ws, ws_bytes, stream) -> status"},
+    {"adapt_grad", (PyCFunction)(void (*)(void))py_adapt_grad, METH_FASTCALL,
+     "adapt_grad(shape, dy, x, a, b, scale, index, dx, da, db, wide, ws, ws_bytes, stream) -> status"},
     {NULL, NULL, 0, NULL},
 };
 

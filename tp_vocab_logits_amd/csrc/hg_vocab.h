@@ -102,11 +102,24 @@ hipError_t launch_zero(void *p, size_t bytes, hipStream_t s);
 hipError_t launch_embed(const VocabMatrix &w, int rows, int dtype, const void *tokens,
                         int token_bytes, int n, float scale, void *out, hipStream_t s);
 
-// Sort passes and workspace of an embedding gradient over n tokens.
-struct EmbedPlan {
+// A stable sort of n keys index[j] (int32 or int64) in 0 .. rows-1, those outside
+// last, as the key `rows`: the sorted keys and the places that they came from, both
+// in the workspace.
+struct SortPlan {
   int passes, tiles;
+  size_t off[5], bytes;
+};
+struct Sorted {
+  const int *keys, *pos;
+};
+SortPlan sort_plan(int rows, long long n);
+hipError_t launch_sort(const SortPlan &p, void *ws, int rows, const void *index, int index_bytes,
+                       long long n, Sorted *sorted, hipStream_t s);
+
+// Workspace of an embedding gradient over n tokens: the sort's, then partial rows.
+struct EmbedPlan {
   int per, blocks;  // sorted positions per block of the sums
-  size_t off[6], bytes;
+  size_t part, bytes;
 };
 EmbedPlan embed_plan(int rows, int hidden, long long n);
 hipError_t launch_embed_grad(const EmbedPlan &p, void *ws, int rows, int hidden, int dtype,

@@ -479,7 +479,8 @@ __global__ __launch_bounds__(kThreads) void k_adapt_segments(const int *keys, in
   for (int i = before + 1; i <= here && i <= adapters; ++i) seg[i] = j;
 }
 
-// The parts' sums, scaled, and their largest: blockIdx.y 0: u, 1: g.
+// The parts' sums, scaled, and their largest (into head, if given): blockIdx.y 0: u,
+// 1: g.
 struct JoinSide {
   const float *part;
   float *sum;
@@ -497,7 +498,15 @@ __global__ __launch_bounds__(kThreads) void k_adapt_join(JoinSide u, JoinSide g,
       const int key = keys[k / rank];  // (four ranks are of one row)
       f32x4 sum = {0.f, 0.f, 0.f, 0.f};
       if (key < adapters) {
-        for (int s = 0; s < side.splits; ++s) sum += *reinterpret_cast<const f32x4 *>(side.part + s * n + k);
+        for (int s0 = 0; s0 < side.splits; s0 += 8) {  // (eight loads in flight)
+          f32x4 v[8];
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            if (s0 + t < side.splits) v[t] = *reinterpret_cast<const f32x4 *>(side.part + (s0 + t) * n + k);
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            if (s0 + t < side.splits) sum += v[t];
+        }
         const float f = scale ? scale[key] : 1.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -511,7 +520,7 @@ __global__ __launch_bounds__(kThreads) void k_adapt_join(JoinSide u, JoinSide g,
 #pragma unroll
   for (int d = 32; d; d >>= 1) largest = fmaxf(largest, __shfl_xor(largest, d));
   // (the largest of all does not depend on the order)
-  if ((threadIdx.x & 63) == 0 && largest > 0.f)
+  if (head && (threadIdx.x & 63) == 0 && largest > 0.f)
     atomicMax(head + blockIdx.y, static_cast<int>(__builtin_bit_cast(uint32_t, largest)));
 }
 
@@ -771,7 +780,7 @@ hipError_t launch_adapt_segments(const AdaptPlan &p, const AdaptRows &r, hipStre
 
 hipError_t launch_adapt_join(const AdaptPlan &p, const AdaptRows &r, const float *scale, hipStream_t s) {
   const int want = ceil_div(static_cast<long long>(p.m) * p.rank, 4 * kThreads);
-  hipLaunchKernelGGL(k_adapt_join, dim3(want < 1024 ? want : 1024, 2), dim3(kThreads), 0, s,
+  hipLaunchKernelGGL(k_adapt_join, dim3(want < 1024 ? want : 1024, p.g ? 2 : 1), dim3(kThreads), 0, s,
                      JoinSide{p.pu, p.u, p.u ? p.split_u : 0}, JoinSide{p.pg, p.g, p.g ? p.split_g : 0}, r.keys,
                      scale, p.m, p.adapters, p.rank, p.head);
   return hipGetLastError();

@@ -70,7 +70,10 @@ size_t lay_out(const hg_adapt_shape &s, int kind, char *ws, AdaptPlan *p) {
   }
   p->split_u = hg::adapt_splits(s.m, 1, s.hidden, s.rank, !p->sorted);
   p->pu = floats(low * p->split_u);
-  if (kind == HG_ADAPT_ADD) return at;
+  if (kind == HG_ADAPT_ADD) {
+    if (p->sorted) p->u = floats(low);
+    return at;
+  }
   p->split_g = hg::adapt_splits(s.m, s.tp, s.shard, s.rank, false);
   p->pg = floats(low * p->split_g);
   p->u = floats(low);
@@ -154,7 +157,15 @@ HG_API int hg_adapt(const hg_adapt_shape *s, const void *y, const void *x, const
     if (rc != HG_OK) return rc;
   }
   HIP_TRY(hg::launch_adapt_low(p, rows, Blocked{x, 1, s->hidden}, a, false, p.split_u, p.pu, st));
-  HIP_TRY(hg::launch_adapt_up(p, rows, p.pu, p.split_u, scale, b, Blocked{y, s->tp, s->shard}, out, st));
+  // The second product's workgroups each read all of their rows' parts: of many
+  // rows they are added up first (2047 rows, 28 parts: 578 us without).
+  const Blocked wide_y{y, s->tp, s->shard};
+  if (p.sorted) {
+    HIP_TRY(hg::launch_adapt_join(p, rows, scale, st));
+    HIP_TRY(hg::launch_adapt_up(p, rows, p.u, 1, nullptr, b, wide_y, out, st));
+  } else {
+    HIP_TRY(hg::launch_adapt_up(p, rows, p.pu, p.split_u, scale, b, wide_y, out, st));
+  }
   return HG_OK;
 }
 

@@ -38,6 +38,8 @@ struct AdaptPlan {
   int *seg;              // [adapters + 1] sorted positions where they begin
   unsigned short *ut, *gt;  // [2][ranks][padded] upper and lower halves of u and g
   unsigned short *at;    // [adapters][hidden][rank]: A turned
+  int parts_a, parts_b;  // of the rows in the sums of dA and dB
+  float *pa, *pb;        // [parts][adapters][..], where there are several
 };
 
 // pu or pg: the products of `of` with A (turned = false: w is [adapters][rank][columns])
@@ -54,11 +56,12 @@ hipError_t launch_adapt_segments(const AdaptPlan &p, const AdaptRows &r, hipStre
 hipError_t launch_adapt_join(const AdaptPlan &p, const AdaptRows &r, const float *scale, hipStream_t s);
 // Their halves, by rank.
 hipError_t launch_adapt_halves(const AdaptPlan &p, hipStream_t s);
-// sum over an adapter's rows of low^T x wide: [adapters][rank][columns], or
-// [adapters][columns][rank] if turned.
+// sum over an adapter's rows of low^T x of: [adapters][rank][columns], or
+// [adapters][columns][rank] if turned; in `parts` parts of the rows, added up if
+// there are several (part: room for them).
 hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Blocked &of,
-                              const unsigned short *low, const int *largest, bool turned, bool wide,
-                              void *out, hipStream_t s);
+                              const unsigned short *low, const int *largest, bool turned, int parts,
+                              float *part, bool wide, void *out, hipStream_t s);
 hipError_t launch_adapt_turn(const AdaptPlan &p, const void *a, hipStream_t s);
 
 // Whether hg_adapt's second product takes big pieces (64 rows x 1024 columns per
@@ -67,5 +70,7 @@ inline bool adapt_big(int m, int rank) { return m > kFewRows && rank <= kRankChu
 
 // Parts that a sum over `columns` columns of `m` rows is cut into.
 int adapt_splits(int m, int blocks, int shard, int rank, bool few);
+// Parts of the rows in the sums over an adapter's rows.
+int adapt_parts(int m, int adapters, int blocks, int shard, int rank);
 
 }  // namespace hg

@@ -111,58 +111,57 @@ __global__ __launch_bounds__(kThreads) void k_adapt_row(AdaptRows rows, const un
 
 // ---------------------------------------------------------------------------
 // Low-rank products of many rows: part[split][p][rank] = sum over the split's
-// columns of of[p][c] w_i[rank][c]. A workgroup has TT tiles of rows, a part of
-// the columns and up to 64 ranks (RB blocks of 16); its waves take every fourth
-// chunk of 64 columns. w's columns are next to each other in memory (A), or, if
-// TURNED, its ranks are (B): those chunks go through LDS and are turned while
-// they are read from it.
+// columns of of[p][c] w_i[rank][c]. A workgroup has 128 rows (two tiles per wave), a
+// part of the columns and up to 64 ranks (RB blocks of 16). Its waves share w's
+// 128 columns of a step in LDS, so that w comes through the L2 once per 128 rows,
+// half of what the rows themselves take; of is read into registers as the matrix
+// cores want it, 256 bytes of a row at a time, a step ahead. w's columns are next
+// to each other in memory (A), or, if TURNED, its ranks are (B): those are turned
+// while they are read from LDS.
 
 struct LowArgs {
   AdaptRows rows;
   const unsigned short *of, *w;
   int m, adapters, rank;
-  int blocks, shard, per_block, chunks;  // chunks of 64 columns per block, in all
+  int blocks, shard, per_block, chunks;  // chunks of kLowCols columns per block, in all
   int splits;
   float *part;
 };
 
-template <class T, bool TURNED, int RB, int TT>
+constexpr int kLowRows = 128, kLowCols = 128;
+
+template <class T, bool TURNED, int RB>
 __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
-  constexpr int kRow = RB * 32 + 16;                // bytes of an LDS row of 16*RB ranks
-  constexpr int kStage = TURNED ? 64 * kRow : 0;    // per wave
-  constexpr int kSum = TT * 16 * RB * 16 * 4;       // a wave's sums
-  constexpr int kLds = 4 * kStage > 2 * kSum ? 4 * kStage : 2 * kSum;
-  __shared__ __align__(16) unsigned char lds[kLds];
-  const int lane = static_cast<int>(threadIdx.x) & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  constexpr int TT = 2, KS = kLowCols / 32;
+  constexpr int kRow = TURNED ? RB * 32 + 16 : kLowCols * 2 + 16;  // bytes of an LDS row: ranks, or columns
+  constexpr int kPieces = TURNED ? RB * 2 : kLowCols / 8;          // 16-byte pieces of one
+  __shared__ __align__(16) unsigned char lds[(TURNED ? kLowCols : RB * 16) * kRow];
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ml = lane & 15, g = lane >> 4;
-  const int groups = (a.m + TT * 16 - 1) / (TT * 16);
+  const int groups = (a.m + kLowRows - 1) / kLowRows;
   const int split = static_cast<int>(blockIdx.x) / groups, group = static_cast<int>(blockIdx.x) - split * groups;
   const int rc = static_cast<int>(blockIdx.y) * kRankChunk;
   const int ranks = a.rank - rc < RB * 16 ? a.rank - rc : RB * 16;  // a multiple of 8
   const int from = static_cast<int>(static_cast<long long>(a.chunks) * split / a.splits);
   const int to = static_cast<int>(static_cast<long long>(a.chunks) * (split + 1) / a.splits);
-  const int p0 = group * TT * 16;
-  const int pend = a.m < p0 + TT * 16 ? a.m : p0 + TT * 16;
+  const int p0 = group * kLowRows;
+  const int pend = a.m < p0 + kLowRows ? a.m : p0 + kLowRows;
   const size_t columns = static_cast<size_t>(a.blocks) * a.shard;
 
-  int key[TT];
-  const unsigned short *src[TT];
+  int key[TT], row[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
-    const int p = p0 + t * 16 + ml;
+    const int p = p0 + (wave * TT + t) * 16 + ml;
     key[t] = p < a.m ? a.rows.keys[p] : a.adapters;
-    src[t] = a.of + static_cast<size_t>(p < a.m ? a.rows.pos[p] : 0) * a.shard;
+    row[t] = p < a.m ? a.rows.pos[p] : 0;
   }
-  int cur = __builtin_amdgcn_readfirstlane(key[0]);
+  int at = p0;  // the first position of the adapter in turn
+  int cur = a.rows.keys[at];
   while (cur < a.adapters) {
     bool active[TT];
-    int done = 0;
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      active[t] = __ballot(key[t] == cur) != 0;
-      done += __popcll(__ballot(key[t] <= cur) & 0xFFFF);
-    }
+    for (int t = 0; t < TT; ++t) active[t] = __ballot(key[t] == cur) != 0;
     f32x4 acc[TT][RB];
 #pragma unroll
     for (int t = 0; t < TT; ++t)
@@ -170,105 +169,79 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
       for (int b = 0; b < RB; ++b) acc[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
     const unsigned short *const wi = a.w + static_cast<size_t>(cur) * a.rank * columns;
 
-    for (int chunk = from + wave; chunk < to; chunk += 4) {
-      const int block = chunk / a.per_block, c0 = (chunk - block * a.per_block) * 64;
+    s16x8 next[TT][KS], piece[RB];
+    auto fetch = [&](int chunk) __attribute__((always_inline)) {
+      const int block = chunk / a.per_block, c0 = (chunk - block * a.per_block) * kLowCols;
       const int left = a.shard - c0;  // columns of the block from here on
-      const size_t at = static_cast<size_t>(block) * a.m * a.shard + c0;
+      const unsigned short *const of = a.of + static_cast<size_t>(block) * a.m * a.shard + c0;
       const size_t col = static_cast<size_t>(block) * a.shard + c0;
-      s16x8 xf[TT][2], wf[RB][2];
 #pragma unroll
       for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
+        for (int ks = 0; ks < KS; ++ks) {
           const int c = ks * 32 + 8 * g;
-          xf[t][ks] = active[t] && c < left ? load8(src[t] + at + c) : zero8();
+          next[t][ks] = active[t] && c < left ? load8(of + static_cast<size_t>(row[t]) * a.shard + c) : zero8();
         }
-      if constexpr (TURNED) {
-        unsigned char *const st = lds + wave * kStage;
-        // 64 rows (columns of the product) of 16*RB ranks: 16-byte pieces
-        constexpr int kPieces = RB * 2;
-        s16x8 piece[kPieces];
 #pragma unroll
-        for (int q = 0; q < kPieces; ++q) {
-          const int id = q * 64 + lane, v = id / kPieces, e = (id % kPieces) * 8;
-          piece[q] = v < left && e < ranks ? load8(wi + (col + v) * a.rank + rc + e) : zero8();
-        }
-        wait_lds();  // the last chunk's reads
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int q = 0; q < kPieces; ++q) {
-          const int id = q * 64 + lane, v = id / kPieces, e = (id % kPieces) * 8;
-          *reinterpret_cast<s16x8 *>(st + v * kRow + e * 2) = piece[q];
-        }
-        wait_lds();
-        __builtin_amdgcn_wave_barrier();
-        typedef __attribute__((address_space(3))) s16x4 *lds4;
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            unsigned char *const q = st + (ks * 32 + g * 8 + (ml >> 2)) * kRow + b * 32 + (ml & 3) * 8;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q + 4 * kRow));
-            wf[b][ks] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-          }
-      } else {
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            const int c = ks * 32 + 8 * g;
-            wf[b][ks] = c < left && b * 16 + ml < ranks
-                            ? load8(wi + static_cast<size_t>(rc + b * 16 + ml) * columns + col + c)
-                            : zero8();
-          }
+      for (int q = 0; q < RB; ++q) {
+        const int id = q * kThreads + tid, line = id / kPieces, e = (id % kPieces) * 8;
+        if constexpr (TURNED)
+          piece[q] = line < left && e < ranks ? load8(wi + (col + line) * a.rank + rc + e) : zero8();
+        else
+          piece[q] = line < ranks && e < left ? load8(wi + static_cast<size_t>(rc + line) * columns + col + e)
+                                              : zero8();
       }
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-          for (int b = 0; b < RB; ++b)
-            if (active[t]) acc[t][b] = T::mma(wf[b][ks], xf[t][ks], acc[t][b]);
-    }
-
-    // the four waves' sums, in a fixed order: (0 + 2) + (1 + 3)
-    auto slot = [&](int w, int t, int b) __attribute__((always_inline)) {
-      return reinterpret_cast<f32x4 *>(lds + w * kSum) + (t * RB + b) * 64 + lane;
     };
-    __syncthreads();
-    if (wave >= 2)
+    if (from < to) fetch(from);
+    for (int chunk = from; chunk < to; ++chunk) {
+      __syncthreads();  // the last step's reads
+#pragma unroll
+      for (int q = 0; q < RB; ++q) {
+        const int id = q * kThreads + tid, line = id / kPieces, e = id % kPieces;
+        *reinterpret_cast<s16x8 *>(lds + line * kRow + e * 16) = piece[q];
+      }
+      s16x8 xf[TT][KS];
 #pragma unroll
       for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int b = 0; b < RB; ++b) *slot(wave - 2, t, b) = acc[t][b];
-    __syncthreads();
-    if (wave < 2)
+        for (int ks = 0; ks < KS; ++ks) xf[t][ks] = next[t][ks];
+      __syncthreads();
+      if (chunk + 1 < to) fetch(chunk + 1);
 #pragma unroll
-      for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int b = 0; b < RB; ++b) acc[t][b] += *slot(wave, t, b);
-    __syncthreads();
-    if (wave == 1)
-#pragma unroll
-      for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int b = 0; b < RB; ++b) *slot(0, t, b) = acc[t][b];
-    __syncthreads();
-    if (wave == 0)
-#pragma unroll
-      for (int t = 0; t < TT; ++t)
+      for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-          const f32x4 sum = acc[t][b] + *slot(0, t, b);
-          const int r = b * 16 + 4 * g;
-          if (key[t] == cur && r < ranks)
-            *reinterpret_cast<f32x4 *>(a.part + (static_cast<size_t>(split) * a.m + p0 + t * 16 + ml) * a.rank +
-                                       rc + r) = sum;
+          s16x8 wf;
+          if constexpr (TURNED) {
+            typedef __attribute__((address_space(3))) s16x4 *lds4;
+            unsigned char *const q = lds + (ks * 32 + g * 8 + (ml >> 2)) * kRow + b * 32 + (ml & 3) * 8;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q + 4 * kRow));
+            wf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          } else {
+            wf = *reinterpret_cast<const s16x8 *>(lds + (b * 16 + ml) * kRow + ks * 64 + g * 16);
+          }
+#pragma unroll
+          for (int t = 0; t < TT; ++t)
+            if (active[t]) acc[t][b] = T::mma(wf, xf[t][ks], acc[t][b]);
         }
-    __syncthreads();
-    const int next = p0 + done;
-    cur = next < pend ? a.rows.keys[next] : a.adapters;
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        const int r = b * 16 + 4 * g;
+        if (key[t] == cur && r < ranks)
+          *reinterpret_cast<f32x4 *>(
+              a.part + (static_cast<size_t>(split) * a.m + p0 + (wave * TT + t) * 16 + ml) * a.rank + rc + r) =
+              acc[t][b];
+      }
+    // the next adapter among the workgroup's rows (they are sorted)
+    while (at < pend && a.rows.keys[at] == cur) {
+      const int p = at + lane;
+      at += __popcll(__ballot(p < pend && a.rows.keys[p < pend ? p : at] == cur));
+    }
+    cur = at < pend ? a.rows.keys[at] : a.adapters;
   }
 }
 
@@ -575,73 +548,94 @@ __global__ __launch_bounds__(kThreads) void k_adapt_turn(const unsigned short *a
 // ---------------------------------------------------------------------------
 // Sums over an adapter's rows: out_i[rank][column] = sum_p low[p][rank] of[p][column]
 // (dA, of = x), or turned, [column][rank] (dB, of = dy). A workgroup has one
-// adapter, 64 columns and up to 64 ranks; its waves take every fourth step of 32
-// rows, which go through LDS and are turned while they are read from it.
+// adapter, 64 columns for each of its four waves and up to 64 ranks, and goes
+// through the rows, or a part of them, 32 at a time: the waves share the rows'
+// low-rank values (half of the bytes that their own columns take) and turn of in
+// LDS. A step's loads are issued before the last one's products.
 
 struct OuterArgs {
   const int *pos, *seg, *largest;
   const unsigned short *of, *low;
   void *out;
-  int m, rank, padded, blocks, shard, per_block;
+  int m, adapters, rank, padded, blocks, shard, per_block, chunks;  // chunks of 64 columns
 };
 
+// WIDE: out is fp32, [parts][adapters]...: the parts (gridDim.y / adapters) are
+// added up by another launch if there are several.
 template <class T, bool TURNED, int RB, bool WIDE>
 __global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
-  constexpr int kRow = 128 + 16;        // bytes of an LDS row of 64 columns
-  constexpr int kStage = 32 * kRow;     // per wave
-  constexpr int kSum = RB * 4 * 64 * 16;  // a wave's sums
-  constexpr int kLds = 4 * kStage > 4 * kSum ? 4 * kStage : 4 * kSum;
-  __shared__ __align__(16) unsigned char lds[kLds];
-  const int lane = static_cast<int>(threadIdx.x) & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  constexpr int kRow = 128 + 16;         // bytes of an LDS row of 64 columns
+  constexpr int kLowRow = 64 + 16;       // of a rank's 32 rows
+  constexpr int kHalf = RB * 16 * kLowRow;
+  constexpr int kQ = (RB + 1) / 2;       // 16-byte pieces of low per thread
+  __shared__ __align__(16) unsigned char lds[4 * 32 * kRow + 2 * kHalf];
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ml = lane & 15, g = lane >> 4;
-  const int i = static_cast<int>(blockIdx.y);
+  const int part = static_cast<int>(blockIdx.y) / a.adapters, i = static_cast<int>(blockIdx.y) - part * a.adapters;
+  const int parts = static_cast<int>(gridDim.y) / a.adapters;
   const int rc = static_cast<int>(blockIdx.z) * kRankChunk;
   const int ranks = a.rank - rc < RB * 16 ? a.rank - rc : RB * 16;
-  const int block = static_cast<int>(blockIdx.x) / a.per_block;
-  const int c0 = (static_cast<int>(blockIdx.x) - block * a.per_block) * 64;
-  const int left = a.shard - c0;
+  const int chunk = static_cast<int>(blockIdx.x) * 4 + wave;
+  const bool has = chunk < a.chunks;
+  const int block = has ? chunk / a.per_block : 0, c0 = has ? (chunk - block * a.per_block) * 64 : 0;
+  const int left = has ? a.shard - c0 : 0;
   const int from = a.seg[i], to = a.seg[i + 1];
+  const int first = from & ~7;  // (low is read eight rows at a time)
+  const int steps = (to - first + 31) / 32;
+  const int s0 = static_cast<int>(static_cast<long long>(steps) * part / parts);
+  const int s1 = static_cast<int>(static_cast<long long>(steps) * (part + 1) / parts);
   const unsigned short *const of = a.of + static_cast<size_t>(block) * a.m * a.shard + c0;
-  unsigned char *const st = lds + wave * kStage;
+  unsigned char *const st = lds + wave * 32 * kRow, *const sl = lds + 4 * 32 * kRow;
   f32x4 acc[RB][4];
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
     for (int v = 0; v < 4; ++v) acc[b][v] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  for (int p0 = from + wave * 32; p0 < to; p0 += 128) {
-    s16x8 piece[4];
+  s16x8 piece[4], low[kQ];
+  auto fetch = [&](int step) __attribute__((always_inline)) {
+    const int p0 = first + step * 32;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int p = p0 + q * 8 + (lane >> 3), c = (lane & 7) * 8;
-      piece[q] = p < to && c < left ? load8(of + static_cast<size_t>(a.pos[p]) * a.shard + c) : zero8();
+      piece[q] = p >= from && p < to && c < left ? load8(of + static_cast<size_t>(a.pos[p]) * a.shard + c) : zero8();
     }
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {  // pieces (half, rank, eight rows)
+      const int id = q * kThreads + tid, line = id >> 2, p = p0 + (id & 3) * 8;
+      const int h = line / (RB * 16), r = line - h * (RB * 16);
+      low[q] = h < 2 && r < ranks && p < to
+                   ? load8(a.low + static_cast<size_t>(h * a.rank + rc + r) * a.padded + p)
+                   : zero8();
+    }
+  };
+  if (s0 < s1) fetch(s0);
+  for (int step = s0; step < s1; ++step) {
+    const int p0 = first + step * 32;
+    __syncthreads();  // the last step's reads
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<s16x8 *>(st + (q * 8 + (lane >> 3)) * kRow + (lane & 7) * 16) = piece[q];
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+      const int id = q * kThreads + tid, p = p0 + (id & 3) * 8;
+      s16x8 v = low[q];
+      if (p < from || p + 8 > to) {  // rows of other adapters
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (p + e < from || p + e >= to) v[e] = 0;
+      }
+      if (id < RB * 128) *reinterpret_cast<s16x8 *>(sl + (id >> 2) * kLowRow + (id & 3) * 16) = v;
+    }
+    __syncthreads();
+    if (step + 1 < s1) fetch(step + 1);
     s16x8 lf[RB][2];
 #pragma unroll
     for (int b = 0; b < RB; ++b)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = b * 16 + ml, p = p0 + 8 * g;
-        s16x8 v = zero8();
-        if (r < ranks && p < to) {
-          // positions begin anywhere: two bytes' alignment
-          typedef short any8 __attribute__((ext_vector_type(8), aligned(2)));
-          v = *reinterpret_cast<const any8 *>(a.low + static_cast<size_t>(h * a.rank + rc + r) * a.padded + p);
-          if (p + 8 > to)  // the rows of the next adapter
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (p + e >= to) v[e] = 0;
-        }
-        lf[b][h] = v;
-      }
-    wait_lds();
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<s16x8 *>(st + (q * 8 + (lane >> 3)) * kRow + (lane & 7) * 16) = piece[q];
-    wait_lds();
-    __builtin_amdgcn_wave_barrier();
+      for (int h = 0; h < 2; ++h)
+        lf[b][h] = *reinterpret_cast<const s16x8 *>(sl + h * kHalf + (b * 16 + ml) * kLowRow + g * 16);
     typedef __attribute__((address_space(3))) s16x4 *lds4;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
@@ -656,38 +650,62 @@ __global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
           acc[b][v] = TURNED ? T::mma(lf[b][h], of8, acc[b][v]) : T::mma(of8, lf[b][h], acc[b][v]);
     }
   }
-  // every wave adds up a quarter of the blocks, in the waves' order
-  __syncthreads();
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) reinterpret_cast<f32x4 *>(lds + wave * kSum)[(b * 4 + v) * 64 + lane] = acc[b][v];
-  __syncthreads();
   const float inv = from_unit<T>(__builtin_bit_cast(float, *a.largest));
   const size_t columns = static_cast<size_t>(a.blocks) * a.shard;
   const size_t col0 = static_cast<size_t>(block) * a.shard + c0;
+  const size_t pair = static_cast<size_t>(blockIdx.y);  // part and adapter
 #pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int v = wave;
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int b = 0; b < RB; ++b)
 #pragma unroll
-    for (int w = 0; w < 4; ++w) sum += reinterpret_cast<const f32x4 *>(lds + w * kSum)[(b * 4 + v) * 64 + lane];
+    for (int v = 0; v < 4; ++v) {
+      const f32x4 sum = acc[b][v] * inv;
+      size_t at;
+      if constexpr (TURNED) {  // column v*16 + ml, ranks b*16 + 4g ..
+        if (v * 16 + ml >= left || b * 16 + 4 * g >= ranks) continue;
+        at = (pair * columns + col0 + v * 16 + ml) * a.rank + rc + b * 16 + 4 * g;
+      } else {  // rank b*16 + ml, columns v*16 + 4g ..
+        if (b * 16 + ml >= ranks || v * 16 + 4 * g >= left) continue;
+        at = (pair * a.rank + rc + b * 16 + ml) * columns + col0 + v * 16 + 4 * g;
+      }
+      if constexpr (WIDE) {
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = sum;
+      } else {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        *reinterpret_cast<u32x2 *>(static_cast<unsigned short *>(a.out) + at) =
+            u32x2{bits16<T>(sum[0]) | bits16<T>(sum[1]) << 16, bits16<T>(sum[2]) | bits16<T>(sum[3]) << 16};
+      }
+    }
+}
+
+// out = the sum of the parts, [n] each, n a multiple of 8.
+template <class T, bool WIDE>
+__global__ __launch_bounds__(kThreads) void k_adapt_parts(const float *part, int parts, size_t n, void *out) {
+  for (size_t k = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) * 8; k < n;
+       k += static_cast<size_t>(gridDim.x) * kThreads * 8) {
+    f32x4 sum[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    for (int p0 = 0; p0 < parts; p0 += 4) {  // (eight loads in flight)
+      f32x4 v[4][2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] *= inv;
-    size_t at;
-    if constexpr (TURNED) {  // column v*16 + ml, ranks b*16 + 4g ..
-      if (v * 16 + ml >= left || b * 16 + 4 * g >= ranks) continue;
-      at = (static_cast<size_t>(i) * columns + col0 + v * 16 + ml) * a.rank + rc + b * 16 + 4 * g;
-    } else {  // rank b*16 + ml, columns v*16 + 4g ..
-      if (b * 16 + ml >= ranks || v * 16 + 4 * g >= left) continue;
-      at = (static_cast<size_t>(i) * a.rank + rc + b * 16 + ml) * columns + col0 + v * 16 + 4 * g;
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (p0 + t < parts) v[t][h] = *reinterpret_cast<const f32x4 *>(part + (p0 + t) * n + k + 4 * h);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (p0 + t < parts) sum[h] += v[t][h];
     }
     if constexpr (WIDE) {
-      *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = sum;
+      f32x4 *const o = reinterpret_cast<f32x4 *>(static_cast<float *>(out) + k);
+      o[0] = sum[0];
+      o[1] = sum[1];
     } else {
-      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-      *reinterpret_cast<u32x2 *>(static_cast<unsigned short *>(a.out) + at) =
-          u32x2{bits16<T>(sum[0]) | bits16<T>(sum[1]) << 16, bits16<T>(sum[2]) | bits16<T>(sum[3]) << 16};
+      u32x4 o;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        o[t] = bits16<T>(sum[t >> 1][2 * (t & 1)]) | bits16<T>(sum[t >> 1][2 * (t & 1) + 1]) << 16;
+      *reinterpret_cast<u32x4 *>(static_cast<unsigned short *>(out) + k) = o;
     }
   }
 }
@@ -709,12 +727,22 @@ int adapt_splits(int m, int blocks, int shard, int rank, bool few) {
     const int steps = ceil_div(shard, 512), want = 256 / m;
     return want < 1 ? 1 : want < steps ? want : steps;
   }
-  // k_adapt_low: about 1024 workgroups, at least four chunks of 64 columns each
-  const long long groups = ceil_div(m, 64) * static_cast<long long>(ceil_div(rank, kRankChunk));
-  const int chunks = blocks * ceil_div(shard, 64);
+  // k_adapt_low: about 1024 workgroups, at least two steps each
+  const long long groups = ceil_div(m, kLowRows) * static_cast<long long>(ceil_div(rank, kRankChunk));
+  const int chunks = blocks * ceil_div(shard, kLowCols);
   long long s = 1024 / groups;
-  if (s > chunks / 4) s = chunks / 4;
+  if (s > chunks / 2) s = chunks / 2;
   if (s > 64) s = 64;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+int adapt_parts(int m, int adapters, int blocks, int shard, int rank) {
+  // k_adapt_outer: about 1024 workgroups, of at least eight steps of rows
+  const long long have = static_cast<long long>(ceil_div(static_cast<long long>(blocks) * ceil_div(shard, 64), 4)) *
+                         adapters * ceil_div(rank, kRankChunk);
+  long long s = 1024 / have;
+  const long long steps = m / (32ll * adapters);
+  if (s > steps / 8) s = steps / 8;
   return s < 1 ? 1 : static_cast<int>(s);
 }
 
@@ -728,19 +756,19 @@ hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocke
     });
     return hipGetLastError();
   }
-  const int per = ceil_div(of.shard, 64);
+  const int per = ceil_div(of.shard, kLowCols);
   const LowArgs a{r, x, wp, p.m, p.adapters, p.rank, of.blocks, of.shard, per, per * of.blocks, splits, part};
   by_type(p.half, [&](auto type) {
     using T = decltype(type);
-    auto go = [&](auto turn, auto rb, auto tt) {
-      constexpr int RB = decltype(rb)::value, TT = decltype(tt)::value;
-      const dim3 grid(static_cast<unsigned>(ceil_div(p.m, TT * 16)) * splits, ceil_div(p.rank, kRankChunk));
-      hipLaunchKernelGGL((k_adapt_low<T, decltype(turn)::value != 0, RB, TT>), grid, dim3(kThreads), 0, s, a);
+    auto go = [&](auto turn, auto rb) {
+      const dim3 grid(static_cast<unsigned>(ceil_div(p.m, kLowRows)) * splits, ceil_div(p.rank, kRankChunk));
+      hipLaunchKernelGGL((k_adapt_low<T, decltype(turn)::value != 0, decltype(rb)::value>), grid, dim3(kThreads), 0, s,
+                         a);
     };
     if (turned)
-      p.rank <= 16 ? go(Int<1>{}, Int<1>{}, Int<4>{}) : go(Int<1>{}, Int<4>{}, Int<4>{});
+      p.rank <= 16 ? go(Int<1>{}, Int<1>{}) : go(Int<1>{}, Int<4>{});
     else
-      p.rank <= 16 ? go(Int<0>{}, Int<1>{}, Int<4>{}) : go(Int<0>{}, Int<4>{}, Int<4>{});
+      p.rank <= 16 ? go(Int<0>{}, Int<1>{}) : go(Int<0>{}, Int<4>{});
   });
   return hipGetLastError();
 }
@@ -796,12 +824,13 @@ hipError_t launch_adapt_halves(const AdaptPlan &p, hipStream_t s) {
 }
 
 hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Blocked &of,
-                              const unsigned short *low, const int *largest, bool turned, bool wide,
-                              void *out, hipStream_t s) {
-  const int per = ceil_div(of.shard, 64);
-  const OuterArgs a{r.pos, p.seg, largest, static_cast<const unsigned short *>(of.p), low, out, p.m, p.rank,
-                    p.padded, of.blocks, of.shard, per};
-  const dim3 grid(per * of.blocks, p.adapters, ceil_div(p.rank, kRankChunk));
+                              const unsigned short *low, const int *largest, bool turned, int parts,
+                              float *part, bool wide, void *out, hipStream_t s) {
+  const int per = ceil_div(of.shard, 64), chunks = per * of.blocks;
+  const bool whole = parts == 1;
+  const OuterArgs a{r.pos, p.seg, largest, static_cast<const unsigned short *>(of.p), low, whole ? out : part, p.m,
+                    p.adapters, p.rank, p.padded, of.blocks, of.shard, per, chunks};
+  const dim3 grid(ceil_div(chunks, 4), p.adapters * parts, ceil_div(p.rank, kRankChunk));
   by_type(p.half, [&](auto type) {
     using T = decltype(type);
     auto go = [&](auto turn, auto rb, auto fp32) {
@@ -811,10 +840,19 @@ hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Bloc
     auto ranks = [&](auto turn, auto fp32) {
       p.rank <= 16 ? go(turn, Int<1>{}, fp32) : go(turn, Int<4>{}, fp32);
     };
+    const bool fp32 = wide || !whole;
     if (turned)
-      wide ? ranks(Int<1>{}, Int<1>{}) : ranks(Int<1>{}, Int<0>{});
+      fp32 ? ranks(Int<1>{}, Int<1>{}) : ranks(Int<1>{}, Int<0>{});
     else
-      wide ? ranks(Int<0>{}, Int<1>{}) : ranks(Int<0>{}, Int<0>{});
+      fp32 ? ranks(Int<0>{}, Int<1>{}) : ranks(Int<0>{}, Int<0>{});
+    if (whole) return;
+    const size_t n = static_cast<size_t>(p.adapters) * p.rank * of.blocks * of.shard;
+    const int want = ceil_div(static_cast<long long>(n), 8 * kThreads);
+    const dim3 sums(want < 2048 ? want : 2048);
+    if (wide)
+      hipLaunchKernelGGL((k_adapt_parts<T, true>), sums, dim3(kThreads), 0, s, part, parts, n, out);
+    else
+      hipLaunchKernelGGL((k_adapt_parts<T, false>), sums, dim3(kThreads), 0, s, part, parts, n, out);
   });
   return hipGetLastError();
 }

@@ -84,10 +84,15 @@ size_t lay_out(const hg_adapt_shape &s, int kind, char *ws, AdaptPlan *p) {
   p->ut = reinterpret_cast<unsigned short *>(take(4 * static_cast<size_t>(s.rank) * p->padded));
   p->gt = reinterpret_cast<unsigned short *>(take(4 * static_cast<size_t>(s.rank) * p->padded));
   p->at = reinterpret_cast<unsigned short *>(take(2 * static_cast<size_t>(s.adapters) * s.rank * s.hidden));
+  p->parts_a = hg::adapt_parts(s.m, s.adapters, 1, s.hidden, s.rank);
+  p->parts_b = hg::adapt_parts(s.m, s.adapters, s.tp, s.shard, s.rank);
+  const size_t pairs = static_cast<size_t>(s.adapters) * s.rank;
+  if (p->parts_a > 1) p->pa = floats(pairs * s.hidden * p->parts_a);
+  if (p->parts_b > 1) p->pb = floats(pairs * s.tp * s.shard * p->parts_b);
   return at;
 }
 
-// What both calls check; `wide_bytes`: of y or dy.
+// Bytes of the arguments.
 struct Sizes {
   size_t y, x, a, b, scale, index;
 };
@@ -211,8 +216,8 @@ HG_API int hg_adapt_grad(const hg_adapt_shape *s, const void *dy, const void *x,
   if (p.g) HIP_TRY(hg::launch_adapt_low(p, rows, wide_y, b, true, p.split_g, p.pg, st));
   HIP_TRY(hg::launch_adapt_join(p, rows, scale, st));
   if (da || db) HIP_TRY(hg::launch_adapt_halves(p, st));
-  if (db) HIP_TRY(hg::launch_adapt_outer(p, rows, wide_y, p.ut, p.head, true, wide != 0, db, st));
-  if (da) HIP_TRY(hg::launch_adapt_outer(p, rows, wide_x, p.gt, p.head + 1, false, wide != 0, da, st));
+  if (db) HIP_TRY(hg::launch_adapt_outer(p, rows, wide_y, p.ut, p.head, true, p.parts_b, p.pb, wide != 0, db, st));
+  if (da) HIP_TRY(hg::launch_adapt_outer(p, rows, wide_x, p.gt, p.head + 1, false, p.parts_a, p.pa, wide != 0, da, st));
   if (dx) {
     HIP_TRY(hg::launch_adapt_turn(p, a, st));
     HIP_TRY(hg::launch_adapt_up(p, rows, p.g, 1, nullptr, p.at, Blocked{nullptr, 1, s->hidden}, dx, st));

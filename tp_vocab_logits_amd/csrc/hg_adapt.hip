@@ -110,34 +110,65 @@ __global__ __launch_bounds__(kThreads) void k_adapt_row(AdaptRows rows, const un
 }
 
 // ---------------------------------------------------------------------------
+// Loads straight into LDS (16 bytes per lane, at lds + 16 * lane), three stages deep,
+// for the two kernels that stream the wide matrices. Written as an instruction
+// because the compiler, which knows that the builtin form writes LDS, waits for
+// every load in flight before it reads LDS; there is no output register, and the
+// order against LDS reads is kept by the waits and barriers below. Each lane has
+// an address of its own (rows are gathered); what lies outside is read from kZeros,
+// so that every wave's count of loads is the same in every step.
+
+__device__ __align__(16) unsigned char kZeros[16];
+
+__device__ __forceinline__ void async16(const void *src, unsigned char *lds) {
+  const uint32_t at = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char *)lds));
+  __asm__ __volatile__("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                       :
+                       : "s"(at), "v"(src)
+                       : "memory");
+}
+// The same for 4 bytes per lane.
+__device__ __forceinline__ void async4(const void *src, unsigned char *lds) {
+  const uint32_t at = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char *)lds));
+  __asm__ __volatile__("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+                       :
+                       : "s"(at), "v"(src)
+                       : "memory");
+}
+
+constexpr int kStages = 3;
+constexpr int kWaveBytes = 32 * 128;                   // 32 rows x 64 columns, or the like
+constexpr int kStageAll = 4 * kWaveBytes + kSubBytes;  // four waves' and 8 KB that they share (or 2 KB each)
+
+// ---------------------------------------------------------------------------
 // Low-rank products of many rows: part[split][p][rank] = sum over the split's
 // columns of of[p][c] w_i[rank][c]. A workgroup has 128 rows (two tiles per wave), a
 // part of the columns and up to 64 ranks (RB blocks of 16). Its waves share w's
-// 128 columns of a step in LDS, so that w comes through the L2 once per 128 rows,
-// half of what the rows themselves take; of is read into registers as the matrix
-// cores want it, 256 bytes of a row at a time, a step ahead. w's columns are next
-// to each other in memory (A), or, if TURNED, its ranks are (B): those are turned
-// while they are read from LDS.
+// 64 columns of a step, so that w comes through the L2 once per 128 rows, half of
+// what the rows themselves take; up to 16 ranks (2 KB) every wave loads its own
+// and none waits for another. w's columns are next to each other in memory (A), or,
+// if TURNED, its ranks are (B): those are turned while they are read from LDS.
 
 struct LowArgs {
   AdaptRows rows;
   const unsigned short *of, *w;
   int m, adapters, rank;
-  int blocks, shard, per_block, chunks;  // chunks of kLowCols columns per block, in all
+  int blocks, shard, per_block, chunks;  // chunks of 64 columns per block, in all
   int splits;
   float *part;
 };
 
-constexpr int kLowRows = 128, kLowCols = 128;
+constexpr int kLowRows = 128;
 
 template <class T, bool TURNED, int RB>
 __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
-  constexpr int TT = 2, KS = kLowCols / 32;
-  constexpr int kRow = TURNED ? RB * 32 + 16 : kLowCols * 2 + 16;  // bytes of an LDS row: ranks, or columns
-  constexpr int kPieces = TURNED ? RB * 2 : kLowCols / 8;          // 16-byte pieces of one
-  __shared__ __align__(16) unsigned char lds[(TURNED ? kLowCols : RB * 16) * kRow];
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  static_assert(RB == 1 || RB == 4);
+  constexpr int TT = 2;
+  __shared__ __align__(1024) unsigned char lds[kStages * kStageAll];
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int ml = lane & 15, g = lane >> 4;
   const int groups = (a.m + kLowRows - 1) / kLowRows;
   const int split = static_cast<int>(blockIdx.x) / groups, group = static_cast<int>(blockIdx.x) - split * groups;
@@ -148,16 +179,28 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
   const int p0 = group * kLowRows;
   const int pend = a.m < p0 + kLowRows ? a.m : p0 + kLowRows;
   const size_t columns = static_cast<size_t>(a.blocks) * a.shard;
+  const LoadLane lr = load_lane<false>(lane), lc = load_lane<true>(lane);
+  FragLane<false> fr;
+  FragLane<true> fc;
+  fr.init(lane);
+  fc.init(lane);
 
-  int key[TT], row[TT];
+  int key[TT];  // of the rows whose results this lane holds
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     const int p = p0 + (wave * TT + t) * 16 + ml;
     key[t] = p < a.m ? a.rows.keys[p] : a.adapters;
-    row[t] = p < a.m ? a.rows.pos[p] : 0;
+  }
+  int lkey[4];  // of the rows that it loads
+  const unsigned short *src[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int p = p0 + wave * 32 + 8 * q + lr.row;
+    lkey[q] = p < a.m ? a.rows.keys[p] : a.adapters;
+    src[q] = a.of + static_cast<size_t>(p < a.m ? a.rows.pos[p] : 0) * a.shard + lr.chunk[q & 1] * 8;
   }
   int at = p0;  // the first position of the adapter in turn
-  int cur = a.rows.keys[at];
+  int cur = __builtin_amdgcn_readfirstlane(a.rows.keys[at]);
   while (cur < a.adapters) {
     bool active[TT];
 #pragma unroll
@@ -169,63 +212,90 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
       for (int b = 0; b < RB; ++b) acc[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
     const unsigned short *const wi = a.w + static_cast<size_t>(cur) * a.rank * columns;
 
-    s16x8 next[TT][KS], piece[RB];
-    auto fetch = [&](int chunk) __attribute__((always_inline)) {
-      const int block = chunk / a.per_block, c0 = (chunk - block * a.per_block) * kLowCols;
+    // six loads per wave and step
+    auto issue = [&](int chunk, int stage) __attribute__((always_inline)) {
+      const int block = chunk / a.per_block, c0 = (chunk - block * a.per_block) * 64;
       const int left = a.shard - c0;  // columns of the block from here on
-      const unsigned short *const of = a.of + static_cast<size_t>(block) * a.m * a.shard + c0;
+      const size_t off = static_cast<size_t>(block) * a.m * a.shard + c0;
       const size_t col = static_cast<size_t>(block) * a.shard + c0;
+      unsigned char *const st = lds + stage * kStageAll + wave * kWaveBytes;
 #pragma unroll
-      for (int t = 0; t < TT; ++t)
+      for (int q = 0; q < 4; ++q) {
+        const bool real = lkey[q] == cur && lr.chunk[q & 1] * 8 < left;
+        async16(real ? static_cast<const void *>(src[q] + off) : kZeros, st + q * 1024);
+      }
+      unsigned char *const sw = lds + stage * kStageAll + 4 * kWaveBytes + wave * 2048;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const int c = ks * 32 + 8 * g;
-          next[t][ks] = active[t] && c < left ? load8(of + static_cast<size_t>(row[t]) * a.shard + c) : zero8();
+      for (int t = 0; t < 2; ++t) {
+        const int q = RB == 1 ? t : 2 * wave + t;
+        bool real;
+        const unsigned short *p;
+        if constexpr (!TURNED) {
+          const int r = 8 * q + lr.row, c = lr.chunk[t] * 8;
+          real = r < ranks && c < left;
+          p = wi + static_cast<size_t>(rc + r) * columns + col + c;
+        } else if constexpr (RB == 1) {  // lines of 16 ranks
+          const int v = 32 * q + (lane >> 1), e = (lane & 1) * 8;
+          real = v < left && e < ranks;
+          p = wi + (col + v) * a.rank + e;
+        } else {
+          const int v = 8 * q + lc.row, e = lc.chunk[t] * 8;
+          real = v < left && e < ranks;
+          p = wi + (col + v) * a.rank + rc + e;
         }
-#pragma unroll
-      for (int q = 0; q < RB; ++q) {
-        const int id = q * kThreads + tid, line = id / kPieces, e = (id % kPieces) * 8;
-        if constexpr (TURNED)
-          piece[q] = line < left && e < ranks ? load8(wi + (col + line) * a.rank + rc + e) : zero8();
-        else
-          piece[q] = line < ranks && e < left ? load8(wi + static_cast<size_t>(rc + line) * columns + col + e)
-                                              : zero8();
+        async16(real ? static_cast<const void *>(p) : kZeros, sw + t * 1024);
       }
     };
-    if (from < to) fetch(from);
-    for (int chunk = from; chunk < to; ++chunk) {
-      __syncthreads();  // the last step's reads
-#pragma unroll
-      for (int q = 0; q < RB; ++q) {
-        const int id = q * kThreads + tid, line = id / kPieces, e = id % kPieces;
-        *reinterpret_cast<s16x8 *>(lds + line * kRow + e * 16) = piece[q];
-      }
-      s16x8 xf[TT][KS];
+    auto multiply = [&](int stage) __attribute__((always_inline)) {
+      const unsigned char *const st = lds + stage * kStageAll + wave * kWaveBytes;
+      unsigned char *const sw = lds + stage * kStageAll + 4 * kWaveBytes + (RB == 1 ? wave * 2048 : 0);
+      s16x8 xf[TT][2];
 #pragma unroll
       for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) xf[t][ks] = next[t][ks];
-      __syncthreads();
-      if (chunk + 1 < to) fetch(chunk + 1);
+        for (int ks = 0; ks < 2; ++ks) xf[t][ks] = fr.read(st, t, ks);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+      for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
           s16x8 wf;
-          if constexpr (TURNED) {
+          if constexpr (!TURNED) {
+            wf = fr.read(sw, b, ks);
+          } else if constexpr (RB == 1) {
             typedef __attribute__((address_space(3))) s16x4 *lds4;
-            unsigned char *const q = lds + (ks * 32 + g * 8 + (ml >> 2)) * kRow + b * 32 + (ml & 3) * 8;
+            unsigned char *const q = sw + (ks * 32 + g * 8 + (ml >> 2)) * 32 + (ml & 3) * 8;
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q + 4 * kRow));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q + 4 * 32));
             wf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
           } else {
-            wf = *reinterpret_cast<const s16x8 *>(lds + (b * 16 + ml) * kRow + ks * 64 + g * 16);
+            wf = fc.read(sw, b, ks);
           }
 #pragma unroll
           for (int t = 0; t < TT; ++t)
             if (active[t]) acc[t][b] = T::mma(wf, xf[t][ks], acc[t][b]);
         }
+    };
+    const int n = to - from;
+    if (n > 0) issue(from, 0);
+    if (n > 1) issue(from + 1, 1);
+    int stage = 0;
+    for (int k = 0; k < n; ++k) {
+      // this step has landed, and the last one's reads are done, here and (RB > 1) in
+      // every wave
+      if (k + 1 < n)
+        wait_vm_lds<6>();
+      else
+        wait_vm_lds<0>();
+      if constexpr (RB > 1)
+        tile_barrier();
+      else
+        __asm__ __volatile__("" ::: "memory");
+      if (k + 2 < n) issue(from + k + 2, stage >= 1 ? stage - 1 : kStages - 1);
+      multiply(stage);
+      stage = stage + 1 < kStages ? stage + 1 : 0;
     }
+    wait_vm_lds<0>();
+    if constexpr (RB > 1) tile_barrier();
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -237,11 +307,12 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
               acc[t][b];
       }
     // the next adapter among the workgroup's rows (they are sorted)
-    while (at < pend && a.rows.keys[at] == cur) {
+    for (int same = 64; same == 64 && at < pend;) {
       const int p = at + lane;
-      at += __popcll(__ballot(p < pend && a.rows.keys[p < pend ? p : at] == cur));
+      same = __popcll(__ballot(p < pend && a.rows.keys[p < pend ? p : at] == cur));
+      at += same;
     }
-    cur = at < pend ? a.rows.keys[at] : a.adapters;
+    cur = at < pend ? __builtin_amdgcn_readfirstlane(a.rows.keys[at]) : a.adapters;
   }
 }
 
@@ -549,9 +620,10 @@ __global__ __launch_bounds__(kThreads) void k_adapt_turn(const unsigned short *a
 // Sums over an adapter's rows: out_i[rank][column] = sum_p low[p][rank] of[p][column]
 // (dA, of = x), or turned, [column][rank] (dB, of = dy). A workgroup has one
 // adapter, 64 columns for each of its four waves and up to 64 ranks, and goes
-// through the rows, or a part of them, 32 at a time: the waves share the rows'
-// low-rank values (half of the bytes that their own columns take) and turn of in
-// LDS. A step's loads are issued before the last one's products.
+// through the rows, or a part of them, 32 at a time, as above: the waves share the
+// rows' low-rank values (half of the bytes that their own columns take; up to 16
+// ranks each loads its own), of is turned while it is read from LDS. The rows'
+// places are loaded two steps before the rows.
 
 struct OuterArgs {
   const int *pos, *seg, *largest;
@@ -564,13 +636,11 @@ struct OuterArgs {
 // added up by another launch if there are several.
 template <class T, bool TURNED, int RB, bool WIDE>
 __global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
-  constexpr int kRow = 128 + 16;         // bytes of an LDS row of 64 columns
-  constexpr int kLowRow = 64 + 16;       // of a rank's 32 rows
-  constexpr int kHalf = RB * 16 * kLowRow;
-  constexpr int kQ = (RB + 1) / 2;       // 16-byte pieces of low per thread
-  __shared__ __align__(16) unsigned char lds[4 * 32 * kRow + 2 * kHalf];
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  static_assert(RB == 1 || RB == 4);
+  constexpr int kPlaces = 4;  // steps' places at once, 256 bytes each, per wave
+  __shared__ __align__(1024) unsigned char lds[kStages * kStageAll + 4 * kPlaces * 256];
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int ml = lane & 15, g = lane >> 4;
   const int part = static_cast<int>(blockIdx.y) / a.adapters, i = static_cast<int>(blockIdx.y) - part * a.adapters;
   const int parts = static_cast<int>(gridDim.y) / a.adapters;
@@ -584,71 +654,104 @@ __global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
   const int first = from & ~7;  // (low is read eight rows at a time)
   const int steps = (to - first + 31) / 32;
   const int s0 = static_cast<int>(static_cast<long long>(steps) * part / parts);
-  const int s1 = static_cast<int>(static_cast<long long>(steps) * (part + 1) / parts);
+  const int n = static_cast<int>(static_cast<long long>(steps) * (part + 1) / parts) - s0;
+  const LoadLane lc = load_lane<true>(lane);
+  FragLane<true> fc;
+  fc.init(lane);
   const unsigned short *const of = a.of + static_cast<size_t>(block) * a.m * a.shard + c0;
-  unsigned char *const st = lds + wave * 32 * kRow, *const sl = lds + 4 * 32 * kRow;
+  unsigned char *const places = lds + kStages * kStageAll + wave * kPlaces * 256;
   f32x4 acc[RB][4];
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
     for (int v = 0; v < 4; ++v) acc[b][v] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  s16x8 piece[4], low[kQ];
-  auto fetch = [&](int step) __attribute__((always_inline)) {
-    const int p0 = first + step * 32;
+  // the places of step k's rows (positions past the last row: that one's)
+  auto locate = [&](int k) __attribute__((always_inline)) {
+    const int p = first + (s0 + k) * 32 + (lane & 31);
+    async4(a.pos + (p < a.m ? p : a.m - 1), places + (k & (kPlaces - 1)) * 256);
+  };
+  // seven loads per wave and step
+  auto issue = [&](int k, int stage) __attribute__((always_inline)) {
+    locate(k + 2);
+    const int p0 = first + (s0 + k) * 32;
+    unsigned char *const st = lds + stage * kStageAll + wave * kWaveBytes;
+    const int *const place = reinterpret_cast<const int *>(places + (k & (kPlaces - 1)) * 256);
+    int row[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) row[q] = place[8 * q + lc.row];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int p = p0 + q * 8 + (lane >> 3), c = (lane & 7) * 8;
-      piece[q] = p >= from && p < to && c < left ? load8(of + static_cast<size_t>(a.pos[p]) * a.shard + c) : zero8();
+      const int p = p0 + 8 * q + lc.row, c = lc.chunk[q & 1] * 8;
+      const bool real = p >= from && p < to && c < left;
+      async16(real ? static_cast<const void *>(of + static_cast<size_t>(row[q]) * a.shard + c) : kZeros,
+              st + q * 1024);
     }
+    // pieces of 16 ranks' 32 rows, a rank's four chunks swizzled by (rank >> 2) & 3
+    unsigned char *const sl = lds + stage * kStageAll + 4 * kWaveBytes + wave * 2048;
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) {  // pieces (half, rank, eight rows)
-      const int id = q * kThreads + tid, line = id >> 2, p = p0 + (id & 3) * 8;
+    for (int t = 0; t < 2; ++t) {
+      const int line = (RB == 1 ? t : 2 * wave + t) * 16 + (lane >> 2);  // half and rank
       const int h = line / (RB * 16), r = line - h * (RB * 16);
-      low[q] = h < 2 && r < ranks && p < to
-                   ? load8(a.low + static_cast<size_t>(h * a.rank + rc + r) * a.padded + p)
-                   : zero8();
+      const int p = p0 + ((lane & 3) ^ (line >> 2 & 3)) * 8;
+      const bool real = r < ranks && p < to;
+      async16(real ? static_cast<const void *>(a.low + static_cast<size_t>(h * a.rank + rc + r) * a.padded + p) : kZeros,
+              sl + t * 1024);
     }
   };
-  if (s0 < s1) fetch(s0);
-  for (int step = s0; step < s1; ++step) {
-    const int p0 = first + step * 32;
-    __syncthreads();  // the last step's reads
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<s16x8 *>(st + (q * 8 + (lane >> 3)) * kRow + (lane & 7) * 16) = piece[q];
-#pragma unroll
-    for (int q = 0; q < kQ; ++q) {
-      const int id = q * kThreads + tid, p = p0 + (id & 3) * 8;
-      s16x8 v = low[q];
-      if (p < from || p + 8 > to) {  // rows of other adapters
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (p + e < from || p + e >= to) v[e] = 0;
-      }
-      if (id < RB * 128) *reinterpret_cast<s16x8 *>(sl + (id >> 2) * kLowRow + (id & 3) * 16) = v;
-    }
-    __syncthreads();
-    if (step + 1 < s1) fetch(step + 1);
+  auto multiply = [&](int k, int stage) __attribute__((always_inline)) {
+    const int p0 = first + (s0 + k) * 32;
+    const unsigned char *const st = lds + stage * kStageAll + wave * kWaveBytes;
+    const unsigned char *const sl = lds + stage * kStageAll + 4 * kWaveBytes + (RB == 1 ? wave * 2048 : 0);
     s16x8 lf[RB][2];
 #pragma unroll
     for (int b = 0; b < RB; ++b)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        lf[b][h] = *reinterpret_cast<const s16x8 *>(sl + h * kHalf + (b * 16 + ml) * kLowRow + g * 16);
-    typedef __attribute__((address_space(3))) s16x4 *lds4;
+      for (int h = 0; h < 2; ++h) {
+        const int line = h * (RB * 16) + b * 16 + ml;
+        lf[b][h] = *reinterpret_cast<const s16x8 *>(sl + line * 64 + ((g ^ (ml >> 2)) << 4));
+      }
+    if (p0 < from || p0 + 32 > to) {  // rows of other adapters
+      const int p = p0 + 8 * g;
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (p + e < from || p + e >= to) lf[b][h][e] = 0;
+    }
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      unsigned char *const q = st + (g * 8 + (ml >> 2)) * kRow + v * 32 + (ml & 3) * 8;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q + 4 * kRow));
-      const s16x8 of8 = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      const s16x8 of8 = fc.read(st, v, 0);
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           acc[b][v] = TURNED ? T::mma(lf[b][h], of8, acc[b][v]) : T::mma(of8, lf[b][h], acc[b][v]);
     }
+  };
+  if (n > 0) {
+    locate(0);
+    locate(1);
+    wait_vm_lds<0>();
+    __asm__ __volatile__("" ::: "memory");
+    issue(0, 0);
+  }
+  if (n > 1) issue(1, 1);
+  int stage = 0;
+  for (int k = 0; k < n; ++k) {
+    if (k + 1 < n)
+      wait_vm_lds<7>();
+    else
+      wait_vm_lds<0>();
+    if constexpr (RB > 1)
+      tile_barrier();
+    else
+      __asm__ __volatile__("" ::: "memory");
+    if (k + 2 < n) issue(k + 2, stage >= 1 ? stage - 1 : kStages - 1);
+    multiply(k, stage);
+    stage = stage + 1 < kStages ? stage + 1 : 0;
   }
   const float inv = from_unit<T>(__builtin_bit_cast(float, *a.largest));
   const size_t columns = static_cast<size_t>(a.blocks) * a.shard;
@@ -727,11 +830,11 @@ int adapt_splits(int m, int blocks, int shard, int rank, bool few) {
     const int steps = ceil_div(shard, 512), want = 256 / m;
     return want < 1 ? 1 : want < steps ? want : steps;
   }
-  // k_adapt_low: about 1024 workgroups, at least two steps each
+  // k_adapt_low: about 1024 workgroups, at least four steps each
   const long long groups = ceil_div(m, kLowRows) * static_cast<long long>(ceil_div(rank, kRankChunk));
-  const int chunks = blocks * ceil_div(shard, kLowCols);
+  const int chunks = blocks * ceil_div(shard, 64);
   long long s = 1024 / groups;
-  if (s > chunks / 2) s = chunks / 2;
+  if (s > chunks / 4) s = chunks / 4;
   if (s > 64) s = 64;
   return s < 1 ? 1 : static_cast<int>(s);
 }
@@ -756,7 +859,7 @@ hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocke
     });
     return hipGetLastError();
   }
-  const int per = ceil_div(of.shard, kLowCols);
+  const int per = ceil_div(of.shard, 64);
   const LowArgs a{r, x, wp, p.m, p.adapters, p.rank, of.blocks, of.shard, per, per * of.blocks, splits, part};
   by_type(p.half, [&](auto type) {
     using T = decltype(type);

@@ -34,6 +34,8 @@ struct AdaptPlan {
   void *sort_ws;
   float *pu, *pg;        // [split][m][rank] partial sums of u and g
   float *u, *g;          // [m][rank] scaled sums, by sorted position
+  unsigned short *low;   // [m][2][16 or 64] their halves, where the second product streams
+  float *back;           // [m] and fp16's factors
   int *head;             // [0], [1]: bits of the largest |u| and |g|
   int *seg;              // [adapters + 1] sorted positions where they begin
   unsigned short *ut, *gt;  // [2][ranks][padded] upper and lower halves of u and g
@@ -64,9 +66,11 @@ hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Bloc
                               float *part, bool wide, void *out, hipStream_t s);
 hipError_t launch_adapt_turn(const AdaptPlan &p, const void *a, hipStream_t s);
 
-// Whether hg_adapt's second product takes big pieces (64 rows x 1024 columns per
-// workgroup) or small ones (16 x 256).
-inline bool adapt_big(int m, int rank) { return m > kFewRows && rank <= kRankChunk; }
+// Whether the second product goes through many rows with W's fragments kept
+// (k_adapt_stream): sorted rows, 64 of an adapter on average, ranks that fit.
+inline bool adapt_streams(int m, int adapters, int rank) {
+  return m > kFewRows && m / 64 >= adapters && rank <= kRankChunk;
+}
 
 // Parts that a sum over `columns` columns of `m` rows is cut into.
 int adapt_splits(int m, int blocks, int shard, int rank, bool few);

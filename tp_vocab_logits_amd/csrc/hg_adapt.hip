@@ -317,10 +317,117 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// out = y + low W^T: W is [adapters][columns][rank]. A workgroup has TT tiles of
-// rows and kCol blocks of 64 columns for each of its four waves. A lane of a tile
-// holds one row's 8 + 8 columns: the rows of W are dealt to the matrix cores' rows
-// so that these are next to each other (stores of 64 bytes per row).
+// A row's low-rank values: the parts' sum, scaled, as two 16-bit numbers each (fp16:
+// brought to a largest of 1 .. 2). PER threads next to each other share a row, each
+// has PIECES times eight ranks.
+
+template <class T, int PER, int PIECES>
+__device__ __forceinline__ void low_values(const float *part, const float *scale, int key, int p, int sub,
+                                           int m, int adapters, int rank, int splits,
+                                           u32x4 (&hi)[PIECES], u32x4 (&lo)[PIECES], float &back) {
+  float v[PIECES][8];
+  float largest = 0.f;
+  const float s = key < adapters && scale ? scale[key] : 1.f;
+#pragma unroll
+  for (int q = 0; q < PIECES; ++q) {
+    const int e = (q * PER + sub) * 8;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) v[q][t] = 0.f;
+    if (key < adapters && e < rank) {
+      for (int k0 = 0; k0 < splits; k0 += 4) {  // (eight loads in flight)
+        f32x4 w[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k0 + k < splits) {
+            const f32x4 *const from =
+                reinterpret_cast<const f32x4 *>(part + (static_cast<size_t>(k0 + k) * m + p) * rank + e);
+            w[k][0] = from[0];
+            w[k][1] = from[1];
+          }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k0 + k < splits)
+#pragma unroll
+            for (int t = 0; t < 8; ++t) v[q][t] += w[k][t >> 2][t & 3];
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      v[q][t] *= s;
+      largest = fmaxf(largest, fabsf(v[q][t]));
+    }
+  }
+  if constexpr (T::kHalf) {
+#pragma unroll
+    for (int d = 1; d < PER; d <<= 1) largest = fmaxf(largest, __shfl_xor(largest, d));
+  }
+  const float unit = to_unit<T>(largest);
+  back = from_unit<T>(largest);
+#pragma unroll
+  for (int q = 0; q < PIECES; ++q)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      uint32_t h0, l0, h1, l1;
+      halves<T>(v[q][2 * t] * unit, h0, l0);
+      halves<T>(v[q][2 * t + 1] * unit, h1, l1);
+      hi[q][t] = h0 | h1 << 16;
+      lo[q][t] = l0 | l1 << 16;
+    }
+}
+
+// All rows' values by sorted position: [m][2][RANKS] (16 or 64 ranks, zeros past
+// `rank`), and fp16's factors back.
+template <class T, int RANKS>
+__global__ __launch_bounds__(kThreads) void k_adapt_values(const float *part, const float *scale, const int *keys,
+                                                           int m, int adapters, int rank, int splits,
+                                                           unsigned short *low, float *back) {
+  constexpr int kPer = RANKS / 8;
+  const int tid = static_cast<int>(threadIdx.x);
+  const int p = static_cast<int>(blockIdx.x) * (kThreads / kPer) + tid / kPer, sub = tid % kPer;
+  if (p >= m) return;
+  u32x4 hi[1], lo[1];
+  float inv;
+  low_values<T, kPer, 1>(part, scale, keys[p], p, sub, m, adapters, rank, splits, hi, lo, inv);
+  unsigned short *const row = low + static_cast<size_t>(p) * (2 * RANKS) + sub * 8;
+  *reinterpret_cast<u32x4 *>(row) = hi[0];
+  *reinterpret_cast<u32x4 *>(row + RANKS) = lo[0];
+  if (T::kHalf && sub == 0) back[p] = inv;
+}
+
+// ---------------------------------------------------------------------------
+// out = y + low W^T: W is [adapters][columns][rank]. A workgroup has a tile of 16
+// rows and 64 columns for each of its four waves. A lane of a tile holds one row's
+// 8 + 8 columns: the rows of W are dealt to the matrix cores' rows so that these are
+// next to each other (stores of 64 bytes per row). For few rows, and for rows of
+// many adapters.
+
+// acc += W's fragments x a row's values, given by read(half, ks); BOTH: the two halves
+// of up to 16 ranks are one fragment.
+template <class T, bool BOTH, int KF, class F>
+__device__ __forceinline__ void add_low(f32x4 (&acc)[4], const s16x8 (&wf)[4][KF], F read) {
+#pragma unroll
+  for (int ks = 0; ks < KF; ++ks)
+#pragma unroll
+    for (int half = 0; half < (BOTH ? 1 : 2); ++half) {
+      const s16x8 f = read(half, ks);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[v] = T::mma(wf[v][ks], f, acc[v]);
+    }
+}
+
+// y + inv * res, eight of a row, rounded once.
+template <class T>
+__device__ __forceinline__ u32x4 sum8(s16x8 y, const f32x4 *res, float inv) {
+  u32x4 o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float f0 = __builtin_fmaf(res[e >> 1][(2 * e) & 3], inv, from16<T>(static_cast<unsigned short>(y[2 * e])));
+    const float f1 =
+        __builtin_fmaf(res[e >> 1][(2 * e + 1) & 3], inv, from16<T>(static_cast<unsigned short>(y[2 * e + 1])));
+    o[e] = bits16<T>(f0) | bits16<T>(f1) << 16;
+  }
+  return o;
+}
 
 struct UpArgs {
   AdaptRows rows;
@@ -335,15 +442,14 @@ struct UpArgs {
 
 // KS: steps of 32 ranks held at once: 0 for up to 16 ranks (upper and lower halves
 // share one step), 2 otherwise (more than 64 ranks: in turns).
-template <class T, int KS, int TT, int COL>
+template <class T, int KS>
 __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
-  constexpr int kRanks = KS == 0 ? 16 : TT > 1 ? kRankChunk : HG_MAX_RANK;
+  constexpr int kRanks = KS == 0 ? 16 : HG_MAX_RANK;
   constexpr int kRow = 2 * kRanks + 8;  // 16-bit elements of an LDS row: upper, lower halves
-  constexpr int kPer = kThreads / (TT * 16);  // threads per row of the prologue
-  constexpr int kPieces = (kRanks / 8 + kPer - 1) / kPer;
+  constexpr int kPieces = KS == 0 ? 1 : 2;
   constexpr int KF = KS ? KS : 1;
-  __shared__ __align__(16) unsigned short low[TT * 16 * kRow];
-  __shared__ float back[TT * 16];
+  __shared__ __align__(16) unsigned short low[16 * kRow];
+  __shared__ float back[16];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ml = lane & 15, g = lane >> 4;
@@ -353,160 +459,257 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
   const int eight = id / (8 * a.groups), in = id - eight * 8 * a.groups;
   const int strip = eight * 8 + in % 8, group = in / 8;
   if (strip >= a.strips) return;
-  const int p0 = group * TT * 16;
+  const int p0 = group * 16;
 
   {
-    const int r = tid / kPer, sub = tid % kPer, p = p0 + r;
+    const int r = tid / 16, sub = tid % 16, p = p0 + r;
     const int key = p < a.m ? key_of_row(a.rows, p, a.adapters) : a.adapters;
-    float v[kPieces][8];
-    float largest = 0.f;
-    const float s = key < a.adapters && a.scale ? a.scale[key] : 1.f;
+    u32x4 hi[kPieces], lo[kPieces];
+    float inv;
+    low_values<T, 16, kPieces>(a.part, a.scale, key, p, sub, a.m, a.adapters, a.rank, a.splits, hi, lo, inv);
+    if (sub == 0) back[r] = inv;
 #pragma unroll
     for (int q = 0; q < kPieces; ++q) {
-      const int e = (q * kPer + sub) * 8;
-#pragma unroll
-      for (int t = 0; t < 8; ++t) v[q][t] = 0.f;
-      if (key < a.adapters && e < a.rank) {
-        for (int k = 0; k < a.splits; ++k) {
-          const f32x4 *const from =
-              reinterpret_cast<const f32x4 *>(a.part + (static_cast<size_t>(k) * a.m + p) * a.rank + e);
-          const f32x4 lo = from[0], hi = from[1];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            v[q][t] += lo[t];
-            v[q][4 + t] += hi[t];
-          }
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        v[q][t] *= s;
-        largest = fmaxf(largest, fabsf(v[q][t]));
-      }
-    }
-    if constexpr (T::kHalf) {
-#pragma unroll
-      for (int d = 1; d < kPer; d <<= 1) largest = fmaxf(largest, __shfl_xor(largest, d));
-    }
-    const float unit = to_unit<T>(largest);
-    if (sub == 0) back[r] = from_unit<T>(largest);
-#pragma unroll
-    for (int q = 0; q < kPieces; ++q) {
-      const int e = (q * kPer + sub) * 8;
+      const int e = (q * 16 + sub) * 8;
       if (e < kRanks) {
-        u32x4 hi, lo;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          uint32_t h0, l0, h1, l1;
-          halves<T>(v[q][2 * t] * unit, h0, l0);
-          halves<T>(v[q][2 * t + 1] * unit, h1, l1);
-          hi[t] = h0 | h1 << 16;
-          lo[t] = l0 | l1 << 16;
-        }
-        *reinterpret_cast<u32x4 *>(low + r * kRow + e) = hi;
-        *reinterpret_cast<u32x4 *>(low + r * kRow + kRanks + e) = lo;
+        *reinterpret_cast<u32x4 *>(low + r * kRow + e) = hi[q];
+        *reinterpret_cast<u32x4 *>(low + r * kRow + kRanks + e) = lo[q];
       }
     }
   }
-  int key[TT];
-  size_t row[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int p = p0 + t * 16 + ml;
-    key[t] = p < a.m ? key_of_row(a.rows, p, a.adapters) : -1;  // -1: no row
-    row[t] = static_cast<size_t>(p < a.m ? row_of(a.rows, p) : 0) * a.shard;
-  }
+  const int p = p0 + ml;
+  const int key = p < a.m ? key_of_row(a.rows, p, a.adapters) : -1;  // -1: no row
+  const size_t row = static_cast<size_t>(p < a.m ? row_of(a.rows, p) : 0) * a.shard;
   __syncthreads();
 
   const int turns = KS == 0 ? 1 : (a.rank + kRankChunk - 1) / kRankChunk;
-  const bool in_place = a.y == a.out;
-#pragma unroll 1
-  for (int c = 0; c < COL; ++c) {
-    const int chunk = (strip * COL + c) * 4 + wave;
-    if (chunk >= a.chunks) break;
-    const int block = chunk / a.per_block, c0 = (chunk - block * a.per_block) * 64;
-    const int left = a.shard - c0;
-    const size_t at = static_cast<size_t>(block) * a.m * a.shard + c0;
-    const unsigned short *const wcol = a.w + (static_cast<size_t>(block) * a.shard + c0) * a.rank;
-    const size_t each = static_cast<size_t>(a.blocks) * a.shard * a.rank;
-    s16x8 yv[TT][2];
+  const int chunk = strip * 4 + wave;
+  if (chunk >= a.chunks) return;
+  const int block = chunk / a.per_block, c0 = (chunk - block * a.per_block) * 64;
+  const int left = a.shard - c0;
+  const size_t at = static_cast<size_t>(block) * a.m * a.shard + c0;
+  const unsigned short *const wcol = a.w + (static_cast<size_t>(block) * a.shard + c0) * a.rank;
+  const size_t each = static_cast<size_t>(a.blocks) * a.shard * a.rank;
+  s16x8 yv[2];
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
+  for (int h = 0; h < 2; ++h)
+    yv[h] = a.y && key >= 0 && h * 32 + 8 * g < left ? load8(a.y + at + row + h * 32 + 8 * g) : zero8();
+  f32x4 res[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        yv[t][h] = a.y && key[t] >= 0 && h * 32 + 8 * g < left ? load8(a.y + at + row[t] + h * 32 + 8 * g)
-                                                               : zero8();
-    int have = -1;
-    s16x8 wf[4][KF];
+  for (int v = 0; v < 4; ++v) res[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const unsigned short *const mine = low + ml * kRow;
+  unsigned todo = static_cast<unsigned>(__ballot(key >= 0 && key < a.adapters)) & 0xFFFF;
+  while (todo) {
+    const int cur = __builtin_amdgcn_readlane(key, __builtin_ctz(todo));
+    todo &= ~static_cast<unsigned>(__ballot(key == cur));
+    const unsigned short *const wi = wcol + static_cast<size_t>(cur) * each;
+    f32x4 acc[4];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
+    for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int turn = 0; turn < turns; ++turn) {
+      const int rc = turn * kRankChunk;
+      s16x8 wf[4][KF];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int col = 32 * (v >> 1) + 8 * (ml >> 2) + 4 * (v & 1) + (ml & 3);
+#pragma unroll
+        for (int ks = 0; ks < KF; ++ks) {
+          const int r = KS == 0 ? 8 * (g & 1) : rc + ks * 32 + 8 * g;
+          wf[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
+        }
+      }
+      add_low<T, KS == 0>(acc, wf, [&](int half, int ks) __attribute__((always_inline)) {
+        return load8(mine + (KS == 0 ? 8 * g : half * kRanks + rc + ks * 32 + 8 * g));
+      });
+    }
+    const bool take = key == cur;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) res[v][e] = take ? acc[v][e] : res[v][e];
+  }
+  const bool has = key < a.adapters;
+  if (key < 0 || (a.y == a.out && !has)) return;
+  const float inv = back[ml];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (h * 32 + 8 * g < left)
+      *reinterpret_cast<u32x4 *>(a.out + at + row + h * 32 + 8 * g) =
+          has ? sum8<T>(yv[h], &res[2 * h], inv) : __builtin_bit_cast(u32x4, yv[h]);
+}
+
+// The same for many rows of few adapters: a workgroup keeps its 256 columns (64 per
+// wave), and with them W's fragments, and goes through the rows, or a part of them,
+// 32 at a time, y and the low-rank values loaded straight into LDS as above. The
+// first form reads W's 8 KB for every 16 rows of 64 columns (2 KB); with 64 rows it
+// still took 365 us where the copy of y alone takes 295 (2047 rows, V = 163840,
+// rank 64).
+
+struct StreamArgs {
+  const int *keys, *pos;
+  const unsigned short *low, *w, *y;
+  const float *back;
+  unsigned short *out;
+  int m, adapters, rank, blocks, shard, per_block, chunks;  // chunks of 64 columns
+};
+
+// RB: blocks of 16 ranks, 1 or 4.
+template <class T, int RB>
+__global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
+  static_assert(RB == 1 || RB == 4);
+  constexpr int KF = RB == 1 ? 1 : 2;
+  constexpr int kPlaces = 4, kPlace = 512;          // per wave and step: places, keys, factors
+  constexpr int kLoads = T::kHalf ? 8 : 7;          // per wave and step
+  __shared__ __align__(1024) unsigned char lds[kStages * kStageAll + 4 * kPlaces * kPlace];
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int ml = lane & 15, g = lane >> 4;
+  const int chunk = static_cast<int>(blockIdx.x) * 4 + wave;
+  const bool has = chunk < a.chunks;
+  const int block = has ? chunk / a.per_block : 0, c0 = has ? (chunk - block * a.per_block) * 64 : 0;
+  const int left = has ? a.shard - c0 : 0;
+  const int steps = (a.m + 31) / 32;
+  const int s0 = static_cast<int>(static_cast<long long>(steps) * blockIdx.y / gridDim.y);
+  const int n = static_cast<int>(static_cast<long long>(steps) * (blockIdx.y + 1) / gridDim.y) - s0;
+  const LoadLane lr = load_lane<false>(lane);
+  FragLane<false> fr;
+  fr.init(lane);
+  const size_t at = static_cast<size_t>(block) * a.m * a.shard + c0;
+  const unsigned short *const wcol = a.w + (static_cast<size_t>(block) * a.shard + c0) * a.rank;
+  const size_t each = static_cast<size_t>(a.blocks) * a.shard * a.rank;
+  unsigned char *const places = lds + kStages * kStageAll + wave * kPlaces * kPlace;
+
+  // the places and keys of step k's rows (positions past the last row: that one's)
+  auto locate = [&](int k) __attribute__((always_inline)) {
+    const int want = (s0 + k) * 32 + (lane & 31), p = want < a.m ? want : a.m - 1;
+    unsigned char *const to = places + (k & (kPlaces - 1)) * kPlace;
+    async4((lane < 32 ? a.pos : a.keys) + p, to);
+    if constexpr (T::kHalf) async4(a.back + p, to + 256);
+  };
+  auto issue = [&](int k, int stage) __attribute__((always_inline)) {
+    locate(k + 2);
+    const int p0 = (s0 + k) * 32;
+    unsigned char *const st = lds + stage * kStageAll + wave * kWaveBytes;
+    const int *const place = reinterpret_cast<const int *>(places + (k & (kPlaces - 1)) * kPlace);
+    int row[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) row[q] = place[8 * q + lr.row];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = lr.chunk[q & 1] * 8;
+      const bool real = a.y && p0 + 8 * q + lr.row < a.m && c < left;
+      async16(real ? static_cast<const void *>(a.y + at + static_cast<size_t>(row[q]) * a.shard + c) : kZeros,
+              st + q * 1024);
+    }
+    unsigned char *const sl = lds + stage * kStageAll + 4 * kWaveBytes + wave * 2048;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      int p, e;  // position, and 16-bit element of its values
+      if constexpr (RB == 1) {  // 64 bytes a row, its four chunks swizzled by (row >> 2) & 3
+        p = p0 + t * 16 + (lane >> 2);
+        e = ((lane & 3) ^ (lane >> 4)) * 8;
+      } else {  // 128 bytes of upper halves, then of lower ones, as an operand's row
+        const int q = 2 * wave + t;
+        p = p0 + (q & 3) * 8 + lr.row;
+        e = (q >> 2) * kRankChunk + lr.chunk[t] * 8;
+      }
+      async16(p < a.m ? static_cast<const void *>(a.low + static_cast<size_t>(p) * (RB * 32) + e) : kZeros,
+              sl + t * 1024);
+    }
+  };
+  if (n > 0) {
+    locate(0);
+    locate(1);
+    wait_vm_lds<0>();
+    __asm__ __volatile__("" ::: "memory");
+    issue(0, 0);
+  }
+  if (n > 1) issue(1, 1);
+  int stage = 0, stored = 0, before = 0;  // stores of the last step and of the one before it
+  int have = -1;
+  s16x8 wf[4][KF];
+  for (int k = 0; k < n; ++k) {
+    // Loads and stores share one counter and are counted off in order: besides the
+    // next step's loads, the last two steps' stores may be under way.
+    if (k + 1 >= n)
+      wait_vm_lds<0>();
+    else if (stored + before == 8)
+      wait_vm_lds<kLoads + 8>();
+    else
+      wait_vm_lds<kLoads>();
+    if constexpr (RB > 1)
+      tile_barrier();
+    else
+      __asm__ __volatile__("" ::: "memory");
+    // (the loads that issue() starts overwrite this step's places)
+    const int p0 = (s0 + k) * 32;
+    int keys[2], rows[2];
+    float factors[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int *const place = reinterpret_cast<const int *>(places + (k & (kPlaces - 1)) * kPlace) + t * 16 + ml;
+      keys[t] = p0 + t * 16 + ml < a.m ? place[32] : -1;  // -1: no row
+      rows[t] = place[0];
+      factors[t] = T::kHalf ? __builtin_bit_cast(float, place[64]) : 1.f;
+    }
+    wait_lds();
+    if (k + 2 < n) issue(k + 2, stage >= 1 ? stage - 1 : kStages - 1);
+    before = stored;
+    stored = 0;
+    const unsigned char *const st = lds + stage * kStageAll + wave * kWaveBytes;
+    const unsigned char *const sl = lds + stage * kStageAll + 4 * kWaveBytes + (RB == 1 ? wave * 2048 : 0);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int key = keys[t];
       f32x4 res[4];
 #pragma unroll
       for (int v = 0; v < 4; ++v) res[v] = f32x4{0.f, 0.f, 0.f, 0.f};
-      unsigned todo = static_cast<unsigned>(__ballot(key[t] >= 0 && key[t] < a.adapters)) & 0xFFFF;
+      unsigned todo = static_cast<unsigned>(__ballot(key >= 0 && key < a.adapters)) & 0xFFFF;
       while (todo) {
-        const int cur = __builtin_amdgcn_readlane(key[t], __builtin_ctz(todo));
-        todo &= ~static_cast<unsigned>(__ballot(key[t] == cur));
+        const int cur = __builtin_amdgcn_readlane(key, __builtin_ctz(todo));
+        todo &= ~static_cast<unsigned>(__ballot(key == cur));
+        if (have != cur) {
+          const unsigned short *const wi = wcol + static_cast<size_t>(cur) * each;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int col = 32 * (v >> 1) + 8 * (ml >> 2) + 4 * (v & 1) + (ml & 3);
+#pragma unroll
+            for (int ks = 0; ks < KF; ++ks) {
+              const int r = RB == 1 ? 8 * (g & 1) : ks * 32 + 8 * g;
+              wf[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
+            }
+          }
+          have = cur;
+        }
         f32x4 acc[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int turn = 0; turn < turns; ++turn) {
-          const int rc = turn * kRankChunk;
-          if (have != cur || turns > 1) {
-            const unsigned short *const wi = wcol + static_cast<size_t>(cur) * each;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const int col = 32 * (v >> 1) + 8 * (ml >> 2) + 4 * (v & 1) + (ml & 3);
-#pragma unroll
-              for (int ks = 0; ks < KF; ++ks) {
-                const int r = KS == 0 ? 8 * (g & 1) : rc + ks * 32 + 8 * g;
-                wf[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
-              }
-            }
-            have = cur;
-          }
-          const unsigned short *const mine = low + (t * 16 + ml) * kRow + rc;
-#pragma unroll
-          for (int ks = 0; ks < KF; ++ks) {
-            if constexpr (KS == 0) {
-              const s16x8 both = load8(mine + 8 * g);
-#pragma unroll
-              for (int v = 0; v < 4; ++v) acc[v] = T::mma(wf[v][0], both, acc[v]);
-            } else {
-              const s16x8 hi = load8(mine + ks * 32 + 8 * g), lo = load8(mine + kRanks + ks * 32 + 8 * g);
-#pragma unroll
-              for (int v = 0; v < 4; ++v) acc[v] = T::mma(wf[v][ks], hi, acc[v]);
-#pragma unroll
-              for (int v = 0; v < 4; ++v) acc[v] = T::mma(wf[v][ks], lo, acc[v]);
-            }
-          }
-        }
-        const bool take = key[t] == cur;
+        add_low<T, RB == 1>(acc, wf, [&](int half, int ks) __attribute__((always_inline)) {
+          if constexpr (RB == 1)
+            return *reinterpret_cast<const s16x8 *>(sl + (t * 16 + ml) * 64 + ((g ^ (ml >> 2)) << 4));
+          else
+            return fr.read(sl + half * 4096, t, ks);
+        });
+        const bool take = key == cur;
 #pragma unroll
         for (int v = 0; v < 4; ++v)
 #pragma unroll
           for (int e = 0; e < 4; ++e) res[v][e] = take ? acc[v][e] : res[v][e];
       }
-      const bool has = key[t] < a.adapters;
-      if (key[t] < 0 || (in_place && !has)) continue;
-      const float inv = back[t * 16 + ml];
+      const bool mine = key >= 0 && key < a.adapters;
+      const bool writes = mine || (key >= 0 && a.y != a.out);
+      if (__ballot(writes) == 0) continue;
+      unsigned short *const to = a.out + at + static_cast<size_t>(rows[t]) * a.shard;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (h * 32 + 8 * g >= left) continue;
-        u32x4 o = __builtin_bit_cast(u32x4, yv[t][h]);
-        if (has) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f0 = __builtin_fmaf(res[2 * h + (e >> 1)][(2 * e) & 3], inv,
-                                            from16<T>(static_cast<unsigned short>(yv[t][h][2 * e])));
-            const float f1 = __builtin_fmaf(res[2 * h + (e >> 1)][(2 * e + 1) & 3], inv,
-                                            from16<T>(static_cast<unsigned short>(yv[t][h][2 * e + 1])));
-            o[e] = bits16<T>(f0) | bits16<T>(f1) << 16;
-          }
-        }
-        *reinterpret_cast<u32x4 *>(a.out + at + row[t] + h * 32 + 8 * g) = o;
+        if (h * 32 >= left) continue;
+        const s16x8 yv = fr.read(st, t, h);
+        const u32x4 o = mine ? sum8<T>(yv, &res[2 * h], factors[t]) : __builtin_bit_cast(u32x4, yv);
+        if (writes && h * 32 + 8 * g < left) *reinterpret_cast<u32x4 *>(to + h * 32 + 8 * g) = o;
+        ++stored;
       }
     }
+    stage = stage + 1 < kStages ? stage + 1 : 0;
   }
 }
 
@@ -830,10 +1033,10 @@ int adapt_splits(int m, int blocks, int shard, int rank, bool few) {
     const int steps = ceil_div(shard, 512), want = 256 / m;
     return want < 1 ? 1 : want < steps ? want : steps;
   }
-  // k_adapt_low: about 1024 workgroups, at least four steps each
+  // k_adapt_low: about 512 workgroups (two per CU), at least four steps each
   const long long groups = ceil_div(m, kLowRows) * static_cast<long long>(ceil_div(rank, kRankChunk));
   const int chunks = blocks * ceil_div(shard, 64);
-  long long s = 1024 / groups;
+  long long s = 512 / groups;
   if (s > chunks / 4) s = chunks / 4;
   if (s > 64) s = 64;
   return s < 1 ? 1 : static_cast<int>(s);
@@ -879,26 +1082,33 @@ hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocke
 hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *part, int splits,
                            const float *scale, const void *w, const Blocked &y, void *out,
                            hipStream_t s) {
-  const int per = ceil_div(y.shard, 64);
-  UpArgs a{r, part, scale, static_cast<const unsigned short *>(w), static_cast<const unsigned short *>(y.p),
-           static_cast<unsigned short *>(out), p.m, p.adapters, p.rank, splits, y.blocks, y.shard, per,
-           per * y.blocks, 0, 0};
+  const int per = ceil_div(y.shard, 64), chunks = per * y.blocks;
+  const auto *wp = static_cast<const unsigned short *>(w), *yp = static_cast<const unsigned short *>(y.p);
+  auto *op = static_cast<unsigned short *>(out);
   by_type(p.half, [&](auto type) {
     using T = decltype(type);
-    auto go = [&](auto ks, auto tt, auto col) {
-      constexpr int KS = decltype(ks)::value, TT = decltype(tt)::value, COL = decltype(col)::value;
-      a.groups = ceil_div(p.m, TT * 16);
-      a.strips = ceil_div(a.chunks, 4 * COL);
-      hipLaunchKernelGGL((k_adapt_up<T, KS, TT, COL>), dim3(static_cast<unsigned>(ceil_div(a.strips, 8)) * 8 * a.groups),
-                         dim3(kThreads), 0, s, a);
-    };
-    auto sized = [&](auto ks) {
-      if (adapt_big(p.m, p.rank))
-        go(ks, Int<4>{}, Int<4>{});
-      else
-        go(ks, Int<1>{}, Int<1>{});
-    };
-    p.rank <= 16 ? sized(Int<0>{}) : sized(Int<2>{});
+    if (adapt_streams(p.m, p.adapters, p.rank)) {
+      auto go = [&](auto rb) {
+        constexpr int RB = decltype(rb)::value;
+        hipLaunchKernelGGL((k_adapt_values<T, RB * 16>), dim3(ceil_div(p.m, kThreads / (RB * 2))), dim3(kThreads), 0, s,
+                           part, scale, r.keys, p.m, p.adapters, p.rank, splits, p.low, p.back);
+        const StreamArgs a{r.keys, r.pos, p.low, wp, yp, p.back, op, p.m, p.adapters, p.rank, y.blocks, y.shard, per,
+                           chunks};
+        // about 2048 workgroups, four rounds of two per CU, of eight steps at least
+        const int strips = ceil_div(chunks, 4), most = ceil_div(p.m, 256), want = ceil_div(2048, strips);
+        hipLaunchKernelGGL((k_adapt_stream<T, RB>), dim3(strips, want < most ? want : most), dim3(kThreads), 0, s, a);
+      };
+      p.rank <= 16 ? go(Int<1>{}) : go(Int<4>{});
+    } else {
+      const int groups = ceil_div(p.m, 16), strips = ceil_div(chunks, 4);
+      const UpArgs a{r, part, scale, wp, yp, op, p.m, p.adapters, p.rank, splits, y.blocks, y.shard, per, chunks,
+                     groups, strips};
+      auto go = [&](auto ks) {
+        hipLaunchKernelGGL((k_adapt_up<T, decltype(ks)::value>),
+                           dim3(static_cast<unsigned>(ceil_div(strips, 8)) * 8 * groups), dim3(kThreads), 0, s, a);
+      };
+      p.rank <= 16 ? go(Int<0>{}) : go(Int<2>{});
+    }
   });
   return hipGetLastError();
 }

@@ -40,8 +40,8 @@ bool shape_ok(const hg_adapt_shape *s, int kind) {
   // them); adapters x 64 columns x rank chunks
   const long long strips = s->tp * ceil_div(s->shard, 64), other = ceil_div(s->hidden, 64);
   const long long wide = strips > other ? strips : other;
-  const bool big = hg::adapt_big(s->m, s->rank);
-  if (ceil_div(s->m, big ? 64 : 16) * (ceil_div(wide, big ? 16 : 4) + 8) >= kMaxGroups) return false;
+  if (ceil_div(s->m, 16) * (ceil_div(wide, 4) + 8) >= kMaxGroups && !hg::adapt_streams(s->m, s->adapters, s->rank))
+    return false;
   return kind == HG_ADAPT_ADD || s->adapters * wide * ceil_div(s->rank, hg::kRankChunk) < kMaxGroups;
 }
 
@@ -70,10 +70,13 @@ size_t lay_out(const hg_adapt_shape &s, int kind, char *ws, AdaptPlan *p) {
   }
   p->split_u = hg::adapt_splits(s.m, 1, s.hidden, s.rank, !p->sorted);
   p->pu = floats(low * p->split_u);
-  if (kind == HG_ADAPT_ADD) {
-    if (p->sorted) p->u = floats(low);
-    return at;
+  if (hg::adapt_streams(s.m, s.adapters, s.rank)) {
+    p->low = reinterpret_cast<unsigned short *>(take(static_cast<size_t>(s.m) * (s.rank <= 16 ? 64 : 256)));
+    p->back = floats(s.m);
+  } else if (kind == HG_ADAPT_ADD && p->sorted) {
+    p->u = floats(low);
   }
+  if (kind == HG_ADAPT_ADD) return at;
   p->split_g = hg::adapt_splits(s.m, s.tp, s.shard, s.rank, false);
   p->pg = floats(low * p->split_g);
   p->u = floats(low);
@@ -163,9 +166,9 @@ HG_API int hg_adapt(const hg_adapt_shape *s, const void *y, const void *x, const
   }
   HIP_TRY(hg::launch_adapt_low(p, rows, Blocked{x, 1, s->hidden}, a, false, p.split_u, p.pu, st));
   // The second product's workgroups each read all of their rows' parts: of many
-  // rows they are added up first (2047 rows, 28 parts: 578 us without).
+  // rows they are added up first (2047 rows, 28 parts: 578 us against 365).
   const Blocked wide_y{y, s->tp, s->shard};
-  if (p.sorted) {
+  if (p.u) {
     HIP_TRY(hg::launch_adapt_join(p, rows, scale, st));
     HIP_TRY(hg::launch_adapt_up(p, rows, p.u, 1, nullptr, b, wide_y, out, st));
   } else {

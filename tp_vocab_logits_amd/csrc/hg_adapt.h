@@ -44,10 +44,10 @@ struct AdaptPlan {
   float *pa, *pb;        // [parts][adapters][..], where there are several
 };
 
-// pu or pg: the products of `of` with A (turned = false: w is [adapters][rank][columns])
-// or B (true: w is [adapters][columns][rank]), in `splits` parts.
-hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocked &of, const void *w,
-                            bool turned, int splits, float *part, hipStream_t s);
+// pu and pg: u's parts from x and A, g's from y and B ([adapters][rank][columns] and
+// [adapters][columns][rank]); a side without p is left out.
+hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocked &x, const void *a,
+                            const Blocked &y, const void *b, hipStream_t s);
 // out = y + (sum of the parts) W^T per row; y NULL: zeros.
 hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *part, int splits,
                            const float *scale, const void *w, const Blocked &y, void *out,
@@ -56,15 +56,12 @@ hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *
 hipError_t launch_adapt_segments(const AdaptPlan &p, const AdaptRows &r, hipStream_t s);
 // u and g from their parts, scaled; their largest.
 hipError_t launch_adapt_join(const AdaptPlan &p, const AdaptRows &r, const float *scale, hipStream_t s);
-// Their halves, by rank.
-hipError_t launch_adapt_halves(const AdaptPlan &p, hipStream_t s);
-// sum over an adapter's rows of low^T x of: [adapters][rank][columns], or
-// [adapters][columns][rank] if turned; in `parts` parts of the rows, added up if
-// there are several (part: room for them).
-hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Blocked &of,
-                              const unsigned short *low, const int *largest, bool turned, int parts,
-                              float *part, bool wide, void *out, hipStream_t s);
-hipError_t launch_adapt_turn(const AdaptPlan &p, const void *a, hipStream_t s);
+// Their halves by rank (ut, gt) and A turned (at), those that are there.
+hipError_t launch_adapt_prepare(const AdaptPlan &p, const void *a, hipStream_t s);
+// da and db, those that are there: the sums over an adapter's rows, in parts of the
+// rows that are added up if there are several.
+hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Blocked &x, void *da, const Blocked &y,
+                              void *db, bool wide, hipStream_t s);
 
 // Whether the second product goes through many rows with W's fragments kept
 // (k_adapt_stream): sorted rows, 64 of an adapter on average, ranks that fit.

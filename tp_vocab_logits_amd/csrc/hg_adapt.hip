@@ -151,34 +151,36 @@ constexpr int kStageAll = 4 * kWaveBytes + kSubBytes;  // four waves' and 8 KB t
 // and none waits for another. w's columns are next to each other in memory (A), or,
 // if TURNED, its ranks are (B): those are turned while they are read from LDS.
 
-struct LowArgs {
-  AdaptRows rows;
+struct LowSide {
   const unsigned short *of, *w;
-  int m, adapters, rank;
   int blocks, shard, per_block, chunks;  // chunks of 64 columns per block, in all
-  int splits;
+  int splits;                            // 0: not wanted
   float *part;
+};
+struct LowArgs {
+  const int *keys, *pos;
+  int m, adapters, rank;
+  LowSide x, y;  // u = A x, g = B^T dy
 };
 
 constexpr int kLowRows = 128;
 
 template <class T, bool TURNED, int RB>
-__global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
+__device__ __forceinline__ void low_products(const LowArgs &a, const LowSide &s, int id, unsigned char *lds) {
   static_assert(RB == 1 || RB == 4);
   constexpr int TT = 2;
-  __shared__ __align__(1024) unsigned char lds[kStages * kStageAll];
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int ml = lane & 15, g = lane >> 4;
   const int groups = (a.m + kLowRows - 1) / kLowRows;
-  const int split = static_cast<int>(blockIdx.x) / groups, group = static_cast<int>(blockIdx.x) - split * groups;
+  const int split = id / groups, group = id - split * groups;
   const int rc = static_cast<int>(blockIdx.y) * kRankChunk;
   const int ranks = a.rank - rc < RB * 16 ? a.rank - rc : RB * 16;  // a multiple of 8
-  const int from = static_cast<int>(static_cast<long long>(a.chunks) * split / a.splits);
-  const int to = static_cast<int>(static_cast<long long>(a.chunks) * (split + 1) / a.splits);
+  const int from = static_cast<int>(static_cast<long long>(s.chunks) * split / s.splits);
+  const int to = static_cast<int>(static_cast<long long>(s.chunks) * (split + 1) / s.splits);
   const int p0 = group * kLowRows;
   const int pend = a.m < p0 + kLowRows ? a.m : p0 + kLowRows;
-  const size_t columns = static_cast<size_t>(a.blocks) * a.shard;
+  const size_t columns = static_cast<size_t>(s.blocks) * s.shard;
   const LoadLane lr = load_lane<false>(lane), lc = load_lane<true>(lane);
   FragLane<false> fr;
   FragLane<true> fc;
@@ -189,18 +191,18 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     const int p = p0 + (wave * TT + t) * 16 + ml;
-    key[t] = p < a.m ? a.rows.keys[p] : a.adapters;
+    key[t] = p < a.m ? a.keys[p] : a.adapters;
   }
   int lkey[4];  // of the rows that it loads
   const unsigned short *src[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int p = p0 + wave * 32 + 8 * q + lr.row;
-    lkey[q] = p < a.m ? a.rows.keys[p] : a.adapters;
-    src[q] = a.of + static_cast<size_t>(p < a.m ? a.rows.pos[p] : 0) * a.shard + lr.chunk[q & 1] * 8;
+    lkey[q] = p < a.m ? a.keys[p] : a.adapters;
+    src[q] = s.of + static_cast<size_t>(p < a.m ? a.pos[p] : 0) * s.shard + lr.chunk[q & 1] * 8;
   }
   int at = p0;  // the first position of the adapter in turn
-  int cur = __builtin_amdgcn_readfirstlane(a.rows.keys[at]);
+  int cur = __builtin_amdgcn_readfirstlane(a.keys[at]);
   while (cur < a.adapters) {
     bool active[TT];
 #pragma unroll
@@ -210,14 +212,14 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
     for (int t = 0; t < TT; ++t)
 #pragma unroll
       for (int b = 0; b < RB; ++b) acc[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const unsigned short *const wi = a.w + static_cast<size_t>(cur) * a.rank * columns;
+    const unsigned short *const wi = s.w + static_cast<size_t>(cur) * a.rank * columns;
 
     // six loads per wave and step
     auto issue = [&](int chunk, int stage) __attribute__((always_inline)) {
-      const int block = chunk / a.per_block, c0 = (chunk - block * a.per_block) * 64;
-      const int left = a.shard - c0;  // columns of the block from here on
-      const size_t off = static_cast<size_t>(block) * a.m * a.shard + c0;
-      const size_t col = static_cast<size_t>(block) * a.shard + c0;
+      const int block = chunk / s.per_block, c0 = (chunk - block * s.per_block) * 64;
+      const int left = s.shard - c0;  // columns of the block from here on
+      const size_t off = static_cast<size_t>(block) * a.m * s.shard + c0;
+      const size_t col = static_cast<size_t>(block) * s.shard + c0;
       unsigned char *const st = lds + stage * kStageAll + wave * kWaveBytes;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -303,17 +305,29 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
         const int r = b * 16 + 4 * g;
         if (key[t] == cur && r < ranks)
           *reinterpret_cast<f32x4 *>(
-              a.part + (static_cast<size_t>(split) * a.m + p0 + (wave * TT + t) * 16 + ml) * a.rank + rc + r) =
+              s.part + (static_cast<size_t>(split) * a.m + p0 + (wave * TT + t) * 16 + ml) * a.rank + rc + r) =
               acc[t][b];
       }
     // the next adapter among the workgroup's rows (they are sorted)
     for (int same = 64; same == 64 && at < pend;) {
       const int p = at + lane;
-      same = __popcll(__ballot(p < pend && a.rows.keys[p < pend ? p : at] == cur));
+      same = __popcll(__ballot(p < pend && a.keys[p < pend ? p : at] == cur));
       at += same;
     }
-    cur = at < pend ? __builtin_amdgcn_readfirstlane(a.rows.keys[at]) : a.adapters;
+    cur = at < pend ? __builtin_amdgcn_readfirstlane(a.keys[at]) : a.adapters;
   }
+}
+
+// u's workgroups first (there are fewer), then g's.
+template <class T, int RB>
+__global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
+  __shared__ __align__(1024) unsigned char lds[kStages * kStageAll];
+  const int id = static_cast<int>(blockIdx.x);
+  const int first = (a.m + kLowRows - 1) / kLowRows * a.x.splits;
+  if (id < first)
+    low_products<T, false, RB>(a, a.x, id, lds);
+  else
+    low_products<T, true, RB>(a, a.y, id - first, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -440,14 +454,17 @@ struct UpArgs {
   int groups, strips;
 };
 
-// KS: steps of 32 ranks held at once: 0 for up to 16 ranks (upper and lower halves
-// share one step), 2 otherwise (more than 64 ranks: in turns).
-template <class T, int KS>
+// RANKS: 16 (upper and lower halves share one fragment), 64, or 256: in turns of 64.
+// A tile's adapters are taken several at a time, so that their fragments of W are on
+// their way together (64 rows of 32 adapters, V = 163840, rank 16: one at a time
+// 45 us, V_BATCHED four).
+template <class T, int RANKS>
 __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
-  constexpr int kRanks = KS == 0 ? 16 : HG_MAX_RANK;
-  constexpr int kRow = 2 * kRanks + 8;  // 16-bit elements of an LDS row: upper, lower halves
-  constexpr int kPieces = KS == 0 ? 1 : 2;
-  constexpr int KF = KS ? KS : 1;
+  constexpr bool kBoth = RANKS == 16;
+  constexpr int kRow = 2 * RANKS + 8;  // 16-bit elements of an LDS row: upper, lower halves
+  constexpr int kPieces = RANKS == 256 ? 2 : 1;
+  constexpr int KF = kBoth ? 1 : 2;
+  constexpr int kBatch = RANKS == 16 ? 4 : RANKS == 64 ? 2 : 1;
   __shared__ __align__(16) unsigned short low[16 * kRow];
   __shared__ float back[16];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
@@ -471,9 +488,9 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
 #pragma unroll
     for (int q = 0; q < kPieces; ++q) {
       const int e = (q * 16 + sub) * 8;
-      if (e < kRanks) {
+      if (e < RANKS) {
         *reinterpret_cast<u32x4 *>(low + r * kRow + e) = hi[q];
-        *reinterpret_cast<u32x4 *>(low + r * kRow + kRanks + e) = lo[q];
+        *reinterpret_cast<u32x4 *>(low + r * kRow + RANKS + e) = lo[q];
       }
     }
   }
@@ -482,7 +499,6 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
   const size_t row = static_cast<size_t>(p < a.m ? row_of(a.rows, p) : 0) * a.shard;
   __syncthreads();
 
-  const int turns = KS == 0 ? 1 : (a.rank + kRankChunk - 1) / kRankChunk;
   const int chunk = strip * 4 + wave;
   if (chunk >= a.chunks) return;
   const int block = chunk / a.per_block, c0 = (chunk - block * a.per_block) * 64;
@@ -498,35 +514,51 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
 #pragma unroll
   for (int v = 0; v < 4; ++v) res[v] = f32x4{0.f, 0.f, 0.f, 0.f};
   const unsigned short *const mine = low + ml * kRow;
+  auto fragments = [&](int i, int rc, s16x8 (&wf)[4][KF]) __attribute__((always_inline)) {
+    const unsigned short *const wi = wcol + static_cast<size_t>(i) * each;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int col = 32 * (v >> 1) + 8 * (ml >> 2) + 4 * (v & 1) + (ml & 3);
+#pragma unroll
+      for (int ks = 0; ks < KF; ++ks) {
+        const int r = kBoth ? 8 * (g & 1) : rc + ks * 32 + 8 * g;
+        wf[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
+      }
+    }
+  };
   unsigned todo = static_cast<unsigned>(__ballot(key >= 0 && key < a.adapters)) & 0xFFFF;
   while (todo) {
-    const int cur = __builtin_amdgcn_readlane(key, __builtin_ctz(todo));
-    todo &= ~static_cast<unsigned>(__ballot(key == cur));
-    const unsigned short *const wi = wcol + static_cast<size_t>(cur) * each;
-    f32x4 acc[4];
+    int cur[kBatch];
+    s16x8 wf[kBatch][4][KF];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int turn = 0; turn < turns; ++turn) {
-      const int rc = turn * kRankChunk;
-      s16x8 wf[4][KF];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int col = 32 * (v >> 1) + 8 * (ml >> 2) + 4 * (v & 1) + (ml & 3);
-#pragma unroll
-        for (int ks = 0; ks < KF; ++ks) {
-          const int r = KS == 0 ? 8 * (g & 1) : rc + ks * 32 + 8 * g;
-          wf[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
-        }
+    for (int n = 0; n < kBatch; ++n) {
+      cur[n] = -1;
+      if (todo) {
+        cur[n] = __builtin_amdgcn_readlane(key, __builtin_ctz(todo));
+        todo &= ~static_cast<unsigned>(__ballot(key == cur[n]));
+        fragments(cur[n], 0, wf[n]);
       }
-      add_low<T, KS == 0>(acc, wf, [&](int half, int ks) __attribute__((always_inline)) {
-        return load8(mine + (KS == 0 ? 8 * g : half * kRanks + rc + ks * 32 + 8 * g));
-      });
     }
-    const bool take = key == cur;
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
+    for (int n = 0; n < kBatch; ++n) {
+      if (cur[n] < 0) break;
+      f32x4 acc[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) res[v][e] = take ? acc[v][e] : res[v][e];
+      for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int rc = 0;;) {
+        add_low<T, kBoth>(acc, wf[n], [&](int half, int ks) __attribute__((always_inline)) {
+          return load8(mine + (kBoth ? 8 * g : half * RANKS + rc + ks * 32 + 8 * g));
+        });
+        rc += kRankChunk;
+        if (RANKS <= kRankChunk || rc >= a.rank) break;
+        fragments(cur[n], rc, wf[n]);
+      }
+      const bool take = key == cur[n];
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) res[v][e] = take ? acc[v][e] : res[v][e];
+    }
   }
   const bool has = key < a.adapters;
   if (key < 0 || (a.y == a.out && !has)) return;
@@ -726,13 +758,13 @@ __global__ __launch_bounds__(kThreads) void k_adapt_segments(const int *keys, in
   for (int i = before + 1; i <= here && i <= adapters; ++i) seg[i] = j;
 }
 
-// The parts' sums, scaled, and their largest (into head, if given): blockIdx.y 0: u,
-// 1: g.
+// The parts' sums, scaled, and (fp16) their largest: blockIdx.y 0: u, 1: g.
 struct JoinSide {
   const float *part;
   float *sum;
-  int splits;
+  int splits;  // 0: not wanted
 };
+template <class T>
 __global__ __launch_bounds__(kThreads) void k_adapt_join(JoinSide u, JoinSide g, const int *keys,
                                                          const float *scale, int m, int adapters,
                                                          int rank, int *head) {
@@ -764,30 +796,33 @@ __global__ __launch_bounds__(kThreads) void k_adapt_join(JoinSide u, JoinSide g,
       }
       *reinterpret_cast<f32x4 *>(side.sum + k) = sum;
     }
+  if constexpr (T::kHalf) {
+    // The largest of all does not depend on the order. Thousands of atomics on one
+    // address took 25 us (4096 rows of 64 ranks): a workgroup's largest, if it is more
+    // than what is there.
+    __shared__ float waves[4];
 #pragma unroll
-  for (int d = 32; d; d >>= 1) largest = fmaxf(largest, __shfl_xor(largest, d));
-  // (the largest of all does not depend on the order)
-  if (head && (threadIdx.x & 63) == 0 && largest > 0.f)
-    atomicMax(head + blockIdx.y, static_cast<int>(__builtin_bit_cast(uint32_t, largest)));
+    for (int d = 32; d; d >>= 1) largest = fmaxf(largest, __shfl_xor(largest, d));
+    if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = largest;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const int bits = static_cast<int>(__builtin_bit_cast(
+          uint32_t, fmaxf(fmaxf(waves[0], waves[1]), fmaxf(waves[2], waves[3]))));
+      if (bits > __hip_atomic_load(head + blockIdx.y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+        atomicMax(head + blockIdx.y, bits);
+    }
+  }
 }
 
-// low [m][rank] -> [2][rank][padded], upper and lower halves, zeros past m.
-// blockIdx.y 0: u, 1: g. A workgroup turns 64 rows of 32 ranks.
-struct HalvesSide {
-  const float *low;
-  unsigned short *out;
-};
+// low [m][rank] -> [2][rank][padded], upper and lower halves, zeros past m: 64 rows
+// of 32 ranks.
 template <class T>
-__global__ __launch_bounds__(kThreads) void k_adapt_halves(HalvesSide u, HalvesSide g, const int *head,
-                                                           int m, int rank, int padded) {
-  const HalvesSide side = blockIdx.y ? g : u;
-  if (!side.out) return;
-  __shared__ float t[64][33];
-  const float unit = to_unit<T>(__builtin_bit_cast(float, head[blockIdx.y]));
-  const int p0 = static_cast<int>(blockIdx.x) * 64, r0 = static_cast<int>(blockIdx.z) * 32;
+__device__ __forceinline__ void turn_halves(const float *low, unsigned short *out, const int *largest, int m,
+                                            int rank, int padded, int p0, int r0, float (&t)[64][33]) {
+  const float unit = to_unit<T>(__builtin_bit_cast(float, *largest));
   for (int k = static_cast<int>(threadIdx.x); k < 64 * 32; k += kThreads) {
     const int p = p0 + k / 32, r = r0 + k % 32;
-    t[k / 32][k % 32] = p < m && r < rank ? side.low[static_cast<size_t>(p) * rank + r] * unit : 0.f;
+    t[k / 32][k % 32] = p < m && r < rank ? low[static_cast<size_t>(p) * rank + r] * unit : 0.f;
   }
   __syncthreads();
   for (int k = static_cast<int>(threadIdx.x); k < 64 * 32; k += kThreads) {
@@ -795,27 +830,59 @@ __global__ __launch_bounds__(kThreads) void k_adapt_halves(HalvesSide u, HalvesS
     if (p >= padded || r >= rank) continue;
     uint32_t hi, lo;
     halves<T>(t[k % 64][k / 64], hi, lo);
-    side.out[static_cast<size_t>(r) * padded + p] = static_cast<unsigned short>(hi);
-    side.out[static_cast<size_t>(rank + r) * padded + p] = static_cast<unsigned short>(lo);
+    out[static_cast<size_t>(r) * padded + p] = static_cast<unsigned short>(hi);
+    out[static_cast<size_t>(rank + r) * padded + p] = static_cast<unsigned short>(lo);
   }
 }
 
-// A [rank][hidden] -> [hidden][rank] of each adapter that has rows, 64 x 64.
-__global__ __launch_bounds__(kThreads) void k_adapt_turn(const unsigned short *a, unsigned short *at,
-                                                         int rank, int hidden, const int *seg) {
-  const int i = static_cast<int>(blockIdx.z);
-  if (seg[i] == seg[i + 1]) return;
-  __shared__ unsigned short t[64][66];
-  const size_t base = static_cast<size_t>(i) * rank * hidden;
-  const int h0 = static_cast<int>(blockIdx.x) * 64, r0 = static_cast<int>(blockIdx.y) * 64;
-  for (int k = static_cast<int>(threadIdx.x); k < 64 * 64; k += kThreads) {
-    const int r = r0 + k / 64, h = h0 + k % 64;
-    if (r < rank && h < hidden) t[k / 64][k % 64] = a[base + static_cast<size_t>(r) * hidden + h];
+// A [rank][hidden] -> [hidden][rank]: 64 x 64, 16 bytes at a time.
+__device__ __forceinline__ void turn_block(const unsigned short *a, unsigned short *at, int rank, int hidden, int h0,
+                                           int r0, unsigned short (&t)[64][72]) {
+  for (int k = static_cast<int>(threadIdx.x); k < 64 * 8; k += kThreads) {
+    const int r = r0 + k / 8, h = h0 + k % 8 * 8;
+    if (r < rank && h < hidden)
+      *reinterpret_cast<s16x8 *>(&t[k / 8][k % 8 * 8]) = load8(a + static_cast<size_t>(r) * hidden + h);
   }
   __syncthreads();
-  for (int k = static_cast<int>(threadIdx.x); k < 64 * 64; k += kThreads) {
-    const int h = h0 + k / 64, r = r0 + k % 64;
-    if (r < rank && h < hidden) at[base + static_cast<size_t>(h) * rank + r] = t[k % 64][k / 64];
+  for (int k = static_cast<int>(threadIdx.x); k < 64 * 8; k += kThreads) {
+    const int h = h0 + k / 8, r = r0 + k % 8 * 8;
+    if (r >= rank || h >= hidden) continue;
+    s16x8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = static_cast<short>(t[k % 8 * 8 + e][k / 8]);
+    *reinterpret_cast<s16x8 *>(at + static_cast<size_t>(h) * rank + r) = v;
+  }
+}
+
+// What the gradients' wide products take, in one launch: the halves of u and g by
+// rank, and A turned, for the adapters that have rows.
+struct PrepareArgs {
+  const float *u, *g;
+  unsigned short *ut, *gt, *at;
+  const unsigned short *a;
+  const int *head, *seg;
+  int m, rank, hidden, padded, adapters;
+  int tiles, across, blocks;  // workgroups of one side's halves, of which per rank chunk; of an adapter's A
+  int first, second;          // workgroups before g's halves, before A's
+};
+template <class T>
+__global__ __launch_bounds__(kThreads) void k_adapt_prepare(PrepareArgs a) {
+  __shared__ union {
+    float f[64][33];
+    __align__(16) unsigned short h[64][72];
+  } t;
+  int id = static_cast<int>(blockIdx.x);
+  if (id < a.second) {
+    const bool g = id >= a.first;
+    if (g) id -= a.first;
+    turn_halves<T>(g ? a.g : a.u, g ? a.gt : a.ut, a.head + g, a.m, a.rank, a.padded, id % a.across * 64,
+                   id / a.across * 32, t.f);
+  } else {
+    id -= a.second;
+    const int i = id / a.blocks, block = id - i * a.blocks, wide = (a.hidden + 63) / 64;
+    if (a.seg[i] == a.seg[i + 1]) return;
+    const size_t base = static_cast<size_t>(i) * a.rank * a.hidden;
+    turn_block(a.a + base, a.at + base, a.rank, a.hidden, block % wide * 64, block / wide * 64, t.h);
   }
 }
 
@@ -828,40 +895,44 @@ __global__ __launch_bounds__(kThreads) void k_adapt_turn(const unsigned short *a
 // ranks each loads its own), of is turned while it is read from LDS. The rows'
 // places are loaded two steps before the rows.
 
-struct OuterArgs {
-  const int *pos, *seg, *largest;
+struct OuterSide {
+  const int *largest;
   const unsigned short *of, *low;
   void *out;
-  int m, adapters, rank, padded, blocks, shard, per_block, chunks;  // chunks of 64 columns
+  int blocks, shard, per_block, chunks;  // chunks of 64 columns
+  int strips, parts;                     // 256 columns; parts of the rows (0: not wanted)
+  int wide;                              // out is fp32, [parts][adapters]...
+};
+struct OuterArgs {
+  const int *pos, *seg;
+  int m, adapters, rank, padded;
+  OuterSide y, x;  // dB, dA
 };
 
-// WIDE: out is fp32, [parts][adapters]...: the parts (gridDim.y / adapters) are
-// added up by another launch if there are several.
-template <class T, bool TURNED, int RB, bool WIDE>
-__global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
+template <class T, bool TURNED, int RB>
+__device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSide &s, int id, unsigned char *lds) {
   static_assert(RB == 1 || RB == 4);
   constexpr int kPlaces = 4;  // steps' places at once, 256 bytes each, per wave
-  __shared__ __align__(1024) unsigned char lds[kStages * kStageAll + 4 * kPlaces * 256];
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int ml = lane & 15, g = lane >> 4;
-  const int part = static_cast<int>(blockIdx.y) / a.adapters, i = static_cast<int>(blockIdx.y) - part * a.adapters;
-  const int parts = static_cast<int>(gridDim.y) / a.adapters;
-  const int rc = static_cast<int>(blockIdx.z) * kRankChunk;
+  const int pair = id / s.strips;  // part and adapter
+  const int part = pair / a.adapters, i = pair - part * a.adapters;
+  const int rc = static_cast<int>(blockIdx.y) * kRankChunk;
   const int ranks = a.rank - rc < RB * 16 ? a.rank - rc : RB * 16;
-  const int chunk = static_cast<int>(blockIdx.x) * 4 + wave;
-  const bool has = chunk < a.chunks;
-  const int block = has ? chunk / a.per_block : 0, c0 = has ? (chunk - block * a.per_block) * 64 : 0;
-  const int left = has ? a.shard - c0 : 0;
+  const int chunk = (id - pair * s.strips) * 4 + wave;
+  const bool has = chunk < s.chunks;
+  const int block = has ? chunk / s.per_block : 0, c0 = has ? (chunk - block * s.per_block) * 64 : 0;
+  const int left = has ? s.shard - c0 : 0;
   const int from = a.seg[i], to = a.seg[i + 1];
   const int first = from & ~7;  // (low is read eight rows at a time)
   const int steps = (to - first + 31) / 32;
-  const int s0 = static_cast<int>(static_cast<long long>(steps) * part / parts);
-  const int n = static_cast<int>(static_cast<long long>(steps) * (part + 1) / parts) - s0;
+  const int s0 = static_cast<int>(static_cast<long long>(steps) * part / s.parts);
+  const int n = static_cast<int>(static_cast<long long>(steps) * (part + 1) / s.parts) - s0;
   const LoadLane lc = load_lane<true>(lane);
   FragLane<true> fc;
   fc.init(lane);
-  const unsigned short *const of = a.of + static_cast<size_t>(block) * a.m * a.shard + c0;
+  const unsigned short *const of = s.of + static_cast<size_t>(block) * a.m * s.shard + c0;
   unsigned char *const places = lds + kStages * kStageAll + wave * kPlaces * 256;
   f32x4 acc[RB][4];
 #pragma unroll
@@ -887,7 +958,7 @@ __global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
     for (int q = 0; q < 4; ++q) {
       const int p = p0 + 8 * q + lc.row, c = lc.chunk[q & 1] * 8;
       const bool real = p >= from && p < to && c < left;
-      async16(real ? static_cast<const void *>(of + static_cast<size_t>(row[q]) * a.shard + c) : kZeros,
+      async16(real ? static_cast<const void *>(of + static_cast<size_t>(row[q]) * s.shard + c) : kZeros,
               st + q * 1024);
     }
     // pieces of 16 ranks' 32 rows, a rank's four chunks swizzled by (rank >> 2) & 3
@@ -898,7 +969,7 @@ __global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
       const int h = line / (RB * 16), r = line - h * (RB * 16);
       const int p = p0 + ((lane & 3) ^ (line >> 2 & 3)) * 8;
       const bool real = r < ranks && p < to;
-      async16(real ? static_cast<const void *>(a.low + static_cast<size_t>(h * a.rank + rc + r) * a.padded + p) : kZeros,
+      async16(real ? static_cast<const void *>(s.low + static_cast<size_t>(h * a.rank + rc + r) * a.padded + p) : kZeros,
               sl + t * 1024);
     }
   };
@@ -956,10 +1027,9 @@ __global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
     multiply(k, stage);
     stage = stage + 1 < kStages ? stage + 1 : 0;
   }
-  const float inv = from_unit<T>(__builtin_bit_cast(float, *a.largest));
-  const size_t columns = static_cast<size_t>(a.blocks) * a.shard;
-  const size_t col0 = static_cast<size_t>(block) * a.shard + c0;
-  const size_t pair = static_cast<size_t>(blockIdx.y);  // part and adapter
+  const float inv = from_unit<T>(__builtin_bit_cast(float, *s.largest));
+  const size_t columns = static_cast<size_t>(s.blocks) * s.shard;
+  const size_t col0 = static_cast<size_t>(block) * s.shard + c0;
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
@@ -968,19 +1038,30 @@ __global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
       size_t at;
       if constexpr (TURNED) {  // column v*16 + ml, ranks b*16 + 4g ..
         if (v * 16 + ml >= left || b * 16 + 4 * g >= ranks) continue;
-        at = (pair * columns + col0 + v * 16 + ml) * a.rank + rc + b * 16 + 4 * g;
+        at = (static_cast<size_t>(pair) * columns + col0 + v * 16 + ml) * a.rank + rc + b * 16 + 4 * g;
       } else {  // rank b*16 + ml, columns v*16 + 4g ..
         if (b * 16 + ml >= ranks || v * 16 + 4 * g >= left) continue;
-        at = (pair * a.rank + rc + b * 16 + ml) * columns + col0 + v * 16 + 4 * g;
+        at = (static_cast<size_t>(pair) * a.rank + rc + b * 16 + ml) * columns + col0 + v * 16 + 4 * g;
       }
-      if constexpr (WIDE) {
-        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = sum;
+      if (s.wide) {
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(s.out) + at) = sum;
       } else {
         typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-        *reinterpret_cast<u32x2 *>(static_cast<unsigned short *>(a.out) + at) =
+        *reinterpret_cast<u32x2 *>(static_cast<unsigned short *>(s.out) + at) =
             u32x2{bits16<T>(sum[0]) | bits16<T>(sum[1]) << 16, bits16<T>(sum[2]) | bits16<T>(sum[3]) << 16};
       }
     }
+}
+
+// dB's workgroups first, then dA's.
+template <class T, int RB>
+__global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
+  __shared__ __align__(1024) unsigned char lds[kStages * kStageAll + 4 * 4 * 256];
+  const int id = static_cast<int>(blockIdx.x), first = a.y.strips * a.y.parts * a.adapters;
+  if (id < first)
+    outer_products<T, true, RB>(a, a.y, id, lds);
+  else
+    outer_products<T, false, RB>(a, a.x, id - first, lds);
 }
 
 // out = the sum of the parts, [n] each, n a multiple of 8.
@@ -1052,29 +1133,30 @@ int adapt_parts(int m, int adapters, int blocks, int shard, int rank) {
   return s < 1 ? 1 : static_cast<int>(s);
 }
 
-hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocked &of, const void *w,
-                            bool turned, int splits, float *part, hipStream_t s) {
-  const auto *x = static_cast<const unsigned short *>(of.p), *wp = static_cast<const unsigned short *>(w);
+hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocked &x, const void *a,
+                            const Blocked &y, const void *b, hipStream_t s) {
+  const auto *xp = static_cast<const unsigned short *>(x.p), *ap = static_cast<const unsigned short *>(a);
   if (!p.sorted) {
     by_type(p.half, [&](auto type) {
-      hipLaunchKernelGGL((k_adapt_row<decltype(type)>), dim3(p.m * splits), dim3(kThreads), 0, s, r, x, wp,
-                         p.adapters, p.m, p.rank, of.shard, splits, part);
+      hipLaunchKernelGGL((k_adapt_row<decltype(type)>), dim3(p.m * p.split_u), dim3(kThreads), 0, s, r, xp, ap,
+                         p.adapters, p.m, p.rank, x.shard, p.split_u, p.pu);
     });
     return hipGetLastError();
   }
-  const int per = ceil_div(of.shard, 64);
-  const LowArgs a{r, x, wp, p.m, p.adapters, p.rank, of.blocks, of.shard, per, per * of.blocks, splits, part};
+  auto side = [&](const Blocked &of, const void *w, int splits, float *part) {
+    const int per = ceil_div(of.shard, 64);
+    return LowSide{static_cast<const unsigned short *>(of.p), static_cast<const unsigned short *>(w), of.blocks,
+                   of.shard, per, per * of.blocks, of.p ? splits : 0, part};
+  };
+  const LowArgs args{r.keys, r.pos, p.m, p.adapters, p.rank, side(x, a, p.split_u, p.pu), side(y, b, p.split_g, p.pg)};
+  const dim3 grid(static_cast<unsigned>(ceil_div(p.m, kLowRows)) * (args.x.splits + args.y.splits),
+                  ceil_div(p.rank, kRankChunk));
   by_type(p.half, [&](auto type) {
     using T = decltype(type);
-    auto go = [&](auto turn, auto rb) {
-      const dim3 grid(static_cast<unsigned>(ceil_div(p.m, kLowRows)) * splits, ceil_div(p.rank, kRankChunk));
-      hipLaunchKernelGGL((k_adapt_low<T, decltype(turn)::value != 0, decltype(rb)::value>), grid, dim3(kThreads), 0, s,
-                         a);
-    };
-    if (turned)
-      p.rank <= 16 ? go(Int<1>{}, Int<1>{}) : go(Int<1>{}, Int<4>{});
+    if (p.rank <= 16)
+      hipLaunchKernelGGL((k_adapt_low<T, 1>), grid, dim3(kThreads), 0, s, args);
     else
-      p.rank <= 16 ? go(Int<0>{}, Int<1>{}) : go(Int<0>{}, Int<4>{});
+      hipLaunchKernelGGL((k_adapt_low<T, 4>), grid, dim3(kThreads), 0, s, args);
   });
   return hipGetLastError();
 }
@@ -1094,8 +1176,8 @@ hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *
                            part, scale, r.keys, p.m, p.adapters, p.rank, splits, p.low, p.back);
         const StreamArgs a{r.keys, r.pos, p.low, wp, yp, p.back, op, p.m, p.adapters, p.rank, y.blocks, y.shard, per,
                            chunks};
-        // about 2048 workgroups, four rounds of two per CU, of eight steps at least
-        const int strips = ceil_div(chunks, 4), most = ceil_div(p.m, 256), want = ceil_div(2048, strips);
+        // about 2048 workgroups, four rounds of two per CU, of two steps at least
+        const int strips = ceil_div(chunks, 4), most = ceil_div(p.m, 64), want = ceil_div(2048, strips);
         hipLaunchKernelGGL((k_adapt_stream<T, RB>), dim3(strips, want < most ? want : most), dim3(kThreads), 0, s, a);
       };
       p.rank <= 16 ? go(Int<1>{}) : go(Int<4>{});
@@ -1103,11 +1185,11 @@ hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *
       const int groups = ceil_div(p.m, 16), strips = ceil_div(chunks, 4);
       const UpArgs a{r, part, scale, wp, yp, op, p.m, p.adapters, p.rank, splits, y.blocks, y.shard, per, chunks,
                      groups, strips};
-      auto go = [&](auto ks) {
-        hipLaunchKernelGGL((k_adapt_up<T, decltype(ks)::value>),
+      auto go = [&](auto ranks) {
+        hipLaunchKernelGGL((k_adapt_up<T, decltype(ranks)::value>),
                            dim3(static_cast<unsigned>(ceil_div(strips, 8)) * 8 * groups), dim3(kThreads), 0, s, a);
       };
-      p.rank <= 16 ? go(Int<0>{}) : go(Int<2>{});
+      p.rank <= 16 ? go(Int<16>{}) : p.rank <= kRankChunk ? go(Int<kRankChunk>{}) : go(Int<HG_MAX_RANK>{});
     }
   });
   return hipGetLastError();
@@ -1121,58 +1203,61 @@ hipError_t launch_adapt_segments(const AdaptPlan &p, const AdaptRows &r, hipStre
 
 hipError_t launch_adapt_join(const AdaptPlan &p, const AdaptRows &r, const float *scale, hipStream_t s) {
   const int want = ceil_div(static_cast<long long>(p.m) * p.rank, 4 * kThreads);
-  hipLaunchKernelGGL(k_adapt_join, dim3(want < 1024 ? want : 1024, p.g ? 2 : 1), dim3(kThreads), 0, s,
-                     JoinSide{p.pu, p.u, p.u ? p.split_u : 0}, JoinSide{p.pg, p.g, p.g ? p.split_g : 0}, r.keys,
-                     scale, p.m, p.adapters, p.rank, p.head);
-  return hipGetLastError();
-}
-
-hipError_t launch_adapt_halves(const AdaptPlan &p, hipStream_t s) {
-  by_type(p.half, [&](auto type) {
-    hipLaunchKernelGGL((k_adapt_halves<decltype(type)>), dim3(ceil_div(p.padded, 64), 2, ceil_div(p.rank, 32)),
-                       dim3(kThreads), 0, s, HalvesSide{p.u, p.ut}, HalvesSide{p.g, p.gt}, p.head, p.m, p.rank,
-                       p.padded);
+  const dim3 grid(want < 1024 ? want : 1024, p.g ? 2 : 1);
+  const JoinSide u{p.pu, p.u, p.u ? p.split_u : 0}, g{p.pg, p.g, p.g ? p.split_g : 0};
+  by_type(p.half && p.head, [&](auto type) {
+    hipLaunchKernelGGL((k_adapt_join<decltype(type)>), grid, dim3(kThreads), 0, s, u, g, r.keys, scale, p.m, p.adapters,
+                       p.rank, p.head);
   });
   return hipGetLastError();
 }
 
-hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Blocked &of,
-                              const unsigned short *low, const int *largest, bool turned, int parts,
-                              float *part, bool wide, void *out, hipStream_t s) {
-  const int per = ceil_div(of.shard, 64), chunks = per * of.blocks;
-  const bool whole = parts == 1;
-  const OuterArgs a{r.pos, p.seg, largest, static_cast<const unsigned short *>(of.p), low, whole ? out : part, p.m,
-                    p.adapters, p.rank, p.padded, of.blocks, of.shard, per, chunks};
-  const dim3 grid(ceil_div(chunks, 4), p.adapters * parts, ceil_div(p.rank, kRankChunk));
+hipError_t launch_adapt_prepare(const AdaptPlan &p, const void *a, hipStream_t s) {
+  PrepareArgs args{p.u, p.g, p.ut, p.gt, p.at, static_cast<const unsigned short *>(a), p.head, p.seg, p.m, p.rank,
+                   p.hidden, p.padded, p.adapters, 0, 0, 0, 0, 0};
+  args.across = ceil_div(p.padded, 64);
+  args.tiles = args.across * ceil_div(p.rank, 32);
+  args.blocks = ceil_div(p.hidden, 64) * ceil_div(p.rank, 64);
+  args.first = p.ut ? args.tiles : 0;
+  args.second = args.first + (p.gt ? args.tiles : 0);
+  const int all = args.second + (p.at ? args.blocks * p.adapters : 0);
+  if (all == 0) return hipSuccess;
+  by_type(p.half, [&](auto type) {
+    hipLaunchKernelGGL((k_adapt_prepare<decltype(type)>), dim3(all), dim3(kThreads), 0, s, args);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Blocked &x, void *da, const Blocked &y,
+                              void *db, bool wide, hipStream_t s) {
+  auto side = [&](const Blocked &of, const int *largest, const unsigned short *low, int parts, float *part, void *out) {
+    const int per = ceil_div(of.shard, 64), chunks = per * of.blocks;
+    return OuterSide{largest, static_cast<const unsigned short *>(of.p), low, parts > 1 ? part : out, of.blocks,
+                     of.shard, per, chunks, ceil_div(chunks, 4), out ? parts : 0, wide || parts > 1};
+  };
+  const OuterArgs a{r.pos, p.seg, p.m, p.adapters, p.rank, p.padded, side(y, p.head, p.ut, p.parts_b, p.pb, db),
+                    side(x, p.head + 1, p.gt, p.parts_a, p.pa, da)};
+  const dim3 grid(static_cast<unsigned>(a.y.strips * a.y.parts + a.x.strips * a.x.parts) * p.adapters,
+                  ceil_div(p.rank, kRankChunk));
   by_type(p.half, [&](auto type) {
     using T = decltype(type);
-    auto go = [&](auto turn, auto rb, auto fp32) {
-      hipLaunchKernelGGL((k_adapt_outer<T, decltype(turn)::value != 0, decltype(rb)::value, decltype(fp32)::value != 0>),
-                         grid, dim3(kThreads), 0, s, a);
-    };
-    auto ranks = [&](auto turn, auto fp32) {
-      p.rank <= 16 ? go(turn, Int<1>{}, fp32) : go(turn, Int<4>{}, fp32);
-    };
-    const bool fp32 = wide || !whole;
-    if (turned)
-      fp32 ? ranks(Int<1>{}, Int<1>{}) : ranks(Int<1>{}, Int<0>{});
+    if (p.rank <= 16)
+      hipLaunchKernelGGL((k_adapt_outer<T, 1>), grid, dim3(kThreads), 0, s, a);
     else
-      fp32 ? ranks(Int<0>{}, Int<1>{}) : ranks(Int<0>{}, Int<0>{});
-    if (whole) return;
-    const size_t n = static_cast<size_t>(p.adapters) * p.rank * of.blocks * of.shard;
-    const int want = ceil_div(static_cast<long long>(n), 8 * kThreads);
-    const dim3 sums(want < 2048 ? want : 2048);
-    if (wide)
-      hipLaunchKernelGGL((k_adapt_parts<T, true>), sums, dim3(kThreads), 0, s, part, parts, n, out);
-    else
-      hipLaunchKernelGGL((k_adapt_parts<T, false>), sums, dim3(kThreads), 0, s, part, parts, n, out);
+      hipLaunchKernelGGL((k_adapt_outer<T, 4>), grid, dim3(kThreads), 0, s, a);
+    auto sum = [&](const Blocked &of, int parts, const float *part, void *out) {
+      if (!out || parts == 1) return;
+      const size_t n = static_cast<size_t>(p.adapters) * p.rank * of.blocks * of.shard;
+      const int want = ceil_div(static_cast<long long>(n), 8 * kThreads);
+      const dim3 sums(want < 2048 ? want : 2048);
+      if (wide)
+        hipLaunchKernelGGL((k_adapt_parts<T, true>), sums, dim3(kThreads), 0, s, part, parts, n, out);
+      else
+        hipLaunchKernelGGL((k_adapt_parts<T, false>), sums, dim3(kThreads), 0, s, part, parts, n, out);
+    };
+    sum(y, p.parts_b, p.pb, db);
+    sum(x, p.parts_a, p.pa, da);
   });
-  return hipGetLastError();
-}
-
-hipError_t launch_adapt_turn(const AdaptPlan &p, const void *a, hipStream_t s) {
-  hipLaunchKernelGGL(k_adapt_turn, dim3(ceil_div(p.hidden, 64), ceil_div(p.rank, 64), p.adapters), dim3(kThreads),
-                     0, s, static_cast<const unsigned short *>(a), p.at, p.rank, p.hidden, p.seg);
   return hipGetLastError();
 }
 

@@ -164,7 +164,7 @@ HG_API int hg_adapt(const hg_adapt_shape *s, const void *y, const void *x, const
     const int rc = sort_rows(p, &rows, st);
     if (rc != HG_OK) return rc;
   }
-  HIP_TRY(hg::launch_adapt_low(p, rows, Blocked{x, 1, s->hidden}, a, false, p.split_u, p.pu, st));
+  HIP_TRY(hg::launch_adapt_low(p, rows, Blocked{x, 1, s->hidden}, a, Blocked{nullptr, 1, 8}, nullptr, st));
   // The second product's workgroups each read all of their rows' parts: of many
   // rows they are added up first (2047 rows, 28 parts: 578 us against 365).
   const Blocked wide_y{y, s->tp, s->shard};
@@ -210,20 +210,16 @@ HG_API int hg_adapt_grad(const hg_adapt_shape *s, const void *dy, const void *x,
   AdaptRows rows = rows_of(*s, index);
   const int rc = sort_rows(p, &rows, st);
   if (rc != HG_OK) return rc;
-  const Blocked wide_x{x, 1, s->hidden}, wide_y{dy, s->tp, s->shard};
+  const Blocked none{nullptr, 1, 8}, wide_x{x, 1, s->hidden}, wide_y{dy, s->tp, s->shard};
   if (!db) p.u = nullptr, p.ut = nullptr;
   if (!dx && !da) p.g = nullptr;
   if (!da) p.gt = nullptr;
+  if (!dx) p.at = nullptr;
   HIP_TRY(hg::launch_adapt_segments(p, rows, st));
-  if (p.u) HIP_TRY(hg::launch_adapt_low(p, rows, wide_x, a, false, p.split_u, p.pu, st));
-  if (p.g) HIP_TRY(hg::launch_adapt_low(p, rows, wide_y, b, true, p.split_g, p.pg, st));
+  HIP_TRY(hg::launch_adapt_low(p, rows, p.u ? wide_x : none, a, p.g ? wide_y : none, b, st));
   HIP_TRY(hg::launch_adapt_join(p, rows, scale, st));
-  if (da || db) HIP_TRY(hg::launch_adapt_halves(p, st));
-  if (db) HIP_TRY(hg::launch_adapt_outer(p, rows, wide_y, p.ut, p.head, true, p.parts_b, p.pb, wide != 0, db, st));
-  if (da) HIP_TRY(hg::launch_adapt_outer(p, rows, wide_x, p.gt, p.head + 1, false, p.parts_a, p.pa, wide != 0, da, st));
-  if (dx) {
-    HIP_TRY(hg::launch_adapt_turn(p, a, st));
-    HIP_TRY(hg::launch_adapt_up(p, rows, p.g, 1, nullptr, p.at, Blocked{nullptr, 1, s->hidden}, dx, st));
-  }
+  HIP_TRY(hg::launch_adapt_prepare(p, a, st));
+  if (da || db) HIP_TRY(hg::launch_adapt_outer(p, rows, wide_x, da, wide_y, db, wide != 0, st));
+  if (dx) HIP_TRY(hg::launch_adapt_up(p, rows, p.g, 1, nullptr, p.at, Blocked{nullptr, 1, s->hidden}, dx, st));
   return HG_OK;
 }

@@ -41,15 +41,22 @@ def _select_bytes(requests, beams, keep, tp, shard, vocab, dtype) -> int:
 
 def _logits(logits, rows: int) -> tuple[tuple[int, ...], int, torch.dtype, torch.device]:
     """Block pointers, row width, type and device of the logits."""
-    blocks = logits
     if isinstance(logits, torch.Tensor):
-        if logits.dim() not in (2, 3) or not logits.is_contiguous():
+        shape = tuple(logits.shape)
+        if len(shape) not in (2, 3) or not logits.is_contiguous():
             raise ValueError("logits must be a contiguous [rows, vocab] or [tp, rows, shard] tensor, or blocks, got "
-                             f"{list(logits.shape)}{'' if logits.is_contiguous() else ', not contiguous'}")
-        blocks = logits.unbind(0) if logits.dim() == 3 else (logits,)
-    elif not isinstance(logits, Iterable):
+                             f"{list(shape)}{'' if logits.is_contiguous() else ', not contiguous'}")
+        tp = shape[0] if len(shape) == 3 else 1
+        if not 1 <= tp <= _lib.HG_MAX_TP or shape[-2] != rows or shape[-1] < 1:
+            raise ValueError(f"logits must have {rows} rows (one per beam of each request) in 1 to {_lib.HG_MAX_TP} "
+                             f"blocks, got {list(shape)}")
+        if logits.dtype not in _DTYPES:
+            raise ValueError(f"logits must be one of {[str(d) for d in _DTYPES]}, got {logits.dtype}")
+        at, step = logits.data_ptr(), rows * shape[-1] * logits.element_size()
+        return tuple(range(at, at + tp * step, step)) if rows else (at,) * tp, shape[-1], logits.dtype, logits.device
+    if not isinstance(logits, Iterable):
         raise ValueError(f"logits must be a tensor or blocks, got {type(logits).__name__}")
-    blocks = list(blocks)
+    blocks = list(logits)
     if not 1 <= len(blocks) <= _lib.HG_MAX_TP:
         raise ValueError(f"the logits must have 1 to {_lib.HG_MAX_TP} blocks, got {len(blocks)}")
     first = blocks[0]
@@ -103,8 +110,7 @@ def beam_select(logits, scores: torch.Tensor, keep: int, vocab: int | None = Non
     if not 0.0 < scale < math.inf:
         raise ValueError(f"scale must be positive and finite, got {scale}")
     out = torch.empty((requests, keep), dtype=torch.float32, device=device)
-    places = torch.empty((2, requests, keep), dtype=torch.int64, device=device)
-    parents, tokens = places[0], places[1]
+    parents, tokens = (torch.empty((requests, keep), dtype=torch.int64, device=device) for _ in range(2))
     if requests:
         nbytes = _select_bytes(requests, beams, keep, tp, shard, vocab, _DTYPES[dtype])
         ws = _workspace(nbytes, device)

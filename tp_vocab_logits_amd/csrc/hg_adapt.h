@@ -6,7 +6,8 @@
 
 namespace hg {
 
-// Up to this many rows hg_adapt goes through them as they are, without a sort.
+// Up to this many rows hg_adapt takes a workgroup (or several) for each row's u, and
+// sorts the rows beside them.
 constexpr int kFewRows = 64;
 constexpr int kRankChunk = 64;  // ranks that a workgroup holds at once
 
@@ -17,8 +18,8 @@ struct Blocked {
   int blocks, shard;
 };
 
-// The rows' adapters: sorted by adapter (keys ascending, rows without one last),
-// or as the caller gave them (keys NULL).
+// The rows' adapters, sorted (keys ascending, rows without one last, as the key
+// `adapters`), and as the caller gave them.
 struct AdaptRows {
   const int *keys, *pos;
   const void *index;
@@ -27,7 +28,9 @@ struct AdaptRows {
 
 struct AdaptPlan {
   int m, adapters, rank, hidden, tp, shard;
-  bool half, sorted;
+  bool half;
+  int few;               // not above kFewRows, and no gradients
+  int *few_keys;         // [2][kFewRows] then: keys and places
   SortPlan sort;
   int split_u, split_g;  // parts of the sums over hidden and over the vocabulary
   int padded;            // rows, up to a multiple of 32
@@ -52,8 +55,6 @@ hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocke
 hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *part, int splits,
                            const float *scale, const void *w, const Blocked &y, void *out,
                            hipStream_t s);
-// The sorted rows' segments; clears head.
-hipError_t launch_adapt_segments(const AdaptPlan &p, const AdaptRows &r, hipStream_t s);
 // u and g from their parts, scaled; their largest.
 hipError_t launch_adapt_join(const AdaptPlan &p, const AdaptRows &r, const float *scale, hipStream_t s);
 // Their halves by rank (ut, gt) and A turned (at), those that are there.

@@ -8,8 +8,7 @@
 // written, dy, B, dB. The products run on the matrix cores all the same
 // (v_mfma_f32_16x16x32, tiles of 16 rows), so that nothing else comes near.
 //
-// Rows. A tile is 16 rows next to each other, sorted by adapter (a few rows go as
-// they are). A tile with rows of several adapters runs through each of them and
+// Rows. A tile is 16 rows next to each other, sorted by adapter. A tile with rows of several adapters runs through each of them and
 // every row takes its own one's result: no tile lists, y passes once whatever the
 // mixture, and no value of one adapter (an infinity in its B) reaches the rows of
 // another.
@@ -28,14 +27,6 @@ namespace hg {
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ int key_of_row(const AdaptRows &r, int p, int adapters) {
-  if (r.keys) return r.keys[p];
-  const long long i = r.index_bytes == 8 ? static_cast<const long long *>(r.index)[p]
-                                         : static_cast<const int *>(r.index)[p];
-  return i >= 0 && i < adapters ? static_cast<int>(i) : adapters;
-}
-__device__ __forceinline__ int row_of(const AdaptRows &r, int p) { return r.keys ? r.pos[p] : p; }
 
 __device__ __forceinline__ s16x8 load8(const unsigned short *p) {
   return *reinterpret_cast<const s16x8 *>(p);
@@ -67,31 +58,60 @@ __device__ __forceinline__ void halves(float f, uint32_t &hi, uint32_t &lo) {
 
 // ---------------------------------------------------------------------------
 // Few rows: u of one row, or a part of it, per workgroup. A lane holds 8 elements
-// of x and meets them with those of each rank's row of A.
+// of x and meets them with those of each rank's row of A. The last workgroup sorts
+// the rows by adapter meanwhile (up to 64: a lane each).
+
+struct RowArgs {
+  const void *index;
+  int index_bytes;
+  const unsigned short *x, *a;
+  int m, adapters, rank, hidden, splits;
+  float *part;
+  int *keys, *pos;
+};
+
+__device__ __forceinline__ int key_of_row(const RowArgs &r, int j) {
+  const long long i = r.index_bytes == 8 ? static_cast<const long long *>(r.index)[j]
+                                         : static_cast<const int *>(r.index)[j];
+  return i >= 0 && i < r.adapters ? static_cast<int>(i) : r.adapters;
+}
 
 template <class T>
-__global__ __launch_bounds__(kThreads) void k_adapt_row(AdaptRows rows, const unsigned short *x,
-                                                        const unsigned short *a, int adapters, int m,
-                                                        int rank, int hidden, int splits, float *part) {
+__global__ __launch_bounds__(kThreads) void k_adapt_row(RowArgs a) {
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-  const int j = static_cast<int>(blockIdx.x) / splits, split = static_cast<int>(blockIdx.x) - j * splits;
-  const int i = key_of_row(rows, j, adapters);
-  if (i >= adapters) return;
-  const unsigned short *const xr = x + static_cast<size_t>(row_of(rows, j)) * hidden;
-  const unsigned short *const ai = a + static_cast<size_t>(i) * rank * hidden;
-  float *const out = part + (static_cast<size_t>(split) * m + j) * rank;
-  const int steps = (hidden + 511) / 512, from = steps * split / splits, to = steps * (split + 1) / splits;
+  const int j = static_cast<int>(blockIdx.x) / a.splits, split = static_cast<int>(blockIdx.x) - j * a.splits;
+  if (j == a.m) {
+    if (wave > 0) return;
+    const int key = lane < a.m ? key_of_row(a, lane) : 0x7FFFFFFF;
+    int rank = 0;
+#pragma unroll
+    for (int o = 0; o < kFewRows; ++o) {
+      const int other = __builtin_amdgcn_readlane(key, o);
+      rank += other < key || (other == key && o < lane);
+    }
+    if (lane < a.m) {
+      a.keys[rank] = key;
+      a.pos[rank] = lane;
+    }
+    return;
+  }
+  const int i = key_of_row(a, j);
+  if (i >= a.adapters) return;
+  const unsigned short *const xr = a.x + static_cast<size_t>(j) * a.hidden;
+  const unsigned short *const ai = a.a + static_cast<size_t>(i) * a.rank * a.hidden;
+  float *const out = a.part + (static_cast<size_t>(split) * a.m + j) * a.rank;
+  const int steps = (a.hidden + 511) / 512, from = steps * split / a.splits, to = steps * (split + 1) / a.splits;
   constexpr int kRows = 4;  // ranks at once per wave
-  for (int r0 = wave * kRows; r0 < rank; r0 += 4 * kRows) {  // (rank is a multiple of 8)
+  for (int r0 = wave * kRows; r0 < a.rank; r0 += 4 * kRows) {  // (rank is a multiple of 8)
     float sum[kRows] = {0.f, 0.f, 0.f, 0.f};
     for (int step = from; step < to; ++step) {
       const int k = step * 512 + lane * 8;
-      if (k >= hidden) continue;
+      if (k >= a.hidden) continue;
       const s16x8 xv = load8(xr + k);
       s16x8 av[kRows];
 #pragma unroll
-      for (int t = 0; t < kRows; ++t) av[t] = load8(ai + static_cast<size_t>(r0 + t) * hidden + k);
+      for (int t = 0; t < kRows; ++t) av[t] = load8(ai + static_cast<size_t>(r0 + t) * a.hidden + k);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float f = from16<T>(static_cast<unsigned short>(xv[e]));
@@ -160,6 +180,7 @@ struct LowSide {
 struct LowArgs {
   const int *keys, *pos;
   int m, adapters, rank;
+  int *head;     // cleared for the join, or NULL
   LowSide x, y;  // u = A x, g = B^T dy
 };
 
@@ -324,6 +345,7 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
   __shared__ __align__(1024) unsigned char lds[kStages * kStageAll];
   const int id = static_cast<int>(blockIdx.x);
   const int first = (a.m + kLowRows - 1) / kLowRows * a.x.splits;
+  if (a.head && id == 0 && threadIdx.x < 2) a.head[threadIdx.x] = 0;
   if (id < first)
     low_products<T, false, RB>(a, a.x, id, lds);
   else
@@ -444,7 +466,8 @@ __device__ __forceinline__ u32x4 sum8(s16x8 y, const f32x4 *res, float inv) {
 }
 
 struct UpArgs {
-  AdaptRows rows;
+  const int *keys, *pos;
+  int by_row;  // the parts are in the caller's order of rows, not in the sorted one
   const float *part;
   const float *scale;
   const unsigned short *w, *y;
@@ -455,16 +478,12 @@ struct UpArgs {
 };
 
 // RANKS: 16 (upper and lower halves share one fragment), 64, or 256: in turns of 64.
-// A tile's adapters are taken several at a time, so that their fragments of W are on
-// their way together (64 rows of 32 adapters, V = 163840, rank 16: one at a time
-// 45 us, V_BATCHED four).
 template <class T, int RANKS>
 __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
   constexpr bool kBoth = RANKS == 16;
   constexpr int kRow = 2 * RANKS + 8;  // 16-bit elements of an LDS row: upper, lower halves
   constexpr int kPieces = RANKS == 256 ? 2 : 1;
   constexpr int KF = kBoth ? 1 : 2;
-  constexpr int kBatch = RANKS == 16 ? 4 : RANKS == 64 ? 2 : 1;
   __shared__ __align__(16) unsigned short low[16 * kRow];
   __shared__ float back[16];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
@@ -480,10 +499,10 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
 
   {
     const int r = tid / 16, sub = tid % 16, p = p0 + r;
-    const int key = p < a.m ? key_of_row(a.rows, p, a.adapters) : a.adapters;
+    const int key = p < a.m ? a.keys[p] : a.adapters;
     u32x4 hi[kPieces], lo[kPieces];
     float inv;
-    low_values<T, 16, kPieces>(a.part, a.scale, key, p, sub, a.m, a.adapters, a.rank, a.splits, hi, lo, inv);
+    low_values<T, 16, kPieces>(a.part, a.scale, key, a.by_row && p < a.m ? a.pos[p] : p, sub, a.m, a.adapters, a.rank, a.splits, hi, lo, inv);
     if (sub == 0) back[r] = inv;
 #pragma unroll
     for (int q = 0; q < kPieces; ++q) {
@@ -495,8 +514,8 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
     }
   }
   const int p = p0 + ml;
-  const int key = p < a.m ? key_of_row(a.rows, p, a.adapters) : -1;  // -1: no row
-  const size_t row = static_cast<size_t>(p < a.m ? row_of(a.rows, p) : 0) * a.shard;
+  const int key = p < a.m ? a.keys[p] : -1;  // -1: no row
+  const size_t row = static_cast<size_t>(p < a.m ? a.pos[p] : 0) * a.shard;
   __syncthreads();
 
   const int chunk = strip * 4 + wave;
@@ -514,51 +533,34 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
 #pragma unroll
   for (int v = 0; v < 4; ++v) res[v] = f32x4{0.f, 0.f, 0.f, 0.f};
   const unsigned short *const mine = low + ml * kRow;
-  auto fragments = [&](int i, int rc, s16x8 (&wf)[4][KF]) __attribute__((always_inline)) {
-    const unsigned short *const wi = wcol + static_cast<size_t>(i) * each;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int col = 32 * (v >> 1) + 8 * (ml >> 2) + 4 * (v & 1) + (ml & 3);
-#pragma unroll
-      for (int ks = 0; ks < KF; ++ks) {
-        const int r = kBoth ? 8 * (g & 1) : rc + ks * 32 + 8 * g;
-        wf[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
-      }
-    }
-  };
   unsigned todo = static_cast<unsigned>(__ballot(key >= 0 && key < a.adapters)) & 0xFFFF;
   while (todo) {
-    int cur[kBatch];
-    s16x8 wf[kBatch][4][KF];
+    const int cur = __builtin_amdgcn_readlane(key, __builtin_ctz(todo));
+    todo &= ~static_cast<unsigned>(__ballot(key == cur));
+    const unsigned short *const wi = wcol + static_cast<size_t>(cur) * each;
+    f32x4 acc[4];
 #pragma unroll
-    for (int n = 0; n < kBatch; ++n) {
-      cur[n] = -1;
-      if (todo) {
-        cur[n] = __builtin_amdgcn_readlane(key, __builtin_ctz(todo));
-        todo &= ~static_cast<unsigned>(__ballot(key == cur[n]));
-        fragments(cur[n], 0, wf[n]);
+    for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int rc = 0; rc < (RANKS <= kRankChunk ? 1 : a.rank); rc += kRankChunk) {
+      s16x8 wf[4][KF];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int col = 32 * (v >> 1) + 8 * (ml >> 2) + 4 * (v & 1) + (ml & 3);
+#pragma unroll
+        for (int ks = 0; ks < KF; ++ks) {
+          const int r = kBoth ? 8 * (g & 1) : rc + ks * 32 + 8 * g;
+          wf[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
+        }
       }
+      add_low<T, kBoth>(acc, wf, [&](int half, int ks) __attribute__((always_inline)) {
+        return load8(mine + (kBoth ? 8 * g : half * RANKS + rc + ks * 32 + 8 * g));
+      });
     }
+    const bool take = key == cur;
 #pragma unroll
-    for (int n = 0; n < kBatch; ++n) {
-      if (cur[n] < 0) break;
-      f32x4 acc[4];
+    for (int v = 0; v < 4; ++v)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int rc = 0;;) {
-        add_low<T, kBoth>(acc, wf[n], [&](int half, int ks) __attribute__((always_inline)) {
-          return load8(mine + (kBoth ? 8 * g : half * RANKS + rc + ks * 32 + 8 * g));
-        });
-        rc += kRankChunk;
-        if (RANKS <= kRankChunk || rc >= a.rank) break;
-        fragments(cur[n], rc, wf[n]);
-      }
-      const bool take = key == cur[n];
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) res[v][e] = take ? acc[v][e] : res[v][e];
-    }
+      for (int e = 0; e < 4; ++e) res[v][e] = take ? acc[v][e] : res[v][e];
   }
   const bool has = key < a.adapters;
   if (key < 0 || (a.y == a.out && !has)) return;
@@ -747,16 +749,6 @@ __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
 
 // ---------------------------------------------------------------------------
 // The gradients' small pieces.
-
-// seg[i]: the first sorted position of adapter i or a later one.
-__global__ __launch_bounds__(kThreads) void k_adapt_segments(const int *keys, int m, int adapters,
-                                                             int *seg, int *head) {
-  const int j = static_cast<int>(blockIdx.x * kThreads + threadIdx.x);
-  if (j == 0) head[0] = head[1] = 0;
-  if (j > m) return;
-  const int before = j > 0 ? keys[j - 1] : -1, here = j < m ? keys[j] : adapters;
-  for (int i = before + 1; i <= here && i <= adapters; ++i) seg[i] = j;
-}
 
 // The parts' sums, scaled, and (fp16) their largest: blockIdx.y 0: u, 1: g.
 struct JoinSide {
@@ -1136,10 +1128,11 @@ int adapt_parts(int m, int adapters, int blocks, int shard, int rank) {
 hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocked &x, const void *a,
                             const Blocked &y, const void *b, hipStream_t s) {
   const auto *xp = static_cast<const unsigned short *>(x.p), *ap = static_cast<const unsigned short *>(a);
-  if (!p.sorted) {
+  if (p.few) {
+    const RowArgs args{r.index, r.index_bytes, xp, ap, p.m, p.adapters, p.rank, x.shard, p.split_u, p.pu,
+                       p.few_keys, p.few_keys + kFewRows};
     by_type(p.half, [&](auto type) {
-      hipLaunchKernelGGL((k_adapt_row<decltype(type)>), dim3(p.m * p.split_u), dim3(kThreads), 0, s, r, xp, ap,
-                         p.adapters, p.m, p.rank, x.shard, p.split_u, p.pu);
+      hipLaunchKernelGGL((k_adapt_row<decltype(type)>), dim3(p.m * p.split_u + 1), dim3(kThreads), 0, s, args);
     });
     return hipGetLastError();
   }
@@ -1148,7 +1141,7 @@ hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocke
     return LowSide{static_cast<const unsigned short *>(of.p), static_cast<const unsigned short *>(w), of.blocks,
                    of.shard, per, per * of.blocks, of.p ? splits : 0, part};
   };
-  const LowArgs args{r.keys, r.pos, p.m, p.adapters, p.rank, side(x, a, p.split_u, p.pu), side(y, b, p.split_g, p.pg)};
+  const LowArgs args{r.keys, r.pos, p.m, p.adapters, p.rank, p.head, side(x, a, p.split_u, p.pu), side(y, b, p.split_g, p.pg)};
   const dim3 grid(static_cast<unsigned>(ceil_div(p.m, kLowRows)) * (args.x.splits + args.y.splits),
                   ceil_div(p.rank, kRankChunk));
   by_type(p.half, [&](auto type) {
@@ -1183,7 +1176,7 @@ hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *
       p.rank <= 16 ? go(Int<1>{}) : go(Int<4>{});
     } else {
       const int groups = ceil_div(p.m, 16), strips = ceil_div(chunks, 4);
-      const UpArgs a{r, part, scale, wp, yp, op, p.m, p.adapters, p.rank, splits, y.blocks, y.shard, per, chunks,
+      const UpArgs a{r.keys, r.pos, p.few, part, scale, wp, yp, op, p.m, p.adapters, p.rank, splits, y.blocks, y.shard, per, chunks,
                      groups, strips};
       auto go = [&](auto ranks) {
         hipLaunchKernelGGL((k_adapt_up<T, decltype(ranks)::value>),
@@ -1192,12 +1185,6 @@ hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *
       p.rank <= 16 ? go(Int<16>{}) : p.rank <= kRankChunk ? go(Int<kRankChunk>{}) : go(Int<HG_MAX_RANK>{});
     }
   });
-  return hipGetLastError();
-}
-
-hipError_t launch_adapt_segments(const AdaptPlan &p, const AdaptRows &r, hipStream_t s) {
-  hipLaunchKernelGGL(k_adapt_segments, dim3(ceil_div(p.m + 1, kThreads)), dim3(kThreads), 0, s, r.keys, p.m,
-                     p.adapters, p.seg, p.head);
   return hipGetLastError();
 }
 

@@ -55,7 +55,7 @@ size_t lay_out(const hg_adapt_shape &s, int kind, char *ws, AdaptPlan *p) {
   p->tp = s.tp;
   p->shard = s.shard;
   p->half = s.dtype == HG_FP16;
-  p->sorted = kind == HG_ADAPT_GRAD || s.m > hg::kFewRows;
+  p->few = kind == HG_ADAPT_ADD && s.m <= hg::kFewRows;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     char *q = ws + at;
@@ -64,16 +64,18 @@ size_t lay_out(const hg_adapt_shape &s, int kind, char *ws, AdaptPlan *p) {
   };
   auto floats = [&](size_t n) { return reinterpret_cast<float *>(take(4 * n)); };
   const size_t low = static_cast<size_t>(s.m) * s.rank;
-  if (p->sorted) {
+  if (p->few) {
+    p->few_keys = reinterpret_cast<int *>(take(8 * hg::kFewRows));
+  } else {
     p->sort = hg::sort_plan(s.adapters, s.m);
     p->sort_ws = take(p->sort.bytes);
   }
-  p->split_u = hg::adapt_splits(s.m, 1, s.hidden, s.rank, !p->sorted);
+  p->split_u = hg::adapt_splits(s.m, 1, s.hidden, s.rank, p->few);
   p->pu = floats(low * p->split_u);
   if (hg::adapt_streams(s.m, s.adapters, s.rank)) {
     p->low = reinterpret_cast<unsigned short *>(take(static_cast<size_t>(s.m) * (s.rank <= 16 ? 64 : 256)));
     p->back = floats(s.m);
-  } else if (kind == HG_ADAPT_ADD && p->sorted) {
+  } else if (kind == HG_ADAPT_ADD && !p->few) {
     p->u = floats(low);
   }
   if (kind == HG_ADAPT_ADD) return at;
@@ -122,7 +124,7 @@ AdaptRows rows_of(const hg_adapt_shape &s, const void *index) {
 
 int sort_rows(const AdaptPlan &p, AdaptRows *r, hipStream_t st) {
   hg::Sorted sorted;
-  HIP_TRY(hg::launch_sort(p.sort, p.sort_ws, p.adapters, r->index, r->index_bytes, p.m, &sorted, st));
+  HIP_TRY(hg::launch_sort(p.sort, p.sort_ws, p.adapters, r->index, r->index_bytes, p.m, p.seg, &sorted, st));
   r->keys = sorted.keys;
   r->pos = sorted.pos;
   return HG_OK;
@@ -160,7 +162,10 @@ HG_API int hg_adapt(const hg_adapt_shape *s, const void *y, const void *x, const
   if (lay_out(*s, HG_ADAPT_ADD, static_cast<char *>(ws), &p) > ws_bytes) return too_small();
   hipStream_t st = static_cast<hipStream_t>(stream);
   AdaptRows rows = rows_of(*s, index);
-  if (p.sorted) {
+  if (p.few) {
+    rows.keys = p.few_keys;
+    rows.pos = p.few_keys + hg::kFewRows;
+  } else {
     const int rc = sort_rows(p, &rows, st);
     if (rc != HG_OK) return rc;
   }
@@ -215,7 +220,6 @@ HG_API int hg_adapt_grad(const hg_adapt_shape *s, const void *dy, const void *x,
   if (!dx && !da) p.g = nullptr;
   if (!da) p.gt = nullptr;
   if (!dx) p.at = nullptr;
-  HIP_TRY(hg::launch_adapt_segments(p, rows, st));
   HIP_TRY(hg::launch_adapt_low(p, rows, p.u ? wide_x : none, a, p.g ? wide_y : none, b, st));
   HIP_TRY(hg::launch_adapt_join(p, rows, scale, st));
   HIP_TRY(hg::launch_adapt_prepare(p, a, st));

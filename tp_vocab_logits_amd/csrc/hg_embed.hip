@@ -206,10 +206,22 @@ __device__ __forceinline__ void fill_part(const Fill &f, int k) {
     f.p[i] = u32x4{0u, 0u, 0u, 0u};
 }
 
-// All keys in one workgroup's LDS.
+// Where the sorted keys begin: seg[i] is the first place of a key of i or more, for i
+// in 0 .. rows; place j writes those between its key and the one before it.
+template <class K>
+__device__ __forceinline__ void begin_segments(K key, int j, int n, int rows, int *seg) {
+  const int before = j > 0 ? key(j - 1) : -1, here = j < n ? key(j) : rows;
+  for (int i = before + 1; i <= here; ++i) seg[i] = j;
+}
+__global__ __launch_bounds__(256) void k_sort_segments(const int *keys, int n, int rows, int *seg) {
+  const int j = static_cast<int>(blockIdx.x * 256 + threadIdx.x);
+  if (j <= n) begin_segments([&](int k) { return keys[k]; }, j, n, rows, seg);
+}
+
+// All keys in one workgroup's LDS. seg may be NULL.
 __global__ __launch_bounds__(1024) void k_sort_tile(const void *tokens, int token_bytes, int n,
                                                     int rows, int passes, int *keys, int *pos,
-                                                    Fill fill) {
+                                                    int *seg, Fill fill) {
   if (blockIdx.x > 0) {
     fill_part(fill, static_cast<int>(blockIdx.x) - 1);
     return;
@@ -246,6 +258,9 @@ __global__ __launch_bounds__(1024) void k_sort_tile(const void *tokens, int toke
     keys[k] = sk[passes & 1][k];
     pos[k] = sp[passes & 1][k];
   }
+  if (seg)
+    for (int k = tid; k <= n; k += 1024)
+      begin_segments([&](int j) { return sk[passes & 1][j]; }, k, n, rows, seg);
 }
 
 // Counts of one pass: hist[digit][tile].
@@ -644,7 +659,7 @@ int sort_launches(const SortPlan &p) { return p.tiles <= 1 ? 1 : 3 * p.passes; }
 // adds the workgroups that it takes.
 template <class F>
 Sorted launch_sort(const SortPlan &p, char *base, int rows, const void *tokens, int token_bytes,
-                   long long n, hipStream_t s, F fill) {
+                   long long n, int *seg, hipStream_t s, F fill) {
   int *buf[4], *hist = reinterpret_cast<int *>(base + p.off[4]);
   for (int k = 0; k < 4; ++k) buf[k] = reinterpret_cast<int *>(base + p.off[k]);
   int side = 0;
@@ -652,7 +667,7 @@ Sorted launch_sort(const SortPlan &p, char *base, int rows, const void *tokens, 
     int groups = 1;
     const Fill f = fill(&groups);
     hipLaunchKernelGGL(k_sort_tile, dim3(groups), dim3(1024), 0, s, tokens, token_bytes,
-                       static_cast<int>(n), rows, p.passes, buf[0], buf[1], f);
+                       static_cast<int>(n), rows, p.passes, buf[0], buf[1], seg, f);
   } else {
     for (int k = 0; k < p.passes; ++k) {
       const int *ik = k ? buf[2 * side] : nullptr, *ip = k ? buf[2 * side + 1] : nullptr;
@@ -665,6 +680,9 @@ Sorted launch_sort(const SortPlan &p, char *base, int rows, const void *tokens, 
       hipLaunchKernelGGL(k_sort_place, dim3(g3), dim3(1024), 0, s, tokens, token_bytes, ik, ip, n,
                          rows, 9 * k, hist, p.tiles, buf[2 * side], buf[2 * side + 1], f3);
     }
+    if (seg)
+      hipLaunchKernelGGL(k_sort_segments, dim3(static_cast<unsigned>(n / 256 + 1)), dim3(256), 0, s, buf[2 * side],
+                         static_cast<int>(n), rows, seg);
   }
   return Sorted{buf[2 * side], buf[2 * side + 1]};
 }
@@ -672,8 +690,8 @@ Sorted launch_sort(const SortPlan &p, char *base, int rows, const void *tokens, 
 }  // namespace
 
 hipError_t launch_sort(const SortPlan &p, void *ws, int rows, const void *index, int index_bytes,
-                       long long n, Sorted *sorted, hipStream_t s) {
-  *sorted = launch_sort(p, static_cast<char *>(ws), rows, index, index_bytes, n, s,
+                       long long n, int *seg, Sorted *sorted, hipStream_t s) {
+  *sorted = launch_sort(p, static_cast<char *>(ws), rows, index, index_bytes, n, seg, s,
                         [](int *) { return Fill{nullptr, 0, 1}; });
   return hipGetLastError();
 }
@@ -740,7 +758,7 @@ hipError_t launch_embed_grad(const EmbedPlan &p, void *ws, int rows, int hidden,
   const long long share = (zeros + launches - 1) / launches;
   int part = 0;
   // the zeros, cut into one part per launch of the sort
-  const Sorted sorted = launch_sort(sort, base, rows, tokens, token_bytes, n, s, [&](int *groups) {
+  const Sorted sorted = launch_sort(sort, base, rows, tokens, token_bytes, n, nullptr, s, [&](int *groups) {
     Fill f;
     const long long at = share * part++;
     f.p = static_cast<u32x4 *>(dw) + at;

@@ -104,7 +104,7 @@ hipError_t launch_embed(const VocabMatrix &w, int rows, int dtype, const void *t
 
 // A stable sort of n keys index[j] (int32 or int64) in 0 .. rows-1, those outside
 // last, as the key `rows`: the sorted keys and the places that they came from, both
-// in the workspace.
+// in the workspace; in seg[rows + 1], if given, where each key's run begins.
 struct SortPlan {
   int passes, tiles;
   size_t off[5], bytes;
@@ -114,7 +114,7 @@ struct Sorted {
 };
 SortPlan sort_plan(int rows, long long n);
 hipError_t launch_sort(const SortPlan &p, void *ws, int rows, const void *index, int index_bytes,
-                       long long n, Sorted *sorted, hipStream_t s);
+                       long long n, int *seg, Sorted *sorted, hipStream_t s);
 
 // Workspace of an embedding gradient over n tokens: the sort's, then partial rows.
 struct EmbedPlan {

@@ -41,7 +41,7 @@ WORKSPACE_LIMIT = 4 << 30
 def _call(fn, name: str, device: torch.device, *args) -> None:
     """One library call on the device's current stream, appended to ``args``."""
     index = device.index
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:  # (torch.cuda.current_device() without its check for a first use)
         code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
@@ -85,6 +85,8 @@ def _matrix(w, tp: int, shard: int, dtypes) -> tuple[tuple[int, ...], int, torch
 
 def _given(t, name: str, shape, dtypes, device) -> torch.Tensor:
     """An argument tensor of the given shape, type and device, contiguous."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.is_contiguous() and t.device == device:
+        return t
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
     if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous():

@@ -52,6 +52,37 @@ struct Lane {
       f[2 * t + 1] = from16<T>(v[t] >> 16);
     }
   }
+  // The largest value, NaN left out, of N vectors: pairs of 16-bit integers in the
+  // values' order (one and a half instructions an element); positive NaN are above
+  // infinity there and taken out if one shows, negative ones below it.
+  template <int J>
+  static __device__ __forceinline__ float largest(const u32x4 (&v)[J]) {
+    typedef short pair __attribute__((ext_vector_type(2)));
+    constexpr short kTop = T::kHalf ? 0x7C00 : 0x7F80;
+    pair top = {-32768, -32768};
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t w = v[j][t];
+        const uint32_t sign = __builtin_bit_cast(uint32_t, __builtin_bit_cast(pair, w) >> 15);
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(pair, w ^ (sign & 0x7FFF7FFFu)));
+      }
+    short most = top[0] > top[1] ? top[0] : top[1];
+    if (__ballot(most > kTop)) {
+      most = -32768;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const short b = static_cast<short>(v[j][t / 2] >> 16 * (t & 1));
+          const short o = static_cast<short>(b ^ (b >> 15 & 0x7FFF));
+          most = o > most && o <= kTop ? o : most;
+        }
+    }
+    const float z = from16<T>(static_cast<unsigned short>(most ^ (most >> 15 & 0x7FFF)));
+    return z == z ? z : -__builtin_inff();  // (negative NaN alone)
+  }
 };
 template <>
 struct Lane<BeamF32> {
@@ -65,6 +96,18 @@ struct Lane<BeamF32> {
       const uint32_t b = v[t];
       f[t] = __builtin_bit_cast(float, b);
     }
+  }
+  template <int J>
+  static __device__ __forceinline__ float largest(const u32x4 (&v)[J]) {
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      float f[4];
+      get(v[j], f);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) top = f[t] > top ? f[t] : top;
+    }
+    return top;
   }
 };
 
@@ -104,18 +147,8 @@ __device__ __forceinline__ uint32_t nth_order(uint32_t o, int n) {
   return t > kLeast ? t : kLeast;
 }
 
-// The n-th largest of the lanes' keys; 1 if fewer than n lanes have one.
-__device__ __forceinline__ u64 nth_key(u64 key, int n) {
-  u64 t = 0;
-  for (int bit = 63; bit >= 0; --bit) {
-    const u64 trial = t | 1ull << bit;
-    if (__popcll(__ballot(key >= trial)) >= n) t = trial;
-  }
-  return t ? t : 1;
-}
-
-// exp2(t) for t <= 0 (below -1000: as at -1000, which adds nothing to a sum of
-// at least 2^-1).
+// exp2(t) for t <= 0 (NaN and what is below -1000: as at -1000, which adds nothing
+// to a sum of at least 2^-1).
 __device__ __forceinline__ double exp2_of(double t) {
   constexpr double kRound = 6755399441055744.0;  // 1.5 * 2^52: its low bits are the rounded t
   t = t > -1000.0 ? t : -1000.0;
@@ -129,10 +162,7 @@ __device__ __forceinline__ double exp2_of(double t) {
   p = __builtin_fma(p, f, 0.24022651213498092661);
   p = __builtin_fma(p, f, 0.69314718055683241353);
   p = __builtin_fma(p, f, 0.99999999995956175074);
-  // times 2^k: into the exponent
-  const u64 b = __builtin_bit_cast(u64, p);
-  const uint32_t hi = static_cast<uint32_t>(b >> 32) + (static_cast<uint32_t>(__builtin_bit_cast(u64, k)) << 20);
-  return __builtin_bit_cast(double, static_cast<u64>(hi) << 32 | static_cast<uint32_t>(b));
+  return __builtin_ldexp(p, static_cast<int>(static_cast<uint32_t>(__builtin_bit_cast(u64, k))));
 }
 
 struct ScanArgs {
@@ -152,7 +182,9 @@ template <class T, int J, int NT>
 __global__ __launch_bounds__(kScanThreads) void k_beam_scan(ShardTableN<NT> logits, ScanArgs a) {
   using L = Lane<T>;
   constexpr float kNoneF = -__builtin_inff();
+  constexpr int kMine = J * L::N;  // entries of a lane
   __shared__ u64 found[kFound];
+  __shared__ u32x4 held[kScanThreads * J];
   __shared__ double sums[4];
   __shared__ float tops[4];
   __shared__ uint32_t bounds[4];
@@ -162,7 +194,6 @@ __global__ __launch_bounds__(kScanThreads) void k_beam_scan(ShardTableN<NT> logi
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int row = static_cast<int>(blockIdx.x) / a.parts;
   const int part = static_cast<int>(blockIdx.x) - row * a.parts;
-  if (!is_live(a.scores[row]) || (a.finished && a.finished[row])) return;  // the join asks for nothing
   const int rank = NT == 1 ? 0 : part / a.per_block;
   const int piece = part - rank * a.per_block;
   const int first = rank * a.shard;  // the block's first place in the vocabulary
@@ -177,6 +208,12 @@ __global__ __launch_bounds__(kScanThreads) void k_beam_scan(ShardTableN<NT> logi
       reinterpret_cast<const typename L::elt *>(logits.p[rank]) + static_cast<size_t>(row) * a.shard;
   const int at0 = (piece * (J * kScanThreads) + tid) * L::N;
   u32x4 v[J];
+  // A beam that is not there, or finished: the join asks for nothing, and nothing is
+  // read of it (few rows: whether it is there is asked meanwhile).
+  auto absent = [&]() __attribute__((always_inline)) {
+    return !is_live(a.scores[row]) || (a.finished && a.finished[row]);
+  };
+  if (J == 4 && absent()) return;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int at = at0 + j * (kScanThreads * L::N);
@@ -196,39 +233,10 @@ __global__ __launch_bounds__(kScanThreads) void k_beam_scan(ShardTableN<NT> logi
       }
     }
   }
+  if (J < 4 && absent()) return;
   if (tid == 0) count = 0;
 
-  // the lane's and the wave's largest; NaN becomes minus infinity
-  float top = kNoneF;
-  bool odd = false;
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    float f[L::N];
-    L::get(v[j], f);
-#pragma unroll
-    for (int e = 0; e < L::N; ++e) {
-      odd |= f[e] != f[e];
-      top = fmaxf(top, f[e]);
-    }
-  }
-  if (__ballot(odd)) {
-    top = kNoneF;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      float f[L::N];
-      L::get(v[j], f);
-#pragma unroll
-      for (int e = 0; e < L::N; ++e) {
-        const bool none = f[e] != f[e];
-        if (!none) top = fmaxf(top, f[e]);
-        if constexpr (L::N == 4) {
-          if (none) v[j][e] = L::kNone;
-        } else {
-          if (none) v[j][e / 2] = (v[j][e / 2] & (e & 1 ? 0xFFFFu : 0xFFFF0000u)) | L::kNone << (e & 1) * 16;
-        }
-      }
-    }
-  }
+  const float top = L::largest(v);
   const float wtop = wave_max(top);
   const uint32_t bound = nth_order<L::kLow>(top > kNoneF ? order_of(top) : 0u, a.keep);
 
@@ -279,13 +287,34 @@ __global__ __launch_bounds__(kScanThreads) void k_beam_scan(ShardTableN<NT> logi
       for (int e = 0; e < L::N; ++e) use(f[e], place + e);
     }
   };
-  if (top >= least)
-    each([&](float z, int place) __attribute__((always_inline)) {
-      if (z >= least) {
-        const int n = atomicAdd(&count, 1);
-        if (n < kFound) found[n] = key_of(z, place);
-      }
-    });
+  // Which of the lane's entries are of interest: a bit each, without a branch; the few
+  // that are, are looked up again in LDS.
+  static_assert(kMine <= 32);
+  uint32_t bits = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    float f[L::N];
+    L::get(v[j], f);
+#pragma unroll
+    for (int e = 0; e < L::N; ++e) bits = bits + bits + (f[e] >= least ? 1u : 0u);
+  }
+  if (bits) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) held[j * kScanThreads + tid] = v[j];
+    do {
+      const int k = 31 - __builtin_clz(bits);  // the last entry is bit 0
+      bits &= ~(1u << k);
+      const int i = kMine - 1 - k, j = i / L::N, e = i % L::N;
+      const u32x4 *const from = held + j * kScanThreads + tid;
+      float z;
+      if constexpr (L::N == 4)
+        z = reinterpret_cast<const float *>(from)[e];
+      else
+        z = from16<T>(reinterpret_cast<const unsigned short *>(from)[e]);
+      const int n = atomicAdd(&count, 1);
+      if (n < kFound) found[n] = key_of(z, first + at0 + j * (kScanThreads * L::N) + e);
+    } while (bits);
+  }
   if (tid == 0) {
     float t = tops[0];
     for (int w = 1; w < 4; ++w) t = fmaxf(t, tops[w]);
@@ -378,44 +407,53 @@ __device__ __forceinline__ int join_row(const JoinArgs &a, int row, int lane, do
   }
   const BeamStat *const stat = a.stat + static_cast<size_t>(row) * a.parts;
   const u64 *const keys = a.keys + static_cast<size_t>(row) * a.parts * a.keep;
-  // the row's largest and its sum; the lane's best entry
-  float top = -__builtin_inff();
-  u64 head = 0;
-  for (int p = lane; p < a.parts; p += 64) {
-    top = fmaxf(top, stat[p].top);
-    const u64 k = keys[static_cast<size_t>(p) * a.keep];
-    head = k > head ? k : head;
-  }
-  top = wave_max(top);
-  if (top == -__builtin_inff()) return 0;
-  const bool boundless = top == __builtin_inff();
-  double sum = 0.0;
-  for (int p = lane; p < a.parts; p += 64) {
-    const BeamStat one = stat[p];
-    if (one.top == top)
-      sum += one.sum;
-    else if (!boundless && one.top > -__builtin_inff())
-      sum += one.sum * exp2_of((static_cast<double>(one.top) - static_cast<double>(top)) * a.rate);
-  }
-  sum = wave_sum(sum);
-  const double lse = boundless ? log(sum) : a.scale * static_cast<double>(top) + log(sum);
-
-  // Entries at or above the keep-th of the lanes' best: at most keep lanes have
-  // any, about twice keep entries in all for logits in no order.
-  u64 bar = nth_key(head, a.keep);
+  // The entries, eight of a lane in registers (all there are, mostly): with the
+  // parts' sums, they are one round trip.
   const int all = a.parts * a.keep;
-  auto each = [&](auto &&use) __attribute__((always_inline)) {
-    for (int i0 = 0; i0 < all; i0 += 64 * 8) {
-      u64 k[8];
+  u64 mine[8];
+  auto load8 = [&](int i0, u64 (&k)[8]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const int i = i0 + t * 64 + lane;
-        k[t] = i < all ? keys[i] : 0;
-      }
+    for (int t = 0; t < 8; ++t) {
+      const int i = i0 + t * 64 + lane;
+      k[t] = i < all ? keys[i] : 0;
+    }
+  };
+  load8(0, mine);
+  auto each = [&](auto &&use) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 8; ++t) use(mine[t]);
+    for (int i0 = 512; i0 < all; i0 += 512) {
+      u64 k[8];
+      load8(i0, k);
 #pragma unroll
       for (int t = 0; t < 8; ++t) use(k[t]);
     }
   };
+  // the row's largest and its sum
+  BeamStat one = lane < a.parts ? stat[lane] : BeamStat{0.0, -__builtin_inff(), 0};
+  float top = one.top;
+  for (int p = lane + 64; p < a.parts; p += 64) top = fmaxf(top, stat[p].top);
+  top = wave_max(top);
+  if (top == -__builtin_inff()) return 0;
+  const bool boundless = top == __builtin_inff();
+  double sum = 0.0;
+  for (int p = lane;;) {
+    if (one.top == top)
+      sum += one.sum;
+    else if (!boundless && one.top > -__builtin_inff())
+      sum += one.sum * exp2_of((static_cast<double>(one.top) - static_cast<double>(top)) * a.rate);
+    if ((p += 64) >= a.parts) break;
+    one = stat[p];
+  }
+  sum = wave_sum(sum);
+  const double lse = boundless ? log(sum) : a.scale * static_cast<double>(top) + log(sum);
+
+  // Entries at or above the keep-th of the lanes' best logits: at most keep lanes
+  // have any that are above it, about twice keep entries in all for logits in no
+  // order.
+  u64 head = 0;
+  each([&](u64 k) __attribute__((always_inline)) { head = k > head ? k : head; });
+  u64 bar = static_cast<u64>(nth_order<0>(static_cast<uint32_t>(head >> 32), a.keep)) << 32;
   auto collect = [&]() __attribute__((always_inline)) {
     wave_fence();
     if (lane == 0) *counter = 0;
@@ -435,7 +473,7 @@ __device__ __forceinline__ int join_row(const JoinArgs &a, int row, int lane, do
     return c;
   };
   int n = collect();
-  if (n > a.room) {  // parts that hold most of the best, many to keep: the bar itself, over all entries
+  if (n > a.room) {  // lanes that hold most of the best, or equal logits: the keep-th itself
     bar = 0;
     for (int bit = 63; bit >= 0; --bit) {
       const u64 trial = bar | 1ull << bit;
@@ -443,15 +481,7 @@ __device__ __forceinline__ int join_row(const JoinArgs &a, int row, int lane, do
       each([&](u64 k) __attribute__((always_inline)) { c += k >= trial; });
       if (total(c) >= a.keep) bar = trial;
     }
-    n = collect();
-  } else if (n > 128) {  // the same over what was found
-    bar = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-      const u64 trial = bar | 1ull << bit;
-      int c = 0;
-      for (int i = lane; i < n; i += 64) c += found[i] >= trial;
-      if (total(c) >= a.keep) bar = trial;
-    }
+    if (bar == 0) bar = 1;
     n = collect();
   }
   int filled = 0;
@@ -470,7 +500,7 @@ __device__ __forceinline__ int join_row(const JoinArgs &a, int row, int lane, do
   return total(filled);
 }
 
-__global__ __launch_bounds__(256) void k_beam_join(JoinArgs a) {
+__global__ __launch_bounds__(1024) void k_beam_join(JoinArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = static_cast<int>(blockDim.x) >> 6;
@@ -570,12 +600,11 @@ hipError_t launch_beam_scan(const BeamPlan &p, const ShardTable &logits, const f
 
 hipError_t launch_beam_join(const BeamPlan &p, const float *scores, const unsigned char *finished,
                             float *out, long long *parents, long long *tokens, hipStream_t s) {
-  // Room for what keep lanes can hold at most, as far as 64 KB go: the rest is
-  // the join's slower way.
-  const int waves = p.beams < 4 ? p.beams : 4;
-  const int most = p.keep * p.keep * ((p.parts + 63) / 64);
-  const int fits = (65536 - join_lds(p.beams, p.keep, waves, 0).bytes) / (8 * waves);
-  const int room = most < fits ? most : fits;
+  // A wave per beam, up to 16, each with room for the most entries that are ranked as
+  // they are (128; more than keep in any case).
+  constexpr int room = 128;
+  int waves = p.beams < 16 ? p.beams : 16;
+  if (join_lds(p.beams, p.keep, waves, room).bytes > 65536) waves = 8;
   const JoinArgs a{p.beams, p.keep, p.parts, p.vocab, p.pad, room, p.scale, p.scale * kLog2E,
                    scores, finished, p.stat, p.keys, out, parents, tokens};
   hipLaunchKernelGGL(k_beam_join, dim3(p.requests), dim3(64 * waves),

@@ -200,7 +200,10 @@ __device__ __forceinline__ void low_products(const LowArgs &a, const LowSide &s,
   const int from = static_cast<int>(static_cast<long long>(s.chunks) * split / s.splits);
   const int to = static_cast<int>(static_cast<long long>(s.chunks) * (split + 1) / s.splits);
   const int p0 = group * kLowRows;
-  const int pend = a.m < p0 + kLowRows ? a.m : p0 + kLowRows;
+  // the rows that go through an adapter together: a wave's where none waits for another
+  const int begin = RB == 1 ? p0 + wave * 32 : p0, most = begin + (RB == 1 ? 32 : kLowRows);
+  const int pend = a.m < most ? a.m : most;
+  if (begin >= a.m) return;
   const size_t columns = static_cast<size_t>(s.blocks) * s.shard;
   const LoadLane lr = load_lane<false>(lane), lc = load_lane<true>(lane);
   FragLane<false> fr;
@@ -222,7 +225,7 @@ __device__ __forceinline__ void low_products(const LowArgs &a, const LowSide &s,
     lkey[q] = p < a.m ? a.keys[p] : a.adapters;
     src[q] = s.of + static_cast<size_t>(p < a.m ? a.pos[p] : 0) * s.shard + lr.chunk[q & 1] * 8;
   }
-  int at = p0;  // the first position of the adapter in turn
+  int at = begin;  // the first position of the adapter in turn
   int cur = __builtin_amdgcn_readfirstlane(a.keys[at]);
   while (cur < a.adapters) {
     bool active[TT];
@@ -496,13 +499,46 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
   const int strip = eight * 8 + in % 8, group = in / 8;
   if (strip >= a.strips) return;
   const int p0 = group * 16;
+  const int p = p0 + ml;
+  const int key = p < a.m ? a.keys[p] : -1;  // -1: no row
+  const size_t row = static_cast<size_t>(p < a.m ? a.pos[p] : 0) * a.shard;
+  const int chunk = strip * 4 + wave;
+  const bool there = chunk < a.chunks;
+  const int block = there ? chunk / a.per_block : 0, c0 = there ? (chunk - block * a.per_block) * 64 : 0;
+  const int left = there ? a.shard - c0 : 0;
+  const size_t at = static_cast<size_t>(block) * a.m * a.shard + c0;
+  const unsigned short *const wcol = a.w + (static_cast<size_t>(block) * a.shard + c0) * a.rank;
+  const size_t each = static_cast<size_t>(a.blocks) * a.shard * a.rank;
+
+  // y and the first adapter's fragments are on their way before the low-rank values
+  s16x8 yv[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    yv[h] = a.y && key >= 0 && h * 32 + 8 * g < left ? load8(a.y + at + row + h * 32 + 8 * g) : zero8();
+  s16x8 wf[4][KF];
+  auto fragments = [&](int i, int rc) __attribute__((always_inline)) {
+    const unsigned short *const wi = wcol + static_cast<size_t>(i) * each;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int col = 32 * (v >> 1) + 8 * (ml >> 2) + 4 * (v & 1) + (ml & 3);
+#pragma unroll
+      for (int ks = 0; ks < KF; ++ks) {
+        const int r = kBoth ? 8 * (g & 1) : rc + ks * 32 + 8 * g;
+        wf[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
+      }
+    }
+  };
+  unsigned todo = static_cast<unsigned>(__ballot(key >= 0 && key < a.adapters)) & 0xFFFF;
+  int cur = todo ? __builtin_amdgcn_readlane(key, __builtin_ctz(todo)) : -1;
+  if (todo) fragments(cur, 0);
 
   {
-    const int r = tid / 16, sub = tid % 16, p = p0 + r;
-    const int key = p < a.m ? a.keys[p] : a.adapters;
+    const int r = tid / 16, sub = tid % 16, q0 = p0 + r;
+    const int other = q0 < a.m ? a.keys[q0] : a.adapters;
     u32x4 hi[kPieces], lo[kPieces];
     float inv;
-    low_values<T, 16, kPieces>(a.part, a.scale, key, a.by_row && p < a.m ? a.pos[p] : p, sub, a.m, a.adapters, a.rank, a.splits, hi, lo, inv);
+    low_values<T, 16, kPieces>(a.part, a.scale, other, a.by_row && q0 < a.m ? a.pos[q0] : q0, sub, a.m, a.adapters,
+                               a.rank, a.splits, hi, lo, inv);
     if (sub == 0) back[r] = inv;
 #pragma unroll
     for (int q = 0; q < kPieces; ++q) {
@@ -513,54 +549,34 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
       }
     }
   }
-  const int p = p0 + ml;
-  const int key = p < a.m ? a.keys[p] : -1;  // -1: no row
-  const size_t row = static_cast<size_t>(p < a.m ? a.pos[p] : 0) * a.shard;
   __syncthreads();
 
-  const int chunk = strip * 4 + wave;
-  if (chunk >= a.chunks) return;
-  const int block = chunk / a.per_block, c0 = (chunk - block * a.per_block) * 64;
-  const int left = a.shard - c0;
-  const size_t at = static_cast<size_t>(block) * a.m * a.shard + c0;
-  const unsigned short *const wcol = a.w + (static_cast<size_t>(block) * a.shard + c0) * a.rank;
-  const size_t each = static_cast<size_t>(a.blocks) * a.shard * a.rank;
-  s16x8 yv[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    yv[h] = a.y && key >= 0 && h * 32 + 8 * g < left ? load8(a.y + at + row + h * 32 + 8 * g) : zero8();
   f32x4 res[4];
 #pragma unroll
   for (int v = 0; v < 4; ++v) res[v] = f32x4{0.f, 0.f, 0.f, 0.f};
   const unsigned short *const mine = low + ml * kRow;
-  unsigned todo = static_cast<unsigned>(__ballot(key >= 0 && key < a.adapters)) & 0xFFFF;
   while (todo) {
-    const int cur = __builtin_amdgcn_readlane(key, __builtin_ctz(todo));
-    todo &= ~static_cast<unsigned>(__ballot(key == cur));
-    const unsigned short *const wi = wcol + static_cast<size_t>(cur) * each;
     f32x4 acc[4];
 #pragma unroll
     for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int rc = 0; rc < (RANKS <= kRankChunk ? 1 : a.rank); rc += kRankChunk) {
-      s16x8 wf[4][KF];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int col = 32 * (v >> 1) + 8 * (ml >> 2) + 4 * (v & 1) + (ml & 3);
-#pragma unroll
-        for (int ks = 0; ks < KF; ++ks) {
-          const int r = kBoth ? 8 * (g & 1) : rc + ks * 32 + 8 * g;
-          wf[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
-        }
-      }
+    for (int rc = 0;;) {
       add_low<T, kBoth>(acc, wf, [&](int half, int ks) __attribute__((always_inline)) {
         return load8(mine + (kBoth ? 8 * g : half * RANKS + rc + ks * 32 + 8 * g));
       });
+      rc += kRankChunk;
+      if (RANKS <= kRankChunk || rc >= a.rank) break;
+      fragments(cur, rc);
     }
     const bool take = key == cur;
 #pragma unroll
     for (int v = 0; v < 4; ++v)
 #pragma unroll
       for (int e = 0; e < 4; ++e) res[v][e] = take ? acc[v][e] : res[v][e];
+    todo &= ~static_cast<unsigned>(__ballot(take));
+    if (todo) {
+      cur = __builtin_amdgcn_readlane(key, __builtin_ctz(todo));
+      fragments(cur, 0);
+    }
   }
   const bool has = key < a.adapters;
   if (key < 0 || (a.y == a.out && !has)) return;

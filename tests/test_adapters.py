@@ -236,6 +236,34 @@ def test_gradients(dtype, wide, tp, shard, hidden, m, n, rank, run):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("tp,shard,hidden,m,n,rank,run", [
+    (2, 328, 264, 300, 2, 40, 60), (1, 264, 72, 200, 1, 64, 200), (3, 520, 136, 513, 3, 24, 17), (2, 64, 520, 129, 2, 16, 9),
+    (4, 1000, 1032, 1100, 5, 64, 1), (1, 8, 8, 65, 1, 8, 65), (2, 2048, 264, 4100, 8, 48, 333)])
+def test_many_rows_of_few_adapters(dtype, tp, shard, hidden, m, n, rank, run):
+    """The second product that keeps its columns and goes through the rows."""
+    note(f"adapt stream {dtype} {tp} {shard} {hidden} {m} {n} {rank} {run}")
+    assert m > 64 and m // 64 >= n and rank <= 64
+    c = Case(dtype, tp, shard, hidden, m, n, rank, run=run, seed=2, sigma=0.5)
+    got = adapt(c.y.to(DEV), *c.on(DEV), tp, shard, **c.how(DEV))
+    c.check(got)
+    place = c.y.to(DEV)
+    adapt(place, *c.on(DEV), tp, shard, out=place, **c.how(DEV))
+    assert torch.equal(place, got)
+    c.check_grads(adapt_grad(c.y.to(DEV), *c.on(DEV), tp, shard, wide=True, **c.how(DEV)), c.y, True)
+
+
+@gpu
+def test_fp16_sums_of_the_smallest_values():
+    """g and u below fp16's and near fp32's smallest normal values still reach a wide gradient."""
+    note("adapt fp16 smallest")
+    c = Case("fp16", 1, 136, 264, 40, 2, 8, run=5, sigma=2.0 ** -13)
+    c.scale = torch.tensor([2.0 ** -100, 2.0 ** -101])
+    got = adapt_grad(c.y.to(DEV), *c.on(DEV), 1, 136, wide=True, need=(False, True, True), **c.how(DEV))
+    c.check_grads((None, *got[1:]), c.y, True, need=(False, True, True))
+
+
+@gpu
 @pytest.mark.parametrize("m", [5, 90])
 @pytest.mark.parametrize("index", [torch.int32, torch.int64])
 def test_index_types_and_no_scale(m, index):

@@ -234,8 +234,8 @@ def test_selection(dtype, requests, beams, keep, vocab, tp):
 @gpu
 @pytest.mark.parametrize("dtype,vecs", [("bf16", 1), ("bf16", 2), ("bf16", 4), ("fp32", 2), ("fp32", 4)])
 def test_selection_of_every_part_size(dtype, vecs):
-    # the part grows with rows x parts: 2048 workgroups, then 4096
-    rows = {1: 100, 2: 900, 4: 2000}[vecs]
+    # the part grows while rows x parts are more than 2048: 9, 5 and 3 parts of bf16, 17, 9 and 5 of fp32
+    rows = {1: 100, 2: 300 if dtype == "bf16" else 200, 4: 2000}[vecs]
     vocab = 8 * 2048 + 5
     note(f"select parts {dtype} {vecs}")
     z, s = rand((rows, vocab), vecs, dtype), rand((rows // 4, 4), 6)

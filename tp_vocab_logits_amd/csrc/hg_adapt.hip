@@ -33,19 +33,19 @@ __device__ __forceinline__ s16x8 load8(const unsigned short *p) {
 }
 __device__ __forceinline__ s16x8 zero8() { return s16x8{0, 0, 0, 0, 0, 0, 0, 0}; }
 
-// A power of two that brings `largest` to 1 .. 2 (1 for bf16, whose exponent
-// needs none), and its inverse. Nothing to scale: 1.
+// A power of two that brings `largest` to 1 .. 4 (1 for bf16, whose exponent needs
+// none), and its inverse.
+__device__ __forceinline__ uint32_t exponent(float largest) {
+  const uint32_t e = __builtin_bit_cast(uint32_t, largest) >> 23 & 255;
+  return e < 1 ? 1 : e > 253 ? 253 : e;
+}
 template <class T>
 __device__ __forceinline__ float to_unit(float largest) {
-  if constexpr (!T::kHalf) return 1.f;
-  const uint32_t e = __builtin_bit_cast(uint32_t, largest) >> 23 & 255;
-  return e == 0 || e > 250 ? 1.f : __builtin_bit_cast(float, (254 - e) << 23);
+  return T::kHalf ? __builtin_bit_cast(float, (254 - exponent(largest)) << 23) : 1.f;
 }
 template <class T>
 __device__ __forceinline__ float from_unit(float largest) {
-  if constexpr (!T::kHalf) return 1.f;
-  const uint32_t e = __builtin_bit_cast(uint32_t, largest) >> 23 & 255;
-  return e == 0 || e > 250 ? 1.f : __builtin_bit_cast(float, e << 23);
+  return T::kHalf ? __builtin_bit_cast(float, exponent(largest) << 23) : 1.f;
 }
 
 // f as upper + lower.
@@ -487,6 +487,7 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
   constexpr int kRow = 2 * RANKS + 8;  // 16-bit elements of an LDS row: upper, lower halves
   constexpr int kPieces = RANKS == 256 ? 2 : 1;
   constexpr int KF = kBoth ? 1 : 2;
+  constexpr int kBatch = kBoth ? 2 : 1;  // adapters whose fragments are loaded together
   __shared__ __align__(16) unsigned short low[16 * kRow];
   __shared__ float back[16];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
@@ -515,8 +516,9 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     yv[h] = a.y && key >= 0 && h * 32 + 8 * g < left ? load8(a.y + at + row + h * 32 + 8 * g) : zero8();
-  s16x8 wf[4][KF];
-  auto fragments = [&](int i, int rc) __attribute__((always_inline)) {
+  s16x8 wf[kBatch][4][KF];
+  int cur[kBatch];
+  auto fragments = [&](int i, int rc, s16x8 (&w)[4][KF]) __attribute__((always_inline)) {
     const unsigned short *const wi = wcol + static_cast<size_t>(i) * each;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
@@ -524,13 +526,23 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
 #pragma unroll
       for (int ks = 0; ks < KF; ++ks) {
         const int r = kBoth ? 8 * (g & 1) : rc + ks * 32 + 8 * g;
-        wf[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
+        w[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
       }
     }
   };
   unsigned todo = static_cast<unsigned>(__ballot(key >= 0 && key < a.adapters)) & 0xFFFF;
-  int cur = todo ? __builtin_amdgcn_readlane(key, __builtin_ctz(todo)) : -1;
-  if (todo) fragments(cur, 0);
+  auto begin = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      cur[n] = -1;
+      if (todo) {
+        cur[n] = __builtin_amdgcn_readlane(key, __builtin_ctz(todo));
+        todo &= ~static_cast<unsigned>(__ballot(key == cur[n]));
+        fragments(cur[n], 0, wf[n]);
+      }
+    }
+  };
+  begin();
 
   {
     const int r = tid / 16, sub = tid % 16, q0 = p0 + r;
@@ -555,28 +567,28 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
 #pragma unroll
   for (int v = 0; v < 4; ++v) res[v] = f32x4{0.f, 0.f, 0.f, 0.f};
   const unsigned short *const mine = low + ml * kRow;
-  while (todo) {
-    f32x4 acc[4];
+  while (cur[0] >= 0) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int rc = 0;;) {
-      add_low<T, kBoth>(acc, wf, [&](int half, int ks) __attribute__((always_inline)) {
-        return load8(mine + (kBoth ? 8 * g : half * RANKS + rc + ks * 32 + 8 * g));
-      });
-      rc += kRankChunk;
-      if (RANKS <= kRankChunk || rc >= a.rank) break;
-      fragments(cur, rc);
+    for (int n = 0; n < kBatch; ++n) {
+      if (cur[n] < 0) break;
+      f32x4 acc[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int rc = 0;;) {
+        add_low<T, kBoth>(acc, wf[n], [&](int half, int ks) __attribute__((always_inline)) {
+          return load8(mine + (kBoth ? 8 * g : half * RANKS + rc + ks * 32 + 8 * g));
+        });
+        rc += kRankChunk;
+        if (RANKS <= kRankChunk || rc >= a.rank) break;
+        fragments(cur[n], rc, wf[n]);
+      }
+      const bool take = key == cur[n];
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) res[v][e] = take ? acc[v][e] : res[v][e];
     }
-    const bool take = key == cur;
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) res[v][e] = take ? acc[v][e] : res[v][e];
-    todo &= ~static_cast<unsigned>(__ballot(take));
-    if (todo) {
-      cur = __builtin_amdgcn_readlane(key, __builtin_ctz(todo));
-      fragments(cur, 0);
-    }
+    begin();
   }
   const bool has = key < a.adapters;
   if (key < 0 || (a.y == a.out && !has)) return;

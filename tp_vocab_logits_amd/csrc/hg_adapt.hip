@@ -31,6 +31,9 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ s16x8 load8(const unsigned short *p) {
   return *reinterpret_cast<const s16x8 *>(p);
 }
+__device__ __forceinline__ s16x8 stream8(const unsigned short *p) {  // read once
+  return __builtin_nontemporal_load(reinterpret_cast<const s16x8 *>(p));
+}
 __device__ __forceinline__ s16x8 zero8() { return s16x8{0, 0, 0, 0, 0, 0, 0, 0}; }
 
 // A power of two that brings `largest` to 1 .. 4 (1 for bf16, whose exponent needs
@@ -140,13 +143,22 @@ __global__ __launch_bounds__(kThreads) void k_adapt_row(RowArgs a) {
 
 __device__ __align__(16) unsigned char kZeros[16];
 
+// PAST: past the caches, for a matrix that they cannot hold until it is read again
+// (dy of 1.3 GB: 33 us of 657; dy of 131 MB: 6 of 87 more).
+template <bool PAST = false>
 __device__ __forceinline__ void async16(const void *src, unsigned char *lds) {
   const uint32_t at = static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char *)lds));
-  __asm__ __volatile__("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                       :
-                       : "s"(at), "v"(src)
-                       : "memory");
+  if constexpr (PAST)
+    __asm__ __volatile__("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt"
+                         :
+                         : "s"(at), "v"(src)
+                         : "memory");
+  else
+    __asm__ __volatile__("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                         :
+                         : "s"(at), "v"(src)
+                         : "memory");
 }
 // The same for 4 bytes per lane.
 __device__ __forceinline__ void async4(const void *src, unsigned char *lds) {
@@ -186,7 +198,7 @@ struct LowArgs {
 
 constexpr int kLowRows = 128;
 
-template <class T, bool TURNED, int RB>
+template <class T, bool TURNED, int RB, bool PAST>
 __device__ __forceinline__ void low_products(const LowArgs &a, const LowSide &s, int id, unsigned char *lds) {
   static_assert(RB == 1 || RB == 4);
   constexpr int TT = 2;
@@ -248,7 +260,7 @@ __device__ __forceinline__ void low_products(const LowArgs &a, const LowSide &s,
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const bool real = lkey[q] == cur && lr.chunk[q & 1] * 8 < left;
-        async16(real ? static_cast<const void *>(src[q] + off) : kZeros, st + q * 1024);
+        async16<PAST>(real ? static_cast<const void *>(src[q] + off) : kZeros, st + q * 1024);
       }
       unsigned char *const sw = lds + stage * kStageAll + 4 * kWaveBytes + wave * 2048;
 #pragma unroll
@@ -343,16 +355,16 @@ __device__ __forceinline__ void low_products(const LowArgs &a, const LowSide &s,
 }
 
 // u's workgroups first (there are fewer), then g's.
-template <class T, int RB>
+template <class T, int RB, bool PAST>
 __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
   __shared__ __align__(1024) unsigned char lds[kStages * kStageAll];
   const int id = static_cast<int>(blockIdx.x);
   const int first = (a.m + kLowRows - 1) / kLowRows * a.x.splits;
   if (a.head && id == 0 && threadIdx.x < 2) a.head[threadIdx.x] = 0;
   if (id < first)
-    low_products<T, false, RB>(a, a.x, id, lds);
+    low_products<T, false, RB, false>(a, a.x, id, lds);
   else
-    low_products<T, true, RB>(a, a.y, id - first, lds);
+    low_products<T, true, RB, PAST>(a, a.y, id - first, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -481,7 +493,8 @@ struct UpArgs {
 };
 
 // RANKS: 16 (upper and lower halves share one fragment), 64, or 256: in turns of 64.
-template <class T, int RANKS>
+// APART: the tiles have adapters of their own, mostly.
+template <class T, int RANKS, bool APART>
 __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
   constexpr bool kBoth = RANKS == 16;
   constexpr int kRow = 2 * RANKS + 8;  // 16-bit elements of an LDS row: upper, lower halves
@@ -493,11 +506,20 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ml = lane & 15, g = lane >> 4;
-  // Row groups of one strip of columns go to one XCD (workgroups are dealt to the
-  // eight in turn): they share W's strip in its L2.
+  // Tiles that share adapters: one strip's go to one XCD (workgroups are dealt to the
+  // eight in turn) and find W's strip in its L2. Otherwise a tile's strips follow one
+  // another, so that W is read in longer runs, and past the caches (64 rows of 32
+  // adapters, V = 163840, rank 16: 43.5 us; through the caches 47.7, the other way 51).
   const int id = static_cast<int>(blockIdx.x);
-  const int eight = id / (8 * a.groups), in = id - eight * 8 * a.groups;
-  const int strip = eight * 8 + in % 8, group = in / 8;
+  int strip, group;
+  if constexpr (APART) {
+    group = id / a.strips;
+    strip = id - group * a.strips;
+  } else {
+    const int eight = id / (8 * a.groups), in = id - eight * 8 * a.groups;
+    strip = eight * 8 + in % 8;
+    group = in / 8;
+  }
   if (strip >= a.strips) return;
   const int p0 = group * 16;
   const int p = p0 + ml;
@@ -526,7 +548,9 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
 #pragma unroll
       for (int ks = 0; ks < KF; ++ks) {
         const int r = kBoth ? 8 * (g & 1) : rc + ks * 32 + 8 * g;
-        w[v][ks] = col < left && r < a.rank ? load8(wi + static_cast<size_t>(col) * a.rank + r) : zero8();
+        const unsigned short *const from = wi + static_cast<size_t>(col) * a.rank + r;
+        w[v][ks] = zero8();
+        if (col < left && r < a.rank) w[v][ks] = APART ? stream8(from) : load8(from);
       }
     }
   };
@@ -616,7 +640,7 @@ struct StreamArgs {
 };
 
 // RB: blocks of 16 ranks, 1 or 4.
-template <class T, int RB>
+template <class T, int RB, bool PAST>
 __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
   static_assert(RB == 1 || RB == 4);
   constexpr int KF = RB == 1 ? 1 : 2;
@@ -660,7 +684,7 @@ __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
     for (int q = 0; q < 4; ++q) {
       const int c = lr.chunk[q & 1] * 8;
       const bool real = a.y && p0 + 8 * q + lr.row < a.m && c < left;
-      async16(real ? static_cast<const void *>(a.y + at + static_cast<size_t>(row[q]) * a.shard + c) : kZeros,
+      async16<PAST>(real ? static_cast<const void *>(a.y + at + static_cast<size_t>(row[q]) * a.shard + c) : kZeros,
               st + q * 1024);
     }
     unsigned char *const sl = lds + stage * kStageAll + 4 * kWaveBytes + wave * 2048;
@@ -929,7 +953,7 @@ struct OuterArgs {
   OuterSide y, x;  // dB, dA
 };
 
-template <class T, bool TURNED, int RB>
+template <class T, bool TURNED, int RB, bool PAST>
 __device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSide &s, int id, unsigned char *lds) {
   static_assert(RB == 1 || RB == 4);
   constexpr int kPlaces = 4;  // steps' places at once, 256 bytes each, per wave
@@ -978,7 +1002,7 @@ __device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSi
     for (int q = 0; q < 4; ++q) {
       const int p = p0 + 8 * q + lc.row, c = lc.chunk[q & 1] * 8;
       const bool real = p >= from && p < to && c < left;
-      async16(real ? static_cast<const void *>(of + static_cast<size_t>(row[q]) * s.shard + c) : kZeros,
+      async16<PAST>(real ? static_cast<const void *>(of + static_cast<size_t>(row[q]) * s.shard + c) : kZeros,
               st + q * 1024);
     }
     // pieces of 16 ranks' 32 rows, a rank's four chunks swizzled by (rank >> 2) & 3
@@ -1074,14 +1098,14 @@ __device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSi
 }
 
 // dB's workgroups first, then dA's.
-template <class T, int RB>
+template <class T, int RB, bool PAST>
 __global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
   __shared__ __align__(1024) unsigned char lds[kStages * kStageAll + 4 * 4 * 256];
   const int id = static_cast<int>(blockIdx.x), first = a.y.strips * a.y.parts * a.adapters;
   if (id < first)
-    outer_products<T, true, RB>(a, a.y, id, lds);
+    outer_products<T, true, RB, PAST>(a, a.y, id, lds);
   else
-    outer_products<T, false, RB>(a, a.x, id - first, lds);
+    outer_products<T, false, RB, false>(a, a.x, id - first, lds);
 }
 
 // out = the sum of the parts, [n] each, n a multiple of 8.
@@ -1123,6 +1147,16 @@ using Int = std::integral_constant<int, V>;
 template <class F>
 void by_type(bool half, F f) {
   half ? f(TypeF16{}) : f(TypeBf16{});
+}
+// f(blocks of 16 ranks held at once, whether a matrix of m rows is read past the
+// caches: more than the 256 MB of the memory-side one).
+template <class F>
+void by_size(int rank, int m, const Blocked &of, F f) {
+  const bool past = of.p && 2ll * m * of.blocks * of.shard > (256ll << 20);
+  if (rank <= 16)
+    past ? f(Int<1>{}, Int<1>{}) : f(Int<1>{}, Int<0>{});
+  else
+    past ? f(Int<4>{}, Int<1>{}) : f(Int<4>{}, Int<0>{});
 }
 
 int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
@@ -1173,11 +1207,10 @@ hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocke
   const dim3 grid(static_cast<unsigned>(ceil_div(p.m, kLowRows)) * (args.x.splits + args.y.splits),
                   ceil_div(p.rank, kRankChunk));
   by_type(p.half, [&](auto type) {
-    using T = decltype(type);
-    if (p.rank <= 16)
-      hipLaunchKernelGGL((k_adapt_low<T, 1>), grid, dim3(kThreads), 0, s, args);
-    else
-      hipLaunchKernelGGL((k_adapt_low<T, 4>), grid, dim3(kThreads), 0, s, args);
+    by_size(p.rank, p.m, y, [&](auto rb, auto past) {
+      hipLaunchKernelGGL((k_adapt_low<decltype(type), decltype(rb)::value, decltype(past)::value != 0>), grid,
+                         dim3(kThreads), 0, s, args);
+    });
   });
   return hipGetLastError();
 }
@@ -1191,7 +1224,7 @@ hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *
   by_type(p.half, [&](auto type) {
     using T = decltype(type);
     if (adapt_streams(p.m, p.adapters, p.rank)) {
-      auto go = [&](auto rb) {
+      by_size(p.rank, p.m, y, [&](auto rb, auto past) {
         constexpr int RB = decltype(rb)::value;
         hipLaunchKernelGGL((k_adapt_values<T, RB * 16>), dim3(ceil_div(p.m, kThreads / (RB * 2))), dim3(kThreads), 0, s,
                            part, scale, r.keys, p.m, p.adapters, p.rank, splits, p.low, p.back);
@@ -1199,16 +1232,19 @@ hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *
                            chunks};
         // about 2048 workgroups, four rounds of two per CU, of two steps at least
         const int strips = ceil_div(chunks, 4), most = ceil_div(p.m, 64), want = ceil_div(2048, strips);
-        hipLaunchKernelGGL((k_adapt_stream<T, RB>), dim3(strips, want < most ? want : most), dim3(kThreads), 0, s, a);
-      };
-      p.rank <= 16 ? go(Int<1>{}) : go(Int<4>{});
+        hipLaunchKernelGGL((k_adapt_stream<T, RB, decltype(past)::value != 0>), dim3(strips, want < most ? want : most), dim3(kThreads), 0, s, a);
+      });
     } else {
       const int groups = ceil_div(p.m, 16), strips = ceil_div(chunks, 4);
       const UpArgs a{r.keys, r.pos, p.few, part, scale, wp, yp, op, p.m, p.adapters, p.rank, splits, y.blocks, y.shard, per, chunks,
                      groups, strips};
       auto go = [&](auto ranks) {
-        hipLaunchKernelGGL((k_adapt_up<T, decltype(ranks)::value>),
-                           dim3(static_cast<unsigned>(ceil_div(strips, 8)) * 8 * groups), dim3(kThreads), 0, s, a);
+        if (p.adapters >= groups)
+          hipLaunchKernelGGL((k_adapt_up<T, decltype(ranks)::value, true>), dim3(static_cast<unsigned>(strips) * groups),
+                             dim3(kThreads), 0, s, a);
+        else
+          hipLaunchKernelGGL((k_adapt_up<T, decltype(ranks)::value, false>),
+                             dim3(static_cast<unsigned>(ceil_div(strips, 8)) * 8 * groups), dim3(kThreads), 0, s, a);
       };
       p.rank <= 16 ? go(Int<16>{}) : p.rank <= kRankChunk ? go(Int<kRankChunk>{}) : go(Int<HG_MAX_RANK>{});
     }
@@ -1256,10 +1292,10 @@ hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Bloc
                   ceil_div(p.rank, kRankChunk));
   by_type(p.half, [&](auto type) {
     using T = decltype(type);
-    if (p.rank <= 16)
-      hipLaunchKernelGGL((k_adapt_outer<T, 1>), grid, dim3(kThreads), 0, s, a);
-    else
-      hipLaunchKernelGGL((k_adapt_outer<T, 4>), grid, dim3(kThreads), 0, s, a);
+    by_size(p.rank, p.m, y, [&](auto rb, auto past) {
+      hipLaunchKernelGGL((k_adapt_outer<T, decltype(rb)::value, decltype(past)::value != 0>), grid, dim3(kThreads), 0, s,
+                         a);
+    });
     auto sum = [&](const Blocked &of, int parts, const float *part, void *out) {
       if (!out || parts == 1) return;
       const size_t n = static_cast<size_t>(p.adapters) * p.rank * of.blocks * of.shard;

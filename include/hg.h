@@ -476,7 +476,8 @@ int hg_adapt_workspace(const hg_adapt_shape *s, int kind, size_t *bytes);
  * out may be y (rows without an adapter are then not written), and overlaps
  * nothing else. x: device [m][hidden]; a: device [adapters][rank][hidden]; b:
  * device [adapters][tp*shard][rank]; scale: device [adapters] fp32, or NULL for
- * ones; index: device [m]. Sums are fp32, the low-rank values are held to 2^-16
+ * ones; index: device [m]. An infinity or a NaN in x, an adapter or its scale
+ * makes what depends on it not finite, and nothing else. Sums are fp32, the low-rank values are held to 2^-16
  * of themselves (bf16) or 2^-21 of the row's largest (fp16), each result is
  * rounded once.
  * All pointers but scale and index 16-byte aligned. ws: device workspace,
@@ -499,8 +500,9 @@ int hg_adapt(const hg_adapt_shape *s, const void *y, const void *x, const void *
  *                                                  u_j = A_i x_j
  * da, db: in dtype, or fp32 if wide; zeros for an adapter that no row has. Each
  * of dx, da and db may be NULL and is then not computed, not all three. Sums are
- * fp32, over the rows in their order; g and u are held as in hg_adapt (fp16: to
- * 2^-21 of the call's largest). m == 0 zeroes da and db. The rest is as above.
+ * fp32, over the rows in their order; g and u are held as in hg_adapt (fp16: in
+ * da and db to 2^-21 of the largest among the adapter's rows). m == 0 zeroes da
+ * and db. The rest is as above.
  */
 int hg_adapt_grad(const hg_adapt_shape *s, const void *dy, const void *x, const void *a,
                   const void *b, const float *scale, const void *index, void *dx, void *da,

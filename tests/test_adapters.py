@@ -361,6 +361,25 @@ def test_fp16_of_any_size():
 
 
 @gpu
+@pytest.mark.parametrize("m,n,rank", [(60, 4, 8), (300, 3, 64), (1100, 40, 24)])
+def test_fp16_gradients_of_small_and_large_adapters(m, n, rank):
+    """Each adapter within what its own rows alone allow, the others' however large."""
+    note(f"adapt fp16 sizes {m} {n} {rank}")
+    c = Case("fp16", 2, 136, 264, m, n, rank, run=3)
+    c.scale = c.scale * 2.0 ** torch.tensor([8.0 if i % 2 else -14.0 for i in range(n)])
+    dx, da, db = adapt_grad(c.y.to(DEV), *c.on(DEV), 2, 136, wide=True, **c.how(DEV))
+    c.check_grads((dx, da, db), c.y, True)
+    dy, (x, a, b, index, scale) = c.flat(c.y), c.low()
+    for i in range(n):
+        rows = np.flatnonzero(index == i)
+        _, bounds = oa.adapt_grad_bound(dy[rows], x[rows], a[i:i + 1], b[i:i + 1], np.zeros(len(rows), int), scale[i:i + 1],
+                                        "fp16", "fp32")
+        wants = oa.adapt_grad(dy[rows], x[rows], a[i:i + 1], b[i:i + 1], np.zeros(len(rows), int), scale[i:i + 1])
+        for got, want, bound in zip((f64(da[i]), f64(db[i])), wants[1:], bounds[1:]):
+            assert (np.abs(got - want[0]) <= bound[0]).all(), (i, np.max(np.abs(got - want[0]) / (bound[0] + 1e-300)))
+
+
+@gpu
 @pytest.mark.parametrize("need", [(True, False, False), (False, True, False), (False, False, True), (True, True, False)])
 def test_gradients_that_are_not_needed(need):
     note(f"adapt need {need}")

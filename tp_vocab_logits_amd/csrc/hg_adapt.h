@@ -39,7 +39,7 @@ struct AdaptPlan {
   float *u, *g;          // [m][rank] scaled sums, by sorted position
   unsigned short *low;   // [m][2][16 or 64] their halves, where the second product streams
   float *back;           // [m] and fp16's factors
-  int *head;             // [0], [1]: bits of the largest |u| and |g|
+  int *head;             // [2][adapters]: bits of the largest |u| and |g| (fp16)
   int *seg;              // [adapters + 1] sorted positions where they begin
   unsigned short *ut, *gt;  // [2][ranks][padded] upper and lower halves of u and g
   unsigned short *at;    // [adapters][hidden][rank]: A turned
@@ -55,10 +55,10 @@ hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocke
 hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *part, int splits,
                            const float *scale, const void *w, const Blocked &y, void *out,
                            hipStream_t s);
-// u and g from their parts, scaled; their largest.
+// u and g from their parts, scaled; each adapter's largest.
 hipError_t launch_adapt_join(const AdaptPlan &p, const AdaptRows &r, const float *scale, hipStream_t s);
 // Their halves by rank (ut, gt) and A turned (at), those that are there.
-hipError_t launch_adapt_prepare(const AdaptPlan &p, const void *a, hipStream_t s);
+hipError_t launch_adapt_prepare(const AdaptPlan &p, const AdaptRows &r, const void *a, hipStream_t s);
 // da and db, those that are there: the sums over an adapter's rows, in parts of the
 // rows that are added up if there are several.
 hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Blocked &x, void *da, const Blocked &y,

@@ -192,7 +192,7 @@ struct LowSide {
 struct LowArgs {
   const int *keys, *pos;
   int m, adapters, rank;
-  int *head;     // cleared for the join, or NULL
+  int *head;     // [2][adapters], cleared for the join, or NULL
   LowSide x, y;  // u = A x, g = B^T dy
 };
 
@@ -360,7 +360,9 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
   __shared__ __align__(1024) unsigned char lds[kStages * kStageAll];
   const int id = static_cast<int>(blockIdx.x);
   const int first = (a.m + kLowRows - 1) / kLowRows * a.x.splits;
-  if (a.head && id == 0 && threadIdx.x < 2) a.head[threadIdx.x] = 0;
+  if (a.head && blockIdx.y == 0)
+    for (int k = id * kThreads + static_cast<int>(threadIdx.x); k < 2 * a.adapters; k += static_cast<int>(gridDim.x) * kThreads)
+      a.head[k] = 0;
   if (id < first)
     low_products<T, false, RB, false>(a, a.x, id, lds);
   else
@@ -802,7 +804,8 @@ __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
 // ---------------------------------------------------------------------------
 // The gradients' small pieces.
 
-// The parts' sums, scaled, and (fp16) their largest: blockIdx.y 0: u, 1: g.
+// The parts' sums, scaled, and (fp16) the largest of each adapter's: blockIdx.y 0: u,
+// 1: g. Four ranks of a row per thread.
 struct JoinSide {
   const float *part;
   float *sum;
@@ -813,60 +816,88 @@ __global__ __launch_bounds__(kThreads) void k_adapt_join(JoinSide u, JoinSide g,
                                                          const float *scale, int m, int adapters,
                                                          int rank, int *head) {
   const JoinSide side = blockIdx.y ? g : u;
+  if (!side.splits) return;
   const size_t n = static_cast<size_t>(m) * rank;
-  float largest = 0.f;
-  if (side.splits)
-    for (size_t k = (static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x) * 4; k < n;
-         k += static_cast<size_t>(gridDim.x) * kThreads * 4) {
-      const int key = keys[k / rank];  // (four ranks are of one row)
-      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-      if (key < adapters) {
-        for (int s0 = 0; s0 < side.splits; s0 += 8) {  // (eight loads in flight)
-          f32x4 v[8];
+  for (size_t k0 = static_cast<size_t>(blockIdx.x) * kThreads * 4; k0 < n;
+       k0 += static_cast<size_t>(gridDim.x) * kThreads * 4) {
+    const size_t k = k0 + threadIdx.x * 4;
+    const int key = k < n ? keys[k / rank] : adapters;
+    float largest = 0.f;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    if (key < adapters) {
+      for (int s0 = 0; s0 < side.splits; s0 += 8) {  // (eight loads in flight)
+        f32x4 v[8];
 #pragma unroll
-          for (int t = 0; t < 8; ++t)
-            if (s0 + t < side.splits) v[t] = *reinterpret_cast<const f32x4 *>(side.part + (s0 + t) * n + k);
+        for (int t = 0; t < 8; ++t)
+          if (s0 + t < side.splits) v[t] = *reinterpret_cast<const f32x4 *>(side.part + (s0 + t) * n + k);
 #pragma unroll
-          for (int t = 0; t < 8; ++t)
-            if (s0 + t < side.splits) sum += v[t];
-        }
-        const float f = scale ? scale[key] : 1.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sum[e] *= f;
-          const float size = fabsf(sum[e]);
-          if (size > largest && size < __builtin_inff()) largest = size;
-        }
+        for (int t = 0; t < 8; ++t)
+          if (s0 + t < side.splits) sum += v[t];
       }
-      *reinterpret_cast<f32x4 *>(side.sum + k) = sum;
-    }
-  if constexpr (T::kHalf) {
-    // The largest of all does not depend on the order. Thousands of atomics on one
-    // address took 25 us (4096 rows of 64 ranks): a workgroup's largest, if it is more
-    // than what is there.
-    __shared__ float waves[4];
+      const float f = scale ? scale[key] : 1.f;
 #pragma unroll
-    for (int d = 32; d; d >>= 1) largest = fmaxf(largest, __shfl_xor(largest, d));
-    if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = largest;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      const int bits = static_cast<int>(__builtin_bit_cast(
-          uint32_t, fmaxf(fmaxf(waves[0], waves[1]), fmaxf(waves[2], waves[3]))));
-      if (bits > __hip_atomic_load(head + blockIdx.y, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
-        atomicMax(head + blockIdx.y, bits);
+      for (int e = 0; e < 4; ++e) {
+        sum[e] *= f;
+        const float size = fabsf(sum[e]);
+        if (size > largest && size < __builtin_inff()) largest = size;
+      }
+    }
+    if (k < n) *reinterpret_cast<f32x4 *>(side.sum + k) = sum;
+    if constexpr (T::kHalf) {
+      // The largest of all does not depend on the order. Thousands of atomics on one
+      // address took 25 us (4096 rows of 64 ranks, one adapter): a workgroup's
+      // largest where it has one adapter, if it is more than what is there.
+      __shared__ float tops[4];
+      __shared__ int whose[4];  // adapters: none, or already done
+      auto note = [&](int i, float top) __attribute__((always_inline)) {
+        int *const to = head + static_cast<size_t>(blockIdx.y) * adapters + i;
+        const int bits = static_cast<int>(__builtin_bit_cast(uint32_t, top));
+        if (bits > __hip_atomic_load(to, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(to, bits);
+      };
+      const int first = __builtin_amdgcn_readfirstlane(key);  // (keys ascend, `adapters` comes last)
+      const bool one = __ballot(key != first && key < adapters) == 0;
+      if (one) {
+#pragma unroll
+        for (int d = 32; d; d >>= 1) largest = fmaxf(largest, __shfl_xor(largest, d));
+      } else if (key < adapters) {
+        note(key, largest);
+      }
+      if ((threadIdx.x & 63) == 0) {
+        tops[threadIdx.x >> 6] = largest;
+        whose[threadIdx.x >> 6] = one ? first : adapters;
+      }
+      __syncthreads();
+      if (threadIdx.x < 4 && whose[threadIdx.x] < adapters) {
+        const int w = static_cast<int>(threadIdx.x);
+        bool last = true;
+        float top = tops[w];
+        for (int o = 0; o < 4; ++o)
+          if (whose[o] == whose[w]) {
+            top = fmaxf(top, tops[o]);
+            if (o > w) last = false;
+          }
+        if (last) note(whose[w], top);
+      }
+      __syncthreads();
     }
   }
 }
 
 // low [m][rank] -> [2][rank][padded], upper and lower halves, zeros past m: 64 rows
-// of 32 ranks.
+// of 32 ranks. fp16: an adapter's largest at 1 .. 2, one factor for all of its rows,
+// which the sums over them take back.
 template <class T>
-__device__ __forceinline__ void turn_halves(const float *low, unsigned short *out, const int *largest, int m,
-                                            int rank, int padded, int p0, int r0, float (&t)[64][33]) {
-  const float unit = to_unit<T>(__builtin_bit_cast(float, *largest));
+__device__ __forceinline__ void turn_halves(const float *low, unsigned short *out, const int *largest, const int *keys,
+                                            int adapters, int m, int rank, int padded, int p0, int r0,
+                                            float (&t)[64][33]) {
   for (int k = static_cast<int>(threadIdx.x); k < 64 * 32; k += kThreads) {
     const int p = p0 + k / 32, r = r0 + k % 32;
-    t[k / 32][k % 32] = p < m && r < rank ? low[static_cast<size_t>(p) * rank + r] * unit : 0.f;
+    float v = p < m && r < rank ? low[static_cast<size_t>(p) * rank + r] : 0.f;
+    if (T::kHalf && p < m) {
+      const int key = keys[p];
+      v *= key < adapters ? to_unit<T>(__builtin_bit_cast(float, largest[key])) : 0.f;
+    }
+    t[k / 32][k % 32] = v;
   }
   __syncthreads();
   for (int k = static_cast<int>(threadIdx.x); k < 64 * 32; k += kThreads) {
@@ -904,7 +935,7 @@ struct PrepareArgs {
   const float *u, *g;
   unsigned short *ut, *gt, *at;
   const unsigned short *a;
-  const int *head, *seg;
+  const int *head, *seg, *keys;
   int m, rank, hidden, padded, adapters;
   int tiles, across, blocks;  // workgroups of one side's halves, of which per rank chunk; of an adapter's A
   int first, second;          // workgroups before g's halves, before A's
@@ -919,8 +950,8 @@ __global__ __launch_bounds__(kThreads) void k_adapt_prepare(PrepareArgs a) {
   if (id < a.second) {
     const bool g = id >= a.first;
     if (g) id -= a.first;
-    turn_halves<T>(g ? a.g : a.u, g ? a.gt : a.ut, a.head + g, a.m, a.rank, a.padded, id % a.across * 64,
-                   id / a.across * 32, t.f);
+    turn_halves<T>(g ? a.g : a.u, g ? a.gt : a.ut, a.head + (g ? a.adapters : 0), a.keys, a.adapters, a.m, a.rank,
+                   a.padded, id % a.across * 64, id / a.across * 32, t.f);
   } else {
     id -= a.second;
     const int i = id / a.blocks, block = id - i * a.blocks, wide = (a.hidden + 63) / 64;
@@ -940,7 +971,7 @@ __global__ __launch_bounds__(kThreads) void k_adapt_prepare(PrepareArgs a) {
 // places are loaded two steps before the rows.
 
 struct OuterSide {
-  const int *largest;
+  const int *largest;  // of each adapter's low-rank values (fp16)
   const unsigned short *of, *low;
   void *out;
   int blocks, shard, per_block, chunks;  // chunks of 64 columns
@@ -1071,7 +1102,7 @@ __device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSi
     multiply(k, stage);
     stage = stage + 1 < kStages ? stage + 1 : 0;
   }
-  const float inv = from_unit<T>(__builtin_bit_cast(float, *s.largest));
+  const float inv = T::kHalf ? from_unit<T>(__builtin_bit_cast(float, s.largest[i])) : 1.f;
   const size_t columns = static_cast<size_t>(s.blocks) * s.shard;
   const size_t col0 = static_cast<size_t>(block) * s.shard + c0;
 #pragma unroll
@@ -1263,8 +1294,8 @@ hipError_t launch_adapt_join(const AdaptPlan &p, const AdaptRows &r, const float
   return hipGetLastError();
 }
 
-hipError_t launch_adapt_prepare(const AdaptPlan &p, const void *a, hipStream_t s) {
-  PrepareArgs args{p.u, p.g, p.ut, p.gt, p.at, static_cast<const unsigned short *>(a), p.head, p.seg, p.m, p.rank,
+hipError_t launch_adapt_prepare(const AdaptPlan &p, const AdaptRows &r, const void *a, hipStream_t s) {
+  PrepareArgs args{p.u, p.g, p.ut, p.gt, p.at, static_cast<const unsigned short *>(a), p.head, p.seg, r.keys, p.m, p.rank,
                    p.hidden, p.padded, p.adapters, 0, 0, 0, 0, 0};
   args.across = ceil_div(p.padded, 64);
   args.tiles = args.across * ceil_div(p.rank, 32);
@@ -1287,7 +1318,7 @@ hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Bloc
                      of.shard, per, chunks, ceil_div(chunks, 4), out ? parts : 0, wide || parts > 1};
   };
   const OuterArgs a{r.pos, p.seg, p.m, p.adapters, p.rank, p.padded, side(y, p.head, p.ut, p.parts_b, p.pb, db),
-                    side(x, p.head + 1, p.gt, p.parts_a, p.pa, da)};
+                    side(x, p.head + p.adapters, p.gt, p.parts_a, p.pa, da)};
   const dim3 grid(static_cast<unsigned>(a.y.strips * a.y.parts + a.x.strips * a.x.parts) * p.adapters,
                   ceil_div(p.rank, kRankChunk));
   by_type(p.half, [&](auto type) {

@@ -83,7 +83,7 @@ size_t lay_out(const hg_adapt_shape &s, int kind, char *ws, AdaptPlan *p) {
   p->pg = floats(low * p->split_g);
   p->u = floats(low);
   p->g = floats(low);
-  p->head = reinterpret_cast<int *>(take(8));
+  if (p->half) p->head = reinterpret_cast<int *>(take(8 * static_cast<size_t>(s.adapters)));
   p->seg = reinterpret_cast<int *>(take(4 * (static_cast<size_t>(s.adapters) + 1)));
   p->padded = static_cast<int>(ceil_div(s.m + 8, 32) * 32);  // (eight are read at once from any row on)
   p->ut = reinterpret_cast<unsigned short *>(take(4 * static_cast<size_t>(s.rank) * p->padded));
@@ -222,7 +222,7 @@ HG_API int hg_adapt_grad(const hg_adapt_shape *s, const void *dy, const void *x,
   if (!dx) p.at = nullptr;
   HIP_TRY(hg::launch_adapt_low(p, rows, p.u ? wide_x : none, a, p.g ? wide_y : none, b, st));
   HIP_TRY(hg::launch_adapt_join(p, rows, scale, st));
-  HIP_TRY(hg::launch_adapt_prepare(p, a, st));
+  HIP_TRY(hg::launch_adapt_prepare(p, rows, a, st));
   if (da || db) HIP_TRY(hg::launch_adapt_outer(p, rows, wide_x, da, wide_y, db, wide != 0, st));
   if (dx) HIP_TRY(hg::launch_adapt_up(p, rows, p.g, 1, nullptr, p.at, Blocked{nullptr, 1, s->hidden}, dx, st));
   return HG_OK;

@@ -182,6 +182,13 @@ constexpr int kStageAll = 4 * kWaveBytes + kSubBytes;  // four waves' and 8 KB t
 // what the rows themselves take; up to 16 ranks (2 KB) every wave loads its own
 // and none waits for another. w's columns are next to each other in memory (A), or,
 // if TURNED, its ranks are (B): those are turned while they are read from LDS.
+//
+// The workgroups of a split follow one another on one XCD, whose L2 then has w's
+// part for all of them, and each begins at a place of its own in the split's columns:
+// rows are a power of two times a small number apart, and at one column they would
+// all be on a few of the memory's channels. 4096 rows of 163840 columns, rank 64, two
+// adapters, gradients: 630 us with neither, 642 with the first alone, 627 with the
+// second alone (a step apart), 606 with both.
 
 struct LowSide {
   const unsigned short *of, *w;
@@ -314,8 +321,13 @@ __device__ __forceinline__ void low_products(const LowArgs &a, const LowSide &s,
         }
     };
     const int n = to - from;
-    if (n > 0) issue(from, 0);
-    if (n > 1) issue(from + 1, 1);
+    const int turn = static_cast<int>(static_cast<long long>(n) * group / groups);
+    auto chunk_of = [&](int k) __attribute__((always_inline)) {
+      k += turn;
+      return from + (k < n ? k : k - n);
+    };
+    if (n > 0) issue(chunk_of(0), 0);
+    if (n > 1) issue(chunk_of(1), 1);
     int stage = 0;
     for (int k = 0; k < n; ++k) {
       // this step has landed, and the last one's reads are done, here and (RB > 1) in
@@ -328,7 +340,7 @@ __device__ __forceinline__ void low_products(const LowArgs &a, const LowSide &s,
         tile_barrier();
       else
         __asm__ __volatile__("" ::: "memory");
-      if (k + 2 < n) issue(from + k + 2, stage >= 1 ? stage - 1 : kStages - 1);
+      if (k + 2 < n) issue(chunk_of(k + 2), stage >= 1 ? stage - 1 : kStages - 1);
       multiply(stage);
       stage = stage + 1 < kStages ? stage + 1 : 0;
     }
@@ -363,10 +375,15 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
   if (a.head && blockIdx.y == 0)
     for (int k = id * kThreads + static_cast<int>(threadIdx.x); k < 2 * a.adapters; k += static_cast<int>(gridDim.x) * kThreads)
       a.head[k] = 0;
+  // consecutive workgroups go to the eight XCDs in turn: each XCD's are a run
+  auto in_runs = [](int k, int all) __attribute__((always_inline)) {
+    const int each = all / 8;
+    return k < each * 8 ? k % 8 * each + k / 8 : k;
+  };
   if (id < first)
-    low_products<T, false, RB, false>(a, a.x, id, lds);
+    low_products<T, false, RB, false>(a, a.x, in_runs(id, first), lds);
   else
-    low_products<T, true, RB, PAST>(a, a.y, id - first, lds);
+    low_products<T, true, RB, PAST>(a, a.y, in_runs(id - first, static_cast<int>(gridDim.x) - first), lds);
 }
 
 // ---------------------------------------------------------------------------

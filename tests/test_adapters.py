@@ -361,7 +361,7 @@ def test_fp16_of_any_size():
 
 
 @gpu
-@pytest.mark.parametrize("m,n,rank", [(60, 4, 8), (300, 3, 64), (1100, 40, 24)])
+@pytest.mark.parametrize("m,n,rank", [(40, 4, 32), (40, 4, 40), (56, 3, 24), (57, 4, 8), (300, 3, 64), (1100, 40, 24)])
 def test_fp16_gradients_of_small_and_large_adapters(m, n, rank):
     """Each adapter within what its own rows alone allow, the others' however large."""
     note(f"adapt fp16 sizes {m} {n} {rank}")
@@ -377,6 +377,15 @@ def test_fp16_gradients_of_small_and_large_adapters(m, n, rank):
         wants = oa.adapt_grad(dy[rows], x[rows], a[i:i + 1], b[i:i + 1], np.zeros(len(rows), int), scale[i:i + 1])
         for got, want, bound in zip((f64(da[i]), f64(db[i])), wants[1:], bounds[1:]):
             assert (np.abs(got - want[0]) <= bound[0]).all(), (i, np.max(np.abs(got - want[0]) / (bound[0] + 1e-300)))
+
+
+@gpu
+@pytest.mark.parametrize("need", [(True, False, False), (False, True, False), (False, False, True)])
+@pytest.mark.parametrize("dtype,m,rank", [("fp16", 30, 16), ("fp16", 30, 72), ("bf16", 30, 16)])
+def test_gradients_of_few_rows_that_are_not_needed(dtype, m, rank, need):
+    note(f"adapt need {dtype} {m} {rank} {need}")
+    c = Case(dtype, 2, 136, 264, m, 4, rank, run=2)
+    c.check_grads(adapt_grad(c.y.to(DEV), *c.on(DEV), 2, 136, need=need, **c.how(DEV)), c.y, need=need)
 
 
 @gpu

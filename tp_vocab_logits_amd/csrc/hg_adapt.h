@@ -57,8 +57,9 @@ hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *
                            hipStream_t s);
 // u and g from their parts, scaled; each adapter's largest.
 hipError_t launch_adapt_join(const AdaptPlan &p, const AdaptRows &r, const float *scale, hipStream_t s);
-// Their halves by rank (ut, gt) and A turned (at), those that are there.
-hipError_t launch_adapt_prepare(const AdaptPlan &p, const AdaptRows &r, const void *a, hipStream_t s);
+// The same and their halves by rank (ut, gt), and A turned (at), those that are there.
+hipError_t launch_adapt_prepare(const AdaptPlan &p, const AdaptRows &r, const float *scale, const void *a,
+                                hipStream_t s);
 // da and db, those that are there: the sums over an adapter's rows, in parts of the
 // rows that are added up if there are several.
 hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Blocked &x, void *da, const Blocked &y,

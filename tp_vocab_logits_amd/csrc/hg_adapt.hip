@@ -821,6 +821,21 @@ __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
 // ---------------------------------------------------------------------------
 // The gradients' small pieces.
 
+// Four values' sums over the parts, [splits][n], at k.
+__device__ __forceinline__ f32x4 sum_parts(const float *part, int splits, size_t n, size_t k) {
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < splits; s0 += 8) {  // (eight loads in flight)
+    f32x4 v[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      if (s0 + t < splits) v[t] = *reinterpret_cast<const f32x4 *>(part + (s0 + t) * n + k);
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      if (s0 + t < splits) sum += v[t];
+  }
+  return sum;
+}
+
 // The parts' sums, scaled, and (fp16) the largest of each adapter's: blockIdx.y 0: u,
 // 1: g. Four ranks of a row per thread.
 struct JoinSide {
@@ -842,15 +857,7 @@ __global__ __launch_bounds__(kThreads) void k_adapt_join(JoinSide u, JoinSide g,
     float largest = 0.f;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     if (key < adapters) {
-      for (int s0 = 0; s0 < side.splits; s0 += 8) {  // (eight loads in flight)
-        f32x4 v[8];
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-          if (s0 + t < side.splits) v[t] = *reinterpret_cast<const f32x4 *>(side.part + (s0 + t) * n + k);
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-          if (s0 + t < side.splits) sum += v[t];
-      }
+      sum = sum_parts(side.part, side.splits, n, k);
       const float f = scale ? scale[key] : 1.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -900,30 +907,87 @@ __global__ __launch_bounds__(kThreads) void k_adapt_join(JoinSide u, JoinSide g,
   }
 }
 
-// low [m][rank] -> [2][rank][padded], upper and lower halves, zeros past m: 64 rows
-// of 32 ranks. fp16: an adapter's largest at 1 .. 2, one factor for all of its rows,
-// which the sums over them take back.
-template <class T>
-__device__ __forceinline__ void turn_halves(const float *low, unsigned short *out, const int *largest, const int *keys,
-                                            int adapters, int m, int rank, int padded, int p0, int r0,
-                                            float (&t)[64][33]) {
-  for (int k = static_cast<int>(threadIdx.x); k < 64 * 32; k += kThreads) {
-    const int p = p0 + k / 32, r = r0 + k % 32;
-    float v = p < m && r < rank ? low[static_cast<size_t>(p) * rank + r] : 0.f;
-    if (T::kHalf && p < m) {
-      const int key = keys[p];
-      v *= key < adapters ? to_unit<T>(__builtin_bit_cast(float, largest[key])) : 0.f;
-    }
-    t[k / 32][k % 32] = v;
-  }
+// low [m][rank] -> turned [2][rank][padded], upper and lower halves, zeros past m: 64
+// rows of 32 ranks. fp16: an adapter's largest at 1 .. 2, one factor for all of its
+// rows, which the sums over them take back.
+struct TurnSide {
+  const float *part;  // JOIN: the parts, of which `splits`, and where their scaled sums
+  int splits;         // go (or NULL)
+  float *low;         // otherwise: those
+  unsigned short *turned;  // (or NULL: the sums alone)
+  int *largest;            // [adapters]
+};
+struct TurnLds {
+  float t[64][33];
+  float of_row[64];
+  int key[64];
+};
+// JOIN: the parts are added up here, a launch less than by k_adapt_join before it
+// (gradients of 2047 rows of 32000 columns, 8 adapters: 80 us instead of 82; 33 rows of
+// 4096: 32.6 instead of 34). fp16 knows its factors then only if the tile has all rows
+// and ranks.
+template <class T, bool JOIN>
+__device__ __forceinline__ void turn_halves(const TurnSide &s, const int *keys, const float *scale, int adapters, int m,
+                                            int rank, int padded, int p0, int r0, TurnLds &l) {
+  const int tid = static_cast<int>(threadIdx.x);
+  if (tid < 64) l.key[tid] = p0 + tid < m ? keys[p0 + tid] : adapters;
   __syncthreads();
-  for (int k = static_cast<int>(threadIdx.x); k < 64 * 32; k += kThreads) {
+  for (int k = tid; k < 64 * 8; k += kThreads) {
+    const int row = k / 8, e = k % 8 * 4, p = p0 + row, r = r0 + e, key = l.key[row];
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (p < m && r < rank) {  // (four ranks are there or not)
+      const size_t at = static_cast<size_t>(p) * rank + r;
+      if constexpr (JOIN) {
+        if (key < adapters) {
+          v = sum_parts(s.part, s.splits, static_cast<size_t>(m) * rank, at);
+          const float f = scale ? scale[key] : 1.f;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[t] *= f;
+        }
+        if (s.low) *reinterpret_cast<f32x4 *>(s.low + at) = v;
+      } else {
+        v = *reinterpret_cast<const f32x4 *>(s.low + at);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) l.t[row][e + t] = v[t];
+  }
+  if (JOIN && !s.turned) return;
+  __syncthreads();
+  if constexpr (T::kHalf) {
+    if constexpr (JOIN) {
+      if (tid < 64) {
+        float top = 0.f;
+        for (int e = 0; e < 32; ++e) {
+          const float size = fabsf(l.t[tid][e]);
+          if (size > top && size < __builtin_inff()) top = size;
+        }
+        l.of_row[tid] = top;
+      }
+      __syncthreads();
+    }
+    float top = 0.f;
+    if (tid < 64) {
+      const int key = l.key[tid];
+      if constexpr (JOIN) {
+        for (int o = 0; o < 64; ++o)
+          if (l.key[o] == key) top = fmaxf(top, l.of_row[o]);
+        if (key < adapters) s.largest[key] = static_cast<int>(__builtin_bit_cast(uint32_t, top));
+      } else if (key < adapters) {
+        top = __builtin_bit_cast(float, s.largest[key]);
+      }
+    }
+    __syncthreads();
+    if (tid < 64) l.of_row[tid] = to_unit<T>(top);
+    __syncthreads();
+  }
+  for (int k = tid; k < 64 * 32; k += kThreads) {
     const int p = p0 + k % 64, r = r0 + k / 64;
     if (p >= padded || r >= rank) continue;
     uint32_t hi, lo;
-    halves<T>(t[k % 64][k / 64], hi, lo);
-    out[static_cast<size_t>(r) * padded + p] = static_cast<unsigned short>(hi);
-    out[static_cast<size_t>(rank + r) * padded + p] = static_cast<unsigned short>(lo);
+    halves<T>(T::kHalf ? l.t[k % 64][k / 64] * l.of_row[k % 64] : l.t[k % 64][k / 64], hi, lo);
+    s.turned[static_cast<size_t>(r) * padded + p] = static_cast<unsigned short>(hi);
+    s.turned[static_cast<size_t>(rank + r) * padded + p] = static_cast<unsigned short>(lo);
   }
 }
 
@@ -949,26 +1013,27 @@ __device__ __forceinline__ void turn_block(const unsigned short *a, unsigned sho
 // What the gradients' wide products take, in one launch: the halves of u and g by
 // rank, and A turned, for the adapters that have rows.
 struct PrepareArgs {
-  const float *u, *g;
-  unsigned short *ut, *gt, *at;
+  TurnSide u, g;
+  unsigned short *at;
   const unsigned short *a;
-  const int *head, *seg, *keys;
+  const int *seg, *keys;
+  const float *scale;
   int m, rank, hidden, padded, adapters;
   int tiles, across, blocks;  // workgroups of one side's halves, of which per rank chunk; of an adapter's A
   int first, second;          // workgroups before g's halves, before A's
 };
-template <class T>
+template <class T, bool JOIN>
 __global__ __launch_bounds__(kThreads) void k_adapt_prepare(PrepareArgs a) {
   __shared__ union {
-    float f[64][33];
+    TurnLds f;
     __align__(16) unsigned short h[64][72];
   } t;
   int id = static_cast<int>(blockIdx.x);
   if (id < a.second) {
     const bool g = id >= a.first;
     if (g) id -= a.first;
-    turn_halves<T>(g ? a.g : a.u, g ? a.gt : a.ut, a.head + (g ? a.adapters : 0), a.keys, a.adapters, a.m, a.rank,
-                   a.padded, id % a.across * 64, id / a.across * 32, t.f);
+    turn_halves<T, JOIN>(g ? a.g : a.u, a.keys, a.scale, a.adapters, a.m, a.rank, a.padded, id % a.across * 64,
+                         id / a.across * 32, t.f);
   } else {
     id -= a.second;
     const int i = id / a.blocks, block = id - i * a.blocks, wide = (a.hidden + 63) / 64;
@@ -1311,18 +1376,39 @@ hipError_t launch_adapt_join(const AdaptPlan &p, const AdaptRows &r, const float
   return hipGetLastError();
 }
 
-hipError_t launch_adapt_prepare(const AdaptPlan &p, const AdaptRows &r, const void *a, hipStream_t s) {
-  PrepareArgs args{p.u, p.g, p.ut, p.gt, p.at, static_cast<const unsigned short *>(a), p.head, p.seg, r.keys, p.m, p.rank,
-                   p.hidden, p.padded, p.adapters, 0, 0, 0, 0, 0};
+hipError_t launch_adapt_prepare(const AdaptPlan &p, const AdaptRows &r, const float *scale, const void *a,
+                                hipStream_t s) {
+  const bool join = !p.half || (p.padded <= 64 && p.rank <= 32);
+  if (!join) {
+    const hipError_t e = launch_adapt_join(p, r, scale, s);
+    if (e != hipSuccess) return e;
+  }
+  PrepareArgs args{};
+  // (u itself goes nowhere else, g to dx)
+  args.u = TurnSide{p.pu, p.split_u, join ? nullptr : p.u, p.ut, p.head};
+  args.g = TurnSide{p.pg, p.split_g, join && !p.at ? nullptr : p.g, p.gt, p.half ? p.head + p.adapters : nullptr};
+  args.at = p.at;
+  args.a = static_cast<const unsigned short *>(a);
+  args.seg = p.seg;
+  args.keys = r.keys;
+  args.scale = scale;
+  args.m = p.m;
+  args.rank = p.rank;
+  args.hidden = p.hidden;
+  args.padded = p.padded;
+  args.adapters = p.adapters;
   args.across = ceil_div(p.padded, 64);
   args.tiles = args.across * ceil_div(p.rank, 32);
   args.blocks = ceil_div(p.hidden, 64) * ceil_div(p.rank, 64);
   args.first = p.ut ? args.tiles : 0;
-  args.second = args.first + (p.gt ? args.tiles : 0);
+  args.second = args.first + (p.gt || (join && p.g) ? args.tiles : 0);
   const int all = args.second + (p.at ? args.blocks * p.adapters : 0);
-  if (all == 0) return hipSuccess;
   by_type(p.half, [&](auto type) {
-    hipLaunchKernelGGL((k_adapt_prepare<decltype(type)>), dim3(all), dim3(kThreads), 0, s, args);
+    using T = decltype(type);
+    if (join)
+      hipLaunchKernelGGL((k_adapt_prepare<T, true>), dim3(all), dim3(kThreads), 0, s, args);
+    else
+      hipLaunchKernelGGL((k_adapt_prepare<T, false>), dim3(all), dim3(kThreads), 0, s, args);
   });
   return hipGetLastError();
 }

@@ -149,7 +149,9 @@ def adapted(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, 
             shard: int, scale: torch.Tensor | None = None) -> torch.Tensor:
     """:func:`adapt` into a new tensor, differentiable in ``y``, ``x``, ``a`` and
     ``b``. Only the inputs are kept for the backward pass, which computes the
-    gradients of those that require one; ``scale`` is a constant."""
+    gradients of those that require one; ``scale`` is a constant. As with any
+    operator, results that an eager call left must be let go before a backward
+    pass of the same leaves is captured: torch cannot capture it otherwise."""
     if scale is not None and scale.requires_grad:
         raise ValueError("adapted has no gradient for scale: it must not require one")
     return _Adapted.apply(y, x, a, b, index, tp, shard, scale)

@@ -81,7 +81,8 @@ def beam_select(logits, scores: torch.Tensor, keep: int, vocab: int | None = Non
 
     ``logits`` are gathered rows ``[requests * beams, vocab]`` or the product's
     shards ``[tp, requests * beams, shard]`` (or tp blocks), BF16, FP16 or FP32;
-    the softmax runs over the first ``vocab`` entries (default: all). ``scores``
+    the softmax runs over the first ``vocab`` entries (default: all), ``scale`` is
+    taken as fp32. ``scores``
     is ``[requests, beams]`` fp32, minus infinity (or any other value that is not
     finite) for a beam that is not there, such as all but one at the start. Equal
     candidates go by beam, then token; sums and order are in 64 bits.

@@ -8,10 +8,10 @@
 // written, dy, B, dB. The products run on the matrix cores all the same
 // (v_mfma_f32_16x16x32, tiles of 16 rows), so that nothing else comes near.
 //
-// Rows. A tile is 16 rows next to each other, sorted by adapter. A tile with rows of several adapters runs through each of them and
-// every row takes its own one's result: no tile lists, y passes once whatever the
-// mixture, and no value of one adapter (an infinity in its B) reaches the rows of
-// another.
+// Rows. A tile is 16 rows next to each other, sorted by adapter. A tile with rows of
+// several adapters runs through each of them and every row takes its own one's
+// result: no tile lists, y passes once whatever the mixture, and no value of one
+// adapter (an infinity in its B) reaches the rows of another.
 //
 // Precision. u and g are fp32 sums that enter a second product of 16-bit operands.
 // They enter as the sum of two 16-bit numbers, so that what is lost is 2^-16 of
@@ -62,7 +62,8 @@ __device__ __forceinline__ void halves(float f, uint32_t &hi, uint32_t &lo) {
 // ---------------------------------------------------------------------------
 // Few rows: u of one row, or a part of it, per workgroup. A lane holds 8 elements
 // of x and meets them with those of each rank's row of A. The last workgroup sorts
-// the rows by adapter meanwhile (up to 64: a lane each).
+// the rows by adapter meanwhile (up to 64: a lane each). Latency: 3.7 us for one row,
+// 5.2 for 64 (hidden 7168, rank 16, 32 adapters).
 
 struct RowArgs {
   const void *index;
@@ -188,7 +189,8 @@ constexpr int kStageAll = 4 * kWaveBytes + kSubBytes;  // four waves' and 8 KB t
 // rows are a power of two times a small number apart, and at one column they would
 // all be on a few of the memory's channels. 4096 rows of 163840 columns, rank 64, two
 // adapters, gradients: 630 us with neither, 642 with the first alone, 627 with the
-// second alone (a step apart), 606 with both.
+// second alone (a step apart), 606 with both. This kernel's part of it is 255 to 295
+// us, 4.6 to 5.3 TB/s of dy: HBM bounds it, A and B come on top (a tenth).
 
 struct LowSide {
   const unsigned short *of, *w;
@@ -373,7 +375,8 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
   const int id = static_cast<int>(blockIdx.x);
   const int first = (a.m + kLowRows - 1) / kLowRows * a.x.splits;
   if (a.head && blockIdx.y == 0)
-    for (int k = id * kThreads + static_cast<int>(threadIdx.x); k < 2 * a.adapters; k += static_cast<int>(gridDim.x) * kThreads)
+    for (int k = id * kThreads + static_cast<int>(threadIdx.x); k < 2 * a.adapters;
+         k += static_cast<int>(gridDim.x) * kThreads)
       a.head[k] = 0;
   // consecutive workgroups go to the eight XCDs in turn: each XCD's are a run
   auto in_runs = [](int k, int all) __attribute__((always_inline)) {
@@ -446,7 +449,7 @@ __device__ __forceinline__ void low_values(const float *part, const float *scale
 }
 
 // All rows' values by sorted position: [m][2][RANKS] (16 or 64 ranks, zeros past
-// `rank`), and fp16's factors back.
+// `rank`), and fp16's factors back. (2047 rows of 64 ranks in 28 parts: 6.6 us.)
 template <class T, int RANKS>
 __global__ __launch_bounds__(kThreads) void k_adapt_values(const float *part, const float *scale, const int *keys,
                                                            int m, int adapters, int rank, int splits,
@@ -469,7 +472,8 @@ __global__ __launch_bounds__(kThreads) void k_adapt_values(const float *part, co
 // rows and 64 columns for each of its four waves. A lane of a tile holds one row's
 // 8 + 8 columns: the rows of W are dealt to the matrix cores' rows so that these are
 // next to each other (stores of 64 bytes per row). For few rows, and for rows of
-// many adapters.
+// many adapters. 64 rows of 32 adapters (V = 163840, rank 16): 36 to 38 us for 190 MB,
+// 5.1 TB/s where a copy reaches 4.8, most of it W read once.
 
 // acc += W's fragments x a row's values, given by read(half, ks); BOTH: the two halves
 // of up to 16 ranks are one fragment.
@@ -647,8 +651,8 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
 // wave), and with them W's fragments, and goes through the rows, or a part of them,
 // 32 at a time, y and the low-rank values loaded straight into LDS as above. The
 // first form reads W's 8 KB for every 16 rows of 64 columns (2 KB); with 64 rows it
-// still took 365 us where the copy of y alone takes 295 (2047 rows, V = 163840,
-// rank 64).
+// still took 365 us; this one takes 313, 4.3 TB/s of y read and written, where a copy
+// reaches 4.8 (2047 rows, V = 163840, rank 64).
 
 struct StreamArgs {
   const int *keys, *pos;
@@ -703,8 +707,9 @@ __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
     for (int q = 0; q < 4; ++q) {
       const int c = lr.chunk[q & 1] * 8;
       const bool real = a.y && p0 + 8 * q + lr.row < a.m && c < left;
-      async16<PAST>(real ? static_cast<const void *>(a.y + at + static_cast<size_t>(row[q]) * a.shard + c) : kZeros,
-              st + q * 1024);
+      async16<PAST>(
+          real ? static_cast<const void *>(a.y + at + static_cast<size_t>(row[q]) * a.shard + c) : kZeros,
+          st + q * 1024);
     }
     unsigned char *const sl = lds + stage * kStageAll + 4 * kWaveBytes + wave * 2048;
 #pragma unroll
@@ -1050,7 +1055,10 @@ __global__ __launch_bounds__(kThreads) void k_adapt_prepare(PrepareArgs a) {
 // through the rows, or a part of them, 32 at a time, as above: the waves share the
 // rows' low-rank values (half of the bytes that their own columns take; up to 16
 // ranks each loads its own), of is turned while it is read from LDS. The rows'
-// places are loaded two steps before the rows.
+// places are loaded two steps before the rows. dB and dA of 4096 rows (V = 163840,
+// hidden 7168, rank 64, two adapters): 280 to 300 us for 1.45 GB, 5.0 TB/s; 1336 equal
+// workgroups on 512 places are 2.6 rounds. Neighbouring columns on one XCD: 25 us
+// slower.
 
 struct OuterSide {
   const int *largest;  // of each adapter's low-rank values (fp16)
@@ -1116,7 +1124,7 @@ __device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSi
       const int p = p0 + 8 * q + lc.row, c = lc.chunk[q & 1] * 8;
       const bool real = p >= from && p < to && c < left;
       async16<PAST>(real ? static_cast<const void *>(of + static_cast<size_t>(row[q]) * s.shard + c) : kZeros,
-              st + q * 1024);
+                    st + q * 1024);
     }
     // pieces of 16 ranks' 32 rows, a rank's four chunks swizzled by (rank >> 2) & 3
     unsigned char *const sl = lds + stage * kStageAll + 4 * kWaveBytes + wave * 2048;
@@ -1345,12 +1353,13 @@ hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *
                            chunks};
         // about 2048 workgroups, four rounds of two per CU, of two steps at least
         const int strips = ceil_div(chunks, 4), most = ceil_div(p.m, 64), want = ceil_div(2048, strips);
-        hipLaunchKernelGGL((k_adapt_stream<T, RB, decltype(past)::value != 0>), dim3(strips, want < most ? want : most), dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((k_adapt_stream<T, RB, decltype(past)::value != 0>),
+                           dim3(strips, want < most ? want : most), dim3(kThreads), 0, s, a);
       });
     } else {
       const int groups = ceil_div(p.m, 16), strips = ceil_div(chunks, 4);
-      const UpArgs a{r.keys, r.pos, p.few, part, scale, wp, yp, op, p.m, p.adapters, p.rank, splits, y.blocks, y.shard, per, chunks,
-                     groups, strips};
+      const UpArgs a{r.keys, r.pos, p.few, part, scale, wp, yp, op, p.m, p.adapters, p.rank, splits, y.blocks,
+                     y.shard, per, chunks, groups, strips};
       auto go = [&](auto ranks) {
         if (p.adapters >= groups)
           hipLaunchKernelGGL((k_adapt_up<T, decltype(ranks)::value, true>), dim3(static_cast<unsigned>(strips) * groups),

@@ -17,11 +17,17 @@
 // many for LDS, the bound is found among all entries, ties included.
 //
 // Order over beams: the candidates of different beams are compared through their
-// rows' sums, so an error of a sum shifts a whole beam. With fp32's 1e-7, two
-// candidates a thousand calls apart would be swapped (spacings are about 0.02);
-// sums and scores are therefore in 64 bits, the exponentials to 6e-11, a
+// rows' sums, so an error of a sum shifts a whole beam. fp32's, about 1e-6 of a
+// logarithm of 12, would swap two candidates in about one of a thousand requests
+// (16 of them, about 0.02 apart); sums and scores are therefore in 64 bits, the
+// exponentials to 6e-11, a
 // polynomial of degree 7 for 2^f on [-1/2, 1/2] (interpolated at the Chebyshev
 // points). The 64-bit instructions run at fp32's rate on this chip.
+//
+// Measured: 512 rows of 163837 bf16 entries, a tenth of them finished, keep 16: scan
+// 70 to 75 us, join 13. Reading alone takes 28 of them, the exponentials 27 more,
+// finding and ranking the entries the rest: instructions bound it. Four rows of 163840
+// are bound by latency: 5.7 and 7.3 us.
 #include <type_traits>
 
 #include "hg_beam.h"
@@ -623,7 +629,8 @@ hipError_t launch_beam_join(const BeamPlan &p, const float *scores, const unsign
 // many beams) of all of a request's rows: it reads what every changed row
 // becomes, then writes. No other thread touches the column, so nothing is read
 // after it was overwritten. Bytes bound it: changed rows are written once, rows
-// that several take are read again from the caches.
+// that several take are read again from the caches (1.8 GB in 347 to 356 us, 5.1 TB/s;
+// a copy reaches 4.8).
 
 namespace {
 

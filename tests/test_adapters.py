@@ -518,6 +518,68 @@ def test_past_32_bit_offsets():
 
 
 @gpu
+@pytest.mark.parametrize("dtype,rank", [("bf16", 64), ("bf16", 136), ("fp16", 16), ("fp16", 40)])
+def test_larger_than_the_caches(dtype, rank):
+    rows, tail = 900, 40  # y and dy are 295 MB
+    note(f"adapt 295 MB {dtype} {rank}")
+    c = Case(dtype, 8, 20480, 136, tail, 3, rank, run=7, sigma=0.1)
+    y = torch.zeros(8, rows, 20480, dtype=DT[dtype], device=DEV)
+    y[:, -tail:] = c.y.to(DEV)
+    x = torch.zeros(rows, 136, dtype=DT[dtype], device=DEV)
+    x[-tail:] = c.x.to(DEV)
+    index = torch.full((rows,), 1, dtype=torch.int64, device=DEV)
+    index[-tail:] = c.index.to(DEV)
+    _, a, b, _ = c.on(DEV)
+    dx, da, db = adapt_grad(y, x, a, b, index, 8, 20480, **c.how(DEV))
+    c.check_grads((dx[-tail:], da, db), c.y)
+    assert not dx[:-tail].any()
+    out = adapt(y, x, a, b, index, 8, 20480, **c.how(DEV))
+    c.check(out[:, -tail:])
+    assert not out[:, :-tail].any()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("m", [1, 20, 300])
+def test_most_adapters(m, dtype):
+    note(f"adapt 32768 adapters {m} {dtype}")
+    c = Case(dtype, 2, 8, 16, m, 1 << 15, 8, run=2)
+    c.index[0], c.index[-1] = (1 << 15) - 1, 1 << 15  # the last one, and none
+    c.check(adapt(c.y.to(DEV), *c.on(DEV), 2, 8, **c.how(DEV)))
+    c.check_grads(adapt_grad(c.y.to(DEV), *c.on(DEV), 2, 8, **c.how(DEV)), c.y)
+
+
+@gpu
+def test_two_graphs_at_once():
+    note("adapt two graphs")
+    cases = [Case("bf16", 2, 1000, 520, 300, 3, 24, run=40), Case("fp16", 3, 328, 264, 50, 7, 16, run=2)]
+    graphs = []
+    for c in cases:
+        args, how = (c.y.to(DEV), *c.on(DEV), c.tp, c.shard), c.how(DEV)
+        eager = [adapt(*args, **how), *adapt_grad(*args, **how)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = [adapt(*args, **how), *adapt_grad(*args, **how)]
+        graphs.append((graph, eager, got, args, how))
+    sides = [torch.cuda.Stream() for _ in cases]
+    for _ in range(4):
+        for _, _, got, _, _ in graphs:
+            for t in got:
+                t.zero_()
+        torch.cuda.synchronize()
+        for side, (graph, _, _, args, how) in zip(sides, graphs):
+            with torch.cuda.stream(side):
+                for _ in range(8):
+                    graph.replay()
+        again = [adapt(*args, **how) for _, _, _, args, how in graphs]  # beside the replays
+        torch.cuda.synchronize()
+        for (_, eager, got, _, _), other in zip(graphs, again):
+            assert torch.equal(other, eager[0])
+            for p, q in zip(got, eager):
+                assert torch.equal(p, q)
+
+
+@gpu
 def test_wrong_workspaces_and_overlaps_are_refused():
     c = Case("bf16", 2, 72, 136, 9, 3, 8)
     y = c.y.to(DEV)

@@ -433,6 +433,34 @@ def test_selection_repeats_its_bits_on_any_stream_and_in_a_graph():
 
 
 @gpu
+def test_two_selections_at_once():
+    note("select two graphs")
+    graphs = []
+    for k, (requests, beams, vocab, keep) in enumerate([(9, 4, 30011, 8), (2, 7, 5003, 14)]):
+        z = rand((requests * beams, vocab), 20 + k, "bf16").to(DEV)
+        s = rand((requests, beams), 30 + k, sigma=1.0).to(DEV)
+        eager = beam_select(z, s, keep)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = beam_select(z, s, keep)
+        graphs.append((graph, eager, got, z, s))  # (a graph does not keep its inputs)
+    sides = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(4):
+        for _, _, got, _, _ in graphs:
+            for t in got:
+                t.zero_()
+        torch.cuda.synchronize()
+        for side, (graph, *_) in zip(sides, graphs):
+            with torch.cuda.stream(side):
+                for _ in range(8):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for _, eager, got, _, _ in graphs:
+            for p, q in zip(got, eager):
+                assert torch.equal(p, q)
+
+
+@gpu
 def test_no_requests():
     got = beam_select(torch.zeros(0, 7, device=DEV), torch.zeros(0, 3, device=DEV), 4)
     assert [tuple(t.shape) for t in got] == [(0, 4)] * 3

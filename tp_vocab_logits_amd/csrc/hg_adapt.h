@@ -47,11 +47,25 @@ struct AdaptPlan {
   float *pa, *pb;        // [parts][adapters][..], where there are several
 };
 
+// Whether the second product goes through many rows with W's fragments kept
+// (k_adapt_stream): sorted rows, 64 of an adapter on average, ranks that fit.
+inline bool adapt_streams(int m, int adapters, int rank) {
+  return m > kFewRows && m / 64 >= adapters && rank <= kRankChunk;
+}
+
+// Whether launch_adapt_prepare leaves g's halves in `low` for it (dx of bf16: fp16's need
+// a row's largest): a launch less, gradients of 2047 rows of 32000 columns 77
+// us instead of 80.
+inline bool adapt_prepares_rows(const AdaptPlan &p) {
+  return p.at && !p.half && adapt_streams(p.m, p.adapters, p.rank);
+}
+
 // pu and pg: u's parts from x and A, g's from y and B ([adapters][rank][columns] and
 // [adapters][columns][rank]); a side without p is left out.
 hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocked &x, const void *a,
                             const Blocked &y, const void *b, hipStream_t s);
-// out = y + (sum of the parts) W^T per row; y NULL: zeros.
+// out = y + (sum of the parts) W^T per row; y NULL: zeros; part NULL: their halves are
+// in `low` (k_adapt_stream's sizes).
 hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *part, int splits,
                            const float *scale, const void *w, const Blocked &y, void *out,
                            hipStream_t s);
@@ -64,12 +78,6 @@ hipError_t launch_adapt_prepare(const AdaptPlan &p, const AdaptRows &r, const fl
 // rows that are added up if there are several.
 hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Blocked &x, void *da, const Blocked &y,
                               void *db, bool wide, hipStream_t s);
-
-// Whether the second product goes through many rows with W's fragments kept
-// (k_adapt_stream): sorted rows, 64 of an adapter on average, ranks that fit.
-inline bool adapt_streams(int m, int adapters, int rank) {
-  return m > kFewRows && m / 64 >= adapters && rank <= kRankChunk;
-}
 
 // Parts that a sum over `columns` columns of `m` rows is cut into.
 int adapt_splits(int m, int blocks, int shard, int rank, bool few);

@@ -920,6 +920,8 @@ struct TurnSide {
   int splits;         // go (or NULL)
   float *low;         // otherwise: those
   unsigned short *turned;  // (or NULL: the sums alone)
+  unsigned short *rows;    // or NULL: the halves by row as well, as k_adapt_values lays
+  int of_row;              // them out for `of_row` ranks (JOIN, bf16)
   int *largest;            // [adapters]
 };
 struct TurnLds {
@@ -957,8 +959,31 @@ __device__ __forceinline__ void turn_halves(const TurnSide &s, const int *keys, 
 #pragma unroll
     for (int t = 0; t < 4; ++t) l.t[row][e + t] = v[t];
   }
-  if (JOIN && !s.turned) return;
   __syncthreads();
+  if constexpr (JOIN && !T::kHalf) {
+    if (s.rows) {
+      const int last = r0 + 32 >= rank ? s.of_row : r0 + 32, width = (last - r0) / 8;
+      for (int k = tid; k < 64 * width; k += kThreads) {
+        const int row = k / width, e = k % width * 8, p = p0 + row;
+        if (p >= m) continue;
+        u32x4 hi, lo;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          uint32_t h0 = 0, l0 = 0, h1 = 0, l1 = 0;
+          if (e < 32) {
+            halves<T>(l.t[row][e + 2 * t], h0, l0);
+            halves<T>(l.t[row][e + 2 * t + 1], h1, l1);
+          }
+          hi[t] = h0 | h1 << 16;
+          lo[t] = l0 | l1 << 16;
+        }
+        unsigned short *const to = s.rows + static_cast<size_t>(p) * (2 * s.of_row) + r0 + e;
+        *reinterpret_cast<u32x4 *>(to) = hi;
+        *reinterpret_cast<u32x4 *>(to + s.of_row) = lo;
+      }
+    }
+  }
+  if (JOIN && !s.turned) return;
   if constexpr (T::kHalf) {
     if constexpr (JOIN) {
       if (tid < 64) {
@@ -1347,8 +1372,9 @@ hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *
     if (adapt_streams(p.m, p.adapters, p.rank)) {
       by_size(p.rank, p.m, y, [&](auto rb, auto past) {
         constexpr int RB = decltype(rb)::value;
-        hipLaunchKernelGGL((k_adapt_values<T, RB * 16>), dim3(ceil_div(p.m, kThreads / (RB * 2))), dim3(kThreads), 0, s,
-                           part, scale, r.keys, p.m, p.adapters, p.rank, splits, p.low, p.back);
+        if (part)
+          hipLaunchKernelGGL((k_adapt_values<T, RB * 16>), dim3(ceil_div(p.m, kThreads / (RB * 2))), dim3(kThreads), 0,
+                             s, part, scale, r.keys, p.m, p.adapters, p.rank, splits, p.low, p.back);
         const StreamArgs a{r.keys, r.pos, p.low, wp, yp, p.back, op, p.m, p.adapters, p.rank, y.blocks, y.shard, per,
                            chunks};
         // about 2048 workgroups, four rounds of two per CU, of two steps at least
@@ -1394,8 +1420,10 @@ hipError_t launch_adapt_prepare(const AdaptPlan &p, const AdaptRows &r, const fl
   }
   PrepareArgs args{};
   // (u itself goes nowhere else, g to dx)
-  args.u = TurnSide{p.pu, p.split_u, join ? nullptr : p.u, p.ut, p.head};
-  args.g = TurnSide{p.pg, p.split_g, join && !p.at ? nullptr : p.g, p.gt, p.half ? p.head + p.adapters : nullptr};
+  const bool rows = adapt_prepares_rows(p);
+  args.u = TurnSide{p.pu, p.split_u, join ? nullptr : p.u, p.ut, nullptr, 0, p.head};
+  args.g = TurnSide{p.pg, p.split_g, join && (rows || !p.at) ? nullptr : p.g, p.gt, rows ? p.low : nullptr,
+                    p.rank <= 16 ? 16 : kRankChunk, p.half ? p.head + p.adapters : nullptr};
   args.at = p.at;
   args.a = static_cast<const unsigned short *>(a);
   args.seg = p.seg;

@@ -223,6 +223,9 @@ HG_API int hg_adapt_grad(const hg_adapt_shape *s, const void *dy, const void *x,
   HIP_TRY(hg::launch_adapt_low(p, rows, p.u ? wide_x : none, a, p.g ? wide_y : none, b, st));
   HIP_TRY(hg::launch_adapt_prepare(p, rows, scale, a, st));
   if (da || db) HIP_TRY(hg::launch_adapt_outer(p, rows, wide_x, da, wide_y, db, wide != 0, st));
-  if (dx) HIP_TRY(hg::launch_adapt_up(p, rows, p.g, 1, nullptr, p.at, Blocked{nullptr, 1, s->hidden}, dx, st));
+  if (dx) {
+    const float *const g = hg::adapt_prepares_rows(p) ? nullptr : p.g;
+    HIP_TRY(hg::launch_adapt_up(p, rows, g, 1, nullptr, p.at, Blocked{nullptr, 1, s->hidden}, dx, st));
+  }
   return HG_OK;
 }

@@ -381,8 +381,9 @@ def test_fp16_gradients_of_small_and_large_adapters(m, n, rank):
 
 @gpu
 @pytest.mark.parametrize("need", [(True, False, False), (False, True, False), (False, False, True)])
-@pytest.mark.parametrize("dtype,m,rank", [("fp16", 30, 16), ("fp16", 30, 72), ("bf16", 30, 16)])
-def test_gradients_of_few_rows_that_are_not_needed(dtype, m, rank, need):
+@pytest.mark.parametrize("dtype,m,rank", [("fp16", 30, 16), ("fp16", 30, 72), ("bf16", 30, 16), ("bf16", 300, 16),
+                                          ("bf16", 300, 40), ("fp16", 300, 16)])
+def test_gradients_that_are_not_needed_of_any_form(dtype, m, rank, need):
     note(f"adapt need {dtype} {m} {rank} {need}")
     c = Case(dtype, 2, 136, 264, m, 4, rank, run=2)
     c.check_grads(adapt_grad(c.y.to(DEV), *c.on(DEV), 2, 136, need=need, **c.how(DEV)), c.y, need=need)

@@ -477,9 +477,9 @@ int hg_adapt_workspace(const hg_adapt_shape *s, int kind, size_t *bytes);
  * nothing else. x: device [m][hidden]; a: device [adapters][rank][hidden]; b:
  * device [adapters][tp*shard][rank]; scale: device [adapters] fp32, or NULL for
  * ones; index: device [m]. An infinity or a NaN in x, an adapter or its scale
- * makes what depends on it not finite, and nothing else. Sums are fp32, the low-rank values are held to 2^-16
- * of themselves (bf16) or 2^-21 of the row's largest (fp16), each result is
- * rounded once.
+ * makes what depends on it not finite, and nothing else. Sums are fp32, the
+ * low-rank values scale_i A_i x_j stay fp32 (fp16: but for what lies 2^-38 below
+ * the row's largest), each result is rounded once.
  * All pointers but scale and index 16-byte aligned. ws: device workspace,
  * 256-byte aligned, as large as hg_adapt_workspace asks (else HG_ESIZE), in use
  * until the call's work on `stream` is done. m == 0 does nothing. HG_EINVAL on
@@ -501,7 +501,7 @@ int hg_adapt(const hg_adapt_shape *s, const void *y, const void *x, const void *
  * da, db: in dtype, or fp32 if wide; zeros for an adapter that no row has. Each
  * of dx, da and db may be NULL and is then not computed, not all three. Sums are
  * fp32, over the rows in their order; g and u are held as in hg_adapt (fp16: in
- * da and db to 2^-21 of the largest among the adapter's rows). m == 0 zeroes da
+ * da and db by the largest among the adapter's rows). m == 0 zeroes da
  * and db. The rest is as above.
  */
 int hg_adapt_grad(const hg_adapt_shape *s, const void *dy, const void *x, const void *a,

@@ -1,5 +1,5 @@
 """Oracle of the low-rank adapters: float64 definitions, one adapter at a time,
-and the bounds that fp32 sums, the split of the low-rank values into two 16-bit
+and the bounds that fp32 sums, the split of the low-rank values into three 16-bit
 numbers and the final rounding put on a result. Test infrastructure only;
 shares nothing with the library."""
 
@@ -13,9 +13,9 @@ U32 = 2.0 ** -24
 
 
 def _split(kind: str, u: np.ndarray, largest) -> np.ndarray:
-    """What two 16-bit numbers leave out of u: bf16 half a step of half a step;
-    fp16, brought to a largest of 1..2, the same or half of the smallest step."""
-    return np.abs(u) * 2.0 ** -16 if kind == "bf16" else np.abs(u) * 2.0 ** -22 + 2.0 ** -25 * largest
+    """What three 16-bit numbers leave out of u: nothing of fp32's 24 bits (2^-24 for u's own rounding); fp16, brought to
+    a largest of 2^13..2^14, half of its smallest step, 2^-25."""
+    return np.abs(u) * U32 + (0.0 if kind == "bf16" else 2.0 ** -38 * largest)
 
 
 def _rows(index, n):

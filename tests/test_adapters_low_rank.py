@@ -1,0 +1,189 @@
+"""The low-rank values of the adapters on their way to a result: sums that come out exact in fp32, so that nothing but
+what the second product makes of them is left (GPU).
+
+Every row has one entry on the side that is summed first, so u (or g) is one product of two 16-bit numbers, at most 22
+bits, and a factor: off by 2^-24 of itself. An entry of the result is then one product with a 16-bit number, in up to
+three pieces that fp32 adds up, each within 2^-23 (a sum that cuts off): 2^-24 + 3 * 2^-23 < 2^-21 in all. What fp16
+holds of a value ends 2^-38 below the largest of its row, or of its adapter's rows."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from tp_vocab_logits_amd import adapt, adapt_grad
+
+DEV = "cuda:0"
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+HALF_STEP = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+LEAST = {"bf16": 2.0 ** -134, "fp16": 2.0 ** -25}  # half of the smallest step of a 16-bit result
+SUMS = 2.0 ** -21
+gpu = pytest.mark.gpu
+
+# rows, adapters, rank: few rows; many of many adapters; many of few (the streaming form), up to 16, 64 and more ranks
+FORMS = [(5, 3, 8), (40, 4, 32), (64, 2, 72), (90, 9, 16), (150, 20, 64), (200, 2, 72), (300, 2, 16), (300, 3, 40), (200, 1, 64)]
+TP, SHARD, HIDDEN = 2, 136, 264
+V = TP * SHARD
+
+
+def note(msg: str) -> None:
+    print(f"[gpu] {msg}", flush=True)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+class Case:
+    def __init__(self, dtype, m, n, rank, seed):
+        g = torch.Generator().manual_seed(1000 * seed + m + rank)
+        self.g, self.kind, self.t, self.m = g, dtype, DT[dtype], m
+        self.index = torch.randint(0, n, (m,), generator=g)
+        self.scale = torch.rand(n, generator=g) + 0.5
+        self.a = (torch.randn(n, rank, HIDDEN, generator=g)).to(self.t)
+        self.b = (torch.randn(n, V, rank, generator=g)).to(self.t)
+        self.sizes = 2.0 ** -torch.randint(0, 10, (m, 1), generator=g)  # rows of different size
+        self.turn = torch.empty(m, dtype=torch.long)  # which of its adapter's rows a row is
+        for i in range(n):
+            rows = torch.nonzero(self.index == i).squeeze(1)
+            self.turn[rows] = torch.arange(len(rows))
+        self.most = int(self.turn.max()) + 1
+
+    def randn(self, *shape):
+        return torch.randn(*shape, generator=self.g)
+
+    def one_entry(self, width):
+        """[m, width]: one entry a row."""
+        out = torch.zeros(self.m, width)
+        at = torch.randint(0, width, (self.m, 1), generator=self.g)
+        return out.scatter_(1, at, self.randn(self.m, 1) * self.sizes).to(self.t)
+
+    def in_turn(self, width):
+        """[m, width]: an adapter's rows have their entries in different columns (as far as there are columns)."""
+        mine = torch.arange(width)[None, :] % self.most == self.turn[:, None]
+        return (self.randn(self.m, width) * mine).to(self.t)
+
+    def shards(self, flat):
+        return flat.view(self.m, TP, SHARD).transpose(0, 1).contiguous()
+
+    def on(self):
+        return [t.to(DEV) for t in (self.a, self.b, self.index)]
+
+    def largest(self, low):
+        """Of each adapter's rows."""
+        return np.array([np.abs(low[self.index.numpy() == i]).max(initial=0.0) for i in range(len(self.scale))])
+
+
+def near(got, want, bound):
+    e = np.abs(got - want)
+    assert (e <= bound).all(), np.max(e / bound)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,n,rank", FORMS)
+def test_wide_gradients_hold_what_fp32_does(dtype, m, n, rank):
+    note(f"adapt wide {dtype} {m} {n} {rank}")
+    c = Case(dtype, m, n, rank, 1)
+    floor = 0.0 if dtype == "bf16" else 2.0 ** -38
+    index, scale = c.index.numpy(), f64(c.scale)
+    # db: u of one entry of x
+    x, dy = c.one_entry(HIDDEN), c.in_turn(V)
+    a, b, i = c.on()
+    _, _, db = adapt_grad(c.shards(dy).to(DEV), x.to(DEV), a, b, i, TP, SHARD, scale=c.scale.to(DEV), wide=True,
+                          need=(False, False, True))
+    u = scale[index][:, None] * np.einsum("mh,mrh->mr", f64(x), f64(c.a)[index])
+    parts = np.einsum("mv,mr->mvr", f64(dy), u)
+    want, size, other = np.zeros((n, V, rank)), np.zeros((n, V, rank)), np.zeros((n, V))
+    np.add.at(want, index, parts)
+    np.add.at(size, index, np.abs(parts))
+    np.add.at(other, index, np.abs(f64(dy)))
+    # (where two rows share a column, their sum: the bound is of what is added)
+    near(f64(db), want, SUMS * size + floor * c.largest(u)[:, None, None] * other[:, :, None] + 2.0 ** -140)
+    # da: g of one entry of dy
+    dy, x = c.one_entry(V), c.in_turn(HIDDEN)
+    _, da, _ = adapt_grad(c.shards(dy).to(DEV), x.to(DEV), a, b, i, TP, SHARD, scale=c.scale.to(DEV), wide=True,
+                          need=(False, True, False))
+    g = scale[index][:, None] * np.einsum("mv,mvr->mr", f64(dy), f64(c.b)[index])
+    parts = np.einsum("mr,mh->mrh", g, f64(x))
+    want, size, other = np.zeros((n, rank, HIDDEN)), np.zeros((n, rank, HIDDEN)), np.zeros((n, HIDDEN))
+    np.add.at(want, index, parts)
+    np.add.at(size, index, np.abs(parts))
+    np.add.at(other, index, np.abs(f64(x)))
+    near(f64(da), want, SUMS * size + floor * c.largest(g)[:, None, None] * other[:, None, :] + 2.0 ** -140)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,n,rank", FORMS)
+def test_what_cancels_is_fp32s(dtype, m, n, rank):
+    """y takes nearly all of what the adapter adds away; the rounding is the small result's own."""
+    note(f"adapt cancel {dtype} {m} {n} {rank}")
+    c = Case(dtype, m, n, rank, 2)
+    x = c.one_entry(HIDDEN)
+    mine = torch.randint(0, rank, (n, V, 1), generator=c.g)
+    c.b = c.b * (torch.arange(rank)[None, None, :] == mine)  # one rank a column
+    a, b, i = c.on()
+    index, scale = c.index.numpy(), f64(c.scale)
+    u = scale[index][:, None] * np.einsum("mh,mrh->mr", f64(x), f64(c.a)[index])
+    more = np.einsum("mvr,mr->mv", f64(c.b)[index], u)
+    y = (-torch.from_numpy(more)).to(c.t)
+    got = adapt(c.shards(y).to(DEV), x.to(DEV), a, b, i, TP, SHARD, scale=c.scale.to(DEV))
+    got = f64(got.transpose(0, 1).reshape(m, V))
+    want = f64(y) + more
+    floor = 0.0 if dtype == "bf16" else 2.0 ** -38
+    lost = SUMS * np.abs(more) + floor * np.abs(u).max(axis=1, keepdims=True) * np.abs(f64(c.b)).max()
+    near(got, want, lost + HALF_STEP[dtype] * (np.abs(want) + lost) + LEAST[dtype])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,n,rank", FORMS)
+def test_input_gradients_that_cancel(dtype, m, n, rank):
+    """Two ranks that all but cancel in dx: g_0 = big + small, g_1 = big, a_1 = -a_0."""
+    note(f"adapt dx cancel {dtype} {m} {n} {rank}")
+    c = Case(dtype, m, n, rank, 3)
+    c.a = torch.zeros_like(c.a)
+    c.a[:, 0] = c.randn(n, HIDDEN).to(c.t)
+    c.a[:, rank - 1] = -c.a[:, 0]
+    c.b = torch.zeros_like(c.b)
+    # integers of up to 8 and 4 bits: big <= 2^16 and small are one fp32 sum that is exact
+    c.b[:, 3, 0] = c.b[:, 3, rank - 1] = torch.randint(128, 256, (n,), generator=c.g).to(c.t)
+    c.b[:, 140, 0] = torch.randint(1, 16, (n,), generator=c.g).to(c.t)
+    dy = torch.zeros(m, V)
+    dy[:, 3] = torch.randint(128, 256, (m,), generator=c.g).float()
+    dy[:, 140] = 1.0
+    dy = dy.to(c.t)
+    a, b, i = c.on()
+    dx, _, _ = adapt_grad(c.shards(dy).to(DEV), torch.zeros(m, HIDDEN, dtype=c.t, device=DEV), a, b, i, TP, SHARD,
+                          scale=c.scale.to(DEV), need=(True, False, False))
+    index = c.index.numpy()
+    g = f64(c.scale)[index][:, None] * np.einsum("mv,mvr->mr", f64(dy), f64(c.b)[index])
+    want = np.einsum("mr,mrh->mh", g, f64(c.a)[index])
+    # g within 2^-24; up to six pieces of at most |g| |a| each, added within 2^-23
+    lost = 6.5 * 2.0 ** -23 * np.einsum("mr,mrh->mh", np.abs(g), np.abs(f64(c.a)[index]))
+    near(f64(dx), want, lost + HALF_STEP[dtype] * (np.abs(want) + lost) + LEAST[dtype])
+
+
+@gpu
+@pytest.mark.parametrize("m,n,rank", [(5, 3, 8), (90, 9, 16), (300, 2, 16), (200, 1, 64), (200, 2, 72)])
+def test_low_rank_values_between_bf16s_largest_and_fp32s(m, n, rank):
+    """A u that bf16 would round to infinity, and a factor that brings the result back."""
+    note(f"adapt near fp32's largest {m} {n} {rank}")
+    c = Case("bf16", m, n, rank, 4)
+    top = 2.0 ** 127
+    c.scale = torch.full((n,), (2.0 - 2.0 ** -12) * top)  # above bf16's largest, (2 - 2^-7) 2^127
+    x = torch.zeros(m, HIDDEN, dtype=c.t)
+    x[:, 5] = 1.0
+    c.a = torch.zeros_like(c.a)
+    c.a[:, 0, 5] = 1.0
+    c.b = (c.b * 2.0 ** -126).to(c.t)
+    a, b, i = c.on()
+    y = torch.zeros(TP, m, SHARD, dtype=c.t, device=DEV)
+    got = adapt(y, x.to(DEV), a, b, i, TP, SHARD, scale=c.scale.to(DEV))
+    got = f64(got.transpose(0, 1).reshape(m, V))
+    want = f64(c.b)[c.index.numpy()][:, :, 0] * f64(c.scale)[0]
+    # bf16's smallest normal b is 2^-126: what lies below it may count as nothing
+    small = np.abs(f64(c.b)[c.index.numpy()][:, :, 0]) < 2.0 ** -126
+    near(np.where(small, want, got), want, (HALF_STEP["bf16"] + 2 * SUMS) * np.abs(want) + 1e-30)

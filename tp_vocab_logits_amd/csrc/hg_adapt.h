@@ -37,11 +37,11 @@ struct AdaptPlan {
   void *sort_ws;
   float *pu, *pg;        // [split][m][rank] partial sums of u and g
   float *u, *g;          // [m][rank] scaled sums, by sorted position
-  unsigned short *low;   // [m][2][16 or 64] their halves, where the second product streams
+  unsigned short *low;   // [m][3][16 or 64] their pieces, where the second product streams
   float *back;           // [m] and fp16's factors
   int *head;             // [2][adapters]: bits of the largest |u| and |g| (fp16)
   int *seg;              // [adapters + 1] sorted positions where they begin
-  unsigned short *ut, *gt;  // [2][ranks][padded] upper and lower halves of u and g
+  unsigned short *ut, *gt;  // [3][ranks][padded] pieces of u and g
   unsigned short *at;    // [adapters][hidden][rank]: A turned
   int parts_a, parts_b;  // of the rows in the sums of dA and dB
   float *pa, *pb;        // [parts][adapters][..], where there are several
@@ -53,7 +53,7 @@ inline bool adapt_streams(int m, int adapters, int rank) {
   return m > kFewRows && m / 64 >= adapters && rank <= kRankChunk;
 }
 
-// Whether launch_adapt_prepare leaves g's halves in `low` for it (dx of bf16: fp16's need
+// Whether launch_adapt_prepare leaves g's pieces in `low` for it (dx of bf16: fp16's need
 // a row's largest): a launch less, gradients of 2047 rows of 32000 columns 77
 // us instead of 80.
 inline bool adapt_prepares_rows(const AdaptPlan &p) {
@@ -64,14 +64,14 @@ inline bool adapt_prepares_rows(const AdaptPlan &p) {
 // [adapters][columns][rank]); a side without p is left out.
 hipError_t launch_adapt_low(const AdaptPlan &p, const AdaptRows &r, const Blocked &x, const void *a,
                             const Blocked &y, const void *b, hipStream_t s);
-// out = y + (sum of the parts) W^T per row; y NULL: zeros; part NULL: their halves are
+// out = y + (sum of the parts) W^T per row; y NULL: zeros; part NULL: their pieces are
 // in `low` (k_adapt_stream's sizes).
 hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *part, int splits,
                            const float *scale, const void *w, const Blocked &y, void *out,
                            hipStream_t s);
 // u and g from their parts, scaled; each adapter's largest.
 hipError_t launch_adapt_join(const AdaptPlan &p, const AdaptRows &r, const float *scale, hipStream_t s);
-// The same and their halves by rank (ut, gt), and A turned (at), those that are there.
+// The same and their pieces by rank (ut, gt), and A turned (at), those that are there.
 hipError_t launch_adapt_prepare(const AdaptPlan &p, const AdaptRows &r, const float *scale, const void *a,
                                 hipStream_t s);
 // da and db, those that are there: the sums over an adapter's rows, in parts of the

@@ -14,9 +14,10 @@
 // adapter (an infinity in its B) reaches the rows of another.
 //
 // Precision. u and g are fp32 sums that enter a second product of 16-bit operands.
-// They enter as the sum of two 16-bit numbers, so that what is lost is 2^-16 of
-// them; rounded to bf16 alone they would add as much error to a row as its own
-// final rounding. For fp16 they are first scaled by a power of two.
+// They enter as the sum of three 16-bit numbers, which hold all of fp32's 24 bits
+// (bf16: 8 each, over the same exponents). For fp16 they are first scaled by a power
+// of two that brings the largest of the row (out, dx) or of the adapter's rows (dA,
+// dB) to 2^13 .. 2^14; what lies 2^-38 below it is lost.
 #include <type_traits>
 
 #include "hg_adapt.h"
@@ -36,27 +37,35 @@ __device__ __forceinline__ s16x8 stream8(const unsigned short *p) {  // read onc
 }
 __device__ __forceinline__ s16x8 zero8() { return s16x8{0, 0, 0, 0, 0, 0, 0, 0}; }
 
-// A power of two that brings `largest` to 1 .. 4 (1 for bf16, whose exponent needs
-// none), and its inverse.
+// A power of two that brings `largest` to 2^13 .. 2^14 (1 for bf16, whose exponent
+// needs none), and its inverse. (Both are normal for every exponent from 14 to 254;
+// an infinity goes by the largest of them.)
 __device__ __forceinline__ uint32_t exponent(float largest) {
   const uint32_t e = __builtin_bit_cast(uint32_t, largest) >> 23 & 255;
-  return e < 1 ? 1 : e > 253 ? 253 : e;
+  return e < 14 ? 14 : e > 254 ? 254 : e;
 }
 template <class T>
-__device__ __forceinline__ float to_unit(float largest) {
-  return T::kHalf ? __builtin_bit_cast(float, (254 - exponent(largest)) << 23) : 1.f;
+__device__ __forceinline__ float to_range(float largest) {
+  return T::kHalf ? __builtin_bit_cast(float, (267 - exponent(largest)) << 23) : 1.f;
 }
 template <class T>
-__device__ __forceinline__ float from_unit(float largest) {
-  return T::kHalf ? __builtin_bit_cast(float, exponent(largest) << 23) : 1.f;
+__device__ __forceinline__ float from_range(float largest) {
+  return T::kHalf ? __builtin_bit_cast(float, (exponent(largest) - 13) << 23) : 1.f;
 }
 
-// f as upper + lower.
+// f as the sum of three, descending. Each takes what the ones before leave, which fp32
+// holds exactly; an infinity or a NaN leaves nothing.
+constexpr int kPieces = 3;
 template <class T>
-__device__ __forceinline__ void halves(float f, uint32_t &hi, uint32_t &lo) {
-  hi = bits16<T>(f);
-  const float rest = f - from16<T>(hi);
-  lo = rest == rest ? bits16<T>(rest) : 0u;  // (an infinity leaves none)
+__device__ __forceinline__ void pieces(float f, uint32_t (&h)[kPieces]) {
+  h[0] = bits16<T>(f);
+  // (bf16: between its largest value and fp32's, a finite value rounds to infinity)
+  if (!T::kHalf && (h[0] & 0x7FFF) == 0x7F80 && fabsf(f) < __builtin_inff()) --h[0];
+#pragma unroll
+  for (int k = 1; k < kPieces; ++k) {
+    f -= from16<T>(h[k - 1]);
+    h[k] = f == f ? bits16<T>(f) : 0u;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -174,6 +183,14 @@ __device__ __forceinline__ void async4(const void *src, unsigned char *lds) {
 constexpr int kStages = 3;
 constexpr int kWaveBytes = 32 * 128;                   // 32 rows x 64 columns, or the like
 constexpr int kStageAll = 4 * kWaveBytes + kSubBytes;  // four waves' and 8 KB that they share (or 2 KB each)
+
+// The kernels of the second products hold low-rank values as well, 32 rows' a step
+// in three pieces: 12 KB that the waves share, or 3 KB each up to 16 ranks. These
+// come from the L2 and are loaded one step ahead only, the rows two steps: 72 KB and the
+// rows' places leave two workgroups per CU, a third stage would leave one.
+constexpr int kRowStage = 4 * kWaveBytes;
+constexpr int kLowWave = 3 * 1024, kLowStage = 4 * kLowWave;
+constexpr int kSecondLds = kStages * kRowStage + 2 * kLowStage;
 
 // ---------------------------------------------------------------------------
 // Low-rank products of many rows: part[split][p][rank] = sum over the split's
@@ -390,19 +407,19 @@ __global__ __launch_bounds__(kThreads) void k_adapt_low(LowArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// A row's low-rank values: the parts' sum, scaled, as two 16-bit numbers each (fp16:
-// brought to a largest of 1 .. 2). PER threads next to each other share a row, each
-// has PIECES times eight ranks.
+// A row's low-rank values: the parts' sum, scaled, as three 16-bit numbers each (fp16:
+// brought to its range). PER threads next to each other share a row, each has TIMES
+// times eight ranks.
 
-template <class T, int PER, int PIECES>
+template <class T, int PER, int TIMES>
 __device__ __forceinline__ void low_values(const float *part, const float *scale, int key, int p, int sub,
                                            int m, int adapters, int rank, int splits,
-                                           u32x4 (&hi)[PIECES], u32x4 (&lo)[PIECES], float &back) {
-  float v[PIECES][8];
+                                           u32x4 (&low)[kPieces][TIMES], float &back) {
+  float v[TIMES][8];
   float largest = 0.f;
   const float s = key < adapters && scale ? scale[key] : 1.f;
 #pragma unroll
-  for (int q = 0; q < PIECES; ++q) {
+  for (int q = 0; q < TIMES; ++q) {
     const int e = (q * PER + sub) * 8;
 #pragma unroll
     for (int t = 0; t < 8; ++t) v[q][t] = 0.f;
@@ -434,21 +451,21 @@ __device__ __forceinline__ void low_values(const float *part, const float *scale
 #pragma unroll
     for (int d = 1; d < PER; d <<= 1) largest = fmaxf(largest, __shfl_xor(largest, d));
   }
-  const float unit = to_unit<T>(largest);
-  back = from_unit<T>(largest);
+  const float factor = to_range<T>(largest);
+  back = from_range<T>(largest);
 #pragma unroll
-  for (int q = 0; q < PIECES; ++q)
+  for (int q = 0; q < TIMES; ++q)
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      uint32_t h0, l0, h1, l1;
-      halves<T>(v[q][2 * t] * unit, h0, l0);
-      halves<T>(v[q][2 * t + 1] * unit, h1, l1);
-      hi[q][t] = h0 | h1 << 16;
-      lo[q][t] = l0 | l1 << 16;
+      uint32_t a[kPieces], b[kPieces];
+      pieces<T>(v[q][2 * t] * factor, a);
+      pieces<T>(v[q][2 * t + 1] * factor, b);
+#pragma unroll
+      for (int h = 0; h < kPieces; ++h) low[h][q][t] = a[h] | b[h] << 16;
     }
 }
 
-// All rows' values by sorted position: [m][2][RANKS] (16 or 64 ranks, zeros past
+// All rows' values by sorted position: [m][3][RANKS] (16 or 64 ranks, zeros past
 // `rank`), and fp16's factors back. (2047 rows of 64 ranks in 28 parts: 6.6 us.)
 template <class T, int RANKS>
 __global__ __launch_bounds__(kThreads) void k_adapt_values(const float *part, const float *scale, const int *keys,
@@ -458,12 +475,12 @@ __global__ __launch_bounds__(kThreads) void k_adapt_values(const float *part, co
   const int tid = static_cast<int>(threadIdx.x);
   const int p = static_cast<int>(blockIdx.x) * (kThreads / kPer) + tid / kPer, sub = tid % kPer;
   if (p >= m) return;
-  u32x4 hi[1], lo[1];
+  u32x4 v[kPieces][1];
   float inv;
-  low_values<T, kPer, 1>(part, scale, keys[p], p, sub, m, adapters, rank, splits, hi, lo, inv);
-  unsigned short *const row = low + static_cast<size_t>(p) * (2 * RANKS) + sub * 8;
-  *reinterpret_cast<u32x4 *>(row) = hi[0];
-  *reinterpret_cast<u32x4 *>(row + RANKS) = lo[0];
+  low_values<T, kPer, 1>(part, scale, keys[p], p, sub, m, adapters, rank, splits, v, inv);
+  unsigned short *const row = low + static_cast<size_t>(p) * (kPieces * RANKS) + sub * 8;
+#pragma unroll
+  for (int h = 0; h < kPieces; ++h) *reinterpret_cast<u32x4 *>(row + h * RANKS) = v[h][0];
   if (T::kHalf && sub == 0) back[p] = inv;
 }
 
@@ -475,15 +492,15 @@ __global__ __launch_bounds__(kThreads) void k_adapt_values(const float *part, co
 // many adapters. 64 rows of 32 adapters (V = 163840, rank 16): 36 to 38 us for 190 MB,
 // 5.1 TB/s where a copy reaches 4.8, most of it W read once.
 
-// acc += W's fragments x a row's values, given by read(half, ks); BOTH: the two halves
-// of up to 16 ranks are one fragment.
+// acc += W's fragments x a row's values, given by read(piece, ks); BOTH: two pieces of
+// up to 16 ranks are one fragment, the third one and zeros another.
 template <class T, bool BOTH, int KF, class F>
 __device__ __forceinline__ void add_low(f32x4 (&acc)[4], const s16x8 (&wf)[4][KF], F read) {
 #pragma unroll
   for (int ks = 0; ks < KF; ++ks)
 #pragma unroll
-    for (int half = 0; half < (BOTH ? 1 : 2); ++half) {
-      const s16x8 f = read(half, ks);
+    for (int h = 0; h < (BOTH ? 2 : kPieces); ++h) {
+      const s16x8 f = read(h, ks);
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[v] = T::mma(wf[v][ks], f, acc[v]);
     }
@@ -515,13 +532,13 @@ struct UpArgs {
   int groups, strips;
 };
 
-// RANKS: 16 (upper and lower halves share one fragment), 64, or 256: in turns of 64.
+// RANKS: 16 (two pieces share one fragment), 64, or 256: in turns of 64.
 // APART: the tiles have adapters of their own, mostly.
 template <class T, int RANKS, bool APART>
 __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
   constexpr bool kBoth = RANKS == 16;
-  constexpr int kRow = 2 * RANKS + 8;  // 16-bit elements of an LDS row: upper, lower halves
-  constexpr int kPieces = RANKS == 256 ? 2 : 1;
+  constexpr int kRow = kPieces * RANKS + 8;  // 16-bit elements of an LDS row, piece by piece
+  constexpr int kTimes = RANKS == 256 ? 2 : 1;
   constexpr int KF = kBoth ? 1 : 2;
   constexpr int kBatch = kBoth ? 2 : 1;  // adapters whose fragments are loaded together
   __shared__ __align__(16) unsigned short low[16 * kRow];
@@ -594,17 +611,17 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
   {
     const int r = tid / 16, sub = tid % 16, q0 = p0 + r;
     const int other = q0 < a.m ? a.keys[q0] : a.adapters;
-    u32x4 hi[kPieces], lo[kPieces];
+    u32x4 v[kPieces][kTimes];
     float inv;
-    low_values<T, 16, kPieces>(a.part, a.scale, other, a.by_row && q0 < a.m ? a.pos[q0] : q0, sub, a.m, a.adapters,
-                               a.rank, a.splits, hi, lo, inv);
+    low_values<T, 16, kTimes>(a.part, a.scale, other, a.by_row && q0 < a.m ? a.pos[q0] : q0, sub, a.m, a.adapters,
+                              a.rank, a.splits, v, inv);
     if (sub == 0) back[r] = inv;
 #pragma unroll
-    for (int q = 0; q < kPieces; ++q) {
+    for (int q = 0; q < kTimes; ++q) {
       const int e = (q * 16 + sub) * 8;
       if (e < RANKS) {
-        *reinterpret_cast<u32x4 *>(low + r * kRow + e) = hi[q];
-        *reinterpret_cast<u32x4 *>(low + r * kRow + RANKS + e) = lo[q];
+#pragma unroll
+        for (int h = 0; h < kPieces; ++h) *reinterpret_cast<u32x4 *>(low + r * kRow + h * RANKS + e) = v[h][q];
       }
     }
   }
@@ -622,8 +639,9 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
       for (int rc = 0;;) {
-        add_low<T, kBoth>(acc, wf[n], [&](int half, int ks) __attribute__((always_inline)) {
-          return load8(mine + (kBoth ? 8 * g : half * RANKS + rc + ks * 32 + 8 * g));
+        add_low<T, kBoth>(acc, wf[n], [&](int h, int ks) __attribute__((always_inline)) {
+          if (kBoth && h == 1) return g < 2 ? load8(mine + 2 * RANKS + 8 * g) : zero8();
+          return load8(mine + (kBoth ? 8 * g : h * RANKS + rc + ks * 32 + 8 * g));
         });
         rc += kRankChunk;
         if (RANKS <= kRankChunk || rc >= a.rank) break;
@@ -668,8 +686,9 @@ __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
   static_assert(RB == 1 || RB == 4);
   constexpr int KF = RB == 1 ? 1 : 2;
   constexpr int kPlaces = 4, kPlace = 512;          // per wave and step: places, keys, factors
-  constexpr int kLoads = T::kHalf ? 8 : 7;          // per wave and step
-  __shared__ __align__(1024) unsigned char lds[kStages * kStageAll + 4 * kPlaces * kPlace];
+  constexpr int kRowLoads = T::kHalf ? 6 : 5;       // per wave and step, places and factors among them
+  __shared__ __align__(1024) unsigned char lds[kSecondLds + 4 * kPlaces * kPlace];
+  unsigned char *const low_lds = lds + kStages * kRowStage;
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int ml = lane & 15, g = lane >> 4;
@@ -686,7 +705,7 @@ __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
   const size_t at = static_cast<size_t>(block) * a.m * a.shard + c0;
   const unsigned short *const wcol = a.w + (static_cast<size_t>(block) * a.shard + c0) * a.rank;
   const size_t each = static_cast<size_t>(a.blocks) * a.shard * a.rank;
-  unsigned char *const places = lds + kStages * kStageAll + wave * kPlaces * kPlace;
+  unsigned char *const places = lds + kSecondLds + wave * kPlaces * kPlace;
 
   // the places and keys of step k's rows (positions past the last row: that one's)
   auto locate = [&](int k) __attribute__((always_inline)) {
@@ -695,10 +714,10 @@ __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
     async4((lane < 32 ? a.pos : a.keys) + p, to);
     if constexpr (T::kHalf) async4(a.back + p, to + 256);
   };
-  auto issue = [&](int k, int stage) __attribute__((always_inline)) {
+  auto issue_rows = [&](int k, int stage) __attribute__((always_inline)) {
     locate(k + 2);
     const int p0 = (s0 + k) * 32;
-    unsigned char *const st = lds + stage * kStageAll + wave * kWaveBytes;
+    unsigned char *const st = lds + stage * kRowStage + wave * kWaveBytes;
     const int *const place = reinterpret_cast<const int *>(places + (k & (kPlaces - 1)) * kPlace);
     int row[4];
 #pragma unroll
@@ -711,20 +730,30 @@ __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
           real ? static_cast<const void *>(a.y + at + static_cast<size_t>(row[q]) * a.shard + c) : kZeros,
           st + q * 1024);
     }
-    unsigned char *const sl = lds + stage * kStageAll + 4 * kWaveBytes + wave * 2048;
+  };
+  auto issue_low = [&](int k) __attribute__((always_inline)) {
+    const int p0 = (s0 + k) * 32;
+    unsigned char *const sl = low_lds + (k & 1) * kLowStage;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < kPieces; ++t) {
       int p, e;  // position, and 16-bit element of its values
-      if constexpr (RB == 1) {  // 64 bytes a row, its four chunks swizzled by (row >> 2) & 3
-        p = p0 + t * 16 + (lane >> 2);
-        e = ((lane & 3) ^ (lane >> 4)) * 8;
-      } else {  // 128 bytes of upper halves, then of lower ones, as an operand's row
-        const int q = 2 * wave + t;
-        p = p0 + (q & 3) * 8 + lr.row;
-        e = (q >> 2) * kRankChunk + lr.chunk[t] * 8;
+      unsigned char *to;
+      if constexpr (RB == 1) {
+        to = sl + wave * kLowWave + t * 1024;
+        if (t < 2) {  // 64 bytes a row, its four chunks swizzled by (row >> 2) & 3
+          p = p0 + t * 16 + (lane >> 2);
+          e = ((lane & 3) ^ (lane >> 4)) * 8;
+        } else {  // the third piece's 32
+          p = p0 + (lane >> 1);
+          e = 32 + (lane & 1) * 8;
+        }
+      } else {  // 128 bytes of a row's piece, as an operand's row
+        to = sl + t * 4096 + wave * 1024;
+        p = p0 + wave * 8 + lr.row;
+        e = t * kRankChunk + (wave & 1 ? lr.chunk[1] : lr.chunk[0]) * 8;
       }
-      async16(p < a.m ? static_cast<const void *>(a.low + static_cast<size_t>(p) * (RB * 32) + e) : kZeros,
-              sl + t * 1024);
+      async16(p < a.m ? static_cast<const void *>(a.low + static_cast<size_t>(p) * (RB * 16 * kPieces) + e) : kZeros,
+              to);
     }
   };
   if (n > 0) {
@@ -732,26 +761,27 @@ __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
     locate(1);
     wait_vm_lds<0>();
     __asm__ __volatile__("" ::: "memory");
-    issue(0, 0);
+    issue_rows(0, 0);
+    issue_low(0);
   }
-  if (n > 1) issue(1, 1);
-  int stage = 0, stored = 0, before = 0;  // stores of the last step and of the one before it
+  if (n > 1) issue_rows(1, 1);
+  int stage = 0, stored = 0;  // stores of the last step
   int have = -1;
   s16x8 wf[4][KF];
   for (int k = 0; k < n; ++k) {
-    // Loads and stores share one counter and are counted off in order: besides the
-    // next step's loads, the last two steps' stores may be under way.
+    // Loads and stores share one counter and are counted off in order: the next step's
+    // rows and the last step's stores may be under way.
     if (k + 1 >= n)
       wait_vm_lds<0>();
-    else if (stored + before == 8)
-      wait_vm_lds<kLoads + 8>();
+    else if (stored == 4)
+      wait_vm_lds<kRowLoads + 4>();
     else
-      wait_vm_lds<kLoads>();
+      wait_vm_lds<kRowLoads>();
     if constexpr (RB > 1)
       tile_barrier();
     else
       __asm__ __volatile__("" ::: "memory");
-    // (the loads that issue() starts overwrite this step's places)
+    // (the loads that issue_rows() starts overwrite this step's places)
     const int p0 = (s0 + k) * 32;
     int keys[2], rows[2];
     float factors[2];
@@ -763,11 +793,11 @@ __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
       factors[t] = T::kHalf ? __builtin_bit_cast(float, place[64]) : 1.f;
     }
     wait_lds();
-    if (k + 2 < n) issue(k + 2, stage >= 1 ? stage - 1 : kStages - 1);
-    before = stored;
+    if (k + 1 < n) issue_low(k + 1);
+    if (k + 2 < n) issue_rows(k + 2, stage >= 1 ? stage - 1 : kStages - 1);
     stored = 0;
-    const unsigned char *const st = lds + stage * kStageAll + wave * kWaveBytes;
-    const unsigned char *const sl = lds + stage * kStageAll + 4 * kWaveBytes + (RB == 1 ? wave * 2048 : 0);
+    const unsigned char *const st = lds + stage * kRowStage + wave * kWaveBytes;
+    const unsigned char *const sl = low_lds + (k & 1) * kLowStage + (RB == 1 ? wave * kLowWave : 0);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int key = keys[t];
@@ -794,11 +824,14 @@ __global__ __launch_bounds__(kThreads) void k_adapt_stream(StreamArgs a) {
         f32x4 acc[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[v] = f32x4{0.f, 0.f, 0.f, 0.f};
-        add_low<T, RB == 1>(acc, wf, [&](int half, int ks) __attribute__((always_inline)) {
-          if constexpr (RB == 1)
-            return *reinterpret_cast<const s16x8 *>(sl + (t * 16 + ml) * 64 + ((g ^ (ml >> 2)) << 4));
-          else
-            return fr.read(sl + half * 4096, t, ks);
+        add_low<T, RB == 1>(acc, wf, [&](int h, int ks) __attribute__((always_inline)) {
+          if constexpr (RB == 1) {
+            const s16x8 f = *reinterpret_cast<const s16x8 *>(
+                h == 0 ? sl + (t * 16 + ml) * 64 + ((g ^ (ml >> 2)) << 4) : sl + 2048 + (t * 16 + ml) * 32 + ((g & 1) << 4));
+            return h == 0 || g < 2 ? f : zero8();
+          } else {
+            return fr.read(sl + h * 4096, t, ks);
+          }
         });
         const bool take = key == cur;
 #pragma unroll
@@ -912,15 +945,15 @@ __global__ __launch_bounds__(kThreads) void k_adapt_join(JoinSide u, JoinSide g,
   }
 }
 
-// low [m][rank] -> turned [2][rank][padded], upper and lower halves, zeros past m: 64
-// rows of 32 ranks. fp16: an adapter's largest at 1 .. 2, one factor for all of its
-// rows, which the sums over them take back.
+// low [m][rank] -> turned [3][rank][padded], piece by piece, zeros past m: 64 rows of 32
+// ranks. fp16: one factor for all of an adapter's rows, by the largest of them, which the
+// sums over them take back.
 struct TurnSide {
   const float *part;  // JOIN: the parts, of which `splits`, and where their scaled sums
   int splits;         // go (or NULL)
   float *low;         // otherwise: those
   unsigned short *turned;  // (or NULL: the sums alone)
-  unsigned short *rows;    // or NULL: the halves by row as well, as k_adapt_values lays
+  unsigned short *rows;    // or NULL: the pieces by row as well, as k_adapt_values lays
   int of_row;              // them out for `of_row` ranks (JOIN, bf16)
   int *largest;            // [adapters]
 };
@@ -934,7 +967,7 @@ struct TurnLds {
 // 4096: 32.6 instead of 34). fp16 knows its factors then only if the tile has all rows
 // and ranks.
 template <class T, bool JOIN>
-__device__ __forceinline__ void turn_halves(const TurnSide &s, const int *keys, const float *scale, int adapters, int m,
+__device__ __forceinline__ void turn_pieces(const TurnSide &s, const int *keys, const float *scale, int adapters, int m,
                                             int rank, int padded, int p0, int r0, TurnLds &l) {
   const int tid = static_cast<int>(threadIdx.x);
   if (tid < 64) l.key[tid] = p0 + tid < m ? keys[p0 + tid] : adapters;
@@ -966,20 +999,20 @@ __device__ __forceinline__ void turn_halves(const TurnSide &s, const int *keys, 
       for (int k = tid; k < 64 * width; k += kThreads) {
         const int row = k / width, e = k % width * 8, p = p0 + row;
         if (p >= m) continue;
-        u32x4 hi, lo;
+        u32x4 v[kPieces];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          uint32_t h0 = 0, l0 = 0, h1 = 0, l1 = 0;
+          uint32_t x[kPieces] = {}, y[kPieces] = {};
           if (e < 32) {
-            halves<T>(l.t[row][e + 2 * t], h0, l0);
-            halves<T>(l.t[row][e + 2 * t + 1], h1, l1);
+            pieces<T>(l.t[row][e + 2 * t], x);
+            pieces<T>(l.t[row][e + 2 * t + 1], y);
           }
-          hi[t] = h0 | h1 << 16;
-          lo[t] = l0 | l1 << 16;
+#pragma unroll
+          for (int h = 0; h < kPieces; ++h) v[h][t] = x[h] | y[h] << 16;
         }
-        unsigned short *const to = s.rows + static_cast<size_t>(p) * (2 * s.of_row) + r0 + e;
-        *reinterpret_cast<u32x4 *>(to) = hi;
-        *reinterpret_cast<u32x4 *>(to + s.of_row) = lo;
+        unsigned short *const to = s.rows + static_cast<size_t>(p) * (kPieces * s.of_row) + r0 + e;
+#pragma unroll
+        for (int h = 0; h < kPieces; ++h) *reinterpret_cast<u32x4 *>(to + h * s.of_row) = v[h];
       }
     }
   }
@@ -1008,16 +1041,17 @@ __device__ __forceinline__ void turn_halves(const TurnSide &s, const int *keys, 
       }
     }
     __syncthreads();
-    if (tid < 64) l.of_row[tid] = to_unit<T>(top);
+    if (tid < 64) l.of_row[tid] = to_range<T>(top);
     __syncthreads();
   }
   for (int k = tid; k < 64 * 32; k += kThreads) {
     const int p = p0 + k % 64, r = r0 + k / 64;
     if (p >= padded || r >= rank) continue;
-    uint32_t hi, lo;
-    halves<T>(T::kHalf ? l.t[k % 64][k / 64] * l.of_row[k % 64] : l.t[k % 64][k / 64], hi, lo);
-    s.turned[static_cast<size_t>(r) * padded + p] = static_cast<unsigned short>(hi);
-    s.turned[static_cast<size_t>(rank + r) * padded + p] = static_cast<unsigned short>(lo);
+    uint32_t v[kPieces];
+    pieces<T>(T::kHalf ? l.t[k % 64][k / 64] * l.of_row[k % 64] : l.t[k % 64][k / 64], v);
+#pragma unroll
+    for (int h = 0; h < kPieces; ++h)
+      s.turned[static_cast<size_t>(h * rank + r) * padded + p] = static_cast<unsigned short>(v[h]);
   }
 }
 
@@ -1040,7 +1074,7 @@ __device__ __forceinline__ void turn_block(const unsigned short *a, unsigned sho
   }
 }
 
-// What the gradients' wide products take, in one launch: the halves of u and g by
+// What the gradients' wide products take, in one launch: the pieces of u and g by
 // rank, and A turned, for the adapters that have rows.
 struct PrepareArgs {
   TurnSide u, g;
@@ -1049,8 +1083,8 @@ struct PrepareArgs {
   const int *seg, *keys;
   const float *scale;
   int m, rank, hidden, padded, adapters;
-  int tiles, across, blocks;  // workgroups of one side's halves, of which per rank chunk; of an adapter's A
-  int first, second;          // workgroups before g's halves, before A's
+  int tiles, across, blocks;  // workgroups of one side's pieces, of which per rank chunk; of an adapter's A
+  int first, second;          // workgroups before g's pieces, before A's
 };
 template <class T, bool JOIN>
 __global__ __launch_bounds__(kThreads) void k_adapt_prepare(PrepareArgs a) {
@@ -1062,7 +1096,7 @@ __global__ __launch_bounds__(kThreads) void k_adapt_prepare(PrepareArgs a) {
   if (id < a.second) {
     const bool g = id >= a.first;
     if (g) id -= a.first;
-    turn_halves<T, JOIN>(g ? a.g : a.u, a.keys, a.scale, a.adapters, a.m, a.rank, a.padded, id % a.across * 64,
+    turn_pieces<T, JOIN>(g ? a.g : a.u, a.keys, a.scale, a.adapters, a.m, a.rank, a.padded, id % a.across * 64,
                          id / a.across * 32, t.f);
   } else {
     id -= a.second;
@@ -1123,7 +1157,8 @@ __device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSi
   FragLane<true> fc;
   fc.init(lane);
   const unsigned short *const of = s.of + static_cast<size_t>(block) * a.m * s.shard + c0;
-  unsigned char *const places = lds + kStages * kStageAll + wave * kPlaces * 256;
+  unsigned char *const low_lds = lds + kStages * kRowStage;
+  unsigned char *const places = lds + kSecondLds + wave * kPlaces * 256;
   f32x4 acc[RB][4];
 #pragma unroll
   for (int b = 0; b < RB; ++b)
@@ -1135,11 +1170,11 @@ __device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSi
     const int p = first + (s0 + k) * 32 + (lane & 31);
     async4(a.pos + (p < a.m ? p : a.m - 1), places + (k & (kPlaces - 1)) * 256);
   };
-  // seven loads per wave and step
-  auto issue = [&](int k, int stage) __attribute__((always_inline)) {
+  // five loads per wave and step
+  auto issue_rows = [&](int k, int stage) __attribute__((always_inline)) {
     locate(k + 2);
     const int p0 = first + (s0 + k) * 32;
-    unsigned char *const st = lds + stage * kStageAll + wave * kWaveBytes;
+    unsigned char *const st = lds + stage * kRowStage + wave * kWaveBytes;
     const int *const place = reinterpret_cast<const int *>(places + (k & (kPlaces - 1)) * 256);
     int row[4];
 #pragma unroll
@@ -1151,27 +1186,29 @@ __device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSi
       async16<PAST>(real ? static_cast<const void *>(of + static_cast<size_t>(row[q]) * s.shard + c) : kZeros,
                     st + q * 1024);
     }
-    // pieces of 16 ranks' 32 rows, a rank's four chunks swizzled by (rank >> 2) & 3
-    unsigned char *const sl = lds + stage * kStageAll + 4 * kWaveBytes + wave * 2048;
+  };
+  // three: 16 ranks' 32 rows of each piece, a rank's four chunks swizzled by (rank >> 2) & 3
+  auto issue_low = [&](int k) __attribute__((always_inline)) {
+    const int p0 = first + (s0 + k) * 32;
+    unsigned char *const sl = low_lds + (k & 1) * kLowStage + (RB == 1 ? wave * kLowWave : wave * 1024);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int line = (RB == 1 ? t : 2 * wave + t) * 16 + (lane >> 2);  // half and rank
-      const int h = line / (RB * 16), r = line - h * (RB * 16);
-      const int p = p0 + ((lane & 3) ^ (line >> 2 & 3)) * 8;
+    for (int h = 0; h < kPieces; ++h) {
+      const int r = (RB == 1 ? 0 : wave * 16) + (lane >> 2);
+      const int p = p0 + ((lane & 3) ^ (lane >> 4)) * 8;
       const bool real = r < ranks && p < to;
       async16(real ? static_cast<const void *>(s.low + static_cast<size_t>(h * a.rank + rc + r) * a.padded + p) : kZeros,
-              sl + t * 1024);
+              sl + h * (RB * 1024));
     }
   };
   auto multiply = [&](int k, int stage) __attribute__((always_inline)) {
     const int p0 = first + (s0 + k) * 32;
-    const unsigned char *const st = lds + stage * kStageAll + wave * kWaveBytes;
-    const unsigned char *const sl = lds + stage * kStageAll + 4 * kWaveBytes + (RB == 1 ? wave * 2048 : 0);
-    s16x8 lf[RB][2];
+    const unsigned char *const st = lds + stage * kRowStage + wave * kWaveBytes;
+    const unsigned char *const sl = low_lds + (k & 1) * kLowStage + (RB == 1 ? wave * kLowWave : 0);
+    s16x8 lf[RB][kPieces];
 #pragma unroll
     for (int b = 0; b < RB; ++b)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kPieces; ++h) {
         const int line = h * (RB * 16) + b * 16 + ml;
         lf[b][h] = *reinterpret_cast<const s16x8 *>(sl + line * 64 + ((g ^ (ml >> 2)) << 4));
       }
@@ -1180,7 +1217,7 @@ __device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSi
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kPieces; ++h)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             if (p + e < from || p + e >= to) lf[b][h][e] = 0;
@@ -1191,7 +1228,7 @@ __device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSi
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kPieces; ++h)
           acc[b][v] = TURNED ? T::mma(lf[b][h], of8, acc[b][v]) : T::mma(of8, lf[b][h], acc[b][v]);
     }
   };
@@ -1200,24 +1237,26 @@ __device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSi
     locate(1);
     wait_vm_lds<0>();
     __asm__ __volatile__("" ::: "memory");
-    issue(0, 0);
+    issue_rows(0, 0);
+    issue_low(0);
   }
-  if (n > 1) issue(1, 1);
+  if (n > 1) issue_rows(1, 1);
   int stage = 0;
   for (int k = 0; k < n; ++k) {
-    if (k + 1 < n)
-      wait_vm_lds<7>();
+    if (k + 1 < n)  // the next step's rows may be under way
+      wait_vm_lds<5>();
     else
       wait_vm_lds<0>();
     if constexpr (RB > 1)
       tile_barrier();
     else
       __asm__ __volatile__("" ::: "memory");
-    if (k + 2 < n) issue(k + 2, stage >= 1 ? stage - 1 : kStages - 1);
+    if (k + 1 < n) issue_low(k + 1);
+    if (k + 2 < n) issue_rows(k + 2, stage >= 1 ? stage - 1 : kStages - 1);
     multiply(k, stage);
     stage = stage + 1 < kStages ? stage + 1 : 0;
   }
-  const float inv = T::kHalf ? from_unit<T>(__builtin_bit_cast(float, s.largest[i])) : 1.f;
+  const float inv = T::kHalf ? from_range<T>(__builtin_bit_cast(float, s.largest[i])) : 1.f;
   const size_t columns = static_cast<size_t>(s.blocks) * s.shard;
   const size_t col0 = static_cast<size_t>(block) * s.shard + c0;
 #pragma unroll
@@ -1246,7 +1285,7 @@ __device__ __forceinline__ void outer_products(const OuterArgs &a, const OuterSi
 // dB's workgroups first, then dA's.
 template <class T, int RB, bool PAST>
 __global__ __launch_bounds__(kThreads) void k_adapt_outer(OuterArgs a) {
-  __shared__ __align__(1024) unsigned char lds[kStages * kStageAll + 4 * 4 * 256];
+  __shared__ __align__(1024) unsigned char lds[kSecondLds + 4 * 4 * 256];
   const int id = static_cast<int>(blockIdx.x), first = a.y.strips * a.y.parts * a.adapters;
   if (id < first)
     outer_products<T, true, RB, PAST>(a, a.y, id, lds);

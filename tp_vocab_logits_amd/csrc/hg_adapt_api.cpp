@@ -73,7 +73,7 @@ size_t lay_out(const hg_adapt_shape &s, int kind, char *ws, AdaptPlan *p) {
   p->split_u = hg::adapt_splits(s.m, 1, s.hidden, s.rank, p->few);
   p->pu = floats(low * p->split_u);
   if (hg::adapt_streams(s.m, s.adapters, s.rank)) {
-    p->low = reinterpret_cast<unsigned short *>(take(static_cast<size_t>(s.m) * (s.rank <= 16 ? 64 : 256)));
+    p->low = reinterpret_cast<unsigned short *>(take(static_cast<size_t>(s.m) * (s.rank <= 16 ? 96 : 384)));
     p->back = floats(s.m);
   } else if (kind == HG_ADAPT_ADD && !p->few) {
     p->u = floats(low);
@@ -86,8 +86,8 @@ size_t lay_out(const hg_adapt_shape &s, int kind, char *ws, AdaptPlan *p) {
   if (p->half) p->head = reinterpret_cast<int *>(take(8 * static_cast<size_t>(s.adapters)));
   p->seg = reinterpret_cast<int *>(take(4 * (static_cast<size_t>(s.adapters) + 1)));
   p->padded = static_cast<int>(ceil_div(s.m + 8, 32) * 32);  // (eight are read at once from any row on)
-  p->ut = reinterpret_cast<unsigned short *>(take(4 * static_cast<size_t>(s.rank) * p->padded));
-  p->gt = reinterpret_cast<unsigned short *>(take(4 * static_cast<size_t>(s.rank) * p->padded));
+  p->ut = reinterpret_cast<unsigned short *>(take(6 * static_cast<size_t>(s.rank) * p->padded));
+  p->gt = reinterpret_cast<unsigned short *>(take(6 * static_cast<size_t>(s.rank) * p->padded));
   p->at = reinterpret_cast<unsigned short *>(take(2 * static_cast<size_t>(s.adapters) * s.rank * s.hidden));
   p->parts_a = hg::adapt_parts(s.m, s.adapters, 1, s.hidden, s.rank);
   p->parts_b = hg::adapt_parts(s.m, s.adapters, s.tp, s.shard, s.rank);

@@ -67,12 +67,10 @@ def adapt_grad_bound(dy, x, a, b, index, scale, kind, out):
         eg = (dy.shape[1] + 64) * U32 * abs(s) * (np.abs(dy[rows]) @ np.abs(b[i])) + 2 * U32 * np.abs(g)
         eu = (x.shape[1] + 64) * U32 * abs(s) * (np.abs(x[rows]) @ np.abs(a[i]).T) + 2 * U32 * np.abs(u)
         parts.append((i, rows, g, u, eg, eu))
-    top_g = max((np.abs(p[2]).max(initial=0.0) for p in parts), default=0.0)
-    top_u = max((np.abs(p[3]).max(initial=0.0) for p in parts), default=0.0)
     for i, rows, g, u, eg, eu in parts:
         row = np.abs(g).max(axis=1, keepdims=True, initial=0.0)
         dx[rows] = (eg + _split(kind, g, row) + (2 * rank + 8) * U32 * np.abs(g)) @ np.abs(a[i])
-        da[i] = (eg + _split(kind, g, top_g) + (2 * m + 8) * U32 * np.abs(g)).T @ np.abs(x[rows])
-        db[i] = np.abs(dy[rows]).T @ (eu + _split(kind, u, top_u) + (2 * m + 8) * U32 * np.abs(u))
+        da[i] = (eg + _split(kind, g, np.abs(g).max(initial=0.0)) + (2 * m + 8) * U32 * np.abs(g)).T @ np.abs(x[rows])
+        db[i] = np.abs(dy[rows]).T @ (eu + _split(kind, u, np.abs(u).max(initial=0.0)) + (2 * m + 8) * U32 * np.abs(u))
     kinds = (kind, out, out)
     return wants, [e + HALF_STEP[k] * (np.abs(w) + e) + LEAST[k] for e, w, k in zip((dx, da, db), wants, kinds)]

@@ -1,5 +1,6 @@
 """The low-rank values of the adapters on their way to a result: sums that come out exact in fp32, so that nothing but
-what the second product makes of them is left (GPU).
+what the second product makes of them is left; infinities and adapters of different size (GPU). And that the oracle's
+bounds see a mistake there (CPU).
 
 Every row has one entry on the side that is summed first, so u (or g) is one product of two 16-bit numbers, at most 22
 bits, and a factor: off by 2^-24 of itself. An entry of the result is then one product with a 16-bit number, in up to
@@ -12,6 +13,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import adapters as oa
 from tp_vocab_logits_amd import adapt, adapt_grad
 
 DEV = "cuda:0"
@@ -73,6 +75,23 @@ class Case:
     def largest(self, low):
         """Of each adapter's rows."""
         return np.array([np.abs(low[self.index.numpy() == i]).max(initial=0.0) for i in range(len(self.scale))])
+
+
+def test_bounds_are_each_adapters_own():
+    """fp16's pieces, emulated: by each adapter's largest value they are within the bounds, by the call's they are not."""
+    rng = np.random.RandomState(0)
+    index, x, dy = rng.randint(0, 2, 40), rng.randn(40, 24), rng.randn(40, 16)
+    a, b, scale = rng.randn(2, 8, 24), rng.randn(2, 16, 8), np.array([2.0 ** 20, 2.0 ** -20])
+    (_, _, want), (_, _, bound) = oa.adapt_grad_bound(dy, x, a, b, index, scale, "fp16", "fp32")
+    us = [scale[i] * (x[index == i] @ a[i].T) for i in range(2)]
+    for tops, good in (([np.abs(u).max() for u in us], True), ([max(np.abs(u).max() for u in us)] * 2, False)):
+        within = []
+        for i, (u, top) in enumerate(zip(us, tops)):
+            factor, held = 2.0 ** (13 - np.floor(np.log2(top))), np.zeros_like(u)
+            for _ in range(3):
+                held += (u * factor - held).astype(np.float16)
+            within.append((np.abs(dy[index == i].T @ (held / factor) - want[i]) <= bound[i]).all())
+        assert all(within) == good
 
 
 def near(got, want, bound):
@@ -187,3 +206,68 @@ def test_low_rank_values_between_bf16s_largest_and_fp32s(m, n, rank):
     # bf16's smallest normal b is 2^-126: what lies below it may count as nothing
     small = np.abs(f64(c.b)[c.index.numpy()][:, :, 0]) < 2.0 ** -126
     near(np.where(small, want, got), want, (HALF_STEP["bf16"] + 2 * SUMS) * np.abs(want) + 1e-30)
+
+
+@gpu
+@pytest.mark.parametrize("m,n,rank", FORMS)
+def test_fp16_adapters_go_by_their_own_largest(m, n, rank):
+    """Adapters 2^40 apart: by one factor for all of them the small ones would be nothing."""
+    note(f"adapt fp16 apart {m} {n} {rank}")
+    n += n == 1
+    c = Case("fp16", m, n, rank, 5)
+    c.scale = c.scale * 2.0 ** torch.tensor([20.0 if i % 2 else -20.0 for i in range(n)])
+    dy, x = (c.randn(m, w).to(c.t) for w in (V, HIDDEN))
+    a, b, i = c.on()
+    got = adapt_grad(c.shards(dy).to(DEV), x.to(DEV), a, b, i, TP, SHARD, scale=c.scale.to(DEV), wide=True,
+                     need=(False, True, True))
+    wants, bounds = oa.adapt_grad_bound(f64(dy), f64(x), f64(c.a), f64(c.b), c.index.numpy(), f64(c.scale), "fp16", "fp32")
+    for t, want, bound in zip(got[1:], wants[1:], bounds[1:]):
+        near(f64(t), want, bound + 1e-300)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,n,rank", [(40, 4, 16), (56, 3, 32), (57, 3, 32), (40, 4, 40), (200, 4, 16), (300, 3, 40), (200, 4, 72)])
+def test_what_is_not_finite_stays_where_it_belongs(dtype, m, n, rank):
+    """An adapter of infinities, rows of infinities that have it, rows without an adapter; then one rank of an adapter."""
+    note(f"adapt not finite {dtype} {m} {n} {rank}")
+    c = Case(dtype, m, n, rank, 6)
+    c.index[::7] = -1
+    c.index[:n] = torch.arange(n)
+    own, bare = c.index == 1, c.index < 0
+    y, dy, x = ((c.randn(m, w) * 0.1).to(c.t) for w in (V, V, HIDDEN))
+    scale = c.scale.to(DEV)
+
+    def run(y, dy, x, a, b):
+        low = (x.to(DEV), a.to(DEV), b.to(DEV), c.index.to(DEV), TP, SHARD)
+        out = adapt(c.shards(y).to(DEV), *low, scale=scale).transpose(0, 1).reshape(m, V)
+        return [t.cpu() for t in (out, *adapt_grad(c.shards(dy).to(DEV), *low, scale=scale, wide=True))]
+
+    clean = run(y, dy, x, c.a, c.b)
+    a, b, bad_y, bad_dy, bad_x = c.a.clone(), c.b.clone(), y.clone(), dy.clone(), x.clone()
+    a[1], b[1] = float("inf"), float("nan")
+    bad_dy[own], bad_x[own], bad_dy[bare], bad_x[bare] = -float("inf"), float("inf"), float("nan"), float("nan")
+    out, dx, da, db = run(bad_y, bad_dy, bad_x, a, b)
+    others = torch.arange(n) != 1
+    assert torch.equal(out[~own], clean[0][~own]) and torch.equal(dx[~own], clean[1][~own])
+    assert torch.equal(da[others], clean[2][others]) and torch.equal(db[others], clean[3][others])
+    assert not any(t.isfinite().any() for t in (out[own], dx[own], da[1], db[1]))
+    # one rank of A: u's; the others' columns of dB are those of an adapter without it
+    a, b = c.a.clone(), c.b.clone()
+    a[1, 3] = float("inf")
+    out, dx, da, db = run(y, dy, x, a, b)
+    assert torch.equal(da, clean[2]) and not db[1, :, 3].isfinite().any() and not out[own].isfinite().any()
+    a[1, 3] = 0.0
+    low = (f64(x), f64(a), f64(b), c.index.numpy(), f64(c.scale))
+    wants, bounds = oa.adapt_grad_bound(f64(dy), *low, dtype, "fp32")
+    keep = np.arange(rank) != 3
+    near(f64(db)[..., keep], wants[2][..., keep], bounds[2][..., keep] + 1e-300)
+    # one rank of B: g's
+    a, b = c.a.clone(), c.b.clone()
+    b[1, 5, 3] = -float("inf")
+    out, dx, da, db = run(y, dy, x, a, b)
+    assert torch.equal(db, clean[3]) and not da[1, 3].isfinite().any() and not dx[own].isfinite().any()
+    b[1, 5, 3] = 0.0
+    low = (f64(x), f64(a), f64(b), c.index.numpy(), f64(c.scale))
+    wants, bounds = oa.adapt_grad_bound(f64(dy), *low, dtype, "fp32")
+    near(f64(da)[:, keep], wants[1][:, keep], bounds[1][:, keep] + 1e-300)

@@ -59,7 +59,7 @@ extern "C" {
 #define HG_OK 0
 #define HG_EDECLINE 1  /* not served: take the stock path; nothing enqueued     */
 #define HG_EINVAL (-1) /* bad argument (sizes, null or misaligned pointer, ...) */
-#define HG_ENOMEM (-2) /* device allocation failed                             */
+#define HG_ENOMEM (-2) /* an allocation failed                                  */
 #define HG_EHIP (-3)   /* a HIP runtime call failed (see hg_last_error_detail)  */
 #define HG_ETIMEOUT (-4) /* a bounded poll gave up (reported by hg_poll_status)  */
 #define HG_ESTATE (-5) /* split-variant call out of order                       */
@@ -578,9 +578,15 @@ typedef struct hg_beam_state {
  * lengths (or NULL): only positions < lengths[q] of request q move, the others
  * keep their bytes; lengths below 0 count as 0, above `steps` as `steps`.
  * parents, lengths: device int32 or int64 (parent_bytes, length_bytes 4 or 8).
- * states: host array of `count` entries. HG_EINVAL on a bad size, a NULL or
- * misaligned pointer, or states that overlap each other, themselves, or
- * parents or lengths.
+ * states: host array of `count` entries (65536 at most). They may lie between each
+ * other's rows and runs, as views of one cache do; where their strides differ, only
+ * as far as the larger of their two strides is the same and the bytes from a row's
+ * (or run's) first one to its last lie apart. HG_EINVAL on a bad size, a NULL or
+ * misaligned pointer, states that overlap each other, themselves, or parents or
+ * lengths (a state counts from its first byte to its last for those), or 2^31 pieces
+ * of 4 KB (1 KB above 16 beams; at least one a run of every request) in the states of
+ * one geometry, 64 at most, that follow one another. HG_ENOMEM if more than 64 states
+ * and the host has no memory for their order.
  */
 int hg_beam_reorder(int requests, int beams, int count, const hg_beam_state *states,
                     const void *parents, int parent_bytes, const void *lengths, int length_bytes,

@@ -173,7 +173,8 @@ def beam_reorder(states, parents: torch.Tensor, lengths: torch.Tensor | None = N
     the beams (-1) leaves its row as it is. With ``lengths`` (``[requests]``,
     int64 or int32) only the first ``lengths[q]`` positions along ``time_dim``
     move (clamped to what there is), the others keep their values. A state must
-    be without gaps from ``time_dim`` on; states must not overlap."""
+    be without gaps from ``time_dim`` on; states must not overlap (views of one
+    cache may lie between each other's rows)."""
     if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
         raise ValueError("parents must be a [requests, beams] tensor")
     requests, beams = (int(v) for v in parents.shape)

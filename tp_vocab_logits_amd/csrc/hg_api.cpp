@@ -620,7 +620,7 @@ HG_API const char *hg_strerror(int code) {
     case HG_OK: return "ok";
     case HG_EDECLINE: return "declined: take the stock gather";
     case HG_EINVAL: return "invalid argument";
-    case HG_ENOMEM: return "device memory allocation failed";
+    case HG_ENOMEM: return "memory allocation failed";
     case HG_EHIP: return "HIP runtime error";
     case HG_ETIMEOUT: return "a bounded mailbox poll gave up";
     case HG_ESTATE: return "split push/collect called out of order";

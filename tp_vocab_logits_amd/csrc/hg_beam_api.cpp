@@ -5,6 +5,10 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "hg_beam.h"
 #include "hg_ranges.h"
 
@@ -116,43 +120,111 @@ HG_API int hg_beam_select(const hg_beam_shape *s, const void *const *logits, con
 
 namespace {
 
-// The bytes of a state: `rows` x `outer` runs of `run` bytes.
+// The bytes of a state: runs of `run` bytes, `many` of them `small` apart, and that
+// (`block` bytes from end to end) `times` over, `large` apart. A stride that nothing
+// takes is 0.
 struct Extent {
   uintptr_t at;
-  long long rows, outer, row_stride, outer_stride, run;
-  size_t span() const { return (rows - 1) * row_stride + (outer - 1) * outer_stride + run; }
+  size_t run, small, large, block, span;
+  size_t many, times;
 };
 
-// Runs of one state apart from each other: the smaller stride takes a run, the
-// larger one all of the smaller's.
-bool apart(const Extent &e) {
-  const bool rows_inside = e.row_stride <= e.outer_stride;
-  const long long small = rows_inside ? e.row_stride : e.outer_stride;
-  const long long large = rows_inside ? e.outer_stride : e.row_stride;
-  const long long many = rows_inside ? e.rows : e.outer, times = rows_inside ? e.outer : e.rows;
-  if (many > 1 && small < e.run) return false;
-  return times == 1 || large >= (many - 1) * small + e.run;
+// False if runs of the state lie in each other.
+bool extent(const hg_beam_state &t, size_t rows, Extent *e) {
+  size_t n[2] = {rows, static_cast<size_t>(t.outer)};
+  size_t step[2] = {static_cast<size_t>(t.row_stride), static_cast<size_t>(t.outer_stride)};
+  for (int k = 0; k < 2; ++k)
+    if (n[k] == 1) step[k] = 0;
+  const int s = step[0] <= step[1] ? 0 : 1;
+  e->at = reinterpret_cast<uintptr_t>(t.ptr);
+  e->run = static_cast<size_t>(t.steps) * t.step_bytes;
+  e->many = n[s];
+  e->small = step[s];
+  e->times = n[1 - s];
+  e->large = step[1 - s];
+  e->block = (e->many - 1) * e->small + e->run;
+  e->span = (e->times - 1) * e->large + e->block;
+  return (e->many == 1 || e->small >= e->run) && (e->times == 1 || e->large >= e->block);
 }
 
-// Whether two states share a byte. States of one geometry may lie between each
-// other's runs (views of one cache); others have to lie apart as a whole.
+// The stride that two counts share (0: neither has one); false if they differ.
+bool shared(size_t a, size_t b, size_t *step) {
+  *step = a ? a : b;
+  return !a || !b || a == b;
+}
+
+// Whether two states, a first, share a byte; true as well if their strides differ where
+// it depends on them.
 bool meet(const Extent &a, const Extent &b) {
-  const Extent &x = a.at <= b.at ? a : b, &y = a.at <= b.at ? b : a;
-  if (y.at - x.at >= x.span()) return false;
-  if (a.rows != b.rows || a.outer != b.outer || a.row_stride != b.row_stride ||
-      a.outer_stride != b.outer_stride || a.run != b.run)
-    return true;
-  // d + i*row_stride + j*outer_stride within a run of 0, |i| < rows, |j| < outer
-  const long long d = static_cast<long long>(y.at - x.at);
-  for (long long j = -(a.outer - 1); j < a.outer; ++j) {
-    const long long left = d + j * a.outer_stride;
-    const long long near = a.rows > 1 ? -left / a.row_stride : 0;
-    for (long long i = near - 1; i <= near + 1; ++i) {
-      const long long gap = left + i * a.row_stride;
-      if (i > -a.rows && i < a.rows && gap < a.run && gap > -a.run) return true;
+  typedef long long wide;
+  const size_t apart = b.at - a.at;
+  if (apart >= a.span) return false;
+  size_t large, small;
+  if (!shared(a.large, b.large, &large)) return true;
+  // Blocks meet where b's is moved by `large` to within a block of a's: two or three
+  // places at most. The same of their runs.
+  if (large && (a.block > large || b.block > large)) return true;
+  const wide d = static_cast<wide>(apart), step = static_cast<wide>(large ? large : 1);
+  const wide near = large ? -(d / step) : 0;
+  for (wide j = near - 1; j <= near + 1; ++j) {
+    if (j <= -static_cast<wide>(a.times) || j >= static_cast<wide>(b.times)) continue;
+    const wide e = d + (large ? j * step : 0);
+    if (e >= static_cast<wide>(a.block) || e <= -static_cast<wide>(b.block)) continue;
+    if (!shared(a.small, b.small, &small)) return true;
+    if (small && (a.run > small || b.run > small)) return true;
+    const wide inner = static_cast<wide>(small ? small : 1), close = small ? -(e / inner) : 0;
+    for (wide i = close - 1; i <= close + 1; ++i) {
+      if (i <= -static_cast<wide>(a.many) || i >= static_cast<wide>(b.many)) continue;
+      const wide gap = e + (small ? i * inner : 0);
+      if (gap < static_cast<wide>(a.run) && gap > -static_cast<wide>(b.run)) return true;
     }
   }
   return false;
+}
+
+// Whether no two of the states' runs (blocks) of `bytes` meet at any multiple of `step`
+// from where they are: then nor do they where they are. `order`: room for n places.
+bool apart_around(const Extent *e, size_t n, size_t step, size_t Extent::*bytes, uint32_t *order) {
+  for (size_t k = 0; k < n; ++k) {
+    if (e[k].*bytes > step) return false;
+    order[k] = static_cast<uint32_t>(k);
+  }
+  std::sort(order, order + n, [&](uint32_t a, uint32_t b) { return e[a].at % step < e[b].at % step; });
+  for (size_t k = 0; k < n; ++k) {
+    const Extent &a = e[order[k]], &b = e[order[k + 1 < n ? k + 1 : 0]];
+    if (a.at % step + a.*bytes > b.at % step + (k + 1 < n ? 0 : step)) return false;
+  }
+  return true;
+}
+
+// The same of all their bytes: of n states, sorted by address, those whose spans are
+// linked. Views of one cache lie apart by their places between two rows, or between two
+// runs, which takes a sort; other ones go by pairs.
+bool all_apart(const Extent *e, size_t n, uint32_t *order) {
+  size_t large = 0, small = 0;
+  bool one = true, same = true;
+  for (size_t k = 0; k < n && one; ++k) one = shared(large, e[k].large, &large);
+  for (size_t k = 0; k < n && same; ++k) same = shared(small, e[k].small, &small);
+  if (one && large && apart_around(e, n, large, &Extent::block, order)) return true;
+  if (one && large && same && small && large % small == 0 && apart_around(e, n, small, &Extent::run, order)) return true;
+  for (size_t k = 1; k < n; ++k)
+    for (size_t i = 0; i < k; ++i)
+      if (meet(e[i], e[k])) return false;
+  return true;
+}
+
+// Whether the states lie apart: a sort by address, then all_apart where spans are linked
+// (64 separate caches, the most of a launch, with the call's other checks: 3 us; 64 views
+// of one cache, 32 heads: 10 us, 4096 views 0.5 ms).
+bool disjoint(Extent *e, size_t n, uint32_t *order) {
+  std::sort(e, e + n, [](const Extent &a, const Extent &b) { return a.at < b.at; });
+  for (size_t k = 0; k < n;) {
+    uintptr_t end = e[k].at + e[k].span;
+    size_t first = k++;
+    for (; k < n && e[k].at < end; ++k) end = std::max<uintptr_t>(end, e[k].at + e[k].span);
+    if (k - first > 1 && !all_apart(e + first, k - first, order)) return false;
+  }
+  return true;
 }
 
 }  // namespace
@@ -169,11 +241,15 @@ HG_API int hg_beam_reorder(int requests, int beams, int count, const hg_beam_sta
     return HG_EINVAL;
   const long long rows = static_cast<long long>(requests) * beams;
   constexpr long long kMost = 1ll << 46;  // bytes of a state: strides and offsets stay far from 2^63
-  auto extent = [&](const hg_beam_state &t) {
-    return Extent{reinterpret_cast<uintptr_t>(t.ptr), rows, t.outer, t.row_stride, t.outer_stride,
-                  t.steps * t.step_bytes};
-  };
   auto empty = [](const hg_beam_state &t) { return t.outer == 0 || t.steps == 0 || t.step_bytes == 0; };
+  constexpr int kFew = 64;  // (a few states need no memory of the host)
+  Extent few[kFew];
+  uint32_t few_order[kFew];
+  std::unique_ptr<Extent[]> more(count > kFew ? new (std::nothrow) Extent[count] : nullptr);
+  std::unique_ptr<uint32_t[]> more_order(count > kFew ? new (std::nothrow) uint32_t[count] : nullptr);
+  if (count > kFew && (!more || !more_order)) return HG_ENOMEM;
+  Extent *const e = count > kFew ? more.get() : few;
+  size_t n = 0;
   for (int i = 0; i < count; ++i) {
     const hg_beam_state &t = states[i];
     if (t.outer < 0 || t.outer > (1 << 20) || t.steps < 0 || t.step_bytes < 0 || t.step_bytes > kMost)
@@ -182,18 +258,25 @@ HG_API int hg_beam_reorder(int requests, int beams, int count, const hg_beam_sta
     if (!t.ptr || t.step_bytes > kMost / t.steps || t.row_stride < 0 || t.outer_stride < 0 ||
         t.row_stride > kMost / rows || t.outer_stride > kMost / t.outer)
       return HG_EINVAL;
-    const Extent e = extent(t);
-    if (!apart(e)) return HG_EINVAL;
-    const uintptr_t end = e.at + e.span();
+    if (!extent(t, rows, e + n)) {
+      hg::record_error("a state's rows overlap each other");
+      return HG_EINVAL;
+    }
+    const uintptr_t begin = e[n].at, end = begin + e[n].span;
     auto touches = [&](const void *p, size_t bytes) {
       const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-      return p && at < end && e.at < at + bytes;
+      return p && at < end && begin < at + bytes;
     };
     if (touches(parents, rows * parent_bytes) ||
-        touches(lengths, static_cast<size_t>(requests) * length_bytes))
+        touches(lengths, static_cast<size_t>(requests) * length_bytes)) {
+      hg::record_error("a state overlaps the parents or the lengths");
       return HG_EINVAL;
-    for (int k = 0; k < i; ++k)
-      if (!empty(states[k]) && meet(e, extent(states[k]))) return HG_EINVAL;
+    }
+    ++n;
+  }
+  if (!disjoint(e, n, count > kFew ? more_order.get() : few_order)) {
+    hg::record_error("states overlap each other, or lie between each other's rows with other strides");
+    return HG_EINVAL;
   }
   hipStream_t st = static_cast<hipStream_t>(stream);
   // States of one geometry that follow one another share a launch. The sizes of
@@ -213,7 +296,10 @@ HG_API int hg_beam_reorder(int requests, int beams, int count, const hg_beam_sta
         table[p.count++] = static_cast<unsigned char *>(o.ptr);
       }
       if (empty(t)) continue;
-      if (!run && hg::beam_reorder_items(p) >= (1ll << 31)) return HG_EINVAL;
+      if (!run && hg::beam_reorder_items(p) >= (1ll << 31)) {
+        hg::record_error("more runs of rows than a launch covers");
+        return HG_EINVAL;
+      }
       if (run) HIP_TRY(hg::launch_beam_reorder(p, table, st));
     }
   }

@@ -22,6 +22,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from ._lib import check, lib
@@ -92,15 +93,21 @@ def adapt(y: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, in
     ``x`` its input ``[M, H]``, both BF16 or FP16 as ``a`` and ``b`` are;
     ``index`` is ``[M]`` int64 or int32, ``scale`` ``[n]`` fp32 (default: ones).
     ``out`` may be ``y``: rows without an adapter are then not touched. ``shard``,
-    ``H`` and the rank (up to 256) are multiples of 8. Autograd does not see this
-    call: :func:`adapted` is the differentiable form."""
+    ``H`` and the rank (up to 256) are multiples of 8. :func:`adapted` is the
+    differentiable form: autograd does not see this call, only that a given ``out``
+    was written, which must not require a gradient while gradients are recorded."""
+    if isinstance(out, torch.Tensor) and out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("out requires a gradient, which would leave the adapters out: use adapted")
     c = _Adapters(y, "y", x, a, b, index, tp, shard, scale)
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty_like(y)
     elif out is not y:
         _given(out, "out", y.shape, (c.dtype,), c.device)
     if c.m:
         c.call(_lib.HG_ADAPT_ADD, out.data_ptr())
+        if given:
+            increment_version(out)
     return out
 
 

@@ -11,8 +11,9 @@ the logits, in the scores and in every state. A step of a search that keeps
 
 Work is enqueued on the current stream of the inputs' device; the workspace
 comes from torch's allocator on that stream. Both can be captured into a
-graph. Autograd sees neither: states that are part of a graph must not be
-reordered.
+graph. Autograd sees neither, but for the version of the states, so that a
+backward pass notices if it needs one that was reordered; states that require a
+gradient are refused.
 """
 
 from __future__ import annotations
@@ -23,6 +24,7 @@ import math
 from collections.abc import Iterable
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from ._lib import check, lib
@@ -202,3 +204,4 @@ def beam_reorder(states, parents: torch.Tensor, lengths: torch.Tensor | None = N
         _call(_lib.fast().beam_reorder, "hg_beam_reorder", device, requests, beams, tuple(table), parents.data_ptr(),
               parents.element_size(), lengths.data_ptr() if lengths is not None else 0,
               lengths.element_size() if lengths is not None else 0)
+        increment_version(states)

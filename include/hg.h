@@ -453,8 +453,9 @@ typedef struct hg_adapt_shape {
   int tp, shard, hidden; /* the head; shard and hidden multiples of 8, hidden at
                             most 2^20, tp*shard below 2^29, tp at most HG_MAX_TP */
   int m;                 /* rows, at most 2^24; m x tp*shard at most 2^40        */
-  int adapters;          /* pairs, 1 .. 2^15; x tp*shard/64 and x hidden/64 below
-                            2^23 for gradients                                  */
+  int adapters;          /* pairs, 1 .. 2^15; for gradients, x rank/64 x tp *
+                            (shard/64), and x rank/64 x hidden/64, each quotient
+                            rounded up, below 2^23                              */
   int rank;              /* a multiple of 8, 8 .. HG_MAX_RANK                    */
   int dtype;             /* HG_BF16 or HG_FP16: x, y, A, B, 16-bit gradients     */
   int index_bytes;       /* 4 or 8: the index is int32 or int64                  */

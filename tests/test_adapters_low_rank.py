@@ -9,12 +9,14 @@ holds of a value ends 2^-38 below the largest of its row, or of its adapter's ro
 
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 from oracle import adapters as oa
-from tp_vocab_logits_amd import adapt, adapt_grad
+from tp_vocab_logits_amd import _lib, adapt, adapt_grad
 
 DEV = "cuda:0"
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
@@ -271,3 +273,46 @@ def test_what_is_not_finite_stays_where_it_belongs(dtype, m, n, rank):
     low = (f64(x), f64(a), f64(b), c.index.numpy(), f64(c.scale))
     wants, bounds = oa.adapt_grad_bound(f64(dy), *low, dtype, "fp32")
     near(f64(da)[:, keep], wants[1][:, keep], bounds[1][:, keep] + 1e-300)
+
+
+def test_every_shape_within_the_limits_is_taken():
+    """As many rows and columns as the form without streaming has no single launch for."""
+    n = ctypes.c_size_t()
+    for kind in (_lib.HG_ADAPT_ADD, _lib.HG_ADAPT_GRAD):
+        for tp, shard, hidden, m, adapters, rank in (
+                (8, 20480, 7168, 212000, 4, 72), (8, 20480, 7168, 262144, 1, 128), (1, 8, 8, 1 << 24, 1, 256),
+                (8, 20480, 7168, 1 << 20, 1 << 10, 16), (1, 8, 1 << 20, 1 << 24, 500, 64), (64, 1 << 17, 8, 1 << 17, 3, 256)):
+            shape = _lib.AdaptShape(tp, shard, hidden, m, adapters, rank, _lib.HG_BF16, 8)
+            assert _lib.lib().hg_adapt_workspace(shape, kind, n) == _lib.HG_OK, (tp, shard, hidden, m, adapters, rank)
+    # gradients: adapters x strips of 64 columns x chunks of 64 ranks
+    for tp, shard, hidden, adapters, rank, taken in (
+            (1, 8, 64 * 64, 1 << 15, 256, False), (1, 8, 64 * 63, 1 << 15, 256, True), (64, 72, 8, 1 << 15, 72, False),
+            (64, 64, 8, 1 << 15, 72, True), (1, 64 * 256, 8, 1 << 15, 64, False), (1, 64 * 255, 8, 1 << 15, 64, True)):
+        shape = _lib.AdaptShape(tp, shard, hidden, 5, adapters, rank, _lib.HG_BF16, 8)
+        assert (_lib.lib().hg_adapt_workspace(shape, _lib.HG_ADAPT_GRAD, n) == _lib.HG_OK) == taken, (tp, shard, hidden, adapters, rank)
+
+
+@gpu
+def test_more_rows_than_one_launch_covers():
+    m, rank, n, hidden, v = 14_950_003, 72, 3, 8, 8  # 934376 tiles x 9 strips, above 2^23
+    note("adapt 15 million rows")
+    g = torch.Generator(device=DEV).manual_seed(3)
+    y, x = (torch.randn(m, w, generator=g, device=DEV).bfloat16() for w in (v, hidden))
+    a = torch.randn(n, rank, hidden, generator=g, device=DEV).bfloat16()
+    b = torch.randn(n, v, rank, generator=g, device=DEV).bfloat16()
+    index = torch.randint(-1, n, (m,), generator=g, device=DEV)
+    got = adapt(y, x, a, b, index, 1, v)
+    # sums of 8 and of 72 terms in three pieces: (8 + 216 + 8) steps of 2^-23, below 2^-15
+    for at in range(0, m, 1 << 20):
+        part = slice(at, at + (1 << 20))
+        want, size = y[part].double(), torch.zeros_like(y[part], dtype=torch.float64)
+        for i in range(n):
+            mine = (index[part] == i)[:, None]
+            xs, ai, bi = x[part].double(), a[i].double(), b[i].double()
+            want += torch.where(mine, (xs @ ai.t()) @ bi.t(), 0.0)
+            size += torch.where(mine, (xs.abs() @ ai.abs().t()) @ bi.abs().t(), 0.0)
+        e = (got[part].double() - want).abs()
+        lost = 2.0 ** -15 * size
+        assert (e <= lost + HALF_STEP["bf16"] * (want.abs() + lost)).all(), at
+        bare = index[part] < 0
+        assert torch.equal(got[part][bare], y[part][bare])

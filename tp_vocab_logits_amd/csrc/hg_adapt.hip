@@ -529,7 +529,7 @@ struct UpArgs {
   unsigned short *out;
   int m, adapters, rank, splits;
   int blocks, shard, per_block, chunks;  // chunks of 64 columns per block, in all
-  int groups, strips;
+  int first, groups, strips;             // groups of 16 rows of this launch, from `first` on
 };
 
 // RANKS: 16 (two pieces share one fragment), 64, or 256: in turns of 64.
@@ -561,7 +561,7 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
     group = in / 8;
   }
   if (strip >= a.strips) return;
-  const int p0 = group * 16;
+  const int p0 = (a.first + group) * 16;
   const int p = p0 + ml;
   const int key = p < a.m ? a.keys[p] : -1;  // -1: no row
   const size_t row = static_cast<size_t>(p < a.m ? a.pos[p] : 0) * a.shard;
@@ -1346,6 +1346,8 @@ void by_size(int rank, int m, const Blocked &of, F f) {
 
 int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
+constexpr int kMaxGroups = 1 << 23;  // workgroups of a launch
+
 }  // namespace
 
 int adapt_splits(int m, int blocks, int shard, int rank, bool few) {
@@ -1424,15 +1426,20 @@ hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *
       });
     } else {
       const int groups = ceil_div(p.m, 16), strips = ceil_div(chunks, 4);
-      const UpArgs a{r.keys, r.pos, p.few, part, scale, wp, yp, op, p.m, p.adapters, p.rank, splits, y.blocks,
-                     y.shard, per, chunks, groups, strips};
+      UpArgs a{r.keys, r.pos, p.few, part, scale, wp, yp, op, p.m, p.adapters, p.rank, splits, y.blocks,
+               y.shard, per, chunks, 0, groups, strips};
+      // (a launch has fewer than 2^32 lanes: 212000 rows of 163840 columns are two)
+      const int most = kMaxGroups / (strips + 8);
       auto go = [&](auto ranks) {
-        if (p.adapters >= groups)
-          hipLaunchKernelGGL((k_adapt_up<T, decltype(ranks)::value, true>), dim3(static_cast<unsigned>(strips) * groups),
-                             dim3(kThreads), 0, s, a);
-        else
-          hipLaunchKernelGGL((k_adapt_up<T, decltype(ranks)::value, false>),
-                             dim3(static_cast<unsigned>(ceil_div(strips, 8)) * 8 * groups), dim3(kThreads), 0, s, a);
+        for (; a.first < groups; a.first += most) {
+          a.groups = groups - a.first < most ? groups - a.first : most;
+          if (p.adapters >= groups)
+            hipLaunchKernelGGL((k_adapt_up<T, decltype(ranks)::value, true>),
+                               dim3(static_cast<unsigned>(strips) * a.groups), dim3(kThreads), 0, s, a);
+          else
+            hipLaunchKernelGGL((k_adapt_up<T, decltype(ranks)::value, false>),
+                               dim3(static_cast<unsigned>(ceil_div(strips, 8)) * 8 * a.groups), dim3(kThreads), 0, s, a);
+        }
       };
       p.rank <= 16 ? go(Int<16>{}) : p.rank <= kRankChunk ? go(Int<kRankChunk>{}) : go(Int<HG_MAX_RANK>{});
     }

@@ -36,12 +36,9 @@ bool shape_ok(const hg_adapt_shape *s, int kind) {
     return false;
   if (s->dtype != HG_BF16 && s->dtype != HG_FP16) return false;
   if (s->index_bytes != 4 && s->index_bytes != 8) return false;
-  // the largest launches: row groups x strips of columns (a multiple of 8 of
-  // them); adapters x 64 columns x rank chunks
+  // the largest launch: adapters x 64 columns x rank chunks
   const long long strips = s->tp * ceil_div(s->shard, 64), other = ceil_div(s->hidden, 64);
   const long long wide = strips > other ? strips : other;
-  if (ceil_div(s->m, 16) * (ceil_div(wide, 4) + 8) >= kMaxGroups && !hg::adapt_streams(s->m, s->adapters, s->rank))
-    return false;
   return kind == HG_ADAPT_ADD || s->adapters * wide * ceil_div(s->rank, hg::kRankChunk) < kMaxGroups;
 }
 

@@ -213,13 +213,11 @@ __global__ __launch_bounds__(kScanThreads) void k_beam_scan(ShardTableN<NT> logi
   const typename L::elt *const base =
       reinterpret_cast<const typename L::elt *>(logits.p[rank]) + static_cast<size_t>(row) * a.shard;
   const int at0 = (piece * (J * kScanThreads) + tid) * L::N;
-  u32x4 v[J];
   // A beam that is not there, or finished: the join asks for nothing, and nothing is
-  // read of it (few rows: whether it is there is asked meanwhile).
-  auto absent = [&]() __attribute__((always_inline)) {
-    return !is_live(a.scores[row]) || (a.finished && a.finished[row]);
-  };
-  if (J == 4 && absent()) return;
+  // read of it. (Asking while the logits are on their way saves nothing: 5.7 us of four
+  // rows of 163840 both ways.)
+  if (!is_live(a.scores[row]) || (a.finished && a.finished[row])) return;
+  u32x4 v[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int at = at0 + j * (kScanThreads * L::N);
@@ -239,7 +237,6 @@ __global__ __launch_bounds__(kScanThreads) void k_beam_scan(ShardTableN<NT> logi
       }
     }
   }
-  if (J < 4 && absent()) return;
   if (tid == 0) count = 0;
 
   const float top = L::largest(v);

@@ -531,7 +531,10 @@ int hg_adapt_grad(const hg_adapt_shape *s, const void *dy, const void *x, const 
  * candidate fills hold score minus infinity, parent -1, token -1.
  */
 typedef struct hg_beam_shape {
-  int requests, beams, keep; /* requests >= 0; beams and keep in 1..64          */
+  int requests, beams, keep; /* requests >= 0; beams and keep in 1..64; requests *
+                                beams * parts of a row at most 2^23, a block of
+                                the row having a part per 8192 entries (fp32:
+                                4096), rounded up                               */
   int tp, shard;             /* blocks of the logits: block r is [requests *
                                 beams][shard], the vocabulary's r*shard and on;
                                 gathered rows are one block. tp at most

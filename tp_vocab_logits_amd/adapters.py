@@ -120,7 +120,8 @@ def adapt_grad(dy: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     ``da`` and ``db`` are fp32 if ``wide``, otherwise of the inputs' type, zero
     for an adapter that no row has; ``dx`` is zero for a row without one. ``need``
     says which of the three to compute, the others are None. Sums are fp32 in the
-    order of the rows, each result is rounded once."""
+    order of the rows, each result is rounded once. ``n`` times
+    rank/64 times the vocabulary/64 (or H/64), rounded up, stays below 2^23."""
     c = _Adapters(dy, "dy", x, a, b, index, tp, shard, scale)
     if len(need) != 3 or not any(need):
         raise ValueError(f"need must name one of dx, da and db at least, got {need}")

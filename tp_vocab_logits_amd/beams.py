@@ -87,7 +87,8 @@ def beam_select(logits, scores: torch.Tensor, keep: int, vocab: int | None = Non
     taken as fp32. ``scores``
     is ``[requests, beams]`` fp32, minus infinity (or any other value that is not
     finite) for a beam that is not there, such as all but one at the start. Equal
-    candidates go by beam, then token; sums and order are in 64 bits.
+    candidates go by beam, then token; sums and order are in 64 bits, of
+    exponentials to 1e-10.
 
     Tokens whose logit is minus infinity or NaN are no candidates. With
     ``finished`` (``[requests, beams]`` bool), a finished beam stands for itself:

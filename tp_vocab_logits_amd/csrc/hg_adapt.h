@@ -48,14 +48,16 @@ struct AdaptPlan {
 };
 
 // Whether the second product goes through many rows with W's fragments kept
-// (k_adapt_stream): sorted rows, 64 of an adapter on average, ranks that fit.
+// (k_adapt_stream): sorted rows, 64 or more for each adapter of the bank, ranks that fit.
+// (How many of the adapters the rows use is on the device alone; see APART in
+// hg_adapt.hip for what it costs where they are few.)
 inline bool adapt_streams(int m, int adapters, int rank) {
   return m > kFewRows && m / 64 >= adapters && rank <= kRankChunk;
 }
 
 // Whether launch_adapt_prepare leaves g's pieces in `low` for it (dx of bf16: fp16's need
 // a row's largest): a launch less, gradients of 2047 rows of 32000 columns 77
-// us instead of 80.
+// us instead of 80 (with two pieces).
 inline bool adapt_prepares_rows(const AdaptPlan &p) {
   return p.at && !p.half && adapt_streams(p.m, p.adapters, p.rank);
 }
@@ -81,7 +83,7 @@ hipError_t launch_adapt_outer(const AdaptPlan &p, const AdaptRows &r, const Bloc
 
 // Parts that a sum over `columns` columns of `m` rows is cut into.
 int adapt_splits(int m, int blocks, int shard, int rank, bool few);
-// Parts of the rows in the sums over an adapter's rows.
+// Parts of the rows in the sums over an adapter's rows, if they are spread over the bank.
 int adapt_parts(int m, int adapters, int blocks, int shard, int rank);
 
 }  // namespace hg

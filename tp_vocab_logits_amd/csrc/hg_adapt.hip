@@ -17,7 +17,8 @@
 // They enter as the sum of three 16-bit numbers, which hold all of fp32's 24 bits
 // (bf16: 8 each, over the same exponents). For fp16 they are first scaled by a power
 // of two that brings the largest of the row (out, dx) or of the adapter's rows (dA,
-// dB) to 2^13 .. 2^14; what lies 2^-38 below it is lost.
+// dB) to 2^13 .. 2^14; what lies 2^-38 below it is lost. (Comparisons below of forms
+// that were not kept were measured with two pieces, 2 to 4 % faster.)
 #include <type_traits>
 
 #include "hg_adapt.h"
@@ -71,8 +72,8 @@ __device__ __forceinline__ void pieces(float f, uint32_t (&h)[kPieces]) {
 // ---------------------------------------------------------------------------
 // Few rows: u of one row, or a part of it, per workgroup. A lane holds 8 elements
 // of x and meets them with those of each rank's row of A. The last workgroup sorts
-// the rows by adapter meanwhile (up to 64: a lane each). Latency: 3.7 us for one row,
-// 5.2 for 64 (hidden 7168, rank 16, 32 adapters).
+// the rows by adapter meanwhile (up to 64: a lane each). Latency: 3.8 us for one row,
+// 5.1 for 64 (hidden 7168, rank 16, 32 adapters).
 
 struct RowArgs {
   const void *index;
@@ -206,8 +207,9 @@ constexpr int kSecondLds = kStages * kRowStage + 2 * kLowStage;
 // rows are a power of two times a small number apart, and at one column they would
 // all be on a few of the memory's channels. 4096 rows of 163840 columns, rank 64, two
 // adapters, gradients: 630 us with neither, 642 with the first alone, 627 with the
-// second alone (a step apart), 606 with both. This kernel's part of it is 255 to 295
-// us, 4.6 to 5.3 TB/s of dy: HBM bounds it, A and B come on top (a tenth).
+// second alone (a step apart), 606 with both. This kernel's part of it is 257 to 304
+// us, 4.4 to 5.2 TB/s of dy: HBM bounds it; x, A and B come on top (a tenth: 1.48 GB in
+// all are read past the L2).
 
 struct LowSide {
   const unsigned short *of, *w;
@@ -466,7 +468,7 @@ __device__ __forceinline__ void low_values(const float *part, const float *scale
 }
 
 // All rows' values by sorted position: [m][3][RANKS] (16 or 64 ranks, zeros past
-// `rank`), and fp16's factors back. (2047 rows of 64 ranks in 28 parts: 6.6 us.)
+// `rank`), and fp16's factors back. (2047 rows of 64 ranks in 28 parts: 7 us.)
 template <class T, int RANKS>
 __global__ __launch_bounds__(kThreads) void k_adapt_values(const float *part, const float *scale, const int *keys,
                                                            int m, int adapters, int rank, int splits,
@@ -490,7 +492,7 @@ __global__ __launch_bounds__(kThreads) void k_adapt_values(const float *part, co
 // 8 + 8 columns: the rows of W are dealt to the matrix cores' rows so that these are
 // next to each other (stores of 64 bytes per row). For few rows, and for rows of
 // many adapters. 64 rows of 32 adapters (V = 163840, rank 16): 36 to 38 us for 190 MB,
-// 5.1 TB/s where a copy reaches 4.8, most of it W read once.
+// 5.0 TB/s where a copy reaches 4.8, most of it W read once.
 
 // acc += W's fragments x a row's values, given by read(piece, ks); BOTH: two pieces of
 // up to 16 ranks are one fragment, the third one and zeros another.
@@ -533,7 +535,11 @@ struct UpArgs {
 };
 
 // RANKS: 16 (two pieces share one fragment), 64, or 256: in turns of 64.
-// APART: the tiles have adapters of their own, mostly.
+// APART: as many adapters as tiles, or more, so that each tile is taken to have its own.
+// (Which ones the rows use is on the device alone: rows of few adapters of a large bank
+// pay for it. 2047 rows of 4 adapters, rank 64, V = 163840: 693 us in a bank of 32, where
+// the tiles share, 880 of 256, apart; 335 of 4 in the form below. 64 rows of one adapter,
+// rank 16: 23 us in a bank of 1, 25 of 256.)
 template <class T, int RANKS, bool APART>
 __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
   constexpr bool kBoth = RANKS == 16;
@@ -669,8 +675,9 @@ __global__ __launch_bounds__(kThreads) void k_adapt_up(UpArgs a) {
 // wave), and with them W's fragments, and goes through the rows, or a part of them,
 // 32 at a time, y and the low-rank values loaded straight into LDS as above. The
 // first form reads W's 8 KB for every 16 rows of 64 columns (2 KB); with 64 rows it
-// still took 365 us; this one takes 313, 4.3 TB/s of y read and written, where a copy
-// reaches 4.8 (2047 rows, V = 163840, rank 64).
+// still took 365 us; this one takes 312 to 340, 4.0 to 4.3 TB/s of y read and written,
+// where a copy reaches 4.8 (2047 rows, V = 163840, rank 64). The form above has any rank:
+// at 72, 2047 rows of 4 adapters take 964 us, at 64 in this form 335.
 
 struct StreamArgs {
   const int *keys, *pos;
@@ -1115,9 +1122,10 @@ __global__ __launch_bounds__(kThreads) void k_adapt_prepare(PrepareArgs a) {
 // rows' low-rank values (half of the bytes that their own columns take; up to 16
 // ranks each loads its own), of is turned while it is read from LDS. The rows'
 // places are loaded two steps before the rows. dB and dA of 4096 rows (V = 163840,
-// hidden 7168, rank 64, two adapters): 280 to 300 us for 1.45 GB, 5.0 TB/s; 1336 equal
-// workgroups on 512 places are 2.6 rounds. Neighbouring columns on one XCD: 25 us
-// slower.
+// hidden 7168, rank 64, two adapters): 305 to 330 us for 1.44 GB, 4.4 to 4.7 TB/s; 1336
+// equal workgroups on 512 places are 2.6 rounds. Neighbouring columns on one XCD: 25 us
+// slower. A fragment of the low-rank values, 16 lines of 64 bytes, is read in four cycles
+// more than one without bank conflicts, 16.4 M cycles in all or 10 % of the LDS's time.
 
 struct OuterSide {
   const int *largest;  // of each adapter's low-rank values (fp16)
@@ -1419,7 +1427,7 @@ hipError_t launch_adapt_up(const AdaptPlan &p, const AdaptRows &r, const float *
         const StreamArgs a{r.keys, r.pos, p.low, wp, yp, p.back, op, p.m, p.adapters, p.rank, y.blocks, y.shard, per,
                            chunks};
         // about 2048 workgroups, four rounds of two per CU, of two steps at least (2047 rows,
-        // V = 163840: 335 us; 1024 of them 362, 5100 349)
+        // V = 163840: 335 us; 1024 of them 362, 5100 349; with two pieces)
         const int strips = ceil_div(chunks, 4), most = ceil_div(p.m, 64), want = ceil_div(2048, strips);
         hipLaunchKernelGGL((k_adapt_stream<T, RB, decltype(past)::value != 0>),
                            dim3(strips, want < most ? want : most), dim3(kThreads), 0, s, a);
